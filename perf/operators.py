@@ -147,7 +147,7 @@ def prepare(case, seed):
     s["fk"], s["fv"] = (0.0123, 0.0171) if case["fp8"] else (1.0, 1.0)
     for name, f in (("k_cache", s["fk"]), ("v_cache", s["fv"])):
         x = torch.randn((P, Hkv, ps, d), generator=g, device=DEV)
-        s[name] = (x / f).to(torch.float8_e4m3fn) if case["fp8"] else x.to(torch.bfloat16)
+        s[name] = (x / f).clamp_(-448, 448).to(torch.float8_e4m3fn) if case["fp8"] else x.to(torch.bfloat16)
         del x
     if op != "store":
         s["o"] = torch.zeros((T, Hq, d), dtype=torch.bfloat16, device=DEV)
