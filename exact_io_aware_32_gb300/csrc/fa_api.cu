@@ -214,6 +214,19 @@ int bwd_common(const void* q, const void* k, const void* v, const void* o, const
 
 }  // namespace
 
+namespace fa {
+
+int device_facts(int* num_sms, unsigned int** status) {
+  DeviceInfo* di = nullptr;
+  const int st = device_info(&di);
+  if (st != FA_OK) return st;
+  *num_sms = di->num_sms;
+  *status = di->status;
+  return FA_OK;
+}
+
+}  // namespace fa
+
 extern "C" {
 
 int fa_fwd(const void* q, const void* k, const void* v, void* o, float* lse, int B, int H, int N, int d,
@@ -402,6 +415,7 @@ const char* fa_status_string(int status) {
     case FA_ERR_WORKSPACE: return "workspace missing, misaligned or too small";
     case FA_ERR_LAUNCH: return "CUDA launch or query failed";
     case FA_ERR_TIMEOUT: return "a kernel wait timed out";
+    case FA_ERR_NO_PAGES: return "too few free pages";
     default: return "unknown status";
   }
 }
@@ -423,7 +437,8 @@ int fa_device_status(int reset) {
     const unsigned int zero = 0;
     if (cudaMemcpyToSymbol(g_fa_device_status, &zero, sizeof(zero)) != cudaSuccess) return FA_ERR_LAUNCH;
   }
-  if (word & ~fa::kStatusBadLength) return FA_ERR_TIMEOUT;
+  if (word & ~(fa::kStatusBadLength | fa::kStatusNoPages)) return FA_ERR_TIMEOUT;
+  if (word & fa::kStatusNoPages) return FA_ERR_NO_PAGES;
   return word ? FA_ERR_INVALID_ARG : FA_OK;
 }
 

@@ -71,6 +71,9 @@ struct BwdArgs {
 // kernel then works with the length clamped into range.
 constexpr unsigned int kStatusBadLength = 32u;
 
+// Status bit of a plan that found too few free pages.
+constexpr unsigned int kStatusNoPages = 64u;
+
 // Lengths of sequence b under the padding masks: sq query rows and sk keys,
 // each lens[b] clamped to [1, N] (N without lengths), and under the causal
 // mask sq cut to sk, so that every valid row sees a key. Returns true when a
@@ -118,5 +121,8 @@ cudaError_t launch_bwd(const BwdArgs& a, int num_sms, cudaStream_t stream);
 // arguments (d = 64, 16-bit, no padding masks, key ranges or dropout), and its launch.
 bool fwd_persist_applies(const FwdArgs& a);
 cudaError_t launch_fwd_persist(const FwdArgs& a, int num_sms, cudaStream_t stream);
+
+// SM count and error word of the current device (FA_OK), or an fa_status error code.
+int device_facts(int* num_sms, unsigned int** status);
 
 }  // namespace fa

@@ -1,0 +1,226 @@
+// The paged cache's bookkeeping: planning a step (block tables, slots) and
+// storing new keys and values.
+#include <algorithm>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+
+#include "fa_internal.h"
+#include "paged.h"
+
+namespace fa {
+namespace {
+
+constexpr int kPlanThreads = 256;
+
+// One request's lengths as the plan takes them.
+struct Need {
+  long long rows;         // new tokens (packed rows)
+  long long ctx, len;     // tokens before and after, cut to the table's width
+  int held, pages;        // pages before, pages to take
+  bool bad;
+};
+
+__device__ __forceinline__ Need need_of(const PlanArgs& a, int r) {
+  Need n;
+  const int c = a.ctx_lens[r], w = a.new_lens[r];
+  const long long cap = (long long)a.max_pages << a.page_shift;
+  n.rows = max(w, 0);
+  n.ctx = max(c, 0);
+  n.len = n.ctx + n.rows;
+  n.bad = c < 0 || w < 0 || n.len > cap;
+  n.len = min(n.len, cap);
+  n.ctx = min(n.ctx, cap);
+  const int up = (1 << a.page_shift) - 1;
+  n.held = (int)((n.ctx + up) >> a.page_shift);
+  n.pages = (int)((n.len + up) >> a.page_shift) - n.held;
+  return n;
+}
+
+__device__ __forceinline__ long long warp_scan(long long x, int lane) {  // inclusive
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, s);
+    if (lane >= s) x += y;
+  }
+  return x;
+}
+
+// Prefix sums over the requests give each its packed rows and its pages; every
+// CTA (a group of requests by a slice of their tokens) adds up the requests
+// before its own, so one launch does it without a pass between CTAs: R lengths
+// are a few KB that L2 serves to all of them, and the call is bound by latency.
+__global__ void __launch_bounds__(kPlanThreads) fa_paged_plan_kernel(const __grid_constant__ PlanArgs a) {
+  constexpr int kWarps = kPlanThreads / 32;
+  __shared__ long long s_sum[2][kWarps];
+  __shared__ long long s_row[kPlanThreads], s_page[kPlanThreads];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int slices = gridDim.y, slice = blockIdx.y;
+  const int r0 = blockIdx.x * a.group, r1 = min(a.R, r0 + a.group);
+  const int head = max(a.free_head ? *a.free_head : 0, 0);
+  const long long avail = max(a.n_free - head, 0);
+
+  // rows and pages of the requests before this group
+  long long rows = 0, pages = 0;
+  for (int r = tid; r < r0; r += kPlanThreads) {
+    const Need n = need_of(a, r);
+    rows += n.rows;
+    pages += n.pages;
+  }
+  rows = warp_scan(rows, lane);
+  pages = warp_scan(pages, lane);
+  if (lane == 31) {
+    s_sum[0][warp] = rows;
+    s_sum[1][warp] = pages;
+  }
+  __syncthreads();
+  rows = pages = 0;
+  for (int w = 0; w < kWarps; ++w) {
+    rows += s_sum[0][w];
+    pages += s_sum[1][w];
+  }
+
+  for (int c0 = r0; c0 < r1; c0 += kPlanThreads) {  // up to kPlanThreads requests at a time
+    const int r = c0 + tid;
+    Need n{};
+    if (r < r1) n = need_of(a, r);
+    const long long ir = warp_scan(n.rows, lane), ip = warp_scan(n.pages, lane);
+    __syncthreads();  // the sums of the pass before have been read
+    if (lane == 31) {
+      s_sum[0][warp] = ir;
+      s_sum[1][warp] = ip;
+    }
+    __syncthreads();
+    long long row = rows + ir - n.rows, page = pages + ip - n.pages;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) {
+        row += s_sum[0][w];
+        page += s_sum[1][w];
+      }
+      rows += s_sum[0][w];
+      pages += s_sum[1][w];
+    }
+    s_row[tid] = row;
+    s_page[tid] = page;
+    if (r < r1 && slice == 0) {
+      a.query_start[r] = (int)min(row, (long long)a.T);
+      a.seq_lens[r] = (int)n.len;
+      if (n.bad || row + n.rows > a.T) atomicOr(a.status, kStatusBadLength);
+    }
+    __syncthreads();
+    for (int i = warp; i < min(kPlanThreads, r1 - c0); i += kWarps) {  // one warp per request
+      const Need m = need_of(a, c0 + i);
+      const long long first_row = s_row[i], first_page = s_page[i];
+      int* tab = a.block_table + (long long)(c0 + i) * a.max_pages;
+      auto fresh = [&](long long x) { return first_page + x < avail ? a.free_pages[head + first_page + x] : -1; };
+      for (int x = slice * 32 + lane; x < m.pages; x += 32 * slices) {
+        tab[m.held + x] = fresh(x);
+        if (first_page + x >= avail) atomicOr(a.status, kStatusNoPages);
+      }
+      const long long n_rows = min(m.rows, (long long)a.T - first_row);
+      for (long long x = slice * 32 + lane; x < n_rows; x += 32 * slices) {
+        const long long pos = m.ctx + x;
+        const long long pi = pos >> a.page_shift;
+        int slot = -1;
+        if (pi < a.max_pages) {
+          const long long pg = pi < m.held ? tab[pi] : fresh(pi - m.held);
+          const long long at = (pg << a.page_shift) + (pos & ((1 << a.page_shift) - 1));
+          if (pg >= 0 && at <= INT32_MAX)
+            slot = (int)at;
+          else if (pi < m.held || pg >= 0)
+            atomicOr(a.status, kStatusBadLength);
+        }
+        a.slots[first_row + x] = slot;
+      }
+    }
+  }
+  if (r1 == a.R) {  // the last group knows the totals
+    if (slice == 0 && tid == 0) {
+      a.query_start[a.R] = (int)min(rows, (long long)a.T);
+      *a.pages_taken = (int)min(pages, avail);
+    }
+    for (long long t = rows + slice * kPlanThreads + tid; t < a.T; t += (long long)kPlanThreads * slices)
+      a.slots[t] = -1;
+  }
+}
+
+// x / f for an E4M3 code, rounded once: the quotient truncated to 24 bits with
+// its last bit set when something was cut off (rounding to odd) rounds to the
+// code's 4 bits as the exact quotient would, ties among them.
+__device__ __forceinline__ float quotient_odd(float x, float f) {
+  const float q = __fdiv_rz(x, f);
+  const bool inexact = isfinite(q) && __fmaf_rn(-q, f, x) != 0.f;
+  return inexact ? __uint_as_float(__float_as_uint(q) | 1u) : q;
+}
+
+// Four values to E4M3 codes, nearest even, +-448 beyond, NaN for NaN.
+__device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
+  uint32_t r;
+  asm("{\n .reg .b16 lo, hi;\n cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n"
+      " mov.b32 %0, {lo, hi};\n}\n"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t quantise4(uint32_t lo, uint32_t hi, float f) {
+  return e4m3x4(quotient_odd(__uint_as_float(lo << 16), f), quotient_odd(__uint_as_float(lo & 0xffff0000u), f),
+                quotient_odd(__uint_as_float(hi << 16), f), quotient_odd(__uint_as_float(hi & 0xffff0000u), f));
+}
+
+// 16 bytes of a row (8 elements) per thread, keys in grid.y 0, values in 1.
+template <bool FP8>
+__global__ void __launch_bounds__(256) fa_paged_store_kernel(const __grid_constant__ StoreArgs a) {
+  const unsigned per_row = (unsigned)a.d / 8u, per_token = (unsigned)a.Hkv * per_row;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const long long t = i / per_token;
+  if (t >= a.T) return;
+  const int slot = a.slots[t];
+  if (slot < 0) return;
+  const long long page = slot >> a.page_shift;
+  if (page >= a.num_pages) {
+    atomicOr(a.status, kStatusBadLength);
+    return;
+  }
+  const unsigned x = (unsigned)(i - t * per_token), h = x / per_row, c = x - h * per_row;
+  const bool value = blockIdx.y != 0;
+  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(value ? a.v : a.k) +
+                             t * (value ? a.v_stride : a.k_stride) + (long long)x * 8;
+  const uint4 w = __ldg(reinterpret_cast<const uint4*>(src));
+  const long long row = ((page * a.Hkv + h) << a.page_shift) + (slot & ((1 << a.page_shift) - 1));
+  uint8_t* cache = static_cast<uint8_t*>(value ? a.v_cache : a.k_cache);
+  const long long at = row * a.d + c * 8;
+  if constexpr (FP8) {
+    const float f = value ? a.descale_v : a.descale_k;
+    *reinterpret_cast<uint2*>(cache + at) = make_uint2(quantise4(w.x, w.y, f), quantise4(w.z, w.w, f));
+  } else {
+    *reinterpret_cast<uint4*>(cache + at * 2) = w;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_plan(const PlanArgs& args, int num_sms, cudaStream_t stream) {
+  PlanArgs a = args;
+  // a warp per request where there are few, and several slices of the tokens
+  // where the rows outnumber the requests by far
+  const int groups = std::max(1, std::min((a.R + 7) / 8, 2 * num_sms));
+  a.group = (a.R + groups - 1) / groups;
+  const int n = (a.R + a.group - 1) / a.group;
+  const int slices = std::max(1, std::min(2 * num_sms / n, (a.T / a.R + 255) / 256));
+  fa_paged_plan_kernel<<<dim3((unsigned)n, (unsigned)slices), kPlanThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_store(const StoreArgs& a, cudaStream_t stream) {
+  const long long n = (long long)a.T * a.Hkv * (a.d / 8);
+  if (n > (long long)INT32_MAX * 256) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)((n + 255) / 256), 2u);
+  if (a.fp8)
+    fa_paged_store_kernel<true><<<grid, 256, 0, stream>>>(a);
+  else
+    fa_paged_store_kernel<false><<<grid, 256, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace fa

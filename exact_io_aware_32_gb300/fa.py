@@ -4,12 +4,14 @@ Argument marshalling only: every step of attention runs in the CUDA kernels
 of the library. The functions named like the C ABI (``fa_fwd``, ``fa_fwd_kv``,
 ``fa_fwd_kv_workspace_bytes``, ``fa_fwd_fp8``, ``fa_fwd_dropout``, ``fa_bwd_dropout``, ``fa_bwd``, ``fa_bwd_workspace_bytes``, ``fa_bwd_kv``,
 ``fa_bwd_kv_workspace_bytes``,
-``fa_status_string``, ``fa_device_status``, ``fa_bwd_noalloc``, ``fa_test_arm_fault``) take either
+``fa_status_string``, ``fa_device_status``, ``fa_bwd_noalloc``, ``fa_test_arm_fault``, ``fa_paged_plan``,
+``fa_paged_store``, ``fa_fwd_paged``, ``fa_fwd_paged_workspace_bytes``) take either
 torch CUDA tensors or raw device addresses (ints). ``attention`` is a
 differentiable torch.autograd.Function over the forward and backward calls; ``forward``,
 ``forward_kv``, ``forward_fp8``, ``forward_dropout``, ``backward``, ``backward_kv`` and
 ``backward_dropout`` are conveniences that
-allocate the outputs with torch.
+allocate the outputs with torch. ``paged_plan``, ``paged_store`` and ``forward_paged`` do the same for
+serving from a paged key/value cache.
 
 If the library has not been built, or cannot be loaded, every call raises:
 there is no fallback implementation.
@@ -30,10 +32,12 @@ FA_ERR_MISALIGNED = 3
 FA_ERR_WORKSPACE = 4
 FA_ERR_LAUNCH = 5
 FA_ERR_TIMEOUT = 6
+FA_ERR_NO_PAGES = 7
 
 EXPORTED = ("fa_fwd", "fa_fwd_kv", "fa_fwd_kv_workspace_bytes", "fa_fwd_fp8", "fa_fwd_dropout", "fa_bwd",
             "fa_bwd_workspace_bytes", "fa_bwd_kv", "fa_bwd_kv_workspace_bytes", "fa_bwd_dropout", "fa_status_string",
-            "fa_device_status", "fa_bwd_noalloc", "fa_test_arm_fault")
+            "fa_device_status", "fa_bwd_noalloc", "fa_test_arm_fault", "fa_paged_plan", "fa_paged_store",
+            "fa_fwd_paged", "fa_fwd_paged_workspace_bytes")
 
 _lock = threading.Lock()
 _lib = None
@@ -93,6 +97,17 @@ def load(path: str | None = None):
         lib.fa_device_status.restype = c_int
         lib.fa_test_arm_fault.argtypes = [c_int]
         lib.fa_test_arm_fault.restype = c_int
+        c_i64 = ctypes.c_longlong
+        lib.fa_paged_plan.argtypes = [vp, vp, c_int, c_int, vp, c_int, vp, vp, c_int, vp, vp, vp, c_int, vp, vp]
+        lib.fa_paged_plan.restype = c_int
+        lib.fa_paged_store.argtypes = [vp, vp, c_i64, c_i64, vp, c_int, c_int, c_int, vp, vp, c_int, c_int, c_int,
+                                       c_float, c_float, vp]
+        lib.fa_paged_store.restype = c_int
+        lib.fa_fwd_paged_workspace_bytes.argtypes = [c_int, c_int, c_int, c_int, c_int, c_int]
+        lib.fa_fwd_paged_workspace_bytes.restype = c_size_t
+        lib.fa_fwd_paged.argtypes = [vp, c_i64, vp, vp, c_int, c_float, c_float, vp, c_int, vp, vp, vp, vp, c_int,
+                                     c_int, c_int, c_int, c_int, c_int, c_int, c_int, c_float, c_int, vp, c_size_t, vp]
+        lib.fa_fwd_paged.restype = c_int
         if path is None:
             _lib = lib
         return lib
@@ -407,3 +422,175 @@ def fa_bwd_noalloc(q, k, v, o, lse, dO, dq, dk, dv, B: int, H: int, N: int, d: i
         fn.restype = c_int
     return int(fn(_addr(q), _addr(k), _addr(v), _addr(o), _addr(lse), _addr(dO), _addr(dq), _addr(dk), _addr(dv),
                   B, H, N, d, float(scale), int(bool(causal)), _stream(stream)))
+
+
+# ---------------------------------------------------------------- paged key/value cache
+def fa_paged_plan(ctx_lens, new_lens, R: int, page_size: int, free_pages, n_free: int, free_head, block_table,
+                  max_pages: int, query_start, seq_lens, slots, T: int, pages_taken, stream=None) -> int:
+    return load().fa_paged_plan(_addr(ctx_lens), _addr(new_lens), R, page_size, _addr(free_pages), n_free,
+                                _addr(free_head), _addr(block_table), max_pages, _addr(query_start), _addr(seq_lens),
+                                _addr(slots), T, _addr(pages_taken), _stream(stream))
+
+
+def fa_paged_store(k, v, k_stride: int, v_stride: int, slots, T: int, Hkv: int, d: int, k_cache, v_cache,
+                   num_pages: int, page_size: int, fp8: bool, descale_k: float, descale_v: float, stream=None) -> int:
+    return load().fa_paged_store(_addr(k), _addr(v), k_stride, v_stride, _addr(slots), T, Hkv, d, _addr(k_cache),
+                                 _addr(v_cache), num_pages, page_size, int(bool(fp8)), descale_k, descale_v,
+                                 _stream(stream))
+
+
+def fa_fwd_paged_workspace_bytes(T: int, R: int, Hq: int, Hkv: int, d: int, max_new: int) -> int:
+    return int(load().fa_fwd_paged_workspace_bytes(T, R, Hq, Hkv, d, max_new))
+
+
+def fa_fwd_paged(q, q_stride: int, k_cache, v_cache, fp8: bool, descale_k: float, descale_v: float, block_table,
+                 max_pages: int, query_start, seq_lens, o, lse, T: int, R: int, Hq: int, Hkv: int, d: int,
+                 num_pages: int, page_size: int, max_new: int, scale: float, causal: bool, workspace,
+                 workspace_bytes: int, stream=None) -> int:
+    return load().fa_fwd_paged(_addr(q), q_stride, _addr(k_cache), _addr(v_cache), int(bool(fp8)), descale_k,
+                               descale_v, _addr(block_table), max_pages, _addr(query_start), _addr(seq_lens), _addr(o),
+                               _addr(lse), T, R, Hq, Hkv, d, num_pages, page_size, max_new, scale, int(bool(causal)),
+                               _addr(workspace), workspace_bytes, _stream(stream))
+
+
+def _ints(device, *named):
+    """Lengths, tables and slots as the library takes them: (name, tensor, shape), int32, contiguous, on ``device``."""
+    import torch
+
+    for name, x, shape in named:
+        if x.dtype != torch.int32 or x.device != device or not x.is_contiguous() or tuple(x.shape) != shape:
+            raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)} on {device}")
+
+
+def _packed(name, x, device):
+    """A packed [T, heads, d] bf16 tensor whose rows of one token are contiguous; returns its token stride."""
+    import torch
+
+    if x.dim() != 3 or x.dtype != torch.bfloat16 or x.device != device:
+        raise ValueError(f"{name} must be a bf16 tensor [T, heads, d] on {device}")
+    T, H, d = x.shape
+    st, sh, sd = x.stride()
+    if (sd != 1 and d > 1) or (sh != d and H > 1):
+        raise ValueError(f"the rows of one token of {name} must be contiguous")
+    return st if T > 1 else max(st - st % 8, H * d)  # one token: its stride is not used
+
+
+def _cache(k_cache, v_cache):
+    """Shape (num_pages, Hkv, page_size, d) of a cache pair, and whether it holds E4M3 codes."""
+    import torch
+
+    fp8 = k_cache.dtype in (torch.uint8, torch.float8_e4m3fn)
+    if k_cache.dim() != 4 or not (fp8 or k_cache.dtype == torch.bfloat16):
+        raise ValueError("the caches must be [num_pages, Hkv, page_size, d] tensors, bf16 or E4M3 codes")
+    if (v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or v_cache.device != k_cache.device
+            or not k_cache.is_contiguous() or not v_cache.is_contiguous() or not k_cache.is_cuda):
+        raise ValueError("k_cache and v_cache must be contiguous CUDA tensors of one shape, type and device")
+    return *k_cache.shape, fp8
+
+
+def _on_device(device, stream):
+    """The context in which a helper allocates and launches: the tensors' device, and the stream asked for."""
+    import contextlib
+
+    import torch
+
+    if stream is None:
+        if device.index == torch.cuda.current_device():
+            return contextlib.nullcontext()
+        return torch.cuda.device(device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    elif stream.device != device:
+        raise ValueError(f"the stream must belong to {device}")
+    return torch.cuda.stream(stream)
+
+
+def paged_plan(ctx_lens, new_lens, block_table, free_pages, page_size: int, num_tokens: int, free_head=None, out=None,
+               stream=None):
+    """Plan a step of R requests: pages for their new tokens out of ``free_pages`` (from entry ``free_head`` on, an
+    int32 [1] tensor) into ``block_table`` [R, max_pages] (in place), and where each of the ``num_tokens`` packed
+    rows goes. All tensors int32 on the GPU. Returns (query_start [R + 1], seq_lens [R], slots [num_tokens],
+    pages_taken [1]); ``out``: the four tensors to write them into."""
+    import torch
+
+    dev = ctx_lens.device
+    if dev.type != "cuda" or ctx_lens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
+        raise ValueError("expected CUDA tensors ctx_lens [R], block_table [R, max_pages], free_pages [n]")
+    R, max_pages, n_free = int(ctx_lens.shape[0]), int(block_table.shape[1]), int(free_pages.shape[0])
+    _ints(dev, ("ctx_lens", ctx_lens, (R,)), ("new_lens", new_lens, (R,)), ("free_pages", free_pages, (n_free,)),
+          ("block_table", block_table, (R, max_pages)))
+    if free_head is not None:
+        _ints(dev, ("free_head", free_head, (1,)))
+    with _on_device(dev, stream):
+        if out is None:
+            out = tuple(torch.empty(n, dtype=torch.int32, device=dev) for n in (R + 1, R, num_tokens, 1))
+        else:
+            _ints(dev, *zip(("query_start", "seq_lens", "slots", "pages_taken"), out,
+                            ((R + 1,), (R,), (num_tokens,), (1,))))
+        # an empty list has no address: any valid one will do, since none of its entries is read
+        st = fa_paged_plan(ctx_lens, new_lens, R, page_size, free_pages if n_free else out[3], n_free, free_head,
+                           block_table, max_pages, out[0], out[1], out[2], num_tokens, out[3])
+    if st != FA_OK:
+        raise FAError(st, "fa_paged_plan")
+    return out
+
+
+def paged_store(k, v, slots, k_cache, v_cache, descale_k: float = 1.0, descale_v: float = 1.0, stream=None) -> None:
+    """Store the new tokens' k, v ([T, Hkv, d] bf16, slices of a projection's output allowed) into the caches
+    [num_pages, Hkv, page_size, d] (bf16, or E4M3 codes of value / descale) at ``slots`` [T] (int32; negative:
+    nowhere)."""
+    P, Hkv, ps, d, fp8 = _cache(k_cache, v_cache)
+    dev = k_cache.device
+    ks, vs = _packed("k", k, dev), _packed("v", v, dev)
+    T = int(k.shape[0])
+    if tuple(k.shape) != (T, Hkv, d) or tuple(v.shape) != (T, Hkv, d):
+        raise ValueError(f"k and v must be [T, {Hkv}, {d}], as the caches")
+    _ints(dev, ("slots", slots, (T,)))
+    with _on_device(dev, stream):
+        st = fa_paged_store(k, v, ks, vs, slots, T, Hkv, d, k_cache, v_cache, P, ps, fp8, descale_k, descale_v)
+    if st != FA_OK:
+        raise FAError(st, "fa_paged_store")
+
+
+def forward_paged(q, k_cache, v_cache, block_table, query_start, seq_lens, max_new: int | None = None,
+                  causal: bool = True, scale: float | None = None, descale_k: float = 1.0, descale_v: float = 1.0,
+                  out=None, lse=None, workspace=None, stream=None):
+    """Attention of the packed new tokens q [T, Hq, d] (bf16) over the paged caches, which hold their keys and values
+    already (paged_store): request r has rows query_start[r] .. query_start[r + 1] - 1, seq_lens[r] keys and the pages
+    of block_table[r]. ``max_new``: the most new tokens a request has, if known (only speed depends on it). ``out``
+    and ``lse`` are written in place if given, rows of no request left as they are (zeros in the ones allocated
+    here). Returns (o [T, Hq, d], lse [T, Hq])."""
+    import torch
+
+    P, Hkv, ps, d, fp8 = _cache(k_cache, v_cache)
+    dev = k_cache.device
+    qs = _packed("q", q, dev)
+    T, Hq = int(q.shape[0]), int(q.shape[1])
+    if int(q.shape[2]) != d or block_table.dim() != 2 or query_start.dim() != 1:
+        raise ValueError(f"expected q [T, Hq, {d}], block_table [R, max_pages], query_start [R + 1]")
+    R, max_pages = int(block_table.shape[0]), int(block_table.shape[1])
+    _ints(dev, ("block_table", block_table, (R, max_pages)), ("query_start", query_start, (R + 1,)),
+          ("seq_lens", seq_lens, (R,)))
+    max_new = T if max_new is None else max_new
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    need = fa_fwd_paged_workspace_bytes(T, R, Hq, Hkv, d, max_new)
+    with _on_device(dev, stream):
+        if out is None:
+            out = torch.zeros((T, Hq, d), dtype=torch.bfloat16, device=dev)
+        elif out.dtype != torch.bfloat16 or tuple(out.shape) != (T, Hq, d) or not out.is_contiguous() \
+                or out.device != dev:
+            raise ValueError(f"out must be a contiguous bf16 tensor [{T}, {Hq}, {d}] on {dev}")
+        if lse is None:
+            lse = torch.zeros((T, Hq), dtype=torch.float32, device=dev)
+        elif lse.dtype != torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous() or lse.device != dev:
+            raise ValueError(f"lse must be a contiguous fp32 tensor [{T}, {Hq}] on {dev}")
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        elif workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        st = fa_fwd_paged(q, qs, k_cache, v_cache, fp8, descale_k, descale_v, block_table, max_pages, query_start,
+                          seq_lens, out, lse, T, R, Hq, Hkv, d, P, ps, max_new, scale, causal, workspace,
+                          workspace.numel() * workspace.element_size())
+    if st != FA_OK:
+        raise FAError(st, "fa_fwd_paged")
+    return out, lse

@@ -62,7 +62,8 @@ typedef enum {
   FA_ERR_MISALIGNED = 3,  /* a pointer is not 16-byte aligned */
   FA_ERR_WORKSPACE = 4,   /* workspace pointer null or smaller than required */
   FA_ERR_LAUNCH = 5,      /* the CUDA runtime rejected a launch or a query */
-  FA_ERR_TIMEOUT = 6      /* a kernel gave up waiting (reported by fa_device_status) */
+  FA_ERR_TIMEOUT = 6,     /* a kernel gave up waiting (reported by fa_device_status) */
+  FA_ERR_NO_PAGES = 7     /* fa_paged_plan found too few free pages (reported by fa_device_status) */
 } fa_status;
 
 /*
@@ -251,15 +252,125 @@ FA_API int fa_bwd_dropout(const void* q, const void* k, const void* v, const voi
                           int causal, int p256, unsigned long long seed, unsigned int offset, void* workspace,
                           size_t workspace_bytes, void* stream);
 
+/*
+ * The paged key/value cache: serving keeps the keys and values of its requests
+ * in pages of a fixed number of tokens, so that requests of any length share
+ * one pool without moving. The pages that this library follows name decoding
+ * against a long cache as the next step; the paged layout is this library's
+ * own choice.
+ *   - k_cache, v_cache: [num_pages, Hkv, page_size, d], contiguous, bf16 or
+ *     (fp8 != 0) E4M3 codes with one dequantisation factor per tensor: a code
+ *     c stands for descale * c. page_size is 16, 32, 64, 128 or 256.
+ *   - block_table: device int32 [R, max_pages]: entry i of row r is the page
+ *     that holds tokens [i * page_size, (i + 1) * page_size) of request r.
+ *     Entries past a request's length are not read. Requests may share pages.
+ *   - slot: page * page_size + place in the page, the place of one token.
+ *   - The new tokens of all requests are packed: request r has rows
+ *     query_start[r] .. query_start[r + 1] - 1 of T rows (device int32
+ *     [R + 1], not decreasing). Rows from query_start[R] on belong to no
+ *     request (a batch padded to a captured graph's size).
+ *   - q, k, v of the new tokens are [T, heads, d] bf16 whose rows of one token
+ *     are contiguous; *_stride is the distance between tokens in elements (at
+ *     least heads * d, a multiple of 8), so slices of one projection's output
+ *     are passed as they are.
+ * All lengths, tables and slots are read on the device: nothing here waits
+ * for the GPU, and a step can be captured in a graph and replayed with other
+ * lengths. What is out of range there is never followed: it is left out, as
+ * said at each call, and reported by fa_device_status.
+ */
+
+/*
+ * Plans a step: gives each request the pages that its new tokens need, in the
+ * order of the requests, and says where every new token goes.
+ *   ctx_lens, new_lens [in]  device int32 [R]: tokens already in the cache, and new tokens of this step (>= 0)
+ *   free_pages     [in]      device int32 [n_free]: pages that nobody uses, in the order in which they are taken
+ *   free_head      [in]      device int32 [1]: the first entry of free_pages still free (NULL: 0)
+ *   block_table    [in, out] device int32 [R, max_pages]: the entries of request r from
+ *                            ceil(ctx / page_size) up to ceil((ctx + new) / page_size) - 1 are
+ *                            written, in order, with the pages taken; no other entry is
+ *   query_start    [out]     device int32 [R + 1]: prefix sums of new_lens
+ *   seq_lens       [out]     device int32 [R]: ctx + new
+ *   slots          [out]     device int32 [T]: the slot of each packed row; -1 for rows from query_start[R] on
+ *   pages_taken    [out]     device int32 [1]: entries of free_pages taken
+ * Nothing but the four outputs and the table entries is changed, so the same
+ * call again gives the same plan; the caller moves free_head on.
+ * Reported by fa_device_status: FA_ERR_INVALID_ARG for a negative length
+ * (taken as 0), a request longer than max_pages pages or more than T new
+ * tokens (the tokens past either get slot -1 or no row; seq_lens and
+ * query_start stay within them), or a token whose page among those already
+ * held is negative (slot -1); FA_ERR_NO_PAGES when free_pages runs out (the
+ * entries and slots that lack a page are -1).
+ * Returns FA_OK or an fa_status error code.
+ */
+FA_API int fa_paged_plan(const int* ctx_lens, const int* new_lens, int R, int page_size, const int* free_pages,
+                         int n_free, const int* free_head, int* block_table, int max_pages, int* query_start,
+                         int* seq_lens, int* slots, int T, int* pages_taken, void* stream);
+
+/*
+ * Stores the new tokens' keys and values into the cache.
+ *   k, v     [in]  bf16 [T, Hkv, d] with token strides k_stride, v_stride
+ *   slots    [in]  device int32 [T]: row t goes to slots[t]; negative: nowhere
+ *   k_cache, v_cache [out] as above; no other slot is changed
+ *   fp8      0: bf16 caches (descale_k, descale_v are not looked at); else E4M3: the code nearest to
+ *            x / descale (ties to even), +-448 beyond, NaN for NaN; the quotient is rounded once
+ * Slots that are not negative must be distinct (two rows in one slot leave
+ * either's elements). A slot past the cache is left out and reported by
+ * fa_device_status as FA_ERR_INVALID_ARG.
+ * Returns FA_OK or an fa_status error code.
+ */
+FA_API int fa_paged_store(const void* k, const void* v, long long k_stride, long long v_stride, const int* slots,
+                          int T, int Hkv, int d, void* k_cache, void* v_cache, int num_pages, int page_size, int fp8,
+                          float descale_k, float descale_v, void* stream);
+
+/*
+ * Attention of the new tokens over the cache, which already holds their own
+ * keys and values: the forward of fa_fwd_kv with packed queries, grouped
+ * heads, paged keys and all lengths on the device. One new token (decoding),
+ * chunks of a prompt and both in one batch are the same call.
+ *   q        [in]  bf16 [T, Hq, d] with token stride q_stride; query head h reads key head
+ *                  h / (Hq / Hkv) (Hq a multiple of Hkv, at most 128 times it)
+ *   k_cache, v_cache, block_table, query_start as above
+ *   seq_lens [in]  device int32 [R]: keys of each request, its new tokens included
+ *   o        [out] bf16 [T, Hq, d], contiguous
+ *   lse      [out] fp32 [T, Hq], the logsumexp of each row's visible scaled scores
+ *   max_new  what the caller knows of the most new tokens a request has; it
+ *            only chooses how the work is laid out, any value >= 1 is right
+ *   scale    as in fa_fwd; with fp8 the keys and values are descale * code
+ *   causal   != 0: new token i of n sees keys 0 .. seq_len - n + i; else every key of its request
+ *   workspace, workspace_bytes
+ *            at least fa_fwd_paged_workspace_bytes bytes, 256-byte aligned;
+ *            contents on entry do not matter; not shared by calls that may run at once
+ * A row that sees no key (seq_len 0, or smaller than the new tokens under the
+ * mask) gets o = 0, lse = -inf. Rows that belong to no request are left as
+ * they were. What the cache holds past a request's last key (unwritten slots,
+ * NaN among them) never reaches a result; keys hidden by the causal mask only
+ * must hold finite values. A page outside the cache reads as zeros, a
+ * seq_len past max_pages pages is cut, a negative one is 0, query_start is
+ * cut into [0, T], and a request that ends before it starts has no rows; each
+ * is reported by fa_device_status as FA_ERR_INVALID_ARG.
+ * Results do not depend on what else is in the batch beyond rounding (the
+ * keys of a request are split over the GPU by the lengths of all); repeated
+ * calls give identical bits.
+ * Returns FA_OK or an fa_status error code.
+ */
+FA_API size_t fa_fwd_paged_workspace_bytes(int T, int R, int Hq, int Hkv, int d, int max_new);
+FA_API int fa_fwd_paged(const void* q, long long q_stride, const void* k_cache, const void* v_cache, int fp8,
+                        float descale_k, float descale_v, const int* block_table, int max_pages,
+                        const int* query_start, const int* seq_lens, void* o, float* lse, int T, int R, int Hq,
+                        int Hkv, int d, int num_pages, int page_size, int max_new, float scale, int causal,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static, human-readable name of a status code. Never NULL. */
 FA_API const char* fa_status_string(int status);
 
 /*
  * Reads (and, if reset != 0, clears) the device-side error word that kernels
  * set when one of their internal waits exceeds its time limit, or when a
- * per-sequence length was out of range, on the current device. Synchronises
- * the device. Returns FA_OK, FA_ERR_TIMEOUT (a wait gave up), FA_ERR_INVALID_ARG
- * (only lengths were out of range), or FA_ERR_LAUNCH if the word cannot be read.
+ * per-sequence length, slot or page was out of range, or when a plan ran out of
+ * free pages, on the current device. Synchronises the device. Returns FA_OK,
+ * FA_ERR_TIMEOUT (a wait gave up), else FA_ERR_NO_PAGES (a plan ran out), else
+ * FA_ERR_INVALID_ARG (only lengths, slots or pages were out of range), or
+ * FA_ERR_LAUNCH if the word cannot be read.
  */
 FA_API int fa_device_status(int reset);
 
