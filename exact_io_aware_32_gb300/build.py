@@ -19,8 +19,9 @@ LIB = os.path.join(BUILD, "libfa.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd_persist.cu", "fa_bwd.cu", "fa_bwd_noalloc.cu", "schedule.cu", "paged_api.cu",
-           "paged_cache.cu", "paged_fwd.cu"]
-HEADERS = ["ptx.cuh", "block_order.cuh", "fa_internal.h", "philox.cuh", "paged.h"]
+           "paged_cache.cu", "paged_fwd.cu", "paged_few.cu", "paged_chunk.cu"]
+HEADERS = ["ptx.cuh", "block_order.cuh", "fa_internal.h", "philox.cuh", "paged.h",
+           "paged_work.cuh", "paged_pipe.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-diag-suppress", "177"]

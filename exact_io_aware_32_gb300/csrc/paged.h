@@ -1,6 +1,7 @@
 // Internal interface of the paged key/value cache's kernels (paged_api.cu calls
 // the launchers of paged_cache.cu and paged_fwd.cu).
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <cstddef>
 
@@ -38,10 +39,40 @@ struct PagedArgs {
   int T, R, Hq, Hkv, d, num_pages, page_shift, max_pages, causal, fp8;
   float scale_log2;  // scale * log2(e), times the key factor
   float o_scale;     // the value factor
+  int max_keys;      // max_pages pages of keys
+  // set by launch_paged
+  CUtensorMap tm_q;         // bf16 [T][Hq][d], box 64 x (Hq / Hkv) x tokens of a 128-row (32-row) tile, 128B swizzle
+  CUtensorMap tm_k, tm_v;   // [num_pages * Hkv][page_size][d], boxes of a page's rows up to 128: bf16 64 columns wide
+                            // with 128B swizzle, or E4M3 whole rows unswizzled
+  int tpt;                  // tokens per tile
+  int tpt1;                 // tokens per 128-row half of a tile (two halves at d = 128)
+  void* parts;              // Parts per CTA, then the cut tiles' results, in the caller's workspace
+  float* part_o;            // fp32 [CTA][2][rows][d]: O / l of a leading (0) and an opening (1) piece
+  float* part_lse;          // fp32 [CTA][2][rows]: their logsumexps in log2 units
+  int test_fault;           // as in FwdArgs
+};
+
+// How a call is laid out (see launch_paged).
+struct PagedPlan {
+  bool few;       // the kernel for at most 32 rows per tile
+  int ctas;       // persistent CTAs
+  int rows;       // rows of a tile
+  int tpt, tpt1;
+  size_t parts_bytes, o_bytes, lse_bytes;  // of the workspace, each a multiple of 256
 };
 
 cudaError_t launch_plan(const PlanArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_store(const StoreArgs& a, cudaStream_t stream);
-cudaError_t launch_paged(const PagedArgs& a, int num_sms, cudaStream_t stream);
+PagedPlan plan_paged(int Hq, int Hkv, int d, int fp8, int max_new, int num_sms);
+// Encodes the tensor maps too; cudaErrorInvalidValue if that fails.
+cudaError_t launch_paged(PagedArgs a, const PagedPlan& p, cudaStream_t stream);
+// The two kernels (paged_few.cu, paged_chunk.cu) and the join of cut tiles.
+cudaError_t launch_paged_few(const PagedArgs& a, int ctas, cudaStream_t stream);
+cudaError_t launch_paged_chunk(const PagedArgs& a, int ctas, cudaStream_t stream);
+// Tensor map of rank 3 (sizes and box innermost first, strides in bytes), 128-byte swizzle or none.
+bool encode_map3(CUtensorMap* m, const void* base, CUtensorMapDataType type, const unsigned long long (&dims)[3],
+                 const unsigned long long (&strides)[2], const unsigned (&box)[3], bool swizzle);
+// Takes the fault that fa_test_arm_fault armed (0: none).
+int take_test_fault();
 
 }  // namespace fa

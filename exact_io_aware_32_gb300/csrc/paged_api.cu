@@ -2,6 +2,7 @@
 // checks and kernel launches.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -37,6 +38,9 @@ int check_stride(long long stride, int heads, int d) {
 }
 
 bool factor(float x) { return std::isfinite(x) && x > 0.f; }
+
+// SMs that a workspace is made for (the GPU has 152), so that its size does not depend on the device.
+constexpr int kMaxSms = 160;
 
 constexpr double kLog2e = 1.4426950408889634074;
 
@@ -118,7 +122,13 @@ int fa_paged_store(const void* k, const void* v, long long k_stride, long long v
 }
 
 size_t fa_fwd_paged_workspace_bytes(int T, int R, int Hq, int Hkv, int d, int max_new) {
-  return check_paged(T, R, Hq, Hkv, d, max_new) == FA_OK ? 256 : 0;
+  if (check_paged(T, R, Hq, Hkv, d, max_new) != FA_OK) return 0;
+  size_t most = 0;
+  for (int fp8 = 0; fp8 < 2; ++fp8) {  // one size for both kinds of cache
+    const fa::PagedPlan p = fa::plan_paged(Hq, Hkv, d, fp8, max_new, kMaxSms);
+    most = std::max(most, p.parts_bytes + p.o_bytes + p.lse_bytes);
+  }
+  return most;
 }
 
 int fa_fwd_paged(const void* q, long long q_stride, const void* k_cache, const void* v_cache, int fp8,
@@ -166,7 +176,14 @@ int fa_fwd_paged(const void* q, long long q_stride, const void* k_cache, const v
   a.fp8 = fp8 ? 1 : 0;
   a.scale_log2 = scale_log2;
   a.o_scale = fp8 ? descale_v : 1.0f;
-  return fa::launch_paged(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+  a.max_keys = max_pages * page_size;
+  const fa::PagedPlan p = fa::plan_paged(Hq, Hkv, d, a.fp8, max_new, std::min(sms, kMaxSms));
+  char* w = static_cast<char*>(workspace);
+  a.parts = w;
+  a.part_o = reinterpret_cast<float*>(w + p.parts_bytes);
+  a.part_lse = reinterpret_cast<float*>(w + p.parts_bytes + p.o_bytes);
+  a.test_fault = fa::take_test_fault();
+  return fa::launch_paged(a, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
 }  // extern "C"

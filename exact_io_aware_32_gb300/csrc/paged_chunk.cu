@@ -1,0 +1,504 @@
+// Attention of chunks of new tokens over the paged cache, on sm_103a.
+//
+// The blocked loop of fa_fwd.cu (S = Q K^T on tcgen05 into TMEM, softmax with a
+// running maximum and one TMEM lane per query row, O += P V with P read back
+// from TMEM) with three things of its own:
+//   - a tile's 128 rows are the new tokens of one request times the query heads
+//     that share a key head (row = token * G + head), so grouped heads read
+//     each key and value once; one TMA box of 64 x G x tokens fetches them;
+//   - a key block's copies come from its pages, one per lane of the loading
+//     warp, each at the page that the block table names;
+//   - the CTAs are persistent and each runs its range of the row of tiles
+//     (paged_work.cuh); the rings and barriers count on across tiles, so the
+//     next tile's loads and first products overlap this one's epilogue.
+// Rows of O go from registers to global memory, 32 bytes per store: packed
+// tokens of neighbouring requests make a tile's rows no rectangle that a
+// tensor store could write.
+//
+// Warp roles: a softmax warpgroup per 128-row half, the TMA warp, the MMA warp,
+// and with E4M3 caches a warpgroup that turns each 8-bit block into the bf16
+// operands of the products (TMA -> 8-bit ring -> converters -> K/V rings).
+#include "paged_pipe.cuh"
+
+namespace fa {
+namespace {
+
+using namespace fa::ptx;
+using namespace fa::paged;
+
+template <int D_, bool FP8_>
+struct CCfg {
+  static constexpr int D = D_;
+  static constexpr bool FP8 = FP8_;
+  // At d = 64 bf16 one 128-row tile per CTA and two CTAs per SM, as in fa_fwd.cu;
+  // otherwise two halves of 128 rows that share the key blocks.
+  static constexpr int kTiles = D == 64 && !FP8 ? 1 : 2;
+  static constexpr int kCtasPerSm = 3 - kTiles;
+  static constexpr int kPanels = D / 64;
+  static constexpr int kTileBytes = kPanels * 16384;  // 128 rows, bf16
+  static constexpr int kCodeBytes = 128 * D;          // 128 rows of codes
+  static constexpr int kKStages = 2, kVStages = FP8 && D == 128 ? 2 : 3;
+  static constexpr int kCStages = FP8 ? (D == 128 ? 2 : 4) : 0;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kOffQ + kTiles * kTileBytes;
+  static constexpr int kOffV = kOffK + kKStages * kTileBytes;
+  static constexpr int kOffC = kOffV + kVStages * kTileBytes;
+  static constexpr int kOffBar = kOffC + kCStages * kCodeBytes;
+  static constexpr int kSmemBytes = kOffBar + 1024 + 1024;  // barriers, alignment slack
+  static_assert(kSmemBytes <= 232448 && (kCtasPerSm == 1 || 2 * (kSmemBytes + 1024) <= 233472), "shared memory");
+  static constexpr uint32_t kTmemCols = kTiles == 2 ? 512u : 256u;
+  __host__ __device__ static constexpr uint32_t col_s(int t) { return (uint32_t)t * 128u; }
+  __host__ __device__ static constexpr uint32_t col_o(int t) { return 128u * kTiles + (uint32_t)t * D; }
+  static constexpr int kWarpTma = 4 * kTiles, kWarpMma = 4 * kTiles + 1;
+  static constexpr int kWarpConv = 4 * kTiles + 2;  // four of them, with FP8
+  static constexpr int kThreads = 128 * kTiles + 64 + (FP8 ? 128 : 0);
+};
+
+struct CBars {
+  uint64_t q_full[2], q_free[2];
+  uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3], c_full[4], c_empty[4];
+  uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
+  uint64_t teardown;
+  uint32_t tmem_base;
+  int abort;
+  Range range;
+  long long sums[2][16];
+};
+static_assert(sizeof(CBars) <= 1024, "barriers exceed their shared memory");
+
+// Key blocks that each 128-row half sees of a piece (nb[t] from p.jb on).
+template <int kTiles>
+__device__ __forceinline__ void half_blocks(const PagedArgs& a, const Piece& p, int (&nb)[2]) {
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int tok = p.tok + t * a.tpt1;
+    const int blocks = t < kTiles && tok < p.q.n ? (keys_seen(a, p.q, tok + a.tpt1) + 127) >> 7 : 0;
+    nb[t] = max(0, min(blocks, p.je) - p.jb);
+  }
+}
+
+template <int D, bool FP8, bool CAUSAL>
+__global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPerSm)
+    fa_paged_chunk_kernel(const __grid_constant__ PagedArgs a) {
+  using C = CCfg<D, FP8>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  CBars& bars = *reinterpret_cast<CBars*>(smem + C::kOffBar);
+  volatile int* abort_flag = &bars.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  find_range<C::kThreads>(a, bars.range, reinterpret_cast<long long(&)[2][C::kThreads / 32]>(bars.sums));
+  if (!bars.range.some) {  // uniform: every thread leaves before any barrier
+    if (threadIdx.x == 0) static_cast<Parts*>(a.parts)[blockIdx.x] = Parts{};
+    return;
+  }
+  if (threadIdx.x == 0) {
+    bars.abort = 0;
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars.q_full[s], 1);
+      mbar_init(&bars.q_free[s], 1);
+      mbar_init(&bars.s_full[s], 1);
+      mbar_init(&bars.p_full[s], 128);
+      mbar_init(&bars.o_done[s], 1);
+      mbar_init(&bars.o_free[s], 128);
+    }
+    for (int s = 0; s < 3; ++s) {
+      mbar_init(&bars.k_full[s], FP8 ? 128 : 1);
+      mbar_init(&bars.k_empty[s], 1);
+      mbar_init(&bars.v_full[s], FP8 ? 128 : 1);
+      mbar_init(&bars.v_empty[s], 1);
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&bars.c_full[s], 1);
+      mbar_init(&bars.c_empty[s], 128);
+    }
+    mbar_init(&bars.teardown, 1);
+    fence_mbar_init();
+  }
+  if (warp == C::kWarpMma) {
+    tmem_alloc(&bars.tmem_base, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem_base;
+  Walk walk;
+  walk.begin(a, bars.range);
+  Piece p;
+
+  if (warp == C::kWarpTma) {
+    // ------------------------------------------------------------ TMA producer
+    if (elect_one()) {
+      tma_prefetch_desc(&a.tm_q);
+      tma_prefetch_desc(&a.tm_k);
+      tma_prefetch_desc(&a.tm_v);
+    }
+    __syncwarp();
+    const uint32_t q_bytes = (uint32_t)(a.Hq / a.Hkv * a.tpt1 * D * 2);
+    Parts parts{};
+    int g = 0, nk = 0, nv = 0, nc = 0, nq[2] = {0, 0};  // key blocks, and loads issued
+    bool ok = true;
+    // test hook: without the first Q tile, the MMA warp's first wait expires
+    bool withhold = a.test_fault == 1;
+    auto load_q = [&](int t) {
+      if (!(ok = warp_wait(&bars.q_free[t], (nq[t] & 1) ^ 1, abort_flag))) return;
+      if (!withhold) {
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&bars.q_full[t], q_bytes);
+          for (int pn = 0; pn < C::kPanels; ++pn)
+            tma_load_3d(smem + C::kOffQ + t * C::kTileBytes + pn * 16384, &a.tm_q, &bars.q_full[t], pn * 64,
+                        p.h * (a.Hq / a.Hkv), p.q.start + p.tok + t * a.tpt1);
+        }
+        __syncwarp();
+        ++nq[t];
+      }
+      withhold = false;
+    };
+    while (ok && walk.step(a, p)) {
+      note_piece(parts, p);
+      int nb[2];
+      half_blocks<C::kTiles>(a, p, nb);
+      const int nbm = max(nb[0], nb[1]);
+      int page = nbm > 0 ? lane_page(a, p, p.jb, lane) : -1;
+      if (nb[0] > 0) load_q(0);
+      for (int j = 0; ok && j < nbm; ++j, ++g) {
+        const int jj = p.jb + j, page_now = page;
+        if (j + 1 < nbm) page = lane_page(a, p, jj + 1, lane);
+        if constexpr (FP8) {
+          const int s0 = nc % C::kCStages;
+          if (!(ok = warp_wait(&bars.c_empty[s0], ((nc / C::kCStages) & 1) ^ 1, abort_flag))) break;
+          load_block<D, true>(a, p, jj, page_now, lane, &a.tm_k, smem + C::kOffC + s0 * C::kCodeBytes, &bars.c_full[s0]);
+          ++nc;
+        } else {
+          const int s = g % C::kKStages;
+          if (!(ok = warp_wait(&bars.k_empty[s], ((g / C::kKStages) & 1) ^ 1, abort_flag))) break;
+          load_block<D, false>(a, p, jj, page_now, lane, &a.tm_k, smem + C::kOffK + s * C::kTileBytes, &bars.k_full[s]);
+          nk = g + 1;
+        }
+        if (C::kTiles == 2 && j == 0 && nb[1] > 0) {
+          load_q(1);
+          if (!ok) break;
+        }
+        if constexpr (FP8) {
+          const int s1 = nc % C::kCStages;
+          if (!(ok = warp_wait(&bars.c_empty[s1], ((nc / C::kCStages) & 1) ^ 1, abort_flag))) break;
+          load_block<D, true>(a, p, jj, page_now, lane, &a.tm_v, smem + C::kOffC + s1 * C::kCodeBytes, &bars.c_full[s1]);
+          ++nc;
+        } else {
+          const int s = g % C::kVStages;
+          if (!(ok = warp_wait(&bars.v_empty[s], ((g / C::kVStages) & 1) ^ 1, abort_flag))) break;
+          load_block<D, false>(a, p, jj, page_now, lane, &a.tm_v, smem + C::kOffV + s * C::kTileBytes, &bars.v_full[s]);
+          nv = g + 1;
+        }
+      }
+    }
+    if (lane == 0) static_cast<Parts*>(a.parts)[blockIdx.x] = parts;
+    // Let every issued copy land before the CTA can exit (an earlier load's slot
+    // was refilled only after its reader completed, so it has landed).
+    for (int t = 0; t < C::kTiles; ++t)
+      if (nq[t] > 0) mbar_wait_drain(&bars.q_full[t], (nq[t] - 1) & 1);
+    for (int x = max(0, nk - C::kKStages); x < nk; ++x)
+      mbar_wait_drain(&bars.k_full[x % C::kKStages], (x / C::kKStages) & 1);
+    for (int x = max(0, nv - C::kVStages); x < nv; ++x)
+      mbar_wait_drain(&bars.v_full[x % C::kVStages], (x / C::kVStages) & 1);
+    if constexpr (FP8)
+      for (int x = max(0, nc - C::kCStages); x < nc; ++x)
+        mbar_wait_drain(&bars.c_full[x % C::kCStages], (x / C::kCStages) & 1);
+  } else if (warp == C::kWarpMma) {
+    // ------------------------------------------------------------ MMA issuer
+    // Per key block j and half t: O_t += P_t V_j, then at once S_t for block
+    // j + 1 (its columns are P_t's, which the products of one thread have read
+    // by then, as they execute in issue order).
+    constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);  // Q, K both K-major
+    constexpr uint32_t kIdO = idesc_bf16(128, D, false, true);     // P from TMEM, V MN-major
+    const uint64_t dq0 = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
+    const uint64_t dk0 = sdesc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
+    const uint64_t dv0 = sdesc_sw128(smem_u32(smem + C::kOffV), 16384, 1024);
+    auto issue_s = [&](int t, int st, bool last) {  // by the elected lane
+      const uint32_t qo = (uint32_t)(t * C::kTileBytes) >> 4, ko = (uint32_t)(st * C::kTileBytes) >> 4;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {  // each k-step reads 32 bytes of every row
+        const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+        mma_ss(tmem + C::col_s(t), dq0 + qo + off, dk0 + ko + off, kIdS, kk > 0);
+      }
+      mma_commit(&bars.s_full[t]);
+      if (last) mma_commit(&bars.q_free[t]);  // the tile's last product to read Q
+    };
+    int g = 0, nq[2] = {0, 0}, np[2] = {0, 0};  // key blocks; tiles and P blocks of each half so far
+    bool ok = true;
+    while (ok && walk.step(a, p)) {
+      int nb[2];
+      half_blocks<C::kTiles>(a, p, nb);
+      const int nbm = max(nb[0], nb[1]);
+      if (nbm == 0) continue;
+      // S of the first block
+      ok = warp_wait(&bars.k_full[g % C::kKStages], (g / C::kKStages) & 1, abort_flag);
+      for (int t = 0; t < C::kTiles && ok; ++t)
+        if (nb[t] > 0) {
+          if (!(ok = warp_wait(&bars.q_full[t], nq[t] & 1, abort_flag))) break;
+          tc_fence_after();
+          if (elect_one()) issue_s(t, g % C::kKStages, nb[t] == 1);
+          __syncwarp();
+        }
+      if (!ok) break;
+      if (elect_one()) mma_commit(&bars.k_empty[g % C::kKStages]);
+      __syncwarp();
+      for (int j = 0; j < nbm; ++j, ++g) {
+        const int s = g % C::kVStages;
+        const uint32_t ph = (g / C::kVStages) & 1;
+        const int v_last = j < nb[1] ? 1 : 0;  // the half whose PV reads V_j last
+        const int jn = j + 1, sn = (g + 1) % C::kKStages;
+        const bool k_next = jn < nbm;
+        ok = warp_wait3(&bars.v_full[s], ph, j < nb[0] ? &bars.p_full[0] : &bars.v_full[s],
+                        j < nb[0] ? (np[0] & 1) : ph, k_next ? &bars.k_full[sn] : &bars.v_full[s],
+                        k_next ? ((g + 1) / C::kKStages) & 1 : ph, abort_flag);
+        if (!ok) break;
+        if constexpr (!FP8) {
+          const int end = p.q.len - (p.jb + j) * 128;
+          if (end < 128) zero_rows_from<D>(smem + C::kOffV + s * C::kTileBytes, end, lane);
+        }
+        for (int t = 0; t < C::kTiles; ++t) {
+          if (j < nb[t]) {
+            if (t == 1 && !(ok = warp_wait(&bars.p_full[1], np[1] & 1, abort_flag))) break;
+            // a tile's first PV overwrites O: the tile before has been read out
+            if (j == 0 && !(ok = warp_wait(&bars.o_free[t], (nq[t] & 1) ^ 1, abort_flag))) break;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t vo = (uint32_t)(s * C::kTileBytes) >> 4;
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)  // P columns [8 kk, 8 kk + 8), V rows [16 kk, 16 kk + 16)
+                mma_ts(tmem + C::col_o(t), tmem + C::col_s(t) + kk * 8, dv0 + vo + kk * (2048 >> 4), kIdO,
+                       (j > 0 || kk > 0) ? 1u : 0u);
+              if (j == nb[t] - 1) mma_commit(&bars.o_done[t]);
+              if (t == v_last) mma_commit(&bars.v_empty[s]);
+            }
+            __syncwarp();
+            ++np[t];
+          }
+          if (jn < nb[t]) {
+            if (elect_one()) issue_s(t, sn, jn == nb[t] - 1);
+            __syncwarp();
+          }
+        }
+        if (!ok) break;
+        if (k_next) {
+          if (elect_one()) mma_commit(&bars.k_empty[sn]);
+          __syncwarp();
+        }
+      }
+      for (int t = 0; t < 2; ++t) nq[t] += nb[t] > 0;
+    }
+    if (elect_one()) mma_commit(&bars.teardown);
+    __syncwarp();
+    mbar_wait_drain(&bars.teardown, 0);
+  } else if (FP8 && warp >= C::kWarpConv) {
+    // ------------------------------------------------------------ converters
+    const int tid = threadIdx.x - C::kWarpConv * 32;
+    int g = 0;
+    bool ok = true;
+    while (ok && walk.step(a, p)) {
+      int nb[2];
+      half_blocks<C::kTiles>(a, p, nb);
+      const int nbm = max(nb[0], nb[1]);
+      for (int j = 0; ok && j < nbm; ++j, ++g) {
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+          constexpr int kCS = FP8 ? C::kCStages : 1;
+          const int x = 2 * g + kv, cs = x % kCS, st = kv ? g % C::kVStages : g % C::kKStages;
+          const int use = kv ? g / C::kVStages : g / C::kKStages;
+          uint64_t* empty = kv ? &bars.v_empty[st] : &bars.k_empty[st];
+          ok = warp_wait2(&bars.c_full[cs], (x / kCS) & 1, empty, (use & 1) ^ 1, abort_flag);
+          if (!ok) break;
+          convert_tile<D>(smem + C::kOffC + cs * C::kCodeBytes,
+                          smem + (kv ? C::kOffV : C::kOffK) + st * C::kTileBytes, p.q.len - (p.jb + j) * 128, tid);
+          fence_proxy_async_smem();
+          mbar_arrive(kv ? &bars.v_full[st] : &bars.k_full[st]);
+          mbar_arrive(&bars.c_empty[cs]);
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax + epilogue
+    const int t = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;  // row within the half = TMEM lane
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lane_off + C::col_s(t);
+    const uint32_t t_o = tmem + lane_off + C::col_o(t);
+    const float sl2 = a.scale_log2;
+    const int G = a.Hq / a.Hkv, rt = r / G, rh = r - rt * G;  // this row's token within the half, and head
+    const bool o32 = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
+    int np = 0, nq = 0;  // blocks and tiles of this half so far
+    bool ok = true;
+    while (ok && walk.step(a, p)) {
+      int nb2[2];
+      half_blocks<C::kTiles>(a, p, nb2);
+      const int nb = nb2[t];
+      const int tok0 = p.tok + t * a.tpt1, tok = tok0 + rt;
+      const int off = p.q.len - p.q.n;  // causal: token i sees keys 0 .. i + off
+      const bool valid = rt < a.tpt1 && tok < p.q.n;
+      float m_ref = -INFINITY;  // exponent reference, log2 units of scaled scores
+      float l_sum = 0.f;        // sum of 2^(s * sl2 - m_ref) over the keys seen so far
+      for (int j = 0; j < nb; ++j, ++np) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars.s_full[t], np & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        // S_t, with the maximum of each 32 columns from the load itself
+        uint32_t sr[4][32];
+        float cmax[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32_max(t_s + c * 32, sr[c], cmax[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_wait(sr[c], cmax[c]);
+        float mx = fmax3(fmax3(cmax[0], cmax[1], cmax[2]), cmax[3], -INFINITY);
+        // only blocks that reach past the first row's last key, or past the request's, need masking
+        const int kv0 = (p.jb + j) * 128;
+        if ((CAUSAL && kv0 + 127 > tok0 + off) || kv0 + 128 > p.q.len) {
+          const int lim = (CAUSAL ? min(tok + off, p.q.len - 1) : p.q.len - 1) - kv0;  // keep column c iff c <= lim
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c > lim) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+          float mxc[8];  // row maximum over eight chains of 16 scores, then a tree
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            mxc[i] = fmaxf(__uint_as_float(sr[0][2 * i]), __uint_as_float(sr[0][2 * i + 1]));
+#pragma unroll
+          for (int c = 16; c < 128; c += 16)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              mxc[i] = fmax3(mxc[i], __uint_as_float(sr[c >> 5][(c & 31) + 2 * i]),
+                             __uint_as_float(sr[c >> 5][(c & 31) + 2 * i + 1]));
+          mx = fmax3(fmax3(mxc[0], mxc[1], mxc[2]), fmax3(mxc[3], mxc[4], mxc[5]), fmaxf(mxc[6], mxc[7]));
+        }
+        float alpha = 1.f;
+        const float m_new = fmaxf(m_ref, mx * sl2);
+        const bool move = m_new > m_ref + kRescaleThreshold;
+        if (move) {
+          alpha = ex2(m_ref - m_new);
+          m_ref = m_new;
+        }
+        const bool rescale = __any_sync(0xffffffffu, move && j > 0);
+        float2 sum4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;  // a row that has seen no key yet: P = 0
+        const float2 scale2 = make_float2(sl2, sl2), shift2 = make_float2(-m_use, -m_use);
+#pragma unroll
+        for (int ch = 0; ch < 4; ++ch) {  // P as bf16 pairs over the first 64 columns of S_t
+          uint32_t pk[16];
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const float2 x =
+                ffma2(make_float2(__uint_as_float(sr[ch][c]), __uint_as_float(sr[ch][c + 1])), scale2, shift2);
+            const float2 e = make_float2(ex2(x.x), ex2(x.y));
+            sum4[(c >> 1) & 3] = fadd2(sum4[(c >> 1) & 3], e);
+            pk[c >> 1] = pack_bf16x2(e.x, e.y);
+          }
+          tmem_st16(t_s + 16 * ch, pk);
+        }
+        const float2 sum = fadd2(fadd2(sum4[0], sum4[1]), fadd2(sum4[2], sum4[3]));
+        l_sum = l_sum * alpha + (sum.x + sum.y);
+        if (rescale) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(t_o + c, o);
+            tmem_ld_wait(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st32(t_o + c, o);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&bars.p_full[t]);
+      }
+      if (ok && nb > 0) ok = mbar_wait(&bars.o_done[t], nq & 1, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const bool seen = l_sum > 0.f;
+      const float lse2 = seen ? m_ref + log2f(l_sum) : -INFINITY;
+      const float inv = seen ? a.o_scale / l_sum : 0.f;
+      if (p.whole()) {
+        const long long row = ((long long)(p.q.start + tok) * a.Hq) + p.h * G + rh;
+        uint8_t* orow = static_cast<uint8_t*>(a.o) + row * (D * 2);
+        if (nb > 0) {
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(t_o + c, o);
+            tmem_ld_wait(o);
+            if (valid) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                uint32_t w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  // a row that has seen no key: 0, whatever its products made
+                  const float x = __uint_as_float(o[16 * h + 2 * i]), y = __uint_as_float(o[16 * h + 2 * i + 1]);
+                  w[i] = seen ? pack_bf16x2(x * inv, y * inv) : 0u;
+                }
+                st_global_32(orow + c * 2 + h * 32, w, o32);
+              }
+            }
+          }
+        } else if (valid) {
+          const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+          for (int c = 0; c < D; c += 16) st_global_32(orow + c * 2, zero, o32);
+        }
+        if (valid) a.lse[row] = seen ? lse2 * kLn2 : -INFINITY;
+      } else {
+        // this part's O / l and logsumexp, fp32, for the join
+        const long long prow =
+            ((long long)blockIdx.x * 2 + (p.jb == 0 ? 1 : 0)) * (128 * C::kTiles) + t * 128 + r;
+        if (nb > 0) {
+          tc_fence_after();
+          uint8_t* orow = reinterpret_cast<uint8_t*>(a.part_o + prow * D);
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(t_o + c, o);
+            tmem_ld_wait(o);
+            if (valid && seen)
+#pragma unroll
+              for (int h = 0; h < 4; ++h) {
+                uint32_t w[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(__uint_as_float(o[8 * h + i]) * inv);
+                st_global_v8(orow + c * 4 + h * 32, w);
+              }
+          }
+        }
+        if (valid) a.part_lse[prow] = lse2;
+      }
+      if (nb > 0) {
+        tc_fence_before();
+        mbar_arrive(&bars.o_free[t]);
+        ++nq;
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::kWarpMma) tmem_dealloc(tmem, C::kTmemCols);
+  if (threadIdx.x == 0 && bars.abort) atomicOr(a.status, 1u);
+}
+
+template <int D, bool FP8>
+cudaError_t launch(const PagedArgs& a, int ctas, cudaStream_t stream) {
+  using C = CCfg<D, FP8>;
+  auto kern = a.causal ? fa_paged_chunk_kernel<D, FP8, true> : fa_paged_chunk_kernel<D, FP8, false>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)ctas, C::kThreads, C::kSmemBytes, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_chunk(const PagedArgs& a, int ctas, cudaStream_t stream) {
+  if (a.d == 64) return a.fp8 ? launch<64, true>(a, ctas, stream) : launch<64, false>(a, ctas, stream);
+  return a.fp8 ? launch<128, true>(a, ctas, stream) : launch<128, false>(a, ctas, stream);
+}
+
+}  // namespace fa

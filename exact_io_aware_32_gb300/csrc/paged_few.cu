@@ -1,0 +1,449 @@
+// Attention of few new tokens (decoding) over the paged cache, on sm_103a: tiles
+// of at most 32 rows (new tokens x query heads of one key head).
+//
+// Such a call is bound by reading the cache: a key block of 128 keys costs 64 KB
+// at bf16 d = 128, 1.47 us of an SM's share of the bandwidth, while one 128-row
+// tile's chain (S, softmax, P V) takes about 1.3 us when a thread works through
+// all 128 scores of its row. Here the tile's 32 rows stand four times in the
+// 128-row Q operand, so that S comes out once per TMEM lane quarter and warp w
+// takes only keys [32 w, 32 w + 32) of every block: a quarter of the softmax
+// chain, with a running maximum and sum of its own, as if the keys were split
+// among four. P of warp w is zero outside its 32 columns (written once), so row
+// 32 w + r of O sums over warp w's keys, and the four quarters are joined
+// through shared memory when the tile ends. The products cost what they cost
+// with 32 rows, since tcgen05 takes 128 anyway.
+//
+// TMEM: S twice (S of the next block is made while the softmax works on this
+// one), P in columns of its own, O. Persistent CTAs over ranges of the row of
+// tiles (paged_work.cuh), rings and barriers counting on across tiles.
+//
+// Warp roles: 0-3 softmax and epilogue, 4 TMA, 5 MMA, and with E4M3 caches four
+// converter warps (codes to bf16 operands).
+#include "paged_pipe.cuh"
+
+namespace fa {
+namespace {
+
+using namespace fa::ptx;
+using namespace fa::paged;
+
+template <int D_, bool FP8_>
+struct FCfg {
+  static constexpr int D = D_;
+  static constexpr int kPanels = D / 64;
+  static constexpr int kTileBytes = kPanels * 16384;  // 128 rows, bf16
+  static constexpr int kCodeBytes = 128 * D;          // 128 rows of codes
+  static constexpr int kKStages = D == 64 ? 4 : 2;
+  static constexpr int kVStages = D == 64 ? 4 : (FP8_ ? 2 : 3);
+  static constexpr int kCStages = FP8_ ? (D == 64 ? 6 : 3) : 0;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kOffQ + kTileBytes;
+  static constexpr int kOffV = kOffK + kKStages * kTileBytes;
+  static constexpr int kOffC = kOffV + kVStages * kTileBytes;
+  static constexpr int kOffJoin = kOffC + kCStages * kCodeBytes;  // 4 quarters x 32 columns x 33 floats
+  static constexpr int kOffBar = kOffJoin + 4 * 32 * 33 * 4 + 4 * 32 * 8;
+  static constexpr int kSmemBytes = kOffBar + 384 + 1024;  // barriers, alignment slack
+  static_assert(kSmemBytes <= 232448, "shared memory");
+  static constexpr uint32_t kColS = 0, kColP = 256, kColO = 320, kTmemCols = 512;
+  static constexpr int kWarpTma = 4, kWarpMma = 5, kWarpConv = 6;
+  static constexpr int kThreads = 192 + (FP8_ ? 128 : 0);
+};
+
+struct FBars {
+  uint64_t q_full, q_free;
+  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], c_full[6], c_empty[6];
+  uint64_t s_full[2], s_free[2], p_full, pv_done, o_free;
+  uint64_t teardown;
+  uint32_t tmem_base;
+  int abort;
+  Range range;
+};
+static_assert(sizeof(FBars) <= 384, "barriers exceed their shared memory");
+
+template <int D, bool FP8, bool CAUSAL>
+__global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel(const __grid_constant__ PagedArgs a) {
+  using C = FCfg<D, FP8>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  FBars& bars = *reinterpret_cast<FBars*>(smem + C::kOffBar);
+  volatile int* abort_flag = &bars.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = a.Hq / a.Hkv;
+
+  // (the sums' place is the join's, not yet in use)
+  find_range<C::kThreads>(a, bars.range,
+                          reinterpret_cast<long long(&)[2][C::kThreads / 32]>(smem[C::kOffJoin]));
+  if (!bars.range.some) {  // uniform: every thread leaves before any barrier
+    if (threadIdx.x == 0) static_cast<Parts*>(a.parts)[blockIdx.x] = Parts{};
+    return;
+  }
+  if (threadIdx.x == 0) {
+    bars.abort = 0;
+    mbar_init(&bars.q_full, 1);
+    mbar_init(&bars.q_free, 1);
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&bars.k_full[s], FP8 ? 128 : 1);
+      mbar_init(&bars.k_empty[s], 1);
+      mbar_init(&bars.v_full[s], FP8 ? 128 : 1);
+      mbar_init(&bars.v_empty[s], 1);
+    }
+    for (int s = 0; s < 6; ++s) {
+      mbar_init(&bars.c_full[s], 1);
+      mbar_init(&bars.c_empty[s], 128);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars.s_full[s], 1);
+      mbar_init(&bars.s_free[s], 128);
+    }
+    mbar_init(&bars.p_full, 128);
+    mbar_init(&bars.pv_done, 1);
+    mbar_init(&bars.o_free, 128);
+    mbar_init(&bars.teardown, 1);
+    fence_mbar_init();
+  }
+  // rows of Q that no copy fills (G that does not divide 32, short tiles) are zeros, not leftovers
+  for (int i = threadIdx.x; i < C::kTileBytes / 16; i += C::kThreads)
+    st_shared_v4(smem_u32(smem + C::kOffQ) + i * 16, 0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
+  if (warp == C::kWarpMma) {
+    tmem_alloc(&bars.tmem_base, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem_base;
+  Walk walk;
+  walk.begin(a, bars.range);
+  Piece p;
+
+  if (warp == C::kWarpTma) {
+    // ------------------------------------------------------------ TMA producer
+    if (elect_one()) {
+      tma_prefetch_desc(&a.tm_q);
+      tma_prefetch_desc(&a.tm_k);
+      tma_prefetch_desc(&a.tm_v);
+    }
+    __syncwarp();
+    const uint32_t q_bytes = (uint32_t)(4 * G * a.tpt * D * 2);
+    Parts parts{};
+    int g = 0, nk = 0, nv = 0, nc = 0, nq = 0;  // key blocks, and loads issued
+    bool ok = true;
+    bool withhold = a.test_fault == 1;  // test hook: the MMA warp's first wait expires
+    while (ok && walk.step(a, p)) {
+      note_piece(parts, p);
+      const int nb = p.je - p.jb;
+      if (nb == 0) continue;
+      int page = lane_page(a, p, p.jb, lane);
+      for (int j = 0; ok && j < nb; ++j, ++g) {
+        const int jj = p.jb + j, page_now = page;
+        if (j + 1 < nb) page = lane_page(a, p, jj + 1, lane);
+        if constexpr (FP8) {
+          const int s0 = nc % C::kCStages;
+          if (!(ok = warp_wait(&bars.c_empty[s0], ((nc / C::kCStages) & 1) ^ 1, abort_flag))) break;
+          load_block<D, true>(a, p, jj, page_now, lane, &a.tm_k, smem + C::kOffC + s0 * C::kCodeBytes, &bars.c_full[s0]);
+          ++nc;
+          const int s1 = nc % C::kCStages;
+          if (!(ok = warp_wait(&bars.c_empty[s1], ((nc / C::kCStages) & 1) ^ 1, abort_flag))) break;
+          load_block<D, true>(a, p, jj, page_now, lane, &a.tm_v, smem + C::kOffC + s1 * C::kCodeBytes, &bars.c_full[s1]);
+          ++nc;
+        } else {
+          const int sk = g % C::kKStages, sv = g % C::kVStages;
+          if (!(ok = warp_wait(&bars.k_empty[sk], ((g / C::kKStages) & 1) ^ 1, abort_flag))) break;
+          load_block<D, false>(a, p, jj, page_now, lane, &a.tm_k, smem + C::kOffK + sk * C::kTileBytes, &bars.k_full[sk]);
+          nk = g + 1;
+          if (!(ok = warp_wait(&bars.v_empty[sv], ((g / C::kVStages) & 1) ^ 1, abort_flag))) break;
+          load_block<D, false>(a, p, jj, page_now, lane, &a.tm_v, smem + C::kOffV + sv * C::kTileBytes, &bars.v_full[sv]);
+          nv = g + 1;
+        }
+        if (j == 0) {  // Q after the first block's keys and values: it is small, and its slot may still be read
+          if (!(ok = warp_wait(&bars.q_free, (nq & 1) ^ 1, abort_flag))) break;
+          if (!withhold) {
+            if (elect_one()) {
+              mbar_arrive_expect_tx(&bars.q_full, q_bytes);
+              for (int w = 0; w < 4; ++w)
+                for (int pn = 0; pn < C::kPanels; ++pn)
+                  tma_load_3d(smem + C::kOffQ + pn * 16384 + w * 4096, &a.tm_q, &bars.q_full, pn * 64, p.h * G,
+                              p.q.start + p.tok);
+            }
+            __syncwarp();
+            ++nq;
+          }
+          withhold = false;
+        }
+      }
+    }
+    if (lane == 0) static_cast<Parts*>(a.parts)[blockIdx.x] = parts;
+    // Let every issued copy land before the CTA can exit.
+    if (nq > 0) mbar_wait_drain(&bars.q_full, (nq - 1) & 1);
+    for (int x = max(0, nk - C::kKStages); x < nk; ++x)
+      mbar_wait_drain(&bars.k_full[x % C::kKStages], (x / C::kKStages) & 1);
+    for (int x = max(0, nv - C::kVStages); x < nv; ++x)
+      mbar_wait_drain(&bars.v_full[x % C::kVStages], (x / C::kVStages) & 1);
+    if constexpr (FP8)
+      for (int x = max(0, nc - C::kCStages); x < nc; ++x)
+        mbar_wait_drain(&bars.c_full[x % C::kCStages], (x / C::kCStages) & 1);
+  } else if (warp == C::kWarpMma) {
+    // ------------------------------------------------------------ MMA issuer
+    // S of block g + 1 while the softmax works on block g, then P V of block g;
+    // at a tile's end P V first, since the next tile's Q is still on its way.
+    constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);  // Q, K both K-major
+    constexpr uint32_t kIdO = idesc_bf16(128, D, false, true);     // P from TMEM, V MN-major
+    const uint64_t dq0 = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
+    const uint64_t dk0 = sdesc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
+    const uint64_t dv0 = sdesc_sw128(smem_u32(smem + C::kOffV), 16384, 1024);
+    auto make_s = [&](int g, bool last) -> bool {
+      const int ks = g % C::kKStages, b = g & 1;
+      if (!warp_wait2(&bars.k_full[ks], (g / C::kKStages) & 1, &bars.s_free[b], ((g >> 1) & 1) ^ 1, abort_flag))
+        return false;
+      tc_fence_after();
+      if (elect_one()) {
+        const uint32_t ko = (uint32_t)(ks * C::kTileBytes) >> 4;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
+          mma_ss(tmem + C::kColS + b * 128, dq0 + off, dk0 + ko + off, kIdS, kk > 0);
+        }
+        mma_commit(&bars.s_full[b]);
+        mma_commit(&bars.k_empty[ks]);
+        if (last) mma_commit(&bars.q_free);
+      }
+      __syncwarp();
+      return true;
+    };
+    int g = 0, n = 0;  // key blocks, tiles
+    bool ok = true;
+    while (ok && walk.step(a, p)) {
+      const int nb = p.je - p.jb;
+      if (nb == 0) continue;
+      ok = warp_wait(&bars.q_full, n & 1, abort_flag) && make_s(g, nb == 1);
+      for (int j = 0; ok && j < nb; ++j, ++g) {
+        if (j + 1 < nb && !(ok = make_s(g + 1, j + 2 == nb))) break;
+        const int s = g % C::kVStages;
+        if (!(ok = warp_wait2(&bars.p_full, g & 1, &bars.v_full[s], (g / C::kVStages) & 1, abort_flag))) break;
+        // a tile's first P V overwrites O: the tile before has been read out
+        if (j == 0 && !(ok = warp_wait(&bars.o_free, (n & 1) ^ 1, abort_flag))) break;
+        if constexpr (!FP8) {
+          const int end = p.q.len - (p.jb + j) * 128;
+          if (end < 128) zero_rows_from<D>(smem + C::kOffV + s * C::kTileBytes, end, lane);
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t vo = (uint32_t)(s * C::kTileBytes) >> 4;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts(tmem + C::kColO, tmem + C::kColP + kk * 8, dv0 + vo + kk * (2048 >> 4), kIdO,
+                   (j > 0 || kk > 0) ? 1u : 0u);
+          mma_commit(&bars.pv_done);
+          mma_commit(&bars.v_empty[s]);
+        }
+        __syncwarp();
+      }
+      ++n;
+    }
+    if (elect_one()) mma_commit(&bars.teardown);
+    __syncwarp();
+    mbar_wait_drain(&bars.teardown, 0);
+  } else if (FP8 && warp >= C::kWarpConv) {
+    // ------------------------------------------------------------ converters
+    const int tid = threadIdx.x - C::kWarpConv * 32;
+    int g = 0;
+    bool ok = true;
+    while (ok && walk.step(a, p)) {
+      for (int j = p.jb; ok && j < p.je; ++j, ++g) {
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+          constexpr int kCS = FP8 ? C::kCStages : 1;
+          const int x = 2 * g + kv, cs = x % kCS, st = kv ? g % C::kVStages : g % C::kKStages;
+          const int use = kv ? g / C::kVStages : g / C::kKStages;
+          ok = warp_wait2(&bars.c_full[cs], (x / kCS) & 1, kv ? &bars.v_empty[st] : &bars.k_empty[st], (use & 1) ^ 1,
+                          abort_flag);
+          if (!ok) break;
+          convert_tile<D>(smem + C::kOffC + cs * C::kCodeBytes,
+                          smem + (kv ? C::kOffV : C::kOffK) + st * C::kTileBytes, p.q.len - j * 128, tid);
+          fence_proxy_async_smem();
+          mbar_arrive(kv ? &bars.v_full[st] : &bars.k_full[st]);
+          mbar_arrive(&bars.c_empty[cs]);
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax + epilogue
+    const uint32_t lane_off = (uint32_t)(warp * 32) << 16;
+    const uint32_t t_s = tmem + lane_off + C::kColS + warp * 32;  // this warp's rows and keys
+    const uint32_t t_p = tmem + lane_off + C::kColP;
+    const uint32_t t_o = tmem + lane_off + C::kColO;
+    const float sl2 = a.scale_log2;
+    const int rt = lane / G;  // this row's token within the tile
+    float* join = reinterpret_cast<float*>(smem + C::kOffJoin);
+    float2* stats = reinterpret_cast<float2*>(join + 4 * 32 * 33);  // (m, l) of each quarter and row
+    {
+      const uint32_t zero[16] = {};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_st16(t_p + c * 16, zero);  // P outside this warp's columns stays 0
+      tmem_st_wait();
+    }
+    int g = 0;
+    bool ok = true;
+    while (ok && walk.step(a, p)) {
+      const int nb = p.je - p.jb;
+      const int off = p.q.len - p.q.n;  // causal: token i sees keys 0 .. i + off
+      const int lim_row = (CAUSAL ? min(p.tok + rt + off, p.q.len - 1) : p.q.len - 1) - warp * 32;
+      const int lim_first = (CAUSAL ? min(p.tok + off, p.q.len - 1) : p.q.len - 1) - warp * 32;
+      const int rows = min(a.tpt, p.q.n - p.tok) * G;
+      float m_ref = -INFINITY;  // exponent reference, log2 units of scaled scores
+      float l_sum = 0.f;        // sum of 2^(s * sl2 - m_ref) over this warp's keys so far
+      for (int j = 0; j < nb; ++j, ++g) {
+        const int b = g & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars.s_full[b], (g >> 1) & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t sr[32];
+        float mx;
+        tmem_ld32_max(t_s + b * 128, sr, mx);
+        tmem_ld_wait(sr, mx);
+        tc_fence_before();
+        mbar_arrive(&bars.s_free[b]);  // S is in registers: the block after the next may overwrite it
+        const int kv0 = (p.jb + j) * 128;
+        if (kv0 + 31 > lim_first) {  // some row does not see all of these keys
+          const int lim = lim_row - kv0;
+          mx = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            if (c > lim) sr[c] = __float_as_uint(-INFINITY);
+            mx = fmaxf(mx, __uint_as_float(sr[c]));
+          }
+        }
+        float alpha = 1.f;
+        const float m_new = fmaxf(m_ref, mx * sl2);
+        const bool move = m_new > m_ref + kRescaleThreshold;
+        if (move) {
+          alpha = ex2(m_ref - m_new);
+          m_ref = m_new;
+        }
+        const bool rescale = __any_sync(0xffffffffu, move && j > 0);
+        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;  // a row that has seen no key yet: P = 0
+        const float2 scale2 = make_float2(sl2, sl2), shift2 = make_float2(-m_use, -m_use);
+        float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        uint32_t pk[16];
+#pragma unroll
+        for (int c = 0; c < 32; c += 2) {
+          const float2 x = ffma2(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), scale2, shift2);
+          const float2 e = make_float2(ex2(x.x), ex2(x.y));
+          sum2[(c >> 1) & 1] = fadd2(sum2[(c >> 1) & 1], e);
+          pk[c >> 1] = pack_bf16x2(e.x, e.y);
+        }
+        const float2 sum = fadd2(sum2[0], sum2[1]);
+        l_sum = l_sum * alpha + (sum.x + sum.y);
+        // P and O are free once the P V before this one has completed
+        if (j > 0) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars.pv_done, (g - 1) & 1, abort_flag));
+          if (!ok) break;
+          tc_fence_after();
+        }
+        tmem_st16(t_p + 16 * warp, pk);
+        if (rescale) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(t_o + c, o);
+            tmem_ld_wait(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+            tmem_st32(t_o + c, o);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&bars.p_full);
+      }
+      // ---- the tile's four quarters joined: o = sum_w 2^(m_w - m) O_w / sum_w 2^(m_w - m) l_w
+      if (ok && nb > 0) ok = mbar_wait(&bars.pv_done, (g - 1) & 1, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      stats[warp * 32 + lane] = make_float2(m_ref, l_sum);
+      if (!named_bar_and(1, 128, ok)) {  // the four warps agree whether to go on
+        ok = false;
+        break;
+      }
+      float m = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) m = fmaxf(m, stats[w * 32 + lane].x);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float2 s = stats[w * 32 + lane];
+        if (s.y > 0.f) l += s.y * ex2(s.x - m);
+      }
+      const bool seen = l > 0.f;
+      const float f = l_sum > 0.f ? ex2(m_ref - m) * (a.o_scale / l) : 0.f;
+      const bool whole = p.whole();
+      const long long row0 = (long long)(p.q.start + p.tok) * a.Hq + p.h * G;  // row r: token r / G, head r % G
+      const long long part0 = ((long long)blockIdx.x * 2 + (p.jb == 0 ? 1 : 0)) * 32;
+      if (warp == 0 && lane < rows) {
+        const float lse2 = seen ? m + log2f(l) : -INFINITY;
+        if (whole)
+          a.lse[row0 + (long long)rt * a.Hq + (lane - rt * G)] = seen ? lse2 * kLn2 : -INFINITY;
+        else
+          a.part_lse[part0 + lane] = lse2;
+      }
+      if (nb > 0) tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        if (nb > 0) {
+          tmem_ld32(t_o + c, o);
+          tmem_ld_wait(o);
+        }
+        if (nb > 0 && c + 32 == D) {
+          tc_fence_before();
+          mbar_arrive(&bars.o_free);  // O is in registers: the next tile may accumulate there
+        }
+        if (lane < rows)
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            join[(warp * 32 + i) * 33 + lane] = f > 0.f ? __uint_as_float(o[i]) * f : 0.f;
+        named_bar_sync(1, 128);
+        for (int i = threadIdx.x; i < rows * 16; i += 128) {  // pairs of columns
+          const int r = i >> 4, x = (i & 15) * 2;
+          float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            s0 += join[(w * 32 + x) * 33 + r];
+            s1 += join[(w * 32 + x + 1) * 33 + r];
+          }
+          if (whole) {
+            const int tk = r / G;
+            const long long row = row0 + (long long)tk * a.Hq + (r - tk * G);
+            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.o) + (row * D + c + x) * 2) = pack_bf16x2(s0, s1);
+          } else {
+            *reinterpret_cast<float2*>(a.part_o + (part0 + r) * D + c + x) = make_float2(s0, s1);
+          }
+        }
+        named_bar_sync(1, 128);
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::kWarpMma) tmem_dealloc(tmem, C::kTmemCols);
+  if (threadIdx.x == 0 && bars.abort) atomicOr(a.status, 1u);
+}
+
+template <int D, bool FP8>
+cudaError_t launch(const PagedArgs& a, int ctas, cudaStream_t stream) {
+  using C = FCfg<D, FP8>;
+  auto kern = a.causal ? fa_paged_few_kernel<D, FP8, true> : fa_paged_few_kernel<D, FP8, false>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  if (e != cudaSuccess) return e;
+  kern<<<(unsigned)ctas, C::kThreads, C::kSmemBytes, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_few(const PagedArgs& a, int ctas, cudaStream_t stream) {
+  if (a.d == 64) return a.fp8 ? launch<64, true>(a, ctas, stream) : launch<64, false>(a, ctas, stream);
+  return a.fp8 ? launch<128, true>(a, ctas, stream) : launch<128, false>(a, ctas, stream);
+}
+
+}  // namespace fa

@@ -1,93 +1,118 @@
-// Attention of new tokens over the paged cache: one warp per (packed row, query
-// head), the keys one after another with a running maximum and sum.
+// Host side of the paged attention (which kernel, how many CTAs, tensor maps) and
+// the kernel that joins tiles cut between CTAs.
+#include <algorithm>
 #include <cstdint>
-
-#include <cuda_bf16.h>
-#include <cuda_fp8.h>
 
 #include "fa_internal.h"
 #include "paged.h"
+#include "paged_work.cuh"
+#include "ptx.cuh"
 
 namespace fa {
 namespace {
 
-template <int V, bool FP8>
-__device__ __forceinline__ void load_row(const void* cache, long long at, float (&x)[V]) {
-  if constexpr (FP8) {
-    const __nv_fp8_e4m3* p = static_cast<const __nv_fp8_e4m3*>(cache) + at;
-#pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = (float)p[i];
-  } else {
-    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(cache) + at;
-#pragma unroll
-    for (int i = 0; i < V; ++i) x[i] = __bfloat162float(p[i]);
-  }
-}
+using paged::Parts;
 
-template <int D, bool FP8>
-__global__ void __launch_bounds__(128) fa_fwd_paged_kernel(const __grid_constant__ PagedArgs a) {
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Joins the parts of one cut tile: with m = max_z lse_z, o = sum_z 2^(lse_z - m) o_z
+// / sum_z 2^(lse_z - m). The CTA that opened the tile names it; the parts after
+// its own are the leading pieces of the CTAs that follow, in order, up to the one
+// that ends the tile: a fixed order, so the same bits every time. One warp per
+// row, grid.y over the tile's rows.
+template <int D>
+__global__ void __launch_bounds__(128) fa_paged_join_kernel(const __grid_constant__ PagedArgs a, int rows_per_tile) {
   constexpr int V = D / 32;
-  const long long w = (long long)blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31;
-  const int t = (int)(w / a.Hq), h = (int)(w - (long long)t * a.Hq), hk = h / (a.Hq / a.Hkv);
-  if (w == 0)  // one warp reports what is out of range in the lengths
-    for (int r = lane; r < a.R; r += 32) {
-      const int s0 = a.query_start[r], s1 = a.query_start[r + 1];
-      if (s0 < 0 || s1 < s0 || s1 > a.T) atomicOr(a.status, kStatusBadLength);
+  const Parts* parts = static_cast<const Parts*>(a.parts);
+  const int c = blockIdx.x, lane = threadIdx.x & 31;
+  const Parts mine = parts[c];
+  if (!mine.open) return;
+  // the CTA that ends the tile: the first after c whose leading piece says so
+  int end = -1;
+  for (int z0 = c + 1; z0 < (int)gridDim.x; z0 += 32) {
+    const int z = z0 + lane;
+    const bool ends = z < (int)gridDim.x && parts[z].lead && parts[z].lead_ends;
+    const unsigned b = __ballot_sync(0xffffffffu, ends);
+    if (b) {
+      end = z0 + __ffs((int)b) - 1;
+      break;
     }
-  if (t >= a.T) return;
-  int lo = 0, hi = a.R;  // the last request that starts at or before row t
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.query_start[mid] <= t) lo = mid;
-    else hi = mid;
   }
-  const int r = lo, start = max(a.query_start[r], 0), n = min(a.query_start[r + 1], a.T) - start;
-  if (t < start || t >= start + n) return;
-  const long long cap = (long long)a.max_pages << a.page_shift;
-  const int asked = a.seq_lens[r];
-  const int len = (int)min((long long)max(asked, 0), cap);
-  if (len != asked && lane == 0) atomicOr(a.status, kStatusBadLength);
-  const int see = a.causal ? min(len, len - n + (t - start) + 1) : len;
-  float q[V], acc[V], m = -INFINITY, l = 0.f;
-  load_row<V, false>(a.q, t * a.q_stride + (long long)h * D + lane * V, q);
+  if (end < 0) return;
+  const int G = a.Hq / a.Hkv;
+  const int row = (int)blockIdx.y * 4 + (threadIdx.x >> 5);
+  // row = half * 128 + token * G + head (halves of tpt1 tokens)
+  const int half = row >> 7, rr = row & 127, tk = rr / G;
+  const int tok = mine.tok + half * a.tpt1 + tk;
+  if (tk >= a.tpt1 || tok >= mine.n) return;
+  auto slot = [&](int z) { return ((long long)z * 2 + (z == c ? 1 : 0)) * rows_per_tile + row; };
+  float m = -INFINITY;
+  for (int z = c + lane; z <= end; z += 32) m = fmaxf(m, a.part_lse[slot(z)]);
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+  float acc[V], tot = 0.f;
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.f;
-  const int mask = (1 << a.page_shift) - 1;
-  for (int j = 0; j < see; ++j) {
-    const int page = a.block_table[(long long)r * a.max_pages + (j >> a.page_shift)];
-    const bool ok = page >= 0 && page < a.num_pages;
-    if (!ok && lane == 0) atomicOr(a.status, kStatusBadLength);
-    const long long at = ((((long long)(ok ? page : 0) * a.Hkv + hk) << a.page_shift) + (j & mask)) * D + lane * V;
-    float k[V], v[V], s = 0.f;
-    load_row<V, FP8>(a.k_cache, at, k);
-    load_row<V, FP8>(a.v_cache, at, v);
+  if (m != -INFINITY)
+#pragma unroll 4
+    for (int z = c; z <= end; ++z) {
+      const float lz = a.part_lse[slot(z)];
+      const float w = exp2f(lz - m);
+      tot += w;
+      if (lz == -INFINITY) continue;  // that part saw no key of this row and wrote no O
+      const float* oz = a.part_o + slot(z) * D + lane * V;
 #pragma unroll
-    for (int i = 0; i < V; ++i) s += ok ? q[i] * k[i] : 0.f;
+      for (int i = 0; i < V; ++i) acc[i] += w * oz[i];
+    }
+  const float inv = tot > 0.f ? 1.f / tot : 0.f;
+  const long long out = (long long)(mine.start + tok) * a.Hq + mine.h * G + (rr - tk * G);
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.o) + (out * D + lane * V) * 2);
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= a.scale_log2;
-    const float m_new = fmaxf(m, s), alpha = exp2f(m - m_new), p = exp2f(s - m_new);
-    m = m_new;
-    l = l * alpha + p;
-#pragma unroll
-    for (int i = 0; i < V; ++i) acc[i] = acc[i] * alpha + (ok ? p * v[i] : 0.f);
-  }
-  const float inv = l > 0.f ? a.o_scale / l : 0.f;
-  __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.o) + ((long long)t * a.Hq + h) * D + lane * V;
-#pragma unroll
-  for (int i = 0; i < V; ++i) o[i] = __float2bfloat16_rn(acc[i] * inv);
-  if (lane == 0) a.lse[(long long)t * a.Hq + h] = l > 0.f ? (m + log2f(l)) * 0.693147180559945309f : -INFINITY;
+  for (int i = 0; i < V / 2; ++i) dst[i] = ptx::pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+  if (lane == 0) a.lse[out] = tot > 0.f ? (m + log2f(tot)) * 0.693147180559945309417f : -INFINITY;
 }
 
 }  // namespace
 
-cudaError_t launch_paged(const PagedArgs& a, int, cudaStream_t stream) {
-  const unsigned grid = (unsigned)(((long long)a.T * a.Hq + 3) / 4);
+PagedPlan plan_paged(int Hq, int Hkv, int d, int fp8, int max_new, int num_sms) {
+  const int G = Hq / Hkv;
+  PagedPlan p;
+  // at most 32 rows a tile: the decoding kernel
+  p.few = (long long)G * max_new <= 32;
+  const int halves = p.few || (d == 64 && !fp8) ? 1 : 2;
+  p.rows = p.few ? 32 : 128 * halves;
+  p.tpt1 = std::min(max_new, (p.few ? 32 : 128) / G);
+  p.tpt = halves * p.tpt1;
+  p.ctas = num_sms * (!p.few && halves == 1 ? 2 : 1);
+  p.parts_bytes = align256(sizeof(Parts) * p.ctas);
+  p.o_bytes = align256((size_t)p.ctas * 2 * p.rows * d * sizeof(float));
+  p.lse_bytes = align256((size_t)p.ctas * 2 * p.rows * sizeof(float));
+  return p;
+}
+
+cudaError_t launch_paged(PagedArgs a, const PagedPlan& p, cudaStream_t stream) {
+  const unsigned long long d = a.d, elem = a.fp8 ? 1 : 2, ps = 1ull << a.page_shift;
+  const unsigned per = (unsigned)std::min(ps, 128ull);
+  const CUtensorMapDataType type = a.fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const unsigned long long kv_dims[3] = {d, ps, (unsigned long long)a.num_pages * a.Hkv};
+  const unsigned long long kv_strides[2] = {d * elem, ps * d * elem};
+  const unsigned kv_box[3] = {a.fp8 ? (unsigned)d : 64u, per, 1u};
+  const unsigned long long q_dims[3] = {d, (unsigned long long)a.Hq, (unsigned long long)a.T};
+  const unsigned long long q_strides[2] = {d * 2, (unsigned long long)a.q_stride * 2};
+  const unsigned q_box[3] = {64u, (unsigned)(a.Hq / a.Hkv), (unsigned)p.tpt1};
+  if (!encode_map3(&a.tm_q, a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, q_dims, q_strides, q_box, true) ||
+      !encode_map3(&a.tm_k, a.k_cache, type, kv_dims, kv_strides, kv_box, !a.fp8) ||
+      !encode_map3(&a.tm_v, a.v_cache, type, kv_dims, kv_strides, kv_box, !a.fp8))
+    return cudaErrorInvalidValue;
+  a.tpt = p.tpt;
+  a.tpt1 = p.tpt1;
+  cudaError_t e = p.few ? launch_paged_few(a, p.ctas, stream) : launch_paged_chunk(a, p.ctas, stream);
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)p.ctas, (unsigned)(p.rows / 4));
   if (a.d == 64)
-    (a.fp8 ? fa_fwd_paged_kernel<64, true> : fa_fwd_paged_kernel<64, false>)<<<grid, 128, 0, stream>>>(a);
+    fa_paged_join_kernel<64><<<grid, 128, 0, stream>>>(a, p.rows);
   else
-    (a.fp8 ? fa_fwd_paged_kernel<128, true> : fa_fwd_paged_kernel<128, false>)<<<grid, 128, 0, stream>>>(a);
+    fa_paged_join_kernel<128><<<grid, 128, 0, stream>>>(a, p.rows);
   return cudaGetLastError();
 }
 

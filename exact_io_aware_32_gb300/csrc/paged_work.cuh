@@ -1,0 +1,226 @@
+// How the work of one paged attention call is cut up, on the device, from the
+// requests' lengths.
+//
+// A tile is the new tokens [i tpt, (i + 1) tpt) of one request with the query
+// heads of one key head; it streams the 128-key blocks its last token sees.
+// The tiles stand in a row (request, key head, token tile), each as long as
+// the keys it sees plus a fixed part for its prologue and epilogue, and the
+// row is cut into one equal range per CTA. So a decoding batch of any lengths
+// and a long prompt alike end at about the same time on every SM. A cut inside a tile falls on a
+// block border; the parts of a cut tile are joined by a second kernel. Every
+// CTA works out its own range from prefix sums over the requests (a few KB
+// that all read through L2), so no kernel has to run before.
+#pragma once
+#include <cstdint>
+
+#include "fa_internal.h"
+#include "paged.h"
+
+namespace fa {
+namespace paged {
+
+// Fixed part of a tile in keys, where the ranges are long enough for tiles to be whole.
+constexpr int kTileCost = 256;
+constexpr long long kLongRange = 1024;  // a range of so many keys counts kTileCost, a shorter one nothing
+constexpr long long kMinRange = 256;    // the shortest range worth a CTA: two blocks
+
+struct Request {
+  int start, n, len;  // packed rows [start, start + n), keys [0, len)
+};
+
+// Request r as the call takes it; bad: something was out of range.
+__device__ __forceinline__ Request request(const PagedArgs& a, int r, bool& bad) {
+  Request q;
+  const int s0 = __ldg(a.query_start + r), s1 = __ldg(a.query_start + r + 1), l = __ldg(a.seq_lens + r);
+  q.start = min(max(s0, 0), a.T);
+  q.n = min(max(s1, q.start), a.T) - q.start;
+  q.len = min(max(l, 0), a.max_keys);
+  bad = q.start != s0 || q.start + q.n != s1 || q.len != l;
+  return q;
+}
+
+// Keys that the tokens before 'upto' (of the request's n) see.
+__device__ __forceinline__ int keys_seen(const PagedArgs& a, const Request& q, int upto) {
+  return a.causal ? max(q.len - q.n + min(upto, q.n), 0) : q.len;
+}
+
+// Length of tile i in the row of tiles, without its fixed part.
+__device__ __forceinline__ long long tile_keys(const PagedArgs& a, const Request& q, int i) {
+  return a.causal ? (long long)max(q.len - q.n, 0) + min((long long)q.n, (long long)(i + 1) * a.tpt) : q.len;
+}
+// The same summed over tiles 0 .. i - 1 of a request of nt tiles.
+__device__ __forceinline__ long long keys_before(const PagedArgs& a, const Request& q, int i, int nt) {
+  if (!a.causal) return (long long)i * q.len;
+  const long long whole = min(i, nt - 1);  // tiles of tpt tokens; the last one may have fewer
+  return (long long)i * max(q.len - q.n, 0) + a.tpt * (whole * (whole + 1) / 2) + (i == nt ? q.n : 0);
+}
+
+struct Range {
+  long long p0, p1;   // this CTA's range of the row of tiles
+  long long pos;      // where the tile that holds p0 begins
+  int r, h, i, cost;  // that tile; the fixed part of each tile
+  int some;           // whether the range holds anything
+};
+
+// A part of a tile for this CTA: key blocks [jb, je) of nb.
+struct Piece {
+  Request q;
+  int r, h, tok;  // request, key head, first token
+  int jb, je, nb;
+  __device__ __forceinline__ bool whole() const { return jb == 0 && je == nb; }
+};
+
+// This CTA's range, by all threads of the block (NT of them, a multiple of 32).
+template <int NT>
+__device__ __forceinline__ void find_range(const PagedArgs& a, Range& out, long long (&s_sum)[2][NT / 32]) {
+  constexpr int kWarps = NT / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int seg = (a.R + NT - 1) / NT, r0 = min(a.R, tid * seg), r1 = min(a.R, r0 + seg);
+  long long keys = 0, tiles = 0;  // of this thread's requests
+  bool any_bad = false;
+  for (int r = r0; r < r1; ++r) {
+    bool bad;
+    const Request q = request(a, r, bad);
+    any_bad |= bad;
+    const int nt = (q.n + a.tpt - 1) / a.tpt;
+    keys += a.Hkv * keys_before(a, q, nt, nt);
+    tiles += (long long)a.Hkv * nt;
+  }
+  if (any_bad && blockIdx.x == 0) atomicOr(a.status, kStatusBadLength);
+  long long ik = keys, it = tiles;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, ik, s), y = __shfl_up_sync(0xffffffffu, it, s);
+    if (lane >= s) {
+      ik += x;
+      it += y;
+    }
+  }
+  if (lane == 31) {
+    s_sum[0][warp] = ik;
+    s_sum[1][warp] = it;
+  }
+  if (tid == 0) out.some = 0;
+  __syncthreads();
+  long long all_k = 0, all_t = 0, k0 = ik - keys, t0 = it - tiles;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) {
+      k0 += s_sum[0][w];
+      t0 += s_sum[1][w];
+    }
+    all_k += s_sum[0][w];
+    all_t += s_sum[1][w];
+  }
+  const long long ctas = gridDim.x;
+  const int cost = all_k >= kLongRange * ctas ? kTileCost : 1;
+  const long long total = all_k + cost * all_t;
+  const long long per = max(kMinRange, (total + ctas - 1) / ctas);
+  const long long p0 = per * blockIdx.x;
+  long long pos = k0 + cost * t0;
+  if (p0 < total && pos <= p0 && p0 < pos + keys + cost * tiles) {  // one thread holds p0
+    int r = r0;
+    for (;; ++r) {
+      bool bad;
+      const Request q = request(a, r, bad);
+      const int nt = (q.n + a.tpt - 1) / a.tpt;
+      const long long head = keys_before(a, q, nt, nt) + (long long)cost * nt;
+      if (p0 >= pos + a.Hkv * head) {
+        pos += a.Hkv * head;
+        continue;
+      }
+      const int h = (int)((p0 - pos) / head);
+      pos += h * head;
+      int lo = 0, hi = nt;  // the last tile that begins at or before p0
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (keys_before(a, q, mid, nt) + (long long)cost * mid <= p0 - pos)
+          lo = mid;
+        else
+          hi = mid;
+      }
+      out.r = r;
+      out.h = h;
+      out.i = lo;
+      out.pos = pos + keys_before(a, q, lo, nt) + (long long)cost * lo;
+      break;
+    }
+    out.p0 = p0;
+    out.p1 = min(total, p0 + per);
+    out.cost = cost;
+    out.some = 1;
+  }
+  __syncthreads();
+}
+
+// Walks a range's pieces in order; every warp role walks the same ones.
+struct Walk {
+  Request q, next;  // 'next': the request after q, loaded ahead
+  long long p0, p1, pos;
+  int r, h, i, nt, cost;
+
+  __device__ __forceinline__ void ahead(const PagedArgs& a) {
+    bool bad;
+    if (r + 1 < a.R) next = request(a, r + 1, bad);
+  }
+  __device__ __forceinline__ void begin(const PagedArgs& a, const Range& g) {
+    p0 = g.p0;
+    p1 = g.p1;
+    pos = g.pos;
+    r = g.r;
+    h = g.h;
+    i = g.i;
+    cost = g.cost;
+    bool bad;
+    q = request(a, r, bad);
+    nt = (q.n + a.tpt - 1) / a.tpt;
+    ahead(a);
+  }
+  // The block border nearest to x keys past the tile's fixed part.
+  __device__ __forceinline__ int border(long long x, int nb) const {
+    const long long b = (x - cost + 64) >> 7;
+    return (int)min(max(b, 0ll), (long long)nb);
+  }
+  __device__ __forceinline__ bool step(const PagedArgs& a, Piece& p) {
+    while (pos < p1) {
+      const long long len = tile_keys(a, q, i) + cost;
+      p.q = q;
+      p.r = r;
+      p.h = h;
+      p.tok = i * a.tpt;
+      p.nb = (keys_seen(a, q, p.tok + a.tpt) + 127) >> 7;
+      p.jb = p0 <= pos ? 0 : border(p0 - pos, p.nb);
+      p.je = p1 >= pos + len ? p.nb : border(p1 - pos, p.nb);
+      const bool use = p.nb ? p.jb < p.je : p0 <= pos;
+      pos += len;
+      if (++i == nt) {
+        i = 0;
+        if (++h == a.Hkv) {
+          h = 0;
+          do {
+            if (++r >= a.R) {
+              p1 = pos;  // past the last request
+              break;
+            }
+            q = next;
+            ahead(a);
+          } while (q.n == 0);
+          nt = (q.n + a.tpt - 1) / a.tpt;
+        }
+      }
+      if (use) return true;
+    }
+    return false;
+  }
+};
+
+// What a CTA tells the joining kernel: whether its first piece continues a tile
+// that CTAs before it began (lead) and ends it, and whether its last piece
+// begins a tile that later CTAs end (open), with that tile.
+struct Parts {
+  int lead, lead_ends, open;
+  int start, n, tok, h;  // the open tile: its request's rows, first token, key head
+  int pad;
+};
+
+}  // namespace paged
+}  // namespace fa

@@ -377,7 +377,7 @@ FA_API int fa_device_status(int reset);
 /*
  * Test hook for the failure path; the pages have no counterpart to it. Arms a
  * one-shot fault that the next forward launch (fa_fwd, fa_fwd_kv,
- * fa_fwd_fp8 or fa_fwd_dropout, from any thread) consumes:
+ * fa_fwd_fp8, fa_fwd_dropout or fa_fwd_paged, from any thread) consumes:
  *   kind 1  every CTA's load warp withholds the copy of its first query
  *           tile, so the MMA warp's bounded wait for it runs out after the
  *           kernels' wait limit (one second). Each CTA then lets the copies

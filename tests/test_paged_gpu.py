@@ -138,6 +138,18 @@ def test_rows_behind_the_last_request_stay(most):
     check(c, o, lse)
 
 
+@pytest.mark.parametrize("most", [1, 200])
+def test_output_aligned_to_16_bytes_only(most):
+    c = paged_ref.case([(100, 1), (5, 130), (0, 1)], 4, 2, 64, 16, seed=18)
+    g = on_gpu(c)
+    n = c["T"] * 4 * 64
+    o = torch.zeros(n + 8, dtype=torch.bfloat16, device="cuda")[8:].view(c["T"], 4, 64)
+    assert o.data_ptr() % 32 == 16
+    o, lse = attend(c, g, max_new=most, out=o)
+    parity.check_status()
+    check(c, o, lse)
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_sharp_softmax(fp8):
     """Scores of hundreds: the running maximum moves far, and most weights vanish."""
@@ -483,6 +495,21 @@ def test_captured_step_replays_with_other_lengths(most):
                 p = c["ctx"][r] + i
                 same["v_cache"][c["table"][r][p // ps], :, p % ps] = c["k_cache"][c["table"][r][p // ps], :, p % ps]
         check(same, o, lse)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("most", [1, 64])
+def test_wait_that_runs_out_is_reported(most, fp8):
+    """The failure path: the first query tile is withheld, every CTA gives up after a second, and the next call is right."""
+    c = paged_ref.case([(100, 1), (600, 20)], 4, 2, 128, 16, fp8=fp8, seed=2)
+    g = on_gpu(c)
+    assert fa.fa_test_arm_fault(1) == fa.FA_OK
+    attend(c, g, max_new=most)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(True) == fa.FA_ERR_TIMEOUT
+    o, lse = attend(c, g, max_new=most)
+    parity.check_status()
+    check(c, o, lse)
 
 
 def test_two_streams_at_once():
