@@ -226,11 +226,17 @@ int device_facts(int* num_sms, unsigned int** status) {
   return FA_OK;
 }
 
-bool encode_map3(CUtensorMap* m, const void* base, CUtensorMapDataType type, const unsigned long long (&dims)[3],
-                 const unsigned long long (&strides)[2], const unsigned (&box)[3], bool swizzle) {
-  const cuuint64_t n[3] = {dims[0], dims[1], dims[2]}, s[2] = {strides[0], strides[1]};
-  const cuuint32_t b[3] = {box[0], box[1], box[2]}, es[3] = {1, 1, 1};
-  return g_encode(m, type, 3, const_cast<void*>(base), n, s, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+bool encode_map(CUtensorMap* m, const void* base, CUtensorMapDataType type, int rank, const unsigned long long* dims,
+                const unsigned long long* strides, const unsigned* box, bool swizzle) {
+  cuuint64_t n[5], s[4];
+  cuuint32_t b[5], es[5];
+  for (int i = 0; i < rank; ++i) {
+    n[i] = dims[i];
+    b[i] = box[i];
+    es[i] = 1;
+    if (i + 1 < rank) s[i] = strides[i];
+  }
+  return g_encode(m, type, (cuuint32_t)rank, const_cast<void*>(base), n, s, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                   swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

@@ -3,6 +3,7 @@
 #pragma once
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstddef>
 
 namespace fa {
@@ -42,8 +43,9 @@ struct PagedArgs {
   int max_keys;      // max_pages pages of keys
   // set by launch_paged
   CUtensorMap tm_q;         // bf16 [T][Hq][d], box 64 x (Hq / Hkv) x tokens of a 128-row (32-row) tile, 128B swizzle
-  CUtensorMap tm_k, tm_v;   // [num_pages * Hkv][page_size][d], boxes of a page's rows up to 128: bf16 64 columns wide
-                            // with 128B swizzle, or E4M3 whole rows unswizzled
+  // A page's rows of one head, up to 128 of them, per copy. bf16: seen as [page, head][row / 8][panel][row % 8][64
+  // columns] with 128B swizzle, so that one copy brings every 64-column panel. E4M3: [page, head][row][d], unswizzled.
+  CUtensorMap tm_k, tm_v;
   int tpt;                  // tokens per tile
   int tpt1;                 // tokens per 128-row half of a tile (two halves at d = 128)
   void* parts;              // Parts per CTA, then the cut tiles' results, in the caller's workspace
@@ -69,9 +71,12 @@ cudaError_t launch_paged(PagedArgs a, const PagedPlan& p, cudaStream_t stream);
 // The two kernels (paged_few.cu, paged_chunk.cu) and the join of cut tiles.
 cudaError_t launch_paged_few(const PagedArgs& a, int ctas, cudaStream_t stream);
 cudaError_t launch_paged_chunk(const PagedArgs& a, int ctas, cudaStream_t stream);
-// Tensor map of rank 3 (sizes and box innermost first, strides in bytes), 128-byte swizzle or none.
-bool encode_map3(CUtensorMap* m, const void* base, CUtensorMapDataType type, const unsigned long long (&dims)[3],
-                 const unsigned long long (&strides)[2], const unsigned (&box)[3], bool swizzle);
+// Tensor map (sizes, strides in bytes and box, innermost first), 128-byte swizzle or none.
+bool encode_map(CUtensorMap* m, const void* base, CUtensorMapDataType type, int rank, const unsigned long long* dims,
+                const unsigned long long* strides, const unsigned* box, bool swizzle);
+// Allows the kernel its dynamic shared memory on the current device, once per device ('done' has a bit for each:
+// the attribute costs a microsecond, as long as a short call's whole kernel).
+cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<unsigned long long>& done);
 // Takes the fault that fa_test_arm_fault armed (0: none).
 int take_test_fault();
 

@@ -16,7 +16,7 @@
 // tensor store could write.
 //
 // Warp roles: a softmax warpgroup per 128-row half, the TMA warp, the MMA warp,
-// and with E4M3 caches a warpgroup that turns each 8-bit block into the bf16
+// and with E4M3 caches a warpgroup that turns each 8-bit block into the f16
 // operands of the products (TMA -> 8-bit ring -> converters -> K/V rings).
 #include "paged_pipe.cuh"
 
@@ -35,7 +35,7 @@ struct CCfg {
   static constexpr int kTiles = D == 64 && !FP8 ? 1 : 2;
   static constexpr int kCtasPerSm = 3 - kTiles;
   static constexpr int kPanels = D / 64;
-  static constexpr int kTileBytes = kPanels * 16384;  // 128 rows, bf16
+  static constexpr int kTileBytes = kPanels * 16384;  // 128 rows, 16-bit
   static constexpr int kCodeBytes = 128 * D;          // 128 rows of codes
   static constexpr int kKStages = 2, kVStages = FP8 && D == 128 ? 2 : 3;
   static constexpr int kCStages = FP8 ? (D == 128 ? 2 : 4) : 0;
@@ -44,7 +44,7 @@ struct CCfg {
   static constexpr int kOffV = kOffK + kKStages * kTileBytes;
   static constexpr int kOffC = kOffV + kVStages * kTileBytes;
   static constexpr int kOffBar = kOffC + kCStages * kCodeBytes;
-  static constexpr int kSmemBytes = kOffBar + 1024 + 1024;  // barriers, alignment slack
+  static constexpr int kSmemBytes = kOffBar + (FP8 ? 1536 : 1024) + 1024;  // barriers, alignment slack
   static_assert(kSmemBytes <= 232448 && (kCtasPerSm == 1 || 2 * (kSmemBytes + 1024) <= 233472), "shared memory");
   static constexpr uint32_t kTmemCols = kTiles == 2 ? 512u : 256u;
   __host__ __device__ static constexpr uint32_t col_s(int t) { return (uint32_t)t * 128u; }
@@ -55,7 +55,9 @@ struct CCfg {
 };
 
 struct CBars {
-  uint64_t q_full[2], q_free[2];
+  // by half. q_full of a half's tile n is q_full[t][n & 1]: with E4M3 caches the softmax waits for it too, maybe only
+  // after the next tile's Q is there, and one barrier would then have gone through both parities
+  uint64_t q_raw[2], q_full[2][2], q_free[2];  // E4M3 caches: Q as loaded, as converted
   uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3], c_full[4], c_empty[4];
   uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
   uint64_t teardown;
@@ -65,6 +67,10 @@ struct CBars {
   long long sums[2][16];
 };
 static_assert(sizeof(CBars) <= 1024, "barriers exceed their shared memory");
+struct CBars8 : CBars {
+  uint8_t q_ex[2][2][128];  // the exponents of Q's row scales, by tile (this one and the one before), half and row
+};
+static_assert(sizeof(CBars8) <= 1536, "barriers exceed their shared memory");
 
 // Key blocks that each 128-row half sees of a piece (nb[t] from p.jb on).
 template <int kTiles>
@@ -83,7 +89,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
   using C = CCfg<D, FP8>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  CBars& bars = *reinterpret_cast<CBars*>(smem + C::kOffBar);
+  CBars8& bars = *reinterpret_cast<CBars8*>(smem + C::kOffBar);  // (q_ex only with E4M3 caches)
   volatile int* abort_flag = &bars.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -95,7 +101,9 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
   if (threadIdx.x == 0) {
     bars.abort = 0;
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&bars.q_full[s], 1);
+      mbar_init(&bars.q_raw[s], 1);
+      mbar_init(&bars.q_full[s][0], FP8 ? kConvArrivals : 1);
+      mbar_init(&bars.q_full[s][1], FP8 ? kConvArrivals : 1);
       mbar_init(&bars.q_free[s], 1);
       mbar_init(&bars.s_full[s], 1);
       mbar_init(&bars.p_full[s], 128);
@@ -103,14 +111,14 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
       mbar_init(&bars.o_free[s], 128);
     }
     for (int s = 0; s < 3; ++s) {
-      mbar_init(&bars.k_full[s], FP8 ? 128 : 1);
+      mbar_init(&bars.k_full[s], FP8 ? kConvArrivals : 1);
       mbar_init(&bars.k_empty[s], 1);
-      mbar_init(&bars.v_full[s], FP8 ? 128 : 1);
+      mbar_init(&bars.v_full[s], FP8 ? kConvArrivals : 1);
       mbar_init(&bars.v_empty[s], 1);
     }
     for (int s = 0; s < 4; ++s) {
       mbar_init(&bars.c_full[s], 1);
-      mbar_init(&bars.c_empty[s], 128);
+      mbar_init(&bars.c_empty[s], kConvArrivals);
     }
     mbar_init(&bars.teardown, 1);
     fence_mbar_init();
@@ -145,9 +153,10 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
       if (!(ok = warp_wait(&bars.q_free[t], (nq[t] & 1) ^ 1, abort_flag))) return;
       if (!withhold) {
         if (elect_one()) {
-          mbar_arrive_expect_tx(&bars.q_full[t], q_bytes);
+          uint64_t* bar = FP8 ? &bars.q_raw[t] : &bars.q_full[t][nq[t] & 1];
+          mbar_arrive_expect_tx(bar, q_bytes);
           for (int pn = 0; pn < C::kPanels; ++pn)
-            tma_load_3d(smem + C::kOffQ + t * C::kTileBytes + pn * 16384, &a.tm_q, &bars.q_full[t], pn * 64,
+            tma_load_3d(smem + C::kOffQ + t * C::kTileBytes + pn * 16384, &a.tm_q, bar, pn * 64,
                         p.h * (a.Hq / a.Hkv), p.q.start + p.tok + t * a.tpt1);
         }
         __syncwarp();
@@ -197,7 +206,10 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     // Let every issued copy land before the CTA can exit (an earlier load's slot
     // was refilled only after its reader completed, so it has landed).
     for (int t = 0; t < C::kTiles; ++t)
-      if (nq[t] > 0) mbar_wait_drain(&bars.q_full[t], (nq[t] - 1) & 1);
+      if (nq[t] > 0) {
+        const int last = nq[t] - 1;
+        mbar_wait_drain(FP8 ? &bars.q_raw[t] : &bars.q_full[t][last & 1], FP8 ? last & 1 : (last >> 1) & 1);
+      }
     for (int x = max(0, nk - C::kKStages); x < nk; ++x)
       mbar_wait_drain(&bars.k_full[x % C::kKStages], (x / C::kKStages) & 1);
     for (int x = max(0, nv - C::kVStages); x < nv; ++x)
@@ -210,18 +222,17 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     // Per key block j and half t: O_t += P_t V_j, then at once S_t for block
     // j + 1 (its columns are P_t's, which the products of one thread have read
     // by then, as they execute in issue order).
-    constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);  // Q, K both K-major
-    constexpr uint32_t kIdO = idesc_bf16(128, D, false, true);     // P from TMEM, V MN-major
+    // Q, K both K-major; P from TMEM, V MN-major
+    constexpr uint32_t kIdS = FP8 ? idesc_f16(128, 128, false, false) : idesc_bf16(128, 128, false, false);
+    constexpr uint32_t kIdO = FP8 ? idesc_f16(128, D, false, true) : idesc_bf16(128, D, false, true);
     const uint64_t dq0 = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
-    const uint64_t dk0 = sdesc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
-    const uint64_t dv0 = sdesc_sw128(smem_u32(smem + C::kOffV), 16384, 1024);
+    const uint64_t dk0 = Tile<D>::desc_k(smem + C::kOffK), dv0 = Tile<D>::desc_v(smem + C::kOffV);
     auto issue_s = [&](int t, int st, bool last) {  // by the elected lane
       const uint32_t qo = (uint32_t)(t * C::kTileBytes) >> 4, ko = (uint32_t)(st * C::kTileBytes) >> 4;
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {  // each k-step reads 32 bytes of every row
-        const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-        mma_ss(tmem + C::col_s(t), dq0 + qo + off, dk0 + ko + off, kIdS, kk > 0);
-      }
+      for (int kk = 0; kk < D / 16; ++kk)  // each k-step reads 32 bytes of every row
+        mma_ss(tmem + C::col_s(t), dq0 + qo + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+               dk0 + ko + Tile<D>::step_k(kk), kIdS, kk > 0);
       mma_commit(&bars.s_full[t]);
       if (last) mma_commit(&bars.q_free[t]);  // the tile's last product to read Q
     };
@@ -236,7 +247,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
       ok = warp_wait(&bars.k_full[g % C::kKStages], (g / C::kKStages) & 1, abort_flag);
       for (int t = 0; t < C::kTiles && ok; ++t)
         if (nb[t] > 0) {
-          if (!(ok = warp_wait(&bars.q_full[t], nq[t] & 1, abort_flag))) break;
+          if (!(ok = warp_wait(&bars.q_full[t][nq[t] & 1], (nq[t] >> 1) & 1, abort_flag))) break;
           tc_fence_after();
           if (elect_one()) issue_s(t, g % C::kKStages, nb[t] == 1);
           __syncwarp();
@@ -268,7 +279,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
               const uint32_t vo = (uint32_t)(s * C::kTileBytes) >> 4;
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk)  // P columns [8 kk, 8 kk + 8), V rows [16 kk, 16 kk + 16)
-                mma_ts(tmem + C::col_o(t), tmem + C::col_s(t) + kk * 8, dv0 + vo + kk * (2048 >> 4), kIdO,
+                mma_ts(tmem + C::col_o(t), tmem + C::col_s(t) + kk * 8, dv0 + vo + Tile<D>::step_v(kk), kIdO,
                        (j > 0 || kk > 0) ? 1u : 0u);
               if (j == nb[t] - 1) mma_commit(&bars.o_done[t]);
               if (t == v_last) mma_commit(&bars.v_empty[s]);
@@ -295,27 +306,36 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
   } else if (FP8 && warp >= C::kWarpConv) {
     // ------------------------------------------------------------ converters
     const int tid = threadIdx.x - C::kWarpConv * 32;
-    int g = 0;
+    constexpr int kCS = FP8 ? C::kCStages : 1;
+    const int G = a.Hq / a.Hkv;
+    int g = 0, nq[2] = {0, 0};
     bool ok = true;
+    auto convert = [&](int x, uint64_t* empty, int use, uint8_t* dst, uint64_t* full, int rows) {
+      const int cs = x % kCS;
+      ok = warp_wait2(&bars.c_full[cs], (x / kCS) & 1, empty, (use & 1) ^ 1, abort_flag);
+      if (!ok) return;
+      convert_tile<D>(smem + C::kOffC + cs * C::kCodeBytes, dst, rows, tid);
+      conv_arrive(full, &bars.c_empty[cs], lane);
+    };
+    auto convert_half = [&](int t) {  // Q of half t, in the order in which it was loaded
+      if (!(ok = warp_wait(&bars.q_raw[t], nq[t] & 1, abort_flag))) return;
+      const int rows = min(a.tpt1, p.q.n - p.tok - t * a.tpt1) * G;
+      convert_q<D, false>(smem + C::kOffQ + t * C::kTileBytes, bars.q_ex[nq[t] & 1][t], (rows + 31) / 32, tid);
+      conv_arrive(&bars.q_full[t][nq[t] & 1], nullptr, lane);
+      ++nq[t];
+    };
     while (ok && walk.step(a, p)) {
       int nb[2];
       half_blocks<C::kTiles>(a, p, nb);
       const int nbm = max(nb[0], nb[1]);
+      if (nb[0] > 0) convert_half(0);
       for (int j = 0; ok && j < nbm; ++j, ++g) {
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-          constexpr int kCS = FP8 ? C::kCStages : 1;
-          const int x = 2 * g + kv, cs = x % kCS, st = kv ? g % C::kVStages : g % C::kKStages;
-          const int use = kv ? g / C::kVStages : g / C::kKStages;
-          uint64_t* empty = kv ? &bars.v_empty[st] : &bars.k_empty[st];
-          ok = warp_wait2(&bars.c_full[cs], (x / kCS) & 1, empty, (use & 1) ^ 1, abort_flag);
-          if (!ok) break;
-          convert_tile<D>(smem + C::kOffC + cs * C::kCodeBytes,
-                          smem + (kv ? C::kOffV : C::kOffK) + st * C::kTileBytes, p.q.len - (p.jb + j) * 128, tid);
-          fence_proxy_async_smem();
-          mbar_arrive(kv ? &bars.v_full[st] : &bars.k_full[st]);
-          mbar_arrive(&bars.c_empty[cs]);
-        }
+        const int ks = g % C::kKStages, vs = g % C::kVStages, rows = p.q.len - (p.jb + j) * 128;
+        convert(2 * g, &bars.k_empty[ks], g / C::kKStages, smem + C::kOffK + ks * C::kTileBytes, &bars.k_full[ks], rows);
+        if (ok && j == 0 && nb[1] > 0) convert_half(1);
+        if (!ok) break;
+        convert(2 * g + 1, &bars.v_empty[vs], g / C::kVStages, smem + C::kOffV + vs * C::kTileBytes, &bars.v_full[vs],
+                rows);
       }
     }
   } else {
@@ -325,7 +345,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lane_off + C::col_s(t);
     const uint32_t t_o = tmem + lane_off + C::col_o(t);
-    const float sl2 = a.scale_log2;
+    constexpr float kBias = FP8 ? kPBias : 0.f;
     const int G = a.Hq / a.Hkv, rt = r / G, rh = r - rt * G;  // this row's token within the half, and head
     const bool o32 = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
     int np = 0, nq = 0;  // blocks and tiles of this half so far
@@ -337,6 +357,11 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
       const int tok0 = p.tok + t * a.tpt1, tok = tok0 + rt;
       const int off = p.q.len - p.q.n;  // causal: token i sees keys 0 .. i + off
       const bool valid = rt < a.tpt1 && tok < p.q.n;
+      float sl2 = a.scale_log2;
+      if (FP8 && nb > 0) {  // (their place is written again two tiles on, after the products of this one's P)
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars.q_full[t][nq & 1], (nq >> 1) & 1, abort_flag)))) break;
+        sl2 *= __uint_as_float((uint32_t)bars.q_ex[nq & 1][t][r] << 23);
+      }
       float m_ref = -INFINITY;  // exponent reference, log2 units of scaled scores
       float l_sum = 0.f;        // sum of 2^(s * sl2 - m_ref) over the keys seen so far
       for (int j = 0; j < nb; ++j, ++np) {
@@ -379,7 +404,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
         }
         const bool rescale = __any_sync(0xffffffffu, move && j > 0);
         float2 sum4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;  // a row that has seen no key yet: P = 0
+        const float m_use = (m_ref == -INFINITY ? 0.f : m_ref) - kBias;  // a row that has seen no key yet: P = 0
         const float2 scale2 = make_float2(sl2, sl2), shift2 = make_float2(-m_use, -m_use);
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch) {  // P as bf16 pairs over the first 64 columns of S_t
@@ -390,7 +415,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
                 ffma2(make_float2(__uint_as_float(sr[ch][c]), __uint_as_float(sr[ch][c + 1])), scale2, shift2);
             const float2 e = make_float2(ex2(x.x), ex2(x.y));
             sum4[(c >> 1) & 3] = fadd2(sum4[(c >> 1) & 3], e);
-            pk[c >> 1] = pack_bf16x2(e.x, e.y);
+            pk[c >> 1] = FP8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
           }
           tmem_st16(t_s + 16 * ch, pk);
         }
@@ -415,7 +440,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const bool seen = l_sum > 0.f;
-      const float lse2 = seen ? m_ref + log2f(l_sum) : -INFINITY;
+      const float lse2 = seen ? m_ref - kBias + log2f(l_sum) : -INFINITY;
       const float inv = seen ? a.o_scale / l_sum : 0.f;
       if (p.whole()) {
         const long long row = ((long long)(p.q.start + tok) * a.Hq) + p.h * G + rh;
@@ -488,7 +513,8 @@ template <int D, bool FP8>
 cudaError_t launch(const PagedArgs& a, int ctas, cudaStream_t stream) {
   using C = CCfg<D, FP8>;
   auto kern = a.causal ? fa_paged_chunk_kernel<D, FP8, true> : fa_paged_chunk_kernel<D, FP8, false>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  static std::atomic<unsigned long long> done[2];  // devices (a bit each) that know the kernel's shared memory
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes, done[a.causal]);
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)ctas, C::kThreads, C::kSmemBytes, stream>>>(a);
   return cudaGetLastError();

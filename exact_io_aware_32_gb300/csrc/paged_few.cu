@@ -17,8 +17,8 @@
 // one), P in columns of its own, O. Persistent CTAs over ranges of the row of
 // tiles (paged_work.cuh), rings and barriers counting on across tiles.
 //
-// Warp roles: 0-3 softmax and epilogue, 4 TMA, 5 MMA, and with E4M3 caches four
-// converter warps (codes to bf16 operands).
+// Warp roles: 0-3 softmax and epilogue, 4 TMA, 5 MMA, and with E4M3 caches eight
+// converter warps (codes to f16 operands).
 #include "paged_pipe.cuh"
 
 namespace fa {
@@ -31,7 +31,7 @@ template <int D_, bool FP8_>
 struct FCfg {
   static constexpr int D = D_;
   static constexpr int kPanels = D / 64;
-  static constexpr int kTileBytes = kPanels * 16384;  // 128 rows, bf16
+  static constexpr int kTileBytes = kPanels * 16384;  // 128 rows, 16-bit
   static constexpr int kCodeBytes = 128 * D;          // 128 rows of codes
   static constexpr int kKStages = D == 64 ? 4 : 2;
   static constexpr int kVStages = D == 64 ? 4 : (FP8_ ? 2 : 3);
@@ -42,23 +42,26 @@ struct FCfg {
   static constexpr int kOffC = kOffV + kVStages * kTileBytes;
   static constexpr int kOffJoin = kOffC + kCStages * kCodeBytes;  // 4 quarters x 32 columns x 33 floats
   static constexpr int kOffBar = kOffJoin + 4 * 32 * 33 * 4 + 4 * 32 * 8;
-  static constexpr int kSmemBytes = kOffBar + 384 + 1024;  // barriers, alignment slack
+  static constexpr int kSmemBytes = kOffBar + 448 + 1024;  // barriers, alignment slack
   static_assert(kSmemBytes <= 232448, "shared memory");
   static constexpr uint32_t kColS = 0, kColP = 256, kColO = 320, kTmemCols = 512;
   static constexpr int kWarpTma = 4, kWarpMma = 5, kWarpConv = 6;
-  static constexpr int kThreads = 192 + (FP8_ ? 128 : 0);
+  static constexpr int kThreads = 192 + (FP8_ ? 256 : 0);
 };
 
 struct FBars {
-  uint64_t q_full, q_free;
+  // q_full of tile n is q_full[n & 1]: with E4M3 caches the softmax waits for it too, maybe only after the next tile's
+  // Q is there, and one barrier would then have gone through both parities
+  uint64_t q_raw, q_full[2], q_free;  // E4M3 caches: Q as loaded, as converted
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], c_full[6], c_empty[6];
   uint64_t s_full[2], s_free[2], p_full, pv_done, o_free;
   uint64_t teardown;
   uint32_t tmem_base;
   int abort;
   Range range;
+  uint8_t q_ex[2][32];  // E4M3 caches: the exponents of Q's row scales, of this tile and the one before
 };
-static_assert(sizeof(FBars) <= 384, "barriers exceed their shared memory");
+static_assert(sizeof(FBars) <= 448, "barriers exceed their shared memory");
 
 template <int D, bool FP8, bool CAUSAL>
 __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel(const __grid_constant__ PagedArgs a) {
@@ -79,17 +82,19 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
   }
   if (threadIdx.x == 0) {
     bars.abort = 0;
-    mbar_init(&bars.q_full, 1);
+    mbar_init(&bars.q_raw, 1);
+    mbar_init(&bars.q_full[0], FP8 ? kConvArrivals : 1);
+    mbar_init(&bars.q_full[1], FP8 ? kConvArrivals : 1);
     mbar_init(&bars.q_free, 1);
     for (int s = 0; s < 4; ++s) {
-      mbar_init(&bars.k_full[s], FP8 ? 128 : 1);
+      mbar_init(&bars.k_full[s], FP8 ? kConvArrivals : 1);
       mbar_init(&bars.k_empty[s], 1);
-      mbar_init(&bars.v_full[s], FP8 ? 128 : 1);
+      mbar_init(&bars.v_full[s], FP8 ? kConvArrivals : 1);
       mbar_init(&bars.v_empty[s], 1);
     }
     for (int s = 0; s < 6; ++s) {
       mbar_init(&bars.c_full[s], 1);
-      mbar_init(&bars.c_empty[s], 128);
+      mbar_init(&bars.c_empty[s], kConvArrivals);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars.s_full[s], 1);
@@ -125,7 +130,9 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
       tma_prefetch_desc(&a.tm_v);
     }
     __syncwarp();
-    const uint32_t q_bytes = (uint32_t)(4 * G * a.tpt * D * 2);
+    // E4M3 caches: one copy of Q, which the converters make four of
+    constexpr int kCopies = FP8 ? 1 : 4;
+    const uint32_t q_bytes = (uint32_t)(kCopies * G * a.tpt * D * 2);
     Parts parts{};
     int g = 0, nk = 0, nv = 0, nc = 0, nq = 0;  // key blocks, and loads issued
     bool ok = true;
@@ -134,6 +141,23 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
       note_piece(parts, p);
       const int nb = p.je - p.jb;
       if (nb == 0) continue;
+      // Q of the tile, once its slot's last reader is done
+      auto load_q = [&]() {
+        if (!(ok = warp_wait(&bars.q_free, (nq & 1) ^ 1, abort_flag))) return;
+        if (!withhold) {
+          uint64_t* q_bar = FP8 ? &bars.q_raw : &bars.q_full[nq & 1];
+          if (elect_one()) {
+            mbar_arrive_expect_tx(q_bar, q_bytes);
+            for (int w = 0; w < kCopies; ++w)
+              for (int pn = 0; pn < C::kPanels; ++pn)
+                tma_load_3d(smem + C::kOffQ + pn * 16384 + w * 4096, &a.tm_q, q_bar, pn * 64, p.h * G,
+                            p.q.start + p.tok);
+          }
+          __syncwarp();
+          ++nq;
+        }
+        withhold = false;
+      };
       int page = lane_page(a, p, p.jb, lane);
       for (int j = 0; ok && j < nb; ++j, ++g) {
         const int jj = p.jb + j, page_now = page;
@@ -156,26 +180,14 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
           load_block<D, false>(a, p, jj, page_now, lane, &a.tm_v, smem + C::kOffV + sv * C::kTileBytes, &bars.v_full[sv]);
           nv = g + 1;
         }
-        if (j == 0) {  // Q after the first block's keys and values: it is small, and its slot may still be read
-          if (!(ok = warp_wait(&bars.q_free, (nq & 1) ^ 1, abort_flag))) break;
-          if (!withhold) {
-            if (elect_one()) {
-              mbar_arrive_expect_tx(&bars.q_full, q_bytes);
-              for (int w = 0; w < 4; ++w)
-                for (int pn = 0; pn < C::kPanels; ++pn)
-                  tma_load_3d(smem + C::kOffQ + pn * 16384 + w * 4096, &a.tm_q, &bars.q_full, pn * 64, p.h * G,
-                              p.q.start + p.tok);
-            }
-            __syncwarp();
-            ++nq;
-          }
-          withhold = false;
-        }
+        // after the first block's keys and values, whose slots are free earlier
+        if (j == 0) load_q();
       }
     }
     if (lane == 0) static_cast<Parts*>(a.parts)[blockIdx.x] = parts;
     // Let every issued copy land before the CTA can exit.
-    if (nq > 0) mbar_wait_drain(&bars.q_full, (nq - 1) & 1);
+    if (nq > 0 && FP8) mbar_wait_drain(&bars.q_raw, (nq - 1) & 1);
+    if (nq > 0 && !FP8) mbar_wait_drain(&bars.q_full[(nq - 1) & 1], ((nq - 1) >> 1) & 1);
     for (int x = max(0, nk - C::kKStages); x < nk; ++x)
       mbar_wait_drain(&bars.k_full[x % C::kKStages], (x / C::kKStages) & 1);
     for (int x = max(0, nv - C::kVStages); x < nv; ++x)
@@ -187,11 +199,11 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     // ------------------------------------------------------------ MMA issuer
     // S of block g + 1 while the softmax works on block g, then P V of block g;
     // at a tile's end P V first, since the next tile's Q is still on its way.
-    constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);  // Q, K both K-major
-    constexpr uint32_t kIdO = idesc_bf16(128, D, false, true);     // P from TMEM, V MN-major
+    // Q, K both K-major; P from TMEM, V MN-major
+    constexpr uint32_t kIdS = FP8 ? idesc_f16(128, 128, false, false) : idesc_bf16(128, 128, false, false);
+    constexpr uint32_t kIdO = FP8 ? idesc_f16(128, D, false, true) : idesc_bf16(128, D, false, true);
     const uint64_t dq0 = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
-    const uint64_t dk0 = sdesc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
-    const uint64_t dv0 = sdesc_sw128(smem_u32(smem + C::kOffV), 16384, 1024);
+    const uint64_t dk0 = Tile<D>::desc_k(smem + C::kOffK), dv0 = Tile<D>::desc_v(smem + C::kOffV);
     auto make_s = [&](int g, bool last) -> bool {
       const int ks = g % C::kKStages, b = g & 1;
       if (!warp_wait2(&bars.k_full[ks], (g / C::kKStages) & 1, &bars.s_free[b], ((g >> 1) & 1) ^ 1, abort_flag))
@@ -200,10 +212,9 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
       if (elect_one()) {
         const uint32_t ko = (uint32_t)(ks * C::kTileBytes) >> 4;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = ((kk >> 2) * 16384 + (kk & 3) * 32) >> 4;
-          mma_ss(tmem + C::kColS + b * 128, dq0 + off, dk0 + ko + off, kIdS, kk > 0);
-        }
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss(tmem + C::kColS + b * 128, dq0 + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
+                 dk0 + ko + Tile<D>::step_k(kk), kIdS, kk > 0);
         mma_commit(&bars.s_full[b]);
         mma_commit(&bars.k_empty[ks]);
         if (last) mma_commit(&bars.q_free);
@@ -216,7 +227,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     while (ok && walk.step(a, p)) {
       const int nb = p.je - p.jb;
       if (nb == 0) continue;
-      ok = warp_wait(&bars.q_full, n & 1, abort_flag) && make_s(g, nb == 1);
+      ok = warp_wait(&bars.q_full[n & 1], (n >> 1) & 1, abort_flag) && make_s(g, nb == 1);
       for (int j = 0; ok && j < nb; ++j, ++g) {
         if (j + 1 < nb && !(ok = make_s(g + 1, j + 2 == nb))) break;
         const int s = g % C::kVStages;
@@ -232,7 +243,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
           const uint32_t vo = (uint32_t)(s * C::kTileBytes) >> 4;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_ts(tmem + C::kColO, tmem + C::kColP + kk * 8, dv0 + vo + kk * (2048 >> 4), kIdO,
+            mma_ts(tmem + C::kColO, tmem + C::kColP + kk * 8, dv0 + vo + Tile<D>::step_v(kk), kIdO,
                    (j > 0 || kk > 0) ? 1u : 0u);
           mma_commit(&bars.pv_done);
           mma_commit(&bars.v_empty[s]);
@@ -246,26 +257,29 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     mbar_wait_drain(&bars.teardown, 0);
   } else if (FP8 && warp >= C::kWarpConv) {
     // ------------------------------------------------------------ converters
-    const int tid = threadIdx.x - C::kWarpConv * 32;
-    int g = 0;
+    // (four warps for the keys and Q, four for the values)
+    const bool values = warp >= C::kWarpConv + 4;
+    const int tid = (threadIdx.x - C::kWarpConv * 32) & 127;
+    constexpr int kCS = FP8 ? C::kCStages : 1;
+    int g = 0, n = 0;
     bool ok = true;
     while (ok && walk.step(a, p)) {
       for (int j = p.jb; ok && j < p.je; ++j, ++g) {
-#pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv) {
-          constexpr int kCS = FP8 ? C::kCStages : 1;
-          const int x = 2 * g + kv, cs = x % kCS, st = kv ? g % C::kVStages : g % C::kKStages;
-          const int use = kv ? g / C::kVStages : g / C::kKStages;
-          ok = warp_wait2(&bars.c_full[cs], (x / kCS) & 1, kv ? &bars.v_empty[st] : &bars.k_empty[st], (use & 1) ^ 1,
-                          abort_flag);
-          if (!ok) break;
-          convert_tile<D>(smem + C::kOffC + cs * C::kCodeBytes,
-                          smem + (kv ? C::kOffV : C::kOffK) + st * C::kTileBytes, p.q.len - j * 128, tid);
-          fence_proxy_async_smem();
-          mbar_arrive(kv ? &bars.v_full[st] : &bars.k_full[st]);
-          mbar_arrive(&bars.c_empty[cs]);
+        const int st = values ? g % C::kVStages : g % C::kKStages, use = values ? g / C::kVStages : g / C::kKStages;
+        const int x = 2 * g + (values ? 1 : 0), cs = x % kCS;
+        ok = warp_wait2(&bars.c_full[cs], (x / kCS) & 1, values ? &bars.v_empty[st] : &bars.k_empty[st], (use & 1) ^ 1,
+                        abort_flag);
+        if (!ok) break;
+        convert_tile<D>(smem + C::kOffC + cs * C::kCodeBytes, smem + (values ? C::kOffV : C::kOffK) + st * C::kTileBytes,
+                        p.q.len - j * 128, tid);
+        conv_arrive(values ? &bars.v_full[st] : &bars.k_full[st], &bars.c_empty[cs], lane);
+        if (!values && j == p.jb) {  // Q, in the order in which it was loaded
+          if (!(ok = warp_wait(&bars.q_raw, n & 1, abort_flag))) break;
+          convert_q<D, true>(smem + C::kOffQ, bars.q_ex[n & 1], 1, tid);
+          conv_arrive(&bars.q_full[n & 1], nullptr, lane);
         }
       }
+      if (p.je > p.jb) ++n;
     }
   } else {
     // ------------------------------------------------------------ softmax + epilogue
@@ -273,7 +287,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     const uint32_t t_s = tmem + lane_off + C::kColS + warp * 32;  // this warp's rows and keys
     const uint32_t t_p = tmem + lane_off + C::kColP;
     const uint32_t t_o = tmem + lane_off + C::kColO;
-    const float sl2 = a.scale_log2;
+    constexpr float kBias = FP8 ? kPBias : 0.f;
     const int rt = lane / G;  // this row's token within the tile
     float* join = reinterpret_cast<float*>(smem + C::kOffJoin);
     float2* stats = reinterpret_cast<float2*>(join + 4 * 32 * 33);  // (m, l) of each quarter and row
@@ -283,17 +297,23 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
       for (int c = 0; c < 4; ++c) tmem_st16(t_p + c * 16, zero);  // P outside this warp's columns stays 0
       tmem_st_wait();
     }
-    int g = 0;
+    int g = 0, n = 0;
     bool ok = true;
     while (ok && walk.step(a, p)) {
       const int nb = p.je - p.jb;
+      float sl2 = a.scale_log2;
+      if (FP8 && nb > 0) {  // (their place is written again two tiles on, after the products of this one's P)
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars.q_full[n & 1], (n >> 1) & 1, abort_flag)))) sl2 = 0.f;
+        sl2 *= __uint_as_float((uint32_t)bars.q_ex[n & 1][lane] << 23);
+        ++n;
+      }
       const int off = p.q.len - p.q.n;  // causal: token i sees keys 0 .. i + off
       const int lim_row = (CAUSAL ? min(p.tok + rt + off, p.q.len - 1) : p.q.len - 1) - warp * 32;
       const int lim_first = (CAUSAL ? min(p.tok + off, p.q.len - 1) : p.q.len - 1) - warp * 32;
       const int rows = min(a.tpt, p.q.n - p.tok) * G;
       float m_ref = -INFINITY;  // exponent reference, log2 units of scaled scores
       float l_sum = 0.f;        // sum of 2^(s * sl2 - m_ref) over this warp's keys so far
-      for (int j = 0; j < nb; ++j, ++g) {
+      for (int j = 0; ok && j < nb; ++j, ++g) {
         const int b = g & 1;
         ok = __all_sync(0xffffffffu, mbar_wait(&bars.s_full[b], (g >> 1) & 1, abort_flag));
         if (!ok) break;
@@ -322,7 +342,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
           m_ref = m_new;
         }
         const bool rescale = __any_sync(0xffffffffu, move && j > 0);
-        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;  // a row that has seen no key yet: P = 0
+        const float m_use = (m_ref == -INFINITY ? 0.f : m_ref) - kBias;  // a row that has seen no key yet: P = 0
         const float2 scale2 = make_float2(sl2, sl2), shift2 = make_float2(-m_use, -m_use);
         float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         uint32_t pk[16];
@@ -331,7 +351,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
           const float2 x = ffma2(make_float2(__uint_as_float(sr[c]), __uint_as_float(sr[c + 1])), scale2, shift2);
           const float2 e = make_float2(ex2(x.x), ex2(x.y));
           sum2[(c >> 1) & 1] = fadd2(sum2[(c >> 1) & 1], e);
-          pk[c >> 1] = pack_bf16x2(e.x, e.y);
+          pk[c >> 1] = FP8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
         }
         const float2 sum = fadd2(sum2[0], sum2[1]);
         l_sum = l_sum * alpha + (sum.x + sum.y);
@@ -379,7 +399,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
       const long long row0 = (long long)(p.q.start + p.tok) * a.Hq + p.h * G;  // row r: token r / G, head r % G
       const long long part0 = ((long long)blockIdx.x * 2 + (p.jb == 0 ? 1 : 0)) * 32;
       if (warp == 0 && lane < rows) {
-        const float lse2 = seen ? m + log2f(l) : -INFINITY;
+        const float lse2 = seen ? m - kBias + log2f(l) : -INFINITY;
         if (whole)
           a.lse[row0 + (long long)rt * a.Hq + (lane - rt * G)] = seen ? lse2 * kLn2 : -INFINITY;
         else
@@ -433,7 +453,8 @@ template <int D, bool FP8>
 cudaError_t launch(const PagedArgs& a, int ctas, cudaStream_t stream) {
   using C = FCfg<D, FP8>;
   auto kern = a.causal ? fa_paged_few_kernel<D, FP8, true> : fa_paged_few_kernel<D, FP8, false>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmemBytes);
+  static std::atomic<unsigned long long> done[2];  // devices (a bit each) that know the kernel's shared memory
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes, done[a.causal]);
   if (e != cudaSuccess) return e;
   kern<<<(unsigned)ctas, C::kThreads, C::kSmemBytes, stream>>>(a);
   return cudaGetLastError();

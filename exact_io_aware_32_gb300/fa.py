@@ -453,56 +453,61 @@ def fa_fwd_paged(q, q_stride: int, k_cache, v_cache, fp8: bool, descale_k: float
                                _addr(workspace), workspace_bytes, _stream(stream))
 
 
-def _ints(device, *named):
-    """Lengths, tables and slots as the library takes them: (name, tensor, shape), int32, contiguous, on ``device``."""
+def _int32(name, x, shape, device):
+    """Lengths, tables and slots as the library takes them: int32, contiguous, on ``device``; returns the address."""
     import torch
 
-    for name, x, shape in named:
-        if x.dtype != torch.int32 or x.device != device or not x.is_contiguous() or tuple(x.shape) != shape:
-            raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)} on {device}")
+    if x.dtype is not torch.int32 or x.shape != shape or x.device != device or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)} on {device}")
+    return x.data_ptr()
 
 
 def _packed(name, x, device):
-    """A packed [T, heads, d] bf16 tensor whose rows of one token are contiguous; returns its token stride."""
+    """Shape and token stride of a packed [T, heads, d] bf16 tensor whose rows of one token are contiguous."""
     import torch
 
-    if x.dim() != 3 or x.dtype != torch.bfloat16 or x.device != device:
+    if x.dtype is not torch.bfloat16 or x.device != device or x.dim() != 3:
         raise ValueError(f"{name} must be a bf16 tensor [T, heads, d] on {device}")
     T, H, d = x.shape
     st, sh, sd = x.stride()
     if (sd != 1 and d > 1) or (sh != d and H > 1):
         raise ValueError(f"the rows of one token of {name} must be contiguous")
-    return st if T > 1 else max(st - st % 8, H * d)  # one token: its stride is not used
+    return T, H, d, st if T > 1 else H * d  # one token: its stride is not used
 
 
 def _cache(k_cache, v_cache):
     """Shape (num_pages, Hkv, page_size, d) of a cache pair, and whether it holds E4M3 codes."""
     import torch
 
-    fp8 = k_cache.dtype in (torch.uint8, torch.float8_e4m3fn)
-    if k_cache.dim() != 4 or not (fp8 or k_cache.dtype == torch.bfloat16):
+    dtype = k_cache.dtype
+    fp8 = dtype is not torch.bfloat16
+    if (fp8 and dtype is not torch.float8_e4m3fn and dtype is not torch.uint8) or k_cache.dim() != 4:
         raise ValueError("the caches must be [num_pages, Hkv, page_size, d] tensors, bf16 or E4M3 codes")
-    if (v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or v_cache.device != k_cache.device
+    if (v_cache.shape != k_cache.shape or v_cache.dtype is not dtype or v_cache.device != k_cache.device
             or not k_cache.is_contiguous() or not v_cache.is_contiguous() or not k_cache.is_cuda):
         raise ValueError("k_cache and v_cache must be contiguous CUDA tensors of one shape, type and device")
     return *k_cache.shape, fp8
 
 
-def _on_device(device, stream):
-    """The context in which a helper allocates and launches: the tensors' device, and the stream asked for."""
-    import contextlib
-
+def _elsewhere(device, stream):
+    """None where a helper can allocate and launch as things stand: on the current device and its current stream. Else
+    the context to enter first (another device, or the stream asked for, for which the tensors it allocates are made)."""
     import torch
 
     if stream is None:
-        if device.index == torch.cuda.current_device():
-            return contextlib.nullcontext()
-        return torch.cuda.device(device)
+        return None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device)
     elif stream.device != device:
         raise ValueError(f"the stream must belong to {device}")
     return torch.cuda.stream(stream)
+
+
+def _current_stream(device) -> int:
+    """The current stream's handle, without making a Stream object (a few microseconds)."""
+    import torch
+
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def paged_plan(ctx_lens, new_lens, block_table, free_pages, page_size: int, num_tokens: int, free_head=None, out=None,
@@ -516,20 +521,24 @@ def paged_plan(ctx_lens, new_lens, block_table, free_pages, page_size: int, num_
     dev = ctx_lens.device
     if dev.type != "cuda" or ctx_lens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
         raise ValueError("expected CUDA tensors ctx_lens [R], block_table [R, max_pages], free_pages [n]")
-    R, max_pages, n_free = int(ctx_lens.shape[0]), int(block_table.shape[1]), int(free_pages.shape[0])
-    _ints(dev, ("ctx_lens", ctx_lens, (R,)), ("new_lens", new_lens, (R,)), ("free_pages", free_pages, (n_free,)),
-          ("block_table", block_table, (R, max_pages)))
-    if free_head is not None:
-        _ints(dev, ("free_head", free_head, (1,)))
-    with _on_device(dev, stream):
-        if out is None:
-            out = tuple(torch.empty(n, dtype=torch.int32, device=dev) for n in (R + 1, R, num_tokens, 1))
-        else:
-            _ints(dev, *zip(("query_start", "seq_lens", "slots", "pages_taken"), out,
-                            ((R + 1,), (R,), (num_tokens,), (1,))))
-        # an empty list has no address: any valid one will do, since none of its entries is read
-        st = fa_paged_plan(ctx_lens, new_lens, R, page_size, free_pages if n_free else out[3], n_free, free_head,
-                           block_table, max_pages, out[0], out[1], out[2], num_tokens, out[3])
+    context = _elsewhere(dev, stream)
+    if context is not None:
+        with context:
+            return paged_plan(ctx_lens, new_lens, block_table, free_pages, page_size, num_tokens, free_head, out)
+    (R, max_pages), n_free = block_table.shape, free_pages.shape[0]
+    ctx = _int32("ctx_lens", ctx_lens, (R,), dev)
+    new = _int32("new_lens", new_lens, (R,), dev)
+    free = _int32("free_pages", free_pages, (n_free,), dev)
+    table = _int32("block_table", block_table, (R, max_pages), dev)
+    head = None if free_head is None else _int32("free_head", free_head, (1,), dev)
+    if out is None:
+        out = tuple(torch.empty(n, dtype=torch.int32, device=dev) for n in (R + 1, R, num_tokens, 1))
+    start, lens, slots, taken = out
+    taken_at = _int32("pages_taken", taken, (1,), dev)
+    # an empty list has no address: any valid one will do, since none of its entries is read
+    st = load().fa_paged_plan(ctx, new, R, page_size, free if n_free else taken_at, n_free, head, table, max_pages,
+                              _int32("query_start", start, (R + 1,), dev), _int32("seq_lens", lens, (R,), dev),
+                              _int32("slots", slots, (num_tokens,), dev), num_tokens, taken_at, _current_stream(dev))
     if st != FA_OK:
         raise FAError(st, "fa_paged_plan")
     return out
@@ -541,13 +550,17 @@ def paged_store(k, v, slots, k_cache, v_cache, descale_k: float = 1.0, descale_v
     nowhere)."""
     P, Hkv, ps, d, fp8 = _cache(k_cache, v_cache)
     dev = k_cache.device
-    ks, vs = _packed("k", k, dev), _packed("v", v, dev)
-    T = int(k.shape[0])
-    if tuple(k.shape) != (T, Hkv, d) or tuple(v.shape) != (T, Hkv, d):
+    context = _elsewhere(dev, stream)
+    if context is not None:
+        with context:
+            return paged_store(k, v, slots, k_cache, v_cache, descale_k, descale_v)
+    T, kh, kd, ks = _packed("k", k, dev)
+    vT, vh, vd, vs = _packed("v", v, dev)
+    if kh != Hkv or vh != Hkv or kd != d or vd != d or vT != T:
         raise ValueError(f"k and v must be [T, {Hkv}, {d}], as the caches")
-    _ints(dev, ("slots", slots, (T,)))
-    with _on_device(dev, stream):
-        st = fa_paged_store(k, v, ks, vs, slots, T, Hkv, d, k_cache, v_cache, P, ps, fp8, descale_k, descale_v)
+    st = load().fa_paged_store(k.data_ptr(), v.data_ptr(), ks, vs, _int32("slots", slots, (T,), dev), T, Hkv, d,
+                               k_cache.data_ptr(), v_cache.data_ptr(), P, ps, fp8, descale_k, descale_v,
+                               _current_stream(dev))
     if st != FA_OK:
         raise FAError(st, "fa_paged_store")
 
@@ -564,33 +577,39 @@ def forward_paged(q, k_cache, v_cache, block_table, query_start, seq_lens, max_n
 
     P, Hkv, ps, d, fp8 = _cache(k_cache, v_cache)
     dev = k_cache.device
-    qs = _packed("q", q, dev)
-    T, Hq = int(q.shape[0]), int(q.shape[1])
-    if int(q.shape[2]) != d or block_table.dim() != 2 or query_start.dim() != 1:
-        raise ValueError(f"expected q [T, Hq, {d}], block_table [R, max_pages], query_start [R + 1]")
-    R, max_pages = int(block_table.shape[0]), int(block_table.shape[1])
-    _ints(dev, ("block_table", block_table, (R, max_pages)), ("query_start", query_start, (R + 1,)),
-          ("seq_lens", seq_lens, (R,)))
-    max_new = T if max_new is None else max_new
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    need = fa_fwd_paged_workspace_bytes(T, R, Hq, Hkv, d, max_new)
-    with _on_device(dev, stream):
-        if out is None:
-            out = torch.zeros((T, Hq, d), dtype=torch.bfloat16, device=dev)
-        elif out.dtype != torch.bfloat16 or tuple(out.shape) != (T, Hq, d) or not out.is_contiguous() \
-                or out.device != dev:
-            raise ValueError(f"out must be a contiguous bf16 tensor [{T}, {Hq}, {d}] on {dev}")
-        if lse is None:
-            lse = torch.zeros((T, Hq), dtype=torch.float32, device=dev)
-        elif lse.dtype != torch.float32 or tuple(lse.shape) != (T, Hq) or not lse.is_contiguous() or lse.device != dev:
-            raise ValueError(f"lse must be a contiguous fp32 tensor [{T}, {Hq}] on {dev}")
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        elif workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-        st = fa_fwd_paged(q, qs, k_cache, v_cache, fp8, descale_k, descale_v, block_table, max_pages, query_start,
-                          seq_lens, out, lse, T, R, Hq, Hkv, d, P, ps, max_new, scale, causal, workspace,
-                          workspace.numel() * workspace.element_size())
+    context = _elsewhere(dev, stream)
+    if context is not None:
+        with context:
+            return forward_paged(q, k_cache, v_cache, block_table, query_start, seq_lens, max_new, causal, scale,
+                                 descale_k, descale_v, out, lse, workspace)
+    T, Hq, qd, qs = _packed("q", q, dev)
+    if qd != d or block_table.dim() != 2:
+        raise ValueError(f"expected q [T, Hq, {d}] and block_table [R, max_pages]")
+    R, max_pages = block_table.shape
+    table = _int32("block_table", block_table, (R, max_pages), dev)
+    start = _int32("query_start", query_start, (R + 1,), dev)
+    lens = _int32("seq_lens", seq_lens, (R,), dev)
+    if max_new is None:
+        max_new = T
+    if scale is None:
+        scale = 1.0 / math.sqrt(d)
+    if out is None:
+        out = torch.zeros((T, Hq, d), dtype=torch.bfloat16, device=dev)
+    elif out.dtype is not torch.bfloat16 or out.shape != q.shape or out.device != dev or not out.is_contiguous():
+        raise ValueError(f"out must be a contiguous bf16 tensor [{T}, {Hq}, {d}] on {dev}")
+    if lse is None:
+        lse = torch.zeros((T, Hq), dtype=torch.float32, device=dev)
+    elif lse.dtype is not torch.float32 or lse.shape != (T, Hq) or lse.device != dev or not lse.is_contiguous():
+        raise ValueError(f"lse must be a contiguous fp32 tensor [{T}, {Hq}] on {dev}")
+    lib = load()
+    if workspace is None:
+        workspace = torch.empty(lib.fa_fwd_paged_workspace_bytes(T, R, Hq, Hkv, d, max_new), dtype=torch.uint8,
+                                device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    st = lib.fa_fwd_paged(q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), fp8, descale_k, descale_v, table,
+                          max_pages, start, lens, out.data_ptr(), lse.data_ptr(), T, R, Hq, Hkv, d, P, ps, max_new,
+                          scale, bool(causal), workspace.data_ptr(), workspace.nbytes, _current_stream(dev))
     if st != FA_OK:
         raise FAError(st, "fa_fwd_paged")
     return out, lse
