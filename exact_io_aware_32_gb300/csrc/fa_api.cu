@@ -227,7 +227,7 @@ int device_facts(int* num_sms, unsigned int** status) {
 }
 
 bool encode_map(CUtensorMap* m, const void* base, CUtensorMapDataType type, int rank, const unsigned long long* dims,
-                const unsigned long long* strides, const unsigned* box, bool swizzle) {
+                const unsigned long long* strides, const unsigned* box, int swizzle) {
   cuuint64_t n[5], s[4];
   cuuint32_t b[5], es[5];
   for (int i = 0; i < rank; ++i) {
@@ -237,8 +237,10 @@ bool encode_map(CUtensorMap* m, const void* base, CUtensorMapDataType type, int 
     if (i + 1 < rank) s[i] = strides[i];
   }
   return g_encode(m, type, (cuuint32_t)rank, const_cast<void*>(base), n, s, b, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  swizzle ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                  swizzle == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                  : swizzle == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                  : CU_TENSOR_MAP_SWIZZLE_NONE,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 int take_test_fault() { return g_test_fault.exchange(0); }

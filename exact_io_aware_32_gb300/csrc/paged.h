@@ -44,7 +44,8 @@ struct PagedArgs {
   // set by launch_paged
   CUtensorMap tm_q;         // bf16 [T][Hq][d], box 64 x (Hq / Hkv) x tokens of a 128-row (32-row) tile, 128B swizzle
   // A page's rows of one head, up to 128 of them, per copy. bf16: seen as [page, head][row / 8][panel][row % 8][64
-  // columns] with 128B swizzle, so that one copy brings every 64-column panel. E4M3: [page, head][row][d], unswizzled.
+  // columns] with 128B swizzle, so that one copy brings every 64-column panel. E4M3: [page, head][row][d], keys
+  // swizzled over their d-byte rows, values not.
   CUtensorMap tm_k, tm_v;
   int tpt;                  // tokens per tile
   int tpt1;                 // tokens per 128-row half of a tile (two halves at d = 128)
@@ -71,9 +72,9 @@ cudaError_t launch_paged(PagedArgs a, const PagedPlan& p, cudaStream_t stream);
 // The two kernels (paged_few.cu, paged_chunk.cu) and the join of cut tiles.
 cudaError_t launch_paged_few(const PagedArgs& a, int ctas, cudaStream_t stream);
 cudaError_t launch_paged_chunk(const PagedArgs& a, int ctas, cudaStream_t stream);
-// Tensor map (sizes, strides in bytes and box, innermost first), 128-byte swizzle or none.
+// Tensor map (sizes, strides in bytes and box, innermost first); swizzle: bytes (128 or 64), or 0 for none.
 bool encode_map(CUtensorMap* m, const void* base, CUtensorMapDataType type, int rank, const unsigned long long* dims,
-                const unsigned long long* strides, const unsigned* box, bool swizzle);
+                const unsigned long long* strides, const unsigned* box, int swizzle);
 // Allows the kernel its dynamic shared memory on the current device, once per device ('done' has a bit for each:
 // the attribute costs a microsecond, as long as a short call's whole kernel).
 cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<unsigned long long>& done);

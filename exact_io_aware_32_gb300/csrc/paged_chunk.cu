@@ -16,8 +16,8 @@
 // tensor store could write.
 //
 // Warp roles: a softmax warpgroup per 128-row half, the TMA warp, the MMA warp,
-// and with E4M3 caches a warpgroup that turns each 8-bit block into the f16
-// operands of the products (TMA -> 8-bit ring -> converters -> K/V rings).
+// and with E4M3 caches a warpgroup that turns value codes into f16 operands (TMA
+// -> ring of codes -> converters -> V ring) and Q into its two 8-bit parts.
 #include "paged_pipe.cuh"
 
 namespace fa {
@@ -37,11 +37,12 @@ struct CCfg {
   static constexpr int kPanels = D / 64;
   static constexpr int kTileBytes = kPanels * 16384;  // 128 rows, 16-bit
   static constexpr int kCodeBytes = 128 * D;          // 128 rows of codes
-  static constexpr int kKStages = 2, kVStages = FP8 && D == 128 ? 2 : 3;
-  static constexpr int kCStages = FP8 ? (D == 128 ? 2 : 4) : 0;
+  static constexpr int kKBytes = FP8 ? kCodeBytes : kTileBytes;  // a key block: codes stay codes
+  static constexpr int kKStages = FP8 ? 3 : 2, kVStages = FP8 && D == 128 ? 2 : 3;
+  static constexpr int kCStages = FP8 ? 3 : 0;  // value codes on their way to f16
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kOffQ + kTiles * kTileBytes;
-  static constexpr int kOffV = kOffK + kKStages * kTileBytes;
+  static constexpr int kOffV = kOffK + kKStages * kKBytes;
   static constexpr int kOffC = kOffV + kVStages * kTileBytes;
   static constexpr int kOffBar = kOffC + kCStages * kCodeBytes;
   static constexpr int kSmemBytes = kOffBar + (FP8 ? 1536 : 1024) + 1024;  // barriers, alignment slack
@@ -58,7 +59,7 @@ struct CBars {
   // by half. q_full of a half's tile n is q_full[t][n & 1]: with E4M3 caches the softmax waits for it too, maybe only
   // after the next tile's Q is there, and one barrier would then have gone through both parities
   uint64_t q_raw[2], q_full[2][2], q_free[2];  // E4M3 caches: Q as loaded, as converted
-  uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3], c_full[4], c_empty[4];
+  uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3], c_full[3], c_empty[3];
   uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
   uint64_t teardown;
   uint32_t tmem_base;
@@ -102,8 +103,8 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     bars.abort = 0;
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars.q_raw[s], 1);
-      mbar_init(&bars.q_full[s][0], FP8 ? kConvArrivals : 1);
-      mbar_init(&bars.q_full[s][1], FP8 ? kConvArrivals : 1);
+      mbar_init(&bars.q_full[s][0], FP8 ? 4 : 1);
+      mbar_init(&bars.q_full[s][1], FP8 ? 4 : 1);
       mbar_init(&bars.q_free[s], 1);
       mbar_init(&bars.s_full[s], 1);
       mbar_init(&bars.p_full[s], 128);
@@ -111,14 +112,12 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
       mbar_init(&bars.o_free[s], 128);
     }
     for (int s = 0; s < 3; ++s) {
-      mbar_init(&bars.k_full[s], FP8 ? kConvArrivals : 1);
+      mbar_init(&bars.k_full[s], 1);
       mbar_init(&bars.k_empty[s], 1);
-      mbar_init(&bars.v_full[s], FP8 ? kConvArrivals : 1);
+      mbar_init(&bars.v_full[s], FP8 ? 4 : 1);
       mbar_init(&bars.v_empty[s], 1);
-    }
-    for (int s = 0; s < 4; ++s) {
       mbar_init(&bars.c_full[s], 1);
-      mbar_init(&bars.c_empty[s], kConvArrivals);
+      mbar_init(&bars.c_empty[s], 4);
     }
     mbar_init(&bars.teardown, 1);
     fence_mbar_init();
@@ -145,7 +144,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     __syncwarp();
     const uint32_t q_bytes = (uint32_t)(a.Hq / a.Hkv * a.tpt1 * D * 2);
     Parts parts{};
-    int g = 0, nk = 0, nv = 0, nc = 0, nq[2] = {0, 0};  // key blocks, and loads issued
+    int g = 0, nk = 0, nv = 0, nq[2] = {0, 0};  // key blocks, and loads issued
     bool ok = true;
     // test hook: without the first Q tile, the MMA warp's first wait expires
     bool withhold = a.test_fault == 1;
@@ -174,32 +173,21 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
       for (int j = 0; ok && j < nbm; ++j, ++g) {
         const int jj = p.jb + j, page_now = page;
         if (j + 1 < nbm) page = lane_page(a, p, jj + 1, lane);
-        if constexpr (FP8) {
-          const int s0 = nc % C::kCStages;
-          if (!(ok = warp_wait(&bars.c_empty[s0], ((nc / C::kCStages) & 1) ^ 1, abort_flag))) break;
-          load_block<D, true>(a, p, jj, page_now, lane, &a.tm_k, smem + C::kOffC + s0 * C::kCodeBytes, &bars.c_full[s0]);
-          ++nc;
-        } else {
-          const int s = g % C::kKStages;
-          if (!(ok = warp_wait(&bars.k_empty[s], ((g / C::kKStages) & 1) ^ 1, abort_flag))) break;
-          load_block<D, false>(a, p, jj, page_now, lane, &a.tm_k, smem + C::kOffK + s * C::kTileBytes, &bars.k_full[s]);
-          nk = g + 1;
-        }
+        const int sk = g % C::kKStages;
+        if (!(ok = warp_wait(&bars.k_empty[sk], ((g / C::kKStages) & 1) ^ 1, abort_flag))) break;
+        load_block<D, FP8>(a, p, jj, page_now, lane, &a.tm_k, smem + C::kOffK + sk * C::kKBytes, &bars.k_full[sk]);
+        nk = g + 1;
         if (C::kTiles == 2 && j == 0 && nb[1] > 0) {
           load_q(1);
           if (!ok) break;
         }
-        if constexpr (FP8) {
-          const int s1 = nc % C::kCStages;
-          if (!(ok = warp_wait(&bars.c_empty[s1], ((nc / C::kCStages) & 1) ^ 1, abort_flag))) break;
-          load_block<D, true>(a, p, jj, page_now, lane, &a.tm_v, smem + C::kOffC + s1 * C::kCodeBytes, &bars.c_full[s1]);
-          ++nc;
-        } else {
-          const int s = g % C::kVStages;
-          if (!(ok = warp_wait(&bars.v_empty[s], ((g / C::kVStages) & 1) ^ 1, abort_flag))) break;
-          load_block<D, false>(a, p, jj, page_now, lane, &a.tm_v, smem + C::kOffV + s * C::kTileBytes, &bars.v_full[s]);
-          nv = g + 1;
-        }
+        constexpr int kS = FP8 ? C::kCStages : C::kVStages;
+        const int sv = g % kS;
+        if (!(ok = warp_wait(FP8 ? &bars.c_empty[sv] : &bars.v_empty[sv], ((g / kS) & 1) ^ 1, abort_flag))) break;
+        load_block<D, FP8>(a, p, jj, page_now, lane, &a.tm_v,
+                           smem + (FP8 ? C::kOffC + sv * C::kCodeBytes : C::kOffV + sv * C::kTileBytes),
+                           FP8 ? &bars.c_full[sv] : &bars.v_full[sv]);
+        nv = g + 1;
       }
     }
     if (lane == 0) static_cast<Parts*>(a.parts)[blockIdx.x] = parts;
@@ -212,27 +200,21 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
       }
     for (int x = max(0, nk - C::kKStages); x < nk; ++x)
       mbar_wait_drain(&bars.k_full[x % C::kKStages], (x / C::kKStages) & 1);
-    for (int x = max(0, nv - C::kVStages); x < nv; ++x)
-      mbar_wait_drain(&bars.v_full[x % C::kVStages], (x / C::kVStages) & 1);
-    if constexpr (FP8)
-      for (int x = max(0, nc - C::kCStages); x < nc; ++x)
-        mbar_wait_drain(&bars.c_full[x % C::kCStages], (x / C::kCStages) & 1);
+    constexpr int kS = FP8 ? C::kCStages : C::kVStages;
+    for (int x = max(0, nv - kS); x < nv; ++x)
+      mbar_wait_drain(FP8 ? &bars.c_full[x % kS] : &bars.v_full[x % kS], (x / kS) & 1);
   } else if (warp == C::kWarpMma) {
     // ------------------------------------------------------------ MMA issuer
     // Per key block j and half t: O_t += P_t V_j, then at once S_t for block
     // j + 1 (its columns are P_t's, which the products of one thread have read
     // by then, as they execute in issue order).
-    // Q, K both K-major; P from TMEM, V MN-major
-    constexpr uint32_t kIdS = FP8 ? idesc_f16(128, 128, false, false) : idesc_bf16(128, 128, false, false);
+    // P from TMEM, V MN-major
     constexpr uint32_t kIdO = FP8 ? idesc_f16(128, D, false, true) : idesc_bf16(128, D, false, true);
     const uint64_t dq0 = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
-    const uint64_t dk0 = Tile<D>::desc_k(smem + C::kOffK), dv0 = Tile<D>::desc_v(smem + C::kOffV);
+    const uint64_t dk0 = desc_keys<D, FP8>(smem + C::kOffK), dv0 = Tile<D>::desc_v(smem + C::kOffV);
     auto issue_s = [&](int t, int st, bool last) {  // by the elected lane
-      const uint32_t qo = (uint32_t)(t * C::kTileBytes) >> 4, ko = (uint32_t)(st * C::kTileBytes) >> 4;
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)  // each k-step reads 32 bytes of every row
-        mma_ss(tmem + C::col_s(t), dq0 + qo + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
-               dk0 + ko + Tile<D>::step_k(kk), kIdS, kk > 0);
+      issue_qk<D, FP8>(tmem + C::col_s(t), dq0 + ((uint32_t)(t * C::kTileBytes) >> 4),
+                       dk0 + ((uint32_t)(st * C::kKBytes) >> 4));
       mma_commit(&bars.s_full[t]);
       if (last) mma_commit(&bars.q_free[t]);  // the tile's last product to read Q
     };
@@ -310,13 +292,6 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     const int G = a.Hq / a.Hkv;
     int g = 0, nq[2] = {0, 0};
     bool ok = true;
-    auto convert = [&](int x, uint64_t* empty, int use, uint8_t* dst, uint64_t* full, int rows) {
-      const int cs = x % kCS;
-      ok = warp_wait2(&bars.c_full[cs], (x / kCS) & 1, empty, (use & 1) ^ 1, abort_flag);
-      if (!ok) return;
-      convert_tile<D>(smem + C::kOffC + cs * C::kCodeBytes, dst, rows, tid);
-      conv_arrive(full, &bars.c_empty[cs], lane);
-    };
     auto convert_half = [&](int t) {  // Q of half t, in the order in which it was loaded
       if (!(ok = warp_wait(&bars.q_raw[t], nq[t] & 1, abort_flag))) return;
       const int rows = min(a.tpt1, p.q.n - p.tok - t * a.tpt1) * G;
@@ -329,13 +304,14 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
       half_blocks<C::kTiles>(a, p, nb);
       const int nbm = max(nb[0], nb[1]);
       if (nb[0] > 0) convert_half(0);
+      if (ok && nb[1] > 0) convert_half(1);
       for (int j = 0; ok && j < nbm; ++j, ++g) {
-        const int ks = g % C::kKStages, vs = g % C::kVStages, rows = p.q.len - (p.jb + j) * 128;
-        convert(2 * g, &bars.k_empty[ks], g / C::kKStages, smem + C::kOffK + ks * C::kTileBytes, &bars.k_full[ks], rows);
-        if (ok && j == 0 && nb[1] > 0) convert_half(1);
+        const int vs = g % C::kVStages, cs = g % kCS;
+        ok = warp_wait2(&bars.c_full[cs], (g / kCS) & 1, &bars.v_empty[vs], ((g / C::kVStages) & 1) ^ 1, abort_flag);
         if (!ok) break;
-        convert(2 * g + 1, &bars.v_empty[vs], g / C::kVStages, smem + C::kOffV + vs * C::kTileBytes, &bars.v_full[vs],
-                rows);
+        convert_tile<D, 128>(smem + C::kOffC + cs * C::kCodeBytes, smem + C::kOffV + vs * C::kTileBytes,
+                             p.q.len - (p.jb + j) * 128, tid);
+        conv_arrive(&bars.v_full[vs], &bars.c_empty[cs], lane);
       }
     }
   } else {
@@ -360,7 +336,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
       float sl2 = a.scale_log2;
       if (FP8 && nb > 0) {  // (their place is written again two tiles on, after the products of this one's P)
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars.q_full[t][nq & 1], (nq >> 1) & 1, abort_flag)))) break;
-        sl2 *= __uint_as_float((uint32_t)bars.q_ex[nq & 1][t][r] << 23);
+        sl2 *= unscale(bars.q_ex[nq & 1][t][r]);
       }
       float m_ref = -INFINITY;  // exponent reference, log2 units of scaled scores
       float l_sum = 0.f;        // sum of 2^(s * sl2 - m_ref) over the keys seen so far

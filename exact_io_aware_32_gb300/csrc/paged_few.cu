@@ -18,7 +18,7 @@
 // tiles (paged_work.cuh), rings and barriers counting on across tiles.
 //
 // Warp roles: 0-3 softmax and epilogue, 4 TMA, 5 MMA, and with E4M3 caches eight
-// converter warps (codes to f16 operands).
+// converter warps (value codes to f16, Q to its two parts).
 #include "paged_pipe.cuh"
 
 namespace fa {
@@ -33,27 +33,28 @@ struct FCfg {
   static constexpr int kPanels = D / 64;
   static constexpr int kTileBytes = kPanels * 16384;  // 128 rows, 16-bit
   static constexpr int kCodeBytes = 128 * D;          // 128 rows of codes
-  static constexpr int kKStages = D == 64 ? 4 : 2;
-  static constexpr int kVStages = D == 64 ? 4 : (FP8_ ? 2 : 3);
-  static constexpr int kCStages = FP8_ ? (D == 64 ? 6 : 3) : 0;
+  static constexpr int kKBytes = FP8_ ? kCodeBytes : kTileBytes;  // a key block: codes stay codes
+  static constexpr int kKStages = FP8_ ? (D == 64 ? 6 : 4) : (D == 64 ? 4 : 2);
+  static constexpr int kVStages = FP8_ ? (D == 64 ? 3 : 2) : (D == 64 ? 4 : 3);
+  static constexpr int kCStages = FP8_ ? (D == 64 ? 6 : 3) : 0;  // value codes on their way to f16
   static constexpr int kOffQ = 0;
   static constexpr int kOffK = kOffQ + kTileBytes;
-  static constexpr int kOffV = kOffK + kKStages * kTileBytes;
+  static constexpr int kOffV = kOffK + kKStages * kKBytes;
   static constexpr int kOffC = kOffV + kVStages * kTileBytes;
   static constexpr int kOffJoin = kOffC + kCStages * kCodeBytes;  // 4 quarters x 32 columns x 33 floats
   static constexpr int kOffBar = kOffJoin + 4 * 32 * 33 * 4 + 4 * 32 * 8;
-  static constexpr int kSmemBytes = kOffBar + 448 + 1024;  // barriers, alignment slack
+  static constexpr int kSmemBytes = kOffBar + 480 + 1024;  // barriers, alignment slack
   static_assert(kSmemBytes <= 232448, "shared memory");
   static constexpr uint32_t kColS = 0, kColP = 256, kColO = 320, kTmemCols = 512;
-  static constexpr int kWarpTma = 4, kWarpMma = 5, kWarpConv = 6;
-  static constexpr int kThreads = 192 + (FP8_ ? 256 : 0);
+  static constexpr int kWarpTma = 4, kWarpMma = 5, kWarpConv = 6, kConvWarps = 8;
+  static constexpr int kThreads = 192 + (FP8_ ? 32 * kConvWarps : 0);
 };
 
 struct FBars {
   // q_full of tile n is q_full[n & 1]: with E4M3 caches the softmax waits for it too, maybe only after the next tile's
   // Q is there, and one barrier would then have gone through both parities
   uint64_t q_raw, q_full[2], q_free;  // E4M3 caches: Q as loaded, as converted
-  uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4], c_full[6], c_empty[6];
+  uint64_t k_full[6], k_empty[6], v_full[4], v_empty[4], c_full[6], c_empty[6];
   uint64_t s_full[2], s_free[2], p_full, pv_done, o_free;
   uint64_t teardown;
   uint32_t tmem_base;
@@ -61,7 +62,7 @@ struct FBars {
   Range range;
   uint8_t q_ex[2][32];  // E4M3 caches: the exponents of Q's row scales, of this tile and the one before
 };
-static_assert(sizeof(FBars) <= 448, "barriers exceed their shared memory");
+static_assert(sizeof(FBars) <= 480, "barriers exceed their shared memory");
 
 template <int D, bool FP8, bool CAUSAL>
 __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel(const __grid_constant__ PagedArgs a) {
@@ -83,18 +84,18 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
   if (threadIdx.x == 0) {
     bars.abort = 0;
     mbar_init(&bars.q_raw, 1);
-    mbar_init(&bars.q_full[0], FP8 ? kConvArrivals : 1);
-    mbar_init(&bars.q_full[1], FP8 ? kConvArrivals : 1);
+    mbar_init(&bars.q_full[0], FP8 ? 4 : 1);
+    mbar_init(&bars.q_full[1], FP8 ? 4 : 1);
     mbar_init(&bars.q_free, 1);
-    for (int s = 0; s < 4; ++s) {
-      mbar_init(&bars.k_full[s], FP8 ? kConvArrivals : 1);
-      mbar_init(&bars.k_empty[s], 1);
-      mbar_init(&bars.v_full[s], FP8 ? kConvArrivals : 1);
-      mbar_init(&bars.v_empty[s], 1);
-    }
     for (int s = 0; s < 6; ++s) {
+      mbar_init(&bars.k_full[s], 1);
+      mbar_init(&bars.k_empty[s], 1);
       mbar_init(&bars.c_full[s], 1);
-      mbar_init(&bars.c_empty[s], kConvArrivals);
+      mbar_init(&bars.c_empty[s], C::kConvWarps);
+    }
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(&bars.v_full[s], FP8 ? C::kConvWarps : 1);
+      mbar_init(&bars.v_empty[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars.s_full[s], 1);
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     constexpr int kCopies = FP8 ? 1 : 4;
     const uint32_t q_bytes = (uint32_t)(kCopies * G * a.tpt * D * 2);
     Parts parts{};
-    int g = 0, nk = 0, nv = 0, nc = 0, nq = 0;  // key blocks, and loads issued
+    int g = 0, nk = 0, nv = 0, nq = 0;  // key blocks, and loads issued
     bool ok = true;
     bool withhold = a.test_fault == 1;  // test hook: the MMA warp's first wait expires
     while (ok && walk.step(a, p)) {
@@ -162,26 +163,18 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
       for (int j = 0; ok && j < nb; ++j, ++g) {
         const int jj = p.jb + j, page_now = page;
         if (j + 1 < nb) page = lane_page(a, p, jj + 1, lane);
-        if constexpr (FP8) {
-          const int s0 = nc % C::kCStages;
-          if (!(ok = warp_wait(&bars.c_empty[s0], ((nc / C::kCStages) & 1) ^ 1, abort_flag))) break;
-          load_block<D, true>(a, p, jj, page_now, lane, &a.tm_k, smem + C::kOffC + s0 * C::kCodeBytes, &bars.c_full[s0]);
-          ++nc;
-          const int s1 = nc % C::kCStages;
-          if (!(ok = warp_wait(&bars.c_empty[s1], ((nc / C::kCStages) & 1) ^ 1, abort_flag))) break;
-          load_block<D, true>(a, p, jj, page_now, lane, &a.tm_v, smem + C::kOffC + s1 * C::kCodeBytes, &bars.c_full[s1]);
-          ++nc;
-        } else {
-          const int sk = g % C::kKStages, sv = g % C::kVStages;
-          if (!(ok = warp_wait(&bars.k_empty[sk], ((g / C::kKStages) & 1) ^ 1, abort_flag))) break;
-          load_block<D, false>(a, p, jj, page_now, lane, &a.tm_k, smem + C::kOffK + sk * C::kTileBytes, &bars.k_full[sk]);
-          nk = g + 1;
-          if (!(ok = warp_wait(&bars.v_empty[sv], ((g / C::kVStages) & 1) ^ 1, abort_flag))) break;
-          load_block<D, false>(a, p, jj, page_now, lane, &a.tm_v, smem + C::kOffV + sv * C::kTileBytes, &bars.v_full[sv]);
-          nv = g + 1;
-        }
-        // after the first block's keys and values, whose slots are free earlier
-        if (j == 0) load_q();
+        const int sk = g % C::kKStages;
+        if (!(ok = warp_wait(&bars.k_empty[sk], ((g / C::kKStages) & 1) ^ 1, abort_flag))) break;
+        load_block<D, FP8>(a, p, jj, page_now, lane, &a.tm_k, smem + C::kOffK + sk * C::kKBytes, &bars.k_full[sk]);
+        nk = g + 1;
+        constexpr int kS = FP8 ? C::kCStages : C::kVStages;
+        const int sv = g % kS;
+        if (!(ok = warp_wait(FP8 ? &bars.c_empty[sv] : &bars.v_empty[sv], ((g / kS) & 1) ^ 1, abort_flag))) break;
+        load_block<D, FP8>(a, p, jj, page_now, lane, &a.tm_v,
+                           smem + (FP8 ? C::kOffC + sv * C::kCodeBytes : C::kOffV + sv * C::kTileBytes),
+                           FP8 ? &bars.c_full[sv] : &bars.v_full[sv]);
+        nv = g + 1;
+        if (j == 0) load_q();  // after the first block, whose slots are free earlier
       }
     }
     if (lane == 0) static_cast<Parts*>(a.parts)[blockIdx.x] = parts;
@@ -190,31 +183,24 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     if (nq > 0 && !FP8) mbar_wait_drain(&bars.q_full[(nq - 1) & 1], ((nq - 1) >> 1) & 1);
     for (int x = max(0, nk - C::kKStages); x < nk; ++x)
       mbar_wait_drain(&bars.k_full[x % C::kKStages], (x / C::kKStages) & 1);
-    for (int x = max(0, nv - C::kVStages); x < nv; ++x)
-      mbar_wait_drain(&bars.v_full[x % C::kVStages], (x / C::kVStages) & 1);
-    if constexpr (FP8)
-      for (int x = max(0, nc - C::kCStages); x < nc; ++x)
-        mbar_wait_drain(&bars.c_full[x % C::kCStages], (x / C::kCStages) & 1);
+    constexpr int kS = FP8 ? C::kCStages : C::kVStages;
+    for (int x = max(0, nv - kS); x < nv; ++x)
+      mbar_wait_drain(FP8 ? &bars.c_full[x % kS] : &bars.v_full[x % kS], (x / kS) & 1);
   } else if (warp == C::kWarpMma) {
     // ------------------------------------------------------------ MMA issuer
     // S of block g + 1 while the softmax works on block g, then P V of block g;
     // at a tile's end P V first, since the next tile's Q is still on its way.
-    // Q, K both K-major; P from TMEM, V MN-major
-    constexpr uint32_t kIdS = FP8 ? idesc_f16(128, 128, false, false) : idesc_bf16(128, 128, false, false);
+    // P from TMEM, V MN-major
     constexpr uint32_t kIdO = FP8 ? idesc_f16(128, D, false, true) : idesc_bf16(128, D, false, true);
     const uint64_t dq0 = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
-    const uint64_t dk0 = Tile<D>::desc_k(smem + C::kOffK), dv0 = Tile<D>::desc_v(smem + C::kOffV);
+    const uint64_t dk0 = desc_keys<D, FP8>(smem + C::kOffK), dv0 = Tile<D>::desc_v(smem + C::kOffV);
     auto make_s = [&](int g, bool last) -> bool {
       const int ks = g % C::kKStages, b = g & 1;
       if (!warp_wait2(&bars.k_full[ks], (g / C::kKStages) & 1, &bars.s_free[b], ((g >> 1) & 1) ^ 1, abort_flag))
         return false;
       tc_fence_after();
       if (elect_one()) {
-        const uint32_t ko = (uint32_t)(ks * C::kTileBytes) >> 4;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss(tmem + C::kColS + b * 128, dq0 + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4),
-                 dk0 + ko + Tile<D>::step_k(kk), kIdS, kk > 0);
+        issue_qk<D, FP8>(tmem + C::kColS + b * 128, dq0, dk0 + ((uint32_t)(ks * C::kKBytes) >> 4));
         mma_commit(&bars.s_full[b]);
         mma_commit(&bars.k_empty[ks]);
         if (last) mma_commit(&bars.q_free);
@@ -257,29 +243,27 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     mbar_wait_drain(&bars.teardown, 0);
   } else if (FP8 && warp >= C::kWarpConv) {
     // ------------------------------------------------------------ converters
-    // (four warps for the keys and Q, four for the values)
-    const bool values = warp >= C::kWarpConv + 4;
-    const int tid = (threadIdx.x - C::kWarpConv * 32) & 127;
+    const int tid = threadIdx.x - C::kWarpConv * 32;
     constexpr int kCS = FP8 ? C::kCStages : 1;
     int g = 0, n = 0;
     bool ok = true;
     while (ok && walk.step(a, p)) {
-      for (int j = p.jb; ok && j < p.je; ++j, ++g) {
-        const int st = values ? g % C::kVStages : g % C::kKStages, use = values ? g / C::kVStages : g / C::kKStages;
-        const int x = 2 * g + (values ? 1 : 0), cs = x % kCS;
-        ok = warp_wait2(&bars.c_full[cs], (x / kCS) & 1, values ? &bars.v_empty[st] : &bars.k_empty[st], (use & 1) ^ 1,
-                        abort_flag);
-        if (!ok) break;
-        convert_tile<D>(smem + C::kOffC + cs * C::kCodeBytes, smem + (values ? C::kOffV : C::kOffK) + st * C::kTileBytes,
-                        p.q.len - j * 128, tid);
-        conv_arrive(values ? &bars.v_full[st] : &bars.k_full[st], &bars.c_empty[cs], lane);
-        if (!values && j == p.jb) {  // Q, in the order in which it was loaded
+      if (p.je > p.jb) {
+        if (tid < 128) {  // Q, by four of the warps
           if (!(ok = warp_wait(&bars.q_raw, n & 1, abort_flag))) break;
           convert_q<D, true>(smem + C::kOffQ, bars.q_ex[n & 1], 1, tid);
           conv_arrive(&bars.q_full[n & 1], nullptr, lane);
         }
+        ++n;
       }
-      if (p.je > p.jb) ++n;
+      for (int j = p.jb; j < p.je; ++j, ++g) {
+        const int vs = g % C::kVStages, cs = g % kCS;
+        ok = warp_wait2(&bars.c_full[cs], (g / kCS) & 1, &bars.v_empty[vs], ((g / C::kVStages) & 1) ^ 1, abort_flag);
+        if (!ok) break;
+        convert_tile<D, 32 * C::kConvWarps>(smem + C::kOffC + cs * C::kCodeBytes, smem + C::kOffV + vs * C::kTileBytes,
+                                            p.q.len - j * 128, tid);
+        conv_arrive(&bars.v_full[vs], &bars.c_empty[cs], lane);
+      }
     }
   } else {
     // ------------------------------------------------------------ softmax + epilogue
@@ -304,7 +288,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
       float sl2 = a.scale_log2;
       if (FP8 && nb > 0) {  // (their place is written again two tiles on, after the products of this one's P)
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars.q_full[n & 1], (n >> 1) & 1, abort_flag)))) sl2 = 0.f;
-        sl2 *= __uint_as_float((uint32_t)bars.q_ex[n & 1][lane] << 23);
+        sl2 *= unscale(bars.q_ex[n & 1][lane]);
         ++n;
       }
       const int off = p.q.len - p.q.n;  // causal: token i sees keys 0 .. i + off

@@ -151,17 +151,17 @@ cudaError_t launch_paged(PagedArgs a, const PagedPlan& p, cudaStream_t stream) {
     if (a.fp8) {
       const unsigned long long dims[3] = {d, ps, heads}, strides[2] = {d, ps * d};
       const unsigned box[3] = {(unsigned)d, per, 1u};
-      ok = ok && encode_map(m, base, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, dims, strides, box, false);
+      ok = ok && encode_map(m, base, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, dims, strides, box, i ? 0 : a.d);
     } else {
       const unsigned long long dims[5] = {64, 8, d / 64, ps / 8, heads}, strides[4] = {d * 2, 128, d * 16, ps * d * 2};
       const unsigned box[5] = {64u, 8u, (unsigned)d / 64u, per / 8u, 1u};
-      ok = ok && encode_map(m, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, dims, strides, box, true);
+      ok = ok && encode_map(m, base, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, dims, strides, box, 128);
     }
   }
   const unsigned long long q_dims[3] = {d, (unsigned long long)a.Hq, (unsigned long long)a.T};
   const unsigned long long q_strides[2] = {d * 2, (unsigned long long)a.q_stride * 2};
   const unsigned q_box[3] = {64u, (unsigned)(a.Hq / a.Hkv), (unsigned)p.tpt1};
-  ok = ok && encode_map(&a.tm_q, a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q_dims, q_strides, q_box, true);
+  ok = ok && encode_map(&a.tm_q, a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q_dims, q_strides, q_box, 128);
   if (!ok) return cudaErrorInvalidValue;
   a.tpt = p.tpt;
   a.tpt1 = p.tpt1;

@@ -79,15 +79,20 @@ __device__ __forceinline__ void zero_rows_from(uint8_t* tile, int row, int lane)
 }
 
 // ---------------------------------------------------------------- E4M3 caches
-// Both products take f16 operands there: every code is an f16 value, so one
-// conversion instruction makes two operands. (bf16 has no such instruction: by
-// integer steps on the bits, the converters took 3.5 us a block of the
-// decoding kernel, 595 us for 48 requests of up to 16384 keys, d = 128.) Q goes
-// from bf16 to f16 with each row scaled by the power of two that brings its
-// largest magnitude into [1, 2), undone in the row's softmax scale; what that
-// loses are elements below 2^-24 of the row's largest. P keeps 11 bits instead
-// of 8, times 2^kPBias so that weights down to 2^-32 do not vanish (P stays
-// below 2^(kRescaleThreshold + kPBias) = 2^15).
+// Keys stay codes: S = Q K^T on 8-bit operands (kind::f8f6f4), with Q as two of
+// them, hi + lo. A bf16 value has 8 significant bits; hi = RN_e4m3(q) takes
+// four, and q - hi needs no more than the other four, so hi + lo = q exactly
+// unless lo falls below E4M3's smallest step. Each row of Q is first scaled by the
+// power of two that brings its largest magnitude into [128, 256) (undone in
+// the row's softmax scale), so what is lost stays below 2^-17 of that
+// magnitude. Two 8-bit products take as long as one 16-bit product.
+// Values become f16 operands, one conversion instruction for two of them, by
+// warps between the copy and the product; P enters that product as f16: 11 bits, times
+// 2^kPBias so that weights down to 2^-32 do not vanish (P stays below
+// 2^(kRescaleThreshold + kPBias) = 2^15). In two E4M3 parts P would lose every
+// weight below 2^-10.
+// Measured, decoding 48 requests of up to 16384 keys at d = 128: both caches to
+// bf16 by integer steps on the bits 595 us, both to f16 211 us.
 constexpr float kPBias = 7.0f;
 
 // Two codes (the low 16 bits) to f16, exactly, NaN among them.
@@ -97,24 +102,25 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t c) {
   return r;
 }
 
-// A 128 x D tile of codes (rows of D bytes) to an f16 tile, by the 128 threads
-// of the converters; rows from 'rows' on become zero. A thread takes 16 codes,
-// two chunks; threads of odd panels store theirs in the other order, so that
-// the eight threads of a quarter warp write to different banks.
-template <int D>
+// A 128 x D tile of value codes (rows of D bytes) to an f16 tile, by NT threads;
+// rows from 'rows' on become zero. A thread takes 16 codes, two chunks; threads
+// of odd panels store theirs in the other order, so that the eight threads of
+// a quarter warp write to different banks.
+template <int D, int NT>
 __device__ __forceinline__ void convert_tile(const uint8_t* src, uint8_t* dst, int rows, int tid) {
-  constexpr int kPairs = D / 16;
-  const uint32_t base = smem_u32(dst);
+  constexpr int kPairs = D / 16, kRows = NT / kPairs;  // threads per row, rows per step
+  static_assert(kRows % 8 == 0, "a step must keep the swizzle");
   const int c = tid % kPairs, r0 = tid / kPairs;
   const bool odd = (c >> 2) & 1;
+  const uint32_t base = smem_u32(dst);
   const uint32_t first = base + Tile<D>::chunk(r0, 2 * c + (odd ? 1 : 0));
   const uint32_t second = base + Tile<D>::chunk(r0, 2 * c + (odd ? 0 : 1));
 #pragma unroll
-  for (int it = 0; it < kPairs; ++it) {  // row r0 + it * 128 / kPairs: a multiple of 8 rows on, the same swizzle
-    const uint4 w = *reinterpret_cast<const uint4*>(src + (it * 128 + tid) * 16);
+  for (int it = 0; it < 128 / kRows; ++it) {
+    const uint4 w = *reinterpret_cast<const uint4*>(src + (it * NT + tid) * 16);
     uint32_t x[4] = {odd ? w.z : w.x, odd ? w.w : w.y, odd ? w.x : w.z, odd ? w.y : w.w};
-    if (rows < 128 && r0 + it * (128 / kPairs) >= rows) x[0] = x[1] = x[2] = x[3] = 0u;  // code 0 is zero
-    constexpr uint32_t kStep = 16 / kPairs * Tile<D>::kGroup;
+    if (rows < 128 && r0 + it * kRows >= rows) x[0] = x[1] = x[2] = x[3] = 0u;  // code 0 is zero
+    constexpr uint32_t kStep = kRows / 8 * Tile<D>::kGroup;
     st_shared_v4(first + it * kStep, e4m3x2_to_f16(x[0]), e4m3x2_to_f16(x[0] >> 16), e4m3x2_to_f16(x[1]),
                  e4m3x2_to_f16(x[1] >> 16));
     st_shared_v4(second + it * kStep, e4m3x2_to_f16(x[2]), e4m3x2_to_f16(x[2] >> 16), e4m3x2_to_f16(x[3]),
@@ -122,48 +128,106 @@ __device__ __forceinline__ void convert_tile(const uint8_t* src, uint8_t* dst, i
   }
 }
 
-// Q rows in a [panel][128 rows][128 bytes] swizzled tile from bf16 to scaled f16
-// in place, by the converters' 128 threads, four per row: rows [0, 32 * groups),
-// and with COPIES rows 0 - 31 also to the other three row quarters. ex[row] gets
-// the biased exponent of the power of two that the softmax has to put back.
+// hi and lo codes of two values (the low and high half of each result).
+__device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
+  uint32_t h, back;
+  asm("{\n .reg .b16 c;\n cvt.rn.satfinite.e4m3x2.f32 c, %3, %2;\n cvt.rn.f16x2.e4m3x2 %1, c;\n mov.b32 %0, {c, c};\n}\n"
+      : "=r"(h), "=r"(back)
+      : "f"(x), "f"(y));
+  float bx, by;
+  asm("{\n .reg .b16 p, q;\n mov.b32 {p, q}, %2;\n cvt.f32.f16 %0, p;\n cvt.f32.f16 %1, q;\n}\n"
+      : "=f"(bx), "=f"(by)
+      : "r"(back));
+  hi = h & 0xFFFFu;
+  asm("{\n .reg .b16 c;\n cvt.rn.satfinite.e4m3x2.f32 c, %2, %1;\n mov.b32 %0, {c, c};\n}\n"
+      : "=r"(lo)
+      : "f"(x - bx), "f"(y - by));
+  lo &= 0xFFFFu;
+}
+
+// Q rows in a [panel][128 rows][128 bytes] swizzled tile from 64 bf16 to 64 hi
+// and 64 lo codes per 128-byte row, in place, by 128 threads, four neighbours
+// per row: rows [0, 32 * groups), and with COPIES rows 0 - 31 also to the other
+// three row quarters. ex[row] gets the biased exponent e of the row's largest
+// magnitude: the row was scaled by 2^(134 - e).
 template <int D, bool COPIES>
 __device__ __forceinline__ void convert_q(uint8_t* q, uint8_t* ex, int groups, int tid) {
-  constexpr int kChunks = D / 8 / 4;  // 16-byte chunks per thread
+  constexpr int kPanels = D / 64;
+  const int part = tid & 3;
+  const uint32_t base = smem_u32(q);
   for (int g = 0; g < groups; ++g) {
-    const int row = g * 32 + (tid >> 2), part = tid & 3;
-    uint4 x[kChunks];
-    uint32_t at[kChunks], big = 0;
+    const int row = g * 32 + (tid >> 2);
+    auto at = [&](int pn, int c) { return (uint32_t)(pn * 16384 + row * 128 + ((c ^ (row & 7)) << 4)); };
+    uint32_t w[kPanels][8], big = 0;  // chunks 2 part and 2 part + 1 of each panel
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      const int c = part * kChunks + i;
-      at[i] = (uint32_t)((c >> 3) * 16384 + row * 128 + (((c & 7) ^ (row & 7)) << 4));
-      x[i] = *reinterpret_cast<const uint4*>(q + at[i]);
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+    for (int pn = 0; pn < kPanels; ++pn) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) big = max(big, max(w[k] & 0x7FFFu, (w[k] >> 16) & 0x7FFFu));
+      for (int i = 0; i < 2; ++i) {
+        const uint4 x = *reinterpret_cast<const uint4*>(q + at(pn, 2 * part + i));
+        w[pn][4 * i] = x.x;
+        w[pn][4 * i + 1] = x.y;
+        w[pn][4 * i + 2] = x.z;
+        w[pn][4 * i + 3] = x.w;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) big = max(big, max(w[pn][k] & 0x7FFFu, (w[pn][k] >> 16) & 0x7FFFu));
     }
-    big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+    big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));  // (all four have read the row now)
     big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-    const uint32_t e = min(max(big >> 7, 1u), 253u);  // exponent of the row's largest magnitude
-    const float f = __uint_as_float((254u - e) << 23);
+    const uint32_t e = min(max(big >> 7, 8u), 253u);
+    const float f = __uint_as_float((261u - e) << 23);
     if (part == 0) ex[row] = (uint8_t)e;
-    const uint32_t base = smem_u32(q);
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-      uint32_t o[4];
+    for (int pn = 0; pn < kPanels; ++pn) {
+      uint32_t hi[4], lo[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        o[k] = pack_f16x2(__uint_as_float(w[k] << 16) * f, __uint_as_float(w[k] & 0xffff0000u) * f);
+      for (int k = 0; k < 4; ++k) {
+        uint32_t h0, l0, h1, l1;
+        split2(__uint_as_float(w[pn][2 * k] << 16) * f, __uint_as_float(w[pn][2 * k] & 0xffff0000u) * f, h0, l0);
+        split2(__uint_as_float(w[pn][2 * k + 1] << 16) * f, __uint_as_float(w[pn][2 * k + 1] & 0xffff0000u) * f, h1, l1);
+        hi[k] = h0 | (h1 << 16);
+        lo[k] = l0 | (l1 << 16);
+      }
 #pragma unroll
-      for (int n = 0; n < (COPIES ? 4 : 1); ++n) st_shared_v4(base + at[i] + n * 4096, o[0], o[1], o[2], o[3]);
+      for (int n = 0; n < (COPIES ? 4 : 1); ++n) {
+        st_shared_v4(base + at(pn, part) + n * 4096, hi[0], hi[1], hi[2], hi[3]);
+        st_shared_v4(base + at(pn, 4 + part) + n * 4096, lo[0], lo[1], lo[2], lo[3]);
+      }
     }
+  }
+}
+// What the softmax multiplies its scale by for a row whose exponent is e.
+__device__ __forceinline__ float unscale(uint32_t e) { return __uint_as_float((e - 7u) << 23); }
+
+// S = Q K^T of one 128 x 128 block by the elected lane: Q and K both K-major, at
+// bf16 from the panels' 32-byte k-steps; with E4M3 caches hi and lo codes of Q
+// (64 bytes each of a panel's rows) against the same key columns.
+template <int D, bool FP8>
+__device__ __forceinline__ uint64_t desc_keys(const uint8_t* p) {
+  if constexpr (!FP8) return Tile<D>::desc_k(p);
+  if constexpr (D == 128) return sdesc_sw128(smem_u32(p), 16, 1024);
+  return sdesc_sw64(smem_u32(p), 16, 512);
+}
+template <int D, bool FP8>
+__device__ __forceinline__ void issue_qk(uint32_t d_s, uint64_t dq, uint64_t dk) {
+  if constexpr (FP8) {
+    constexpr uint32_t kId = idesc_e4m3(128, 128, false, false);
+#pragma unroll
+    for (int pn = 0; pn < D / 64; ++pn)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)  // hi, hi, lo, lo
+        mma_ss_f8(d_s, dq + ((pn * 16384 + i * 32) >> 4), dk + ((pn * 64 + (i & 1) * 32) >> 4), kId,
+                  pn > 0 || i > 0);
+  } else {
+    constexpr uint32_t kId = idesc_bf16(128, 128, false, false);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+      mma_ss(d_s, dq + (((kk >> 2) * 16384 + (kk & 3) * 32) >> 4), dk + Tile<D>::step_k(kk), kId, kk > 0);
   }
 }
 
 // The converters' hand-over of shared memory that they wrote to the products:
-// one arrival per warp (barriers count kConvArrivals).
-constexpr uint32_t kConvArrivals = 4;
+// one arrival per warp.
 __device__ __forceinline__ void conv_arrive(uint64_t* full, uint64_t* empty, int lane) {
   fence_proxy_async_smem();
   __syncwarp();
