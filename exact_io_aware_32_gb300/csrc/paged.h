@@ -65,7 +65,7 @@ struct PagedPlan {
 };
 
 cudaError_t launch_plan(const PlanArgs& a, int num_sms, cudaStream_t stream);
-cudaError_t launch_store(const StoreArgs& a, cudaStream_t stream);
+cudaError_t launch_store(const StoreArgs& a, int num_sms, cudaStream_t stream);
 PagedPlan plan_paged(int Hq, int Hkv, int d, int fp8, int max_new, int num_sms);
 // Encodes the tensor maps too; cudaErrorInvalidValue if that fails.
 cudaError_t launch_paged(PagedArgs a, const PagedPlan& p, cudaStream_t stream);

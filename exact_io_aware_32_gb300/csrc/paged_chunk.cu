@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
       withhold = false;
     };
     while (ok && walk.step(a, p)) {
-      note_piece(parts, p);
+      note_piece(parts, p, walk, bars.range.per);
       int nb[2];
       half_blocks<C::kTiles>(a, p, nb);
       const int nbm = max(nb[0], nb[1]);

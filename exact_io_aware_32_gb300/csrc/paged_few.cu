@@ -13,12 +13,14 @@
 // through shared memory when the tile ends. The products cost what they cost
 // with 32 rows, since tcgen05 takes 128 anyway.
 //
-// TMEM: S twice (S of the next block is made while the softmax works on this
-// one), P in columns of its own, O. Persistent CTAs over ranges of the row of
-// tiles (paged_work.cuh), rings and barriers counting on across tiles.
+// TMEM: S twice and P twice (S of the next block is made while the softmax works
+// on this one, P of the next is written while this one's product runs), O.
+// Persistent CTAs over ranges of the row of tiles (paged_work.cuh), rings and
+// barriers counting on across tiles.
 //
-// Warp roles: 0-3 softmax and epilogue, 4 TMA, 5 MMA, and with E4M3 caches eight
-// converter warps (value codes to f16, Q to its two parts).
+// Warp roles: 0-3 softmax and epilogue; 4 copies keys and Q, 5 values; 6 issues
+// P V and owns TMEM, 7 issues Q K^T; with E4M3 caches eight converter warps
+// (value codes to f16, Q to its two parts).
 #include "paged_pipe.cuh"
 
 namespace fa {
@@ -41,28 +43,28 @@ struct FCfg {
   static constexpr int kOffK = kOffQ + kTileBytes;
   static constexpr int kOffV = kOffK + kKStages * kKBytes;
   static constexpr int kOffC = kOffV + kVStages * kTileBytes;
-  static constexpr int kOffJoin = kOffC + kCStages * kCodeBytes;  // 4 quarters x 32 columns x 33 floats
-  static constexpr int kOffBar = kOffJoin + 4 * 32 * 33 * 4 + 4 * 32 * 8;
-  static constexpr int kSmemBytes = kOffBar + 480 + 1024;  // barriers, alignment slack
+  // the quarters' O of kJoinRows rows at a time, rows padded by 16 bytes against bank conflicts; (m, l) of all rows
+  static constexpr int kJoinRows = D == 64 ? 16 : 8, kJoinStride = D + 4;
+  static constexpr int kOffJoin = kOffC + kCStages * kCodeBytes;
+  static constexpr int kOffBar = kOffJoin + 4 * kJoinRows * kJoinStride * 4 + 4 * 32 * 8;
+  static constexpr int kSmemBytes = kOffBar + 512 + 1024;  // barriers, alignment slack
   static_assert(kSmemBytes <= 232448, "shared memory");
-  static constexpr uint32_t kColS = 0, kColP = 256, kColO = 320, kTmemCols = 512;
-  static constexpr int kWarpTma = 4, kWarpMma = 5, kWarpConv = 6, kConvWarps = 8;
-  static constexpr int kThreads = 192 + (FP8_ ? 32 * kConvWarps : 0);
+  static constexpr uint32_t kColS = 0, kColP = 256, kColO = 384, kTmemCols = 512;  // S and P twice
+  static constexpr int kWarpTmaK = 4, kWarpTmaV = 5, kWarpPv = 6, kWarpQk = 7, kWarpConv = 8, kConvWarps = 8;
+  static constexpr int kThreads = 256 + (FP8_ ? 32 * kConvWarps : 0);
 };
 
 struct FBars {
-  // q_full of tile n is q_full[n & 1]: with E4M3 caches the softmax waits for it too, maybe only after the next tile's
-  // Q is there, and one barrier would then have gone through both parities
-  uint64_t q_raw, q_full[2], q_free;  // E4M3 caches: Q as loaded, as converted
+  // q_full of tile n is q_full[n % 3]: with E4M3 caches the softmax waits for it too, and reads the exponents, maybe only
+  // after the next two tiles' Q are there (S runs two blocks ahead of it, and a tile may be one block)
+  uint64_t q_raw, q_full[3], q_free;  // E4M3 caches: Q as loaded, as converted
   uint64_t k_full[6], k_empty[6], v_full[4], v_empty[4], c_full[6], c_empty[6];
-  uint64_t s_full[2], s_free[2], p_full, pv_done, o_free;
-  uint64_t teardown;
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], o_free;
+  uint64_t teardown[2];
   uint32_t tmem_base;
   int abort;
-  Range range;
-  uint8_t q_ex[2][32];  // E4M3 caches: the exponents of Q's row scales, of this tile and the one before
 };
-static_assert(sizeof(FBars) <= 480, "barriers exceed their shared memory");
+static_assert(sizeof(FBars) <= 400, "barriers exceed their shared memory");
 
 template <int D, bool FP8, bool CAUSAL>
 __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel(const __grid_constant__ PagedArgs a) {
@@ -71,21 +73,25 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   FBars& bars = *reinterpret_cast<FBars*>(smem + C::kOffBar);
   volatile int* abort_flag = &bars.abort;
+  // in the join's place, which is not in use yet: the range and its sums; behind the barriers: the exponents of Q's row
+  // scales (E4M3 caches), of this tile and the two before
+  Range& range = *reinterpret_cast<Range*>(smem + C::kOffJoin);
+  auto& sums = *reinterpret_cast<long long(*)[2][C::kThreads / 32]>(smem + C::kOffJoin + 256);
+  auto& q_ex = *reinterpret_cast<uint8_t(*)[3][32]>(smem + C::kOffBar + 400);
+  static_assert(sizeof(Range) <= 256, "the sums follow the range");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.Hq / a.Hkv;
 
-  // (the sums' place is the join's, not yet in use)
-  find_range<C::kThreads>(a, bars.range,
-                          reinterpret_cast<long long(&)[2][C::kThreads / 32]>(smem[C::kOffJoin]));
-  if (!bars.range.some) {  // uniform: every thread leaves before any barrier
-    if (threadIdx.x == 0) static_cast<Parts*>(a.parts)[blockIdx.x] = Parts{};
-    return;
+  // Everything that does not depend on the lengths first; the range's barriers cover it.
+  if (warp == C::kWarpTmaK && elect_one()) {
+    tma_prefetch_desc(&a.tm_q);
+    tma_prefetch_desc(&a.tm_k);
+    tma_prefetch_desc(&a.tm_v);
   }
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 32) {
     bars.abort = 0;
     mbar_init(&bars.q_raw, 1);
-    mbar_init(&bars.q_full[0], FP8 ? 4 : 1);
-    mbar_init(&bars.q_full[1], FP8 ? 4 : 1);
+    for (int s = 0; s < 3; ++s) mbar_init(&bars.q_full[s], FP8 ? 4 : 1);
     mbar_init(&bars.q_free, 1);
     for (int s = 0; s < 6; ++s) {
       mbar_init(&bars.k_full[s], 1);
@@ -100,128 +106,141 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars.s_full[s], 1);
       mbar_init(&bars.s_free[s], 128);
+      mbar_init(&bars.p_full[s], 128);
+      mbar_init(&bars.pv_done[s], 1);
+      mbar_init(&bars.teardown[s], 1);
     }
-    mbar_init(&bars.p_full, 128);
-    mbar_init(&bars.pv_done, 1);
     mbar_init(&bars.o_free, 128);
-    mbar_init(&bars.teardown, 1);
     fence_mbar_init();
   }
   // rows of Q that no copy fills (G that does not divide 32, short tiles) are zeros, not leftovers
   for (int i = threadIdx.x; i < C::kTileBytes / 16; i += C::kThreads)
     st_shared_v4(smem_u32(smem + C::kOffQ) + i * 16, 0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
-  if (warp == C::kWarpMma) {
+  if (warp == C::kWarpPv) {
     tmem_alloc(&bars.tmem_base, C::kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  find_range<C::kThreads>(a, range, sums);
   tc_fence_after();
   const uint32_t tmem = bars.tmem_base;
+  if (!range.some) {  // uniform: nothing has been issued
+    if (warp == C::kWarpPv) tmem_dealloc(tmem, C::kTmemCols);
+    if (threadIdx.x == 0) static_cast<Parts*>(a.parts)[blockIdx.x] = Parts{};
+    return;
+  }
   Walk walk;
-  walk.begin(a, bars.range);
+  walk.begin(a, range);
+  const long long per = range.per;
   Piece p;
-
-  if (warp == C::kWarpTma) {
-    // ------------------------------------------------------------ TMA producer
-    if (elect_one()) {
-      tma_prefetch_desc(&a.tm_q);
-      tma_prefetch_desc(&a.tm_k);
-      tma_prefetch_desc(&a.tm_v);
-    }
-    __syncwarp();
+  __syncthreads();  // all have read the range: the join may write there
+  if (warp == C::kWarpTmaK) {
+    // ------------------------------------------------------------ keys and Q
     // E4M3 caches: one copy of Q, which the converters make four of
     constexpr int kCopies = FP8 ? 1 : 4;
     const uint32_t q_bytes = (uint32_t)(kCopies * G * a.tpt * D * 2);
     Parts parts{};
-    int g = 0, nk = 0, nv = 0, nq = 0;  // key blocks, and loads issued
+    int g = 0, nk = 0, nq = 0;  // key blocks, and loads issued
     bool ok = true;
-    bool withhold = a.test_fault == 1;  // test hook: the MMA warp's first wait expires
+    bool withhold = a.test_fault == 1;  // test hook: the MMA warps' first wait expires
     while (ok && walk.step(a, p)) {
-      note_piece(parts, p);
+      note_piece(parts, p, walk, per);
       const int nb = p.je - p.jb;
       if (nb == 0) continue;
-      // Q of the tile, once its slot's last reader is done
-      auto load_q = [&]() {
-        if (!(ok = warp_wait(&bars.q_free, (nq & 1) ^ 1, abort_flag))) return;
+      int page = lane_page(a, p, p.jb, lane);
+      for (int j = 0; j < nb; ++j, ++g) {
+        const int jj = p.jb + j, page_now = page;
+        if (j + 1 < nb) page = lane_page(a, p, jj + 1, lane);
+        const int s = g % C::kKStages;
+        if (!(ok = warp_wait(&bars.k_empty[s], ((g / C::kKStages) & 1) ^ 1, abort_flag))) break;
+        load_block<D, FP8>(a, p, jj, page_now, lane, &a.tm_k, smem + C::kOffK + s * C::kKBytes, &bars.k_full[s]);
+        nk = g + 1;
+        if (j > 0) continue;
+        // Q after the first block's keys, whose slot is free earlier
+        if (!(ok = warp_wait(&bars.q_free, (nq & 1) ^ 1, abort_flag))) break;
         if (!withhold) {
-          uint64_t* q_bar = FP8 ? &bars.q_raw : &bars.q_full[nq & 1];
+          uint64_t* bar = FP8 ? &bars.q_raw : &bars.q_full[nq % 3];
           if (elect_one()) {
-            mbar_arrive_expect_tx(q_bar, q_bytes);
+            mbar_arrive_expect_tx(bar, q_bytes);
             for (int w = 0; w < kCopies; ++w)
               for (int pn = 0; pn < C::kPanels; ++pn)
-                tma_load_3d(smem + C::kOffQ + pn * 16384 + w * 4096, &a.tm_q, q_bar, pn * 64, p.h * G,
-                            p.q.start + p.tok);
+                tma_load_3d(smem + C::kOffQ + pn * 16384 + w * 4096, &a.tm_q, bar, pn * 64, p.h * G, p.q.start + p.tok);
           }
           __syncwarp();
           ++nq;
         }
         withhold = false;
-      };
-      int page = lane_page(a, p, p.jb, lane);
-      for (int j = 0; ok && j < nb; ++j, ++g) {
-        const int jj = p.jb + j, page_now = page;
-        if (j + 1 < nb) page = lane_page(a, p, jj + 1, lane);
-        const int sk = g % C::kKStages;
-        if (!(ok = warp_wait(&bars.k_empty[sk], ((g / C::kKStages) & 1) ^ 1, abort_flag))) break;
-        load_block<D, FP8>(a, p, jj, page_now, lane, &a.tm_k, smem + C::kOffK + sk * C::kKBytes, &bars.k_full[sk]);
-        nk = g + 1;
-        constexpr int kS = FP8 ? C::kCStages : C::kVStages;
-        const int sv = g % kS;
-        if (!(ok = warp_wait(FP8 ? &bars.c_empty[sv] : &bars.v_empty[sv], ((g / kS) & 1) ^ 1, abort_flag))) break;
-        load_block<D, FP8>(a, p, jj, page_now, lane, &a.tm_v,
-                           smem + (FP8 ? C::kOffC + sv * C::kCodeBytes : C::kOffV + sv * C::kTileBytes),
-                           FP8 ? &bars.c_full[sv] : &bars.v_full[sv]);
-        nv = g + 1;
-        if (j == 0) load_q();  // after the first block, whose slots are free earlier
       }
     }
     if (lane == 0) static_cast<Parts*>(a.parts)[blockIdx.x] = parts;
     // Let every issued copy land before the CTA can exit.
     if (nq > 0 && FP8) mbar_wait_drain(&bars.q_raw, (nq - 1) & 1);
-    if (nq > 0 && !FP8) mbar_wait_drain(&bars.q_full[(nq - 1) & 1], ((nq - 1) >> 1) & 1);
+    if (nq > 0 && !FP8) mbar_wait_drain(&bars.q_full[(nq - 1) % 3], ((nq - 1) / 3) & 1);
     for (int x = max(0, nk - C::kKStages); x < nk; ++x)
       mbar_wait_drain(&bars.k_full[x % C::kKStages], (x / C::kKStages) & 1);
+  } else if (warp == C::kWarpTmaV) {
+    // ------------------------------------------------------------ values
+    // (a warp of their own: a copy holds its warp for about 150 cycles, and with pages of 16 tokens a block has 16)
     constexpr int kS = FP8 ? C::kCStages : C::kVStages;
-    for (int x = max(0, nv - kS); x < nv; ++x)
-      mbar_wait_drain(FP8 ? &bars.c_full[x % kS] : &bars.v_full[x % kS], (x / kS) & 1);
-  } else if (warp == C::kWarpMma) {
-    // ------------------------------------------------------------ MMA issuer
-    // S of block g + 1 while the softmax works on block g, then P V of block g;
-    // at a tile's end P V first, since the next tile's Q is still on its way.
-    // P from TMEM, V MN-major
-    constexpr uint32_t kIdO = FP8 ? idesc_f16(128, D, false, true) : idesc_bf16(128, D, false, true);
-    const uint64_t dq0 = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
-    const uint64_t dk0 = desc_keys<D, FP8>(smem + C::kOffK), dv0 = Tile<D>::desc_v(smem + C::kOffV);
-    auto make_s = [&](int g, bool last) -> bool {
-      const int ks = g % C::kKStages, b = g & 1;
-      if (!warp_wait2(&bars.k_full[ks], (g / C::kKStages) & 1, &bars.s_free[b], ((g >> 1) & 1) ^ 1, abort_flag))
-        return false;
-      tc_fence_after();
-      if (elect_one()) {
-        issue_qk<D, FP8>(tmem + C::kColS + b * 128, dq0, dk0 + ((uint32_t)(ks * C::kKBytes) >> 4));
-        mma_commit(&bars.s_full[b]);
-        mma_commit(&bars.k_empty[ks]);
-        if (last) mma_commit(&bars.q_free);
+    uint64_t *full = FP8 ? bars.c_full : bars.v_full, *empty = FP8 ? bars.c_empty : bars.v_empty;
+    int g = 0, nv = 0;
+    bool ok = true;
+    while (ok && walk.step(a, p)) {
+      if (p.jb == p.je) continue;
+      int page = lane_page(a, p, p.jb, lane);
+      for (int jj = p.jb; jj < p.je; ++jj, ++g) {
+        const int page_now = page, s = g % kS;
+        if (jj + 1 < p.je) page = lane_page(a, p, jj + 1, lane);
+        if (!(ok = warp_wait(&empty[s], ((g / kS) & 1) ^ 1, abort_flag))) break;
+        load_block<D, FP8>(a, p, jj, page_now, lane, &a.tm_v,
+                           smem + (FP8 ? C::kOffC + s * C::kCodeBytes : C::kOffV + s * C::kTileBytes), &full[s]);
+        nv = g + 1;
       }
-      __syncwarp();
-      return true;
-    };
+    }
+    for (int x = max(0, nv - kS); x < nv; ++x) mbar_wait_drain(&full[x % kS], (x / kS) & 1);
+  } else if (warp == C::kWarpQk) {
+    // ------------------------------------------------------------ S = Q K^T, up to two blocks ahead of the softmax
+    const uint64_t dq = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
+    const uint64_t dk = desc_keys<D, FP8>(smem + C::kOffK);
     int g = 0, n = 0;  // key blocks, tiles
     bool ok = true;
     while (ok && walk.step(a, p)) {
-      const int nb = p.je - p.jb;
-      if (nb == 0) continue;
-      ok = warp_wait(&bars.q_full[n & 1], (n >> 1) & 1, abort_flag) && make_s(g, nb == 1);
-      for (int j = 0; ok && j < nb; ++j, ++g) {
-        if (j + 1 < nb && !(ok = make_s(g + 1, j + 2 == nb))) break;
-        const int s = g % C::kVStages;
-        if (!(ok = warp_wait2(&bars.p_full, g & 1, &bars.v_full[s], (g / C::kVStages) & 1, abort_flag))) break;
+      if (p.jb == p.je) continue;
+      if (!(ok = warp_wait(&bars.q_full[n % 3], (n / 3) & 1, abort_flag))) break;
+      ++n;
+      for (int jj = p.jb; jj < p.je; ++jj, ++g) {
+        const int s = g % C::kKStages, b = g & 1;
+        ok = warp_wait2(&bars.k_full[s], (g / C::kKStages) & 1, &bars.s_free[b], ((g >> 1) & 1) ^ 1, abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          issue_qk<D, FP8>(tmem + C::kColS + b * 128, dq, dk + ((uint32_t)(s * C::kKBytes) >> 4));
+          mma_commit(&bars.s_full[b]);
+          mma_commit(&bars.k_empty[s]);
+          if (jj + 1 == p.je) mma_commit(&bars.q_free);  // the tile's last product to read Q
+        }
+        __syncwarp();
+      }
+    }
+    if (elect_one()) mma_commit(&bars.teardown[0]);
+    __syncwarp();
+    mbar_wait_drain(&bars.teardown[0], 0);
+  } else if (warp == C::kWarpPv) {
+    // ------------------------------------------------------------ O += P V
+    constexpr uint32_t kIdO = FP8 ? idesc_f16(128, D, false, true) : idesc_bf16(128, D, false, true);  // V MN-major
+    const uint64_t dv = Tile<D>::desc_v(smem + C::kOffV);
+    int g = 0, n = 0;  // key blocks, tiles
+    bool ok = true;
+    while (ok && walk.step(a, p)) {
+      if (p.jb == p.je) continue;
+      for (int jj = p.jb; jj < p.je; ++jj, ++g) {
+        const int s = g % C::kVStages, b = g & 1;
+        if (!(ok = warp_wait2(&bars.v_full[s], (g / C::kVStages) & 1, &bars.p_full[b], (g >> 1) & 1, abort_flag))) break;
         // a tile's first P V overwrites O: the tile before has been read out
-        if (j == 0 && !(ok = warp_wait(&bars.o_free, (n & 1) ^ 1, abort_flag))) break;
+        if (jj == p.jb && !(ok = warp_wait(&bars.o_free, (n & 1) ^ 1, abort_flag))) break;
         if constexpr (!FP8) {
-          const int end = p.q.len - (p.jb + j) * 128;
+          const int end = p.q.len - jj * 128;
           if (end < 128) zero_rows_from<D>(smem + C::kOffV + s * C::kTileBytes, end, lane);
         }
         tc_fence_after();
@@ -229,18 +248,18 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
           const uint32_t vo = (uint32_t)(s * C::kTileBytes) >> 4;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_ts(tmem + C::kColO, tmem + C::kColP + kk * 8, dv0 + vo + Tile<D>::step_v(kk), kIdO,
-                   (j > 0 || kk > 0) ? 1u : 0u);
-          mma_commit(&bars.pv_done);
+            mma_ts(tmem + C::kColO, tmem + C::kColP + b * 64 + kk * 8, dv + vo + Tile<D>::step_v(kk), kIdO,
+                   (jj > p.jb || kk > 0) ? 1u : 0u);
+          mma_commit(&bars.pv_done[b]);
           mma_commit(&bars.v_empty[s]);
         }
         __syncwarp();
       }
       ++n;
     }
-    if (elect_one()) mma_commit(&bars.teardown);
+    if (elect_one()) mma_commit(&bars.teardown[1]);
     __syncwarp();
-    mbar_wait_drain(&bars.teardown, 0);
+    mbar_wait_drain(&bars.teardown[1], 0);
   } else if (FP8 && warp >= C::kWarpConv) {
     // ------------------------------------------------------------ converters
     const int tid = threadIdx.x - C::kWarpConv * 32;
@@ -251,8 +270,8 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
       if (p.je > p.jb) {
         if (tid < 128) {  // Q, by four of the warps
           if (!(ok = warp_wait(&bars.q_raw, n & 1, abort_flag))) break;
-          convert_q<D, true>(smem + C::kOffQ, bars.q_ex[n & 1], 1, tid);
-          conv_arrive(&bars.q_full[n & 1], nullptr, lane);
+          convert_q<D, true>(smem + C::kOffQ, q_ex[n % 3], 1, tid);
+          conv_arrive(&bars.q_full[n % 3], nullptr, lane);
         }
         ++n;
       }
@@ -274,11 +293,11 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     constexpr float kBias = FP8 ? kPBias : 0.f;
     const int rt = lane / G;  // this row's token within the tile
     float* join = reinterpret_cast<float*>(smem + C::kOffJoin);
-    float2* stats = reinterpret_cast<float2*>(join + 4 * 32 * 33);  // (m, l) of each quarter and row
+    float2* stats = reinterpret_cast<float2*>(join + 4 * C::kJoinRows * C::kJoinStride);  // (m, l) by quarter and row
     {
       const uint32_t zero[16] = {};
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_st16(t_p + c * 16, zero);  // P outside this warp's columns stays 0
+      for (int c = 0; c < 8; ++c) tmem_st16(t_p + c * 16, zero);  // both P outside this warp's columns stay 0
       tmem_st_wait();
     }
     int g = 0, n = 0;
@@ -286,9 +305,9 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     while (ok && walk.step(a, p)) {
       const int nb = p.je - p.jb;
       float sl2 = a.scale_log2;
-      if (FP8 && nb > 0) {  // (their place is written again two tiles on, after the products of this one's P)
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars.q_full[n & 1], (n >> 1) & 1, abort_flag)))) sl2 = 0.f;
-        sl2 *= unscale(bars.q_ex[n & 1][lane]);
+      if (FP8 && nb > 0) {  // (their place is written again three tiles on, after this warp has read the first S of this one)
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars.q_full[n % 3], (n / 3) & 1, abort_flag)))) sl2 = 0.f;
+        sl2 *= unscale(q_ex[n % 3][lane]);
         ++n;
       }
       const int off = p.q.len - p.q.n;  // causal: token i sees keys 0 .. i + off
@@ -339,13 +358,12 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
         }
         const float2 sum = fadd2(sum2[0], sum2[1]);
         l_sum = l_sum * alpha + (sum.x + sum.y);
-        // P and O are free once the P V before this one has completed
-        if (j > 0) {
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars.pv_done, (g - 1) & 1, abort_flag));
-          if (!ok) break;
-          tc_fence_after();
-        }
-        tmem_st16(t_p + 16 * warp, pk);
+        // this P's place is free once the P V two blocks back has completed; O may be rescaled once the last one has
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars.pv_done[b], ((g >> 1) & 1) ^ 1, abort_flag));
+        if (ok && rescale) ok = __all_sync(0xffffffffu, mbar_wait(&bars.pv_done[b ^ 1], ((g - 1) >> 1) & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        tmem_st16(t_p + b * 64 + 16 * warp, pk);
         if (rescale) {
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
@@ -359,10 +377,10 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&bars.p_full);
+        mbar_arrive(&bars.p_full[b]);
       }
       // ---- the tile's four quarters joined: o = sum_w 2^(m_w - m) O_w / sum_w 2^(m_w - m) l_w
-      if (ok && nb > 0) ok = mbar_wait(&bars.pv_done, (g - 1) & 1, abort_flag);
+      if (ok && nb > 0) ok = mbar_wait(&bars.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       stats[warp * 32 + lane] = make_float2(m_ref, l_sum);
       if (!named_bar_and(1, 128, ok)) {  // the four warps agree whether to go on
@@ -390,36 +408,50 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
           a.part_lse[part0 + lane] = lse2;
       }
       if (nb > 0) tc_fence_after();
+      for (int r0 = 0; r0 < rows; r0 += C::kJoinRows) {  // kJoinRows rows at a time
+        const int mine = lane - r0;
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t o[32];
-        if (nb > 0) {
-          tmem_ld32(t_o + c, o);
-          tmem_ld_wait(o);
-        }
-        if (nb > 0 && c + 32 == D) {
-          tc_fence_before();
-          mbar_arrive(&bars.o_free);  // O is in registers: the next tile may accumulate there
-        }
-        if (lane < rows)
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          if (nb > 0) {
+            tmem_ld32(t_o + c, o);
+            tmem_ld_wait(o);
+          }
+          if (mine >= 0 && mine < C::kJoinRows) {
+            const uint32_t dst = smem_u32(join + (warp * C::kJoinRows + mine) * C::kJoinStride + c);
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            join[(warp * 32 + i) * 33 + lane] = f > 0.f ? __uint_as_float(o[i]) * f : 0.f;
+            for (int i = 0; i < 32; i += 4) {
+              uint32_t x[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) x[k] = f > 0.f ? __float_as_uint(__uint_as_float(o[i + k]) * f) : 0u;
+              st_shared_v4(dst + i * 4, x[0], x[1], x[2], x[3]);
+            }
+          }
+        }
+        if (nb > 0 && r0 + C::kJoinRows >= rows) {
+          tc_fence_before();
+          mbar_arrive(&bars.o_free);  // O has been read: the next tile may accumulate there
+        }
         named_bar_sync(1, 128);
-        for (int i = threadIdx.x; i < rows * 16; i += 128) {  // pairs of columns
-          const int r = i >> 4, x = (i & 15) * 2;
-          float s0 = 0.f, s1 = 0.f;
+        const int count = min(C::kJoinRows, rows - r0);
+        for (int i = threadIdx.x; i < count * (D / 4); i += 128) {  // four columns each
+          const int rr = i / (D / 4), c = (i % (D / 4)) * 4, r = r0 + rr;
+          float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            s0 += join[(w * 32 + x) * 33 + r];
-            s1 += join[(w * 32 + x + 1) * 33 + r];
+            const float4 x = *reinterpret_cast<const float4*>(join + (w * C::kJoinRows + rr) * C::kJoinStride + c);
+            s.x += x.x;
+            s.y += x.y;
+            s.z += x.z;
+            s.w += x.w;
           }
           if (whole) {
             const int tk = r / G;
             const long long row = row0 + (long long)tk * a.Hq + (r - tk * G);
-            *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.o) + (row * D + c + x) * 2) = pack_bf16x2(s0, s1);
+            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.o) + (row * D + c) * 2) =
+                make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
           } else {
-            *reinterpret_cast<float2*>(a.part_o + (part0 + r) * D + c + x) = make_float2(s0, s1);
+            *reinterpret_cast<float4*>(a.part_o + (part0 + r) * D + c) = s;
           }
         }
         named_bar_sync(1, 128);
@@ -429,7 +461,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
 
   tc_fence_before();
   __syncthreads();
-  if (warp == C::kWarpMma) tmem_dealloc(tmem, C::kTmemCols);
+  if (warp == C::kWarpPv) tmem_dealloc(tmem, C::kTmemCols);
   if (threadIdx.x == 0 && bars.abort) atomicOr(a.status, 1u);
 }
 

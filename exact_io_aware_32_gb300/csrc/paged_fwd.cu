@@ -2,6 +2,7 @@
 // the kernel that joins tiles cut between CTAs.
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "fa_internal.h"
 #include "paged.h"
@@ -18,97 +19,95 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // Joins the parts of one cut tile: with m = max_z lse_z, o = sum_z 2^(lse_z - m) o_z
 // / sum_z 2^(lse_z - m). The CTA that opened the tile names it; the parts after
 // its own are the leading pieces of the CTAs that follow, in order, up to the one
-// that ends the tile: a fixed order, so the same bits every time. W warps per
-// row, each taking every W-th part with kAhead parts' loads in flight: a tile of
-// one long request can have a part on every SM.
-constexpr int kJoinWarps = 16;
+// that ends the tile: a fixed order, so the same bits every time. A block of
+// kJoinWarps warps takes kJoinWarps / W rows of a tile, W warps per row, each
+// every W-th part with kAhead parts' loads in flight. A part's O is read beside
+// its logsumexp, not after it: bound by latency, not by the few bytes.
+constexpr int kJoinWarps = 8;
 template <int D, int W>
 __global__ void __launch_bounds__(32 * kJoinWarps) fa_paged_join_kernel(const __grid_constant__ PagedArgs a,
                                                                         int rows_per_tile) {
-  constexpr int V = D / 32, kAhead = 4;
-  __shared__ float s_acc[kJoinWarps][D];
-  __shared__ float s_tot[kJoinWarps];
-  const Parts* parts = static_cast<const Parts*>(a.parts);
+  constexpr int V = D / 32, kAhead = W > 1 ? 8 : 4;
+  using Vec = typename std::conditional<V == 4, float4, float2>::type;
+  __shared__ float s_acc[W > 1 ? kJoinWarps : 1][D];
+  __shared__ float2 s_ml[W > 1 ? kJoinWarps : 1];
   const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % W;
-  const Parts mine = parts[c];
+  const Parts mine = static_cast<const Parts*>(a.parts)[c];
   if (!mine.open) return;
-  const int G = a.Hq / a.Hkv, row = (int)blockIdx.y * (kJoinWarps / W) + warp / W;
-  // row = half * 128 + token * G + head (halves of tpt1 tokens)
-  const int half = row >> 7, rr = row & 127, tk = rr / G;
+  const int G = a.Hq / a.Hkv, rows1 = a.tpt1 * G;
+  const int i = (int)blockIdx.y * (kJoinWarps / W) + warp / W;  // half * rows1 + token * G + head
+  const int half = i / rows1, rr = i - half * rows1, tk = rr / G, row = half * 128 + rr;
   const int tok = mine.tok + half * a.tpt1 + tk;
-  const bool valid = tk < a.tpt1 && tok < mine.n;
-  if (__syncthreads_or(valid) == 0) return;
-  // the CTA that ends the tile: the first after c whose leading piece says so
-  int end = -1;
-  for (int z0 = c + 1; z0 < (int)gridDim.x; z0 += 32) {
-    const int z = z0 + lane;
-    const bool ends = z < (int)gridDim.x && parts[z].lead && parts[z].lead_ends;
-    const unsigned b = __ballot_sync(0xffffffffu, ends);
-    if (b) {
-      end = z0 + __ffs((int)b) - 1;
-      break;
-    }
-  }
-  auto slot = [&](int z) { return ((long long)z * 2 + (z == c ? 1 : 0)) * rows_per_tile + row; };
-  float m = -INFINITY;
+  const bool valid = half * a.tpt1 < a.tpt && tok < mine.n;
+  float m = -INFINITY, tot = 0.f, acc[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) acc[k] = 0.f;
   if (valid)
-    for (int z = c + lane; z <= end; z += 32) m = fmaxf(m, a.part_lse[slot(z)]);
-#pragma unroll
-  for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
-  float acc[V], tot = 0.f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) acc[i] = 0.f;
-  if (m != -INFINITY)
-    for (int z0 = c + sub; z0 <= end; z0 += kAhead * W) {
-      float w[kAhead], x[kAhead][V];
+    for (int z0 = c + sub; z0 <= mine.end; z0 += kAhead * W) {
+      float l[kAhead];
+      Vec x[kAhead];
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
         const int z = z0 + u * W;
-        const float lz = z <= end ? a.part_lse[slot(z)] : -INFINITY;
-        w[u] = exp2f(lz - m);
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[u][i] = 0.f;
-        if (lz != -INFINITY) {  // else that part saw no key of this row and wrote no O
-          const float* oz = a.part_o + slot(z) * D + lane * V;
-#pragma unroll
-          for (int i = 0; i < V; ++i) x[u][i] = oz[i];
-        }
+        const long long slot = ((long long)z * 2 + (z == c ? 1 : 0)) * rows_per_tile + row;
+        l[u] = z <= mine.end ? a.part_lse[slot] : -INFINITY;
+        x[u] = z <= mine.end ? reinterpret_cast<const Vec*>(a.part_o + slot * D)[lane] : Vec{};
       }
+      float m_new = m;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) m_new = fmaxf(m_new, l[u]);
+      if (m_new == -INFINITY) continue;
+      const float back = exp2f(m - m_new);
+      tot *= back;
+#pragma unroll
+      for (int k = 0; k < V; ++k) acc[k] *= back;
 #pragma unroll
       for (int u = 0; u < kAhead; ++u) {
-        tot += w[u];
+        const float w = exp2f(l[u] - m_new);
+        tot += w;
+        const float* xs = reinterpret_cast<const float*>(&x[u]);
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] += w[u] * x[u][i];
+        for (int k = 0; k < V; ++k) acc[k] += w > 0.f ? w * xs[k] : 0.f;  // (a part without keys wrote no O)
       }
+      m = m_new;
     }
   if constexpr (W > 1) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) s_acc[warp][lane * V + i] = acc[i];
-    if (lane == 0) s_tot[warp] = tot;
+    for (int k = 0; k < V; ++k) s_acc[warp][lane * V + k] = acc[k];
+    if (lane == 0) s_ml[warp] = make_float2(m, tot);
     __syncthreads();
     if (sub != 0) return;
+    float top = -INFINITY;
 #pragma unroll
-    for (int w = 1; w < W; ++w) {
-      tot += s_tot[warp + w];
+    for (int w = 0; w < W; ++w) top = fmaxf(top, s_ml[warp + w].x);
+    tot = 0.f;
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] += s_acc[warp + w][lane * V + i];
+    for (int k = 0; k < V; ++k) acc[k] = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const float2 s = s_ml[warp + w];
+      const float f = s.y > 0.f ? exp2f(s.x - top) : 0.f;
+      tot += f * s.y;
+#pragma unroll
+      for (int k = 0; k < V; ++k) acc[k] += f * s_acc[warp + w][lane * V + k];
     }
+    m = top;
   }
   if (!valid) return;
   const float inv = tot > 0.f ? 1.f / tot : 0.f;
   const long long out = (long long)(mine.start + tok) * a.Hq + mine.h * G + (rr - tk * G);
   uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.o) + (out * D + lane * V) * 2);
 #pragma unroll
-  for (int i = 0; i < V / 2; ++i) dst[i] = ptx::pack_bf16x2(acc[2 * i] * inv, acc[2 * i + 1] * inv);
+  for (int k = 0; k < V / 2; ++k) dst[k] = ptx::pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
   if (lane == 0) a.lse[out] = tot > 0.f ? (m + log2f(tot)) * 0.693147180559945309417f : -INFINITY;
 }
 
 template <int D>
 void launch_join(const PagedArgs& a, const PagedPlan& p, cudaStream_t stream) {
-  // four warps per row where tiles have few rows and many parts, else one
-  const int w = p.few ? 4 : 1;
-  const dim3 grid((unsigned)p.ctas, (unsigned)(p.rows * w / kJoinWarps));
-  auto kern = p.few ? fa_paged_join_kernel<D, 4> : fa_paged_join_kernel<D, 1>;
+  // a block per row where tiles have few rows and maybe a part on every SM, else a warp per row
+  const int rows = p.tpt * (a.Hq / a.Hkv), w = p.few ? kJoinWarps : 1;
+  const dim3 grid((unsigned)p.ctas, (unsigned)((rows * w + kJoinWarps - 1) / kJoinWarps));
+  auto kern = p.few ? fa_paged_join_kernel<D, kJoinWarps> : fa_paged_join_kernel<D, 1>;
   kern<<<grid, 32 * kJoinWarps, 0, stream>>>(a, p.rows);
 }
 

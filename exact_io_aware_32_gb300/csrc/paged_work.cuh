@@ -57,7 +57,9 @@ __device__ __forceinline__ long long keys_before(const PagedArgs& a, const Reque
 
 struct Range {
   long long p0, p1;   // this CTA's range of the row of tiles
+  long long per;      // length of a range
   long long pos;      // where the tile that holds p0 begins
+  Request q;          // that tile's request
   int r, h, i, cost;  // that tile; the fixed part of each tile
   int some;           // whether the range holds anything
 };
@@ -70,7 +72,14 @@ struct Piece {
   __device__ __forceinline__ bool whole() const { return jb == 0 && je == nb; }
 };
 
+// a / b for non-negative a, in 32 bits where that is enough (64-bit division takes several times as long).
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
+  return a / b;
+}
+
 // This CTA's range, by all threads of the block (NT of them, a multiple of 32).
+// Two block barriers, so what was set up in shared memory before is there after.
 template <int NT>
 __device__ __forceinline__ void find_range(const PagedArgs& a, Range& out, long long (&s_sum)[2][NT / 32]) {
   constexpr int kWarps = NT / 32;
@@ -78,9 +87,11 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, Range& out, long 
   const int seg = (a.R + NT - 1) / NT, r0 = min(a.R, tid * seg), r1 = min(a.R, r0 + seg);
   long long keys = 0, tiles = 0;  // of this thread's requests
   bool any_bad = false;
+  Request first{};
   for (int r = r0; r < r1; ++r) {
     bool bad;
     const Request q = request(a, r, bad);
+    if (r == r0) first = q;
     any_bad |= bad;
     const int nt = (q.n + a.tpt - 1) / a.tpt;
     keys += a.Hkv * keys_before(a, q, nt, nt);
@@ -103,32 +114,34 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, Range& out, long 
   if (tid == 0) out.some = 0;
   __syncthreads();
   long long all_k = 0, all_t = 0, k0 = ik - keys, t0 = it - tiles;
+#pragma unroll
   for (int w = 0; w < kWarps; ++w) {
+    const long long x = s_sum[0][w], y = s_sum[1][w];
     if (w < warp) {
-      k0 += s_sum[0][w];
-      t0 += s_sum[1][w];
+      k0 += x;
+      t0 += y;
     }
-    all_k += s_sum[0][w];
-    all_t += s_sum[1][w];
+    all_k += x;
+    all_t += y;
   }
   const long long ctas = gridDim.x;
   const int cost = all_k >= kLongRange * ctas ? kTileCost : 1;
   const long long total = all_k + cost * all_t;
-  const long long per = max(kMinRange, (total + ctas - 1) / ctas);
+  const long long per = max(kMinRange, divide(total + ctas - 1, ctas));
   const long long p0 = per * blockIdx.x;
   long long pos = k0 + cost * t0;
   if (p0 < total && pos <= p0 && p0 < pos + keys + cost * tiles) {  // one thread holds p0
-    int r = r0;
-    for (;; ++r) {
-      bool bad;
-      const Request q = request(a, r, bad);
+    Request q = first;
+    for (int r = r0;;) {
       const int nt = (q.n + a.tpt - 1) / a.tpt;
       const long long head = keys_before(a, q, nt, nt) + (long long)cost * nt;
       if (p0 >= pos + a.Hkv * head) {
         pos += a.Hkv * head;
+        bool bad;
+        q = request(a, ++r, bad);
         continue;
       }
-      const int h = (int)((p0 - pos) / head);
+      const int h = (int)divide(p0 - pos, head);
       pos += h * head;
       int lo = 0, hi = nt;  // the last tile that begins at or before p0
       while (hi - lo > 1) {
@@ -138,6 +151,7 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, Range& out, long 
         else
           hi = mid;
       }
+      out.q = q;
       out.r = r;
       out.h = h;
       out.i = lo;
@@ -145,6 +159,7 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, Range& out, long 
       break;
     }
     out.p0 = p0;
+    out.per = per;
     out.p1 = min(total, p0 + per);
     out.cost = cost;
     out.some = 1;
@@ -156,6 +171,7 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, Range& out, long 
 struct Walk {
   Request q, next;  // 'next': the request after q, loaded ahead
   long long p0, p1, pos;
+  long long last, last_len;  // the tile of the last step
   int r, h, i, nt, cost;
 
   __device__ __forceinline__ void ahead(const PagedArgs& a) {
@@ -170,10 +186,16 @@ struct Walk {
     h = g.h;
     i = g.i;
     cost = g.cost;
-    bool bad;
-    q = request(a, r, bad);
+    q = g.q;
     nt = (q.n + a.tpt - 1) / a.tpt;
     ahead(a);
+  }
+  // The CTA that ends the tile of the last step, which this one opened: the last
+  // whose range begins inside the tile and, its cut rounded to a block, before its last block's end.
+  __device__ __forceinline__ int ender(long long per, const Piece& p) const {
+    long long z = divide(last + last_len - 1, per);
+    while (border(z * per - last, p.nb) >= p.nb) --z;
+    return (int)z;
   }
   // The block border nearest to x keys past the tile's fixed part.
   __device__ __forceinline__ int border(long long x, int nb) const {
@@ -191,6 +213,8 @@ struct Walk {
       p.jb = p0 <= pos ? 0 : border(p0 - pos, p.nb);
       p.je = p1 >= pos + len ? p.nb : border(p1 - pos, p.nb);
       const bool use = p.nb ? p.jb < p.je : p0 <= pos;
+      last = pos;
+      last_len = len;
       pos += len;
       if (++i == nt) {
         i = 0;
@@ -218,8 +242,8 @@ struct Walk {
 // begins a tile that later CTAs end (open), with that tile.
 struct Parts {
   int lead, lead_ends, open;
+  int end;               // the CTA that ends the open tile
   int start, n, tok, h;  // the open tile: its request's rows, first token, key head
-  int pad;
 };
 
 }  // namespace paged
