@@ -51,8 +51,9 @@ struct CCfg {
   __host__ __device__ static constexpr uint32_t col_s(int t) { return (uint32_t)t * 128u; }
   __host__ __device__ static constexpr uint32_t col_o(int t) { return 128u * kTiles + (uint32_t)t * D; }
   static constexpr int kWarpTma = 4 * kTiles, kWarpMma = 4 * kTiles + 1;
-  static constexpr int kWarpConv = 4 * kTiles + 2;  // four of them, with FP8
-  static constexpr int kThreads = 128 * kTiles + 64 + (FP8 ? 128 : 0);
+  // with FP8: values copied by a warp of their own, and four converter warps
+  static constexpr int kWarpTmaV = FP8 ? 4 * kTiles + 2 : kWarpTma, kWarpConv = 4 * kTiles + 4;
+  static constexpr int kThreads = 128 * kTiles + (FP8 ? 256 : 64);
 };
 
 struct CBars {
@@ -94,12 +95,13 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
   volatile int* abort_flag = &bars.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  find_range<C::kThreads>(a, bars.range, reinterpret_cast<long long(&)[2][C::kThreads / 32]>(bars.sums));
-  if (!bars.range.some) {  // uniform: every thread leaves before any barrier
-    if (threadIdx.x == 0) static_cast<Parts*>(a.parts)[blockIdx.x] = Parts{};
-    return;
+  // Everything that does not depend on the lengths first; the range's barriers cover it.
+  if (warp == C::kWarpTma && elect_one()) {
+    tma_prefetch_desc(&a.tm_q);
+    tma_prefetch_desc(&a.tm_k);
+    tma_prefetch_desc(&a.tm_v);
   }
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 32) {
     bars.abort = 0;
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars.q_raw[s], 1);
@@ -127,21 +129,20 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  find_range<C::kThreads>(a, bars.range, reinterpret_cast<long long(&)[2][C::kThreads / 32]>(bars.sums));
   tc_fence_after();
   const uint32_t tmem = bars.tmem_base;
+  if (!bars.range.some) {  // uniform: nothing has been issued
+    if (warp == C::kWarpMma) tmem_dealloc(tmem, C::kTmemCols);
+    if (threadIdx.x == 0) static_cast<Parts*>(a.parts)[blockIdx.x] = Parts{};
+    return;
+  }
   Walk walk;
-  walk.begin(a, bars.range);
   Piece p;
+  bool more = walk.begin(a, bars.range, p);
 
   if (warp == C::kWarpTma) {
     // ------------------------------------------------------------ TMA producer
-    if (elect_one()) {
-      tma_prefetch_desc(&a.tm_q);
-      tma_prefetch_desc(&a.tm_k);
-      tma_prefetch_desc(&a.tm_v);
-    }
-    __syncwarp();
     const uint32_t q_bytes = (uint32_t)(a.Hq / a.Hkv * a.tpt1 * D * 2);
     Parts parts{};
     int g = 0, nk = 0, nv = 0, nq[2] = {0, 0};  // key blocks, and loads issued
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
       }
       withhold = false;
     };
-    while (ok && walk.step(a, p)) {
+    for (; ok && more; more = walk.step(a, p)) {
       note_piece(parts, p, walk, bars.range.per);
       int nb[2];
       half_blocks<C::kTiles>(a, p, nb);
@@ -181,13 +182,12 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
           load_q(1);
           if (!ok) break;
         }
-        constexpr int kS = FP8 ? C::kCStages : C::kVStages;
-        const int sv = g % kS;
-        if (!(ok = warp_wait(FP8 ? &bars.c_empty[sv] : &bars.v_empty[sv], ((g / kS) & 1) ^ 1, abort_flag))) break;
-        load_block<D, FP8>(a, p, jj, page_now, lane, &a.tm_v,
-                           smem + (FP8 ? C::kOffC + sv * C::kCodeBytes : C::kOffV + sv * C::kTileBytes),
-                           FP8 ? &bars.c_full[sv] : &bars.v_full[sv]);
-        nv = g + 1;
+        if constexpr (!FP8) {
+          const int sv = g % C::kVStages;
+          if (!(ok = warp_wait(&bars.v_empty[sv], ((g / C::kVStages) & 1) ^ 1, abort_flag))) break;
+          load_block<D, false>(a, p, jj, page_now, lane, &a.tm_v, smem + C::kOffV + sv * C::kTileBytes, &bars.v_full[sv]);
+          nv = g + 1;
+        }
       }
     }
     if (lane == 0) static_cast<Parts*>(a.parts)[blockIdx.x] = parts;
@@ -200,9 +200,27 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
       }
     for (int x = max(0, nk - C::kKStages); x < nk; ++x)
       mbar_wait_drain(&bars.k_full[x % C::kKStages], (x / C::kKStages) & 1);
-    constexpr int kS = FP8 ? C::kCStages : C::kVStages;
-    for (int x = max(0, nv - kS); x < nv; ++x)
-      mbar_wait_drain(FP8 ? &bars.c_full[x % kS] : &bars.v_full[x % kS], (x / kS) & 1);
+    for (int x = max(0, nv - C::kVStages); x < nv; ++x)
+      mbar_wait_drain(&bars.v_full[x % C::kVStages], (x / C::kVStages) & 1);
+  } else if (FP8 && warp == C::kWarpTmaV) {
+    // ------------------------------------------------------------ value codes
+    constexpr int kCS = FP8 ? C::kCStages : 1;
+    int g = 0, nc = 0;
+    bool ok = true;
+    for (; ok && more; more = walk.step(a, p)) {
+      int nb[2];
+      half_blocks<C::kTiles>(a, p, nb);
+      const int nbm = max(nb[0], nb[1]);
+      int page = nbm > 0 ? lane_page(a, p, p.jb, lane) : -1;
+      for (int j = 0; j < nbm; ++j, ++g) {
+        const int jj = p.jb + j, page_now = page, s = g % kCS;
+        if (j + 1 < nbm) page = lane_page(a, p, jj + 1, lane);
+        if (!(ok = warp_wait(&bars.c_empty[s], ((g / kCS) & 1) ^ 1, abort_flag))) break;
+        load_block<D, FP8>(a, p, jj, page_now, lane, &a.tm_v, smem + C::kOffC + s * C::kCodeBytes, &bars.c_full[s]);
+        nc = g + 1;
+      }
+    }
+    for (int x = max(0, nc - kCS); x < nc; ++x) mbar_wait_drain(&bars.c_full[x % kCS], (x / kCS) & 1);
   } else if (warp == C::kWarpMma) {
     // ------------------------------------------------------------ MMA issuer
     // Per key block j and half t: O_t += P_t V_j, then at once S_t for block
@@ -220,7 +238,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     };
     int g = 0, nq[2] = {0, 0}, np[2] = {0, 0};  // key blocks; tiles and P blocks of each half so far
     bool ok = true;
-    while (ok && walk.step(a, p)) {
+    for (; ok && more; more = walk.step(a, p)) {
       int nb[2];
       half_blocks<C::kTiles>(a, p, nb);
       const int nbm = max(nb[0], nb[1]);
@@ -299,7 +317,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
       conv_arrive(&bars.q_full[t][nq[t] & 1], nullptr, lane);
       ++nq[t];
     };
-    while (ok && walk.step(a, p)) {
+    for (; ok && more; more = walk.step(a, p)) {
       int nb[2];
       half_blocks<C::kTiles>(a, p, nb);
       const int nbm = max(nb[0], nb[1]);
@@ -314,7 +332,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
         conv_arrive(&bars.v_full[vs], &bars.c_empty[cs], lane);
       }
     }
-  } else {
+  } else if (warp < 4 * C::kTiles) {
     // ------------------------------------------------------------ softmax + epilogue
     const int t = warp >> 2;
     const int r = (warp & 3) * 32 + lane;  // row within the half = TMEM lane
@@ -326,7 +344,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     const bool o32 = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
     int np = 0, nq = 0;  // blocks and tiles of this half so far
     bool ok = true;
-    while (ok && walk.step(a, p)) {
+    for (; ok && more; more = walk.step(a, p)) {
       int nb2[2];
       half_blocks<C::kTiles>(a, p, nb2);
       const int nb = nb2[t];
@@ -344,32 +362,42 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
         ok = __all_sync(0xffffffffu, mbar_wait(&bars.s_full[t], np & 1, abort_flag));
         if (!ok) break;
         tc_fence_after();
-        // S_t, with the maximum of each 32 columns from the load itself
-        uint32_t sr[4][32];
-        float cmax[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32_max(t_s + c * 32, sr[c], cmax[c]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_wait(sr[c], cmax[c]);
-        float mx = fmax3(fmax3(cmax[0], cmax[1], cmax[2]), cmax[3], -INFINITY);
         // only blocks that reach past the first row's last key, or past the request's, need masking
         const int kv0 = (p.jb + j) * 128;
-        if ((CAUSAL && kv0 + 127 > tok0 + off) || kv0 + 128 > p.q.len) {
-          const int lim = (CAUSAL ? min(tok + off, p.q.len - 1) : p.q.len - 1) - kv0;  // keep column c iff c <= lim
+        const bool need_mask = (CAUSAL && kv0 + 127 > tok0 + off) || kv0 + 128 > p.q.len;
+        const int lim = (CAUSAL ? min(tok + off, p.q.len - 1) : p.q.len - 1) - kv0;  // keep column c iff c <= lim
+        // S_t, with the maximum of each 32 columns from the load itself. All of it stays in registers for the
+        // exponentials, except with E4M3 caches: 512 threads leave 128 registers each, so there S is loaded twice, 64
+        // columns at a time (held once, it spilled 600 bytes a thread).
+        constexpr int kHeld = FP8 ? 2 : 4;  // chunks of 32 columns in registers
+        uint32_t sr[kHeld][32];
+        float mx = -INFINITY;
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c > lim) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
-          float mxc[8];  // row maximum over eight chains of 16 scores, then a tree
+        for (int c0 = 0; c0 < 4; c0 += kHeld) {
+          float cmax[kHeld];
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            mxc[i] = fmaxf(__uint_as_float(sr[0][2 * i]), __uint_as_float(sr[0][2 * i + 1]));
+          for (int c = 0; c < kHeld; ++c) tmem_ld32_max(t_s + (c0 + c) * 32, sr[c], cmax[c]);
 #pragma unroll
-          for (int c = 16; c < 128; c += 16)
+          for (int c = 0; c < kHeld; ++c) tmem_ld_wait(sr[c], cmax[c]);
+          if (need_mask) {
+#pragma unroll
+            for (int c = 0; c < 32 * kHeld; ++c)
+              if (c0 * 32 + c > lim) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+            float mxc[8];  // row maximum over eight chains, then a tree
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              mxc[i] = fmax3(mxc[i], __uint_as_float(sr[c >> 5][(c & 31) + 2 * i]),
-                             __uint_as_float(sr[c >> 5][(c & 31) + 2 * i + 1]));
-          mx = fmax3(fmax3(mxc[0], mxc[1], mxc[2]), fmax3(mxc[3], mxc[4], mxc[5]), fmaxf(mxc[6], mxc[7]));
+              mxc[i] = fmaxf(__uint_as_float(sr[0][2 * i]), __uint_as_float(sr[0][2 * i + 1]));
+#pragma unroll
+            for (int c = 16; c < 32 * kHeld; c += 16)
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                mxc[i] = fmax3(mxc[i], __uint_as_float(sr[c >> 5][(c & 31) + 2 * i]),
+                               __uint_as_float(sr[c >> 5][(c & 31) + 2 * i + 1]));
+            mx = fmaxf(mx, fmax3(fmax3(mxc[0], mxc[1], mxc[2]), fmax3(mxc[3], mxc[4], mxc[5]), fmaxf(mxc[6], mxc[7])));
+          } else {
+#pragma unroll
+            for (int c = 0; c < kHeld; c += 2) mx = fmax3(mx, cmax[c], cmax[c + 1]);
+          }
         }
         float alpha = 1.f;
         const float m_new = fmaxf(m_ref, mx * sl2);
@@ -383,12 +411,23 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
         const float m_use = (m_ref == -INFINITY ? 0.f : m_ref) - kBias;  // a row that has seen no key yet: P = 0
         const float2 scale2 = make_float2(sl2, sl2), shift2 = make_float2(-m_use, -m_use);
 #pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {  // P as bf16 pairs over the first 64 columns of S_t
+        for (int ch = 0; ch < 4; ++ch) {  // P as 16-bit pairs over the first 64 columns of S_t
+          const int held = ch % kHeld;
+          if (FP8 && held == 0) {  // (P of the chunks before lies over S columns that have been read)
+            tmem_ld32(t_s + ch * 32, sr[0]);
+            tmem_ld32(t_s + ch * 32 + 32, sr[1]);
+            tmem_ld_wait(sr[0]);
+            tmem_ld_wait(sr[1]);
+            if (need_mask)
+#pragma unroll
+              for (int c = 0; c < 64; ++c)
+                if (ch * 32 + c > lim) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+          }
           uint32_t pk[16];
 #pragma unroll
           for (int c = 0; c < 32; c += 2) {
             const float2 x =
-                ffma2(make_float2(__uint_as_float(sr[ch][c]), __uint_as_float(sr[ch][c + 1])), scale2, shift2);
+                ffma2(make_float2(__uint_as_float(sr[held][c]), __uint_as_float(sr[held][c + 1])), scale2, shift2);
             const float2 e = make_float2(ex2(x.x), ex2(x.y));
             sum4[(c >> 1) & 3] = fadd2(sum4[(c >> 1) & 3], e);
             pk[c >> 1] = FP8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);

@@ -18,8 +18,8 @@
 // Persistent CTAs over ranges of the row of tiles (paged_work.cuh), rings and
 // barriers counting on across tiles.
 //
-// Warp roles: 0-3 softmax and epilogue; 4 copies keys and Q, 5 values; 6 issues
-// P V and owns TMEM, 7 issues Q K^T; with E4M3 caches eight converter warps
+// Warp roles: 0-3 softmax and epilogue; 4 copies keys, 5 values; 6 issues P V and
+// owns TMEM, 7 copies Q and issues Q K^T; with E4M3 caches eight converter warps
 // (value codes to f16, Q to its two parts).
 #include "paged_pipe.cuh"
 
@@ -131,20 +131,16 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     return;
   }
   Walk walk;
-  walk.begin(a, range);
-  const long long per = range.per;
   Piece p;
+  bool more = walk.begin(a, range, p);
+  const long long per = range.per;
   __syncthreads();  // all have read the range: the join may write there
   if (warp == C::kWarpTmaK) {
-    // ------------------------------------------------------------ keys and Q
-    // E4M3 caches: one copy of Q, which the converters make four of
-    constexpr int kCopies = FP8 ? 1 : 4;
-    const uint32_t q_bytes = (uint32_t)(kCopies * G * a.tpt * D * 2);
+    // ------------------------------------------------------------ keys
     Parts parts{};
-    int g = 0, nk = 0, nq = 0;  // key blocks, and loads issued
+    int g = 0, nk = 0;  // key blocks, and loads issued
     bool ok = true;
-    bool withhold = a.test_fault == 1;  // test hook: the MMA warps' first wait expires
-    while (ok && walk.step(a, p)) {
+    for (; ok && more; more = walk.step(a, p)) {
       note_piece(parts, p, walk, per);
       const int nb = p.je - p.jb;
       if (nb == 0) continue;
@@ -156,27 +152,10 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
         if (!(ok = warp_wait(&bars.k_empty[s], ((g / C::kKStages) & 1) ^ 1, abort_flag))) break;
         load_block<D, FP8>(a, p, jj, page_now, lane, &a.tm_k, smem + C::kOffK + s * C::kKBytes, &bars.k_full[s]);
         nk = g + 1;
-        if (j > 0) continue;
-        // Q after the first block's keys, whose slot is free earlier
-        if (!(ok = warp_wait(&bars.q_free, (nq & 1) ^ 1, abort_flag))) break;
-        if (!withhold) {
-          uint64_t* bar = FP8 ? &bars.q_raw : &bars.q_full[nq % 3];
-          if (elect_one()) {
-            mbar_arrive_expect_tx(bar, q_bytes);
-            for (int w = 0; w < kCopies; ++w)
-              for (int pn = 0; pn < C::kPanels; ++pn)
-                tma_load_3d(smem + C::kOffQ + pn * 16384 + w * 4096, &a.tm_q, bar, pn * 64, p.h * G, p.q.start + p.tok);
-          }
-          __syncwarp();
-          ++nq;
-        }
-        withhold = false;
       }
     }
     if (lane == 0) static_cast<Parts*>(a.parts)[blockIdx.x] = parts;
     // Let every issued copy land before the CTA can exit.
-    if (nq > 0 && FP8) mbar_wait_drain(&bars.q_raw, (nq - 1) & 1);
-    if (nq > 0 && !FP8) mbar_wait_drain(&bars.q_full[(nq - 1) % 3], ((nq - 1) / 3) & 1);
     for (int x = max(0, nk - C::kKStages); x < nk; ++x)
       mbar_wait_drain(&bars.k_full[x % C::kKStages], (x / C::kKStages) & 1);
   } else if (warp == C::kWarpTmaV) {
@@ -186,7 +165,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     uint64_t *full = FP8 ? bars.c_full : bars.v_full, *empty = FP8 ? bars.c_empty : bars.v_empty;
     int g = 0, nv = 0;
     bool ok = true;
-    while (ok && walk.step(a, p)) {
+    for (; ok && more; more = walk.step(a, p)) {
       if (p.jb == p.je) continue;
       int page = lane_page(a, p, p.jb, lane);
       for (int jj = p.jb; jj < p.je; ++jj, ++g) {
@@ -203,10 +182,27 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     // ------------------------------------------------------------ S = Q K^T, up to two blocks ahead of the softmax
     const uint64_t dq = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
     const uint64_t dk = desc_keys<D, FP8>(smem + C::kOffK);
-    int g = 0, n = 0;  // key blocks, tiles
+    // Q is copied by this warp too, as soon as the tile before has been read (E4M3 caches: once, which the converters
+    // make four of)
+    constexpr int kCopies = FP8 ? 1 : 4;
+    const uint32_t q_bytes = (uint32_t)(kCopies * G * a.tpt * D * 2);
+    const bool withhold = a.test_fault == 1;  // test hook: without its Q the wait below expires
+    int g = 0, n = 0, nq = 0;                 // key blocks, tiles, copies of Q issued
     bool ok = true;
-    while (ok && walk.step(a, p)) {
+    for (; ok && more; more = walk.step(a, p)) {
       if (p.jb == p.je) continue;
+      if (!(ok = warp_wait(&bars.q_free, (n & 1) ^ 1, abort_flag))) break;
+      if (!withhold) {
+        uint64_t* bar = FP8 ? &bars.q_raw : &bars.q_full[n % 3];
+        if (elect_one()) {
+          mbar_arrive_expect_tx(bar, q_bytes);
+          for (int w = 0; w < kCopies; ++w)
+            for (int pn = 0; pn < C::kPanels; ++pn)
+              tma_load_3d(smem + C::kOffQ + pn * 16384 + w * 4096, &a.tm_q, bar, pn * 64, p.h * G, p.q.start + p.tok);
+        }
+        __syncwarp();
+        ++nq;
+      }
       if (!(ok = warp_wait(&bars.q_full[n % 3], (n / 3) & 1, abort_flag))) break;
       ++n;
       for (int jj = p.jb; jj < p.je; ++jj, ++g) {
@@ -223,6 +219,8 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
         __syncwarp();
       }
     }
+    // a copy of Q still on its way after an abort lands before the CTA can exit
+    if (nq > n) mbar_wait_drain(FP8 ? &bars.q_raw : &bars.q_full[n % 3], FP8 ? n & 1 : (n / 3) & 1);
     if (elect_one()) mma_commit(&bars.teardown[0]);
     __syncwarp();
     mbar_wait_drain(&bars.teardown[0], 0);
@@ -232,7 +230,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     const uint64_t dv = Tile<D>::desc_v(smem + C::kOffV);
     int g = 0, n = 0;  // key blocks, tiles
     bool ok = true;
-    while (ok && walk.step(a, p)) {
+    for (; ok && more; more = walk.step(a, p)) {
       if (p.jb == p.je) continue;
       for (int jj = p.jb; jj < p.je; ++jj, ++g) {
         const int s = g % C::kVStages, b = g & 1;
@@ -266,7 +264,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     constexpr int kCS = FP8 ? C::kCStages : 1;
     int g = 0, n = 0;
     bool ok = true;
-    while (ok && walk.step(a, p)) {
+    for (; ok && more; more = walk.step(a, p)) {
       if (p.je > p.jb) {
         if (tid < 128) {  // Q, by four of the warps
           if (!(ok = warp_wait(&bars.q_raw, n & 1, abort_flag))) break;
@@ -302,7 +300,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     }
     int g = 0, n = 0;
     bool ok = true;
-    while (ok && walk.step(a, p)) {
+    for (; ok && more; more = walk.step(a, p)) {
       const int nb = p.je - p.jb;
       float sl2 = a.scale_log2;
       if (FP8 && nb > 0) {  // (their place is written again three tiles on, after this warp has read the first S of this one)

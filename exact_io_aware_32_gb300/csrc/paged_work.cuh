@@ -55,15 +55,6 @@ __device__ __forceinline__ long long keys_before(const PagedArgs& a, const Reque
   return (long long)i * max(q.len - q.n, 0) + a.tpt * (whole * (whole + 1) / 2) + (i == nt ? q.n : 0);
 }
 
-struct Range {
-  long long p0, p1;   // this CTA's range of the row of tiles
-  long long per;      // length of a range
-  long long pos;      // where the tile that holds p0 begins
-  Request q;          // that tile's request
-  int r, h, i, cost;  // that tile; the fixed part of each tile
-  int some;           // whether the range holds anything
-};
-
 // A part of a tile for this CTA: key blocks [jb, je) of nb.
 struct Piece {
   Request q;
@@ -72,105 +63,149 @@ struct Piece {
   __device__ __forceinline__ bool whole() const { return jb == 0 && je == nb; }
 };
 
+struct Range {
+  long long p0, p1;    // this CTA's range of the row of tiles
+  long long per;       // length of a range
+  long long pos, len;  // the tile that holds p0: where it begins, and its length
+  int i, nt, cost;     // its number of its request's nt tiles; the fixed part of each tile
+  int some, use;       // whether the range holds anything, and whether that tile's part of it is a piece
+  Piece first;         // that part
+};
+
 // a / b for non-negative a, in 32 bits where that is enough (64-bit division takes several times as long).
 __device__ __forceinline__ long long divide(long long a, long long b) {
   if (((a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
   return a / b;
 }
 
-// This CTA's range, by all threads of the block (NT of them, a multiple of 32).
-// Two block barriers, so what was set up in shared memory before is there after.
+// The block border nearest to x keys past a tile's fixed part.
+__device__ __forceinline__ int border(long long x, int cost, int nb) {
+  const long long b = (x - cost + 64) >> 7;
+  return (int)min(max(b, 0ll), (long long)nb);
+}
+
+// The part of tile i of request q, at pos and len long, that lies in [p0, p1): p.jb, p.je, p.nb; whether it is a piece
+// (a tile that sees no key is one of the CTA where it begins).
+__device__ __forceinline__ bool cut(const PagedArgs& a, const Request& q, int i, long long pos, long long len, int cost,
+                                    long long p0, long long p1, Piece& p) {
+  p.q = q;
+  p.tok = i * a.tpt;
+  p.nb = (keys_seen(a, q, p.tok + a.tpt) + 127) >> 7;
+  p.jb = p0 <= pos ? 0 : border(p0 - pos, cost, p.nb);
+  p.je = p1 >= pos + len ? p.nb : border(p1 - pos, cost, p.nb);
+  return p.nb ? p.jb < p.je : p0 <= pos;
+}
+
+// This CTA's range, by all NT threads of the block. What was set up in shared
+// memory before is there after. Up to 32 * kWarpRequests requests are one warp's
+// work, the others wait: every instruction here counts once per warp that runs
+// it, and all warps working it out took 1500 cycles more.
+constexpr int kWarpRequests = 8;
 template <int NT>
 __device__ __forceinline__ void find_range(const PagedArgs& a, Range& out, long long (&s_sum)[2][NT / 32]) {
   constexpr int kWarps = NT / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int seg = (a.R + NT - 1) / NT, r0 = min(a.R, tid * seg), r1 = min(a.R, r0 + seg);
-  long long keys = 0, tiles = 0;  // of this thread's requests
-  bool any_bad = false;
-  Request first{};
-  for (int r = r0; r < r1; ++r) {
-    bool bad;
-    const Request q = request(a, r, bad);
-    if (r == r0) first = q;
-    any_bad |= bad;
-    const int nt = (q.n + a.tpt - 1) / a.tpt;
-    keys += a.Hkv * keys_before(a, q, nt, nt);
-    tiles += (long long)a.Hkv * nt;
-  }
-  if (any_bad && blockIdx.x == 0) atomicOr(a.status, kStatusBadLength);
-  long long ik = keys, it = tiles;
-#pragma unroll
-  for (int s = 1; s < 32; s <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, ik, s), y = __shfl_up_sync(0xffffffffu, it, s);
-    if (lane >= s) {
-      ik += x;
-      it += y;
-    }
-  }
-  if (lane == 31) {
-    s_sum[0][warp] = ik;
-    s_sum[1][warp] = it;
-  }
-  if (tid == 0) out.some = 0;
-  __syncthreads();
-  long long all_k = 0, all_t = 0, k0 = ik - keys, t0 = it - tiles;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const long long x = s_sum[0][w], y = s_sum[1][w];
-    if (w < warp) {
-      k0 += x;
-      t0 += y;
-    }
-    all_k += x;
-    all_t += y;
-  }
-  const long long ctas = gridDim.x;
-  const int cost = all_k >= kLongRange * ctas ? kTileCost : 1;
-  const long long total = all_k + cost * all_t;
-  const long long per = max(kMinRange, divide(total + ctas - 1, ctas));
-  const long long p0 = per * blockIdx.x;
-  long long pos = k0 + cost * t0;
-  if (p0 < total && pos <= p0 && p0 < pos + keys + cost * tiles) {  // one thread holds p0
-    Request q = first;
-    for (int r = r0;;) {
+  const bool alone = a.R <= 32 * kWarpRequests;  // by the first warp
+  if (!alone || warp == 0) {
+    const int threads = alone ? 32 : NT;
+    const int seg = (a.R + threads - 1) / threads, r0 = min(a.R, tid * seg), r1 = min(a.R, r0 + seg);
+    long long keys = 0, tiles = 0;  // of this thread's requests
+    bool any_bad = false;
+    Request first{};
+    for (int r = r0; r < r1; ++r) {
+      bool bad;
+      const Request q = request(a, r, bad);
+      if (r == r0) first = q;
+      any_bad |= bad;
       const int nt = (q.n + a.tpt - 1) / a.tpt;
-      const long long head = keys_before(a, q, nt, nt) + (long long)cost * nt;
-      if (p0 >= pos + a.Hkv * head) {
-        pos += a.Hkv * head;
-        bool bad;
-        q = request(a, ++r, bad);
-        continue;
-      }
-      const int h = (int)divide(p0 - pos, head);
-      pos += h * head;
-      int lo = 0, hi = nt;  // the last tile that begins at or before p0
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (keys_before(a, q, mid, nt) + (long long)cost * mid <= p0 - pos)
-          lo = mid;
-        else
-          hi = mid;
-      }
-      out.q = q;
-      out.r = r;
-      out.h = h;
-      out.i = lo;
-      out.pos = pos + keys_before(a, q, lo, nt) + (long long)cost * lo;
-      break;
+      keys += a.Hkv * keys_before(a, q, nt, nt);
+      tiles += (long long)a.Hkv * nt;
     }
-    out.p0 = p0;
-    out.per = per;
-    out.p1 = min(total, p0 + per);
-    out.cost = cost;
-    out.some = 1;
+    if (any_bad && blockIdx.x == 0) atomicOr(a.status, kStatusBadLength);
+    long long ik = keys, it = tiles;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, ik, s), y = __shfl_up_sync(0xffffffffu, it, s);
+      if (lane >= s) {
+        ik += x;
+        it += y;
+      }
+    }
+    long long all_k = __shfl_sync(0xffffffffu, ik, 31), all_t = __shfl_sync(0xffffffffu, it, 31);
+    long long k0 = ik - keys, t0 = it - tiles;
+    if (!alone) {
+      if (lane == 31) {
+        s_sum[0][warp] = ik;
+        s_sum[1][warp] = it;
+      }
+      __syncthreads();
+      all_k = all_t = 0;
+#pragma unroll 1
+      for (int w = 0; w < kWarps; ++w) {
+        const long long x = s_sum[0][w], y = s_sum[1][w];
+        if (w < warp) {
+          k0 += x;
+          t0 += y;
+        }
+        all_k += x;
+        all_t += y;
+      }
+    }
+    const long long ctas = gridDim.x;
+    const int cost = all_k >= kLongRange * ctas ? kTileCost : 1;
+    const long long total = all_k + cost * all_t;
+    const long long per = max(kMinRange, divide(total + ctas - 1, ctas));
+    const long long p0 = per * blockIdx.x, p1 = min(total, p0 + per);
+    if (tid == 0 && p0 >= total) out.some = 0;
+    long long pos = k0 + cost * t0;
+    if (p0 < total && pos <= p0 && p0 < pos + keys + cost * tiles) {  // one thread holds p0
+      Request q = first;
+      for (int r = r0;;) {
+        const int nt = (q.n + a.tpt - 1) / a.tpt;
+        const long long head = keys_before(a, q, nt, nt) + (long long)cost * nt;
+        if (p0 >= pos + a.Hkv * head) {
+          pos += a.Hkv * head;
+          bool bad;
+          q = request(a, ++r, bad);
+          continue;
+        }
+        const int h = (int)divide(p0 - pos, head);
+        pos += h * head;
+        int lo = 0, hi = nt;  // the last tile that begins at or before p0
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (keys_before(a, q, mid, nt) + (long long)cost * mid <= p0 - pos)
+            lo = mid;
+          else
+            hi = mid;
+        }
+        pos += keys_before(a, q, lo, nt) + (long long)cost * lo;
+        Range g;
+        g.p0 = p0;
+        g.p1 = p1;
+        g.per = per;
+        g.pos = pos;
+        g.len = tile_keys(a, q, lo) + cost;
+        g.i = lo;
+        g.nt = nt;
+        g.cost = cost;
+        g.some = 1;
+        g.use = cut(a, q, lo, pos, g.len, cost, p0, p1, g.first);
+        g.first.r = r;
+        g.first.h = h;
+        out = g;
+        break;
+      }
+    }
   }
   __syncthreads();
 }
 
-// Walks a range's pieces in order; every warp role walks the same ones.
+// Walks a range's pieces in order; every warp role walks the same ones:
+// for (bool more = walk.begin(a, range, p); more; more = walk.step(a, p)).
 struct Walk {
-  Request q, next;  // 'next': the request after q, loaded ahead
-  long long p0, p1, pos;
+  Request q, next;           // 'next': the request after q, loaded ahead
+  long long p0, p1, pos;     // pos: where the next tile begins
   long long last, last_len;  // the tile of the last step
   int r, h, i, nt, cost;
 
@@ -178,62 +213,56 @@ struct Walk {
     bool bad;
     if (r + 1 < a.R) next = request(a, r + 1, bad);
   }
-  __device__ __forceinline__ void begin(const PagedArgs& a, const Range& g) {
+  __device__ __forceinline__ void advance(const PagedArgs& a, long long len) {
+    last = pos;
+    last_len = len;
+    pos += len;
+    if (++i < nt) return;
+    i = 0;
+    if (++h < a.Hkv) return;
+    h = 0;
+    do {
+      if (++r >= a.R) {
+        p1 = pos;  // past the last request
+        return;
+      }
+      q = next;
+      ahead(a);
+    } while (q.n == 0);
+    nt = (q.n + a.tpt - 1) / a.tpt;
+  }
+  __device__ __forceinline__ bool begin(const PagedArgs& a, const Range& g, Piece& p) {
+    p = g.first;
     p0 = g.p0;
     p1 = g.p1;
     pos = g.pos;
-    r = g.r;
-    h = g.h;
+    q = p.q;
+    r = p.r;
+    h = p.h;
     i = g.i;
+    nt = g.nt;
     cost = g.cost;
-    q = g.q;
-    nt = (q.n + a.tpt - 1) / a.tpt;
     ahead(a);
+    advance(a, g.len);
+    return g.use ? true : step(a, p);
+  }
+  __device__ __forceinline__ bool step(const PagedArgs& a, Piece& p) {
+    while (pos < p1) {
+      const long long len = tile_keys(a, q, i) + cost;
+      p.r = r;
+      p.h = h;
+      const bool use = cut(a, q, i, pos, len, cost, p0, p1, p);
+      advance(a, len);
+      if (use) return true;
+    }
+    return false;
   }
   // The CTA that ends the tile of the last step, which this one opened: the last
   // whose range begins inside the tile and, its cut rounded to a block, before its last block's end.
   __device__ __forceinline__ int ender(long long per, const Piece& p) const {
     long long z = divide(last + last_len - 1, per);
-    while (border(z * per - last, p.nb) >= p.nb) --z;
+    while (border(z * per - last, cost, p.nb) >= p.nb) --z;
     return (int)z;
-  }
-  // The block border nearest to x keys past the tile's fixed part.
-  __device__ __forceinline__ int border(long long x, int nb) const {
-    const long long b = (x - cost + 64) >> 7;
-    return (int)min(max(b, 0ll), (long long)nb);
-  }
-  __device__ __forceinline__ bool step(const PagedArgs& a, Piece& p) {
-    while (pos < p1) {
-      const long long len = tile_keys(a, q, i) + cost;
-      p.q = q;
-      p.r = r;
-      p.h = h;
-      p.tok = i * a.tpt;
-      p.nb = (keys_seen(a, q, p.tok + a.tpt) + 127) >> 7;
-      p.jb = p0 <= pos ? 0 : border(p0 - pos, p.nb);
-      p.je = p1 >= pos + len ? p.nb : border(p1 - pos, p.nb);
-      const bool use = p.nb ? p.jb < p.je : p0 <= pos;
-      last = pos;
-      last_len = len;
-      pos += len;
-      if (++i == nt) {
-        i = 0;
-        if (++h == a.Hkv) {
-          h = 0;
-          do {
-            if (++r >= a.R) {
-              p1 = pos;  // past the last request
-              break;
-            }
-            q = next;
-            ahead(a);
-          } while (q.n == 0);
-          nt = (q.n + a.tpt - 1) / a.tpt;
-        }
-      }
-      if (use) return true;
-    }
-    return false;
   }
 };
 
