@@ -16,8 +16,8 @@
 // tensor store could write.
 //
 // Warp roles: a softmax warpgroup per 128-row half, the TMA warp, the MMA warp,
-// and with E4M3 caches a warpgroup that turns value codes into f16 operands (TMA
-// -> ring of codes -> converters -> V ring) and Q into its two 8-bit parts.
+// and with E4M3 caches two warps that turn value codes into f16 operands (TMA ->
+// ring of codes -> converters -> V ring) and Q into its two 8-bit parts.
 #include "paged_pipe.cuh"
 
 namespace fa {
@@ -51,9 +51,11 @@ struct CCfg {
   __host__ __device__ static constexpr uint32_t col_s(int t) { return (uint32_t)t * 128u; }
   __host__ __device__ static constexpr uint32_t col_o(int t) { return 128u * kTiles + (uint32_t)t * D; }
   static constexpr int kWarpTma = 4 * kTiles, kWarpMma = 4 * kTiles + 1;
-  // with FP8: values copied by a warp of their own, and four converter warps
-  static constexpr int kWarpTmaV = FP8 ? 4 * kTiles + 2 : kWarpTma, kWarpConv = 4 * kTiles + 4;
-  static constexpr int kThreads = 128 * kTiles + (FP8 ? 256 : 64);
+  // With FP8 two converter warps: more than 384 threads leave a softmax thread, which holds 128 scores, no more than 128
+  // registers. (Four of them and a warp for the values' copies, with S loaded twice: chunks of prompts at d = 128 333 us;
+  // with S held once and spilled 433 us.)
+  static constexpr int kWarpConv = 4 * kTiles + 2, kConvWarps = 2;
+  static constexpr int kThreads = 128 * kTiles + 64 + (FP8 ? 32 * kConvWarps : 0);
 };
 
 struct CBars {
@@ -105,8 +107,8 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     bars.abort = 0;
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars.q_raw[s], 1);
-      mbar_init(&bars.q_full[s][0], FP8 ? 4 : 1);
-      mbar_init(&bars.q_full[s][1], FP8 ? 4 : 1);
+      mbar_init(&bars.q_full[s][0], FP8 ? C::kConvWarps : 1);
+      mbar_init(&bars.q_full[s][1], FP8 ? C::kConvWarps : 1);
       mbar_init(&bars.q_free[s], 1);
       mbar_init(&bars.s_full[s], 1);
       mbar_init(&bars.p_full[s], 128);
@@ -116,10 +118,10 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     for (int s = 0; s < 3; ++s) {
       mbar_init(&bars.k_full[s], 1);
       mbar_init(&bars.k_empty[s], 1);
-      mbar_init(&bars.v_full[s], FP8 ? 4 : 1);
+      mbar_init(&bars.v_full[s], FP8 ? C::kConvWarps : 1);
       mbar_init(&bars.v_empty[s], 1);
       mbar_init(&bars.c_full[s], 1);
-      mbar_init(&bars.c_empty[s], 4);
+      mbar_init(&bars.c_empty[s], C::kConvWarps);
     }
     mbar_init(&bars.teardown, 1);
     fence_mbar_init();
@@ -144,6 +146,8 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
   if (warp == C::kWarpTma) {
     // ------------------------------------------------------------ TMA producer
     const uint32_t q_bytes = (uint32_t)(a.Hq / a.Hkv * a.tpt1 * D * 2);
+    constexpr int kS = FP8 ? C::kCStages : C::kVStages;  // values, or their codes
+    uint64_t *v_full = FP8 ? bars.c_full : bars.v_full, *v_empty = FP8 ? bars.c_empty : bars.v_empty;
     Parts parts{};
     int g = 0, nk = 0, nv = 0, nq[2] = {0, 0};  // key blocks, and loads issued
     bool ok = true;
@@ -182,12 +186,11 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
           load_q(1);
           if (!ok) break;
         }
-        if constexpr (!FP8) {
-          const int sv = g % C::kVStages;
-          if (!(ok = warp_wait(&bars.v_empty[sv], ((g / C::kVStages) & 1) ^ 1, abort_flag))) break;
-          load_block<D, false>(a, p, jj, page_now, lane, &a.tm_v, smem + C::kOffV + sv * C::kTileBytes, &bars.v_full[sv]);
-          nv = g + 1;
-        }
+        const int sv = g % kS;
+        if (!(ok = warp_wait(&v_empty[sv], ((g / kS) & 1) ^ 1, abort_flag))) break;
+        load_block<D, FP8>(a, p, jj, page_now, lane, &a.tm_v,
+                           smem + (FP8 ? C::kOffC + sv * C::kCodeBytes : C::kOffV + sv * C::kTileBytes), &v_full[sv]);
+        nv = g + 1;
       }
     }
     if (lane == 0) static_cast<Parts*>(a.parts)[blockIdx.x] = parts;
@@ -200,27 +203,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
       }
     for (int x = max(0, nk - C::kKStages); x < nk; ++x)
       mbar_wait_drain(&bars.k_full[x % C::kKStages], (x / C::kKStages) & 1);
-    for (int x = max(0, nv - C::kVStages); x < nv; ++x)
-      mbar_wait_drain(&bars.v_full[x % C::kVStages], (x / C::kVStages) & 1);
-  } else if (FP8 && warp == C::kWarpTmaV) {
-    // ------------------------------------------------------------ value codes
-    constexpr int kCS = FP8 ? C::kCStages : 1;
-    int g = 0, nc = 0;
-    bool ok = true;
-    for (; ok && more; more = walk.step(a, p)) {
-      int nb[2];
-      half_blocks<C::kTiles>(a, p, nb);
-      const int nbm = max(nb[0], nb[1]);
-      int page = nbm > 0 ? lane_page(a, p, p.jb, lane) : -1;
-      for (int j = 0; j < nbm; ++j, ++g) {
-        const int jj = p.jb + j, page_now = page, s = g % kCS;
-        if (j + 1 < nbm) page = lane_page(a, p, jj + 1, lane);
-        if (!(ok = warp_wait(&bars.c_empty[s], ((g / kCS) & 1) ^ 1, abort_flag))) break;
-        load_block<D, FP8>(a, p, jj, page_now, lane, &a.tm_v, smem + C::kOffC + s * C::kCodeBytes, &bars.c_full[s]);
-        nc = g + 1;
-      }
-    }
-    for (int x = max(0, nc - kCS); x < nc; ++x) mbar_wait_drain(&bars.c_full[x % kCS], (x / kCS) & 1);
+    for (int x = max(0, nv - kS); x < nv; ++x) mbar_wait_drain(&v_full[x % kS], (x / kS) & 1);
   } else if (warp == C::kWarpMma) {
     // ------------------------------------------------------------ MMA issuer
     // Per key block j and half t: O_t += P_t V_j, then at once S_t for block
@@ -313,7 +296,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     auto convert_half = [&](int t) {  // Q of half t, in the order in which it was loaded
       if (!(ok = warp_wait(&bars.q_raw[t], nq[t] & 1, abort_flag))) return;
       const int rows = min(a.tpt1, p.q.n - p.tok - t * a.tpt1) * G;
-      convert_q<D, false>(smem + C::kOffQ + t * C::kTileBytes, bars.q_ex[nq[t] & 1][t], (rows + 31) / 32, tid);
+      convert_q<D, false, 32 * C::kConvWarps>(smem + C::kOffQ + t * C::kTileBytes, bars.q_ex[nq[t] & 1][t], rows, tid);
       conv_arrive(&bars.q_full[t][nq[t] & 1], nullptr, lane);
       ++nq[t];
     };
@@ -327,8 +310,8 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
         const int vs = g % C::kVStages, cs = g % kCS;
         ok = warp_wait2(&bars.c_full[cs], (g / kCS) & 1, &bars.v_empty[vs], ((g / C::kVStages) & 1) ^ 1, abort_flag);
         if (!ok) break;
-        convert_tile<D, 128>(smem + C::kOffC + cs * C::kCodeBytes, smem + C::kOffV + vs * C::kTileBytes,
-                             p.q.len - (p.jb + j) * 128, tid);
+        convert_tile<D, 32 * C::kConvWarps>(smem + C::kOffC + cs * C::kCodeBytes, smem + C::kOffV + vs * C::kTileBytes,
+                                            p.q.len - (p.jb + j) * 128, tid);
         conv_arrive(&bars.v_full[vs], &bars.c_empty[cs], lane);
       }
     }
@@ -362,42 +345,32 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
         ok = __all_sync(0xffffffffu, mbar_wait(&bars.s_full[t], np & 1, abort_flag));
         if (!ok) break;
         tc_fence_after();
+        // S_t, with the maximum of each 32 columns from the load itself
+        uint32_t sr[4][32];
+        float cmax[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32_max(t_s + c * 32, sr[c], cmax[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_wait(sr[c], cmax[c]);
+        float mx = fmax3(fmax3(cmax[0], cmax[1], cmax[2]), cmax[3], -INFINITY);
         // only blocks that reach past the first row's last key, or past the request's, need masking
         const int kv0 = (p.jb + j) * 128;
-        const bool need_mask = (CAUSAL && kv0 + 127 > tok0 + off) || kv0 + 128 > p.q.len;
-        const int lim = (CAUSAL ? min(tok + off, p.q.len - 1) : p.q.len - 1) - kv0;  // keep column c iff c <= lim
-        // S_t, with the maximum of each 32 columns from the load itself. All of it stays in registers for the
-        // exponentials, except with E4M3 caches: 512 threads leave 128 registers each, so there S is loaded twice, 64
-        // columns at a time (held once, it spilled 600 bytes a thread).
-        constexpr int kHeld = FP8 ? 2 : 4;  // chunks of 32 columns in registers
-        uint32_t sr[kHeld][32];
-        float mx = -INFINITY;
+        if ((CAUSAL && kv0 + 127 > tok0 + off) || kv0 + 128 > p.q.len) {
+          const int lim = (CAUSAL ? min(tok + off, p.q.len - 1) : p.q.len - 1) - kv0;  // keep column c iff c <= lim
 #pragma unroll
-        for (int c0 = 0; c0 < 4; c0 += kHeld) {
-          float cmax[kHeld];
+          for (int c = 0; c < 128; ++c)
+            if (c > lim) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+          float mxc[8];  // row maximum over eight chains of 16 scores, then a tree
 #pragma unroll
-          for (int c = 0; c < kHeld; ++c) tmem_ld32_max(t_s + (c0 + c) * 32, sr[c], cmax[c]);
+          for (int i = 0; i < 8; ++i)
+            mxc[i] = fmaxf(__uint_as_float(sr[0][2 * i]), __uint_as_float(sr[0][2 * i + 1]));
 #pragma unroll
-          for (int c = 0; c < kHeld; ++c) tmem_ld_wait(sr[c], cmax[c]);
-          if (need_mask) {
-#pragma unroll
-            for (int c = 0; c < 32 * kHeld; ++c)
-              if (c0 * 32 + c > lim) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
-            float mxc[8];  // row maximum over eight chains, then a tree
+          for (int c = 16; c < 128; c += 16)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              mxc[i] = fmaxf(__uint_as_float(sr[0][2 * i]), __uint_as_float(sr[0][2 * i + 1]));
-#pragma unroll
-            for (int c = 16; c < 32 * kHeld; c += 16)
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                mxc[i] = fmax3(mxc[i], __uint_as_float(sr[c >> 5][(c & 31) + 2 * i]),
-                               __uint_as_float(sr[c >> 5][(c & 31) + 2 * i + 1]));
-            mx = fmaxf(mx, fmax3(fmax3(mxc[0], mxc[1], mxc[2]), fmax3(mxc[3], mxc[4], mxc[5]), fmaxf(mxc[6], mxc[7])));
-          } else {
-#pragma unroll
-            for (int c = 0; c < kHeld; c += 2) mx = fmax3(mx, cmax[c], cmax[c + 1]);
-          }
+              mxc[i] = fmax3(mxc[i], __uint_as_float(sr[c >> 5][(c & 31) + 2 * i]),
+                             __uint_as_float(sr[c >> 5][(c & 31) + 2 * i + 1]));
+          mx = fmax3(fmax3(mxc[0], mxc[1], mxc[2]), fmax3(mxc[3], mxc[4], mxc[5]), fmaxf(mxc[6], mxc[7]));
         }
         float alpha = 1.f;
         const float m_new = fmaxf(m_ref, mx * sl2);
@@ -412,22 +385,11 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
         const float2 scale2 = make_float2(sl2, sl2), shift2 = make_float2(-m_use, -m_use);
 #pragma unroll
         for (int ch = 0; ch < 4; ++ch) {  // P as 16-bit pairs over the first 64 columns of S_t
-          const int held = ch % kHeld;
-          if (FP8 && held == 0) {  // (P of the chunks before lies over S columns that have been read)
-            tmem_ld32(t_s + ch * 32, sr[0]);
-            tmem_ld32(t_s + ch * 32 + 32, sr[1]);
-            tmem_ld_wait(sr[0]);
-            tmem_ld_wait(sr[1]);
-            if (need_mask)
-#pragma unroll
-              for (int c = 0; c < 64; ++c)
-                if (ch * 32 + c > lim) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
-          }
           uint32_t pk[16];
 #pragma unroll
           for (int c = 0; c < 32; c += 2) {
             const float2 x =
-                ffma2(make_float2(__uint_as_float(sr[held][c]), __uint_as_float(sr[held][c + 1])), scale2, shift2);
+                ffma2(make_float2(__uint_as_float(sr[ch][c]), __uint_as_float(sr[ch][c + 1])), scale2, shift2);
             const float2 e = make_float2(ex2(x.x), ex2(x.y));
             sum4[(c >> 1) & 3] = fadd2(sum4[(c >> 1) & 3], e);
             pk[c >> 1] = FP8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);

@@ -103,28 +103,24 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t c) {
 }
 
 // A 128 x D tile of value codes (rows of D bytes) to an f16 tile, by NT threads;
-// rows from 'rows' on become zero. A thread takes 16 codes, two chunks; threads
-// of odd panels store theirs in the other order, so that the eight threads of
-// a quarter warp write to different banks.
+// rows from 'rows' on become zero. A thread takes 8 codes, one 16-byte chunk, at
+// a time: sixteen threads read 128 neighbouring bytes and a quarter warp writes
+// the eight chunks of one 128-byte row, so neither meets a bank twice.
 template <int D, int NT>
 __device__ __forceinline__ void convert_tile(const uint8_t* src, uint8_t* dst, int rows, int tid) {
-  constexpr int kPairs = D / 16, kRows = NT / kPairs;  // threads per row, rows per step
-  static_assert(kRows % 8 == 0, "a step must keep the swizzle");
-  const int c = tid % kPairs, r0 = tid / kPairs;
-  const bool odd = (c >> 2) & 1;
+  constexpr int kChunks = D / 8, kRows = NT / kChunks;  // chunks per row, rows per step
+  static_assert(kRows % 4 == 0, "two steps must keep the swizzle");
+  const int c = tid % kChunks, r0 = tid / kChunks;
   const uint32_t base = smem_u32(dst);
-  const uint32_t first = base + Tile<D>::chunk(r0, 2 * c + (odd ? 1 : 0));
-  const uint32_t second = base + Tile<D>::chunk(r0, 2 * c + (odd ? 0 : 1));
-#pragma unroll
+  // where this thread's chunk of the steps' rows lies: the swizzle goes by row % 8
+  const uint32_t even = base + Tile<D>::chunk(r0, c), odd = base + Tile<D>::chunk(r0 + kRows, c);
+#pragma unroll 8
   for (int it = 0; it < 128 / kRows; ++it) {
-    const uint4 w = *reinterpret_cast<const uint4*>(src + (it * NT + tid) * 16);
-    uint32_t x[4] = {odd ? w.z : w.x, odd ? w.w : w.y, odd ? w.x : w.z, odd ? w.y : w.w};
-    if (rows < 128 && r0 + it * kRows >= rows) x[0] = x[1] = x[2] = x[3] = 0u;  // code 0 is zero
-    constexpr uint32_t kStep = kRows / 8 * Tile<D>::kGroup;
-    st_shared_v4(first + it * kStep, e4m3x2_to_f16(x[0]), e4m3x2_to_f16(x[0] >> 16), e4m3x2_to_f16(x[1]),
-                 e4m3x2_to_f16(x[1] >> 16));
-    st_shared_v4(second + it * kStep, e4m3x2_to_f16(x[2]), e4m3x2_to_f16(x[2] >> 16), e4m3x2_to_f16(x[3]),
-                 e4m3x2_to_f16(x[3] >> 16));
+    uint2 w = *reinterpret_cast<const uint2*>(src + (it * NT + tid) * 8);
+    if (rows < 128 && r0 + it * kRows >= rows) w = make_uint2(0u, 0u);  // code 0 is zero
+    const uint32_t at = (it & 1) ? odd + (it >> 1) * (2 * kRows / 8) * Tile<D>::kGroup
+                                 : even + (it >> 1) * (2 * kRows / 8) * Tile<D>::kGroup;
+    st_shared_v4(at, e4m3x2_to_f16(w.x), e4m3x2_to_f16(w.x >> 16), e4m3x2_to_f16(w.y), e4m3x2_to_f16(w.y >> 16));
   }
 }
 
@@ -146,17 +142,17 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
 }
 
 // Q rows in a [panel][128 rows][128 bytes] swizzled tile from 64 bf16 to 64 hi
-// and 64 lo codes per 128-byte row, in place, by 128 threads, four neighbours
-// per row: rows [0, 32 * groups), and with COPIES rows 0 - 31 also to the other
-// three row quarters. ex[row] gets the biased exponent e of the row's largest
+// and 64 lo codes per 128-byte row, in place, by NT threads, four neighbours per
+// row: rows [0, rows) rounded up to NT / 4, and with COPIES rows 0 - 31 also to
+// the other three row quarters. ex[row] gets the biased exponent e of the row's largest
 // magnitude: the row was scaled by 2^(134 - e).
-template <int D, bool COPIES>
-__device__ __forceinline__ void convert_q(uint8_t* q, uint8_t* ex, int groups, int tid) {
+template <int D, bool COPIES, int NT>
+__device__ __forceinline__ void convert_q(uint8_t* q, uint8_t* ex, int rows, int tid) {
   constexpr int kPanels = D / 64;
   const int part = tid & 3;
   const uint32_t base = smem_u32(q);
-  for (int g = 0; g < groups; ++g) {
-    const int row = g * 32 + (tid >> 2);
+  for (int r0 = 0; r0 < rows; r0 += NT / 4) {
+    const int row = r0 + (tid >> 2);
     auto at = [&](int pn, int c) { return (uint32_t)(pn * 16384 + row * 128 + ((c ^ (row & 7)) << 4)); };
     uint32_t w[kPanels][8], big = 0;  // chunks 2 part and 2 part + 1 of each panel
 #pragma unroll
