@@ -38,10 +38,11 @@ struct CCfg {
   static constexpr int kTileBytes = kPanels * 16384;  // 128 rows, 16-bit
   static constexpr int kCodeBytes = 128 * D;          // 128 rows of codes
   static constexpr int kKBytes = FP8 ? kCodeBytes : kTileBytes;  // a key block: codes stay codes
-  static constexpr int kKStages = FP8 ? 3 : 2, kVStages = FP8 && D == 128 ? 2 : 3;
+  static constexpr int kKStages = FP8 ? 3 : 2, kVStages = (FP8 && D == 128) || kTiles == 1 ? 2 : 3;
   static constexpr int kCStages = FP8 ? 3 : 0;  // value codes on their way to f16
+  // Q tiles: one per half, or two for one half, so that the next tile's is there when this one ends
   static constexpr int kOffQ = 0;
-  static constexpr int kOffK = kOffQ + kTiles * kTileBytes;
+  static constexpr int kOffK = kOffQ + 2 * kTileBytes;
   static constexpr int kOffV = kOffK + kKStages * kKBytes;
   static constexpr int kOffC = kOffV + kVStages * kTileBytes;
   static constexpr int kOffBar = kOffC + kCStages * kCodeBytes;
@@ -49,7 +50,10 @@ struct CCfg {
   static_assert(kSmemBytes <= 232448 && (kCtasPerSm == 1 || 2 * (kSmemBytes + 1024) <= 233472), "shared memory");
   static constexpr uint32_t kTmemCols = kTiles == 2 ? 512u : 256u;
   __host__ __device__ static constexpr uint32_t col_s(int t) { return (uint32_t)t * 128u; }
-  __host__ __device__ static constexpr uint32_t col_o(int t) { return 128u * kTiles + (uint32_t)t * D; }
+  // P lies over the first 64 columns of its S; with one half in columns of its own, so that S of the next block can be
+  // made during the softmax
+  __host__ __device__ static constexpr uint32_t col_p(int t) { return kTiles == 2 ? col_s(t) : 128u; }
+  __host__ __device__ static constexpr uint32_t col_o(int t) { return kTiles == 2 ? 256u + (uint32_t)t * D : 192u; }
   static constexpr int kWarpTma = 4 * kTiles, kWarpMma = 4 * kTiles + 1;
   // With FP8 two converter warps: more than 384 threads leave a softmax thread, which holds 128 scores, no more than 128
   // registers. (Four of them and a warp for the values' copies, with S loaded twice: chunks of prompts at d = 128 333 us;
@@ -63,7 +67,8 @@ struct CBars {
   // after the next tile's Q is there, and one barrier would then have gone through both parities
   uint64_t q_raw[2], q_full[2][2], q_free[2];  // E4M3 caches: Q as loaded, as converted
   uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3], c_full[3], c_empty[3];
-  uint64_t s_full[2], p_full[2], o_done[2], o_free[2];
+  uint64_t s_full[2], p_full[2], o_done[2], o_free[2];  // (one half: o_done follows every P V)
+  uint64_t s_free;                                      // one half: S is in registers
   uint64_t teardown;
   uint32_t tmem_base;
   int abort;
@@ -123,6 +128,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
       mbar_init(&bars.c_full[s], 1);
       mbar_init(&bars.c_empty[s], C::kConvWarps);
     }
+    mbar_init(&bars.s_free, 128);
     mbar_init(&bars.teardown, 1);
     fence_mbar_init();
   }
@@ -154,13 +160,15 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     // test hook: without the first Q tile, the MMA warp's first wait expires
     bool withhold = a.test_fault == 1;
     auto load_q = [&](int t) {
-      if (!(ok = warp_wait(&bars.q_free[t], (nq[t] & 1) ^ 1, abort_flag))) return;
+      // the slot and its uses so far: half t's own, or the two in turn
+      const int s = C::kTiles == 2 ? t : nq[t] & 1, use = C::kTiles == 2 ? nq[t] : nq[t] >> 1;
+      if (!(ok = warp_wait(&bars.q_free[s], (use & 1) ^ 1, abort_flag))) return;
       if (!withhold) {
         if (elect_one()) {
           uint64_t* bar = FP8 ? &bars.q_raw[t] : &bars.q_full[t][nq[t] & 1];
           mbar_arrive_expect_tx(bar, q_bytes);
           for (int pn = 0; pn < C::kPanels; ++pn)
-            tma_load_3d(smem + C::kOffQ + t * C::kTileBytes + pn * 16384, &a.tm_q, bar, pn * 64,
+            tma_load_3d(smem + C::kOffQ + s * C::kTileBytes + pn * 16384, &a.tm_q, bar, pn * 64,
                         p.h * (a.Hq / a.Hkv), p.q.start + p.tok + t * a.tpt1);
         }
         __syncwarp();
@@ -197,8 +205,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     // Let every issued copy land before the CTA can exit (an earlier load's slot
     // was refilled only after its reader completed, so it has landed).
     for (int t = 0; t < C::kTiles; ++t)
-      if (nq[t] > 0) {
-        const int last = nq[t] - 1;
+      for (int last = max(0, nq[t] - (C::kTiles == 2 ? 1 : 2)); last < nq[t]; ++last) {
         mbar_wait_drain(FP8 ? &bars.q_raw[t] : &bars.q_full[t][last & 1], FP8 ? last & 1 : (last >> 1) & 1);
       }
     for (int x = max(0, nk - C::kKStages); x < nk; ++x)
@@ -206,78 +213,118 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     for (int x = max(0, nv - kS); x < nv; ++x) mbar_wait_drain(&v_full[x % kS], (x / kS) & 1);
   } else if (warp == C::kWarpMma) {
     // ------------------------------------------------------------ MMA issuer
-    // Per key block j and half t: O_t += P_t V_j, then at once S_t for block
-    // j + 1 (its columns are P_t's, which the products of one thread have read
-    // by then, as they execute in issue order).
     // P from TMEM, V MN-major
     constexpr uint32_t kIdO = FP8 ? idesc_f16(128, D, false, true) : idesc_bf16(128, D, false, true);
     const uint64_t dq0 = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
     const uint64_t dk0 = desc_keys<D, FP8>(smem + C::kOffK), dv0 = Tile<D>::desc_v(smem + C::kOffV);
-    auto issue_s = [&](int t, int st, bool last) {  // by the elected lane
-      issue_qk<D, FP8>(tmem + C::col_s(t), dq0 + ((uint32_t)(t * C::kTileBytes) >> 4),
+    // by the elected lane: S of half t from Q slot qs and key slot st
+    auto issue_s = [&](int t, int qs, int st, bool last) {
+      issue_qk<D, FP8>(tmem + C::col_s(t), dq0 + ((uint32_t)(qs * C::kTileBytes) >> 4),
                        dk0 + ((uint32_t)(st * C::kKBytes) >> 4));
       mma_commit(&bars.s_full[t]);
-      if (last) mma_commit(&bars.q_free[t]);  // the tile's last product to read Q
+      if (last) mma_commit(&bars.q_free[qs]);  // the tile's last product to read Q
+    };
+    auto issue_pv = [&](int t, int st, bool first) {
+      const uint32_t vo = (uint32_t)(st * C::kTileBytes) >> 4;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)  // P columns [8 kk, 8 kk + 8), V rows [16 kk, 16 kk + 16)
+        mma_ts(tmem + C::col_o(t), tmem + C::col_p(t) + kk * 8, dv0 + vo + Tile<D>::step_v(kk), kIdO,
+               (!first || kk > 0) ? 1u : 0u);
     };
     int g = 0, nq[2] = {0, 0}, np[2] = {0, 0};  // key blocks; tiles and P blocks of each half so far
     bool ok = true;
-    for (; ok && more; more = walk.step(a, p)) {
+    Piece next;
+    for (bool more_next; ok && more; p = next, more = more_next) {
       int nb[2];
       half_blocks<C::kTiles>(a, p, nb);
       const int nbm = max(nb[0], nb[1]);
-      if (nbm == 0) continue;
-      // S of the first block
-      ok = warp_wait(&bars.k_full[g % C::kKStages], (g / C::kKStages) & 1, abort_flag);
-      for (int t = 0; t < C::kTiles && ok; ++t)
-        if (nb[t] > 0) {
-          if (!(ok = warp_wait(&bars.q_full[t][nq[t] & 1], (nq[t] >> 1) & 1, abort_flag))) break;
-          tc_fence_after();
-          if (elect_one()) issue_s(t, g % C::kKStages, nb[t] == 1);
-          __syncwarp();
-        }
-      if (!ok) break;
-      if (elect_one()) mma_commit(&bars.k_empty[g % C::kKStages]);
-      __syncwarp();
-      for (int j = 0; j < nbm; ++j, ++g) {
-        const int s = g % C::kVStages;
-        const uint32_t ph = (g / C::kVStages) & 1;
-        const int v_last = j < nb[1] ? 1 : 0;  // the half whose PV reads V_j last
-        const int jn = j + 1, sn = (g + 1) % C::kKStages;
-        const bool k_next = jn < nbm;
-        ok = warp_wait3(&bars.v_full[s], ph, j < nb[0] ? &bars.p_full[0] : &bars.v_full[s],
-                        j < nb[0] ? (np[0] & 1) : ph, k_next ? &bars.k_full[sn] : &bars.v_full[s],
-                        k_next ? ((g + 1) / C::kKStages) & 1 : ph, abort_flag);
+      if (nbm > 0) {
+        // S of the first block
+        ok = warp_wait(&bars.k_full[g % C::kKStages], (g / C::kKStages) & 1, abort_flag);
+        if (C::kTiles == 1 && ok) ok = warp_wait(&bars.s_free, (g & 1) ^ 1, abort_flag);
+        for (int t = 0; t < C::kTiles && ok; ++t)
+          if (nb[t] > 0) {
+            if (!(ok = warp_wait(&bars.q_full[t][nq[t] & 1], (nq[t] >> 1) & 1, abort_flag))) break;
+            tc_fence_after();
+            if (elect_one()) issue_s(t, C::kTiles == 2 ? t : nq[0] & 1, g % C::kKStages, nb[t] == 1);
+            __syncwarp();
+          }
         if (!ok) break;
-        if constexpr (!FP8) {
-          const int end = p.q.len - (p.jb + j) * 128;
-          if (end < 128) zero_rows_from<D>(smem + C::kOffV + s * C::kTileBytes, end, lane);
+        if (elect_one()) mma_commit(&bars.k_empty[g % C::kKStages]);
+        __syncwarp();
+      }
+      // the next piece is worked out here, while the softmax has this one's first S (about 1400 cycles that would
+      // otherwise lie between this tile's last product and the next one's first)
+      next = p;
+      more_next = walk.step(a, next);
+      if constexpr (C::kTiles == 2) {
+        // Per key block j and half t: O_t += P_t V_j, then at once S_t for block j + 1 (its columns are P_t's, which the
+        // products of one thread have read by then, as they execute in issue order).
+        for (int j = 0; j < nbm; ++j, ++g) {
+          const int s = g % C::kVStages;
+          const uint32_t ph = (g / C::kVStages) & 1;
+          const int v_last = j < nb[1] ? 1 : 0;  // the half whose PV reads V_j last
+          const int jn = j + 1, sn = (g + 1) % C::kKStages;
+          const bool k_next = jn < nbm;
+          ok = warp_wait3(&bars.v_full[s], ph, j < nb[0] ? &bars.p_full[0] : &bars.v_full[s],
+                          j < nb[0] ? (np[0] & 1) : ph, k_next ? &bars.k_full[sn] : &bars.v_full[s],
+                          k_next ? ((g + 1) / C::kKStages) & 1 : ph, abort_flag);
+          if (!ok) break;
+          if constexpr (!FP8) {
+            const int end = p.q.len - (p.jb + j) * 128;
+            if (end < 128) zero_rows_from<D>(smem + C::kOffV + s * C::kTileBytes, end, lane);
+          }
+          for (int t = 0; t < 2; ++t) {
+            if (j < nb[t]) {
+              if (t == 1 && !(ok = warp_wait(&bars.p_full[1], np[1] & 1, abort_flag))) break;
+              // a tile's first PV overwrites O: the tile before has been read out
+              if (j == 0 && !(ok = warp_wait(&bars.o_free[t], (nq[t] & 1) ^ 1, abort_flag))) break;
+              tc_fence_after();
+              if (elect_one()) {
+                issue_pv(t, s, j == 0);
+                if (j == nb[t] - 1) mma_commit(&bars.o_done[t]);
+                if (t == v_last) mma_commit(&bars.v_empty[s]);
+              }
+              __syncwarp();
+              ++np[t];
+            }
+            if (jn < nb[t]) {
+              if (elect_one()) issue_s(t, t, sn, jn == nb[t] - 1);
+              __syncwarp();
+            }
+          }
+          if (!ok) break;
+          if (k_next) {
+            if (elect_one()) mma_commit(&bars.k_empty[sn]);
+            __syncwarp();
+          }
         }
-        for (int t = 0; t < C::kTiles; ++t) {
-          if (j < nb[t]) {
-            if (t == 1 && !(ok = warp_wait(&bars.p_full[1], np[1] & 1, abort_flag))) break;
-            // a tile's first PV overwrites O: the tile before has been read out
-            if (j == 0 && !(ok = warp_wait(&bars.o_free[t], (nq[t] & 1) ^ 1, abort_flag))) break;
+      } else {
+        // Per key block: S of the tile's next block as soon as the softmax has this one's in registers, then O += P V.
+        for (int j = 0; j < nbm; ++j, ++g) {
+          if (j + 1 < nbm) {
+            const int sn = (g + 1) % C::kKStages;
+            ok = warp_wait2(&bars.s_free, g & 1, &bars.k_full[sn], ((g + 1) / C::kKStages) & 1, abort_flag);
+            if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-              const uint32_t vo = (uint32_t)(s * C::kTileBytes) >> 4;
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)  // P columns [8 kk, 8 kk + 8), V rows [16 kk, 16 kk + 16)
-                mma_ts(tmem + C::col_o(t), tmem + C::col_s(t) + kk * 8, dv0 + vo + Tile<D>::step_v(kk), kIdO,
-                       (j > 0 || kk > 0) ? 1u : 0u);
-              if (j == nb[t] - 1) mma_commit(&bars.o_done[t]);
-              if (t == v_last) mma_commit(&bars.v_empty[s]);
+              issue_s(0, nq[0] & 1, sn, j + 2 == nbm);
+              mma_commit(&bars.k_empty[sn]);
             }
             __syncwarp();
-            ++np[t];
           }
-          if (jn < nb[t]) {
-            if (elect_one()) issue_s(t, sn, jn == nb[t] - 1);
-            __syncwarp();
+          const int s = g % C::kVStages;
+          ok = warp_wait2(&bars.p_full[0], g & 1, &bars.v_full[s], (g / C::kVStages) & 1, abort_flag);
+          if (ok && j == 0) ok = warp_wait(&bars.o_free[0], (nq[0] & 1) ^ 1, abort_flag);
+          if (!ok) break;
+          const int end = p.q.len - (p.jb + j) * 128;
+          if (end < 128) zero_rows_from<D>(smem + C::kOffV + s * C::kTileBytes, end, lane);
+          tc_fence_after();
+          if (elect_one()) {
+            issue_pv(0, s, j == 0);
+            mma_commit(&bars.o_done[0]);
+            mma_commit(&bars.v_empty[s]);
           }
-        }
-        if (!ok) break;
-        if (k_next) {
-          if (elect_one()) mma_commit(&bars.k_empty[sn]);
           __syncwarp();
         }
       }
@@ -321,6 +368,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     const int r = (warp & 3) * 32 + lane;  // row within the half = TMEM lane
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lane_off + C::col_s(t);
+    const uint32_t t_p = tmem + lane_off + C::col_p(t);
     const uint32_t t_o = tmem + lane_off + C::col_o(t);
     constexpr float kBias = FP8 ? kPBias : 0.f;
     const int G = a.Hq / a.Hkv, rt = r / G, rh = r - rt * G;  // this row's token within the half, and head
@@ -352,6 +400,10 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
         for (int c = 0; c < 4; ++c) tmem_ld32_max(t_s + c * 32, sr[c], cmax[c]);
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld_wait(sr[c], cmax[c]);
+        if constexpr (C::kTiles == 1) {
+          tc_fence_before();
+          mbar_arrive(&bars.s_free);  // S is in registers: the next block's S may overwrite it
+        }
         float mx = fmax3(fmax3(cmax[0], cmax[1], cmax[2]), cmax[3], -INFINITY);
         // only blocks that reach past the first row's last key, or past the request's, need masking
         const int kv0 = (p.jb + j) * 128;
@@ -383,19 +435,41 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
         float2 sum4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         const float m_use = (m_ref == -INFINITY ? 0.f : m_ref) - kBias;  // a row that has seen no key yet: P = 0
         const float2 scale2 = make_float2(sl2, sl2), shift2 = make_float2(-m_use, -m_use);
-#pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {  // P as 16-bit pairs over the first 64 columns of S_t
-          uint32_t pk[16];
+        auto chunk = [&](int ch) {  // P of 32 keys as 16-bit pairs, packed in place (pair c / 2 into word c / 2, already read)
 #pragma unroll
           for (int c = 0; c < 32; c += 2) {
             const float2 x =
                 ffma2(make_float2(__uint_as_float(sr[ch][c]), __uint_as_float(sr[ch][c + 1])), scale2, shift2);
             const float2 e = make_float2(ex2(x.x), ex2(x.y));
             sum4[(c >> 1) & 3] = fadd2(sum4[(c >> 1) & 3], e);
-            pk[c >> 1] = FP8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
+            sr[ch][c >> 1] = FP8 ? pack_f16x2(e.x, e.y) : pack_bf16x2(e.x, e.y);
           }
-          tmem_st16(t_s + 16 * ch, pk);
+        };
+        auto store = [&](int ch) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) pk[i] = sr[ch][i];
+          tmem_st16(t_p + 16 * ch, pk);
+        };
+        chunk(0);
+        if constexpr (C::kTiles == 2) {
+          store(0);
+          chunk(1);
+        } else {
+          // P and O are free once the P V before this one has completed (a tile's first block: the epilogue waited)
+          chunk(1);
+          if (j > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars.o_done[0], (np - 1) & 1, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+          }
+          store(0);
         }
+        store(1);
+        chunk(2);
+        store(2);
+        chunk(3);
+        store(3);
         const float2 sum = fadd2(fadd2(sum4[0], sum4[1]), fadd2(sum4[2], sum4[3]));
         l_sum = l_sum * alpha + (sum.x + sum.y);
         if (rescale) {
@@ -413,7 +487,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
         tc_fence_before();
         mbar_arrive(&bars.p_full[t]);
       }
-      if (ok && nb > 0) ok = mbar_wait(&bars.o_done[t], nq & 1, abort_flag);
+      if (ok && nb > 0) ok = mbar_wait(&bars.o_done[t], (C::kTiles == 2 ? nq : np - 1) & 1, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const bool seen = l_sum > 0.f;

@@ -80,12 +80,11 @@ __device__ __forceinline__ void zero_rows_from(uint8_t* tile, int row, int lane)
 
 // ---------------------------------------------------------------- E4M3 caches
 // Keys stay codes: S = Q K^T on 8-bit operands (kind::f8f6f4), with Q as two of
-// them, hi + lo. A bf16 value has 8 significant bits; hi = RN_e4m3(q) takes
-// four, and q - hi needs no more than the other four, so hi + lo = q exactly
-// unless lo falls below E4M3's smallest step. Each row of Q is first scaled by the
-// power of two that brings its largest magnitude into [128, 256) (undone in
-// the row's softmax scale), so what is lost stays below 2^-17 of that
-// magnitude. Two 8-bit products take as long as one 16-bit product.
+// them, hi + lo. A bf16 value has 8 significant bits; hi takes the upper
+// four, lo the lower four, so hi + lo = q exactly unless a part falls below
+// E4M3's normal range. Each row of Q is first scaled by the power of two that
+// brings its largest magnitude into [128, 256) (undone in the row's softmax
+// scale), so what is lost stays below 2^-16 of that magnitude. Two 8-bit products take as long as one 16-bit product.
 // Values become f16 operands, one conversion instruction for two of them, by
 // warps between the copy and the product; P enters that product as f16: 11 bits, times
 // 2^kPBias so that weights down to 2^-32 do not vanish (P stays below
@@ -124,21 +123,15 @@ __device__ __forceinline__ void convert_tile(const uint8_t* src, uint8_t* dst, i
   }
 }
 
-// hi and lo codes of two values (the low and high half of each result).
+// hi and lo codes of two values (the low half of each result): hi is the value cut to four significant bits, lo the rest.
 __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t& lo) {
-  uint32_t h, back;
-  asm("{\n .reg .b16 c;\n cvt.rn.satfinite.e4m3x2.f32 c, %3, %2;\n cvt.rn.f16x2.e4m3x2 %1, c;\n mov.b32 %0, {c, c};\n}\n"
-      : "=r"(h), "=r"(back)
-      : "f"(x), "f"(y));
-  float bx, by;
-  asm("{\n .reg .b16 p, q;\n mov.b32 {p, q}, %2;\n cvt.f32.f16 %0, p;\n cvt.f32.f16 %1, q;\n}\n"
-      : "=f"(bx), "=f"(by)
-      : "r"(back));
-  hi = h & 0xFFFFu;
-  asm("{\n .reg .b16 c;\n cvt.rn.satfinite.e4m3x2.f32 c, %2, %1;\n mov.b32 %0, {c, c};\n}\n"
+  const float hx = __uint_as_float(__float_as_uint(x) & 0xFFF00000u), hy = __uint_as_float(__float_as_uint(y) & 0xFFF00000u);
+  asm("{\n .reg .b16 c, z;\n cvt.rn.satfinite.e4m3x2.f32 c, %2, %1;\n mov.b16 z, 0;\n mov.b32 %0, {c, z};\n}\n"
+      : "=r"(hi)
+      : "f"(hx), "f"(hy));
+  asm("{\n .reg .b16 c, z;\n cvt.rn.satfinite.e4m3x2.f32 c, %2, %1;\n mov.b16 z, 0;\n mov.b32 %0, {c, z};\n}\n"
       : "=r"(lo)
-      : "f"(x - bx), "f"(y - by));
-  lo &= 0xFFFFu;
+      : "f"(x - hx), "f"(y - hy));
 }
 
 // Q rows in a [panel][128 rows][128 bytes] swizzled tile from 64 bf16 to 64 hi

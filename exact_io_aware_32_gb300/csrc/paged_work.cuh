@@ -28,15 +28,26 @@ struct Request {
   int start, n, len;  // packed rows [start, start + n), keys [0, len)
 };
 
-// Request r as the call takes it; bad: something was out of range.
-__device__ __forceinline__ Request request(const PagedArgs& a, int r, bool& bad) {
+// What memory says of request r.
+struct RawRequest {
+  int s0, s1, l;
+};
+__device__ __forceinline__ RawRequest load_request(const PagedArgs& a, int r) {
+  return {__ldg(a.query_start + r), __ldg(a.query_start + r + 1), __ldg(a.seq_lens + r)};
+}
+// The request as the call takes it; bad: something was out of range.
+__device__ __forceinline__ Request request(const PagedArgs& a, const RawRequest& raw, bool& bad) {
   Request q;
-  const int s0 = __ldg(a.query_start + r), s1 = __ldg(a.query_start + r + 1), l = __ldg(a.seq_lens + r);
+  const int s0 = raw.s0, s1 = raw.s1, l = raw.l;
   q.start = min(max(s0, 0), a.T);
   q.n = min(max(s1, q.start), a.T) - q.start;
   q.len = min(max(l, 0), a.max_keys);
   bad = q.start != s0 || q.start + q.n != s1 || q.len != l;
   return q;
+}
+
+__device__ __forceinline__ Request request(const PagedArgs& a, int r, bool& bad) {
+  return request(a, load_request(a, r), bad);
 }
 
 // Keys that the tokens before 'upto' (of the request's n) see.
@@ -204,15 +215,13 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, Range& out, long 
 // Walks a range's pieces in order; every warp role walks the same ones:
 // for (bool more = walk.begin(a, range, p); more; more = walk.step(a, p)).
 struct Walk {
-  Request q, next;           // 'next': the request after q, loaded ahead
+  Request q;
+  RawRequest next;           // the request after q, loaded ahead and not looked at before it is needed
   long long p0, p1, pos;     // pos: where the next tile begins
   long long last, last_len;  // the tile of the last step
   int r, h, i, nt, cost;
 
-  __device__ __forceinline__ void ahead(const PagedArgs& a) {
-    bool bad;
-    if (r + 1 < a.R) next = request(a, r + 1, bad);
-  }
+  __device__ __forceinline__ void ahead(const PagedArgs& a) { next = load_request(a, min(r + 1, a.R - 1)); }
   __device__ __forceinline__ void advance(const PagedArgs& a, long long len) {
     last = pos;
     last_len = len;
@@ -226,7 +235,8 @@ struct Walk {
         p1 = pos;  // past the last request
         return;
       }
-      q = next;
+      bool bad;
+      q = request(a, next, bad);
       ahead(a);
     } while (q.n == 0);
     nt = (q.n + a.tpt - 1) / a.tpt;
