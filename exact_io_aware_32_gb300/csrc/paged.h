@@ -64,6 +64,24 @@ struct PagedPlan {
   size_t parts_bytes, o_bytes, lse_bytes;  // of the workspace, each a multiple of 256
 };
 
+// Launches a kernel that begins with grid_wait (ptx.cuh) once its own set-up is done, so that the set-up and the launch
+// itself overlap the end of the kernel before it in the stream.
+template <class Args, class... More>
+cudaError_t launch_dependent(void (*kernel)(Args, More...), dim3 grid, int threads, int smem, cudaStream_t stream,
+                             const Args& args, const More&... more) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3((unsigned)threads);
+  c.dynamicSmemBytes = (size_t)smem;
+  c.stream = stream;
+  c.attrs = &attr;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, args, more...);
+}
+
 cudaError_t launch_plan(const PlanArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_store(const StoreArgs& a, int num_sms, cudaStream_t stream);
 PagedPlan plan_paged(int Hq, int Hkv, int d, int fp8, int max_new, int num_sms);

@@ -7,6 +7,7 @@
 
 #include "fa_internal.h"
 #include "paged.h"
+#include "ptx.cuh"
 
 namespace fa {
 namespace {
@@ -57,6 +58,8 @@ __global__ void __launch_bounds__(kPlanThreads) fa_paged_plan_kernel(const __gri
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int slices = gridDim.y, slice = blockIdx.y;
   const int r0 = blockIdx.x * a.group, r1 = min(a.R, r0 + a.group);
+  ptx::grid_release();
+  ptx::grid_wait();
   const int head = max(a.free_head ? *a.free_head : 0, 0);
   const long long avail = max(a.n_free - head, 0);
 
@@ -203,6 +206,8 @@ __global__ void __launch_bounds__(256) fa_paged_store_kernel(const __grid_consta
   const long long stride = value ? a.v_stride : a.k_stride;
   uint8_t* cache = static_cast<uint8_t*>(value ? a.v_cache : a.k_cache);
   const long long i0 = (long long)blockIdx.x * (256 * kStoreAhead) + threadIdx.x;
+  ptx::grid_release();
+  ptx::grid_wait();
   uint4 w[kStoreAhead][2];
   long long at[kStoreAhead];  // element offset in the cache, or -1
 #pragma unroll
@@ -256,8 +261,7 @@ cudaError_t launch_plan(const PlanArgs& args, int num_sms, cudaStream_t stream) 
   a.group = (a.R + groups - 1) / groups;
   const int n = (a.R + a.group - 1) / a.group;
   const int slices = std::max(1, std::min(2 * num_sms / n, (a.T / a.R + 255) / 256));
-  fa_paged_plan_kernel<<<dim3((unsigned)n, (unsigned)slices), kPlanThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(fa_paged_plan_kernel, dim3((unsigned)n, (unsigned)slices), kPlanThreads, 0, stream, a);
 }
 
 namespace {
@@ -265,8 +269,7 @@ template <bool FP8, int kAhead>
 cudaError_t launch_store_t(const StoreArgs& a, long long pieces, cudaStream_t stream) {
   const long long blocks = (pieces + 256 * kAhead - 1) / (256 * kAhead);
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  fa_paged_store_kernel<FP8, kAhead><<<dim3((unsigned)blocks, 2u), 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(fa_paged_store_kernel<FP8, kAhead>, dim3((unsigned)blocks, 2u), 256, 0, stream, a);
 }
 }  // namespace
 

@@ -567,8 +567,7 @@ cudaError_t launch(const PagedArgs& a, int ctas, cudaStream_t stream) {
   static std::atomic<unsigned long long> done[2];  // devices (a bit each) that know the kernel's shared memory
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes, done[a.causal]);
   if (e != cudaSuccess) return e;
-  kern<<<(unsigned)ctas, C::kThreads, C::kSmemBytes, stream>>>(a);
-  return cudaGetLastError();
+  return launch_dependent(kern, dim3((unsigned)ctas), C::kThreads, C::kSmemBytes, stream, a);
 }
 
 }  // namespace

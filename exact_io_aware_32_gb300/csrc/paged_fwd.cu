@@ -32,6 +32,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) fa_paged_join_kernel(const __
   __shared__ float s_acc[W > 1 ? kJoinWarps : 1][D];
   __shared__ float2 s_ml[W > 1 ? kJoinWarps : 1];
   const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % W;
+  ptx::grid_wait();
   const Parts mine = static_cast<const Parts*>(a.parts)[c];
   if (!mine.open) return;
   const int G = a.Hq / a.Hkv, rows1 = a.tpt1 * G;
@@ -103,12 +104,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) fa_paged_join_kernel(const __
 }
 
 template <int D>
-void launch_join(const PagedArgs& a, const PagedPlan& p, cudaStream_t stream) {
+cudaError_t launch_join(const PagedArgs& a, const PagedPlan& p, cudaStream_t stream) {
   // a block per row where tiles have few rows and maybe a part on every SM, else a warp per row
   const int rows = p.tpt * (a.Hq / a.Hkv), w = p.few ? kJoinWarps : 1;
   const dim3 grid((unsigned)p.ctas, (unsigned)((rows * w + kJoinWarps - 1) / kJoinWarps));
   auto kern = p.few ? fa_paged_join_kernel<D, kJoinWarps> : fa_paged_join_kernel<D, 1>;
-  kern<<<grid, 32 * kJoinWarps, 0, stream>>>(a, p.rows);
+  return launch_dependent(kern, grid, 32 * kJoinWarps, 0, stream, a, p.rows);
 }
 
 }  // namespace
@@ -166,11 +167,7 @@ cudaError_t launch_paged(PagedArgs a, const PagedPlan& p, cudaStream_t stream) {
   a.tpt1 = p.tpt1;
   cudaError_t e = p.few ? launch_paged_few(a, p.ctas, stream) : launch_paged_chunk(a, p.ctas, stream);
   if (e != cudaSuccess) return e;
-  if (a.d == 64)
-    launch_join<64>(a, p, stream);
-  else
-    launch_join<128>(a, p, stream);
-  return cudaGetLastError();
+  return a.d == 64 ? launch_join<64>(a, p, stream) : launch_join<128>(a, p, stream);
 }
 
 }  // namespace fa

@@ -144,6 +144,7 @@ __device__ __forceinline__ void convert_q(uint8_t* q, uint8_t* ex, int rows, int
   constexpr int kPanels = D / 64;
   const int part = tid & 3;
   const uint32_t base = smem_u32(q);
+#pragma unroll 2
   for (int r0 = 0; r0 < rows; r0 += NT / 4) {
     const int row = r0 + (tid >> 2);
     auto at = [&](int pn, int c) { return (uint32_t)(pn * 16384 + row * 128 + ((c ^ (row & 7)) << 4)); };

@@ -15,6 +15,7 @@
 
 #include "fa_internal.h"
 #include "paged.h"
+#include "ptx.cuh"
 
 namespace fa {
 namespace paged {
@@ -117,6 +118,8 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, Range& out, long 
   constexpr int kWarps = NT / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const bool alone = a.R <= 32 * kWarpRequests;  // by the first warp
+  ptx::grid_wait();  // nothing before this has read or written what other kernels do
+  ptx::grid_release();
   if (!alone || warp == 0) {
     const int threads = alone ? 32 : NT;
     const int seg = (a.R + threads - 1) / threads, r0 = min(a.R, tid * seg), r1 = min(a.R, r0 + seg);

@@ -411,6 +411,11 @@ __device__ __forceinline__ bool named_bar_and(uint32_t id, uint32_t nthreads, bo
       : "memory");
   return r != 0;
 }
+// Programmatic dependent launch: a kernel launched so may begin before the one
+// ahead of it in the stream has ended, and must not touch anything that one
+// reads or writes before grid_wait; grid_release lets the one behind it begin.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ bool elect_one() {
   uint32_t pred = 0;
   asm volatile(

@@ -19,9 +19,12 @@ there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
+
+import torch
 
 from . import build as _build
 
@@ -453,10 +456,11 @@ def fa_fwd_paged(q, q_stride: int, k_cache, v_cache, fp8: bool, descale_k: float
                                _addr(workspace), workspace_bytes, _stream(stream))
 
 
+_paged_workspace = functools.lru_cache(maxsize=1024)(fa_fwd_paged_workspace_bytes)  # (a function of its arguments alone)
+
+
 def _int32(name, x, shape, device):
     """Lengths, tables and slots as the library takes them: int32, contiguous, on ``device``; returns the address."""
-    import torch
-
     if x.dtype is not torch.int32 or x.shape != shape or x.device != device or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)} on {device}")
     return x.data_ptr()
@@ -464,8 +468,6 @@ def _int32(name, x, shape, device):
 
 def _packed(name, x, device):
     """Shape and token stride of a packed [T, heads, d] bf16 tensor whose rows of one token are contiguous."""
-    import torch
-
     if x.dtype is not torch.bfloat16 or x.device != device or x.dim() != 3:
         raise ValueError(f"{name} must be a bf16 tensor [T, heads, d] on {device}")
     T, H, d = x.shape
@@ -477,8 +479,6 @@ def _packed(name, x, device):
 
 def _cache(k_cache, v_cache):
     """Shape (num_pages, Hkv, page_size, d) of a cache pair, and whether it holds E4M3 codes."""
-    import torch
-
     dtype = k_cache.dtype
     fp8 = dtype is not torch.bfloat16
     if (fp8 and dtype is not torch.float8_e4m3fn and dtype is not torch.uint8) or k_cache.dim() != 4:
@@ -492,10 +492,8 @@ def _cache(k_cache, v_cache):
 def _elsewhere(device, stream):
     """None where a helper can allocate and launch as things stand: on the current device and its current stream. Else
     the context to enter first (another device, or the stream asked for, for which the tensors it allocates are made)."""
-    import torch
-
     if stream is None:
-        return None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        return None if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device)
     elif stream.device != device:
@@ -505,8 +503,6 @@ def _elsewhere(device, stream):
 
 def _current_stream(device) -> int:
     """The current stream's handle, without making a Stream object (a few microseconds)."""
-    import torch
-
     return torch._C._cuda_getCurrentRawStream(device.index)
 
 
@@ -516,8 +512,6 @@ def paged_plan(ctx_lens, new_lens, block_table, free_pages, page_size: int, num_
     int32 [1] tensor) into ``block_table`` [R, max_pages] (in place), and where each of the ``num_tokens`` packed
     rows goes. All tensors int32 on the GPU. Returns (query_start [R + 1], seq_lens [R], slots [num_tokens],
     pages_taken [1]); ``out``: the four tensors to write them into."""
-    import torch
-
     dev = ctx_lens.device
     if dev.type != "cuda" or ctx_lens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
         raise ValueError("expected CUDA tensors ctx_lens [R], block_table [R, max_pages], free_pages [n]")
@@ -536,9 +530,11 @@ def paged_plan(ctx_lens, new_lens, block_table, free_pages, page_size: int, num_
     start, lens, slots, taken = out
     taken_at = _int32("pages_taken", taken, (1,), dev)
     # an empty list has no address: any valid one will do, since none of its entries is read
-    st = load().fa_paged_plan(ctx, new, R, page_size, free if n_free else taken_at, n_free, head, table, max_pages,
-                              _int32("query_start", start, (R + 1,), dev), _int32("seq_lens", lens, (R,), dev),
-                              _int32("slots", slots, (num_tokens,), dev), num_tokens, taken_at, _current_stream(dev))
+    st = (_lib or load()).fa_paged_plan(ctx, new, R, page_size, free if n_free else taken_at, n_free, head, table,
+                                        max_pages, _int32("query_start", start, (R + 1,), dev),
+                                        _int32("seq_lens", lens, (R,), dev),
+                                        _int32("slots", slots, (num_tokens,), dev), num_tokens, taken_at,
+                                        _current_stream(dev))
     if st != FA_OK:
         raise FAError(st, "fa_paged_plan")
     return out
@@ -558,9 +554,9 @@ def paged_store(k, v, slots, k_cache, v_cache, descale_k: float = 1.0, descale_v
     vT, vh, vd, vs = _packed("v", v, dev)
     if kh != Hkv or vh != Hkv or kd != d or vd != d or vT != T:
         raise ValueError(f"k and v must be [T, {Hkv}, {d}], as the caches")
-    st = load().fa_paged_store(k.data_ptr(), v.data_ptr(), ks, vs, _int32("slots", slots, (T,), dev), T, Hkv, d,
-                               k_cache.data_ptr(), v_cache.data_ptr(), P, ps, fp8, descale_k, descale_v,
-                               _current_stream(dev))
+    st = (_lib or load()).fa_paged_store(k.data_ptr(), v.data_ptr(), ks, vs, _int32("slots", slots, (T,), dev), T, Hkv,
+                                         d, k_cache.data_ptr(), v_cache.data_ptr(), P, ps, fp8, descale_k, descale_v,
+                                         _current_stream(dev))
     if st != FA_OK:
         raise FAError(st, "fa_paged_store")
 
@@ -573,8 +569,6 @@ def forward_paged(q, k_cache, v_cache, block_table, query_start, seq_lens, max_n
     of block_table[r]. ``max_new``: the most new tokens a request has, if known (only speed depends on it). ``out``
     and ``lse`` are written in place if given, rows of no request left as they are (zeros in the ones allocated
     here). Returns (o [T, Hq, d], lse [T, Hq])."""
-    import torch
-
     P, Hkv, ps, d, fp8 = _cache(k_cache, v_cache)
     dev = k_cache.device
     context = _elsewhere(dev, stream)
@@ -601,15 +595,14 @@ def forward_paged(q, k_cache, v_cache, block_table, query_start, seq_lens, max_n
         lse = torch.zeros((T, Hq), dtype=torch.float32, device=dev)
     elif lse.dtype is not torch.float32 or lse.shape != (T, Hq) or lse.device != dev or not lse.is_contiguous():
         raise ValueError(f"lse must be a contiguous fp32 tensor [{T}, {Hq}] on {dev}")
-    lib = load()
     if workspace is None:
-        workspace = torch.empty(lib.fa_fwd_paged_workspace_bytes(T, R, Hq, Hkv, d, max_new), dtype=torch.uint8,
-                                device=dev)
+        workspace = torch.empty(_paged_workspace(T, R, Hq, Hkv, d, max_new), dtype=torch.uint8, device=dev)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    st = lib.fa_fwd_paged(q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), fp8, descale_k, descale_v, table,
-                          max_pages, start, lens, out.data_ptr(), lse.data_ptr(), T, R, Hq, Hkv, d, P, ps, max_new,
-                          scale, bool(causal), workspace.data_ptr(), workspace.nbytes, _current_stream(dev))
+    st = (_lib or load()).fa_fwd_paged(q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), fp8, descale_k,
+                                       descale_v, table, max_pages, start, lens, out.data_ptr(), lse.data_ptr(), T, R,
+                                       Hq, Hkv, d, P, ps, max_new, scale, bool(causal), workspace.data_ptr(),
+                                       workspace.nbytes, _current_stream(dev))
     if st != FA_OK:
         raise FAError(st, "fa_fwd_paged")
     return out, lse
