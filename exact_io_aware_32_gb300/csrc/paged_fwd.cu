@@ -16,100 +16,150 @@ using paged::Parts;
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// Joins the parts of one cut tile: with m = max_z lse_z, o = sum_z 2^(lse_z - m) o_z
+// Joining the parts of a cut tile: with m = max_z lse_z, o = sum_z 2^(lse_z - m) o_z
 // / sum_z 2^(lse_z - m). The CTA that opened the tile names it; the parts after
 // its own are the leading pieces of the CTAs that follow, in order, up to the one
-// that ends the tile: a fixed order, so the same bits every time. A block of
-// kJoinWarps warps takes kJoinWarps / W rows of a tile, W warps per row, each
-// every W-th part with kAhead parts' loads in flight. A part's O is read beside
-// its logsumexp, not after it: bound by latency, not by the few bytes.
+// that ends the tile: a fixed order, so the same bits every time. A part's O is
+// read beside its logsumexp, not after it (one that saw no key of the row wrote
+// none: weight 0, its O not looked at).
 constexpr int kJoinWarps = 8;
-template <int D, int W>
-__global__ void __launch_bounds__(32 * kJoinWarps) fa_paged_join_kernel(const __grid_constant__ PagedArgs a,
-                                                                        int rows_per_tile) {
-  constexpr int V = D / 32, kAhead = W > 1 ? 8 : 4;
-  using Vec = typename std::conditional<V == 4, float4, float2>::type;
-  __shared__ float s_acc[W > 1 ? kJoinWarps : 1][D];
-  __shared__ float2 s_ml[W > 1 ? kJoinWarps : 1];
-  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = warp % W;
-  ptx::grid_wait();
-  const Parts mine = static_cast<const Parts*>(a.parts)[c];
-  if (!mine.open) return;
-  const int G = a.Hq / a.Hkv, rows1 = a.tpt1 * G;
-  const int i = (int)blockIdx.y * (kJoinWarps / W) + warp / W;  // half * rows1 + token * G + head
-  const int half = i / rows1, rr = i - half * rows1, tk = rr / G, row = half * 128 + rr;
-  const int tok = mine.tok + half * a.tpt1 + tk;
-  const bool valid = half * a.tpt1 < a.tpt && tok < mine.n;
-  float m = -INFINITY, tot = 0.f, acc[V];
-#pragma unroll
-  for (int k = 0; k < V; ++k) acc[k] = 0.f;
-  if (valid)
-    for (int z0 = c + sub; z0 <= mine.end; z0 += kAhead * W) {
-      float l[kAhead];
-      Vec x[kAhead];
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const int z = z0 + u * W;
-        const long long slot = ((long long)z * 2 + (z == c ? 1 : 0)) * rows_per_tile + row;
-        l[u] = z <= mine.end ? a.part_lse[slot] : -INFINITY;
-        x[u] = z <= mine.end ? reinterpret_cast<const Vec*>(a.part_o + slot * D)[lane] : Vec{};
-      }
-      float m_new = m;
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) m_new = fmaxf(m_new, l[u]);
-      if (m_new == -INFINITY) continue;
-      const float back = exp2f(m - m_new);
-      tot *= back;
-#pragma unroll
-      for (int k = 0; k < V; ++k) acc[k] *= back;
-#pragma unroll
-      for (int u = 0; u < kAhead; ++u) {
-        const float w = exp2f(l[u] - m_new);
-        tot += w;
-        const float* xs = reinterpret_cast<const float*>(&x[u]);
-#pragma unroll
-        for (int k = 0; k < V; ++k) acc[k] += w > 0.f ? w * xs[k] : 0.f;  // (a part without keys wrote no O)
-      }
-      m = m_new;
-    }
-  if constexpr (W > 1) {
-#pragma unroll
-    for (int k = 0; k < V; ++k) s_acc[warp][lane * V + k] = acc[k];
-    if (lane == 0) s_ml[warp] = make_float2(m, tot);
-    __syncthreads();
-    if (sub != 0) return;
-    float top = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < W; ++w) top = fmaxf(top, s_ml[warp + w].x);
+
+template <int V>
+struct Joined {  // of one row, V columns per lane
+  float m, tot, acc[V];
+  __device__ __forceinline__ void clear() {
+    m = -INFINITY;
     tot = 0.f;
 #pragma unroll
     for (int k = 0; k < V; ++k) acc[k] = 0.f;
-#pragma unroll
-    for (int w = 0; w < W; ++w) {
-      const float2 s = s_ml[warp + w];
-      const float f = s.y > 0.f ? exp2f(s.x - top) : 0.f;
-      tot += f * s.y;
-#pragma unroll
-      for (int k = 0; k < V; ++k) acc[k] += f * s_acc[warp + w][lane * V + k];
-    }
-    m = top;
   }
-  if (!valid) return;
-  const float inv = tot > 0.f ? 1.f / tot : 0.f;
-  const long long out = (long long)(mine.start + tok) * a.Hq + mine.h * G + (rr - tk * G);
-  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.o) + (out * D + lane * V) * 2);
+  __device__ __forceinline__ void add(float l, const float* x) {  // a part: its logsumexp and O / l
+    if (l == -INFINITY) return;
+    const float m_new = fmaxf(m, l), back = exp2f(m - m_new), w = exp2f(l - m_new);
+    tot = tot * back + w;
 #pragma unroll
-  for (int k = 0; k < V / 2; ++k) dst[k] = ptx::pack_bf16x2(acc[2 * k] * inv, acc[2 * k + 1] * inv);
-  if (lane == 0) a.lse[out] = tot > 0.f ? (m + log2f(tot)) * 0.693147180559945309417f : -INFINITY;
+    for (int k = 0; k < V; ++k) acc[k] = acc[k] * back + w * x[k];
+    m = m_new;
+  }
+};
+
+template <int D>
+__device__ __forceinline__ void write_row(const PagedArgs& a, long long out, const Joined<D / 32>& s, int lane) {
+  constexpr int V = D / 32;
+  const float inv = s.tot > 0.f ? 1.f / s.tot : 0.f;
+  uint32_t w[V / 2];
+#pragma unroll
+  for (int k = 0; k < V / 2; ++k) w[k] = ptx::pack_bf16x2(s.acc[2 * k] * inv, s.acc[2 * k + 1] * inv);
+  uint8_t* dst = static_cast<uint8_t*>(a.o) + (out * D + lane * V) * 2;
+  if constexpr (V == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+  else
+    *reinterpret_cast<uint32_t*>(dst) = w[0];
+  if (lane == 0) a.lse[out] = s.tot > 0.f ? (s.m + log2f(s.tot)) * 0.693147180559945309417f : -INFINITY;
+}
+
+// Few rows (decoding): one long request's tile can have a part on every SM, so a
+// block takes one row, each warp every kJoinWarps-th part, eight in flight.
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) fa_paged_join_few_kernel(const __grid_constant__ PagedArgs a) {
+  constexpr int V = D / 32, kAhead = 8;
+  using Vec = typename std::conditional<V == 4, float4, float2>::type;
+  __shared__ float s_acc[kJoinWarps][D];
+  __shared__ float2 s_ml[kJoinWarps];
+  const int c = blockIdx.x, row = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  ptx::grid_wait();
+  const Parts mine = static_cast<const Parts*>(a.parts)[c];
+  if (!mine.open) return;
+  const int G = a.Hq / a.Hkv, tk = row / G, tok = mine.tok + tk;
+  if (tok >= mine.n) return;
+  Joined<V> s;
+  s.clear();
+  for (int z0 = c + warp; z0 <= mine.end; z0 += kAhead * kJoinWarps) {
+    float l[kAhead];
+    Vec x[kAhead];
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int z = z0 + u * kJoinWarps;
+      const long long slot = ((long long)z * 2 + (z == c ? 1 : 0)) * 32 + row;
+      l[u] = z <= mine.end ? a.part_lse[slot] : -INFINITY;
+      x[u] = z <= mine.end ? reinterpret_cast<const Vec*>(a.part_o + slot * D)[lane] : Vec{};
+    }
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) s.add(l[u], reinterpret_cast<const float*>(&x[u]));
+  }
+#pragma unroll
+  for (int k = 0; k < V; ++k) s_acc[warp][lane * V + k] = s.acc[k];
+  if (lane == 0) s_ml[warp] = make_float2(s.m, s.tot);
+  __syncthreads();
+  if (warp != 0) return;
+  float top = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, s_ml[w].x);
+  s.clear();
+  s.m = top;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    const float2 ml = s_ml[w];
+    const float f = ml.y > 0.f ? exp2f(ml.x - top) : 0.f;
+    s.tot += f * ml.y;
+#pragma unroll
+    for (int k = 0; k < V; ++k) s.acc[k] += f * s_acc[w][lane * V + k];
+  }
+  write_row<D>(a, (long long)(mine.start + tok) * a.Hq + mine.h * G + (row - tk * G), s, lane);
+}
+
+// Tiles of 128 or 256 rows, mostly of two parts: a warp per four rows. (A warp per
+// row spent its time on the rows' indices: 17 us for the 152 cut tiles of three
+// chunks of 1024 tokens, 32 heads of 128.)
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) fa_paged_join_chunk_kernel(const __grid_constant__ PagedArgs a,
+                                                                              int rows_per_tile) {
+  constexpr int V = D / 32, kRows = 4;
+  using Vec = typename std::conditional<V == 4, float4, float2>::type;
+  const int c = blockIdx.x, lane = threadIdx.x & 31;
+  const int row0 = ((int)blockIdx.y * kJoinWarps + (threadIdx.x >> 5)) * kRows;  // half * 128 + token * G + head
+  ptx::grid_wait();
+  const Parts mine = static_cast<const Parts*>(a.parts)[c];
+  if (!mine.open) return;
+  const int G = a.Hq / a.Hkv, half = row0 >> 7, r0 = row0 & 127, tk0 = r0 / G;
+  const int tok0 = mine.tok + half * a.tpt1;
+  const int rows = min(a.tpt1, mine.n - tok0) * G - r0;  // of this half from r0 on
+  if (rows <= 0) return;
+  Joined<V> s[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) s[i].clear();
+  for (int z = c; z <= mine.end; ++z) {
+    const long long slot = ((long long)z * 2 + (z == c ? 1 : 0)) * rows_per_tile + row0;
+    const float* lp = a.part_lse + slot;
+    const Vec* xp = reinterpret_cast<const Vec*>(a.part_o + slot * D) + lane;
+    float l[kRows];
+    Vec x[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      l[i] = i < rows ? lp[i] : -INFINITY;
+      x[i] = i < rows ? xp[i * 32] : Vec{};
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) s[i].add(l[i], reinterpret_cast<const float*>(&x[i]));
+  }
+  int tk = tk0, h = r0 - tk0 * G;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    if (i < rows) write_row<D>(a, (long long)(mine.start + tok0 + tk) * a.Hq + mine.h * G + h, s[i], lane);
+    if (++h == G) {
+      h = 0;
+      ++tk;
+    }
+  }
 }
 
 template <int D>
 cudaError_t launch_join(const PagedArgs& a, const PagedPlan& p, cudaStream_t stream) {
-  // a block per row where tiles have few rows and maybe a part on every SM, else a warp per row
-  const int rows = p.tpt * (a.Hq / a.Hkv), w = p.few ? kJoinWarps : 1;
-  const dim3 grid((unsigned)p.ctas, (unsigned)((rows * w + kJoinWarps - 1) / kJoinWarps));
-  auto kern = p.few ? fa_paged_join_kernel<D, kJoinWarps> : fa_paged_join_kernel<D, 1>;
-  return launch_dependent(kern, grid, 32 * kJoinWarps, 0, stream, a, p.rows);
+  if (p.few)
+    return launch_dependent(fa_paged_join_few_kernel<D>, dim3((unsigned)p.ctas, (unsigned)(p.tpt * (a.Hq / a.Hkv))),
+                            32 * kJoinWarps, 0, stream, a);
+  return launch_dependent(fa_paged_join_chunk_kernel<D>, dim3((unsigned)p.ctas, (unsigned)(p.rows / (4 * kJoinWarps))),
+                          32 * kJoinWarps, 0, stream, a, p.rows);
 }
 
 }  // namespace
