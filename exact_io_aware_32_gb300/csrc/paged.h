@@ -47,6 +47,7 @@ struct PagedArgs {
   // columns] with 128B swizzle, so that one copy brings every 64-column panel. E4M3: [page, head][row][d], keys
   // swizzled over their d-byte rows, values not.
   CUtensorMap tm_k, tm_v;
+  int n_min, n_max;         // new tokens of the requests to take
   int tpt;                  // tokens per tile
   int tpt1;                 // tokens per 128-row half of a tile (two halves at d = 128)
   void* parts;              // Parts per CTA, then the cut tiles' results, in the caller's workspace
@@ -55,13 +56,15 @@ struct PagedArgs {
   int test_fault;           // as in FwdArgs
 };
 
-// How a call is laid out (see launch_paged).
+// How one kernel of a call is laid out (see plan_paged).
 struct PagedPlan {
-  bool few;       // the kernel for at most 32 rows per tile
-  int ctas;       // persistent CTAs
-  int rows;       // rows of a tile
+  bool few;          // the kernel for at most 32 rows per tile
+  int ctas;          // persistent CTAs
+  int rows;          // rows of a tile
   int tpt, tpt1;
+  int n_min, n_max;  // the requests that are this kernel's: those with so many new tokens
   size_t parts_bytes, o_bytes, lse_bytes;  // of the workspace, each a multiple of 256
+  size_t bytes() const { return parts_bytes + o_bytes + lse_bytes; }
 };
 
 // Launches a kernel that begins with grid_wait (ptx.cuh) once its own set-up is done, so that the set-up and the launch
@@ -84,9 +87,12 @@ cudaError_t launch_dependent(void (*kernel)(Args, More...), dim3 grid, int threa
 
 cudaError_t launch_plan(const PlanArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_store(const StoreArgs& a, int num_sms, cudaStream_t stream);
-PagedPlan plan_paged(int Hq, int Hkv, int d, int fp8, int max_new, int num_sms);
-// Encodes the tensor maps too; cudaErrorInvalidValue if that fails.
-cudaError_t launch_paged(PagedArgs a, const PagedPlan& p, cudaStream_t stream);
+// The kernels of a call (1 or 2) in p[]; each may use the whole workspace, one after the other.
+int plan_paged(int T, int R, int Hq, int Hkv, int d, int fp8, int max_new, int max_keys, int num_sms,
+               PagedPlan (&p)[2]);
+// Encodes the tensor maps, gives the kernel its parts of the workspace and launches it with its join;
+// cudaErrorInvalidValue if the encoding fails.
+cudaError_t launch_paged(PagedArgs a, const PagedPlan& p, void* workspace, cudaStream_t stream);
 // The two kernels (paged_few.cu, paged_chunk.cu) and the join of cut tiles.
 cudaError_t launch_paged_few(const PagedArgs& a, int ctas, cudaStream_t stream);
 cudaError_t launch_paged_chunk(const PagedArgs& a, int ctas, cudaStream_t stream);

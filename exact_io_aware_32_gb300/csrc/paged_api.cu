@@ -125,8 +125,9 @@ size_t fa_fwd_paged_workspace_bytes(int T, int R, int Hq, int Hkv, int d, int ma
   if (check_paged(T, R, Hq, Hkv, d, max_new) != FA_OK) return 0;
   size_t most = 0;
   for (int fp8 = 0; fp8 < 2; ++fp8) {  // one size for both kinds of cache
-    const fa::PagedPlan p = fa::plan_paged(Hq, Hkv, d, fp8, max_new, kMaxSms);
-    most = std::max(most, p.parts_bytes + p.o_bytes + p.lse_bytes);
+    fa::PagedPlan p[2];
+    const int n = fa::plan_paged(T, R, Hq, Hkv, d, fp8, max_new, INT32_MAX, kMaxSms, p);  // (any table width)
+    for (int i = 0; i < n; ++i) most = std::max(most, p[i].bytes());
   }
   return most;
 }
@@ -177,13 +178,12 @@ int fa_fwd_paged(const void* q, long long q_stride, const void* k_cache, const v
   a.scale_log2 = scale_log2;
   a.o_scale = fp8 ? descale_v : 1.0f;
   a.max_keys = max_pages * page_size;
-  const fa::PagedPlan p = fa::plan_paged(Hq, Hkv, d, a.fp8, max_new, std::min(sms, kMaxSms));
-  char* w = static_cast<char*>(workspace);
-  a.parts = w;
-  a.part_o = reinterpret_cast<float*>(w + p.parts_bytes);
-  a.part_lse = reinterpret_cast<float*>(w + p.parts_bytes + p.o_bytes);
   a.test_fault = fa::take_test_fault();
-  return fa::launch_paged(a, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+  fa::PagedPlan p[2];
+  const int n = fa::plan_paged(T, R, Hq, Hkv, d, a.fp8, max_new, a.max_keys, std::min(sms, kMaxSms), p);
+  for (int i = 0; i < n; ++i)
+    if (fa::launch_paged(a, p[i], workspace, static_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_LAUNCH;
+  return FA_OK;
 }
 
 }  // extern "C"

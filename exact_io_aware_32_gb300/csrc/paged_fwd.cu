@@ -174,23 +174,51 @@ cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<unsigned long 
   return e;
 }
 
-PagedPlan plan_paged(int Hq, int Hkv, int d, int fp8, int max_new, int num_sms) {
-  const int G = Hq / Hkv;
+namespace {
+PagedPlan plan_kernel(bool few, int G, int d, int fp8, int max_new, int num_sms) {
   PagedPlan p;
-  // at most 32 rows a tile: the decoding kernel
-  p.few = (long long)G * max_new <= 32;
-  const int halves = p.few || (d == 64 && !fp8) ? 1 : 2;
-  p.rows = p.few ? 32 : 128 * halves;
-  p.tpt1 = std::min(max_new, (p.few ? 32 : 128) / G);
+  p.few = few;
+  const int halves = few || (d == 64 && !fp8) ? 1 : 2;
+  p.rows = few ? 32 : 128 * halves;
+  p.tpt1 = std::min(max_new, (few ? 32 : 128) / G);
   p.tpt = halves * p.tpt1;
-  p.ctas = num_sms * (!p.few && halves == 1 ? 2 : 1);
+  p.n_min = 0;
+  p.n_max = INT32_MAX;
+  p.ctas = num_sms * (!few && halves == 1 ? 2 : 1);
   p.parts_bytes = align256(sizeof(Parts) * p.ctas);
   p.o_bytes = align256((size_t)p.ctas * 2 * p.rows * d * sizeof(float));
   p.lse_bytes = align256((size_t)p.ctas * 2 * p.rows * sizeof(float));
   return p;
 }
+}  // namespace
 
-cudaError_t launch_paged(PagedArgs a, const PagedPlan& p, cudaStream_t stream) {
+int plan_paged(int T, int R, int Hq, int Hkv, int d, int fp8, int max_new, int max_keys, int num_sms,
+               PagedPlan (&p)[2]) {
+  const int G = Hq / Hkv;
+  // no request has more than 32 rows per key head: the decoding kernel alone
+  if ((long long)G * max_new <= 32) {
+    p[0] = plan_kernel(true, G, d, fp8, max_new, num_sms);
+    return 1;
+  }
+  p[0] = plan_kernel(false, G, d, fp8, max_new, num_sms);
+  // Requests of mostly far fewer tokens than the largest: decoding requests beside chunks of prompts. A tile of 128 rows
+  // for a few takes the chunk kernel 3000 cycles per key block and the decoding kernel a third of that, but a second
+  // kernel with its join costs 20 us, so each takes its requests only where there may be many keys. Measured with one
+  // chunk of 777 tokens beside 128 requests of up to 8192 keys, 32 heads over 8 of 128: E4M3 454 us in the chunk kernel,
+  // 326 us in both, bf16 453 and 422 us; beside 32 of up to 4096 keys, 16 heads over 4: 76 and 89 us, 64 and 87 us.
+  const long long keys = (long long)R * max_keys * Hkv;
+  if (G <= 32 && (long long)T * 2 < (long long)R * max_new && keys >= (fp8 ? 3000000ll : 8000000ll)) {
+    const int most = 32 / G;
+    p[1] = p[0];
+    p[1].n_min = most + 1;
+    p[0] = plan_kernel(true, G, d, fp8, most, num_sms);
+    p[0].n_max = most;
+    return 2;
+  }
+  return 1;
+}
+
+cudaError_t launch_paged(PagedArgs a, const PagedPlan& p, void* workspace, cudaStream_t stream) {
   const unsigned long long d = a.d, ps = 1ull << a.page_shift;
   const unsigned per = (unsigned)std::min(ps, 128ull);
   const unsigned long long heads = (unsigned long long)a.num_pages * a.Hkv;
@@ -213,8 +241,14 @@ cudaError_t launch_paged(PagedArgs a, const PagedPlan& p, cudaStream_t stream) {
   const unsigned q_box[3] = {64u, (unsigned)(a.Hq / a.Hkv), (unsigned)p.tpt1};
   ok = ok && encode_map(&a.tm_q, a.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, q_dims, q_strides, q_box, 128);
   if (!ok) return cudaErrorInvalidValue;
+  a.n_min = p.n_min;
+  a.n_max = p.n_max;
   a.tpt = p.tpt;
   a.tpt1 = p.tpt1;
+  char* w = static_cast<char*>(workspace);
+  a.parts = w;
+  a.part_o = reinterpret_cast<float*>(w + p.parts_bytes);
+  a.part_lse = reinterpret_cast<float*>(w + p.parts_bytes + p.o_bytes);
   cudaError_t e = p.few ? launch_paged_few(a, p.ctas, stream) : launch_paged_chunk(a, p.ctas, stream);
   if (e != cudaSuccess) return e;
   return a.d == 64 ? launch_join<64>(a, p, stream) : launch_join<128>(a, p, stream);

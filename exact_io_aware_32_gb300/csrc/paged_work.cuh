@@ -44,6 +44,7 @@ __device__ __forceinline__ Request request(const PagedArgs& a, const RawRequest&
   q.n = min(max(s1, q.start), a.T) - q.start;
   q.len = min(max(l, 0), a.max_keys);
   bad = q.start != s0 || q.start + q.n != s1 || q.len != l;
+  if (q.n < a.n_min || q.n > a.n_max) q.n = 0;  // the other kernel's
   return q;
 }
 
@@ -223,6 +224,7 @@ struct Walk {
   long long p0, p1, pos;     // pos: where the next tile begins
   long long last, last_len;  // the tile of the last step
   int r, h, i, nt, cost;
+  bool first;  // the range's first tile has not been left yet
 
   __device__ __forceinline__ void ahead(const PagedArgs& a) { next = load_request(a, min(r + 1, a.R - 1)); }
   __device__ __forceinline__ void advance(const PagedArgs& a, long long len) {
@@ -248,18 +250,23 @@ struct Walk {
     p = g.first;
     p0 = g.p0;
     p1 = g.p1;
-    pos = g.pos;
+    pos = last = g.pos;
+    last_len = g.len;
     q = p.q;
     r = p.r;
     h = p.h;
     i = g.i;
     nt = g.nt;
     cost = g.cost;
-    ahead(a);
-    advance(a, g.len);
+    first = true;
     return g.use ? true : step(a, p);
   }
   __device__ __forceinline__ bool step(const PagedArgs& a, Piece& p) {
+    if (first) {  // put off until here: the first piece's copies do not wait for it
+      first = false;
+      ahead(a);
+      advance(a, last_len);
+    }
     while (pos < p1) {
       const long long len = tile_keys(a, q, i) + cost;
       p.r = r;

@@ -182,6 +182,23 @@ def test_long_chunk_with_decoding_requests():
     check(c, o, lse)
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_mixed_batch_with_a_wide_table(d, fp8):
+    """A table wide enough for many keys: decoding requests and chunks go to kernels of their own."""
+    lens = [((i * 531) % 900, 1 + i % 3) for i in range(150)]
+    lens[7], lens[70], lens[71], lens[149] = (300, 290), (0, 9), (40, 0), (10, 200)
+    c = paged_ref.case(lens, 8, 2, d, 16, fp8=fp8, seed=31, width=2048, pad=3)
+    g = on_gpu(c)
+    lens = list(c["lens"])
+    lens[70], lens[3], lens[149] = 4, 0, 100  # rows that see no key in each
+    g["lens"] = ints(lens)
+    for causal in (True, False):
+        o, lse = attend(c, g, causal=causal, max_new=290)
+        parity.check_status()
+        check(c, o, lse, causal=causal, lens=lens)
+
+
 def test_many_requests():
     """More requests than threads of a block, most of them short, some empty."""
     lens = [((i * 37) % 90, (i * 7) % 3) for i in range(1500)]
