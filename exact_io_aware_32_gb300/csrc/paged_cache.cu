@@ -152,9 +152,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_paged_plan_kernel(const __gri
 // exact quotient would, ties among them. q = x / f to within one last place by
 // one correction of x * (1 / f); the remainder x - q f is exact and its sign
 // says on which side of q the quotient lies: an odd neighbour of q (or q, if
-// odd) on that side has no tie between it and the quotient. A correctly truncated division
-// instead made the store compute-bound: 58 us for 15523 tokens of 8 heads of
-// 128, 14 us of traffic.
+// odd) on that side has no tie between it and the quotient.
 __device__ __forceinline__ float quotient_odd(float x, float f, float inv) {
   const float q0 = x * inv;
   const float q = fmaf(fmaf(-q0, f, x), inv, q0);
@@ -165,7 +163,7 @@ __device__ __forceinline__ float quotient_odd(float x, float f, float inv) {
   return fabsf(q0) < 512.f ? y : q0;  // past the largest code, infinite or NaN: as it is
 }
 // Factors far from 1, where the remainder or 1 / f would leave the normal range: by division.
-__device__ __noinline__ float quotient_odd_far(float x, float f) {
+__device__ __forceinline__ float quotient_odd_far(float x, float f) {
   const float q = __fdiv_rz(x, f);
   const bool inexact = isfinite(q) && __fmaf_rn(-q, f, x) != 0.f;
   return inexact ? __uint_as_float(__float_as_uint(q) | 1u) : q;
@@ -187,67 +185,68 @@ struct Factor {
 };
 __device__ __forceinline__ Factor factor_of(float f) { return {f, 1.0f / f, f > 0x1p-100f && f < 0x1p100f}; }
 
-__device__ __forceinline__ uint32_t quantise4(uint32_t lo, uint32_t hi, const Factor& s) {
+// Four bf16 values as codes, each quotient rounded to odd first.
+__device__ __noinline__ uint32_t quantise4_exact(uint32_t lo, uint32_t hi, float f, float inv, bool near) {
   float x[4] = {__uint_as_float(lo << 16), __uint_as_float(lo & 0xffff0000u), __uint_as_float(hi << 16),
                 __uint_as_float(hi & 0xffff0000u)};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = s.near ? quotient_odd(x[i], s.f, s.inv) : quotient_odd_far(x[i], s.f);
+  for (int i = 0; i < 4; ++i) x[i] = near ? quotient_odd(x[i], f, inv) : quotient_odd_far(x[i], f);
   return e4m3x4(x[0], x[1], x[2], x[3]);
 }
 
-// 32 bytes of a row (16 elements) at a time, kStoreAhead of them in flight per
-// thread; keys in grid.y 0, values in 1. Neighbouring threads take neighbouring
-// pieces of one token, so reads and writes are whole rows of a head.
-template <bool FP8, int kStoreAhead>
+// The same. x * (1 / f) is within two last places of the quotient, so its code is the quotient's unless a tie of two
+// codes lies that near: the 20 bits that a normal code drops within two of 0x80000. Those, and values below the normal
+// codes, whose ties lie elsewhere, go the exact way. (All values that way: 27 us for 15523 tokens of 8 heads of 128,
+// bound by its 14 instructions a value; a correctly truncated division for each: 58 us.)
+__device__ __forceinline__ uint32_t quantise4(uint32_t lo, uint32_t hi, const Factor& s) {
+  const float x[4] = {__uint_as_float(lo << 16), __uint_as_float(lo & 0xffff0000u), __uint_as_float(hi << 16),
+                      __uint_as_float(hi & 0xffff0000u)};
+  float q[4];
+  bool exact = !s.near;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    q[i] = x[i] * s.inv;
+    exact |= ((__float_as_uint(q[i]) - 0x7FFFEu) & 0xFFFFFu) <= 4u || fabsf(q[i]) < 0x1p-6f;
+  }
+  return exact ? quantise4_exact(lo, hi, s.f, s.inv, s.near) : e4m3x4(q[0], q[1], q[2], q[3]);
+}
+
+// 32 bytes of a row (16 elements) per thread; keys in grid.y 0, values in 1.
+// Neighbouring threads take neighbouring pieces of one token, so reads and writes
+// are whole rows of a head. Bound by memory: 15523 tokens of 8 heads of 128 to
+// E4M3 in 18.3 us, 5.2 TB/s. (Two to four pieces per thread: 18.7 to 20.8 us,
+// fewer threads being resident.)
+template <bool FP8>
 __global__ void __launch_bounds__(256) fa_paged_store_kernel(const __grid_constant__ StoreArgs a) {
-  const unsigned per_row = (unsigned)a.d / 16u, per_token = (unsigned)a.Hkv * per_row;
+  const unsigned row_shift = a.d == 64 ? 2u : 3u, per_token = (unsigned)a.Hkv << row_shift;  // pieces of a row, of a token
   const bool value = blockIdx.y != 0;
-  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(value ? a.v : a.k);
-  const long long stride = value ? a.v_stride : a.k_stride;
-  uint8_t* cache = static_cast<uint8_t*>(value ? a.v_cache : a.k_cache);
-  const long long i0 = (long long)blockIdx.x * (256 * kStoreAhead) + threadIdx.x;
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   ptx::grid_release();
   ptx::grid_wait();
-  uint4 w[kStoreAhead][2];
-  long long at[kStoreAhead];  // element offset in the cache, or -1
-#pragma unroll
-  for (int u = 0; u < kStoreAhead; ++u) {
-    const long long i = i0 + u * 256;
-    long long t;
-    unsigned x;
-    if (i <= 0xFFFFFFFFll) {  // (64-bit division takes several times as long)
-      t = (unsigned)i / per_token;
-      x = (unsigned)i - (unsigned)t * per_token;
-    } else {
-      t = i / per_token;
-      x = (unsigned)(i - t * per_token);
-    }
-    at[u] = -1;
-    if (t >= a.T) continue;
-    const int slot = __ldg(a.slots + t);
-    const uint4* s = reinterpret_cast<const uint4*>(src + t * stride + (long long)x * 16);
-    w[u][0] = __ldg(s);
-    w[u][1] = __ldg(s + 1);
-    const int page = slot >> a.page_shift;
-    if (slot >= 0 && page >= a.num_pages) atomicOr(a.status, kStatusBadLength);
-    if (slot < 0 || page >= a.num_pages) continue;
-    const unsigned h = x / per_row, c = x - h * per_row;
-    const long long row = (((long long)page * a.Hkv + h) << a.page_shift) + (slot & ((1 << a.page_shift) - 1));
-    at[u] = row * a.d + c * 16;
+  const long long t = i <= 0xFFFFFFFFll ? (unsigned)i / per_token : i / per_token;  // (64-bit division takes far longer)
+  if (t >= a.T) return;
+  const unsigned x = (unsigned)(i - t * per_token), h = x >> row_shift, c = x & ((1u << row_shift) - 1u);
+  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(value ? a.v : a.k);
+  const uint4* s = reinterpret_cast<const uint4*>(src + t * (value ? a.v_stride : a.k_stride) + (long long)x * 16);
+  const int slot = __ldg(a.slots + t);
+  const uint4 w0 = __ldg(s), w1 = __ldg(s + 1);
+  if (slot < 0) return;
+  const int page = slot >> a.page_shift;
+  if (page >= a.num_pages) {
+    atomicOr(a.status, kStatusBadLength);
+    return;
   }
-  const Factor f = factor_of(FP8 ? (value ? a.descale_v : a.descale_k) : 1.0f);
-#pragma unroll
-  for (int u = 0; u < kStoreAhead; ++u) {
-    if (at[u] < 0) continue;
-    if constexpr (FP8) {
-      *reinterpret_cast<uint4*>(cache + at[u]) =
-          make_uint4(quantise4(w[u][0].x, w[u][0].y, f), quantise4(w[u][0].z, w[u][0].w, f),
-                     quantise4(w[u][1].x, w[u][1].y, f), quantise4(w[u][1].z, w[u][1].w, f));
-    } else {
-      uint4* d = reinterpret_cast<uint4*>(cache + at[u] * 2);
-      d[0] = w[u][0];
-      d[1] = w[u][1];
-    }
+  const long long row = (((long long)page * a.Hkv + h) << a.page_shift) + (slot & ((1 << a.page_shift) - 1));
+  const long long at = row * a.d + c * 16;
+  uint8_t* cache = static_cast<uint8_t*>(value ? a.v_cache : a.k_cache);
+  if constexpr (FP8) {
+    const Factor f = factor_of(value ? a.descale_v : a.descale_k);
+    *reinterpret_cast<uint4*>(cache + at) =
+        make_uint4(quantise4(w0.x, w0.y, f), quantise4(w0.z, w0.w, f), quantise4(w1.x, w1.y, f), quantise4(w1.z, w1.w, f));
+  } else {
+    uint4* d = reinterpret_cast<uint4*>(cache + at * 2);
+    d[0] = w0;
+    d[1] = w1;
   }
 }
 
@@ -264,22 +263,11 @@ cudaError_t launch_plan(const PlanArgs& args, int num_sms, cudaStream_t stream) 
   return launch_dependent(fa_paged_plan_kernel, dim3((unsigned)n, (unsigned)slices), kPlanThreads, 0, stream, a);
 }
 
-namespace {
-template <bool FP8, int kAhead>
-cudaError_t launch_store_t(const StoreArgs& a, long long pieces, cudaStream_t stream) {
-  const long long blocks = (pieces + 256 * kAhead - 1) / (256 * kAhead);
+cudaError_t launch_store(const StoreArgs& a, cudaStream_t stream) {
+  const long long blocks = ((long long)a.T * a.Hkv * (a.d / 16) + 255) / 256;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  return launch_dependent(fa_paged_store_kernel<FP8, kAhead>, dim3((unsigned)blocks, 2u), 256, 0, stream, a);
-}
-}  // namespace
-
-cudaError_t launch_store(const StoreArgs& a, int num_sms, cudaStream_t stream) {
-  const long long pieces = (long long)a.T * a.Hkv * (a.d / 16);
-  // One piece per thread while that fills the GPU no more than once (64 tokens of
-  // 8 heads of 128: 1.9 us, with four 3.6 us); past that four, for the bandwidth.
-  const bool few = pieces <= (long long)num_sms * 1024;
-  if (a.fp8) return few ? launch_store_t<true, 1>(a, pieces, stream) : launch_store_t<true, 4>(a, pieces, stream);
-  return few ? launch_store_t<false, 1>(a, pieces, stream) : launch_store_t<false, 4>(a, pieces, stream);
+  return launch_dependent(a.fp8 ? fa_paged_store_kernel<true> : fa_paged_store_kernel<false>,
+                          dim3((unsigned)blocks, 2u), 256, 0, stream, a);
 }
 
 }  // namespace fa
