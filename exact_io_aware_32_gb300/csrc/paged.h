@@ -48,6 +48,7 @@ struct PagedArgs {
   // swizzled over their d-byte rows, values not.
   CUtensorMap tm_k, tm_v;
   int n_min, n_max;         // new tokens of the requests to take
+  int whole, snap;          // key blocks of a tile that is not cut; of the smallest part of one that is
   int tpt;                  // tokens per tile
   int tpt1;                 // tokens per 128-row half of a tile (two halves at d = 128)
   void* parts;              // Parts per CTA, then the cut tiles' results, in the caller's workspace
@@ -61,7 +62,7 @@ struct PagedPlan {
   bool few;          // the kernel for at most 32 rows per tile
   int ctas;          // persistent CTAs
   int rows;          // rows of a tile
-  int tpt, tpt1;
+  int tpt, tpt1, whole, snap;
   int n_min, n_max;  // the requests that are this kernel's: those with so many new tokens
   size_t parts_bytes, o_bytes, lse_bytes;  // of the workspace, each a multiple of 256
   size_t bytes() const { return parts_bytes + o_bytes + lse_bytes; }

@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
                            smem + (FP8 ? C::kOffC + sv * C::kCodeBytes : C::kOffV + sv * C::kTileBytes), &v_full[sv]);
         nv = g + 1;
       }
-      note_piece(parts, p, walk, bars.range.per);
+      note_piece(a, parts, p, walk, bars.range.per);
     }
     if (lane == 0) static_cast<Parts*>(a.parts)[blockIdx.x] = parts;
     // Let every issued copy land before the CTA can exit (an earlier load's slot

@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     int g = 0, nk = 0;  // key blocks, and loads issued
     bool ok = true;
     for (; ok && more; more = walk.step(a, p)) {
-      note_piece(parts, p, walk, per);
+      note_piece(a, parts, p, walk, per);
       const int nb = p.je - p.jb;
       if (nb == 0) continue;
       int page = lane_page(a, p, p.jb, lane);

@@ -245,13 +245,14 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t (&v)[8], bo
 }
 
 // The part descriptor of this CTA, kept up by one thread as it walks the pieces.
-__device__ __forceinline__ void note_piece(Parts& s, const Piece& p, const Walk& walk, long long per) {
+__device__ __forceinline__ void note_piece(const PagedArgs& a, Parts& s, const Piece& p, const Walk& walk,
+                                           long long per) {
   if (p.jb > 0) {
     s.lead = 1;
     s.lead_ends = p.je == p.nb;
   } else if (p.je < p.nb) {
     s.open = 1;
-    s.end = walk.ender(per, p);
+    s.end = walk.ender(a, per, p);
     s.start = p.q.start;
     s.n = p.q.n;
     s.tok = p.tok;

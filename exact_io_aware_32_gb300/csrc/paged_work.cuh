@@ -20,9 +20,10 @@
 namespace fa {
 namespace paged {
 
-// Fixed part of a tile in keys, where the ranges are long enough for tiles to be whole.
+// Fixed part of a tile, in keys: what a CTA spends between two tiles (the last products, the epilogue, the next tile's Q
+// and first product) is about the time of two key blocks. Without it a CTA whose range holds a hundred requests of one
+// token each took 320 us beside others of 20.
 constexpr int kTileCost = 256;
-constexpr long long kLongRange = 1024;  // a range of so many keys counts kTileCost, a shorter one nothing
 constexpr long long kMinRange = 256;    // the shortest range worth a CTA: two blocks
 
 struct Request {
@@ -80,7 +81,7 @@ struct Range {
   long long p0, p1;    // this CTA's range of the row of tiles
   long long per;       // length of a range
   long long pos, len;  // the tile that holds p0: where it begins, and its length
-  int i, nt, cost;     // its number of its request's nt tiles; the fixed part of each tile
+  int i, nt;           // its number of its request's nt tiles
   int some, use;       // whether the range holds anything, and whether that tile's part of it is a piece
   Piece first;         // that part
 };
@@ -91,22 +92,30 @@ __device__ __forceinline__ long long divide(long long a, long long b) {
   return a / b;
 }
 
-// The block border nearest to x keys past a tile's fixed part.
-__device__ __forceinline__ int border(long long x, int cost, int nb) {
-  const long long b = (x - cost + 64) >> 7;
-  return (int)min(max(b, 0ll), (long long)nb);
+// Where a cut x keys past a tile's fixed part falls: the nearest block border, or the tile's end where fewer than a.snap
+// blocks would be left on that side.
+__device__ __forceinline__ int border(const PagedArgs& a, long long x, int nb) {
+  const long long b = (x - kTileCost + 64) >> 7;
+  return b < a.snap ? 0 : b > nb - a.snap ? nb : (int)b;
 }
 
-// The part of tile i of request q, at pos and len long, that lies in [p0, p1): p.jb, p.je, p.nb; whether it is a piece
-// (a tile that sees no key is one of the CTA where it begins).
-__device__ __forceinline__ bool cut(const PagedArgs& a, const Request& q, int i, long long pos, long long len, int cost,
-                                    long long p0, long long p1, Piece& p) {
+// The part of tile i of request q, at pos and len long, that lies in [p0, p1): p.jb, p.je, p.nb; whether it is a piece.
+// A tile of at most a.whole blocks is not cut but goes to the CTA that holds its middle (one that sees no key: its
+// beginning).
+__device__ __forceinline__ bool cut(const PagedArgs& a, const Request& q, int i, long long pos, long long len, long long p0,
+                                    long long p1, Piece& p) {
   p.q = q;
   p.tok = i * a.tpt;
   p.nb = (keys_seen(a, q, p.tok + a.tpt) + 127) >> 7;
-  p.jb = p0 <= pos ? 0 : border(p0 - pos, cost, p.nb);
-  p.je = p1 >= pos + len ? p.nb : border(p1 - pos, cost, p.nb);
-  return p.nb ? p.jb < p.je : p0 <= pos;
+  if (p.nb <= a.whole) {
+    p.jb = 0;
+    p.je = p.nb;
+    const long long at = p.nb ? pos + (len >> 1) : pos;
+    return p0 <= at && at < p1;
+  }
+  p.jb = p0 <= pos ? 0 : border(a, p0 - pos, p.nb);
+  p.je = p1 >= pos + len ? p.nb : border(a, p1 - pos, p.nb);
+  return p.jb < p.je;
 }
 
 // This CTA's range, by all NT threads of the block. What was set up in shared
@@ -167,17 +176,16 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, Range& out, long 
       }
     }
     const long long ctas = gridDim.x;
-    const int cost = all_k >= kLongRange * ctas ? kTileCost : 1;
-    const long long total = all_k + cost * all_t;
+    const long long total = all_k + kTileCost * all_t;
     const long long per = max(kMinRange, divide(total + ctas - 1, ctas));
     const long long p0 = per * blockIdx.x, p1 = min(total, p0 + per);
     if (tid == 0 && p0 >= total) out.some = 0;
-    long long pos = k0 + cost * t0;
-    if (p0 < total && pos <= p0 && p0 < pos + keys + cost * tiles) {  // one thread holds p0
+    long long pos = k0 + kTileCost * t0;
+    if (p0 < total && pos <= p0 && p0 < pos + keys + kTileCost * tiles) {  // one thread holds p0
       Request q = first;
       for (int r = r0;;) {
         const int nt = (q.n + a.tpt - 1) / a.tpt;
-        const long long head = keys_before(a, q, nt, nt) + (long long)cost * nt;
+        const long long head = keys_before(a, q, nt, nt) + (long long)kTileCost * nt;
         if (p0 >= pos + a.Hkv * head) {
           pos += a.Hkv * head;
           bool bad;
@@ -189,23 +197,22 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, Range& out, long 
         int lo = 0, hi = nt;  // the last tile that begins at or before p0
         while (hi - lo > 1) {
           const int mid = (lo + hi) >> 1;
-          if (keys_before(a, q, mid, nt) + (long long)cost * mid <= p0 - pos)
+          if (keys_before(a, q, mid, nt) + (long long)kTileCost * mid <= p0 - pos)
             lo = mid;
           else
             hi = mid;
         }
-        pos += keys_before(a, q, lo, nt) + (long long)cost * lo;
+        pos += keys_before(a, q, lo, nt) + (long long)kTileCost * lo;
         Range g;
         g.p0 = p0;
         g.p1 = p1;
         g.per = per;
         g.pos = pos;
-        g.len = tile_keys(a, q, lo) + cost;
+        g.len = tile_keys(a, q, lo) + kTileCost;
         g.i = lo;
         g.nt = nt;
-        g.cost = cost;
         g.some = 1;
-        g.use = cut(a, q, lo, pos, g.len, cost, p0, p1, g.first);
+        g.use = cut(a, q, lo, pos, g.len, p0, p1, g.first);
         g.first.r = r;
         g.first.h = h;
         out = g;
@@ -223,7 +230,7 @@ struct Walk {
   RawRequest next;           // the request after q, loaded ahead and not looked at before it is needed
   long long p0, p1, pos;     // pos: where the next tile begins
   long long last, last_len;  // the tile of the last step
-  int r, h, i, nt, cost;
+  int r, h, i, nt;
   bool first;  // the range's first tile has not been left yet
 
   __device__ __forceinline__ void ahead(const PagedArgs& a) { next = load_request(a, min(r + 1, a.R - 1)); }
@@ -257,7 +264,6 @@ struct Walk {
     h = p.h;
     i = g.i;
     nt = g.nt;
-    cost = g.cost;
     first = true;
     return g.use ? true : step(a, p);
   }
@@ -268,10 +274,10 @@ struct Walk {
       advance(a, last_len);
     }
     while (pos < p1) {
-      const long long len = tile_keys(a, q, i) + cost;
+      const long long len = tile_keys(a, q, i) + kTileCost;
       p.r = r;
       p.h = h;
-      const bool use = cut(a, q, i, pos, len, cost, p0, p1, p);
+      const bool use = cut(a, q, i, pos, len, p0, p1, p);
       advance(a, len);
       if (use) return true;
     }
@@ -279,9 +285,9 @@ struct Walk {
   }
   // The CTA that ends the tile of the last step, which this one opened: the last
   // whose range begins inside the tile and, its cut rounded to a block, before its last block's end.
-  __device__ __forceinline__ int ender(long long per, const Piece& p) const {
+  __device__ __forceinline__ int ender(const PagedArgs& a, long long per, const Piece& p) const {
     long long z = divide(last + last_len - 1, per);
-    while (border(z * per - last, cost, p.nb) >= p.nb) --z;
+    while (border(a, z * per - last, p.nb) >= p.nb) --z;
     return (int)z;
   }
 };

@@ -199,6 +199,17 @@ def test_mixed_batch_with_a_wide_table(d, fp8):
         check(c, o, lse, causal=causal, lens=lens)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+def test_tiles_around_the_shortest_cut(d):
+    """Tiles of 7 to 20 key blocks, few of them, so that every CTA's range ends somewhere inside one."""
+    for blocks in (7, 8, 9, 11, 12, 13, 16, 20):
+        c = paged_ref.case([(128 * blocks - 40, 36), (0, 1), (128 * blocks - 1, 1)], 2, 1, d, 128, seed=blocks)
+        g = on_gpu(c)
+        o, lse = attend(c, g, max_new=40)
+        parity.check_status()
+        check(c, o, lse)
+
+
 def test_many_requests():
     """More requests than threads of a block, most of them short, some empty."""
     lens = [((i * 37) % 90, (i * 7) % 3) for i in range(1500)]
