@@ -1,4 +1,5 @@
-"""Builds the CUDA library libfa.so in-tree with nvcc, for sm_103a only.
+"""Builds the CUDA library libfa.so in-tree with nvcc, for sm_103a only, and with the
+host compiler the small module through which torch tensors reach the paged cache's calls.
 
 Each translation unit is compiled in parallel; the objects are linked into
 ``exact_io_aware_32_gb300/_build/libfa.so`` with the CUDA runtime linked
@@ -8,9 +9,11 @@ driver's tensor-map encoder is looked up at run time).
 from __future__ import annotations
 
 import os
+import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
@@ -25,6 +28,26 @@ HEADERS = ["ptx.cuh", "block_order.cuh", "fa_internal.h", "philox.cuh", "paged.h
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-diag-suppress", "177"]
+
+
+def torch_module() -> str:
+    """Path of the module built against the torch that is installed (another torch is another file)."""
+    import torch
+
+    return os.path.join(BUILD, "_fa_torch." + re.sub(r"[^0-9A-Za-z]+", "_", torch.__version__) + ".so")
+
+
+def _torch_module_cmd(out: str) -> list:
+    import torch
+
+    root = os.path.dirname(torch.__file__)
+    inc = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")]
+    lib = os.path.join(root, "lib")
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"] + [f"-I{i}" for i in inc] +
+            [os.path.join(CSRC, "fa_torch.cpp"), "-o", out, f"-L{lib}", f"-Wl,-rpath,{lib}", "-ltorch_python",
+             "-ltorch_cpu", "-lc10_cuda", "-lc10"])
 
 
 def nvcc() -> str:
@@ -54,12 +77,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
             if verbose:
                 cmd.insert(1, "-Xptxas=-v")
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    module = torch_module()
+    module_tmp = module + f".tmp{os.getpid()}"
+    if force or _stale(module, [os.path.join(CSRC, "fa_torch.cpp")]):
+        procs.append(("fa_torch.cpp", subprocess.Popen(_torch_module_cmd(module_tmp), stdout=subprocess.PIPE,
+                                                       stderr=subprocess.STDOUT)))
     for src, p in procs:
         out, _ = p.communicate()
         if p.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}:\n{out.decode(errors='replace')}")
         if verbose and out:
             sys.stderr.write(out.decode(errors="replace"))
+    if os.path.exists(module_tmp):
+        os.replace(module_tmp, module)
     if force or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs + ["-Xcompiler", "-fPIC"]

@@ -19,7 +19,6 @@ there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
 import threading
@@ -456,54 +455,37 @@ def fa_fwd_paged(q, q_stride: int, k_cache, v_cache, fp8: bool, descale_k: float
                                _addr(workspace), workspace_bytes, _stream(stream))
 
 
-_paged_workspace = functools.lru_cache(maxsize=1024)(fa_fwd_paged_workspace_bytes)  # (a function of its arguments alone)
+_torch_module = None
 
 
-def _int32(name, x, shape, device):
-    """Lengths, tables and slots as the library takes them: int32, contiguous, on ``device``; returns the address."""
-    if x.dtype is not torch.int32 or x.shape != shape or x.device != device or not x.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {list(shape)} on {device}")
-    return x.data_ptr()
+def _paged():
+    """The module that checks torch tensors and makes the calls (built and loaded on first use)."""
+    global _torch_module
+    if _torch_module is None:
+        import importlib.machinery
+        import importlib.util
+
+        lib = load()
+        path = _build.torch_module()
+        if not os.path.exists(path):
+            _build.build()
+        loader = importlib.machinery.ExtensionFileLoader("_fa_torch", path)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_fa_torch", path, loader=loader))
+        loader.exec_module(module)
+        module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.fa_paged_plan, lib.fa_paged_store, lib.fa_fwd_paged_workspace_bytes, lib.fa_fwd_paged)))
+        _torch_module = module
+    return _torch_module
 
 
-def _packed(name, x, device):
-    """Shape and token stride of a packed [T, heads, d] bf16 tensor whose rows of one token are contiguous."""
-    if x.dtype is not torch.bfloat16 or x.device != device or x.dim() != 3:
-        raise ValueError(f"{name} must be a bf16 tensor [T, heads, d] on {device}")
-    T, H, d = x.shape
-    st, sh, sd = x.stride()
-    if (sd != 1 and d > 1) or (sh != d and H > 1):
-        raise ValueError(f"the rows of one token of {name} must be contiguous")
-    return T, H, d, st if T > 1 else H * d  # one token: its stride is not used
-
-
-def _cache(k_cache, v_cache):
-    """Shape (num_pages, Hkv, page_size, d) of a cache pair, and whether it holds E4M3 codes."""
-    dtype = k_cache.dtype
-    fp8 = dtype is not torch.bfloat16
-    if (fp8 and dtype is not torch.float8_e4m3fn and dtype is not torch.uint8) or k_cache.dim() != 4:
-        raise ValueError("the caches must be [num_pages, Hkv, page_size, d] tensors, bf16 or E4M3 codes")
-    if (v_cache.shape != k_cache.shape or v_cache.dtype is not dtype or v_cache.device != k_cache.device
-            or not k_cache.is_contiguous() or not v_cache.is_contiguous() or not k_cache.is_cuda):
-        raise ValueError("k_cache and v_cache must be contiguous CUDA tensors of one shape, type and device")
-    return *k_cache.shape, fp8
-
-
-def _elsewhere(device, stream):
-    """None where a helper can allocate and launch as things stand: on the current device and its current stream. Else
-    the context to enter first (another device, or the stream asked for, for which the tensors it allocates are made)."""
-    if stream is None:
-        return None if device.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
+def _on(stream, x):
+    """The context of a call on ``stream`` (a torch.cuda.Stream or a handle) of the device of tensor ``x``: the tensors it
+    allocates are that stream's."""
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=device)
-    elif stream.device != device:
-        raise ValueError(f"the stream must belong to {device}")
+        stream = torch.cuda.ExternalStream(stream, device=x.device)
+    elif stream.device != x.device:
+        raise ValueError(f"the stream must belong to {x.device}")
     return torch.cuda.stream(stream)
-
-
-def _current_stream(device) -> int:
-    """The current stream's handle, without making a Stream object (a few microseconds)."""
-    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def paged_plan(ctx_lens, new_lens, block_table, free_pages, page_size: int, num_tokens: int, free_head=None, out=None,
@@ -512,53 +494,26 @@ def paged_plan(ctx_lens, new_lens, block_table, free_pages, page_size: int, num_
     int32 [1] tensor) into ``block_table`` [R, max_pages] (in place), and where each of the ``num_tokens`` packed
     rows goes. All tensors int32 on the GPU. Returns (query_start [R + 1], seq_lens [R], slots [num_tokens],
     pages_taken [1]); ``out``: the four tensors to write them into."""
-    dev = ctx_lens.device
-    if dev.type != "cuda" or ctx_lens.dim() != 1 or block_table.dim() != 2 or free_pages.dim() != 1:
-        raise ValueError("expected CUDA tensors ctx_lens [R], block_table [R, max_pages], free_pages [n]")
-    context = _elsewhere(dev, stream)
-    if context is not None:
-        with context:
+    if stream is not None:
+        with _on(stream, ctx_lens):
             return paged_plan(ctx_lens, new_lens, block_table, free_pages, page_size, num_tokens, free_head, out)
-    (R, max_pages), n_free = block_table.shape, free_pages.shape[0]
-    ctx = _int32("ctx_lens", ctx_lens, (R,), dev)
-    new = _int32("new_lens", new_lens, (R,), dev)
-    free = _int32("free_pages", free_pages, (n_free,), dev)
-    table = _int32("block_table", block_table, (R, max_pages), dev)
-    head = None if free_head is None else _int32("free_head", free_head, (1,), dev)
-    if out is None:
-        out = tuple(torch.empty(n, dtype=torch.int32, device=dev) for n in (R + 1, R, num_tokens, 1))
-    start, lens, slots, taken = out
-    taken_at = _int32("pages_taken", taken, (1,), dev)
-    # an empty list has no address: any valid one will do, since none of its entries is read
-    st = (_lib or load()).fa_paged_plan(ctx, new, R, page_size, free if n_free else taken_at, n_free, head, table,
-                                        max_pages, _int32("query_start", start, (R + 1,), dev),
-                                        _int32("seq_lens", lens, (R,), dev),
-                                        _int32("slots", slots, (num_tokens,), dev), num_tokens, taken_at,
-                                        _current_stream(dev))
-    if st != FA_OK:
-        raise FAError(st, "fa_paged_plan")
-    return out
+    r = (_torch_module or _paged()).plan(ctx_lens, new_lens, block_table, free_pages, page_size, num_tokens, free_head,
+                                         None if out is None else tuple(out))
+    if type(r) is int:
+        raise FAError(r, "fa_paged_plan")
+    return r
 
 
 def paged_store(k, v, slots, k_cache, v_cache, descale_k: float = 1.0, descale_v: float = 1.0, stream=None) -> None:
     """Store the new tokens' k, v ([T, Hkv, d] bf16, slices of a projection's output allowed) into the caches
     [num_pages, Hkv, page_size, d] (bf16, or E4M3 codes of value / descale) at ``slots`` [T] (int32; negative:
     nowhere)."""
-    P, Hkv, ps, d, fp8 = _cache(k_cache, v_cache)
-    dev = k_cache.device
-    context = _elsewhere(dev, stream)
-    if context is not None:
-        with context:
+    if stream is not None:
+        with _on(stream, k_cache):
             return paged_store(k, v, slots, k_cache, v_cache, descale_k, descale_v)
-    T, kh, kd, ks = _packed("k", k, dev)
-    vT, vh, vd, vs = _packed("v", v, dev)
-    if kh != Hkv or vh != Hkv or kd != d or vd != d or vT != T:
-        raise ValueError(f"k and v must be [T, {Hkv}, {d}], as the caches")
-    st = (_lib or load()).fa_paged_store(k.data_ptr(), v.data_ptr(), ks, vs, _int32("slots", slots, (T,), dev), T, Hkv,
-                                         d, k_cache.data_ptr(), v_cache.data_ptr(), P, ps, fp8, descale_k, descale_v,
-                                         _current_stream(dev))
-    if st != FA_OK:
-        raise FAError(st, "fa_paged_store")
+    r = (_torch_module or _paged()).store(k, v, slots, k_cache, v_cache, descale_k, descale_v)
+    if r is not None:
+        raise FAError(r, "fa_paged_store")
 
 
 def forward_paged(q, k_cache, v_cache, block_table, query_start, seq_lens, max_new: int | None = None,
@@ -569,40 +524,12 @@ def forward_paged(q, k_cache, v_cache, block_table, query_start, seq_lens, max_n
     of block_table[r]. ``max_new``: the most new tokens a request has, if known (only speed depends on it). ``out``
     and ``lse`` are written in place if given, rows of no request left as they are (zeros in the ones allocated
     here). Returns (o [T, Hq, d], lse [T, Hq])."""
-    P, Hkv, ps, d, fp8 = _cache(k_cache, v_cache)
-    dev = k_cache.device
-    context = _elsewhere(dev, stream)
-    if context is not None:
-        with context:
+    if stream is not None:
+        with _on(stream, k_cache):
             return forward_paged(q, k_cache, v_cache, block_table, query_start, seq_lens, max_new, causal, scale,
                                  descale_k, descale_v, out, lse, workspace)
-    T, Hq, qd, qs = _packed("q", q, dev)
-    if qd != d or block_table.dim() != 2:
-        raise ValueError(f"expected q [T, Hq, {d}] and block_table [R, max_pages]")
-    R, max_pages = block_table.shape
-    table = _int32("block_table", block_table, (R, max_pages), dev)
-    start = _int32("query_start", query_start, (R + 1,), dev)
-    lens = _int32("seq_lens", seq_lens, (R,), dev)
-    if max_new is None:
-        max_new = T
-    if scale is None:
-        scale = 1.0 / math.sqrt(d)
-    if out is None:
-        out = torch.zeros((T, Hq, d), dtype=torch.bfloat16, device=dev)
-    elif out.dtype is not torch.bfloat16 or out.shape != q.shape or out.device != dev or not out.is_contiguous():
-        raise ValueError(f"out must be a contiguous bf16 tensor [{T}, {Hq}, {d}] on {dev}")
-    if lse is None:
-        lse = torch.zeros((T, Hq), dtype=torch.float32, device=dev)
-    elif lse.dtype is not torch.float32 or lse.shape != (T, Hq) or lse.device != dev or not lse.is_contiguous():
-        raise ValueError(f"lse must be a contiguous fp32 tensor [{T}, {Hq}] on {dev}")
-    if workspace is None:
-        workspace = torch.empty(_paged_workspace(T, R, Hq, Hkv, d, max_new), dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-    st = (_lib or load()).fa_fwd_paged(q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), fp8, descale_k,
-                                       descale_v, table, max_pages, start, lens, out.data_ptr(), lse.data_ptr(), T, R,
-                                       Hq, Hkv, d, P, ps, max_new, scale, bool(causal), workspace.data_ptr(),
-                                       workspace.nbytes, _current_stream(dev))
-    if st != FA_OK:
-        raise FAError(st, "fa_fwd_paged")
-    return out, lse
+    r = (_torch_module or _paged()).forward(q, k_cache, v_cache, block_table, query_start, seq_lens, max_new, causal,
+                                            scale, descale_k, descale_v, out, lse, workspace)
+    if type(r) is int:
+        raise FAError(r, "fa_fwd_paged")
+    return r
