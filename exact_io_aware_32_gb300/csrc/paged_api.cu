@@ -181,6 +181,11 @@ int fa_fwd_paged(const void* q, long long q_stride, const void* k_cache, const v
   a.test_fault = fa::take_test_fault();
   fa::PagedPlan p[2];
   const int n = fa::plan_paged(T, R, Hq, Hkv, d, a.fp8, max_new, a.max_keys, std::min(sms, kMaxSms), p);
+  // places in the row of tiles are 32-bit numbers of key blocks (paged_work.cuh)
+  for (int i = 0; i < n; ++i) {
+    const double tiles = ((double)T / p[i].tpt + R) * Hkv;
+    if (tiles * (a.max_keys / 128.0 + 4.0) >= 2147483648.0) return FA_ERR_INVALID_ARG;
+  }
   for (int i = 0; i < n; ++i)
     if (fa::launch_paged(a, p[i], workspace, static_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_LAUNCH;
   return FA_OK;

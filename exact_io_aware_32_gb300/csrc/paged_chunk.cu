@@ -73,7 +73,7 @@ struct CBars {
   uint32_t tmem_base;
   int abort;
   Range range;
-  long long sums[2][16];
+  int sums[16];
 };
 static_assert(sizeof(CBars) <= 1024, "barriers exceed their shared memory");
 struct CBars8 : CBars {
@@ -137,7 +137,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     tmem_relinquish();
   }
   tc_fence_before();
-  find_range<C::kThreads>(a, bars.range, reinterpret_cast<long long(&)[2][C::kThreads / 32]>(bars.sums));
+  find_range<C::kThreads>(a, bars.range, reinterpret_cast<int(&)[C::kThreads / 32]>(bars.sums));
   tc_fence_after();
   const uint32_t tmem = bars.tmem_base;
   if (!bars.range.some) {  // uniform: nothing has been issued

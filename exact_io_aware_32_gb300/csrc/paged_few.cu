@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
   // in the join's place, which is not in use yet: the range and its sums; behind the barriers: the exponents of Q's row
   // scales (E4M3 caches), of this tile and the two before
   Range& range = *reinterpret_cast<Range*>(smem + C::kOffJoin);
-  auto& sums = *reinterpret_cast<long long(*)[2][C::kThreads / 32]>(smem + C::kOffJoin + 256);
+  auto& sums = *reinterpret_cast<int(*)[C::kThreads / 32]>(smem + C::kOffJoin + 256);
   auto& q_ex = *reinterpret_cast<uint8_t(*)[3][32]>(smem + C::kOffBar + 400);
   static_assert(sizeof(Range) <= 256, "the sums follow the range");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
   Walk walk;
   Piece p;
   bool more = walk.begin(a, range, p);
-  const long long per = range.per;
+  const int per = range.per;
   __syncthreads();  // all have read the range: the join may write there
   if (warp == C::kWarpTmaK) {
     // ------------------------------------------------------------ keys

@@ -246,7 +246,7 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t (&v)[8], bo
 
 // The part descriptor of this CTA, kept up by one thread as it walks the pieces.
 __device__ __forceinline__ void note_piece(const PagedArgs& a, Parts& s, const Piece& p, const Walk& walk,
-                                           long long per) {
+                                           int per) {
   if (p.jb > 0) {
     s.lead = 1;
     s.lead_ends = p.je == p.nb;

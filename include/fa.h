@@ -348,6 +348,10 @@ FA_API int fa_paged_store(const void* k, const void* v, long long k_stride, long
  * seq_len past max_pages pages is cut, a negative one is 0, query_start is
  * cut into [0, T], and a request that ends before it starts has no rows; each
  * is reported by fa_device_status as FA_ERR_INVALID_ARG.
+ * The largest call: with tiles = (T / tokens per tile + R) Hkv (a tile is 32
+ * or 128 rows of a key head, 256 at d = 128), tiles times the table's width
+ * in blocks of 128 keys must stay below 2^31 (seconds of work), else
+ * FA_ERR_INVALID_ARG.
  * Results do not depend on what else is in the batch beyond rounding (the
  * keys of a request are split over the GPU by the lengths of all); repeated
  * calls give identical bits.
