@@ -17,7 +17,8 @@
 //
 // Warp roles: a softmax warpgroup per 128-row half, the TMA warp, the MMA warp,
 // and with E4M3 caches two warps that turn value codes into f16 operands (TMA ->
-// ring of codes -> converters -> V ring) and Q into its two 8-bit parts.
+// ring of codes -> converters -> V ring); Q's rows become their two 8-bit parts by
+// the softmax threads that own them (by the converters that took 5500 cycles a half).
 #include "paged_pipe.cuh"
 
 namespace fa {
@@ -46,7 +47,7 @@ struct CCfg {
   static constexpr int kOffV = kOffK + kKStages * kKBytes;
   static constexpr int kOffC = kOffV + kVStages * kTileBytes;
   static constexpr int kOffBar = kOffC + kCStages * kCodeBytes;
-  static constexpr int kSmemBytes = kOffBar + (FP8 ? 1536 : 1024) + 1024;  // barriers, alignment slack
+  static constexpr int kSmemBytes = kOffBar + 1024 + 1024;  // barriers, alignment slack
   static_assert(kSmemBytes <= 232448 && (kCtasPerSm == 1 || 2 * (kSmemBytes + 1024) <= 233472), "shared memory");
   static constexpr uint32_t kTmemCols = kTiles == 2 ? 512u : 256u;
   __host__ __device__ static constexpr uint32_t col_s(int t) { return (uint32_t)t * 128u; }
@@ -63,9 +64,7 @@ struct CCfg {
 };
 
 struct CBars {
-  // by half. q_full of a half's tile n is q_full[t][n & 1]: with E4M3 caches the softmax waits for it too, maybe only
-  // after the next tile's Q is there, and one barrier would then have gone through both parities
-  uint64_t q_raw[2], q_full[2][2], q_free[2];  // E4M3 caches: Q as loaded, as converted
+  uint64_t q_raw[2], q_full[2][2], q_free[2];  // by half (q_full: and tile in turn); E4M3 caches: Q as loaded, as converted
   uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3], c_full[3], c_empty[3];
   uint64_t s_full[2], p_full[2], o_done[2], o_free[2];  // (one half: o_done follows every P V)
   uint64_t s_free;                                      // one half: S is in registers
@@ -76,10 +75,6 @@ struct CBars {
   int sums[16];
 };
 static_assert(sizeof(CBars) <= 1024, "barriers exceed their shared memory");
-struct CBars8 : CBars {
-  uint8_t q_ex[2][2][128];  // the exponents of Q's row scales, by tile (this one and the one before), half and row
-};
-static_assert(sizeof(CBars8) <= 1536, "barriers exceed their shared memory");
 
 // Key blocks that each 128-row half sees of a piece (nb[t] from p.jb on).
 template <int kTiles>
@@ -98,7 +93,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
   using C = CCfg<D, FP8>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  CBars8& bars = *reinterpret_cast<CBars8*>(smem + C::kOffBar);  // (q_ex only with E4M3 caches)
+  CBars& bars = *reinterpret_cast<CBars*>(smem + C::kOffBar);
   volatile int* abort_flag = &bars.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -112,8 +107,8 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     bars.abort = 0;
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars.q_raw[s], 1);
-      mbar_init(&bars.q_full[s][0], FP8 ? C::kConvWarps : 1);
-      mbar_init(&bars.q_full[s][1], FP8 ? C::kConvWarps : 1);
+      mbar_init(&bars.q_full[s][0], FP8 ? 4 : 1);
+      mbar_init(&bars.q_full[s][1], FP8 ? 4 : 1);
       mbar_init(&bars.q_free[s], 1);
       mbar_init(&bars.s_full[s], 1);
       mbar_init(&bars.p_full[s], 128);
@@ -337,22 +332,12 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     // ------------------------------------------------------------ converters
     const int tid = threadIdx.x - C::kWarpConv * 32;
     constexpr int kCS = FP8 ? C::kCStages : 1;
-    const int G = a.Hq / a.Hkv;
-    int g = 0, nq[2] = {0, 0};
+    int g = 0;
     bool ok = true;
-    auto convert_half = [&](int t) {  // Q of half t, in the order in which it was loaded
-      if (!(ok = warp_wait(&bars.q_raw[t], nq[t] & 1, abort_flag))) return;
-      const int rows = min(a.tpt1, p.q.n - p.tok - t * a.tpt1) * G;
-      convert_q<D, false, 32 * C::kConvWarps>(smem + C::kOffQ + t * C::kTileBytes, bars.q_ex[nq[t] & 1][t], rows, tid);
-      conv_arrive(&bars.q_full[t][nq[t] & 1], nullptr, lane);
-      ++nq[t];
-    };
     for (; ok && more; more = walk.step(a, p)) {
       int nb[2];
       half_blocks<C::kTiles>(a, p, nb);
       const int nbm = max(nb[0], nb[1]);
-      if (nb[0] > 0) convert_half(0);
-      if (ok && nb[1] > 0) convert_half(1);
       for (int j = 0; ok && j < nbm; ++j, ++g) {
         const int vs = g % C::kVStages, cs = g % kCS;
         ok = warp_wait2(&bars.c_full[cs], (g / kCS) & 1, &bars.v_empty[vs], ((g / C::kVStages) & 1) ^ 1, abort_flag);
@@ -383,9 +368,10 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
       const int off = p.q.len - p.q.n;  // causal: token i sees keys 0 .. i + off
       const bool valid = rt < a.tpt1 && tok < p.q.n;
       float sl2 = a.scale_log2;
-      if (FP8 && nb > 0) {  // (their place is written again two tiles on, after the products of this one's P)
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars.q_full[t][nq & 1], (nq >> 1) & 1, abort_flag)))) break;
-        sl2 *= unscale(bars.q_ex[nq & 1][t][r]);
+      if (FP8 && nb > 0) {  // this thread's row of Q to its two 8-bit parts
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars.q_raw[t], nq & 1, abort_flag)))) break;
+        sl2 *= unscale(convert_row<D>(smem + C::kOffQ + t * C::kTileBytes, r));
+        conv_arrive(&bars.q_full[t][nq & 1], nullptr, lane);
       }
       float m_ref = -INFINITY;  // exponent reference, log2 units of scaled scores
       float l_sum = 0.f;        // sum of 2^(s * sl2 - m_ref) over the keys seen so far

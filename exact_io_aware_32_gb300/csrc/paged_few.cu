@@ -268,7 +268,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
       if (p.je > p.jb) {
         if (tid < 128) {  // Q, by four of the warps
           if (!(ok = warp_wait(&bars.q_raw, n & 1, abort_flag))) break;
-          convert_q<D, true, 128>(smem + C::kOffQ, q_ex[n % 3], 32, tid);
+          convert_q<D>(smem + C::kOffQ, q_ex[n % 3], tid);
           conv_arrive(&bars.q_full[n % 3], nullptr, lane);
         }
         ++n;

@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) fa_paged_join_few_kernel(cons
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) fa_paged_join_chunk_kernel(const __grid_constant__ PagedArgs a,
                                                                               int rows_per_tile) {
-  constexpr int V = D / 32, kRows = 4;
+  constexpr int V = D / 32, kRows = 4, kAhead = 3;
   using Vec = typename std::conditional<V == 4, float4, float2>::type;
   const int c = blockIdx.x, lane = threadIdx.x & 31;
   const int row0 = ((int)blockIdx.y * kJoinWarps + (threadIdx.x >> 5)) * kRows;  // half * 128 + token * G + head
@@ -128,19 +128,26 @@ __global__ void __launch_bounds__(32 * kJoinWarps) fa_paged_join_chunk_kernel(co
   Joined<V> s[kRows];
 #pragma unroll
   for (int i = 0; i < kRows; ++i) s[i].clear();
-  for (int z = c; z <= mine.end; ++z) {
-    const long long slot = ((long long)z * 2 + (z == c ? 1 : 0)) * rows_per_tile + row0;
-    const float* lp = a.part_lse + slot;
-    const Vec* xp = reinterpret_cast<const Vec*>(a.part_o + slot * D) + lane;
-    float l[kRows];
-    Vec x[kRows];
+  for (int z0 = c; z0 <= mine.end; z0 += kAhead) {
+    float l[kAhead][kRows];
+    Vec x[kAhead][kRows];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      l[i] = i < rows ? lp[i] : -INFINITY;
-      x[i] = i < rows ? xp[i * 32] : Vec{};
+    for (int u = 0; u < kAhead; ++u) {
+      const int z = z0 + u;
+      const long long slot = ((long long)z * 2 + (z == c ? 1 : 0)) * rows_per_tile + row0;
+      const float* lp = a.part_lse + slot;
+      const Vec* xp = reinterpret_cast<const Vec*>(a.part_o + slot * D) + lane;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const bool there = i < rows && z <= mine.end;
+        l[u][i] = there ? lp[i] : -INFINITY;
+        x[u][i] = there ? xp[i * 32] : Vec{};
+      }
     }
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) s[i].add(l[i], reinterpret_cast<const float*>(&x[i]));
+    for (int u = 0; u < kAhead; ++u)
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) s[i].add(l[u][i], reinterpret_cast<const float*>(&x[u][i]));
   }
   int tk = tk0, h = r0 - tk0 * G;
 #pragma unroll

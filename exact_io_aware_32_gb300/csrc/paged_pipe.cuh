@@ -134,19 +134,17 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
       : "f"(x - hx), "f"(y - hy));
 }
 
-// Q rows in a [panel][128 rows][128 bytes] swizzled tile from 64 bf16 to 64 hi
-// and 64 lo codes per 128-byte row, in place, by NT threads, four neighbours per
-// row: rows [0, rows) rounded up to NT / 4, and with COPIES rows 0 - 31 also to
-// the other three row quarters. ex[row] gets the biased exponent e of the row's largest
-// magnitude: the row was scaled by 2^(134 - e).
-template <int D, bool COPIES, int NT>
-__device__ __forceinline__ void convert_q(uint8_t* q, uint8_t* ex, int rows, int tid) {
+// Q rows 0 - 31 of a [panel][128 rows][128 bytes] swizzled tile from 64 bf16 to
+// 64 hi and 64 lo codes per 128-byte row, in place and copied to the other three
+// row quarters, by 128 threads, four neighbours per row. ex[row] gets the biased
+// exponent e of the row's largest magnitude: the row was scaled by 2^(134 - e).
+template <int D>
+__device__ __forceinline__ void convert_q(uint8_t* q, uint8_t* ex, int tid) {
   constexpr int kPanels = D / 64;
   const int part = tid & 3;
   const uint32_t base = smem_u32(q);
-#pragma unroll 2
-  for (int r0 = 0; r0 < rows; r0 += NT / 4) {
-    const int row = r0 + (tid >> 2);
+  {
+    const int row = tid >> 2;
     auto at = [&](int pn, int c) { return (uint32_t)(pn * 16384 + row * 128 + ((c ^ (row & 7)) << 4)); };
     uint32_t w[kPanels][8], big = 0;  // chunks 2 part and 2 part + 1 of each panel
 #pragma unroll
@@ -179,12 +177,53 @@ __device__ __forceinline__ void convert_q(uint8_t* q, uint8_t* ex, int rows, int
         lo[k] = l0 | (l1 << 16);
       }
 #pragma unroll
-      for (int n = 0; n < (COPIES ? 4 : 1); ++n) {
+      for (int n = 0; n < 4; ++n) {
         st_shared_v4(base + at(pn, part) + n * 4096, hi[0], hi[1], hi[2], hi[3]);
         st_shared_v4(base + at(pn, 4 + part) + n * 4096, lo[0], lo[1], lo[2], lo[3]);
       }
     }
   }
+}
+// The same for one row by one thread (neighbouring lanes take neighbouring rows); returns e.
+template <int D>
+__device__ __forceinline__ uint32_t convert_row(uint8_t* q, int row) {
+  constexpr int kPanels = D / 64;
+  const uint32_t base = smem_u32(q);
+  auto at = [&](int pn, int c) { return (uint32_t)(pn * 16384 + row * 128 + ((c ^ (row & 7)) << 4)); };
+  uint32_t w[kPanels][32], big = 0;
+#pragma unroll
+  for (int pn = 0; pn < kPanels; ++pn)
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const uint4 x = *reinterpret_cast<const uint4*>(q + at(pn, c));
+      w[pn][4 * c] = x.x;
+      w[pn][4 * c + 1] = x.y;
+      w[pn][4 * c + 2] = x.z;
+      w[pn][4 * c + 3] = x.w;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        big = max(big, max(w[pn][4 * c + k] & 0x7FFFu, (w[pn][4 * c + k] >> 16) & 0x7FFFu));
+    }
+  const uint32_t e = min(max(big >> 7, 8u), 253u);
+  const float f = __uint_as_float((261u - e) << 23);
+#pragma unroll
+  for (int pn = 0; pn < kPanels; ++pn)
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {  // 16 values: a chunk of hi and one of lo
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t x = w[pn][8 * c + 2 * k], y = w[pn][8 * c + 2 * k + 1];
+        uint32_t h0, l0, h1, l1;
+        split2(__uint_as_float(x << 16) * f, __uint_as_float(x & 0xffff0000u) * f, h0, l0);
+        split2(__uint_as_float(y << 16) * f, __uint_as_float(y & 0xffff0000u) * f, h1, l1);
+        hi[k] = h0 | (h1 << 16);
+        lo[k] = l0 | (l1 << 16);
+      }
+      st_shared_v4(base + at(pn, c), hi[0], hi[1], hi[2], hi[3]);
+      st_shared_v4(base + at(pn, 4 + c), lo[0], lo[1], lo[2], lo[3]);
+    }
+  return e;
 }
 // What the softmax multiplies its scale by for a row whose exponent is e.
 __device__ __forceinline__ float unscale(uint32_t e) { return __uint_as_float((e - 7u) << 23); }
