@@ -175,11 +175,11 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
       int nb[2];
       half_blocks<C::kTiles>(a, p, nb);
       const int nbm = max(nb[0], nb[1]);
-      int page = nbm > 0 ? lane_page(a, p, p.jb, lane) : -1;
+      Pages pages;
+      if (nbm > 0) pages.begin(a, p, lane);
       if (nb[0] > 0) load_q(0);
       for (int j = 0; ok && j < nbm; ++j, ++g) {
-        const int jj = p.jb + j, page_now = page;
-        if (j + 1 < nbm) page = lane_page(a, p, jj + 1, lane);
+        const int jj = p.jb + j, page_now = pages.of(a, p, jj, lane);
         const int sk = g % C::kKStages;
         if (!(ok = warp_wait(&bars.k_empty[sk], ((g / C::kKStages) & 1) ^ 1, abort_flag))) break;
         load_block<D, FP8>(a, p, jj, page_now, lane, &a.tm_k, smem + C::kOffK + sk * C::kKBytes, &bars.k_full[sk]);

@@ -144,10 +144,10 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
       note_piece(a, parts, p, walk, per);
       const int nb = p.je - p.jb;
       if (nb == 0) continue;
-      int page = lane_page(a, p, p.jb, lane);
+      Pages pages;
+      pages.begin(a, p, lane);
       for (int j = 0; j < nb; ++j, ++g) {
-        const int jj = p.jb + j, page_now = page;
-        if (j + 1 < nb) page = lane_page(a, p, jj + 1, lane);
+        const int jj = p.jb + j, page_now = pages.of(a, p, jj, lane);
         const int s = g % C::kKStages;
         if (!(ok = warp_wait(&bars.k_empty[s], ((g / C::kKStages) & 1) ^ 1, abort_flag))) break;
         load_block<D, FP8>(a, p, jj, page_now, lane, &a.tm_k, smem + C::kOffK + s * C::kKBytes, &bars.k_full[s]);
@@ -167,10 +167,10 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     bool ok = true;
     for (; ok && more; more = walk.step(a, p)) {
       if (p.jb == p.je) continue;
-      int page = lane_page(a, p, p.jb, lane);
+      Pages pages;
+      pages.begin(a, p, lane);
       for (int jj = p.jb; jj < p.je; ++jj, ++g) {
-        const int page_now = page, s = g % kS;
-        if (jj + 1 < p.je) page = lane_page(a, p, jj + 1, lane);
+        const int page_now = pages.of(a, p, jj, lane), s = g % kS;
         if (!(ok = warp_wait(&empty[s], ((g / kS) & 1) ^ 1, abort_flag))) break;
         load_block<D, FP8>(a, p, jj, page_now, lane, &a.tm_v,
                            smem + (FP8 ? C::kOffC + s * C::kCodeBytes : C::kOffV + s * C::kTileBytes), &full[s]);
