@@ -108,13 +108,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) fa_paged_join_few_kernel(cons
   write_row<D>(a, (long long)(mine.start + tok) * a.Hq + mine.h * G + (row - tk * G), s, lane);
 }
 
-// Tiles of 128 or 256 rows, mostly of two parts: a warp per four rows. (A warp per
-// row spent its time on the rows' indices: 17 us for the 152 cut tiles of three
-// chunks of 1024 tokens, 32 heads of 128.)
+// Tiles of 128 or 256 rows, mostly of two parts: a warp per two rows. (Three chunks
+// of 1024 tokens, 32 heads of 128, whole call: a warp per row 243 us, per two rows
+// 236 us, per four 238 us, four with three parts in flight 240 us.)
+constexpr int kJoinRows = 2;
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) fa_paged_join_chunk_kernel(const __grid_constant__ PagedArgs a,
                                                                               int rows_per_tile) {
-  constexpr int V = D / 32, kRows = 4, kAhead = 3;
+  constexpr int V = D / 32, kRows = kJoinRows, kAhead = 2;
   using Vec = typename std::conditional<V == 4, float4, float2>::type;
   const int c = blockIdx.x, lane = threadIdx.x & 31;
   const int row0 = ((int)blockIdx.y * kJoinWarps + (threadIdx.x >> 5)) * kRows;  // half * 128 + token * G + head
@@ -165,7 +166,7 @@ cudaError_t launch_join(const PagedArgs& a, const PagedPlan& p, cudaStream_t str
   if (p.few)
     return launch_dependent(fa_paged_join_few_kernel<D>, dim3((unsigned)p.ctas, (unsigned)(p.tpt * (a.Hq / a.Hkv))),
                             32 * kJoinWarps, 0, stream, a);
-  return launch_dependent(fa_paged_join_chunk_kernel<D>, dim3((unsigned)p.ctas, (unsigned)(p.rows / (4 * kJoinWarps))),
+  return launch_dependent(fa_paged_join_chunk_kernel<D>, dim3((unsigned)p.ctas, (unsigned)(p.rows / (kJoinRows * kJoinWarps))),
                           32 * kJoinWarps, 0, stream, a, p.rows);
 }
 
