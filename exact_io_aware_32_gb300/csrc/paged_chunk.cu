@@ -219,12 +219,9 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
       mma_commit(&bars.s_full[t]);
       if (last) mma_commit(&bars.q_free[qs]);  // the tile's last product to read Q
     };
-    auto issue_pv = [&](int t, int st, bool first) {
-      const uint32_t vo = (uint32_t)(st * C::kTileBytes) >> 4;
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)  // P columns [8 kk, 8 kk + 8), V rows [16 kk, 16 kk + 16)
-        mma_ts(tmem + C::col_o(t), tmem + C::col_p(t) + kk * 8, dv0 + vo + Tile<D>::step_v(kk), kIdO,
-               (!first || kk > 0) ? 1u : 0u);
+    auto issue_pv = [&](int t, int st, int steps, bool first) {
+      issue_pv_steps<D>(tmem + C::col_o(t), tmem + C::col_p(t), dv0 + ((uint32_t)(st * C::kTileBytes) >> 4), kIdO, steps,
+                        first);
     };
     int g = 0, nq[2] = {0, 0}, np[2] = {0, 0};  // key blocks; tiles and P blocks of each half so far
     bool ok = true;
@@ -265,10 +262,8 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
                           j < nb[0] ? (np[0] & 1) : ph, k_next ? &bars.k_full[sn] : &bars.v_full[s],
                           k_next ? ((g + 1) / C::kKStages) & 1 : ph, abort_flag);
           if (!ok) break;
-          if constexpr (!FP8) {
-            const int end = p.q.len - (p.jb + j) * 128;
-            if (end < 128) zero_rows_from<D>(smem + C::kOffV + s * C::kTileBytes, end, lane);
-          }
+          const int keys = p.q.len - (p.jb + j) * 128, steps = pv_steps(keys);
+          if (!FP8 && keys < steps * 16) zero_rows<D>(smem + C::kOffV + s * C::kTileBytes, keys, steps * 16, lane);
           for (int t = 0; t < 2; ++t) {
             if (j < nb[t]) {
               if (t == 1 && !(ok = warp_wait(&bars.p_full[1], np[1] & 1, abort_flag))) break;
@@ -276,7 +271,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
               if (j == 0 && !(ok = warp_wait(&bars.o_free[t], (nq[t] & 1) ^ 1, abort_flag))) break;
               tc_fence_after();
               if (elect_one()) {
-                issue_pv(t, s, j == 0);
+                issue_pv(t, s, steps, j == 0);
                 if (j == nb[t] - 1) mma_commit(&bars.o_done[t]);
                 if (t == v_last) mma_commit(&bars.v_empty[s]);
               }
@@ -312,11 +307,11 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
           ok = warp_wait2(&bars.p_full[0], g & 1, &bars.v_full[s], (g / C::kVStages) & 1, abort_flag);
           if (ok && j == 0) ok = warp_wait(&bars.o_free[0], (nq[0] & 1) ^ 1, abort_flag);
           if (!ok) break;
-          const int end = p.q.len - (p.jb + j) * 128;
-          if (end < 128) zero_rows_from<D>(smem + C::kOffV + s * C::kTileBytes, end, lane);
+          const int keys = p.q.len - (p.jb + j) * 128, steps = pv_steps(keys);
+          if (keys < steps * 16) zero_rows<D>(smem + C::kOffV + s * C::kTileBytes, keys, steps * 16, lane);
           tc_fence_after();
           if (elect_one()) {
-            issue_pv(0, s, j == 0);
+            issue_pv(0, s, steps, j == 0);
             mma_commit(&bars.o_done[0]);
             mma_commit(&bars.v_empty[s]);
           }

@@ -237,17 +237,12 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
         if (!(ok = warp_wait2(&bars.v_full[s], (g / C::kVStages) & 1, &bars.p_full[b], (g >> 1) & 1, abort_flag))) break;
         // a tile's first P V overwrites O: the tile before has been read out
         if (jj == p.jb && !(ok = warp_wait(&bars.o_free, (n & 1) ^ 1, abort_flag))) break;
-        if constexpr (!FP8) {
-          const int end = p.q.len - jj * 128;
-          if (end < 128) zero_rows_from<D>(smem + C::kOffV + s * C::kTileBytes, end, lane);
-        }
+        const int keys = p.q.len - jj * 128, steps = pv_steps(keys);
+        if (!FP8 && keys < steps * 16) zero_rows<D>(smem + C::kOffV + s * C::kTileBytes, keys, steps * 16, lane);
         tc_fence_after();
         if (elect_one()) {
           const uint32_t vo = (uint32_t)(s * C::kTileBytes) >> 4;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ts(tmem + C::kColO, tmem + C::kColP + b * 64 + kk * 8, dv + vo + Tile<D>::step_v(kk), kIdO,
-                   (jj > p.jb || kk > 0) ? 1u : 0u);
+          issue_pv_steps<D>(tmem + C::kColO, tmem + C::kColP + b * 64, dv + vo, kIdO, steps, jj == p.jb);
           mma_commit(&bars.pv_done[b]);
           mma_commit(&bars.v_empty[s]);
         }

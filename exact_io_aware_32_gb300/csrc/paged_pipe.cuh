@@ -85,13 +85,32 @@ __device__ __forceinline__ void load_block(const PagedArgs& a, const Piece& p, i
   __syncwarp();
 }
 
-// Zeros the rows of a bf16 value tile from 'row' on (past the request's last
-// key): whatever the cache or an earlier block left there, even NaN, must meet
-// its zero weights as a number. By one warp, before its products are issued.
+// 16-key steps of P V for a block with 'keys' keys left in its request: the rest of a last block is not multiplied.
+__device__ __forceinline__ int pv_steps(int keys) { return min(8, (keys + 15) >> 4); }
+
+// O += P V of 'steps' 16-key steps by the elected lane: all eight in straight code, since a condition on each costs the
+// issuing warp time that it does not have.
 template <int D>
-__device__ __forceinline__ void zero_rows_from(uint8_t* tile, int row, int lane) {
+__device__ __forceinline__ void issue_pv_steps(uint32_t d_o, uint32_t a_p, uint64_t dv, uint32_t idesc, int steps,
+                                               bool first) {
+  if (steps == 8) {
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)  // P columns [8 kk, 8 kk + 8), V rows [16 kk, 16 kk + 16)
+      mma_ts(d_o, a_p + kk * 8, dv + Tile<D>::step_v(kk), idesc, (!first || kk > 0) ? 1u : 0u);
+  } else {
+#pragma unroll 1
+    for (int kk = 0; kk < steps; ++kk)
+      mma_ts(d_o, a_p + kk * 8, dv + Tile<D>::step_v(kk), idesc, (!first || kk > 0) ? 1u : 0u);
+  }
+}
+
+// Zeros rows [row, end) of a value tile, those past the request's last key that
+// its last step still multiplies: whatever the cache or an earlier block left there, even
+// NaN, must meet its zero weights as a number. By one warp, before the products are issued.
+template <int D>
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int row, int end, int lane) {
   const uint32_t base = smem_u32(tile);
-  for (int i = row * (D / 8) + lane; i < 128 * (D / 8); i += 32)
+  for (int i = row * (D / 8) + lane; i < end * (D / 8); i += 32)
     st_shared_v4(base + Tile<D>::chunk(i / (D / 8), i % (D / 8)), 0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   __syncwarp();
@@ -121,7 +140,7 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t c) {
 }
 
 // A 128 x D tile of value codes (rows of D bytes) to an f16 tile, by NT threads;
-// rows from 'rows' on become zero. A thread takes 8 codes, one 16-byte chunk, at
+// of the rows from 'rows' on those that pv_steps still multiplies become zero. A thread takes 8 codes, one 16-byte chunk, at
 // a time: sixteen threads read 128 neighbouring bytes and a quarter warp writes
 // the eight chunks of one 128-byte row, so neither meets a bank twice.
 template <int D, int NT>
@@ -132,13 +151,19 @@ __device__ __forceinline__ void convert_tile(const uint8_t* src, uint8_t* dst, i
   const uint32_t base = smem_u32(dst);
   // where this thread's chunk of the steps' rows lies: the swizzle goes by row % 8
   const uint32_t even = base + Tile<D>::chunk(r0, c), odd = base + Tile<D>::chunk(r0 + kRows, c);
-#pragma unroll 8
-  for (int it = 0; it < 128 / kRows; ++it) {
+  auto convert = [&](int it) {
     uint2 w = *reinterpret_cast<const uint2*>(src + (it * NT + tid) * 8);
     if (rows < 128 && r0 + it * kRows >= rows) w = make_uint2(0u, 0u);  // code 0 is zero
     const uint32_t at = (it & 1) ? odd + (it >> 1) * (2 * kRows / 8) * Tile<D>::kGroup
                                  : even + (it >> 1) * (2 * kRows / 8) * Tile<D>::kGroup;
     st_shared_v4(at, e4m3x2_to_f16(w.x), e4m3x2_to_f16(w.x >> 16), e4m3x2_to_f16(w.y), e4m3x2_to_f16(w.y >> 16));
+  };
+  if (rows >= 128) {
+#pragma unroll 8
+    for (int it = 0; it < 128 / kRows; ++it) convert(it);
+  } else {
+#pragma unroll 1
+    for (int it = 0; it * kRows < pv_steps(rows) * 16; ++it) convert(it);
   }
 }
 
