@@ -375,79 +375,72 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
       // ---- the tile's four quarters joined: o = sum_w 2^(m_w - m) O_w / sum_w 2^(m_w - m) l_w
       if (ok && nb > 0) ok = mbar_wait(&bars.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
-      stats[warp * 32 + lane] = make_float2(m_ref, l_sum);
-      if (!named_bar_and(1, 128, ok)) {  // the four warps agree whether to go on
+      if (!named_bar_and(1, 128, ok)) {  // the four warps agree whether to go on, and have read the join before
         ok = false;
         break;
       }
-      float m = -INFINITY, l = 0.f;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) m = fmaxf(m, stats[w * 32 + lane].x);
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float2 s = stats[w * 32 + lane];
-        if (s.y > 0.f) l += s.y * ex2(s.x - m);
-      }
-      const bool seen = l > 0.f;
-      const float f = l_sum > 0.f ? ex2(m_ref - m) * (a.o_scale / l) : 0.f;
       const bool whole = p.whole();
       const long long row0 = (long long)(p.q.start + p.tok) * a.Hq + p.h * G;  // row r: token r / G, head r % G
       const long long part0 = ((long long)blockIdx.x * 2 + (p.jb == 0 ? 1 : 0)) * 32;
-      if (warp == 0 && lane < rows) {
-        const float lse2 = seen ? m - kBias + log2f(l) : -INFINITY;
-        if (whole)
-          a.lse[row0 + (long long)rt * a.Hq + (lane - rt * G)] = seen ? lse2 * kLn2 : -INFINITY;
-        else
-          a.part_lse[part0 + lane] = lse2;
-      }
+      stats[warp * 32 + lane] = make_float2(m_ref, l_sum);
       if (nb > 0) tc_fence_after();
       for (int r0 = 0; r0 < rows; r0 += C::kJoinRows) {  // kJoinRows rows at a time
         const int mine = lane - r0;
+        const bool writes = mine >= 0 && mine < C::kJoinRows;
+        const uint32_t dst = smem_u32(join + (warp * C::kJoinRows + mine) * C::kJoinStride);
+        if (nb > 0) {
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          if (nb > 0) {
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
             tmem_ld32(t_o + c, o);
             tmem_ld_wait(o);
-          }
-          if (mine >= 0 && mine < C::kJoinRows) {
-            const uint32_t dst = smem_u32(join + (warp * C::kJoinRows + mine) * C::kJoinStride + c);
+            if (writes)
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              uint32_t x[4];
-#pragma unroll
-              for (int k = 0; k < 4; ++k) x[k] = f > 0.f ? __float_as_uint(__uint_as_float(o[i + k]) * f) : 0u;
-              st_shared_v4(dst + i * 4, x[0], x[1], x[2], x[3]);
-            }
+              for (int i = 0; i < 32; i += 4) st_shared_v4(dst + (c + i) * 4, o[i], o[i + 1], o[i + 2], o[i + 3]);
           }
-        }
-        if (nb > 0 && r0 + C::kJoinRows >= rows) {
-          tc_fence_before();
-          mbar_arrive(&bars.o_free);  // O has been read: the next tile may accumulate there
+          if (r0 + C::kJoinRows >= rows) {
+            tc_fence_before();
+            mbar_arrive(&bars.o_free);  // O has been read: the next tile may accumulate there
+          }
         }
         named_bar_sync(1, 128);
         const int count = min(C::kJoinRows, rows - r0);
-        for (int i = threadIdx.x; i < count * (D / 4); i += 128) {  // four columns each
+        for (int i = threadIdx.x; i < count * (D / 4); i += 128) {  // a row's four columns each
           const int rr = i / (D / 4), c = (i % (D / 4)) * 4, r = r0 + rr;
+          float2 ml[4];
+          float m = -INFINITY, l = 0.f;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            ml[w] = stats[w * 32 + r];
+            m = fmaxf(m, ml[w].x);
+          }
           float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
+            if (!(ml[w].y > 0.f)) continue;  // that warp saw no key of this row
+            const float f = ex2(ml[w].x - m);
             const float4 x = *reinterpret_cast<const float4*>(join + (w * C::kJoinRows + rr) * C::kJoinStride + c);
-            s.x += x.x;
-            s.y += x.y;
-            s.z += x.z;
-            s.w += x.w;
+            l += f * ml[w].y;
+            s.x += f * x.x;
+            s.y += f * x.y;
+            s.z += f * x.z;
+            s.w += f * x.w;
           }
+          const bool seen = l > 0.f;
+          const float inv = seen ? a.o_scale / l : 0.f, lse2 = seen ? m - kBias + log2f(l) : -INFINITY;
+          s = make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv);
           if (whole) {
             const int tk = r / G;
             const long long row = row0 + (long long)tk * a.Hq + (r - tk * G);
             *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.o) + (row * D + c) * 2) =
                 make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+            if (c == 0) a.lse[row] = seen ? lse2 * kLn2 : -INFINITY;
           } else {
             *reinterpret_cast<float4*>(a.part_o + (part0 + r) * D + c) = s;
+            if (c == 0) a.part_lse[part0 + r] = lse2;
           }
         }
-        named_bar_sync(1, 128);
+        if (r0 + C::kJoinRows < rows) named_bar_sync(1, 128);
       }
     }
   }
