@@ -152,6 +152,14 @@ int fa_fwd_paged(const void* q, long long q_stride, const void* k_cache, const v
   if (!workspace || !aligned(workspace, 256) ||
       workspace_bytes < fa_fwd_paged_workspace_bytes(T, R, Hq, Hkv, d, max_new))
     return FA_ERR_WORKSPACE;
+  // places in the row of tiles are 32-bit numbers of key blocks (paged_work.cuh)
+  const int max_keys = max_pages * page_size;
+  fa::PagedPlan p[2];
+  int n = fa::plan_paged(T, R, Hq, Hkv, d, fp8 ? 1 : 0, max_new, max_keys, kMaxSms, p);
+  for (int i = 0; i < n; ++i) {
+    const double tiles = ((double)T / p[i].tpt + R) * Hkv;
+    if (tiles * (max_keys / 128.0 + 4.0) >= 2147483648.0) return FA_ERR_INVALID_ARG;
+  }
   fa::PagedArgs a;
   std::memset(&a, 0, sizeof(a));
   int sms = 0;
@@ -177,15 +185,9 @@ int fa_fwd_paged(const void* q, long long q_stride, const void* k_cache, const v
   a.fp8 = fp8 ? 1 : 0;
   a.scale_log2 = scale_log2;
   a.o_scale = fp8 ? descale_v : 1.0f;
-  a.max_keys = max_pages * page_size;
+  a.max_keys = max_keys;
   a.test_fault = fa::take_test_fault();
-  fa::PagedPlan p[2];
-  const int n = fa::plan_paged(T, R, Hq, Hkv, d, a.fp8, max_new, a.max_keys, std::min(sms, kMaxSms), p);
-  // places in the row of tiles are 32-bit numbers of key blocks (paged_work.cuh)
-  for (int i = 0; i < n; ++i) {
-    const double tiles = ((double)T / p[i].tpt + R) * Hkv;
-    if (tiles * (a.max_keys / 128.0 + 4.0) >= 2147483648.0) return FA_ERR_INVALID_ARG;
-  }
+  n = fa::plan_paged(T, R, Hq, Hkv, d, a.fp8, max_new, a.max_keys, std::min(sms, kMaxSms), p);
   for (int i = 0; i < n; ++i)
     if (fa::launch_paged(a, p[i], workspace, static_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_LAUNCH;
   return FA_OK;

@@ -471,7 +471,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
       if (ok && nb > 0) ok = mbar_wait(&bars.o_done[t], (C::kTiles == 2 ? nq : np - 1) & 1, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const bool seen = l_sum > 0.f;
+      const bool seen = l_sum != 0.f;  // (a NaN sum goes on to the result)
       const float lse2 = seen ? m_ref - kBias + log2f(l_sum) : -INFINITY;
       const float inv = seen ? a.o_scale / l_sum : 0.f;
       if (p.whole()) {

@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
           float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
-            if (!(ml[w].y > 0.f)) continue;  // that warp saw no key of this row
+            if (ml[w].y == 0.f) continue;  // that warp saw no key of this row (a NaN sum goes on to the result)
             const float f = ex2(ml[w].x - m);
             const float4 x = *reinterpret_cast<const float4*>(join + (w * C::kJoinRows + rr) * C::kJoinStride + c);
             l += f * ml[w].y;
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
             s.z += f * x.z;
             s.w += f * x.w;
           }
-          const bool seen = l > 0.f;
+          const bool seen = l != 0.f;
           const float inv = seen ? a.o_scale / l : 0.f, lse2 = seen ? m - kBias + log2f(l) : -INFINITY;
           s = make_float4(s.x * inv, s.y * inv, s.z * inv, s.w * inv);
           if (whole) {

@@ -46,7 +46,7 @@ struct Joined {  // of one row, V columns per lane
 template <int D>
 __device__ __forceinline__ void write_row(const PagedArgs& a, long long out, const Joined<D / 32>& s, int lane) {
   constexpr int V = D / 32;
-  const float inv = s.tot > 0.f ? 1.f / s.tot : 0.f;
+  const float inv = s.tot == 0.f ? 0.f : 1.f / s.tot;  // (a NaN goes on to the result)
   uint32_t w[V / 2];
 #pragma unroll
   for (int k = 0; k < V / 2; ++k) w[k] = ptx::pack_bf16x2(s.acc[2 * k] * inv, s.acc[2 * k + 1] * inv);
@@ -55,7 +55,7 @@ __device__ __forceinline__ void write_row(const PagedArgs& a, long long out, con
     *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
   else
     *reinterpret_cast<uint32_t*>(dst) = w[0];
-  if (lane == 0) a.lse[out] = s.tot > 0.f ? (s.m + log2f(s.tot)) * 0.693147180559945309417f : -INFINITY;
+  if (lane == 0) a.lse[out] = s.tot != 0.f ? (s.m + log2f(s.tot)) * 0.693147180559945309417f : -INFINITY;
 }
 
 // Few rows (decoding): one long request's tile can have a part on every SM, so a
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) fa_paged_join_few_kernel(cons
 #pragma unroll
   for (int w = 0; w < kJoinWarps; ++w) {
     const float2 ml = s_ml[w];
-    const float f = ml.y > 0.f ? exp2f(ml.x - top) : 0.f;
+    const float f = ml.y != 0.f ? exp2f(ml.x - top) : 0.f;
     s.tot += f * ml.y;
 #pragma unroll
     for (int k = 0; k < V; ++k) s.acc[k] += f * s_acc[w][lane * V + k];

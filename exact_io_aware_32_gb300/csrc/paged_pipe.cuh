@@ -206,7 +206,7 @@ __device__ __forceinline__ void convert_q(uint8_t* q, uint8_t* ex, int tid) {
     }
     big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));  // (all four have read the row now)
     big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-    const uint32_t e = min(max(big >> 7, 8u), 253u);
+    const uint32_t e = min(max(big >> 7, 8u), 254u);
     const float f = __uint_as_float((261u - e) << 23);
     if (part == 0) ex[row] = (uint8_t)e;
 #pragma unroll
@@ -248,7 +248,7 @@ __device__ __forceinline__ uint32_t convert_row(uint8_t* q, int row) {
       for (int k = 0; k < 4; ++k)
         big = max(big, max(w[pn][4 * c + k] & 0x7FFFu, (w[pn][4 * c + k] >> 16) & 0x7FFFu));
     }
-  const uint32_t e = min(max(big >> 7, 8u), 253u);
+  const uint32_t e = min(max(big >> 7, 8u), 254u);
   const float f = __uint_as_float((261u - e) << 23);
 #pragma unroll
   for (int pn = 0; pn < kPanels; ++pn)

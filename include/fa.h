@@ -342,9 +342,10 @@ FA_API int fa_paged_store(const void* k, const void* v, long long k_stride, long
  *            contents on entry do not matter; not shared by calls that may run at once
  * A row that sees no key (seq_len 0, or smaller than the new tokens under the
  * mask) gets o = 0, lse = -inf. Rows that belong to no request are left as
- * they were. What the cache holds past a request's last key (unwritten slots,
- * NaN among them) never reaches a result; keys hidden by the causal mask only
- * must hold finite values. A page outside the cache reads as zeros, a
+ * they were. A NaN in a row's query or in a key or value that it sees reaches
+ * its result. What the cache holds past a request's last key (unwritten slots,
+ * NaN among them) never does; keys hidden by the causal mask only must hold
+ * finite values. A page outside the cache reads as zeros, a
  * seq_len past max_pages pages is cut, a negative one is 0, query_start is
  * cut into [0, T], and a request that ends before it starts has no rows; each
  * is reported by fa_device_status as FA_ERR_INVALID_ARG.

@@ -123,6 +123,42 @@ def test_rows_without_keys(d, fp8, most):
 
 
 @pytest.mark.parametrize("most", [1, 200])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_nan_in_what_a_row_sees_is_not_hidden(d, fp8, most):
+    """A NaN in a query, a key or a value reaches the rows that see it, no others (those keep their bits), also where
+    the keys are split over the GPU."""
+    c = paged_ref.case([(20000, 1), (70, 1), (500, 1 if most == 1 else 150)], 8, 2, d, 32, fp8=fp8, seed=d + most)
+    g = on_gpu(c)
+    o, lse = attend(c, g, max_new=most)
+    check(c, o, lse)
+
+    def planted(name, at):
+        x = g[name].clone()
+        (x.view(torch.uint8) if x.dtype == torch.float8_e4m3fn else x)[at] = 0x7F if name != "q" and fp8 else math.nan
+        return attend(c, dict(g, **{name: x}), max_new=most)
+
+    def expect(got, rows, heads, cols, lse_too):
+        nan = torch.zeros_like(o, dtype=torch.bool)
+        nan[rows, heads, cols] = True
+        assert torch.equal(torch.isnan(got[0]), nan)
+        assert torch.equal(torch.isnan(got[1]), nan.any(-1) if lse_too else torch.zeros_like(lse, dtype=torch.bool))
+        assert torch.equal(got[0][~nan], o[~nan])
+        keep = ~nan.any(-1) if lse_too else slice(None)
+        assert torch.equal(got[1][keep], lse[keep])
+
+    every = slice(None)
+    expect(planted("q", (0, 3, 17)), slice(0, 1), slice(3, 4), every, True)
+    expect(planted("q", (2, 6, 1)), slice(2, 3), slice(6, 7), every, True)
+    for r, key in ((0, 12345), (0, 20000), (1, 3), (2, 7)):  # keys that all tokens of the request see
+        rows = slice(c["start"][r], c["start"][r + 1])
+        page, slot = c["table"][r][key // 32], key % 32
+        expect(planted("k_cache", (page, 1, slot, d - 1)), rows, slice(4, 8), every, True)
+        expect(planted("v_cache", (page, 0, slot, 9)), rows, slice(0, 4), slice(9, 10), False)
+    parity.check_status()
+
+
+@pytest.mark.parametrize("most", [1, 200])
 def test_rows_behind_the_last_request_stay(most):
     c = paged_ref.case([(100, 1), (5, 130), (0, 1)], 6, 2, 128, 16, pad=37, seed=8)
     g = on_gpu(c)

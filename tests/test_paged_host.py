@@ -97,6 +97,14 @@ def test_fwd_paged_rejects_bad_args(args, status):
     assert fa.fa_fwd_paged(**kw, stream=0) == status
 
 
+def test_fwd_paged_rejects_more_work_than_it_counts():
+    """Places in the row of tiles are 32-bit numbers of key blocks: 600 requests x 2 key heads x 2^31 / 128 blocks."""
+    kw = dict(q=A, q_stride=1024, k_cache=A, v_cache=A, fp8=False, descale_k=1.0, descale_v=1.0, block_table=A,
+              max_pages=(1 << 26) - 1, query_start=A, seq_lens=A, o=A, lse=A, T=600, R=600, Hq=8, Hkv=2, d=128,
+              num_pages=11, page_size=32, max_new=1, scale=0.1, causal=True, workspace=A, workspace_bytes=1 << 40)
+    assert fa.fa_fwd_paged(**kw, stream=0) == fa.FA_ERR_INVALID_ARG
+
+
 def test_helpers_reject_bad_tensors():
     c = paged_ref.case([(5, 2)], 4, 2, 64, 16)
     ints = lambda x: torch.tensor(x, dtype=torch.int32)  # noqa: E731
