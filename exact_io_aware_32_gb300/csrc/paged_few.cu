@@ -39,12 +39,12 @@ struct FCfg {
   static constexpr int kKStages = FP8_ ? (D == 64 ? 6 : 4) : (D == 64 ? 4 : 2);
   static constexpr int kVStages = FP8_ ? (D == 64 ? 3 : 2) : (D == 64 ? 4 : 3);
   static constexpr int kCStages = FP8_ ? (D == 64 ? 6 : 3) : 0;  // value codes on their way to f16
-  static constexpr int kOffQ = 0;
-  static constexpr int kOffK = kOffQ + kTileBytes;
+  static constexpr int kOffQ = 0, kOffRaw = kOffQ + kTileBytes;  // E4M3 caches: the next tile's 32 rows as loaded
+  static constexpr int kOffK = kOffRaw + (FP8_ ? 32 * D * 2 : 0);
   static constexpr int kOffV = kOffK + kKStages * kKBytes;
   static constexpr int kOffC = kOffV + kVStages * kTileBytes;
   // the quarters' O of kJoinRows rows at a time, rows padded by 16 bytes against bank conflicts; (m, l) of all rows
-  static constexpr int kJoinRows = D == 64 ? 16 : 8, kJoinStride = D + 4;
+  static constexpr int kJoinRows = (D == 64 ? 16 : 8) / (FP8_ ? 2 : 1), kJoinStride = D + 4;
   static constexpr int kOffJoin = kOffC + kCStages * kCodeBytes;
   static constexpr int kOffBar = kOffJoin + 4 * kJoinRows * kJoinStride * 4 + 4 * 32 * 8;
   static constexpr int kSmemBytes = kOffBar + 512 + 1024;  // barriers, alignment slack
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     fence_mbar_init();
   }
   // rows of Q that no copy fills (G that does not divide 32, short tiles) are zeros, not leftovers
-  for (int i = threadIdx.x; i < C::kTileBytes / 16; i += C::kThreads)
+  for (int i = threadIdx.x; i < (C::kOffK - C::kOffQ) / 16; i += C::kThreads)
     st_shared_v4(smem_u32(smem + C::kOffQ) + i * 16, 0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   if (warp == C::kWarpPv) {
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     Parts parts{};
     int g = 0, nk = 0;  // key blocks, and loads issued
     bool ok = true;
-    for (; ok && more; more = walk.step(a, p)) {
+    for (; ok && more; more = walk.step<true>(a, p)) {
       note_piece(a, parts, p, walk, per);
       const int nb = p.je - p.jb;
       if (nb == 0) continue;
@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     uint64_t *full = FP8 ? bars.c_full : bars.v_full, *empty = FP8 ? bars.c_empty : bars.v_empty;
     int g = 0, nv = 0;
     bool ok = true;
-    for (; ok && more; more = walk.step(a, p)) {
+    for (; ok && more; more = walk.step<true>(a, p)) {
       if (p.jb == p.je) continue;
       Pages pages;
       pages.begin(a, p, lane);
@@ -182,28 +182,42 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     // ------------------------------------------------------------ S = Q K^T, up to two blocks ahead of the softmax
     const uint64_t dq = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
     const uint64_t dk = desc_keys<D, FP8>(smem + C::kOffK);
-    // Q is copied by this warp too, as soon as the tile before has been read (E4M3 caches: once, which the converters
-    // make four of)
-    constexpr int kCopies = FP8 ? 1 : 4;
-    const uint32_t q_bytes = (uint32_t)(kCopies * G * a.tpt * D * 2);
+    // Q is copied by this warp too: at bf16 four times into the operand, as soon as the tile before has been read; with
+    // E4M3 caches once into a place of its own, as soon as the converters have made the tile before's four from there, so
+    // that it is there when they come to this tile's.
     const bool withhold = a.test_fault == 1;  // test hook: without its Q the wait below expires
     int g = 0, n = 0, nq = 0;                 // key blocks, tiles, copies of Q issued
-    bool ok = true;
-    for (; ok && more; more = walk.step(a, p)) {
-      if (p.jb == p.je) continue;
-      if (!(ok = warp_wait(&bars.q_free, (n & 1) ^ 1, abort_flag))) break;
-      if (!withhold) {
-        uint64_t* bar = FP8 ? &bars.q_raw : &bars.q_full[n % 3];
-        if (elect_one()) {
-          mbar_arrive_expect_tx(bar, q_bytes);
-          for (int w = 0; w < kCopies; ++w)
-            for (int pn = 0; pn < C::kPanels; ++pn)
-              tma_load_3d(smem + C::kOffQ + pn * 16384 + w * 4096, &a.tm_q, bar, pn * 64, p.h * G, p.q.start + p.tok);
-        }
-        __syncwarp();
-        ++nq;
+    auto load_q = [&](const Piece& x) {
+      constexpr int kCopies = FP8 ? 1 : 4, kPanelBytes = FP8 ? 4096 : 16384;
+      if (withhold) return;
+      uint64_t* bar = FP8 ? &bars.q_raw : &bars.q_full[nq % 3];
+      if (elect_one()) {
+        mbar_arrive_expect_tx(bar, (uint32_t)(kCopies * G * a.tpt * D * 2));
+        for (int w = 0; w < kCopies; ++w)
+          for (int pn = 0; pn < C::kPanels; ++pn)
+            tma_load_3d(smem + (FP8 ? C::kOffRaw : C::kOffQ) + pn * kPanelBytes + w * 4096, &a.tm_q, bar, pn * 64, x.h * G,
+                        x.q.start + x.tok);
       }
+      __syncwarp();
+      ++nq;
+    };
+    bool ok = true, more_next = more;
+    Piece next = p;
+    auto seek = [&] {  // the next piece that has keys
+      while (more_next && next.jb == next.je) more_next = walk.step<true>(a, next);
+    };
+    seek();
+    if (FP8 && more_next) load_q(next);
+    while (ok && more_next) {
+      p = next;
+      if (!FP8) {
+        if (!(ok = warp_wait(&bars.q_free, (n & 1) ^ 1, abort_flag))) break;
+        load_q(p);
+      }
+      more_next = walk.step<true>(a, next);
+      seek();
       if (!(ok = warp_wait(&bars.q_full[n % 3], (n / 3) & 1, abort_flag))) break;
+      if (FP8 && more_next) load_q(next);
       ++n;
       for (int jj = p.jb; jj < p.je; ++jj, ++g) {
         const int s = g % C::kKStages, b = g & 1;
@@ -220,7 +234,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
       }
     }
     // a copy of Q still on its way after an abort lands before the CTA can exit
-    if (nq > n) mbar_wait_drain(FP8 ? &bars.q_raw : &bars.q_full[n % 3], FP8 ? n & 1 : (n / 3) & 1);
+    if (nq > n) mbar_wait_drain(FP8 ? &bars.q_raw : &bars.q_full[n % 3], FP8 ? (nq - 1) & 1 : (n / 3) & 1);
     if (elect_one()) mma_commit(&bars.teardown[0]);
     __syncwarp();
     mbar_wait_drain(&bars.teardown[0], 0);
@@ -230,7 +244,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     const uint64_t dv = Tile<D>::desc_v(smem + C::kOffV);
     int g = 0, n = 0;  // key blocks, tiles
     bool ok = true;
-    for (; ok && more; more = walk.step(a, p)) {
+    for (; ok && more; more = walk.step<true>(a, p)) {
       if (p.jb == p.je) continue;
       for (int jj = p.jb; jj < p.je; ++jj, ++g) {
         const int s = g % C::kVStages, b = g & 1;
@@ -259,11 +273,11 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     constexpr int kCS = FP8 ? C::kCStages : 1;
     int g = 0, n = 0;
     bool ok = true;
-    for (; ok && more; more = walk.step(a, p)) {
+    for (; ok && more; more = walk.step<true>(a, p)) {
       if (p.je > p.jb) {
         if (tid < 128) {  // Q, by four of the warps
-          if (!(ok = warp_wait(&bars.q_raw, n & 1, abort_flag))) break;
-          convert_q<D>(smem + C::kOffQ, q_ex[n % 3], tid);
+          if (!(ok = warp_wait2(&bars.q_raw, n & 1, &bars.q_free, (n & 1) ^ 1, abort_flag))) break;
+          convert_q<D>(smem + C::kOffRaw, smem + C::kOffQ, q_ex[n % 3], tid);
           conv_arrive(&bars.q_full[n % 3], nullptr, lane);
         }
         ++n;
@@ -295,7 +309,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     }
     int g = 0, n = 0;
     bool ok = true;
-    for (; ok && more; more = walk.step(a, p)) {
+    while (ok && more) {
       const int nb = p.je - p.jb;
       float sl2 = a.scale_log2;
       if (FP8 && nb > 0) {  // (their place is written again three tiles on, after this warp has read the first S of this one)
@@ -372,6 +386,10 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
         tc_fence_before();
         mbar_arrive(&bars.p_full[b]);
       }
+      const bool whole = p.whole();
+      const long long row0 = (long long)(p.q.start + p.tok) * a.Hq + p.h * G;  // row r: token r / G, head r % G
+      const long long part0 = ((long long)blockIdx.x * 2 + (p.jb == 0 ? 1 : 0)) * 32;
+      more = walk.step<true>(a, p);  // while the last product runs
       // ---- the tile's four quarters joined: o = sum_w 2^(m_w - m) O_w / sum_w 2^(m_w - m) l_w
       if (ok && nb > 0) ok = mbar_wait(&bars.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag);
       ok = __all_sync(0xffffffffu, ok);
@@ -379,9 +397,6 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
         ok = false;
         break;
       }
-      const bool whole = p.whole();
-      const long long row0 = (long long)(p.q.start + p.tok) * a.Hq + p.h * G;  // row r: token r / G, head r % G
-      const long long part0 = ((long long)blockIdx.x * 2 + (p.jb == 0 ? 1 : 0)) * 32;
       stats[warp * 32 + lane] = make_float2(m_ref, l_sum);
       if (nb > 0) tc_fence_after();
       for (int r0 = 0; r0 < rows; r0 += C::kJoinRows) {  // kJoinRows rows at a time

@@ -255,6 +255,8 @@ struct Walk {
     first = true;
     return g.use ? true : step(a, p);
   }
+  // kOne: most requests are one tile per key head.
+  template <bool kOne = false>
   __device__ __forceinline__ bool step(const PagedArgs& a, Piece& p) {
     if (first) {  // put off until here: the first piece's copies do not wait for it
       first = false;
@@ -262,10 +264,17 @@ struct Walk {
       advance(a, last_len);
     }
     while (pos < p1) {
-      const int len = head + tiles_len(a, q, i + 1, nt) - pos;
+      const bool again = kOne && nt == 1 && p.r == r;  // the same tile of the next key head
+      const int len = again ? last_len : head + tiles_len(a, q, i + 1, nt) - pos;
       p.r = r;
       p.h = h;
-      const bool use = cut(a, q, i, pos, len, p0, p1, p);
+      bool use = true;
+      if (again && p0 <= pos && pos + len <= p1) {
+        p.jb = 0;
+        p.je = p.nb;
+      } else {
+        use = cut(a, q, i, pos, len, p0, p1, p);
+      }
       advance(a, len);
       if (use) return true;
     }
