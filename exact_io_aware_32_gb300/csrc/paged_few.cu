@@ -47,7 +47,7 @@ struct FCfg {
   static constexpr int kJoinRows = (D == 64 ? 16 : 8) / (FP8_ ? 2 : 1), kJoinStride = D + 4;
   static constexpr int kOffJoin = kOffC + kCStages * kCodeBytes;
   static constexpr int kOffBar = kOffJoin + 4 * kJoinRows * kJoinStride * 4 + 4 * 32 * 8;
-  static constexpr int kSmemBytes = kOffBar + 512 + 1024;  // barriers, alignment slack
+  static constexpr int kSmemBytes = kOffBar + 768 + 1024;  // barriers, alignment slack
   static_assert(kSmemBytes <= 232448, "shared memory");
   static constexpr uint32_t kColS = 0, kColP = 256, kColO = 384, kTmemCols = 512;  // S and P twice
   static constexpr int kWarpTmaK = 4, kWarpTmaV = 5, kWarpPv = 6, kWarpQk = 7, kWarpConv = 8, kConvWarps = 8;
@@ -61,10 +61,11 @@ struct FBars {
   uint64_t k_full[6], k_empty[6], v_full[4], v_empty[4], c_full[6], c_empty[6];
   uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], o_free;
   uint64_t teardown[2];
+  PieceRing ring;
   uint32_t tmem_base;
   int abort;
 };
-static_assert(sizeof(FBars) <= 400, "barriers exceed their shared memory");
+static_assert(sizeof(FBars) <= 672, "barriers exceed their shared memory");
 
 template <int D, bool FP8, bool CAUSAL>
 __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel(const __grid_constant__ PagedArgs a) {
@@ -77,7 +78,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
   // scales (E4M3 caches), of this tile and the two before
   Range& range = *reinterpret_cast<Range*>(smem + C::kOffJoin);
   auto& sums = *reinterpret_cast<int(*)[C::kThreads / 32]>(smem + C::kOffJoin + 256);
-  auto& q_ex = *reinterpret_cast<uint8_t(*)[3][32]>(smem + C::kOffBar + 400);
+  auto& q_ex = *reinterpret_cast<uint8_t(*)[3][32]>(smem + C::kOffBar + 672);
   static_assert(sizeof(Range) <= 256, "the sums follow the range");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.Hq / a.Hkv;
@@ -111,6 +112,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
       mbar_init(&bars.teardown[s], 1);
     }
     mbar_init(&bars.o_free, 128);
+    bars.ring.init(7 + (FP8 ? C::kConvWarps : 0));  // four softmax warps, V, Q K^T, P V, converters
     fence_mbar_init();
   }
   // rows of Q that no copy fills (G that does not divide 32, short tiles) are zeros, not leftovers
@@ -130,28 +132,33 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     if (threadIdx.x == 0) static_cast<Parts*>(a.parts)[blockIdx.x] = Parts{};
     return;
   }
-  Walk walk;
+  PieceReader in(bars.ring, abort_flag, lane);
   Piece p;
-  bool more = walk.begin(a, range, p);
-  const int per = range.per;
-  __syncthreads();  // all have read the range: the join may write there
   if (warp == C::kWarpTmaK) {
-    // ------------------------------------------------------------ keys
+    // ------------------------------------------------------------ keys, and the walk for all
+    Walk walk;
+    bool more = walk.begin(a, range, p);
+    const int per = range.per;
     Parts parts{};
-    int g = 0, nk = 0;  // key blocks, and loads issued
-    bool ok = true;
-    for (; ok && more; more = walk.step<true>(a, p)) {
+    int g = 0, nk = 0, n = 0;  // key blocks, loads issued, pieces
+    bool ok = bars.ring.tell(n++, p, more, 0, 0, lane, abort_flag);
+    for (Piece next = p; ok && more; p = next) {
       note_piece(a, parts, p, walk, per);
       const int nb = p.je - p.jb;
-      if (nb == 0) continue;
       Pages pages;
-      pages.begin(a, p, lane);
-      for (int j = 0; j < nb; ++j, ++g) {
-        const int jj = p.jb + j, page_now = pages.of(a, p, jj, lane);
-        const int s = g % C::kKStages;
-        if (!(ok = warp_wait(&bars.k_empty[s], ((g / C::kKStages) & 1) ^ 1, abort_flag))) break;
-        load_block<D, FP8>(a, p, jj, page_now, lane, &a.tm_k, smem + C::kOffK + s * C::kKBytes, &bars.k_full[s]);
-        nk = g + 1;
+      if (nb > 0) pages.begin(a, p, lane);
+      for (int j = 0; j < max(nb, 1); ++j) {
+        if (nb > 0) {
+          const int jj = p.jb + j, page_now = pages.of(a, p, jj, lane);
+          const int s = g % C::kKStages;
+          if (!(ok = warp_wait(&bars.k_empty[s], ((g / C::kKStages) & 1) ^ 1, abort_flag))) break;
+          load_block<D, FP8>(a, p, jj, page_now, lane, &a.tm_k, smem + C::kOffK + s * C::kKBytes, &bars.k_full[s]);
+          nk = ++g;
+        }
+        if (j == 0) {  // before this piece's other blocks: the Q K^T warp looks one piece ahead
+          more = walk.step<true>(a, next);
+          if (!(ok = bars.ring.tell(n++, next, more, 0, 0, lane, abort_flag))) break;
+        }
       }
     }
     if (lane == 0) static_cast<Parts*>(a.parts)[blockIdx.x] = parts;
@@ -165,7 +172,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     uint64_t *full = FP8 ? bars.c_full : bars.v_full, *empty = FP8 ? bars.c_empty : bars.v_empty;
     int g = 0, nv = 0;
     bool ok = true;
-    for (; ok && more; more = walk.step<true>(a, p)) {
+    while (ok && in.next(p)) {
       if (p.jb == p.je) continue;
       Pages pages;
       pages.begin(a, p, lane);
@@ -201,12 +208,15 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
       __syncwarp();
       ++nq;
     };
-    bool ok = true, more_next = more;
-    Piece next = p;
+    bool ok = true;
+    Piece next;
     auto seek = [&] {  // the next piece that has keys
-      while (more_next && next.jb == next.je) more_next = walk.step<true>(a, next);
+      bool more;
+      do more = in.next(next);
+      while (more && next.jb == next.je);
+      return more;
     };
-    seek();
+    bool more_next = seek();
     if (FP8 && more_next) load_q(next);
     while (ok && more_next) {
       p = next;
@@ -214,8 +224,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
         if (!(ok = warp_wait(&bars.q_free, (n & 1) ^ 1, abort_flag))) break;
         load_q(p);
       }
-      more_next = walk.step<true>(a, next);
-      seek();
+      more_next = seek();
       if (!(ok = warp_wait(&bars.q_full[n % 3], (n / 3) & 1, abort_flag))) break;
       if (FP8 && more_next) load_q(next);
       ++n;
@@ -244,7 +253,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     const uint64_t dv = Tile<D>::desc_v(smem + C::kOffV);
     int g = 0, n = 0;  // key blocks, tiles
     bool ok = true;
-    for (; ok && more; more = walk.step<true>(a, p)) {
+    while (ok && in.next(p)) {
       if (p.jb == p.je) continue;
       for (int jj = p.jb; jj < p.je; ++jj, ++g) {
         const int s = g % C::kVStages, b = g & 1;
@@ -273,7 +282,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     constexpr int kCS = FP8 ? C::kCStages : 1;
     int g = 0, n = 0;
     bool ok = true;
-    for (; ok && more; more = walk.step<true>(a, p)) {
+    while (ok && in.next(p)) {
       if (p.je > p.jb) {
         if (tid < 128) {  // Q, by four of the warps
           if (!(ok = warp_wait2(&bars.q_raw, n & 1, &bars.q_free, (n & 1) ^ 1, abort_flag))) break;
@@ -308,7 +317,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
       tmem_st_wait();
     }
     int g = 0, n = 0;
-    bool ok = true;
+    bool more = in.next(p), ok = named_bar_and(1, 128, in.ok);
     while (ok && more) {
       const int nb = p.je - p.jb;
       float sl2 = a.scale_log2;
@@ -389,7 +398,10 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
       const bool whole = p.whole();
       const long long row0 = (long long)(p.q.start + p.tok) * a.Hq + p.h * G;  // row r: token r / G, head r % G
       const long long part0 = ((long long)blockIdx.x * 2 + (p.jb == 0 ? 1 : 0)) * 32;
-      more = walk.step<true>(a, p);  // while the last product runs
+      if (ok) {
+        more = in.next(p);
+        ok = in.ok;
+      }
       // ---- the tile's four quarters joined: o = sum_w 2^(m_w - m) O_w / sum_w 2^(m_w - m) l_w
       if (ok && nb > 0) ok = mbar_wait(&bars.pv_done[(g - 1) & 1], ((g - 1) >> 1) & 1, abort_flag);
       ok = __all_sync(0xffffffffu, ok);

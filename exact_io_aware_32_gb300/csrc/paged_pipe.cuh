@@ -325,6 +325,61 @@ __device__ __forceinline__ void st_global_32(void* p, const uint32_t (&v)[8], bo
   }
 }
 
+// The pieces of a CTA's range, worked out by its loading warp and told to the
+// other warps: a step of the walk takes about 1000 cycles, most of them waiting
+// for instructions that run once per tile, and stood in every role's chain.
+constexpr int kRing = 4;
+struct alignas(16) PieceRing {
+  int4 at[kRing][3];
+  uint64_t full[kRing], empty[kRing];
+  __device__ __forceinline__ void init(int readers) {  // readers: warps
+    for (int s = 0; s < kRing; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], readers);
+    }
+  }
+  // The n-th piece (more: not the end), with two numbers of the caller's.
+  __device__ __forceinline__ bool tell(int n, const Piece& p, bool more, int x, int y, int lane, volatile int* abort_flag) {
+    const int s = n % kRing;
+    if (!warp_wait(&empty[s], ((n / kRing) & 1) ^ 1, abort_flag)) return false;
+    if (lane == 0) {
+      at[s][0] = make_int4(p.q.start, p.q.n, p.q.len, more);
+      at[s][1] = make_int4(p.h, p.tok, p.jb, p.je);
+      at[s][2] = make_int4(p.nb, p.r, x, y);
+      mbar_arrive(&full[s]);
+    }
+    __syncwarp();
+    return true;
+  }
+};
+// A reading warp's place in the ring: for (bool more = in.next(p); more; more = in.next(p)).
+struct PieceReader {
+  PieceRing& ring;
+  volatile int* abort_flag;
+  int lane, n = 0, x = 0, y = 0;
+  bool ok = true;
+  __device__ __forceinline__ PieceReader(PieceRing& ring_, volatile int* flag, int lane_)
+      : ring(ring_), abort_flag(flag), lane(lane_) {}
+  __device__ __forceinline__ bool next(Piece& p) {  // false: the end, or (ok) the wait ran out
+    const int s = n % kRing;
+    if (!(ok = warp_wait(&ring.full[s], (n / kRing) & 1, abort_flag))) return false;
+    ++n;
+    const int4 u = ring.at[s][0], v = ring.at[s][1], w = ring.at[s][2];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&ring.empty[s]);
+    p.q = {u.x, u.y, u.z};
+    p.h = v.x;
+    p.tok = v.y;
+    p.jb = v.z;
+    p.je = v.w;
+    p.nb = w.x;
+    p.r = w.y;
+    x = w.z;
+    y = w.w;
+    return u.w != 0;
+  }
+};
+
 // The part descriptor of this CTA, kept up by one thread as it walks the pieces.
 __device__ __forceinline__ void note_piece(const PagedArgs& a, Parts& s, const Piece& p, const Walk& walk,
                                            int per) {
