@@ -69,6 +69,7 @@ struct CBars {
   uint64_t s_full[2], p_full[2], o_done[2], o_free[2];  // (one half: o_done follows every P V)
   uint64_t s_free;                                      // one half: S is in registers
   uint64_t teardown;
+  PieceRing ring;
   uint32_t tmem_base;
   int abort;
   Range range;
@@ -125,6 +126,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     }
     mbar_init(&bars.s_free, 128);
     mbar_init(&bars.teardown, 1);
+    bars.ring.init(4 * C::kTiles + 1 + (FP8 ? C::kConvWarps : 0));  // softmax, MMA and converter warps
     fence_mbar_init();
   }
   if (warp == C::kWarpMma) {
@@ -140,9 +142,17 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     if (threadIdx.x == 0) static_cast<Parts*>(a.parts)[blockIdx.x] = Parts{};
     return;
   }
-  Walk walk;
-  Piece p;
-  bool more = walk.begin(a, bars.range, p);
+  PieceReader in(bars.ring, abort_flag, lane);
+  Piece p = bars.range.first;
+  const bool first = bars.range.use;  // the first piece is there already
+  int blocks[2];                      // key blocks that each half sees of it
+  half_blocks<C::kTiles>(a, p, blocks);
+  auto next_piece = [&] {
+    const bool there = in.next(p);
+    blocks[0] = in.x;
+    blocks[1] = in.y;
+    return there;
+  };
 
   if (warp == C::kWarpTma) {
     // ------------------------------------------------------------ TMA producer
@@ -171,30 +181,45 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
       }
       withhold = false;
     };
-    for (; ok && more; more = walk.step(a, p)) {
-      int nb[2];
-      half_blocks<C::kTiles>(a, p, nb);
-      const int nbm = max(nb[0], nb[1]);
+    Walk walk;
+    walk.begin(bars.range);
+    Piece next = p;
+    int next_nb[2] = {blocks[0], blocks[1]}, told = 0;
+    bool more = true;
+    auto step = [&] {  // works out the next piece and tells the others
+      more = walk.step(a, next);
+      half_blocks<C::kTiles>(a, next, next_nb);
+      ok = bars.ring.tell(told++, next, more, next_nb[0], next_nb[1], lane, abort_flag);
+    };
+    if (!first) step();
+    while (ok && more) {
+      p = next;
+      blocks[0] = next_nb[0];
+      blocks[1] = next_nb[1];
+      note_piece(a, parts, p, walk, bars.range.per);
+      const int nbm = max(blocks[0], blocks[1]);
       Pages pages;
       if (nbm > 0) pages.begin(a, p, lane);
-      if (nb[0] > 0) load_q(0);
-      for (int j = 0; ok && j < nbm; ++j, ++g) {
-        const int jj = p.jb + j, page_now = pages.of(a, p, jj, lane);
-        const int sk = g % C::kKStages;
-        if (!(ok = warp_wait(&bars.k_empty[sk], ((g / C::kKStages) & 1) ^ 1, abort_flag))) break;
-        load_block<D, FP8>(a, p, jj, page_now, lane, &a.tm_k, smem + C::kOffK + sk * C::kKBytes, &bars.k_full[sk]);
-        nk = g + 1;
-        if (C::kTiles == 2 && j == 0 && nb[1] > 0) {
-          load_q(1);
-          if (!ok) break;
+      if (blocks[0] > 0) load_q(0);
+      for (int j = 0; ok && j < max(nbm, 1); ++j) {
+        if (nbm > 0) {
+          const int jj = p.jb + j, page_now = pages.of(a, p, jj, lane);
+          const int sk = g % C::kKStages;
+          if (!(ok = warp_wait(&bars.k_empty[sk], ((g / C::kKStages) & 1) ^ 1, abort_flag))) break;
+          load_block<D, FP8>(a, p, jj, page_now, lane, &a.tm_k, smem + C::kOffK + sk * C::kKBytes, &bars.k_full[sk]);
+          nk = g + 1;
+          if (C::kTiles == 2 && j == 0 && blocks[1] > 0) {
+            load_q(1);
+            if (!ok) break;
+          }
+          const int sv = g % kS;
+          if (!(ok = warp_wait(&v_empty[sv], ((g / kS) & 1) ^ 1, abort_flag))) break;
+          load_block<D, FP8>(a, p, jj, page_now, lane, &a.tm_v,
+                             smem + (FP8 ? C::kOffC + sv * C::kCodeBytes : C::kOffV + sv * C::kTileBytes), &v_full[sv]);
+          nv = ++g;
         }
-        const int sv = g % kS;
-        if (!(ok = warp_wait(&v_empty[sv], ((g / kS) & 1) ^ 1, abort_flag))) break;
-        load_block<D, FP8>(a, p, jj, page_now, lane, &a.tm_v,
-                           smem + (FP8 ? C::kOffC + sv * C::kCodeBytes : C::kOffV + sv * C::kTileBytes), &v_full[sv]);
-        nv = g + 1;
+        if (j == 0) step();  // while those are on their way
       }
-      note_piece(a, parts, p, walk, bars.range.per);
     }
     if (lane == 0) static_cast<Parts*>(a.parts)[blockIdx.x] = parts;
     // Let every issued copy land before the CTA can exit (an earlier load's slot
@@ -225,61 +250,54 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     };
     int g = 0, nq[2] = {0, 0}, np[2] = {0, 0};  // key blocks; tiles and P blocks of each half so far
     bool ok = true;
-    Piece next;
-    for (bool more_next; ok && more; p = next, more = more_next) {
-      int nb[2];
-      half_blocks<C::kTiles>(a, p, nb);
-      const int nbm = max(nb[0], nb[1]);
+    for (bool more = first || next_piece(); ok && more; more = next_piece()) {
+      const int nbm = max(blocks[0], blocks[1]);
       if (nbm > 0) {
         // S of the first block
         ok = warp_wait(&bars.k_full[g % C::kKStages], (g / C::kKStages) & 1, abort_flag);
         if (C::kTiles == 1 && ok) ok = warp_wait(&bars.s_free, (g & 1) ^ 1, abort_flag);
         for (int t = 0; t < C::kTiles && ok; ++t)
-          if (nb[t] > 0) {
+          if (blocks[t] > 0) {
             if (!(ok = warp_wait(&bars.q_full[t][nq[t] & 1], (nq[t] >> 1) & 1, abort_flag))) break;
             tc_fence_after();
-            if (elect_one()) issue_s(t, C::kTiles == 2 ? t : nq[0] & 1, g % C::kKStages, nb[t] == 1);
+            if (elect_one()) issue_s(t, C::kTiles == 2 ? t : nq[0] & 1, g % C::kKStages, blocks[t] == 1);
             __syncwarp();
           }
         if (!ok) break;
         if (elect_one()) mma_commit(&bars.k_empty[g % C::kKStages]);
         __syncwarp();
       }
-      // the next piece is worked out here, while the softmax has this one's first S (about 1400 cycles that would
-      // otherwise lie between this tile's last product and the next one's first)
-      next = p;
-      more_next = walk.step(a, next);
       if constexpr (C::kTiles == 2) {
         // Per key block j and half t: O_t += P_t V_j, then at once S_t for block j + 1 (its columns are P_t's, which the
         // products of one thread have read by then, as they execute in issue order).
         for (int j = 0; j < nbm; ++j, ++g) {
           const int s = g % C::kVStages;
           const uint32_t ph = (g / C::kVStages) & 1;
-          const int v_last = j < nb[1] ? 1 : 0;  // the half whose PV reads V_j last
+          const int v_last = j < blocks[1] ? 1 : 0;  // the half whose PV reads V_j last
           const int jn = j + 1, sn = (g + 1) % C::kKStages;
           const bool k_next = jn < nbm;
-          ok = warp_wait3(&bars.v_full[s], ph, j < nb[0] ? &bars.p_full[0] : &bars.v_full[s],
-                          j < nb[0] ? (np[0] & 1) : ph, k_next ? &bars.k_full[sn] : &bars.v_full[s],
+          ok = warp_wait3(&bars.v_full[s], ph, j < blocks[0] ? &bars.p_full[0] : &bars.v_full[s],
+                          j < blocks[0] ? (np[0] & 1) : ph, k_next ? &bars.k_full[sn] : &bars.v_full[s],
                           k_next ? ((g + 1) / C::kKStages) & 1 : ph, abort_flag);
           if (!ok) break;
           const int keys = p.q.len - (p.jb + j) * 128, steps = pv_steps(keys);
           if (!FP8 && keys < steps * 16) zero_rows<D>(smem + C::kOffV + s * C::kTileBytes, keys, steps * 16, lane);
           for (int t = 0; t < 2; ++t) {
-            if (j < nb[t]) {
+            if (j < blocks[t]) {
               if (t == 1 && !(ok = warp_wait(&bars.p_full[1], np[1] & 1, abort_flag))) break;
               // a tile's first PV overwrites O: the tile before has been read out
               if (j == 0 && !(ok = warp_wait(&bars.o_free[t], (nq[t] & 1) ^ 1, abort_flag))) break;
               tc_fence_after();
               if (elect_one()) {
                 issue_pv(t, s, steps, j == 0);
-                if (j == nb[t] - 1) mma_commit(&bars.o_done[t]);
+                if (j == blocks[t] - 1) mma_commit(&bars.o_done[t]);
                 if (t == v_last) mma_commit(&bars.v_empty[s]);
               }
               __syncwarp();
               ++np[t];
             }
-            if (jn < nb[t]) {
-              if (elect_one()) issue_s(t, t, sn, jn == nb[t] - 1);
+            if (jn < blocks[t]) {
+              if (elect_one()) issue_s(t, t, sn, jn == blocks[t] - 1);
               __syncwarp();
             }
           }
@@ -318,7 +336,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
           __syncwarp();
         }
       }
-      for (int t = 0; t < 2; ++t) nq[t] += nb[t] > 0;
+      for (int t = 0; t < 2; ++t) nq[t] += blocks[t] > 0;
     }
     if (elect_one()) mma_commit(&bars.teardown);
     __syncwarp();
@@ -329,10 +347,8 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     constexpr int kCS = FP8 ? C::kCStages : 1;
     int g = 0;
     bool ok = true;
-    for (; ok && more; more = walk.step(a, p)) {
-      int nb[2];
-      half_blocks<C::kTiles>(a, p, nb);
-      const int nbm = max(nb[0], nb[1]);
+    for (bool more = first || next_piece(); ok && more; more = next_piece()) {
+      const int nbm = max(blocks[0], blocks[1]);
       for (int j = 0; ok && j < nbm; ++j, ++g) {
         const int vs = g % C::kVStages, cs = g % kCS;
         ok = warp_wait2(&bars.c_full[cs], (g / kCS) & 1, &bars.v_empty[vs], ((g / C::kVStages) & 1) ^ 1, abort_flag);
@@ -355,10 +371,8 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     const bool o32 = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
     int np = 0, nq = 0;  // blocks and tiles of this half so far
     bool ok = true;
-    for (; ok && more; more = walk.step(a, p)) {
-      int nb2[2];
-      half_blocks<C::kTiles>(a, p, nb2);
-      const int nb = nb2[t];
+    for (bool more = first || next_piece(); ok && more; more = next_piece()) {
+      const int nb = t ? blocks[1] : blocks[0];
       const int tok0 = p.tok + t * a.tpt1, tok = tok0 + rt;
       const int off = p.q.len - p.q.n;  // causal: token i sees keys 0 .. i + off
       const bool valid = rt < a.tpt1 && tok < p.q.n;

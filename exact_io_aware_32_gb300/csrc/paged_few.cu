@@ -133,15 +133,21 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     return;
   }
   PieceReader in(bars.ring, abort_flag, lane);
-  Piece p;
+  Piece p = range.first;
+  const bool first = range.use;  // the first piece is there already
+  Walk walk;
+  if (warp == C::kWarpTmaK) walk.begin(range);
+  const int per = range.per;
+  __syncthreads();  // all have read the range: the join may write there
   if (warp == C::kWarpTmaK) {
     // ------------------------------------------------------------ keys, and the walk for all
-    Walk walk;
-    bool more = walk.begin(a, range, p);
-    const int per = range.per;
     Parts parts{};
     int g = 0, nk = 0, n = 0;  // key blocks, loads issued, pieces
-    bool ok = bars.ring.tell(n++, p, more, 0, 0, lane, abort_flag);
+    bool more = true, ok = true;
+    if (!first) {
+      more = walk.step<true>(a, p);
+      ok = bars.ring.tell(n++, p, more, 0, 0, lane, abort_flag);
+    }
     for (Piece next = p; ok && more; p = next) {
       note_piece(a, parts, p, walk, per);
       const int nb = p.je - p.jb;
@@ -172,7 +178,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     uint64_t *full = FP8 ? bars.c_full : bars.v_full, *empty = FP8 ? bars.c_empty : bars.v_empty;
     int g = 0, nv = 0;
     bool ok = true;
-    while (ok && in.next(p)) {
+    for (bool more = first || in.next(p); ok && more; more = in.next(p)) {
       if (p.jb == p.je) continue;
       Pages pages;
       pages.begin(a, p, lane);
@@ -209,14 +215,12 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
       ++nq;
     };
     bool ok = true;
-    Piece next;
-    auto seek = [&] {  // the next piece that has keys
-      bool more;
-      do more = in.next(next);
-      while (more && next.jb == next.je);
+    Piece next = p;
+    auto seek = [&](bool more) {  // to a piece that has keys
+      while (more && next.jb == next.je) more = in.next(next);
       return more;
     };
-    bool more_next = seek();
+    bool more_next = seek(first || in.next(next));
     if (FP8 && more_next) load_q(next);
     while (ok && more_next) {
       p = next;
@@ -224,7 +228,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
         if (!(ok = warp_wait(&bars.q_free, (n & 1) ^ 1, abort_flag))) break;
         load_q(p);
       }
-      more_next = seek();
+      more_next = seek(in.next(next));
       if (!(ok = warp_wait(&bars.q_full[n % 3], (n / 3) & 1, abort_flag))) break;
       if (FP8 && more_next) load_q(next);
       ++n;
@@ -253,7 +257,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     const uint64_t dv = Tile<D>::desc_v(smem + C::kOffV);
     int g = 0, n = 0;  // key blocks, tiles
     bool ok = true;
-    while (ok && in.next(p)) {
+    for (bool more = first || in.next(p); ok && more; more = in.next(p)) {
       if (p.jb == p.je) continue;
       for (int jj = p.jb; jj < p.je; ++jj, ++g) {
         const int s = g % C::kVStages, b = g & 1;
@@ -282,7 +286,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     constexpr int kCS = FP8 ? C::kCStages : 1;
     int g = 0, n = 0;
     bool ok = true;
-    while (ok && in.next(p)) {
+    for (bool more = first || in.next(p); ok && more; more = in.next(p)) {
       if (p.je > p.jb) {
         if (tid < 128) {  // Q, by four of the warps
           if (!(ok = warp_wait2(&bars.q_raw, n & 1, &bars.q_free, (n & 1) ^ 1, abort_flag))) break;
@@ -317,7 +321,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
       tmem_st_wait();
     }
     int g = 0, n = 0;
-    bool more = in.next(p), ok = named_bar_and(1, 128, in.ok);
+    bool more = first || in.next(p), ok = first || named_bar_and(1, 128, in.ok);
     while (ok && more) {
       const int nb = p.je - p.jb;
       float sl2 = a.scale_log2;

@@ -240,8 +240,8 @@ struct Walk {
     } while (q.n == 0);
     nt = tiles_of(a, q);
   }
-  __device__ __forceinline__ bool begin(const PagedArgs& a, const Range& g, Piece& p) {
-    p = g.first;
+  __device__ __forceinline__ void begin(const Range& g) {
+    const Piece& p = g.first;
     p0 = g.p0;
     p1 = g.p1;
     head = g.head;
@@ -253,6 +253,10 @@ struct Walk {
     i = g.i;
     nt = g.nt;
     first = true;
+  }
+  __device__ __forceinline__ bool begin(const PagedArgs& a, const Range& g, Piece& p) {
+    begin(g);
+    p = g.first;
     return g.use ? true : step(a, p);
   }
   // kOne: most requests are one tile per key head.
