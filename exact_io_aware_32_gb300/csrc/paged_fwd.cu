@@ -217,10 +217,13 @@ int plan_paged(int T, int R, int Hq, int Hkv, int d, int fp8, int max_new, int m
   // Requests of mostly far fewer tokens than the largest: decoding requests beside chunks of prompts. A tile of 128 rows
   // for a few takes the chunk kernel 3000 cycles per key block and the decoding kernel a third of that, but a second
   // kernel with its join costs 20 us, so each takes its requests only where there may be many keys. Measured with one
-  // chunk of 777 tokens beside 128 requests of up to 8192 keys, 32 heads over 8 of 128: E4M3 454 us in the chunk kernel,
-  // 326 us in both, bf16 453 and 422 us; beside 32 of up to 4096 keys, 16 heads over 4: 76 and 89 us, 64 and 87 us.
+  // chunk of 777 tokens beside R requests of one token and up to n keys, d = 128, chunk kernel alone and both:
+  //   R = 128, n = 8192, 32 heads over 8   E4M3 452 and 300 us, bf16 451 and 409 us
+  //   R = 128, n = 4096, 32 heads over 8        287 and 191 us,      242 and 237 us
+  //   R = 64,  n = 8192, 16 heads over 4        158 and 136 us,      144 and 159 us
+  //   R = 64,  n = 4096, 16 heads over 4        100 and 101 us,       88 and 106 us
   const long long keys = (long long)R * max_keys * Hkv;
-  if (G <= 32 && (long long)T * 2 < (long long)R * max_new && keys >= (fp8 ? 3000000ll : 8000000ll)) {
+  if (G <= 32 && (long long)T * 2 < (long long)R * max_new && keys >= (fp8 ? 1500000ll : 4000000ll)) {
     const int most = 32 / G;
     p[1] = p[0];
     p[1].n_min = most + 1;
