@@ -18,9 +18,16 @@
 // Persistent CTAs over ranges of the row of tiles (paged_work.cuh), rings and
 // barriers counting on across tiles.
 //
-// Warp roles: 0-3 softmax and epilogue; 4 copies keys, 5 values; 6 issues P V and
-// owns TMEM, 7 copies Q and issues Q K^T; with E4M3 caches eight converter warps
-// (value codes to f16, Q to its two parts).
+// Warp roles: 0-3 softmax and epilogue; 4 walks the range, tells the others its
+// pieces and copies keys, 5 copies values; 6 issues P V and owns TMEM, 7 copies Q
+// and issues Q K^T; with E4M3 caches eight converter warps (value codes to f16, Q
+// to its two parts: by four of them 107 us instead of 100 where tiles are short).
+//
+// Measured, d = 128, 8 key heads, 32 query heads: 64 requests of up to 8192 keys
+// 158 us, 6.6 TB/s of keys and values (bound by them); 48 of up to 16384, E4M3
+// caches, 138 us (the tensor cores, which take 128 rows, and the bytes about alike);
+// 256 requests of up to 1000 keys 88 and 100 us, of up to 100 keys 45 and 55 us
+// (bound by a tile's chain: its first S, softmax, last product, join).
 #include "paged_pipe.cuh"
 
 namespace fa {
@@ -92,7 +99,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
   if (threadIdx.x == 32) {
     bars.abort = 0;
     mbar_init(&bars.q_raw, 1);
-    for (int s = 0; s < 3; ++s) mbar_init(&bars.q_full[s], FP8 ? 4 : 1);
+    for (int s = 0; s < 3; ++s) mbar_init(&bars.q_full[s], FP8 ? C::kConvWarps : 1);
     mbar_init(&bars.q_free, 1);
     for (int s = 0; s < 6; ++s) {
       mbar_init(&bars.k_full[s], 1);
@@ -288,11 +295,9 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     bool ok = true;
     for (bool more = first || in.next(p); ok && more; more = in.next(p)) {
       if (p.je > p.jb) {
-        if (tid < 128) {  // Q, by four of the warps
-          if (!(ok = warp_wait2(&bars.q_raw, n & 1, &bars.q_free, (n & 1) ^ 1, abort_flag))) break;
-          convert_q<D>(smem + C::kOffRaw, smem + C::kOffQ, q_ex[n % 3], tid);
-          conv_arrive(&bars.q_full[n % 3], nullptr, lane);
-        }
+        if (!(ok = warp_wait2(&bars.q_raw, n & 1, &bars.q_free, (n & 1) ^ 1, abort_flag))) break;
+        convert_q<D>(smem + C::kOffRaw, smem + C::kOffQ, q_ex[n % 3], tid);
+        conv_arrive(&bars.q_full[n % 3], nullptr, lane);
         ++n;
       }
       for (int j = p.jb; j < p.je; ++j, ++g) {

@@ -180,49 +180,44 @@ __device__ __forceinline__ void split2(float x, float y, uint32_t& hi, uint32_t&
 
 // Rows 0 - 31 of Q, a [panel][32 rows][128 bytes] swizzled tile, from 64 bf16 to
 // 64 hi and 64 lo codes per 128-byte row, four times (a row quarter each) into a
-// [panel][128 rows][128 bytes] one, by 128 threads, four neighbours per row.
+// [panel][128 rows][128 bytes] one, by 256 threads, eight neighbours per row.
 // ex[row] gets the biased exponent e of the row's largest magnitude: the row was
 // scaled by 2^(134 - e).
 template <int D>
 __device__ __forceinline__ void convert_q(const uint8_t* raw, uint8_t* q, uint8_t* ex, int tid) {
   constexpr int kPanels = D / 64;
-  const int part = tid & 3, row = tid >> 2;
-  const uint32_t base = smem_u32(q);
+  const int part = tid & 7, row = tid >> 3;
   auto at = [&](int c) { return (uint32_t)(row * 128 + ((c ^ (row & 7)) << 4)); };
-  uint32_t w[kPanels][8], big = 0;  // chunks 2 part and 2 part + 1 of each panel
+  uint32_t w[kPanels][4], big = 0;  // chunk 'part' of each panel
 #pragma unroll
   for (int pn = 0; pn < kPanels; ++pn) {
+    const uint4 x = *reinterpret_cast<const uint4*>(raw + pn * 4096 + at(part));
+    w[pn][0] = x.x;
+    w[pn][1] = x.y;
+    w[pn][2] = x.z;
+    w[pn][3] = x.w;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint4 x = *reinterpret_cast<const uint4*>(raw + pn * 4096 + at(2 * part + i));
-      w[pn][4 * i] = x.x;
-      w[pn][4 * i + 1] = x.y;
-      w[pn][4 * i + 2] = x.z;
-      w[pn][4 * i + 3] = x.w;
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) big = max(big, max(w[pn][k] & 0x7FFFu, (w[pn][k] >> 16) & 0x7FFFu));
+    for (int k = 0; k < 4; ++k) big = max(big, max(w[pn][k] & 0x7FFFu, (w[pn][k] >> 16) & 0x7FFFu));
   }
-  big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
-  big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+#pragma unroll
+  for (int s = 1; s < 8; s <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, s));
   const uint32_t e = min(max(big >> 7, 8u), 254u);
   const float f = __uint_as_float((261u - e) << 23);
   if (part == 0) ex[row] = (uint8_t)e;
+  uint8_t* dst = q + at(part >> 1) + (part & 1) * 8;  // hi codes; lo codes four chunks on
+  const int lo_at = (int)at(4 + (part >> 1)) - (int)at(part >> 1);
 #pragma unroll
   for (int pn = 0; pn < kPanels; ++pn) {
-    uint32_t hi[4], lo[4];
+    uint32_t h[4], l[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      uint32_t h0, l0, h1, l1;
-      split2(__uint_as_float(w[pn][2 * k] << 16) * f, __uint_as_float(w[pn][2 * k] & 0xffff0000u) * f, h0, l0);
-      split2(__uint_as_float(w[pn][2 * k + 1] << 16) * f, __uint_as_float(w[pn][2 * k + 1] & 0xffff0000u) * f, h1, l1);
-      hi[k] = h0 | (h1 << 16);
-      lo[k] = l0 | (l1 << 16);
-    }
+    for (int k = 0; k < 4; ++k)
+      split2(__uint_as_float(w[pn][k] << 16) * f, __uint_as_float(w[pn][k] & 0xffff0000u) * f, h[k], l[k]);
+    const uint2 hi = make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+    const uint2 lo = make_uint2(l[0] | (l[1] << 16), l[2] | (l[3] << 16));
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
-      st_shared_v4(base + pn * 16384 + n * 4096 + at(part), hi[0], hi[1], hi[2], hi[3]);
-      st_shared_v4(base + pn * 16384 + n * 4096 + at(4 + part), lo[0], lo[1], lo[2], lo[3]);
+      *reinterpret_cast<uint2*>(dst + pn * 16384 + n * 4096) = hi;
+      *reinterpret_cast<uint2*>(dst + pn * 16384 + n * 4096 + lo_at) = lo;
     }
   }
 }
