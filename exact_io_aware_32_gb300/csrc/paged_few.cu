@@ -343,7 +343,8 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
       float l_sum = 0.f;        // sum of 2^(s * sl2 - m_ref) over this warp's keys so far
       for (int j = 0; ok && j < nb; ++j, ++g) {
         const int b = g & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars.s_full[b], (g >> 1) & 1, abort_flag));
+        // S, and with it the place of this block's P: free once the P V two blocks back has completed
+        ok = warp_wait2(&bars.s_full[b], (g >> 1) & 1, &bars.pv_done[b], ((g >> 1) & 1) ^ 1, abort_flag);
         if (!ok) break;
         tc_fence_after();
         uint32_t sr[32];
@@ -383,13 +384,10 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
         }
         const float2 sum = fadd2(sum2[0], sum2[1]);
         l_sum = l_sum * alpha + (sum.x + sum.y);
-        // this P's place is free once the P V two blocks back has completed; O may be rescaled once the last one has
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars.pv_done[b], ((g >> 1) & 1) ^ 1, abort_flag));
-        if (ok && rescale) ok = __all_sync(0xffffffffu, mbar_wait(&bars.pv_done[b ^ 1], ((g - 1) >> 1) & 1, abort_flag));
-        if (!ok) break;
-        tc_fence_after();
         tmem_st16(t_p + b * 64 + 16 * warp, pk);
-        if (rescale) {
+        if (rescale) {  // O, once the last P V has completed
+          if (!(ok = warp_wait(&bars.pv_done[b ^ 1], ((g - 1) >> 1) & 1, abort_flag))) break;
+          tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
             uint32_t o[32];
