@@ -15,11 +15,6 @@ using namespace fa::ptx;
 constexpr float kLn2 = 0.693147180559945309417f;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: how far the exponent reference may lag the row maximum
 
-// Pages of key block jj of a piece that hold keys (one copy each, by lane l).
-__device__ __forceinline__ int block_pages(const PagedArgs& a, const Request& q, int jj) {
-  const int rows = min(128, q.len - jj * 128), per = min(1 << a.page_shift, 128);
-  return (rows + per - 1) / per;
-}
 // A request's block table as one warp reads it: 32 entries in the lanes'
 // registers and the next 32 on their way, so that no key block waits for a load
 // from the table (one block ahead, each took 950 cycles to issue).
@@ -65,21 +60,24 @@ struct Tile {
 // one barrier. One copy per page, not one per panel: with pages of 16 tokens
 // the number of copies sets the pace (decoding, 64 requests, d = 128: 184 us
 // with a copy per panel, against 163 us with pages of 32). A page outside the
-// cache reads as zeros: its copy lies past the tensor map's end.
+// cache reads as zeros: its copy lies past the tensor map's end. (A copy may
+// complete before lane 0 has said how many bytes are to come: the phase waits
+// for that arrival.)
 template <int D, bool FP8>
 __device__ __forceinline__ void load_block(const PagedArgs& a, const Piece& p, int jj, int page, int lane,
                                            const CUtensorMap* tm, uint8_t* dst, uint64_t* bar) {
-  const int n = block_pages(a, p.q, jj), per = min(1 << a.page_shift, 128);
-  if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)(n * per * D * (FP8 ? 1 : 2)));
-  __syncwarp();
+  const int shift = min(a.page_shift, 7), rows = min(128, p.q.len - jj * 128);
+  const int n = (rows + (1 << shift) - 1) >> shift;  // pages with keys
   if (lane < n) {
-    const bool ok = page >= 0 && page < a.num_pages;
-    const int z = ok ? page * a.Hkv + p.h : a.num_pages * a.Hkv;
+    constexpr int kRow = D * (FP8 ? 1 : 2);
+    if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)((n << shift) * kRow));
+    const bool ok = (unsigned)page < (unsigned)a.num_pages;
+    const int z = (ok ? page : a.num_pages) * a.Hkv + (ok ? p.h : 0);
     const int y = (jj * 128) & ((1 << a.page_shift) - 1) & ~127;  // a 256-token page's second half
     if constexpr (FP8)
-      tma_load_3d(dst + lane * per * D, tm, bar, 0, y, z);
+      tma_load_3d(dst + (lane << shift) * kRow, tm, bar, 0, y, z);
     else
-      tma_load_5d(dst + lane * per * D * 2, tm, bar, 0, 0, 0, y >> 3, z);
+      tma_load_5d(dst + (lane << shift) * kRow, tm, bar, 0, 0, 0, y >> 3, z);
     if (!ok) atomicOr(a.status, kStatusBadLength);
   }
   __syncwarp();
