@@ -63,6 +63,7 @@ struct PagedPlan {
   int ctas;          // persistent CTAs
   int rows;          // rows of a tile
   int tpt, tpt1, whole, snap;
+  bool join;         // whether any tile may be cut
   int n_min, n_max;  // the requests that are this kernel's: those with so many new tokens
   size_t parts_bytes, o_bytes, lse_bytes;  // of the workspace, each a multiple of 256
   size_t bytes() const { return parts_bytes + o_bytes + lse_bytes; }

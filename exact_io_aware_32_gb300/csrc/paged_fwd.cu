@@ -183,7 +183,12 @@ cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<unsigned long 
 }
 
 namespace {
-PagedPlan plan_kernel(bool few, int G, int d, int fp8, int max_new, int num_sms) {
+// Tables for no more than 8 blocks a request: nothing is cut, and there is no join to launch. Measured with 32 heads over 8
+// of 128, cut and whole: 16 requests of up to 300 keys 13.0 and 10.0 us, of up to 1000 15.2 and 12.4 us, 256 of up to 1000
+// 87.4 and 84.7 us (E4M3 93.9 and 93.5 us); at 16 blocks 4 requests of up to 1500 keys 12.0 and 13.5 us.
+constexpr int kWholeBlocks = 8;
+
+PagedPlan plan_kernel(bool few, int G, int d, int fp8, int max_new, int max_keys, int num_sms) {
   PagedPlan p;
   p.few = few;
   const int halves = few || (d == 64 && !fp8) ? 1 : 2;
@@ -191,9 +196,11 @@ PagedPlan plan_kernel(bool few, int G, int d, int fp8, int max_new, int num_sms)
   p.tpt1 = std::min(max_new, (few ? 32 : 128) / G);
   p.tpt = halves * p.tpt1;
   // Cutting a tile of the chunk kernel costs two more epilogues and a join: short tiles stay whole and parts have at least
-  // four blocks (eight prompts of up to 1024 tokens, 12 heads of 64: 44 us with every cut, 35 us). The decoding kernel's
-  // parts are a few rows.
-  p.whole = few ? 0 : 8;
+  // four blocks (eight prompts of up to 1024 tokens, 12 heads of 64, when it was chosen: 44 us with every cut, 35 us). The
+  // decoding kernel's parts are a few rows: there only a call without any cut is worth it.
+  const int blocks = (max_keys >> 7) + (max_keys % 128 != 0);  // of the longest request there can be
+  p.whole = few && blocks > kWholeBlocks ? 0 : kWholeBlocks;
+  p.join = blocks > p.whole;
   p.snap = few ? 0 : 4;
   p.n_min = 0;
   p.n_max = INT32_MAX;
@@ -210,10 +217,10 @@ int plan_paged(int T, int R, int Hq, int Hkv, int d, int fp8, int max_new, int m
   const int G = Hq / Hkv;
   // no request has more than 32 rows per key head: the decoding kernel alone
   if ((long long)G * max_new <= 32) {
-    p[0] = plan_kernel(true, G, d, fp8, max_new, num_sms);
+    p[0] = plan_kernel(true, G, d, fp8, max_new, max_keys, num_sms);
     return 1;
   }
-  p[0] = plan_kernel(false, G, d, fp8, max_new, num_sms);
+  p[0] = plan_kernel(false, G, d, fp8, max_new, max_keys, num_sms);
   // Requests of mostly far fewer tokens than the largest: decoding requests beside chunks of prompts. A tile of 128 rows
   // for a few takes the chunk kernel 3000 cycles per key block and the decoding kernel a third of that, but a second
   // kernel with its join costs 20 us, so each takes its requests only where there may be many keys. Measured with one
@@ -227,7 +234,7 @@ int plan_paged(int T, int R, int Hq, int Hkv, int d, int fp8, int max_new, int m
     const int most = 32 / G;
     p[1] = p[0];
     p[1].n_min = most + 1;
-    p[0] = plan_kernel(true, G, d, fp8, most, num_sms);
+    p[0] = plan_kernel(true, G, d, fp8, most, max_keys, num_sms);
     p[0].n_max = most;
     return 2;
   }
@@ -268,7 +275,7 @@ cudaError_t launch_paged(PagedArgs a, const PagedPlan& p, void* workspace, cudaS
   a.part_o = reinterpret_cast<float*>(w + p.parts_bytes);
   a.part_lse = reinterpret_cast<float*>(w + p.parts_bytes + p.o_bytes);
   cudaError_t e = p.few ? launch_paged_few(a, p.ctas, stream) : launch_paged_chunk(a, p.ctas, stream);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || !p.join) return e;
   return a.d == 64 ? launch_join<64>(a, p, stream) : launch_join<128>(a, p, stream);
 }
 

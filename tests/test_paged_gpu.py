@@ -246,6 +246,20 @@ def test_tiles_around_the_shortest_cut(d):
         check(c, o, lse)
 
 
+@pytest.mark.parametrize("width", [64, 65])
+@pytest.mark.parametrize("most", [1, 40])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_tables_of_eight_blocks_and_one_page_more(d, fp8, most, width):
+    """Tables for 1024 keys: no tile is cut and no second kernel joins; for 1040: cuts again."""
+    lens = [(16 * width - most, most), (1000, 1), (0, 1), (16 * width - 1, 1), (500, most)] * 7
+    c = paged_ref.case(lens, 8, 2, d, 16, fp8=fp8, seed=width)
+    g = on_gpu(c)
+    o, lse = attend(c, g, max_new=most)
+    parity.check_status()
+    check(c, o, lse)
+
+
 def test_many_requests():
     """More requests than threads of a block, most of them short, some empty."""
     lens = [((i * 37) % 90, (i * 7) % 3) for i in range(1500)]
