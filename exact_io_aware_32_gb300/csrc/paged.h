@@ -27,6 +27,7 @@ struct StoreArgs {
   unsigned int* status;
   int T, Hkv, d, num_pages, page_shift, fp8;
   float descale_k, descale_v;
+  int step_tokens, step_pieces;  // set by launch_store
 };
 
 struct PagedArgs {
@@ -88,7 +89,7 @@ cudaError_t launch_dependent(void (*kernel)(Args, More...), dim3 grid, int threa
 }
 
 cudaError_t launch_plan(const PlanArgs& a, int num_sms, cudaStream_t stream);
-cudaError_t launch_store(const StoreArgs& a, cudaStream_t stream);
+cudaError_t launch_store(const StoreArgs& a, int num_sms, cudaStream_t stream);
 // The kernels of a call (1 or 2) in p[]; each may use the whole workspace, one after the other.
 int plan_paged(int T, int R, int Hq, int Hkv, int d, int fp8, int max_new, int max_keys, int num_sms,
                PagedPlan (&p)[2]);

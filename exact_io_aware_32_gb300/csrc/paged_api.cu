@@ -118,7 +118,7 @@ int fa_paged_store(const void* k, const void* v, long long k_stride, long long v
   a.fp8 = fp8 ? 1 : 0;
   a.descale_k = descale_k;
   a.descale_v = descale_v;
-  return fa::launch_store(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+  return fa::launch_store(a, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
 size_t fa_fwd_paged_workspace_bytes(int T, int R, int Hq, int Hkv, int d, int max_new) {

@@ -211,42 +211,74 @@ __device__ __forceinline__ uint32_t quantise4(uint32_t lo, uint32_t hi, const Fa
   return exact ? quantise4_exact(lo, hi, s.f, s.inv, s.near) : e4m3x4(q[0], q[1], q[2], q[3]);
 }
 
-// 32 bytes of a row (16 elements) per thread; keys in grid.y 0, values in 1.
-// Neighbouring threads take neighbouring pieces of one token, so reads and writes
-// are whole rows of a head. Bound by memory: 15523 tokens of 8 heads of 128 to
-// E4M3 in 18.3 us, 5.2 TB/s. (Two to four pieces per thread: 18.7 to 20.8 us,
-// fewer threads being resident.)
-template <bool FP8>
+// 32 bytes of a row (16 elements) at a time per thread; keys in grid.y 0, values
+// in 1. Neighbouring threads take neighbouring pieces of one token, so reads and
+// writes are whole rows of a head. LOOP: a thread takes several pieces, the next
+// on its way while one is converted (E4M3 only: the conversion is what a load
+// can hide behind). 15523 tokens of 8 heads of 128 to E4M3: a piece per thread
+// 20.3 us, a loop over three, four or six blocks per SM 20.4, 18.5 and 19.0 us
+// (5.2 TB/s); bf16 21.2 us (6.0 TB/s), in a loop 22 to 27 us.
+constexpr int kStoreBlocks = 4;  // per SM, of keys and of values each, in a loop
+constexpr int kStoreLoop = 3;    // pieces per thread from which on it pays (4000 tokens: 5.7 and 6.1 us, 8000 alike)
+template <bool FP8, bool LOOP>
 __global__ void __launch_bounds__(256) fa_paged_store_kernel(const __grid_constant__ StoreArgs a) {
   const unsigned row_shift = a.d == 64 ? 2u : 3u, per_token = (unsigned)a.Hkv << row_shift;  // pieces of a row, of a token
   const bool value = blockIdx.y != 0;
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
   ptx::grid_release();
   ptx::grid_wait();
-  const long long t = i <= 0xFFFFFFFFll ? (unsigned)i / per_token : i / per_token;  // (64-bit division takes far longer)
+  long long t = i <= 0xFFFFFFFFll ? (unsigned)i / per_token : i / per_token;  // (64-bit division takes far longer)
   if (t >= a.T) return;
-  const unsigned x = (unsigned)(i - t * per_token), h = x >> row_shift, c = x & ((1u << row_shift) - 1u);
+  unsigned x = (unsigned)(i - t * per_token);
   const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(value ? a.v : a.k);
-  const uint4* s = reinterpret_cast<const uint4*>(src + t * (value ? a.v_stride : a.k_stride) + (long long)x * 16);
-  const int slot = __ldg(a.slots + t);
-  const uint4 w0 = __ldg(s), w1 = __ldg(s + 1);
-  if (slot < 0) return;
-  const int page = slot >> a.page_shift;
-  if (page >= a.num_pages) {
-    atomicOr(a.status, kStatusBadLength);
-    return;
-  }
-  const long long row = (((long long)page * a.Hkv + h) << a.page_shift) + (slot & ((1 << a.page_shift) - 1));
-  const long long at = row * a.d + c * 16;
   uint8_t* cache = static_cast<uint8_t*>(value ? a.v_cache : a.k_cache);
-  if constexpr (FP8) {
-    const Factor f = factor_of(value ? a.descale_v : a.descale_k);
-    *reinterpret_cast<uint4*>(cache + at) =
-        make_uint4(quantise4(w0.x, w0.y, f), quantise4(w0.z, w0.w, f), quantise4(w1.x, w1.y, f), quantise4(w1.z, w1.w, f));
+  int slot;
+  uint4 w0, w1;
+  auto load = [&] {
+    const uint4* s = reinterpret_cast<const uint4*>(src + t * (value ? a.v_stride : a.k_stride) + (long long)x * 16);
+    slot = __ldg(a.slots + t);
+    w0 = __ldg(s);
+    w1 = __ldg(s + 1);
+  };
+  auto store = [&](int slot, uint4 w0, uint4 w1, unsigned x) {
+    if (slot < 0) return;
+    const int page = slot >> a.page_shift;
+    if (page >= a.num_pages) {
+      atomicOr(a.status, kStatusBadLength);
+      return;
+    }
+    const unsigned h = x >> row_shift, c = x & ((1u << row_shift) - 1u);
+    const long long row = (((long long)page * a.Hkv + h) << a.page_shift) + (slot & ((1 << a.page_shift) - 1));
+    const long long at = row * a.d + c * 16;
+    if constexpr (FP8) {
+      const Factor f = factor_of(value ? a.descale_v : a.descale_k);
+      *reinterpret_cast<uint4*>(cache + at) = make_uint4(quantise4(w0.x, w0.y, f), quantise4(w0.z, w0.w, f),
+                                                         quantise4(w1.x, w1.y, f), quantise4(w1.z, w1.w, f));
+    } else {
+      uint4* d = reinterpret_cast<uint4*>(cache + at * 2);
+      d[0] = w0;
+      d[1] = w1;
+    }
+  };
+  load();
+  if constexpr (LOOP) {
+    for (;;) {
+      const int slot_now = slot;
+      const uint4 u0 = w0, u1 = w1;
+      const unsigned x_now = x;
+      t += a.step_tokens;
+      x += (unsigned)a.step_pieces;
+      if (x >= per_token) {
+        x -= per_token;
+        ++t;
+      }
+      const bool more = t < a.T;
+      if (more) load();
+      store(slot_now, u0, u1, x_now);
+      if (!more) return;
+    }
   } else {
-    uint4* d = reinterpret_cast<uint4*>(cache + at * 2);
-    d[0] = w0;
-    d[1] = w1;
+    store(slot, w0, w1, x);
   }
 }
 
@@ -263,11 +295,18 @@ cudaError_t launch_plan(const PlanArgs& args, int num_sms, cudaStream_t stream) 
   return launch_dependent(fa_paged_plan_kernel, dim3((unsigned)n, (unsigned)slices), kPlanThreads, 0, stream, a);
 }
 
-cudaError_t launch_store(const StoreArgs& a, cudaStream_t stream) {
-  const long long blocks = ((long long)a.T * a.Hkv * (a.d / 16) + 255) / 256;
+cudaError_t launch_store(const StoreArgs& args, int num_sms, cudaStream_t stream) {
+  StoreArgs a = args;
+  const int per_token = a.Hkv * (a.d / 16), resident = kStoreBlocks * num_sms;
+  const long long blocks = ((long long)a.T * per_token + 255) / 256;
   if (blocks > INT32_MAX) return cudaErrorInvalidValue;
-  return launch_dependent(a.fp8 ? fa_paged_store_kernel<true> : fa_paged_store_kernel<false>,
-                          dim3((unsigned)blocks, 2u), 256, 0, stream, a);
+  const bool loop = a.fp8 && blocks > kStoreLoop * resident;
+  a.step_tokens = resident * 256 / per_token;  // from one piece of a thread to its next
+  a.step_pieces = resident * 256 % per_token;
+  return launch_dependent(!a.fp8 ? fa_paged_store_kernel<false, false>
+                          : loop ? fa_paged_store_kernel<true, true>
+                                 : fa_paged_store_kernel<true, false>,
+                          dim3(loop ? (unsigned)resident : (unsigned)blocks, 2u), 256, 0, stream, a);
 }
 
 }  // namespace fa

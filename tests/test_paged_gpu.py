@@ -426,6 +426,33 @@ def test_store(T, Hkv, d, ps, fused, fp8):
         assert parity.guards_intact(b) and torch.equal(t.cpu(), w)
 
 
+@pytest.mark.parametrize("T,Hkv,d,ps,fused", [(12007, 8, 128, 64, True), (31001, 5, 64, 16, False), (16411, 3, 128, 256, False)])
+def test_store_of_many_tokens(T, Hkv, d, ps, fused):
+    """More E4M3 pieces than threads: each thread takes several, and pieces of the last pass end inside a block."""
+    gen = torch.Generator().manual_seed(T)
+    P = T // ps + 2
+    base = torch.randn((T, 3 * Hkv * d), generator=gen).to(torch.bfloat16)
+    k, v = (base[:, i * Hkv * d:(i + 1) * Hkv * d].unflatten(1, (Hkv, d)) for i in (1, 2))
+    on = base.cuda()
+    gk, gv = (on[:, i * Hkv * d:(i + 1) * Hkv * d].unflatten(1, (Hkv, d)) for i in (1, 2))
+    if not fused:
+        gk, gv = gk.contiguous(), gv.contiguous()
+    slots = torch.randperm(P * ps, generator=gen)[:T].to(torch.int32)
+    slots[::7] = -2
+    caches = [parity.guarded_empty((P, Hkv, ps, d), torch.uint8) for _ in range(2)]
+    for t, _ in caches:
+        t.fill_(77)
+    fa.paged_store(gk, gv, slots.cuda(), caches[0][0], caches[1][0], 0.0131, 0.37)
+    parity.check_status()
+    put = slots >= 0
+    s = slots[put].long()
+    for x, f, (t, b) in zip((k, v), (0.0131, 0.37), caches):
+        want = torch.full((P, ps, Hkv, d), 77, dtype=torch.uint8)
+        codes = paged_ref.e4m3(x[put].double() / f32(f)).float().to(torch.float8_e4m3fn).view(torch.uint8)
+        want.view(P * ps, Hkv, d)[s] = codes
+        assert parity.guards_intact(b) and torch.equal(t.cpu(), want.transpose(1, 2))
+
+
 def f32(x):
     return float(torch.tensor(x, dtype=torch.float32))
 
