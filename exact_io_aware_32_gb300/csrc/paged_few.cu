@@ -21,12 +21,12 @@
 // Warp roles: 0-3 softmax and epilogue; 4 walks the range, tells the others its
 // pieces and copies keys, 5 copies values; 6 issues P V and owns TMEM, 7 copies Q
 // and issues Q K^T; with E4M3 caches eight converter warps (value codes to f16, Q
-// to its two parts: by four of them 107 us instead of 100 where tiles are short).
+// to its two parts; by four of them 7% slower where tiles are short).
 //
 // Measured, d = 128, 8 key heads, 32 query heads: 64 requests of up to 8192 keys
-// 158 us, 6.6 TB/s of keys and values (bound by them); 48 of up to 16384, E4M3
+// 157 us, 6.6 TB/s of keys and values (bound by them); 48 of up to 16384, E4M3
 // caches, 138 us (the tensor cores, which take 128 rows, and the bytes about alike);
-// 256 requests of up to 1000 keys 88 and 100 us, of up to 100 keys 45 and 55 us
+// 256 requests of up to 1000 keys 85 and 94 us, of up to 100 keys 39 and 51 us
 // (bound by a tile's chain: its first S, softmax, last product, join).
 #include "paged_pipe.cuh"
 
