@@ -221,23 +221,22 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
       __syncwarp();
       ++nq;
     };
-    bool ok = true;
-    Piece next = p;
-    auto seek = [&](bool more) {  // to a piece that has keys
-      while (more && next.jb == next.je) more = in.next(next);
-      return more;
-    };
-    bool more_next = seek(first || in.next(next));
-    if (FP8 && more_next) load_q(next);
-    while (ok && more_next) {
-      p = next;
-      if (!FP8) {
-        if (!(ok = warp_wait(&bars.q_free, (n & 1) ^ 1, abort_flag))) break;
-        load_q(p);
+    // It looks one piece ahead and no further before this one's products are issued: the loading warp may wait for the
+    // softmax, which waits for them, before it tells the piece after that.
+    bool ok = true, asked = false;  // asked: for p's Q (E4M3 caches)
+    Piece next;
+    for (bool more = first || in.next(p), more_next; ok && more; p = next, more = more_next) {
+      if (p.jb == p.je) {
+        more_next = in.next(next);
+        asked = false;
+        continue;
       }
-      more_next = seek(in.next(next));
+      if (!FP8 && !(ok = warp_wait(&bars.q_free, (n & 1) ^ 1, abort_flag))) break;
+      if (!asked) load_q(p);
+      more_next = in.next(next);
       if (!(ok = warp_wait(&bars.q_full[n % 3], (n / 3) & 1, abort_flag))) break;
-      if (FP8 && more_next) load_q(next);
+      asked = FP8 && more_next && next.jb < next.je;
+      if (asked) load_q(next);
       ++n;
       for (int jj = p.jb; jj < p.je; ++jj, ++g) {
         const int s = g % C::kKStages, b = g & 1;

@@ -122,6 +122,26 @@ def test_rows_without_keys(d, fp8, most):
         check(c, o, lse, causal=causal, lens=lens)
 
 
+@pytest.mark.parametrize("most", [1, 5, 60])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_long_runs_of_requests_without_keys(d, fp8, most):
+    """Dozens of tiles in a row that stream nothing (eight key heads each), between, before and behind ones that do."""
+    for start in (0, 1):
+        lens, keys = [], []
+        for i in range(60):
+            n = 1 + i % most
+            lens.append((30 + 70 * (i % 3), n))
+            keys.append(0 if (i // 7 + start) % 2 else lens[-1][0] + n)
+        c = paged_ref.case(lens, 16, 8, d, 16, fp8=fp8, seed=d + most, width=100)
+        g = on_gpu(c)
+        g["lens"] = ints(keys)
+        for causal in (True, False):
+            o, lse = attend(c, g, causal=causal, max_new=most)
+            parity.check_status()
+            check(c, o, lse, causal=causal, lens=keys)
+
+
 @pytest.mark.parametrize("most", [1, 200])
 @pytest.mark.parametrize("fp8", [False, True])
 @pytest.mark.parametrize("d", [64, 128])
