@@ -480,9 +480,9 @@ def _paged():
 
 def _on(stream, x):
     """The context of a call on ``stream`` (a torch.cuda.Stream or a handle) of the device of tensor ``x``: the tensors it
-    allocates are that stream's."""
+    allocates are that stream's. Handle 0 is the default stream (an ExternalStream of 0 would be a new stream)."""
     if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream, device=x.device)
+        stream = torch.cuda.ExternalStream(stream, device=x.device) if stream else torch.cuda.default_stream(x.device)
     elif stream.device != x.device:
         raise ValueError(f"the stream must belong to {x.device}")
     return torch.cuda.stream(stream)
