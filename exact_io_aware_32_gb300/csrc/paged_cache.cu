@@ -236,9 +236,9 @@ __global__ void __launch_bounds__(256) fa_paged_store_kernel(const __grid_consta
   uint4 w0, w1;
   auto load = [&] {
     const uint4* s = reinterpret_cast<const uint4*>(src + t * (value ? a.v_stride : a.k_stride) + (long long)x * 16);
-    slot = __ldg(a.slots + t);
-    w0 = __ldg(s);
-    w1 = __ldg(s + 1);
+    slot = a.slots[t];
+    w0 = s[0];
+    w1 = s[1];
   };
   auto store = [&](int slot, uint4 w0, uint4 w1, unsigned x) {
     if (slot < 0) return;

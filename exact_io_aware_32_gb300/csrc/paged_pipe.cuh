@@ -21,7 +21,7 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units: how far the exponent r
 struct Pages {
   int base, now, next;  // entries base + lane and base + 32 + lane
   __device__ __forceinline__ int entry(const PagedArgs& a, const Piece& p, int i) const {
-    return i <= (p.q.len - 1) >> a.page_shift ? __ldg(a.block_table + (long long)p.r * a.max_pages + i) : -1;
+    return i <= (p.q.len - 1) >> a.page_shift ? a.block_table[(long long)p.r * a.max_pages + i] : -1;
   }
   __device__ __forceinline__ void begin(const PagedArgs& a, const Piece& p, int lane) {
     base = ((p.jb * 128) >> a.page_shift) & ~31;

@@ -38,7 +38,7 @@ struct RawRequest {
   int s0, s1, l;
 };
 __device__ __forceinline__ RawRequest load_request(const PagedArgs& a, int r) {
-  return {__ldg(a.query_start + r), __ldg(a.query_start + r + 1), __ldg(a.seq_lens + r)};
+  return {a.query_start[r], a.query_start[r + 1], a.seq_lens[r]};
 }
 // The request as the call takes it; bad: something was out of range.
 __device__ __forceinline__ Request request(const PagedArgs& a, const RawRequest& raw, bool& bad) {

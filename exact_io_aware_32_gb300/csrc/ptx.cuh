@@ -414,6 +414,9 @@ __device__ __forceinline__ bool named_bar_and(uint32_t id, uint32_t nthreads, bo
 // Programmatic dependent launch: a kernel launched so may begin before the one
 // ahead of it in the stream has ended, and must not touch anything that one
 // reads or writes before grid_wait; grid_release lets the one behind it begin.
+// What a kernel ahead may write is read by ordinary loads, not by __ldg (or
+// ld.global.nc): that is for data which stays as it is for the whole life of
+// the reading kernel, and the compiler may move it ahead of grid_wait.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ bool elect_one() {

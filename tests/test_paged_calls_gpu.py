@@ -8,7 +8,7 @@ import torch
 from exact_io_aware_32_gb300 import fa
 import paged_ref
 import parity
-from test_paged_gpu import attend, check, ints, on_gpu
+from test_paged_gpu import attend, check, f32, ints, on_gpu
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +35,76 @@ def test_stream_handles():
             attend(c, late, max_new=3, out=o, lse=lse, stream=handle)
         parity.check_status()
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("d", [64, 128])
+def test_steps_back_to_back(d, fp8, captured):
+    """Twelve steps of plan, store and attention with no other kernel between them, each step's lengths, table and rows
+    written by the kernels just ahead, in place: every row as in plain attention over its request's whole text."""
+    Hq, Hkv, ps, steps = 6, 2, 16, 12
+    per = [(150, 1, 33) if i % 3 == 0 else (1, 1, 1) if i % 3 == 1 else (2, 70, 1) for i in range(steps)]
+    total = [sum(s[r] for s in per) for r in range(3)]
+    c = [paged_ref.case([(0, n)], Hq, Hkv, d, ps, fp8=fp8, seed=50 + r) for r, n in enumerate(total)]
+    g = [on_gpu(x) for x in c]
+    fk, fv = c[0]["fk"], c[0]["fv"]
+    need = sum(-(-n // ps) for n in total)
+    perm = torch.randperm(need + 3, generator=torch.Generator().manual_seed(d)).tolist()
+    free = ints(perm)
+    cache = [torch.zeros((need + 3, Hkv, ps, d), device="cuda").to(torch.float8_e4m3fn if fp8 else torch.bfloat16) for _ in "kv"]
+    table = torch.full((3, max(-(-n // ps) for n in total)), -1, dtype=torch.int32, device="cuda")
+    state, done, at = [], [0, 0, 0], 0
+    ctx = zero = torch.zeros(3, dtype=torch.int32, device="cuda")
+    for s in per:
+        T = sum(s)
+        rows = {n: torch.cat([g[r][n][done[r]:done[r] + s[r]] for r in range(3)]) for n in "qkv"}
+        out = [torch.zeros(n, dtype=torch.int32, device="cuda") for n in (4, 3, T, 1)]
+        state.append(dict(rows, new=ints(list(s)), T=T, ctx=ctx, free=free[at:], out=out, most=max(s),
+                          o=torch.zeros((T, Hq, d), dtype=torch.bfloat16, device="cuda"),
+                          lse=torch.zeros((T, Hq), dtype=torch.float32, device="cuda")))
+        ctx = out[1]
+        at += sum(-(-(done[r] + s[r]) // ps) - -(-done[r] // ps) for r in range(3))
+        done = [a + b for a, b in zip(done, s)]
+    ws = torch.empty(max(fa.fa_fwd_paged_workspace_bytes(x["T"], 3, Hq, Hkv, d, x["most"]) for x in state),
+                     dtype=torch.uint8, device="cuda")
+
+    def run():
+        for x in state:
+            start, lens, slots, _ = fa.paged_plan(x["ctx"], x["new"], table, x["free"], ps, x["T"], out=x["out"])
+            fa.paged_store(x["k"], x["v"], slots, *cache, descale_k=fk, descale_v=fv)
+            fa.forward_paged(x["q"], *cache, table, start, lens, max_new=x["most"], descale_k=fk, descale_v=fv,
+                             out=x["o"], lse=x["lse"], workspace=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            run()
+    for again in range(3):
+        for x in state:
+            x["o"].fill_(7.0)
+            x["lse"].fill_(7.0)
+            for t in x["out"]:
+                t.fill_(-9)
+        table.fill_(-1)
+        for t in cache:
+            t.view(torch.uint8).fill_(0)
+        free.copy_(ints(perm if again != 1 else perm[::-1]))
+        zero.zero_()
+        graph.replay() if captured else run()
+        parity.check_status()
+        for r, n in enumerate(total):
+            x = dict(c[r])
+            pages = -(-n // ps)
+            for name, src, f in (("k_cache", "k", fk), ("v_cache", "v", fv)):
+                full = torch.zeros((pages * ps, Hkv, d), dtype=torch.float64)
+                full[:n] = paged_ref.e4m3(x[src].double() / f32(f)) if fp8 else x[src].double()
+                x[name] = full.reshape(pages, ps, Hkv, d).permute(0, 2, 1, 3)
+            x["table"] = [list(range(pages))]
+            at = [sum(s[:r]) for s in per]
+            check(x, *(torch.cat([y[name][a:a + s[r]] for y, a, s in zip(state, at, per)]) for name in ("o", "lse")))

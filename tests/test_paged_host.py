@@ -150,3 +150,19 @@ def test_plain_plan_by_hand():
     got = paged_ref.plan([3, 0], [14, 2], [[5, -1], [-1, -1]], [9, 8, 7], 0, 16, 20)
     assert got == ([0, 14, 16], [17, 2], [5 * 16 + p for p in range(3, 16)] + [9 * 16] + [128, 129] + [-1] * 4, 2,
                    [[5, 9], [8, -1]])
+
+
+def test_kernels_launched_ahead_use_ordinary_loads():
+    """A kernel launched as a programmatic dependent is there while the one ahead still writes what it will read, so
+    its loads must not be those for data that nobody writes."""
+    import os
+    import re
+
+    files = [f for f in os.listdir(build.CSRC) if f.endswith((".cu", ".cuh"))]
+    text = {f: re.sub(r"//.*", "", open(os.path.join(build.CSRC, f)).read()) for f in files}
+    ahead = {f for f in files if re.search(r"launch_dependent|grid_wait", text[f])}
+    for _ in files:  # and what these include
+        ahead |= {g for f in ahead for g in re.findall(r'#include "([^"/]+\.cuh)"', text[f])}
+    assert {"paged_cache.cu", "paged_few.cu", "paged_chunk.cu", "paged_fwd.cu", "paged_pipe.cuh", "paged_work.cuh"} <= ahead
+    for f in sorted(ahead):
+        assert not re.search(r"__ldg|\.nc\b|__restrict__", text[f]), f
