@@ -57,23 +57,25 @@ __device__ __forceinline__ Request request(const PagedArgs& a, int r, bool& bad)
 }
 
 // Keys that the tokens before 'upto' (of the request's n) see.
-__device__ __forceinline__ int keys_seen(const PagedArgs& a, const Request& q, int upto) {
+__host__ __device__ __forceinline__ int keys_seen(const PagedArgs& a, const Request& q, int upto) {
   return a.causal ? max(q.len - q.n + min(upto, q.n), 0) : q.len;
 }
 
 // Length of the first i of a request's nt tiles (for one key head): the keys that their last tokens see, summed and then
-// taken as blocks, and the fixed parts.
-__device__ __forceinline__ int tiles_len(const PagedArgs& a, const Request& q, int i, int nt) {
-  long long keys;
+// taken as blocks, and the fixed parts. Where the first tokens see no key it counts more than they see, up to the request's
+// keys for each tile. (Exact sums, with a division for such requests, cost the others too: one short request 10.2 us,
+// with this 9.9 us.)
+__host__ __device__ __forceinline__ int tiles_len(const PagedArgs& a, const Request& q, int i, int nt) {
+  long long keys = (long long)i * q.len;
   if (a.causal) {
     const int whole = min(i, nt - 1);  // tiles of tpt tokens; the last one may have fewer
-    keys = (long long)i * max(q.len - q.n, 0) + (long long)whole * (whole + 1) / 2 * a.tpt + (i == nt ? q.n : 0);
-  } else {
-    keys = (long long)i * q.len;
+    const long long seen =
+        (long long)i * max(q.len - q.n, 0) + (long long)whole * (whole + 1) / 2 * a.tpt + (i == nt ? q.n : 0);
+    keys = min(keys, seen);  // (the sum is the smaller one unless the first tokens see no key)
   }
   return (int)(keys >> 7) + kTileCost * i;
 }
-__device__ __forceinline__ int tiles_of(const PagedArgs& a, const Request& q) { return (q.n + a.tpt - 1) / a.tpt; }
+__host__ __device__ __forceinline__ int tiles_of(const PagedArgs& a, const Request& q) { return (q.n + a.tpt - 1) / a.tpt; }
 
 // A part of a tile for this CTA: key blocks [jb, je) of nb.
 struct Piece {

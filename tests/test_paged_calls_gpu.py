@@ -108,3 +108,18 @@ def test_steps_back_to_back(d, fp8, captured):
             x["table"] = [list(range(pages))]
             at = [sum(s[:r]) for s in per]
             check(x, *(torch.cat([y[name][a:a + s[r]] for y, a, s in zip(state, at, per)]) for name in ("o", "lse")))
+
+
+@pytest.mark.parametrize("most", [32, 1 << 21])
+def test_two_million_tokens_of_which_few_see_a_key(most):
+    """A request of 2^21 new tokens and 128 keys: the last 128 rows are right, the others saw no key. (Counted as if the
+    tokens without keys had some, its tiles of 32 rows were more blocks than 32 bits hold.)"""
+    T, n = 1 << 21, 128
+    c = paged_ref.case([(0, n)], 8, 8, 64, 128, seed=60)
+    g = on_gpu(c)
+    q = torch.randn((T, 8, 64), device="cuda", dtype=torch.bfloat16)
+    q[T - n:] = g["q"]
+    o, lse = fa.forward_paged(q, g["k_cache"], g["v_cache"], g["table"], ints([0, T]), ints([n]), max_new=most)
+    parity.check_status()
+    check(c, o[T - n:], lse[T - n:])
+    assert not bool(o[:T - n].any()) and bool((lse[:T - n] == -float("inf")).all())
