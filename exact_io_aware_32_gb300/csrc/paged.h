@@ -49,6 +49,7 @@ struct PagedArgs {
   // swizzled over their d-byte rows, values not.
   CUtensorMap tm_k, tm_v;
   int n_min, n_max;         // new tokens of the requests to take
+  int most;                 // length of the row of tiles, at most (most_blocks)
   int whole, snap;          // key blocks of a tile that is not cut; of the smallest part of one that is
   int tpt;                  // tokens per tile
   int tpt1;                 // tokens per 128-row half of a tile (two halves at d = 128)
@@ -69,6 +70,12 @@ struct PagedPlan {
   size_t parts_bytes, o_bytes, lse_bytes;  // of the workspace, each a multiple of 256
   size_t bytes() const { return parts_bytes + o_bytes + lse_bytes; }
 };
+
+// The length of a kernel's row of tiles in key blocks (paged_work.cuh), at most: requests that share no rows have T / tpt + R
+// tiles per key head, each with the table's key blocks and its fixed part, rounded up.
+inline double most_blocks(int T, int R, int Hkv, int tpt, int max_keys) {
+  return ((double)T / tpt + R) * Hkv * (max_keys / 128.0 + 4.0);
+}
 
 // Launches a kernel that begins with grid_wait (ptx.cuh) once its own set-up is done, so that the set-up and the launch
 // itself overlap the end of the kernel before it in the stream.

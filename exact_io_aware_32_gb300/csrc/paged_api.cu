@@ -156,10 +156,8 @@ int fa_fwd_paged(const void* q, long long q_stride, const void* k_cache, const v
   const int max_keys = max_pages * page_size;
   fa::PagedPlan p[2];
   int n = fa::plan_paged(T, R, Hq, Hkv, d, fp8 ? 1 : 0, max_new, max_keys, kMaxSms, p);
-  for (int i = 0; i < n; ++i) {
-    const double tiles = ((double)T / p[i].tpt + R) * Hkv;
-    if (tiles * (max_keys / 128.0 + 4.0) >= 2147483648.0) return FA_ERR_INVALID_ARG;
-  }
+  for (int i = 0; i < n; ++i)
+    if (fa::most_blocks(T, R, Hkv, p[i].tpt, max_keys) >= (double)INT32_MAX) return FA_ERR_INVALID_ARG;
   fa::PagedArgs a;
   std::memset(&a, 0, sizeof(a));
   int sms = 0;
@@ -188,8 +186,10 @@ int fa_fwd_paged(const void* q, long long q_stride, const void* k_cache, const v
   a.max_keys = max_keys;
   a.test_fault = fa::take_test_fault();
   n = fa::plan_paged(T, R, Hq, Hkv, d, a.fp8, max_new, a.max_keys, std::min(sms, kMaxSms), p);
-  for (int i = 0; i < n; ++i)
+  for (int i = 0; i < n; ++i) {
+    a.most = (int)fa::most_blocks(T, R, Hkv, p[i].tpt, max_keys);
     if (fa::launch_paged(a, p[i], workspace, static_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_LAUNCH;
+  }
   return FA_OK;
 }
 

@@ -12,7 +12,8 @@
 // (a few KB that all read through L2), so no kernel has to run before. Places in
 // the row are blocks in 32 bits (the host refuses calls of 2^31 blocks), since
 // this is latency that every call pays: in 64 bits, by keys, the first copy went
-// out 2500 cycles later.
+// out 2500 cycles later. What the host counts holds for requests that share no
+// rows; the sum here saturates, and a row of tiles longer than that is not walked.
 #pragma once
 #include <cstdint>
 
@@ -74,6 +75,10 @@ __host__ __device__ __forceinline__ int tiles_len(const PagedArgs& a, const Requ
     keys = min(keys, seen);  // (the sum is the smaller one unless the first tokens see no key)
   }
   return (int)(keys >> 7) + kTileCost * i;
+}
+// (two lengths or sums of them; INT_MAX: too many to count)
+__host__ __device__ __forceinline__ int add_len(int x, int y) {
+  return (int)min((unsigned)x + (unsigned)y, 0x7FFFFFFFu);
 }
 __host__ __device__ __forceinline__ int tiles_of(const PagedArgs& a, const Request& q) { return (q.n + a.tpt - 1) / a.tpt; }
 
@@ -145,14 +150,13 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, Range& out, int (
       if (r == r0) first = q;
       any_bad |= bad;
       const int nt = tiles_of(a, q);
-      if (nt) mine += a.Hkv * tiles_len(a, q, nt, nt);
+      if (nt) mine = add_len(mine, a.Hkv * tiles_len(a, q, nt, nt));
     }
-    if (any_bad && blockIdx.x == 0) atomicOr(a.status, kStatusBadLength);
     int upto = mine;
 #pragma unroll
     for (int s = 1; s < 32; s <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, upto, s);
-      if (lane >= s) upto += x;
+      if (lane >= s) upto = add_len(upto, x);
     }
     int total = __shfl_sync(0xffffffffu, upto, 31), pos = upto - mine;
     if (!alone) {
@@ -162,11 +166,16 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, Range& out, int (
 #pragma unroll 1
       for (int w = 0; w < kWarps; ++w) {
         const int x = s_sum[w];
-        if (w < warp) pos += x;
-        total += x;
+        if (w < warp) pos = add_len(pos, x);
+        total = add_len(total, x);
       }
     }
-    const int ctas = (int)gridDim.x, per = max(kMinRange, (int)((unsigned)(total + ctas - 1) / (unsigned)ctas));
+    if (total > a.most) {  // requests that share rows: nobody's range holds anything
+      total = 0;
+      any_bad = true;
+    }
+    if (any_bad && blockIdx.x == 0) atomicOr(a.status, kStatusBadLength);
+    const int ctas = (int)gridDim.x, per = max(kMinRange, (int)(((unsigned)total + ctas - 1) / (unsigned)ctas));
     const long long at = (long long)per * blockIdx.x;
     const int p0 = (int)min(at, (long long)total), p1 = (int)min(at + per, (long long)total);
     if (tid == 0 && p0 >= total) out.some = 0;

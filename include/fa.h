@@ -348,11 +348,16 @@ FA_API int fa_paged_store(const void* k, const void* v, long long k_stride, long
  * finite values. A page outside the cache reads as zeros, a
  * seq_len past max_pages pages is cut, a negative one is 0, query_start is
  * cut into [0, T], and a request that ends before it starts has no rows; each
- * is reported by fa_device_status as FA_ERR_INVALID_ARG.
- * The largest call: with tiles = (T / tokens per tile + R) Hkv (a tile is 32
- * or 128 rows of a key head, 256 at d = 128), tiles times the table's width
- * in blocks of 128 keys must stay below 2^31 (seconds of work), else
- * FA_ERR_INVALID_ARG.
+ * is reported by fa_device_status as FA_ERR_INVALID_ARG. Requests whose rows
+ * overlap (a query_start that decreases in between) leave either's results
+ * there; where they make the call larger than any of T rows could be, rows
+ * are not computed but stay as they were.
+ * The largest call: with tiles = (T / tokens per tile + R) Hkv, tiles times
+ * the table's width in blocks of 128 keys plus four must stay below 2^31
+ * (seconds of work), else FA_ERR_INVALID_ARG. A tile is 32 rows (tokens times
+ * Hq / Hkv), or 128 or 256 where max_new calls for it, of at most max_new
+ * tokens: a max_new far below the requests' tokens makes a call count for
+ * more.
  * Results do not depend on what else is in the batch beyond rounding (the
  * keys of a request are split over the GPU by the lengths of all); repeated
  * calls give identical bits.

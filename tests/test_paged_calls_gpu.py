@@ -123,3 +123,22 @@ def test_two_million_tokens_of_which_few_see_a_key(most):
     parity.check_status()
     check(c, o[T - n:], lse[T - n:])
     assert not bool(o[:T - n].any()) and bool((lse[:T - n] == -float("inf")).all())
+
+
+@pytest.mark.parametrize("R", [64, 512])
+@pytest.mark.parametrize("most", [1, 64, 1 << 16])
+def test_requests_that_share_rows_are_not_counted_past_the_call(R, most):
+    """Every other request claims all 2^16 rows: far more blocks than the call of so many rows that the host admitted
+    (with 512 requests than 32 bits hold). Reported, and nothing out of range is walked."""
+    T, Hq, Hkv, d, ps, keys = 1 << 16, 32, 8, 64, 256, 131072
+    q = torch.ones((T, Hq, d), dtype=torch.bfloat16, device="cuda")
+    kc, vc = (torch.ones((3, Hkv, ps, d), dtype=torch.bfloat16, device="cuda") for _ in "kv")
+    table = torch.zeros((R, keys // ps), dtype=torch.int32, device="cuda")
+    out, bo = parity.guarded_empty((T, Hq, d), torch.bfloat16, fill=2.5)
+    lse, bl = parity.guarded_empty((T, Hq), torch.float32, fill=-3.5)
+    fa.forward_paged(q, kc, vc, table, ints([0, T] * (R // 2) + [0]), ints([keys] * R), max_new=most, causal=False, out=out,
+                     lse=lse)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(True) == fa.FA_ERR_INVALID_ARG
+    assert parity.guards_intact(bo) and parity.guards_intact(bl)
+    assert bool((out == 2.5).all()) and bool((lse == -3.5).all())

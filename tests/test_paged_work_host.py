@@ -15,7 +15,18 @@ using namespace fa::paged;
 int main() {
   fa::PagedArgs a{};
   Request q{};
-  int i;
+  int i, R;
+  if (scanf("%d", &R) == 1 && R > 0) {  // a batch: its length as the kernels add it up, and the host's bound
+    scanf("%d %d %d %d %d", &a.causal, &a.tpt, &a.T, &a.Hkv, &a.max_keys);
+    int sum = 0;
+    for (int r = 0; r < R; ++r) {
+      scanf("%d %d", &q.n, &q.len);
+      const int nt = tiles_of(a, q);
+      if (nt) sum = add_len(sum, a.Hkv * tiles_len(a, q, nt, nt));
+    }
+    printf("%d %.1f\n", sum, fa::most_blocks(a.T, R, a.Hkv, a.tpt, a.max_keys));
+    return 0;
+  }
   while (scanf("%d %d %d %d %d", &a.causal, &a.tpt, &q.n, &q.len, &i) == 5) {
     const int nt = (q.n + a.tpt - 1) / a.tpt;
     printf("%d %d\n", tiles_len(a, q, i, nt), keys_seen(a, q, i * a.tpt));
@@ -32,10 +43,10 @@ def lengths(tmp_path_factory):
     exe = str(d / "driver")
     subprocess.check_call([build.nvcc()] + build.ARCH + build.FLAGS + ["-I", build.CSRC, str(d / "driver.cu"), "-o", exe])
 
-    def run(cases):
-        out = subprocess.run([exe], input="\n".join(" ".join(map(str, c)) for c in cases), capture_output=True, text=True,
-                             check=True).stdout.split()
-        return [(int(a), int(b)) for a, b in zip(out[::2], out[1::2])]
+    def run(cases, batch=0):
+        out = subprocess.run([exe], input=f"{batch}\n" + "\n".join(" ".join(map(str, c)) for c in cases),
+                             capture_output=True, text=True, check=True).stdout.split()
+        return [(int(a), float(b)) for a, b in zip(out[::2], out[1::2])]
     return run
 
 
@@ -71,3 +82,20 @@ def test_tokens_without_keys_count_few_blocks(lengths):
     n, tpt = 1 << 21, 32
     (got, _), = lengths([(1, tpt, n, 128, n // tpt)])
     assert 2 * (n // tpt) <= got <= 3 * (n // tpt)
+
+
+def test_batches_stay_within_the_hosts_count(lengths):
+    """Requests that share no rows never come to more blocks than the host admits a call by; requests that do are added
+    up without an overflow."""
+    rng = random.Random(6)
+    for _ in range(60):
+        R, tpt, keys = rng.choice([1, 2, 7, 200]), rng.choice([1, 4, 32, 256]), rng.choice([16, 1000, 70000])
+        n = [rng.choice([0, 1, rng.randint(0, 600)]) for _ in range(R)]
+        lens = [rng.choice([0, keys, rng.randint(0, keys)]) for _ in range(R)]
+        T, Hkv = max(1, sum(n) + rng.randint(0, 3)), rng.choice([1, 8])
+        (got, most), = lengths([(rng.randint(0, 1), tpt, T, Hkv, keys)] + list(zip(n, lens)), batch=R)
+        assert got <= int(most), (R, tpt, keys)
+    # every other request has all T rows
+    T, R, keys = 1 << 16, 512, 131072
+    (got, most), = lengths([(0, 32, T, 8, keys)] + [(T, keys), (0, keys)] * (R // 2), batch=R)
+    assert got == 2 ** 31 - 1 > most
