@@ -42,6 +42,9 @@ bool factor(float x) { return std::isfinite(x) && x > 0.f; }
 // SMs that a workspace is made for (the GPU has 152), so that its size does not depend on the device.
 constexpr int kMaxSms = 160;
 
+// Keys of the widest table: the kernels add up to four blocks of 128 to a place among the keys, in 32 bits.
+constexpr int kMaxKeys = INT32_MAX - 511;
+
 constexpr double kLog2e = 1.4426950408889634074;
 
 int check_paged(int T, int R, int Hq, int Hkv, int d, int max_new) {
@@ -141,7 +144,7 @@ int fa_fwd_paged(const void* q, long long q_stride, const void* k_cache, const v
   int st = check_paged(T, R, Hq, Hkv, d, max_new);
   if (st == FA_OK) st = check_cache(num_pages, page_size, Hkv, d);
   if (st != FA_OK) return st;
-  if (max_pages < 1 || (long long)max_pages * page_size > INT32_MAX || !factor(scale)) return FA_ERR_INVALID_ARG;
+  if (max_pages < 1 || (long long)max_pages * page_size > kMaxKeys || !factor(scale)) return FA_ERR_INVALID_ARG;
   if (fp8 && (!factor(descale_k) || !factor(descale_v))) return FA_ERR_INVALID_ARG;
   const float scale_log2 = (float)((double)scale * (fp8 ? (double)descale_k : 1.0) * kLog2e);
   if (!factor(scale_log2)) return FA_ERR_INVALID_ARG;  // over- or underflow

@@ -352,6 +352,8 @@ FA_API int fa_paged_store(const void* k, const void* v, long long k_stride, long
  * overlap (a query_start that decreases in between) leave either's results
  * there; where they make the call larger than any of T rows could be, rows
  * are not computed but stay as they were.
+ * The widest table: max_pages * page_size below 2^31 - 511, else
+ * FA_ERR_INVALID_ARG.
  * The largest call: with tiles = (T / tokens per tile + R) Hkv, tiles times
  * the table's width in blocks of 128 keys plus four must stay below 2^31
  * (seconds of work), else FA_ERR_INVALID_ARG. A tile is 32 rows (tokens times

@@ -142,3 +142,33 @@ def test_requests_that_share_rows_are_not_counted_past_the_call(R, most):
     assert fa.fa_device_status(True) == fa.FA_ERR_INVALID_ARG
     assert parity.guards_intact(bo) and parity.guards_intact(bl)
     assert bool((out == 2.5).all()) and bool((lse == -3.5).all())
+
+
+@pytest.mark.parametrize("n", [1, 40])
+@pytest.mark.parametrize("d,fp8", [(64, False), (128, True)])
+def test_the_widest_table(d, fp8, n):
+    """2^31 - 612 keys, all but the last page's the same page of zero keys; the last page's keys stand out so far (a score
+    of 40) that a row is the mean of its visible values there. Equal weights are powers of two, so o is off by its own
+    rounding (2^-8) and fp32 sums of at most 156 terms (below 2^-12 of their mean magnitude); the 2^31 other keys weigh
+    2^31 e^-39 < 2^-25."""
+    ps, width = 256, (2 ** 31 - 512) // 256
+    L = width * ps - 100
+    dt = torch.float8_e4m3fn if fp8 else torch.bfloat16
+    gen = torch.Generator().manual_seed(d)
+    c = 5.0 if d == 64 else 3.5
+    kc = torch.zeros((2, 1, ps, d))
+    kc[1, 0, :156] = c
+    vc = torch.randn((2, 1, ps, d), generator=gen)
+    kc[1, 0, 156:], vc[1, 0, 156:] = float("nan"), float("nan")
+    kc, vc = kc.to(dt), vc.to(dt)
+    table = torch.zeros((1, width), dtype=torch.int32, device="cuda")
+    table[0, -1] = 1
+    q = torch.ones((n, 2, d), dtype=torch.bfloat16, device="cuda")
+    o, lse = fa.forward_paged(q, kc.cuda(), vc.cuda(), table, ints([0, n]), ints([L]), max_new=n)
+    parity.check_status()
+    for t in range(n):
+        seen = vc[1, 0, :156 - n + t + 1].double()
+        want, mag = seen.mean(0), seen.abs().mean(0)
+        assert bool(((o[t].double().cpu() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -12 * mag).all()), t
+        s = math.sqrt(d) * c + math.log(seen.shape[0])
+        assert bool(((lse[t].double().cpu() - s).abs() <= 2.0 ** -12).all()), t

@@ -105,6 +105,18 @@ def test_fwd_paged_rejects_more_work_than_it_counts():
     assert fa.fa_fwd_paged(**kw, stream=0) == fa.FA_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("page_size", [16, 32, 64, 128, 256])
+def test_fwd_paged_rejects_tables_whose_keys_it_cannot_count(page_size):
+    """A place among the keys plus a few blocks must fit 32 bits: a table that ends within 512 tokens of 2^31 is refused,
+    one page less is not (there the missing workspace is what stops the call)."""
+    kw = dict(q=A, q_stride=64, k_cache=A, v_cache=A, fp8=True, descale_k=1.0, descale_v=1.0, block_table=A,
+              query_start=A, seq_lens=A, o=A, lse=A, T=1, R=1, Hq=1, Hkv=1, d=64, num_pages=11, page_size=page_size,
+              max_new=1, scale=0.1, causal=True, workspace=0, workspace_bytes=0)
+    most = (2 ** 31 - 512) // page_size
+    assert fa.fa_fwd_paged(max_pages=most + 1, **kw, stream=0) == fa.FA_ERR_INVALID_ARG
+    assert fa.fa_fwd_paged(max_pages=most, **kw, stream=0) == fa.FA_ERR_WORKSPACE
+
+
 def test_helpers_reject_bad_tensors():
     c = paged_ref.case([(5, 2)], 4, 2, 64, 16)
     ints = lambda x: torch.tensor(x, dtype=torch.int32)  # noqa: E731
