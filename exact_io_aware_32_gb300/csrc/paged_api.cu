@@ -42,6 +42,9 @@ bool factor(float x) { return std::isfinite(x) && x > 0.f; }
 // SMs that a workspace is made for (the GPU has 152), so that its size does not depend on the device.
 constexpr int kMaxSms = 160;
 
+// Requests of a plan: its kernel counts them in 32 bits, a few hundred at a time.
+constexpr int kMaxPlanRequests = 1 << 30;
+
 // Keys of the widest table: the kernels add up to four blocks of 128 to a place among the keys, in 32 bits.
 constexpr int kMaxKeys = INT32_MAX - 511;
 
@@ -63,7 +66,7 @@ int fa_paged_plan(const int* ctx_lens, const int* new_lens, int R, int page_size
                   int T, int* pages_taken, void* stream) {
   if (!ctx_lens || !new_lens || !free_pages || !block_table || !query_start || !seq_lens || !slots || !pages_taken)
     return FA_ERR_INVALID_ARG;
-  if (R < 1 || T < 1 || n_free < 0 || max_pages < 1 || page_size < 1) return FA_ERR_INVALID_ARG;
+  if (R < 1 || R > kMaxPlanRequests || T < 1 || n_free < 0 || max_pages < 1 || page_size < 1) return FA_ERR_INVALID_ARG;
   const int shift = page_shift(page_size);
   if (shift < 0) return FA_ERR_UNSUPPORTED;
   if (((long long)max_pages << shift) > INT32_MAX) return FA_ERR_INVALID_ARG;

@@ -281,7 +281,7 @@ FA_API int fa_bwd_dropout(const void* q, const void* k, const void* v, const voi
 
 /*
  * Plans a step: gives each request the pages that its new tokens need, in the
- * order of the requests, and says where every new token goes.
+ * order of the requests (up to 2^30 of them), and says where every new token goes.
  *   ctx_lens, new_lens [in]  device int32 [R]: tokens already in the cache, and new tokens of this step (>= 0)
  *   free_pages     [in]      device int32 [n_free]: pages that nobody uses, in the order in which they are taken
  *   free_head      [in]      device int32 [1]: the first entry of free_pages still free (NULL: 0)
