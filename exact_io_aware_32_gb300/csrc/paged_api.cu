@@ -74,6 +74,17 @@ int fa_paged_plan(const int* ctx_lens, const int* new_lens, int R, int page_size
                         (const void*)block_table, (const void*)query_start, (const void*)seq_lens, (const void*)slots,
                         (const void*)pages_taken})
     if (!aligned(p, 4)) return FA_ERR_MISALIGNED;
+  // every block reads all lengths and the free list's head while others write: nothing written may be read elsewhere
+  const struct {
+    const int* at;
+    long long n;
+  } arrays[] = {{block_table, (long long)R * max_pages}, {query_start, R + 1ll}, {seq_lens, R}, {slots, T}, {pages_taken, 1},
+                {ctx_lens, R}, {new_lens, R}, {free_pages, n_free}, {free_head, free_head ? 1 : 0}};
+  for (int i = 0; i < 5; ++i)  // the first five are written
+    for (int j = i + 1; j < 9; ++j) {
+      const uintptr_t x = reinterpret_cast<uintptr_t>(arrays[i].at), y = reinterpret_cast<uintptr_t>(arrays[j].at);
+      if (x < y + arrays[j].n * sizeof(int) && y < x + arrays[i].n * sizeof(int)) return FA_ERR_INVALID_ARG;
+    }
   fa::PlanArgs a;
   std::memset(&a, 0, sizeof(a));
   int sms = 0;

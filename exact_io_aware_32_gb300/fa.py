@@ -493,7 +493,7 @@ def paged_plan(ctx_lens, new_lens, block_table, free_pages, page_size: int, num_
     """Plan a step of R requests: pages for their new tokens out of ``free_pages`` (from entry ``free_head`` on, an
     int32 [1] tensor) into ``block_table`` [R, max_pages] (in place), and where each of the ``num_tokens`` packed
     rows goes. All tensors int32 on the GPU. Returns (query_start [R + 1], seq_lens [R], slots [num_tokens],
-    pages_taken [1]); ``out``: the four tensors to write them into."""
+    pages_taken [1]); ``out``: the four tensors to write them into, none of them an input's memory."""
     if stream is not None:
         with _on(stream, ctx_lens):
             return paged_plan(ctx_lens, new_lens, block_table, free_pages, page_size, num_tokens, free_head, out)

@@ -293,7 +293,9 @@ FA_API int fa_bwd_dropout(const void* q, const void* k, const void* v, const voi
  *   slots          [out]     device int32 [T]: the slot of each packed row; -1 for rows from query_start[R] on
  *   pages_taken    [out]     device int32 [1]: entries of free_pages taken
  * Nothing but the four outputs and the table entries is changed, so the same
- * call again gives the same plan; the caller moves free_head on.
+ * call again gives the same plan; the caller moves free_head on. The outputs
+ * and the table share no memory with one another or with an input (lengths
+ * written over lengths that are still read): FA_ERR_INVALID_ARG.
  * Reported by fa_device_status: FA_ERR_INVALID_ARG for a negative length
  * (taken as 0), a request longer than max_pages pages or more than T new
  * tokens (the tokens past either get slot -1 or no row; seq_lens and
