@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_paged_plan_kernel(const __gri
   const int r0 = blockIdx.x * a.group, r1 = min(a.R, r0 + a.group);
   ptx::grid_release();
   ptx::grid_wait();
-  const int head = max(a.free_head ? *a.free_head : 0, 0);
+  const int told = a.free_head ? *a.free_head : 0, head = max(told, 0);
   const long long avail = max(a.n_free - head, 0);
 
   // rows and pages of the requests before this group
@@ -117,8 +117,9 @@ __global__ void __launch_bounds__(kPlanThreads) fa_paged_plan_kernel(const __gri
       int* tab = a.block_table + (long long)(c0 + i) * a.max_pages;
       auto fresh = [&](long long x) { return first_page + x < avail ? a.free_pages[head + first_page + x] : -1; };
       for (int x = slice * 32 + lane; x < m.pages; x += 32 * slices) {
-        tab[m.held + x] = fresh(x);
-        if (first_page + x >= avail) atomicOr(a.status, kStatusNoPages);
+        const int page = fresh(x);
+        tab[m.held + x] = page;
+        if (page < 0) atomicOr(a.status, first_page + x >= avail ? kStatusNoPages : kStatusBadLength);
       }
       const long long n_rows = min(m.rows, (long long)a.T - first_row);
       for (long long x = slice * 32 + lane; x < n_rows; x += 32 * slices) {
@@ -141,6 +142,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_paged_plan_kernel(const __gri
     if (slice == 0 && tid == 0) {
       a.query_start[a.R] = (int)min(rows, (long long)a.T);
       *a.pages_taken = (int)min(pages, avail);
+      if (told < 0) atomicOr(a.status, kStatusBadLength);
     }
     for (long long t = rows + slice * kPlanThreads + tid; t < a.T; t += (long long)kPlanThreads * slices)
       a.slots[t] = -1;

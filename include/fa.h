@@ -299,9 +299,10 @@ FA_API int fa_bwd_dropout(const void* q, const void* k, const void* v, const voi
  * Reported by fa_device_status: FA_ERR_INVALID_ARG for a negative length
  * (taken as 0), a request longer than max_pages pages or more than T new
  * tokens (the tokens past either get slot -1 or no row; seq_lens and
- * query_start stay within them), or a token whose page among those already
- * held is negative (slot -1); FA_ERR_NO_PAGES when free_pages runs out (the
- * entries and slots that lack a page are -1).
+ * query_start stay within them), a negative free_head (taken as 0), a page
+ * taken that is negative, or a token whose page among those already held is
+ * negative (slot -1 for the tokens of either); FA_ERR_NO_PAGES when free_pages
+ * runs out (the entries and slots that lack a page are -1).
  * Returns FA_OK or an fa_status error code.
  */
 FA_API int fa_paged_plan(const int* ctx_lens, const int* new_lens, int R, int page_size, const int* free_pages,

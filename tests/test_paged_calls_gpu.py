@@ -172,3 +172,24 @@ def test_the_widest_table(d, fp8, n):
         assert bool(((o[t].double().cpu() - want).abs() <= 2.0 ** -8 * want.abs() + 2.0 ** -12 * mag).all()), t
         s = math.sqrt(d) * c + math.log(seen.shape[0])
         assert bool(((lse[t].double().cpu() - s).abs() <= 2.0 ** -12).all()), t
+
+
+def test_plan_reports_a_bad_free_list():
+    """A negative page in the free list and a negative head are reported like any other entry out of range; what does
+    not depend on them is right."""
+    tab = ints([[3, -1], [-1, -1]])
+    start, lens, slots, taken = fa.paged_plan(ints([10, 0]), ints([10, 4]), tab, ints([-5, 7]), 16, 14)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(True) == fa.FA_ERR_INVALID_ARG
+    assert start.tolist() == [0, 10, 14] and lens.tolist() == [20, 4] and taken.tolist() == [2]
+    assert slots.tolist() == [3 * 16 + p for p in range(10, 16)] + [-1] * 4 + [7 * 16 + p for p in range(4)]
+    assert tab.tolist()[1] == [7, -1] and tab.tolist()[0][0] == 3
+    tab = ints([[3, -1], [-1, -1]])
+    start, lens, slots, taken = fa.paged_plan(ints([10, 0]), ints([2, 4]), tab, ints([5, 7]), 16, 6, free_head=ints([-2]))
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(True) == fa.FA_ERR_INVALID_ARG
+    assert tab.tolist() == [[3, -1], [5, -1]] and taken.tolist() == [1]
+    assert slots.tolist() == [58, 59, 80, 81, 82, 83]
+    # a negative page that nobody takes is nobody's fault
+    fa.paged_plan(ints([10, 0]), ints([2, 4]), tab, ints([5, -7]), 16, 6)
+    parity.check_status()
