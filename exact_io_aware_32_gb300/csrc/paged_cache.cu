@@ -164,12 +164,6 @@ __device__ __forceinline__ float quotient_odd(float x, float f, float inv) {
   const float y = r != 0.f ? __uint_as_float(odd) : q;
   return fabsf(q0) < 512.f ? y : q0;  // past the largest code, infinite or NaN: as it is
 }
-// Factors far from 1, where the remainder or 1 / f would leave the normal range: by division.
-__device__ __forceinline__ float quotient_odd_far(float x, float f) {
-  const float q = __fdiv_rz(x, f);
-  const bool inexact = isfinite(q) && __fmaf_rn(-q, f, x) != 0.f;
-  return inexact ? __uint_as_float(__float_as_uint(q) | 1u) : q;
-}
 
 // Four values to E4M3 codes, nearest even, +-448 beyond, NaN for NaN.
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
@@ -181,18 +175,23 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d) {
   return r;
 }
 
+// Factors far from 1, where the remainder or 1 / f would leave the normal range: f and the values are first multiplied by
+// a power of two, 2^120 or 2^-110. f, subnormal or not, stays exact so. A value that overflows is 2^100 factors or more,
+// the largest code; one that is rounded is below 2^-100 factors, code zero.
 struct Factor {
-  float f, inv;
-  bool near;
+  float f, inv, scale;
 };
-__device__ __forceinline__ Factor factor_of(float f) { return {f, 1.0f / f, f > 0x1p-100f && f < 0x1p100f}; }
+__device__ __forceinline__ Factor factor_of(float f) {
+  const float scale = f <= 0x1p-100f ? 0x1p120f : f >= 0x1p100f ? 0x1p-110f : 1.0f;
+  return {f * scale, 1.0f / (f * scale), scale};
+}
 
 // Four bf16 values as codes, each quotient rounded to odd first.
-__device__ __noinline__ uint32_t quantise4_exact(uint32_t lo, uint32_t hi, float f, float inv, bool near) {
+__device__ __noinline__ uint32_t quantise4_exact(uint32_t lo, uint32_t hi, float f, float inv, float scale) {
   float x[4] = {__uint_as_float(lo << 16), __uint_as_float(lo & 0xffff0000u), __uint_as_float(hi << 16),
                 __uint_as_float(hi & 0xffff0000u)};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = near ? quotient_odd(x[i], f, inv) : quotient_odd_far(x[i], f);
+  for (int i = 0; i < 4; ++i) x[i] = quotient_odd(x[i] * scale, f, inv);
   return e4m3x4(x[0], x[1], x[2], x[3]);
 }
 
@@ -204,13 +203,13 @@ __device__ __forceinline__ uint32_t quantise4(uint32_t lo, uint32_t hi, const Fa
   const float x[4] = {__uint_as_float(lo << 16), __uint_as_float(lo & 0xffff0000u), __uint_as_float(hi << 16),
                       __uint_as_float(hi & 0xffff0000u)};
   float q[4];
-  bool exact = !s.near;
+  bool exact = s.scale != 1.0f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     q[i] = x[i] * s.inv;
     exact |= ((__float_as_uint(q[i]) - 0x7FFFEu) & 0xFFFFFu) <= 4u || fabsf(q[i]) < 0x1p-6f;
   }
-  return exact ? quantise4_exact(lo, hi, s.f, s.inv, s.near) : e4m3x4(q[0], q[1], q[2], q[3]);
+  return exact ? quantise4_exact(lo, hi, s.f, s.inv, s.scale) : e4m3x4(q[0], q[1], q[2], q[3]);
 }
 
 // 32 bytes of a row (16 elements) at a time per thread; keys in grid.y 0, values
@@ -227,6 +226,8 @@ __global__ void __launch_bounds__(256) fa_paged_store_kernel(const __grid_consta
   const unsigned row_shift = a.d == 64 ? 2u : 3u, per_token = (unsigned)a.Hkv << row_shift;  // pieces of a row, of a token
   const bool value = blockIdx.y != 0;
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  Factor f{};
+  if constexpr (FP8) f = factor_of(value ? a.descale_v : a.descale_k);
   ptx::grid_release();
   ptx::grid_wait();
   long long t = i <= 0xFFFFFFFFll ? (unsigned)i / per_token : i / per_token;  // (64-bit division takes far longer)
@@ -253,7 +254,6 @@ __global__ void __launch_bounds__(256) fa_paged_store_kernel(const __grid_consta
     const long long row = (((long long)page * a.Hkv + h) << a.page_shift) + (slot & ((1 << a.page_shift) - 1));
     const long long at = row * a.d + c * 16;
     if constexpr (FP8) {
-      const Factor f = factor_of(value ? a.descale_v : a.descale_k);
       *reinterpret_cast<uint4*>(cache + at) = make_uint4(quantise4(w0.x, w0.y, f), quantise4(w0.z, w0.w, f),
                                                          quantise4(w1.x, w1.y, f), quantise4(w1.z, w1.w, f));
     } else {

@@ -193,3 +193,30 @@ def test_plan_reports_a_bad_free_list():
     # a negative page that nobody takes is nobody's fault
     fa.paged_plan(ints([10, 0]), ints([2, 4]), tab, ints([5, -7]), 16, 6)
     parity.check_status()
+
+
+# Factors past 2^-100 and 2^100 and subnormal ones; then f = floor(2^20 X / 17) 2^-149 for 8-bit X, where x = X 2^-133 lies so
+# little above f times 17 / 16, the middle of two codes, that x - 17 / 16 f is less than half the smallest subnormal.
+FAR = [1.1 * 2.0 ** -101, 1.1 * 2.0 ** 101, 2.0 ** -100, 2.0 ** 100, 1e-37, 1e37, 1e-38, 3e-39, 1e-40, 7 * 2.0 ** -149, 2.0 ** -149,
+       2.0 ** -126 * 1.37, 2.0 ** -127 * 1.9, 3.4e38] + [(2 ** 20 * X // 17) * 2.0 ** -149 for X in range(136, 256)]
+
+
+def test_store_rounds_once_with_factors_far_from_one():
+    """Every finite bf16 value over each factor, as the exact quotient rounds."""
+    bits = torch.arange(1 << 16, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    x = bits[torch.isfinite(bits.float())]
+    x = torch.cat([x, torch.zeros((-x.numel()) % 64)]).to(torch.bfloat16).reshape(-1, 1, 64)
+    T = x.shape[0]
+    gx, slots = x.cuda(), ints(list(range(T)))
+    near = 0
+    for f in map(f32, FAR):
+        k8, v8 = (torch.zeros((T // 16 + 1, 1, 16, 64), dtype=torch.uint8, device="cuda") for _ in range(2))
+        fa.paged_store(gx, gx, slots, k8, v8, f, f)
+        parity.check_status()
+        # in 64 bits the quotient of 8 and 24 bits is never rounded onto the middle of two codes
+        want = paged_ref.e4m3(x.double() / f).float().to(torch.float8_e4m3fn).float()
+        got = k8.cpu().view(torch.float8_e4m3fn).float().reshape(-1, 1, 64)[:T]
+        assert torch.equal(got, want), (f, x[got != want])
+        assert torch.equal(k8, v8)
+        near += int(((x.double() / f - 17 / 16).abs() < 2.0 ** -24).sum())
+    assert near >= 50  # the factors do what they are there for
