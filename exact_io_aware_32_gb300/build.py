@@ -1,10 +1,13 @@
-"""Builds the CUDA library libfa.so in-tree with nvcc, for sm_103a only, and with the
-host compiler the small module through which torch tensors reach the paged cache's calls.
+"""Builds the CUDA library libfa.so in-tree with nvcc, for sm_103a only.
 
 Each translation unit is compiled in parallel; the objects are linked into
 ``exact_io_aware_32_gb300/_build/libfa.so`` with the CUDA runtime linked
 statically, so the library has no dependency on libcuda at load time (the
 driver's tensor-map encoder is looked up at run time).
+
+``build_torch_module`` builds, with the host compiler, the small module through
+which torch tensors reach the paged cache's calls: on its own, since the library
+needs neither torch nor a host tool chain that can compile against it.
 """
 from __future__ import annotations
 
@@ -31,10 +34,11 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", 
 
 
 def torch_module() -> str:
-    """Path of the module built against the torch that is installed (another torch is another file)."""
+    """Path of the module built against the torch that is installed, for this interpreter (others are other files)."""
     import torch
 
-    return os.path.join(BUILD, "_fa_torch." + re.sub(r"[^0-9A-Za-z]+", "_", torch.__version__) + ".so")
+    tags = (torch.__version__, sysconfig.get_config_var("SOABI") or sys.implementation.cache_tag)
+    return os.path.join(BUILD, ".".join(["_fa_torch"] + [re.sub(r"[^0-9A-Za-z]+", "_", t) for t in tags] + ["so"]))
 
 
 def _torch_module_cmd(out: str) -> list:
@@ -77,19 +81,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
             if verbose:
                 cmd.insert(1, "-Xptxas=-v")
             procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    module = torch_module()
-    module_tmp = module + f".tmp{os.getpid()}"
-    if force or _stale(module, [os.path.join(CSRC, "fa_torch.cpp")]):
-        procs.append(("fa_torch.cpp", subprocess.Popen(_torch_module_cmd(module_tmp), stdout=subprocess.PIPE,
-                                                       stderr=subprocess.STDOUT)))
     for src, p in procs:
         out, _ = p.communicate()
         if p.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}:\n{out.decode(errors='replace')}")
         if verbose and out:
             sys.stderr.write(out.decode(errors="replace"))
-    if os.path.exists(module_tmp):
-        os.replace(module_tmp, module)
     if force or _stale(LIB, objs):
         tmp = LIB + f".tmp{os.getpid()}"
         cmd = [nvcc()] + ARCH + ["-shared", "-o", tmp] + objs + ["-Xcompiler", "-fPIC"]
@@ -98,6 +95,18 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"link failed:\n{r.stdout.decode(errors='replace')}")
         os.replace(tmp, LIB)
     return LIB
+
+
+def build_torch_module(force: bool = False) -> str:
+    path = torch_module()
+    if force or _stale(path, [os.path.join(CSRC, "fa_torch.cpp")]):
+        os.makedirs(BUILD, exist_ok=True)
+        tmp = path + f".tmp{os.getpid()}"
+        r = subprocess.run(_torch_module_cmd(tmp), stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed on fa_torch.cpp:\n{r.stdout.decode(errors='replace')}")
+        os.replace(tmp, path)
+    return path
 
 
 if __name__ == "__main__":

@@ -23,8 +23,6 @@ import math
 import os
 import threading
 
-import torch
-
 from . import build as _build
 
 FA_OK = 0
@@ -466,9 +464,8 @@ def _paged():
         import importlib.util
 
         lib = load()
-        path = _build.torch_module()
-        if not os.path.exists(path):
-            _build.build()
+        with _lock:
+            path = _build.build_torch_module()
         loader = importlib.machinery.ExtensionFileLoader("_fa_torch", path)
         module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_fa_torch", path, loader=loader))
         loader.exec_module(module)
@@ -481,6 +478,8 @@ def _paged():
 def _on(stream, x):
     """The context of a call on ``stream`` (a torch.cuda.Stream or a handle) of the device of tensor ``x``: the tensors it
     allocates are that stream's. Handle 0 is the default stream (an ExternalStream of 0 would be a new stream)."""
+    import torch
+
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=x.device) if stream else torch.cuda.default_stream(x.device)
     elif stream.device != x.device:
