@@ -338,7 +338,11 @@ FA_API int fa_paged_store(const void* k, const void* v, long long k_stride, long
  *   lse      [out] fp32 [T, Hq], the logsumexp of each row's visible scaled scores
  *   max_new  what the caller knows of the most new tokens a request has; it
  *            only chooses how the work is laid out, any value >= 1 is right
- *   scale    as in fa_fwd; with fp8 the keys and values are descale * code
+ *   scale    as in fa_fwd; with fp8 the keys and values are descale * code,
+ *            and q enters the products as two E4M3 parts of each row scaled
+ *            by a power of two: an element is then off by less than 2^-16 of
+ *            its row's largest magnitude (by nothing if it is above 2^-9 of
+ *            it), a score by scale * descale_k * sum |code| times that
  *   causal   != 0: new token i of n sees keys 0 .. seq_len - n + i; else every key of its request
  *   workspace, workspace_bytes
  *            at least fa_fwd_paged_workspace_bytes bytes, 256-byte aligned;

@@ -220,3 +220,32 @@ def test_store_rounds_once_with_factors_far_from_one():
         assert torch.equal(k8, v8)
         near += int(((x.double() / f - 17 / 16).abs() < 2.0 ** -24).sum())
     assert near >= 50  # the factors do what they are there for
+
+
+@pytest.mark.parametrize("most", [1, 60])
+@pytest.mark.parametrize("times", [1, 30, 300])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_dominating_channel_over_e4m3_keys(d, times, most):
+    """One channel of q far above the others, its keys small, so that what the two E4M3 parts of q lose of the others is
+    what shows. An element of q is off by less than 2^-16 of its row's largest, a score by D = scale f_k 2^-16 max |q| sum
+    |code| at most, a weight by a factor within e^+-2D, the logsumexp by D; with that the roundings of P to f16 (2^-11),
+    of o (2^-8), and of fp32 scores (|s| < 40: 128 2^-24 sum |q k| scale < 2^-10)."""
+    c = paged_ref.case([(500, 1), (2000, most), (60, 1)], 8, 2, d, 16, fp8=True, seed=70 + d)
+    c["q"][..., 5] = (c["q"][..., 5].float().sign() * times).to(torch.bfloat16)
+    codes = c["k_cache"].float()
+    codes[..., 5] = (codes[..., 5] / times).clamp(-20, 20)  # (NaN where nothing was written stays)
+    c["k_cache"] = codes.to(torch.float8_e4m3fn)
+    g = on_gpu(c)
+    o, lse = attend(c, g, max_new=most)
+    parity.check_status()
+    scale = 1.0 / math.sqrt(d)
+    ro, rl, spread = paged_ref.attention(c["q"], c["k_cache"], c["v_cache"], c["table"], c["start"], c["lens"], scale, True,
+                                         c["fk"], c["fv"])
+    worst = float(torch.nan_to_num(c["k_cache"].float()).abs().sum(-1).max())
+    D = 2.0 ** -16 * c["q"].double().abs().amax(-1) * scale * c["fk"] * worst
+    n = c["start"][-1]
+    o, lse = o[:n].double().cpu(), lse[:n].double().cpu()
+    assert bool(((lse - rl[:n]).abs() <= D[:n] + 2.0 ** -10).all())
+    part = torch.expm1(2 * D)[:n, :, None] + 2.0 ** -10 + 2.0 ** -11
+    assert bool(((o - ro[:n]).abs() <= 2.0 ** -8 * ro[:n].abs() + part * spread[:n]).all())
+    print(times, float(D.max()), float((lse - rl[:n]).abs().max()))
