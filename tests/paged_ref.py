@@ -96,3 +96,21 @@ def case(lens, Hq, Hkv, d, ps, fp8=False, pad=0, seed=0, fused=False, spare=3, w
     return dict(q=q, k=k, v=v, k_cache=caches[0], v_cache=caches[1], table=table, start=start,
                 lens=[c + n for c, n in lens], ctx=[c for c, _ in lens], new=[n for _, n in lens], fk=fk, fv=fv, T=T,
                 free=perm[at:], R=R, Hq=Hq, Hkv=Hkv, d=d, ps=ps, fp8=fp8)
+
+
+def rms_errors(o, ro, start):
+    """Relative RMS error of o [T, Hq, d] against ro, by request and query head: [(request, head, error)]."""
+    out = []
+    for r in range(len(start) - 1):
+        a, b = o[start[r]:start[r + 1]].double(), ro[start[r]:start[r + 1]].double()
+        if a.numel():
+            e = ((a - b) ** 2).sum((0, 2)) / (b ** 2).sum((0, 2)).clamp(min=1e-300)
+            out += [(r, h, math.sqrt(float(x))) for h, x in enumerate(e)]
+    return out
+
+
+def rms_bound(fp8):
+    """What relative RMS error the roundings leave: those of independent weights in P and of o are each at most half a step
+    of 2^-7 relative and spread evenly over it, 2^-8 / sqrt(3) (P over E4M3 caches, in f16: 2^-11 / sqrt(3)); added as
+    squares 0.0032 (0.0023), and a quarter more because a head of one token is 64 or 128 of them."""
+    return 1.25 * math.sqrt((4.0 ** -11 if fp8 else 4.0 ** -8) + 4.0 ** -8) / math.sqrt(3)
