@@ -114,6 +114,9 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int row, int end, int l
   __syncwarp();
 }
 
+// With bf16 caches P enters O += P V as bf16, since one tcgen05.mma takes both 16-bit operands of one type: half a step
+// of each weight, 2^-8 at most, which leaves o a relative RMS error of 0.0020 to 0.0024 where rounding o alone leaves
+// 0.0017. The weights' sum is taken before that rounding, in fp32.
 // ---------------------------------------------------------------- E4M3 caches
 // Keys stay codes: S = Q K^T on 8-bit operands (kind::f8f6f4), with Q as two of
 // them, hi + lo. A bf16 value has 8 significant bits; hi takes the upper

@@ -520,9 +520,11 @@ def forward_paged(q, k_cache, v_cache, block_table, query_start, seq_lens, max_n
                   out=None, lse=None, workspace=None, stream=None):
     """Attention of the packed new tokens q [T, Hq, d] (bf16) over the paged caches, which hold their keys and values
     already (paged_store): request r has rows query_start[r] .. query_start[r + 1] - 1, seq_lens[r] keys and the pages
-    of block_table[r]. ``max_new``: the most new tokens a request has, if known (only speed depends on it). ``out``
-    and ``lse`` are written in place if given, rows of no request left as they are (zeros in the ones allocated
-    here). Returns (o [T, Hq, d], lse [T, Hq])."""
+    of block_table[r]. ``max_new``: the most new tokens a request has, if known. Only speed depends on it, but much: without
+    it every request may have all T, so a batch of single tokens should say 1. The table's width stands for the longest
+    request there may be: one much wider than the step's lengths costs a second launch or two. ``out`` and ``lse`` are
+    written in place if given, rows of no request left as they are (zeros in the ones allocated here). No gradients: a
+    cache is not trained through. Returns (o [T, Hq, d], lse [T, Hq])."""
     if stream is not None:
         with _on(stream, k_cache):
             return forward_paged(q, k_cache, v_cache, block_table, query_start, seq_lens, max_new, causal, scale,

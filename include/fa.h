@@ -337,7 +337,17 @@ FA_API int fa_paged_store(const void* k, const void* v, long long k_stride, long
  *   o        [out] bf16 [T, Hq, d], contiguous
  *   lse      [out] fp32 [T, Hq], the logsumexp of each row's visible scaled scores
  *   max_new  what the caller knows of the most new tokens a request has; it
- *            only chooses how the work is laid out, any value >= 1 is right
+ *            only chooses how the work is laid out, any value >= 1 is right.
+ *            A batch of single tokens wants 1: larger values take tiles of 128
+ *            rows for a few each, or launch a second kernel for chunks that
+ *            are not there
+ *   max_pages
+ *            the table's width, also stands for what a request's length may
+ *            be: with tables for more than 1024 keys tiles are cut and a
+ *            second launch joins them (3 us of a decoding call), and batches of
+ *            chunks beside single tokens take two kernels where R * Hkv * max_pages
+ *            * page_size is above 1.5 (bf16: 4) million keys (20 us). Tables
+ *            much wider than the step's lengths cost that time
  *   scale    as in fa_fwd; with fp8 the keys and values are descale * code,
  *            and q enters the products as two E4M3 parts of each row scaled
  *            by a power of two: an element is then off by less than 2^-16 of
@@ -350,7 +360,8 @@ FA_API int fa_paged_store(const void* k, const void* v, long long k_stride, long
  * A row that sees no key (seq_len 0, or smaller than the new tokens under the
  * mask) gets o = 0, lse = -inf. Rows that belong to no request are left as
  * they were. A NaN in a row's query or in a key or value that it sees reaches
- * its result. What the cache holds past a request's last key (unwritten slots,
+ * its result; so does an infinity, but as a NaN where weights of zero meet it.
+ * What the cache holds past a request's last key (unwritten slots,
  * NaN among them) never does; keys hidden by the causal mask only must hold
  * finite values. A page outside the cache reads as zeros, a
  * seq_len past max_pages pages is cut, a negative one is 0, query_start is
