@@ -10,12 +10,13 @@
 // tile falls on a block border; the parts of a cut tile are joined by a second
 // kernel. (Tiles of at most a.whole blocks stay whole, and loads are as uneven as
 // they are: eight prompts of up to 1024 tokens, 12 heads of 64, leave the fullest
-// of 304 CTAs 19 blocks of work for 12 on average.) Every CTA works out its own range from prefix sums over the requests
-// (a few KB that all read through L2), so no kernel has to run before. Places in
-// the row are blocks in 32 bits (the host refuses calls of 2^31 blocks), since
-// this is latency that every call pays: in 64 bits, by keys, the first copy went
-// out 2500 cycles later. What the host counts holds for requests that share no
-// rows; the sum here saturates, and a row of tiles longer than that is not walked.
+// of 304 CTAs 19 blocks of work for 12 on average.) Every CTA works out its own
+// range from prefix sums over the requests (a few KB that all read through L2),
+// so no kernel has to run before. Places in the row are blocks in 32 bits (the
+// host refuses calls of 2^31 blocks), since this is latency that every call
+// pays: in 64 bits, by keys, the first copy went out 2500 cycles later. What the
+// host counts holds for requests that share no rows; the sum here saturates, and
+// a row of tiles longer than that is not walked.
 #pragma once
 #include <cstdint>
 
