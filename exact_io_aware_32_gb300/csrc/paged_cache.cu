@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kPlanThreads) fa_paged_plan_kernel(const __gri
     s_page[tid] = page;
     if (r < r1 && slice == 0) {
       a.query_start[r] = (int)min(row, (long long)a.T);
-      a.seq_lens[r] = (int)n.len;
+      a.seq_lens[r] = (int)min(n.len, n.ctx + max((long long)a.T - row, 0ll));  // tokens that have no row are not there
       if (n.bad || row + n.rows > a.T) atomicOr(a.status, kStatusBadLength);
     }
     __syncthreads();

@@ -299,7 +299,7 @@ FA_API int fa_bwd_dropout(const void* q, const void* k, const void* v, const voi
  * Reported by fa_device_status: FA_ERR_INVALID_ARG for a negative length
  * (taken as 0), a request longer than max_pages pages or more than T new
  * tokens (the tokens past either get slot -1 or no row; seq_lens and
- * query_start stay within them), a negative free_head (taken as 0), a page
+ * query_start stay within them: a token without a row is not counted), a negative free_head (taken as 0), a page
  * taken that is negative, or a token whose page among those already held is
  * negative (slot -1 for the tokens of either); FA_ERR_NO_PAGES when free_pages
  * runs out (the entries and slots that lack a page are -1).

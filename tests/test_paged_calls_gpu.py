@@ -249,3 +249,20 @@ def test_a_dominating_channel_over_e4m3_keys(d, times, most):
     part = torch.expm1(2 * D)[:n, :, None] + 2.0 ** -10 + 2.0 ** -11
     assert bool(((o - ro[:n]).abs() <= 2.0 ** -8 * ro[:n].abs() + part * spread[:n]).all())
     print(times, float(D.max()), float((lse - rl[:n]).abs().max()))
+
+
+def test_plan_with_more_tokens_than_rows_keeps_the_rest_right():
+    """Ten new tokens for six rows: reported; the request that is cut has the keys of the tokens that got a row, the one
+    after it none of its own, so that the step's attention reads nothing that was never stored."""
+    Hq, Hkv, d, ps = 4, 2, 64, 16
+    c = paged_ref.case([(20, 4), (33, 3), (18, 3)], Hq, Hkv, d, ps, seed=90)
+    g = on_gpu(c)
+    start, lens, slots, _ = fa.paged_plan(ints(c["ctx"]), ints(c["new"]), g["table"], ints([0]), ps, 6)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(True) == fa.FA_ERR_INVALID_ARG
+    assert start.tolist() == [0, 4, 6, 6] and lens.tolist() == [24, 35, 18]
+    place = lambda r, p: c["table"][r][p // ps] * ps + p % ps  # noqa: E731
+    assert slots.tolist() == [place(0, p) for p in range(20, 24)] + [place(1, p) for p in range(33, 35)]
+    o, lse = fa.forward_paged(g["q"][:6], g["k_cache"], g["v_cache"], g["table"], start, lens, max_new=4)
+    parity.check_status()
+    check(c, o, lse, start=start.tolist(), lens=lens.tolist())
