@@ -25,9 +25,10 @@ LIB = os.path.join(BUILD, "libfa.so")
 INCLUDE = os.path.join(os.path.dirname(PKG), "include")
 
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd_persist.cu", "fa_bwd.cu", "fa_bwd_noalloc.cu", "schedule.cu", "paged_api.cu",
-           "paged_cache.cu", "paged_fwd.cu", "paged_few.cu", "paged_chunk.cu"]
+           "paged_cache.cu", "paged_fwd.cu", "paged_few.cu", "paged_chunk.cu", "rope_api.cu", "rope.cu",
+           "fa_fwd_window.cu"]
 HEADERS = ["ptx.cuh", "block_order.cuh", "fa_internal.h", "philox.cuh", "paged.h",
-           "paged_work.cuh", "paged_pipe.cuh"]
+           "paged_work.cuh", "paged_pipe.cuh", "quant.cuh", "rope.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-diag-suppress", "177"]
@@ -99,7 +100,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
 
 def build_torch_module(force: bool = False) -> str:
     path = torch_module()
-    if force or _stale(path, [os.path.join(CSRC, "fa_torch.cpp")]):
+    if force or _stale(path, [os.path.join(CSRC, "fa_torch.cpp"), os.path.join(INCLUDE, "fa.h")]):
         os.makedirs(BUILD, exist_ok=True)
         tmp = path + f".tmp{os.getpid()}"
         r = subprocess.run(_torch_module_cmd(tmp), stdout=subprocess.PIPE, stderr=subprocess.STDOUT)

@@ -84,6 +84,12 @@ int check_shape(int B, int H, int N, int d, float scale) {
   return FA_OK;
 }
 
+int check_window(int B, int Hq, int Hkv, int Nq, int Nk, int d, float scale, int window, int sinks) {
+  if (window < 1 || sinks < 0 || Hkv < 1 || Hq % Hkv || Nq > Nk) return FA_ERR_INVALID_ARG;
+  const int st = check_shape(B, Hq, Nq, d, scale);
+  return st == FA_OK ? check_shape(B, Hkv, Nk, d, scale) : st;
+}
+
 // Tensor map over a contiguous [BH][N][d] tensor, boxes of box_x columns by
 // box_rows rows of one head, 128-byte swizzle (box_x * elem == 128 bytes).
 bool encode_3d_uncached(CUtensorMap* m, const void* base, CUtensorMapDataType dtype, int elem, int BH, int N, int d,
@@ -161,24 +167,25 @@ constexpr double kLog2e = 1.4426950408889634074;
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // The backward of every entry point: arguments validated, then the kernels (launch_bwd).
+// (window 0: none, and Hkv = H; else a window and sinks, and Hkv key heads).
 int bwd_common(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO, void* dq,
-               void* dk, void* dv, int B, int H, int Nq, int Nk, int d, float scale, int causal,
+               void* dk, void* dv, int B, int H, int Hkv, int Nq, int Nk, int d, float scale, int causal,
                const int* seqlens_q, const int* seqlens_k, int p256, unsigned long long seed, unsigned int offset,
-               void* workspace, size_t workspace_bytes, void* stream) {
+               int window, int sinks, void* workspace, size_t workspace_bytes, void* stream) {
   if (!q || !k || !v || !o || !lse || !dO || !dq || !dk || !dv) return FA_ERR_INVALID_ARG;
   int st = check_shape(B, H, Nq, d, scale);
-  if (st == FA_OK) st = check_shape(B, H, Nk, d, scale);
+  if (st == FA_OK) st = check_shape(B, Hkv, Nk, d, scale);
   if (st != FA_OK) return st;
   if (causal && Nq > Nk) return FA_ERR_INVALID_ARG;  // the first rows would see no key
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) || !aligned16(dO) ||
       !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned4(seqlens_q) || !aligned4(seqlens_k))
     return FA_ERR_MISALIGNED;
-  const size_t need = fa_bwd_kv_workspace_bytes(B, H, Nq, Nk, d);
+  const size_t need = fa_bwd_kv_workspace_bytes(B, H, Nq, Nq, d);
   if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return FA_ERR_WORKSPACE;
   DeviceInfo* di = nullptr;
   if ((st = device_info(&di)) != FA_OK) return st;
-  const int BH = B * H;
+  const int BH = B * H, BHk = B * Hkv;
   fa::BwdArgs a;
   std::memset(&a, 0, sizeof(a));
   a.Dsum = static_cast<float*>(workspace);
@@ -186,11 +193,11 @@ int bwd_common(const void* q, const void* k, const void* v, const void* o, const
   if (!encode_3d(&a.tm_q, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, BH, Nq, d, 64, 128) ||
       !encode_3d(&a.tm_do, dO, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, BH, Nq, d, 64, 128) ||
       !encode_3d(&a.tm_o, o, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, BH, Nq, d, 64, 128) ||
-      !encode_3d(&a.tm_k, k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, BH, Nk, d, 64, 128) ||
-      !encode_3d(&a.tm_v, v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, BH, Nk, d, 64, 128) ||
+      !encode_3d(&a.tm_k, k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, BHk, Nk, d, 64, 128) ||
+      !encode_3d(&a.tm_v, v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, BHk, Nk, d, 64, 128) ||
       !encode_3d(&a.tm_dq, dq, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, BH, Nq, d, 64, 128) ||
-      !encode_3d(&a.tm_dk, dk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, BH, Nk, d, 64, 128) ||
-      !encode_3d(&a.tm_dv, dv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, BH, Nk, d, 64, 128))
+      !encode_3d(&a.tm_dk, dk, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, BHk, Nk, d, 64, 128) ||
+      !encode_3d(&a.tm_dv, dv, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, BHk, Nk, d, 64, 128))
     return FA_ERR_LAUNCH;
   a.o = o;
   a.dO = dO;
@@ -210,6 +217,9 @@ int bwd_common(const void* q, const void* k, const void* v, const void* o, const
   a.drop_offset = offset;
   a.drop_scale = (float)(256.0 / (256.0 - p256));
   fa::philox::round_keys(seed, a.drop_rk);
+  a.window = window;
+  a.sinks = sinks;
+  a.group = H / Hkv;
   return fa::launch_bwd(a, di->num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
@@ -415,15 +425,65 @@ int fa_bwd_dropout(const void* q, const void* k, const void* v, const void* o, c
                    unsigned long long seed, unsigned int offset, void* workspace, size_t workspace_bytes,
                    void* stream) {
   if (p256 < 0 || p256 > 255) return FA_ERR_INVALID_ARG;
-  return bwd_common(q, k, v, o, lse, dO, dq, dk, dv, B, H, N, N, d, scale, causal, nullptr, nullptr, p256, seed,
-                    offset, workspace, workspace_bytes, stream);
+  return bwd_common(q, k, v, o, lse, dO, dq, dk, dv, B, H, H, N, N, d, scale, causal, nullptr, nullptr, p256, seed,
+                    offset, 0, 0, workspace, workspace_bytes, stream);
 }
 
 int fa_bwd_kv(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO, void* dq,
               void* dk, void* dv, int B, int H, int Nq, int Nk, int d, float scale, int causal,
               const int* seqlens_q, const int* seqlens_k, void* workspace, size_t workspace_bytes, void* stream) {
-  return bwd_common(q, k, v, o, lse, dO, dq, dk, dv, B, H, Nq, Nk, d, scale, causal, seqlens_q, seqlens_k, 0, 0, 0,
-                    workspace, workspace_bytes, stream);
+  return bwd_common(q, k, v, o, lse, dO, dq, dk, dv, B, H, H, Nq, Nk, d, scale, causal, seqlens_q, seqlens_k, 0, 0, 0,
+                    0, 0, workspace, workspace_bytes, stream);
+}
+
+int fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv, int Nq, int Nk,
+                  int d, float scale, int window, int sinks, const int* seqlens_q, const int* seqlens_k, void* stream) {
+  if (!q || !k || !v || !o || !lse) return FA_ERR_INVALID_ARG;
+  int st = check_window(B, Hq, Hkv, Nq, Nk, d, scale, window, sinks);
+  if (st != FA_OK) return st;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) || !aligned4(seqlens_q) ||
+      !aligned4(seqlens_k))
+    return FA_ERR_MISALIGNED;
+  DeviceInfo* di = nullptr;
+  if ((st = device_info(&di)) != FA_OK) return st;
+  fa::WindowArgs a;
+  std::memset(&a, 0, sizeof(a));
+  if (!encode_3d(&a.tm_q, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, B * Hq, Nq, d, 64, 128) ||
+      !encode_3d(&a.tm_k, k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, B * Hkv, Nk, d, 64, 128) ||
+      !encode_3d(&a.tm_v, v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, B * Hkv, Nk, d, 64, 128))
+    return FA_ERR_LAUNCH;
+  a.o = o;
+  a.lse = lse;
+  a.status = di->status;
+  a.B = B;
+  a.Hkv = Hkv;
+  a.group = Hq / Hkv;
+  a.Nq = Nq;
+  a.Nk = Nk;
+  a.d = d;
+  a.scale_log2 = (float)((double)scale * kLog2e);
+  a.window = window < Nk ? window : Nk;
+  a.sinks = sinks < Nk ? sinks : Nk;
+  a.seqlens_q = seqlens_q;
+  a.seqlens_k = seqlens_k;
+  a.test_fault = g_test_fault.exchange(0);
+  return fa::launch_fwd_window(a, di->num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+size_t fa_bwd_window_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d, int window, int sinks) {
+  if (check_window(B, Hq, Hkv, Nq, Nk, d, 1.0f, window, sinks) != FA_OK) return 0;
+  return fa_bwd_kv_workspace_bytes(B, Hq, Nq, Nq, d);
+}
+
+int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO, void* dq,
+                  void* dk, void* dv, int B, int Hq, int Hkv, int Nq, int Nk, int d, float scale, int window, int sinks,
+                  const int* seqlens_q, const int* seqlens_k, void* workspace, size_t workspace_bytes, void* stream) {
+  const int st = check_window(B, Hq, Hkv, Nq, Nk, d, scale, window, sinks);
+  if (st != FA_OK) return st;
+  if (!workspace || workspace_bytes < fa_bwd_window_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, window, sinks))
+    return FA_ERR_WORKSPACE;
+  return bwd_common(q, k, v, o, lse, dO, dq, dk, dv, B, Hq, Hkv, Nq, Nk, d, scale, 1, seqlens_q, seqlens_k, 0, 0, 0,
+                    window < Nk ? window : Nk, sinks < Nk ? sinks : Nk, workspace, workspace_bytes, stream);
 }
 
 const char* fa_status_string(int status) {

@@ -37,9 +37,11 @@
 // elementwise work.
 //
 // Template flags add per-sequence lengths (padding masks: each tile reads its
-// sequence's lengths) and dropout (the forward's Philox mask made again from
-// the seed, applied to P^T for dV and to dP in dS) without changing the plain
-// kernels.
+// sequence's lengths), dropout (the forward's Philox mask made again from
+// the seed, applied to P^T for dV and to dP in dS) and a sliding window with
+// grouped heads (each tile walks only the blocks that it sees, and a dK/dV tile
+// the query heads that share its key head one after another) without changing
+// the plain kernels.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -160,15 +162,37 @@ __device__ __forceinline__ constexpr int dkdv_half_kstep(int h, int i) { return 
 
 // A dK/dV tile: (head, key block), its first query block and how many it
 // sees, and the sequence's query rows sq and keys sk (padding masks).
+// (WIN: bh is the key head; n counts the nq query blocks from i_start on of each of its a.group query heads in turn.)
 struct DkdvTile {
-  int bh, kblk, i_start, n, sq, sk;
+  int bh, kblk, i_start, n, sq, sk, nq;
 };
 
 // VARLEN: per-sequence lengths are given (padding masks); without them the
 // lengths are the array sizes, which the kernels then take as constants.
-template <bool CAUSAL, bool VARLEN>
+template <bool CAUSAL, bool VARLEN, bool WIN>
 __device__ __forceinline__ DkdvTile dkdv_tile(int L, const BwdArgs& a, int nkv) {
   DkdvTile t;
+  if constexpr (WIN) {
+    const int BH = a.BH / a.group, sunk = (a.sinks + 127) / 128;
+    if (L < BH * sunk) {  // blocks that every row sees first, of all heads
+      t.kblk = L / BH;
+      t.bh = L - t.kblk * BH;
+    } else {
+      grouped_index(L - BH * sunk, BH, nkv - sunk, a.head_group, t.bh, t.kblk);
+      t.kblk += sunk;
+    }
+    seq_lens(a.seqlens_q, a.seqlens_k, t.bh / (a.H / a.group), a.Nq, a.Nk, true, t.sq, t.sk);
+    const int off = t.sk - t.sq, key = t.kblk * 128;
+    t.i_start = max(key - off, 0) / 128;
+    const int last = key < a.sinks ? t.sq - 1 : min(t.sq - 1, min(key + 127, t.sk - 1) + a.window - 1 - off);
+    t.nq = (last >> 7) + 1 - t.i_start;
+    t.n = t.nq * a.group;
+    if (key >= t.sk || t.nq <= 0) {  // keys that no row sees: one block, fully masked, gives dk = dv = 0
+      t.i_start = 0;
+      t.nq = t.n = 1;
+    }
+    return t;
+  }
   grouped_index(L, a.BH, nkv, a.head_group, t.bh, t.kblk);  // key block 0 (the heaviest) first
   t.sq = a.Nq;
   t.sk = a.Nk;
@@ -187,7 +211,8 @@ __device__ __forceinline__ DkdvTile dkdv_tile(int L, const BwdArgs& a, int nkv) 
 }
 
 // DROP: the forward's dropout mask, made again from the seed (philox.cuh).
-template <int D, bool CAUSAL, bool VARLEN, bool DROP = false>
+// WIN (with CAUSAL and VARLEN): a window of a.window keys and a.sinks first ones, a.group query heads per key head.
+template <int D, bool CAUSAL, bool VARLEN, bool DROP = false, bool WIN = false>
 __global__ void __launch_bounds__(352, 1) fa_bwd_dkdv_kernel(const __grid_constant__ BwdArgs a) {
   using C = DkdvCfg<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -203,7 +228,7 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dkdv_kernel(const __grid_consta
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int Nq = a.Nq;  // rows of the q / lse / D arrays
   const int nkv = (a.Nk + C::BK - 1) / C::BK;
-  const int total = a.BH * nkv;
+  const int total = (WIN ? a.BH / a.group : a.BH) * nkv;
 
   if (threadIdx.x == 0) {
     bars.abort = 0;
@@ -321,7 +346,7 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dkdv_kernel(const __grid_consta
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.item_full[is]);  // release: the tile index is visible
       if (L >= total) break;
-      const DkdvTile t = dkdv_tile<CAUSAL, VARLEN>(L, a, nkv);
+      const DkdvTile t = dkdv_tile<CAUSAL, VARLEN, WIN>(L, a, nkv);
       bars.st_bh[k & 7] = t.bh;  // every lane writes the same values
       bars.st_kblk[k & 7] = t.kblk;
       bars.st_last[k & 7] = g + t.n - 1;
@@ -335,6 +360,7 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dkdv_kernel(const __grid_consta
       }
       __syncwarp();
       kv_tiles = k + 1;
+      int qh = WIN ? t.bh * a.group : t.bh, qb = t.i_start;  // the query head and block of this iteration
       for (int it = 0; it < t.n; ++it, ++g) {
         const int qs = g % C::kQStages, ds = g % C::kDOStages;
         if (!(ok = store_due(g, C::kQStages))) break;
@@ -344,7 +370,7 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dkdv_kernel(const __grid_consta
           mbar_arrive_expect_tx(&bars.q_full[qs], C::kTileBytes);
           for (int pn = 0; pn < D / 64; ++pn)
             tma_load_3d(smem + C::kOffQ + qs * C::kTileBytes + pn * kPanelBytes, &a.tm_q, &bars.q_full[qs],
-                        pn * 64, (t.i_start + it) * C::BQ, t.bh);
+                        pn * 64, qb * C::BQ, qh);
         }
         __syncwarp();
         q_issued = g + 1;
@@ -368,10 +394,15 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dkdv_kernel(const __grid_consta
           mbar_arrive_expect_tx(&bars.do_full[ds], C::kTileBytes);
           for (int pn = 0; pn < D / 64; ++pn)
             tma_load_3d(smem + C::kOffDO + ds * C::kTileBytes + pn * kPanelBytes, &a.tm_do, &bars.do_full[ds],
-                        pn * 64, (t.i_start + it) * C::BQ, t.bh);
+                        pn * 64, qb * C::BQ, qh);
         }
         __syncwarp();
         do_issued = g + 1;
+        ++qb;
+        if (WIN && qb == t.i_start + t.nq) {  // the next head that shares these keys
+          qb = t.i_start;
+          ++qh;
+        }
       }
     }
     // the tiles still staged, the last with a full wait; then every copy in flight lands
@@ -426,7 +457,7 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dkdv_kernel(const __grid_consta
           tiles_done = true;
           return Blk{0, 0, -1};
         }
-        cursor = Blk{0, dkdv_tile<CAUSAL, VARLEN>(L, a, nkv).n, cursor.kt + 1};
+        cursor = Blk{0, dkdv_tile<CAUSAL, VARLEN, WIN>(L, a, nkv).n, cursor.kt + 1};
         return cursor;
       };
       if (warp == 10) {
@@ -563,18 +594,19 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dkdv_kernel(const __grid_consta
     // query block qb, threads 64-127 fetch D; one block ahead, through
     // registers, and negated (lse also to log2 units) only when stored a block
     // later, so that no thread waits for the load in between.
-    auto fetch = [&](const DkdvTile& t, int qb) -> float {
+    auto fetch = [&](const DkdvTile& t, int qb, int qh) -> float {
       const int q = qb * C::BQ + 64 * w + (tt & 63);
       const int sq = VARLEN ? t.sq : Nq;
-      if (tt < 64) return q < sq ? a.lse[(size_t)t.bh * Nq + q] : INFINITY;  // 2^(x - inf) = 0 past sq
-      return q < sq ? a.Dsum[(size_t)t.bh * Nq + q] : 0.f;
+      if (tt < 64) return q < sq ? a.lse[(size_t)qh * Nq + q] : INFINITY;  // 2^(x - inf) = 0 past sq
+      return q < sq ? a.Dsum[(size_t)qh * Nq + q] : 0.f;
     };
+    auto head0 = [&](const DkdvTile& t) { return WIN ? t.bh * a.group : t.bh; };
     // After a failed wait a warp keeps going without work; at every block the
     // group's named barrier also ANDs the warps' states, so the four warps
     // always agree on their blocks and tiles and meet at the same barriers.
     int L = take_tile(0);
-    DkdvTile t = L >= 0 ? dkdv_tile<CAUSAL, VARLEN>(L, a, nkv) : DkdvTile{0, 0, 0, 0, 1, 1};
-    float next = L >= 0 ? fetch(t, t.i_start) : 0.f;
+    DkdvTile t = L >= 0 ? dkdv_tile<CAUSAL, VARLEN, WIN>(L, a, nkv) : DkdvTile{0, 0, 0, 0, 1, 1, 0};
+    float next = L >= 0 ? fetch(t, t.i_start, head0(t)) : 0.f;
     bool ok = L >= 0;
     int g = 0;
     for (int k = 0; L >= 0; ++k) {
@@ -584,19 +616,25 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dkdv_kernel(const __grid_consta
       const bool keys_all_ok = (t.kblk + 1) * C::BK <= sk;  // uniform over the CTA
       const int off = sk - (VARLEN ? t.sq : Nq);  // causal: query row i sees keys 0 .. i + off
       int L_next = -1;
-      DkdvTile nt = {0, 0, 0, 0, 1, 1};
+      DkdvTile nt = {0, 0, 0, 0, 1, 1, 0};
+      int qb = t.i_start, qh = head0(t);  // the query block and head of this iteration, of the next from the fetch on
       for (int it = 0; it < t.n; ++it, ++g) {
-        const int q0 = (t.i_start + it) * C::BQ;
+        const int q0 = qb * C::BQ;
         float* rb = rowbuf + ((g & 1) * 2 + w) * 128;
         rb[tt] = tt < 64 ? -next * kLog2e : -next;  // -lse (log2 units) | -D
         ok = named_bar_and(1 + w, 128, ok);
         if (it + 1 < t.n) {
-          next = fetch(t, t.i_start + it + 1);
+          ++qb;
+          if (WIN && qb == t.i_start + t.nq) {
+            qb = t.i_start;
+            ++qh;
+          }
+          next = fetch(t, qb, qh);
         } else {  // the next tile's first block
           L_next = take_tile(k + 1);
           if (L_next >= 0) {
-            nt = dkdv_tile<CAUSAL, VARLEN>(L_next, a, nkv);
-            next = fetch(nt, nt.i_start);
+            nt = dkdv_tile<CAUSAL, VARLEN, WIN>(L_next, a, nkv);
+            next = fetch(nt, nt.i_start, head0(nt));
           }
         }
         if (!ok) continue;
@@ -621,11 +659,14 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dkdv_kernel(const __grid_consta
           // sk - sq is not a multiple of 128) and a ragged last key block need
           // masking: there a hidden score becomes -inf, so P = 0 (scale > 0).
           // Query q0 + 64 w + col sees key kblk * BK + r iff q0 + 64 w + col + off >= key.
-          if ((CAUSAL && q0 + off < (t.kblk + 1) * C::BK - 1) || !keys_all_ok) {
+          // A window also hides keys from the rows past it (unless they are sinks), which its last blocks hold.
+          if ((CAUSAL && q0 + off < (t.kblk + 1) * C::BK - 1) || !keys_all_ok ||
+              (WIN && q0 + C::BQ - 1 + off - t.kblk * C::BK >= a.window && (t.kblk + 1) * C::BK > a.sinks)) {
             const int lim = CAUSAL ? key - off - (q0 + 64 * w) : -1;  // drop columns col < lim
+            const int far = WIN ? (key < a.sinks ? 64 : lim + a.window) : 0;  // window: and col >= far
 #pragma unroll
             for (int c = 0; c < 64; ++c)
-              if (c < lim || !key_ok) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+              if (c < lim || !key_ok || (WIN && c >= far)) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
           }
           const float2 scale2 = make_float2(sl2, sl2);
 #pragma unroll
@@ -810,14 +851,18 @@ __device__ __forceinline__ void tile_row_to_tmem(const uint8_t* tile, int r, uin
   }
 }
 
-// A dQ tile: (head, query block) and the number of key blocks it sees.
 // A dQ tile: (head, query block), the key blocks it sees, and the sequence's
-// query rows sq and keys sk (padding masks).
+// query rows sq and keys sk (padding masks). WIN: its j-th block is block j of the
+// first 'sunk' ones, then block j + skip.
 struct DqTile {
-  int bh, qblk, nk, sq, sk;
+  int bh, qblk, nk, sq, sk, sunk, skip;
+  template <bool WIN>
+  __device__ __forceinline__ int at(int j) const {
+    return WIN && j >= sunk ? j + skip : j;
+  }
 };
 
-template <bool CAUSAL, bool VARLEN>
+template <bool CAUSAL, bool VARLEN, bool WIN>
 __device__ __forceinline__ DqTile dq_tile(int L, const BwdArgs& a, int nq) {
   DqTile t;
   int blk;
@@ -825,15 +870,22 @@ __device__ __forceinline__ DqTile dq_tile(int L, const BwdArgs& a, int nq) {
   t.qblk = CAUSAL ? nq - 1 - blk : blk;  // heaviest first under the causal mask
   t.sq = a.Nq;
   t.sk = a.Nk;
+  t.sunk = t.skip = 0;
   if (VARLEN) seq_lens(a.seqlens_q, a.seqlens_k, t.bh / a.H, a.Nq, a.Nk, CAUSAL, t.sq, t.sk);
   const int nkv = (t.sk + 127) / 128;
   // BQ == BK: query block i sees key blocks 0 .. (128 i + 127 + sk - sq) / 128 (with sq = sk: 0..i);
   // a block of padding rows only takes one key block, whose P = 0 gives dq = 0
   t.nk = VARLEN && t.qblk * 128 >= t.sq ? 1 : CAUSAL ? min((t.qblk * 128 + 127 + t.sk - t.sq) / 128 + 1, nkv) : nkv;
+  if (WIN && t.qblk * 128 < t.sq) {
+    const int low = max(t.qblk * 128 + t.sk - t.sq - a.window + 1, 0) / 128;  // the first row's window begins in this block
+    t.sunk = min((a.sinks + 127) / 128, low);
+    t.skip = low - t.sunk;
+    t.nk -= t.skip;
+  }
   return t;
 }
 
-template <int D, bool CAUSAL, bool VARLEN, bool DROP = false>
+template <int D, bool CAUSAL, bool VARLEN, bool DROP = false, bool WIN = false>
 __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant__ BwdArgs a) {
   using C = DqCfg<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -950,7 +1002,7 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.item_full[is]);  // release: the tile index is visible
       if (L >= total) break;
-      const DqTile t = dq_tile<CAUSAL, VARLEN>(L, a, nq);
+      const DqTile t = dq_tile<CAUSAL, VARLEN, WIN>(L, a, nq);
       if (k == 1 && !(ok = warp_wait(&bars.qt_ready, 0, abort_flag))) break;
       if (k >= 2 && !(ok = store_dq(k - 2, false))) break;
       if (k & 1)
@@ -965,6 +1017,7 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
       }
       __syncwarp();
       q_loads = k + 1;
+      const int kv_head = WIN ? t.bh / a.group : t.bh;
       for (int j = 0; j < t.nk; ++j, ++g) {
         const int sk = g % C::kKStages, sv = g % C::kVStages;
         if (!(ok = warp_wait(&bars.k_empty[sk], ((g / C::kKStages) & 1) ^ 1, abort_flag))) break;
@@ -972,7 +1025,7 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
           mbar_arrive_expect_tx(&bars.k_full[sk], C::kTileBytes);
           for (int pn = 0; pn < D / 64; ++pn)
             tma_load_3d(smem + C::kOffK + sk * C::kTileBytes + pn * kPanelBytes, &a.tm_k, &bars.k_full[sk],
-                        pn * 64, j * C::BK, t.bh);
+                        pn * 64, t.template at<WIN>(j) * C::BK, kv_head);
         }
         __syncwarp();
         k_issued = g + 1;
@@ -994,7 +1047,7 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
           mbar_arrive_expect_tx(&bars.v_full[sv], C::kTileBytes);
           for (int pn = 0; pn < D / 64; ++pn)
             tma_load_3d(smem + C::kOffV + sv * C::kTileBytes + pn * kPanelBytes, &a.tm_v, &bars.v_full[sv],
-                        pn * 64, j * C::BK, t.bh);
+                        pn * 64, t.template at<WIN>(j) * C::BK, kv_head);
         }
         __syncwarp();
         v_issued = g + 1;
@@ -1033,7 +1086,7 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
         int k = 0, g = 0;  // tile and key block over the CTA's run
         bool ok = true;
         for (int L = take_tile(0); ok && L >= 0; L = take_tile(++k)) {
-          const DqTile t = dq_tile<CAUSAL, VARLEN>(L, a, nq);
+          const DqTile t = dq_tile<CAUSAL, VARLEN, WIN>(L, a, nq);
           for (int j = 0; j < t.nk; ++j) {
             const int gj = g + j;
             if (!(ok = warp_wait2(&bars.ds_ready, gj & 1, &bars.k_full[gj % C::kKStages], k_phase(gj), abort_flag)))
@@ -1086,7 +1139,7 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
         };
         int k = 0, g = 0;  // tile and key block over the CTA's run
         int L = take_tile(0);
-        DqTile t = L >= 0 ? dq_tile<CAUSAL, VARLEN>(L, a, nq) : DqTile{0, 0, 0, 1, 1};
+        DqTile t = L >= 0 ? dq_tile<CAUSAL, VARLEN, WIN>(L, a, nq) : DqTile{0, 0, 0, 1, 1, 0, 0};
         bool ok = L >= 0;
         while (ok) {
           // the tile's first block: S needs its Q in TMEM (the warpgroups copy it
@@ -1117,7 +1170,7 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
           g += t.nk;
           ++k;
           if ((L = take_tile(k)) < 0) break;
-          t = dq_tile<CAUSAL, VARLEN>(L, a, nq);
+          t = dq_tile<CAUSAL, VARLEN, WIN>(L, a, nq);
         }
         if (elect_one()) mma_commit(&bars.teardown);  // the same lane as above: elect.sync picks the lowest
         __syncwarp();
@@ -1162,7 +1215,7 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
     int k = 0, g = 0;
     int L = take_tile(0);
     bool ok = L >= 0;
-    DqTile t = ok ? dq_tile<CAUSAL, VARLEN>(L, a, nq) : DqTile{0, 0, 0, 1, 1};
+    DqTile t = ok ? dq_tile<CAUSAL, VARLEN, WIN>(L, a, nq) : DqTile{0, 0, 0, 1, 1, 0, 0};
     float lse2 = 0.f, dsum = 0.f;
     if (ok) {
       float lr, dr;
@@ -1204,7 +1257,7 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
           break;
         }
         tc_fence_after();
-        const int k0 = j * C::BK + 64 * w;  // first key of this warpgroup's columns
+        const int kb = t.template at<WIN>(j) * C::BK, k0 = kb + 64 * w;  // first key of the block, of this warpgroup's columns
         float2 pf[32];  // P, this thread's row, keys k0 .. k0 + 63 (fp32: only dS, not P, feeds a product here)
         {
           uint32_t sr[2][32];
@@ -1220,11 +1273,14 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
           // -inf score, so P = 0 (scale > 0).
           const int sk = VARLEN ? t.sk : a.Nk;
           const int off = sk - (VARLEN ? t.sq : Nq);  // causal: query row i sees keys 0 .. i + off
-          if ((CAUSAL && (j + 1) * C::BK - 1 > t.qblk * C::BQ + off) || (j + 1) * C::BK > sk) {
+          // A window also hides the keys behind it (unless they are sinks) from the tile's later rows.
+          if ((CAUSAL && kb + C::BK - 1 > t.qblk * C::BQ + off) || kb + C::BK > sk ||
+              (WIN && t.qblk * C::BQ + C::BQ - 1 + off - kb >= a.window && kb + C::BK > a.sinks)) {
             const int lim = (CAUSAL ? min(q + off, sk - 1) : sk - 1) - k0;  // keep key k0 + col iff col <= lim
+            const int out = q + off - a.window - k0, sunk = a.sinks - k0;  // window: drop col <= out, from 'sunk' on
 #pragma unroll
             for (int c = 0; c < 64; ++c)
-              if (c > lim) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+              if (c > lim || (WIN && c <= out && c >= sunk)) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
           }
           const float2 scale2 = make_float2(sl2, sl2), shift2 = make_float2(-lse2, -lse2);
 #pragma unroll
@@ -1313,7 +1369,7 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
       DqTile nt = {0, 0, 0};
       float lse_next = 0.f, d_next = 0.f;
       if (L >= 0) {
-        nt = dq_tile<CAUSAL, VARLEN>(L, a, nq);
+        nt = dq_tile<CAUSAL, VARLEN, WIN>(L, a, nq);
         load_row_terms(nt, lse_next, d_next);
         ok = copy_q(k + 1);
       }
@@ -1396,8 +1452,12 @@ cudaError_t launch_bwd_t(const BwdArgs& a, int num_sms, cudaStream_t stream) {
   const bool varlen = a.seqlens_q || a.seqlens_k;
   auto kv = varlen ? fa_bwd_dkdv_kernel<D, CAUSAL, true> : fa_bwd_dkdv_kernel<D, CAUSAL, false>;
   if (a.drop_p256 > 0) kv = fa_bwd_dkdv_kernel<D, CAUSAL, false, true>;  // dropout: no lengths
+  if constexpr (CAUSAL)
+    if (a.window) kv = fa_bwd_dkdv_kernel<D, true, true, false, true>;
   auto kq = varlen ? fa_bwd_dq_kernel<D, CAUSAL, true> : fa_bwd_dq_kernel<D, CAUSAL, false>;
   if (a.drop_p256 > 0) kq = fa_bwd_dq_kernel<D, CAUSAL, false, true>;
+  if constexpr (CAUSAL)
+    if (a.window) kq = fa_bwd_dq_kernel<D, true, true, false, true>;
   if ((e = cudaFuncSetAttribute(kv, cudaFuncAttributeMaxDynamicSharedMemorySize, DkdvCfg<D>::kSmemBytes)) !=
       cudaSuccess)
     return e;
@@ -1405,7 +1465,7 @@ cudaError_t launch_bwd_t(const BwdArgs& a, int num_sms, cudaStream_t stream) {
       cudaSuccess)
     return e;
   // persistent: one CTA per SM at most (both main kernels take their tiles from counters)
-  const long long kv_tiles = (long long)a.BH * ((a.Nk + 127) / 128), q_tiles = (long long)a.BH * ((a.Nq + 127) / 128);
+  const long long kv_tiles = (long long)(a.window ? a.BH / a.group : a.BH) * ((a.Nk + 127) / 128), q_tiles = (long long)a.BH * ((a.Nq + 127) / 128);
   const unsigned kv_ctas = (unsigned)std::min<long long>(kv_tiles, num_sms);
   const unsigned q_ctas = (unsigned)std::min<long long>(q_tiles, num_sms);
   if constexpr (DqCfg<D>::kFuseD) {
@@ -1434,6 +1494,7 @@ cudaError_t launch_bwd(const BwdArgs& args, int num_sms, cudaStream_t stream) {
   // a CTA's fixed cost (loads before the first product, epilogue) is about 2.5 blocks of work
   a.head_group = pick_head_group(a.BH, (a.Nk + 127) / 128, a.causal != 0, num_sms, 2.5);
   a.head_group_dq = pick_head_group(a.BH, (a.Nq + 127) / 128, a.causal != 0, num_sms, 2.5);
+  if (a.window) a.head_group = a.head_group_dq = 1;  // tiles of about equal cost: a head at a time, its blocks out of L2
   if (a.d == 64)
     return a.causal ? launch_bwd_t<64, true>(a, num_sms, stream) : launch_bwd_t<64, false>(a, num_sms, stream);
   return a.causal ? launch_bwd_t<128, true>(a, num_sms, stream) : launch_bwd_t<128, false>(a, num_sms, stream);

@@ -1,0 +1,535 @@
+// Forward attention with a sliding window and a few first keys that stay visible
+// (sinks), grouped heads, on sm_103a.
+//
+// Row i of a sequence stands at p = i + sk - sq and sees key j iff j <= p and
+// (p - j < window or j < sinks). Per 128-row tile that leaves the key blocks of
+// its rows' windows, and before them the blocks of the sinks: a tile of any
+// text length streams (window + 127) / 128 + 1 blocks or so, five or nine where
+// the causal forward streams hundreds. What a tile costs besides (its Q, the first S,
+// reading O out) counts accordingly, so the CTAs are persistent as in fa_fwd_persist.cu:
+// the rings and barriers count on across tiles, and the next tile's loads and
+// first products run beside this one's epilogue. S = Q K^T, the softmax with one TMEM lane per row
+// and O += P V with P from TMEM are those of fa_fwd.cu.
+//
+// d = 128: a CTA has two tiles at a time, which share the key blocks: two query heads
+// of one key head on the same rows (or, without grouped heads, two
+// neighbouring row blocks, whose bands differ by a block at either end: each
+// skips the one that it does not see). d = 64: one tile per CTA and two CTAs per
+// SM, P in TMEM columns of its own.
+//
+// Every block but those where a window begins or ends (and a sink block beyond its sinks) is
+// unmasked: its row maximum comes with the TMEM load.
+//
+// Warp roles: a softmax warpgroup per tile, the TMA warp, the MMA warp.
+#include <algorithm>
+
+#include "fa_internal.h"
+#include "paged.h"
+#include "ptx.cuh"
+
+namespace fa {
+namespace {
+
+using namespace fa::ptx;
+
+constexpr float kLn2 = 0.693147180559945309417f;
+constexpr float kRescaleThreshold = 8.0f;  // log2 units, as in fa_fwd.cu
+
+template <int D_>
+struct WCfg {
+  static constexpr int D = D_;
+  static constexpr int kTiles = D == 64 ? 1 : 2;
+  static constexpr int kCtasPerSm = 3 - kTiles;
+  static constexpr int kPanels = D / 64, kPanelBytes = 128 * 128, kTileBytes = kPanels * kPanelBytes;
+  static constexpr int kKStages = 2, kVStages = 3;  // V is read last, so it gets the deeper ring
+  // Q: a slot per tile, or two for one tile, so that the next one's is there when this one ends
+  static constexpr int kOffQ = 0, kOffK = 2 * kTileBytes, kOffV = kOffK + kKStages * kTileBytes;
+  static constexpr int kOffBar = kOffV + kVStages * kTileBytes;
+  // No alignment slack (two CTAs share an SM's 228 KB): the kernel checks that shared memory starts on 1024 bytes.
+  static constexpr int kSmemBytes = kOffBar + 512;
+  static_assert(kSmemBytes <= 232448 && (kCtasPerSm == 1 || 2 * (kSmemBytes + 1024) <= 233472), "shared memory");
+  static constexpr uint32_t kTmemCols = kTiles == 2 ? 512u : 256u;
+  // S (fp32, 128 columns), P (bf16 pairs, 64 columns: over S, or in columns of its own) and O (fp32, D columns) of tile t
+  __host__ __device__ static constexpr uint32_t col_s(int t) { return (uint32_t)t * 128u; }
+  __host__ __device__ static constexpr uint32_t col_p(int t) { return kTiles == 2 ? col_s(t) : 128u; }
+  __host__ __device__ static constexpr uint32_t col_o(int t) { return kTiles == 2 ? 256u + (uint32_t)t * D : 192u; }
+  static constexpr int kWarpTma = 4 * kTiles, kWarpMma = 4 * kTiles + 1, kThreads = 128 * kTiles + 64;
+};
+
+struct WBars {
+  uint64_t q_full[2][2], q_free[2];  // by tile (q_full: and its items in turn); one tile: by slot
+  uint64_t k_full[2], k_empty[2], v_full[3], v_empty[3];
+  uint64_t s_full[2], p_full[2], o_done[2], o_free[2];  // (one tile: o_done follows every P V)
+  uint64_t s_free;                                      // one tile: S is in registers
+  uint64_t teardown;
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(WBars) <= 512, "barriers exceed their shared memory");
+
+// What a CTA works on at a time: up to two tiles of 128 rows of one key head, and the key blocks that they stream:
+// block j of the first 'sunk' ones, then block j + skip.
+struct Item {
+  int bhk;              // batch and key head; < 0: past the last item
+  int head[2], row[2];  // query head, first row
+  int nb[2];            // blocks up to the last one that the tile sees (0: padding rows, or no tile)
+  int sunk, skip;
+  int miss;             // a block that the second tile does not see (its window begins one later)
+  int sq, off;
+  bool there[2];        // the tile has rows of the array
+  __device__ __forceinline__ int at(int j) const { return j < sunk ? j : j + skip; }
+  __device__ __forceinline__ bool uses(int t, int j) const { return j < nb[t] && (t == 0 || j != miss); }
+};
+
+// The i-th item of this CTA. Items are dealt in rounds of one per CTA, odd rounds in reverse: a head's later rows, with whole
+// windows, first.
+template <int kTiles>
+__device__ __forceinline__ Item item(const WindowArgs& a, int i) {
+  Item x;
+  const int ctas = (int)gridDim.x, c = (int)blockIdx.x;
+  const long long L = (long long)i * ctas + ((i & 1) ? ctas - 1 - c : c);
+  x.bhk = -1;
+  if (L >= a.items) return x;
+  const int per = a.items_per_head, G = a.group, tiles = G * ((a.Nq + 127) / 128);
+  x.bhk = (int)L / per;
+  const int u0 = kTiles * (per - 1 - ((int)L - x.bhk * per));
+  int sk;
+  seq_lens(a.seqlens_q, a.seqlens_k, x.bhk / a.Hkv, a.Nq, a.Nk, true, x.sq, sk);
+  x.off = sk - x.sq;
+  int low[2] = {0, 0};
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int u = u0 + t, blk = u / G;
+    x.there[t] = t < kTiles && u < tiles;
+    x.head[t] = x.bhk * G + u - blk * G;
+    x.row[t] = blk * 128;
+    low[t] = max(x.row[t] + x.off - a.window + 1, 0) >> 7;
+    x.nb[t] = x.there[t] && x.row[t] < x.sq ? ((min(x.row[t] + 127, x.sq - 1) + x.off) >> 7) + 1 : 0;
+  }
+  const int sunk = (a.sinks + 127) >> 7;  // blocks that hold sinks
+  x.sunk = min(sunk, low[0]);
+  x.skip = low[0] - x.sunk;
+  x.miss = low[1] > low[0] && low[0] >= sunk ? x.sunk : -1;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) x.nb[t] = max(x.nb[t] - x.skip, 0);
+  return x;
+}
+
+template <int D>
+__global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
+    fa_fwd_window_kernel(const __grid_constant__ WindowArgs a) {
+  using C = WCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw;
+  if (smem_u32(smem) & 1023u) {  // uniform over the CTA: every thread leaves before any barrier
+    if (threadIdx.x == 0) atomicOr(a.status, 16u);
+    return;
+  }
+  WBars& bars = *reinterpret_cast<WBars*>(smem + C::kOffBar);
+  volatile int* abort_flag = &bars.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (warp == C::kWarpTma && elect_one()) {
+    tma_prefetch_desc(&a.tm_q);
+    tma_prefetch_desc(&a.tm_k);
+    tma_prefetch_desc(&a.tm_v);
+  }
+  if (threadIdx.x == 0) {
+    bars.abort = 0;
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars.q_full[s][0], 1);
+      mbar_init(&bars.q_full[s][1], 1);
+      mbar_init(&bars.q_free[s], 1);
+      mbar_init(&bars.s_full[s], 1);
+      mbar_init(&bars.p_full[s], 128);
+      mbar_init(&bars.o_done[s], 1);
+      mbar_init(&bars.o_free[s], 128);
+    }
+    for (int s = 0; s < C::kKStages; ++s) {
+      mbar_init(&bars.k_full[s], 1);
+      mbar_init(&bars.k_empty[s], 1);
+    }
+    for (int s = 0; s < C::kVStages; ++s) {
+      mbar_init(&bars.v_full[s], 1);
+      mbar_init(&bars.v_empty[s], 1);
+    }
+    mbar_init(&bars.s_free, 128);
+    mbar_init(&bars.teardown, 1);
+    fence_mbar_init();
+  }
+  if (warp == C::kWarpMma) {
+    tmem_alloc(&bars.tmem_base, C::kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem_base;
+  grid_release();
+  grid_wait();  // nothing before this has read or written what other kernels do
+  if (a.seqlens_q || a.seqlens_k)  // the CTAs check the lengths among themselves
+    for (int b = blockIdx.x * C::kThreads + threadIdx.x; b < a.B; b += gridDim.x * C::kThreads) {
+      int sq, sk;
+      if (seq_lens(a.seqlens_q, a.seqlens_k, b, a.Nq, a.Nk, true, sq, sk)) atomicOr(a.status, kStatusBadLength);
+    }
+
+  if (warp == C::kWarpTma) {
+    // ------------------------------------------------------------ TMA producer
+    int g = 0, nk = 0, nv = 0, nq[2] = {0, 0};  // key blocks, and loads issued
+    bool ok = true;
+    // test hook: without the first Q tile, the MMA warp's first wait expires
+    bool withhold = a.test_fault == 1;
+    auto load_q = [&](const Item& x, int t) -> bool {
+      // the slot and its uses so far: tile t's own, or the two in turn
+      const int s = C::kTiles == 2 ? t : nq[t] & 1, use = C::kTiles == 2 ? nq[t] : nq[t] >> 1;
+      if (!warp_wait(&bars.q_free[s], (use & 1) ^ 1, abort_flag)) return false;
+      if (!withhold) {
+        if (elect_one()) {
+          uint64_t* bar = &bars.q_full[t][nq[t] & 1];
+          mbar_arrive_expect_tx(bar, C::kTileBytes);
+          for (int pn = 0; pn < C::kPanels; ++pn)
+            tma_load_3d(smem + C::kOffQ + s * C::kTileBytes + pn * C::kPanelBytes, &a.tm_q, bar, pn * 64, x.row[t], x.head[t]);
+        }
+        __syncwarp();
+        ++nq[t];
+      }
+      withhold = false;
+      return true;
+    };
+    auto load = [&](const CUtensorMap* tm, uint8_t* dst, uint64_t* bar, int row, int head) {
+      if (elect_one()) {
+        mbar_arrive_expect_tx(bar, C::kTileBytes);
+        for (int pn = 0; pn < C::kPanels; ++pn) tma_load_3d(dst + pn * C::kPanelBytes, tm, bar, pn * 64, row, head);
+      }
+      __syncwarp();
+    };
+    for (int i = 0; ok; ++i) {
+      const Item x = item<C::kTiles>(a, i);
+      if (x.bhk < 0) break;
+      const int n = max(x.nb[0], x.nb[1]);
+      if (x.nb[0] > 0 && !(ok = load_q(x, 0))) break;
+      for (int j = 0; j < n; ++j, ++g) {
+        const int ks = g % C::kKStages, vs = g % C::kVStages, row = x.at(j) * 128;
+        if (!(ok = warp_wait(&bars.k_empty[ks], ((g / C::kKStages) & 1) ^ 1, abort_flag))) break;
+        load(&a.tm_k, smem + C::kOffK + ks * C::kTileBytes, &bars.k_full[ks], row, x.bhk);
+        nk = g + 1;
+        if (C::kTiles == 2 && j == 0 && x.nb[1] > 0 && !(ok = load_q(x, 1))) break;
+        if (!(ok = warp_wait(&bars.v_empty[vs], ((g / C::kVStages) & 1) ^ 1, abort_flag))) break;
+        load(&a.tm_v, smem + C::kOffV + vs * C::kTileBytes, &bars.v_full[vs], row, x.bhk);
+        nv = g + 1;
+      }
+    }
+    // Let every issued copy land before the CTA can exit (an earlier load's slot was refilled only after its reader
+    // completed, so it has landed).
+    for (int t = 0; t < C::kTiles; ++t)
+      for (int last = max(0, nq[t] - 2); last < nq[t]; ++last) mbar_wait_drain(&bars.q_full[t][last & 1], (last >> 1) & 1);
+    for (int s = max(0, nk - C::kKStages); s < nk; ++s)
+      mbar_wait_drain(&bars.k_full[s % C::kKStages], (s / C::kKStages) & 1);
+    for (int s = max(0, nv - C::kVStages); s < nv; ++s)
+      mbar_wait_drain(&bars.v_full[s % C::kVStages], (s / C::kVStages) & 1);
+  } else if (warp == C::kWarpMma) {
+    // ------------------------------------------------------------ MMA issuer
+    constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);  // Q, K both K-major
+    constexpr uint32_t kIdO = idesc_bf16(128, D, false, true);     // P from TMEM, V MN-major
+    const uint64_t dq0 = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
+    const uint64_t dk0 = sdesc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
+    const uint64_t dv0 = sdesc_sw128(smem_u32(smem + C::kOffV), C::kPanelBytes, 1024);
+    auto issue_s = [&](int t, int qs, int ks, bool last) {  // by the elected lane
+      const uint32_t qo = (uint32_t)(qs * C::kTileBytes) >> 4, ko = (uint32_t)(ks * C::kTileBytes) >> 4;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {  // each k-step reads 32 bytes of every row
+        const uint32_t o = ((kk >> 2) * C::kPanelBytes + (kk & 3) * 32) >> 4;
+        mma_ss(tmem + C::col_s(t), dq0 + qo + o, dk0 + ko + o, kIdS, kk > 0);
+      }
+      mma_commit(&bars.s_full[t]);
+      if (last) mma_commit(&bars.q_free[qs]);  // the tile's last product to read Q
+    };
+    auto issue_pv = [&](int t, int vs, bool first) {
+      const uint32_t vo = (uint32_t)(vs * C::kTileBytes) >> 4;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)  // P columns [8 kk, 8 kk + 8), V rows [16 kk, 16 kk + 16)
+        mma_ts(tmem + C::col_o(t), tmem + C::col_p(t) + kk * 8, dv0 + vo + kk * ((16 * 128) >> 4), kIdO,
+               (!first || kk > 0) ? 1u : 0u);
+    };
+    int g = 0, nq[2] = {0, 0}, np[2] = {0, 0};  // key blocks; items and P blocks of each tile so far
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      const Item x = item<C::kTiles>(a, i);
+      if (x.bhk < 0) break;
+      const int n = max(x.nb[0], x.nb[1]);
+      if (n == 0) continue;
+      // S of the first block
+      ok = warp_wait(&bars.k_full[g % C::kKStages], (g / C::kKStages) & 1, abort_flag);
+      if (C::kTiles == 1 && ok) ok = warp_wait(&bars.s_free, (g & 1) ^ 1, abort_flag);
+      for (int t = 0; t < C::kTiles && ok; ++t)
+        if (x.nb[t] > 0) {
+          if (!(ok = warp_wait(&bars.q_full[t][nq[t] & 1], (nq[t] >> 1) & 1, abort_flag))) break;
+          tc_fence_after();
+          if (x.uses(t, 0)) {
+            if (elect_one()) issue_s(t, C::kTiles == 2 ? t : nq[0] & 1, g % C::kKStages, x.nb[t] == 1);
+            __syncwarp();
+          }
+        }
+      if (!ok) break;
+      if (elect_one()) mma_commit(&bars.k_empty[g % C::kKStages]);
+      __syncwarp();
+      if constexpr (C::kTiles == 2) {
+        // Per key block j and tile t: O_t += P_t V_j, then at once S_t for block j + 1 (its columns are P_t's, which the
+        // products of one thread have read by then, as they execute in issue order).
+        bool begun[2] = {false, false};  // whether O_t holds anything of this item
+        for (int j = 0; j < n; ++j, ++g) {
+          const int s = g % C::kVStages;
+          const uint32_t ph = (g / C::kVStages) & 1;
+          const int v_last = x.uses(1, j) ? 1 : 0;  // the tile whose PV reads V_j last
+          const int jn = j + 1, sn = (g + 1) % C::kKStages;
+          const bool k_next = jn < n, u0 = x.uses(0, j);
+          ok = warp_wait3(&bars.v_full[s], ph, u0 ? &bars.p_full[0] : &bars.v_full[s], u0 ? (np[0] & 1) : ph,
+                          k_next ? &bars.k_full[sn] : &bars.v_full[s], k_next ? ((g + 1) / C::kKStages) & 1 : ph, abort_flag);
+          if (!ok) break;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (x.uses(t, j)) {
+              if (t == 1 && !(ok = warp_wait(&bars.p_full[1], np[1] & 1, abort_flag))) break;
+              // an item's first PV overwrites O: the tile before has been read out
+              if (!begun[t] && !(ok = warp_wait(&bars.o_free[t], (nq[t] & 1) ^ 1, abort_flag))) break;
+              tc_fence_after();
+              if (elect_one()) {
+                issue_pv(t, s, !begun[t]);
+                if (j == x.nb[t] - 1) mma_commit(&bars.o_done[t]);
+                if (t == v_last) mma_commit(&bars.v_empty[s]);
+              }
+              __syncwarp();
+              begun[t] = true;
+              ++np[t];
+            }
+            if (x.uses(t, jn)) {
+              if (elect_one()) issue_s(t, t, sn, jn == x.nb[t] - 1);
+              __syncwarp();
+            }
+          }
+          if (!ok) break;
+          if (k_next) {
+            if (elect_one()) mma_commit(&bars.k_empty[sn]);
+            __syncwarp();
+          }
+        }
+      } else {
+        // Per key block: S of the tile's next block as soon as the softmax has this one's in registers, then O += P V.
+        for (int j = 0; j < n; ++j, ++g) {
+          if (j + 1 < n) {
+            const int sn = (g + 1) % C::kKStages;
+            ok = warp_wait2(&bars.s_free, g & 1, &bars.k_full[sn], ((g + 1) / C::kKStages) & 1, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            if (elect_one()) {
+              issue_s(0, nq[0] & 1, sn, j + 2 == n);
+              mma_commit(&bars.k_empty[sn]);
+            }
+            __syncwarp();
+          }
+          const int s = g % C::kVStages;
+          ok = warp_wait2(&bars.p_full[0], g & 1, &bars.v_full[s], (g / C::kVStages) & 1, abort_flag);
+          if (ok && j == 0) ok = warp_wait(&bars.o_free[0], (nq[0] & 1) ^ 1, abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            issue_pv(0, s, j == 0);
+            mma_commit(&bars.o_done[0]);
+            mma_commit(&bars.v_empty[s]);
+          }
+          __syncwarp();
+        }
+      }
+      for (int t = 0; t < 2; ++t) nq[t] += x.nb[t] > 0;
+    }
+    if (elect_one()) mma_commit(&bars.teardown);
+    __syncwarp();
+    mbar_wait_drain(&bars.teardown, 0);
+  } else {
+    // ------------------------------------------------------------ softmax + epilogue
+    const int t = warp >> 2;
+    const int r = (warp & 3) * 32 + lane;  // row within the tile = TMEM lane
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lane_off + C::col_s(t);
+    const uint32_t t_p = tmem + lane_off + C::col_p(t);
+    const uint32_t t_o = tmem + lane_off + C::col_o(t);
+    const float sl2 = a.scale_log2;
+    const bool o32 = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
+    int np = 0, nq = 0;  // blocks and items of this tile so far
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      const Item x = item<C::kTiles>(a, i);
+      if (x.bhk < 0) break;
+      if (!x.there[t]) continue;
+      const int row0 = x.row[t], row = row0 + r, p = row + x.off, nb = x.nb[t];  // p: the row's position
+      const int p_last = row0 + 127 + x.off;
+      float m_ref = -INFINITY;  // exponent reference, log2 units of scaled scores
+      float l_sum = 0.f;        // sum of 2^(s * sl2 - m_ref) over the keys seen so far
+      bool begun = false;       // whether O holds anything
+      for (int j = 0; j < nb; ++j) {
+        if (!x.uses(t, j)) continue;
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars.s_full[t], np & 1, abort_flag));
+        if (!ok) break;
+        tc_fence_after();
+        // S_t, with the maximum of each 32 columns from the load itself
+        uint32_t sr[4][32];
+        float cmax[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32_max(t_s + c * 32, sr[c], cmax[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_wait(sr[c], cmax[c]);
+        if constexpr (C::kTiles == 1) {
+          tc_fence_before();
+          mbar_arrive(&bars.s_free);  // S is in registers: the next block's S may overwrite it
+        }
+        float mx = fmax3(fmax3(cmax[0], cmax[1], cmax[2]), cmax[3], -INFINITY);
+        // Masked: blocks that reach past the first row's position (keys past sk are past every row's) and those with keys
+        // behind the last row's window that are not all sinks.
+        const int kv0 = x.at(j) * 128;
+        if (kv0 + 127 > row0 + x.off || (p_last - kv0 >= a.window && kv0 + 128 > a.sinks)) {
+          // keep column c iff c <= lim and (c > out or c < sunk)
+          const int lim = p - kv0, out = lim - a.window, sunk = a.sinks - kv0;
+#pragma unroll
+          for (int c = 0; c < 128; ++c)
+            if (c > lim || (c <= out && c >= sunk)) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+          float mxc[8];  // row maximum over eight chains of 16 scores, then a tree
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            mxc[q] = fmaxf(__uint_as_float(sr[0][2 * q]), __uint_as_float(sr[0][2 * q + 1]));
+#pragma unroll
+          for (int c = 16; c < 128; c += 16)
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              mxc[q] = fmax3(mxc[q], __uint_as_float(sr[c >> 5][(c & 31) + 2 * q]),
+                             __uint_as_float(sr[c >> 5][(c & 31) + 2 * q + 1]));
+          mx = fmax3(fmax3(mxc[0], mxc[1], mxc[2]), fmax3(mxc[3], mxc[4], mxc[5]), fmaxf(mxc[6], mxc[7]));
+        }
+        float alpha = 1.f;
+        const float m_new = fmaxf(m_ref, mx * sl2);
+        const bool move = m_new > m_ref + kRescaleThreshold;
+        if (move) {
+          alpha = ex2(m_ref - m_new);
+          m_ref = m_new;
+        }
+        const bool rescale = __any_sync(0xffffffffu, move && begun);
+        float2 sum4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float m_use = m_ref == -INFINITY ? 0.f : m_ref;  // a row that has seen no key yet: P = 0
+        const float2 scale2 = make_float2(sl2, sl2), shift2 = make_float2(-m_use, -m_use);
+        auto chunk = [&](int ch) {  // P of 32 keys as bf16 pairs, packed in place (pair c / 2 into word c / 2, already read)
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const float2 y =
+                ffma2(make_float2(__uint_as_float(sr[ch][c]), __uint_as_float(sr[ch][c + 1])), scale2, shift2);
+            const float2 e = make_float2(ex2(y.x), ex2(y.y));
+            sum4[(c >> 1) & 3] = fadd2(sum4[(c >> 1) & 3], e);
+            sr[ch][c >> 1] = pack_bf16x2(e.x, e.y);
+          }
+        };
+        auto store = [&](int ch) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int q = 0; q < 16; ++q) pk[q] = sr[ch][q];
+          tmem_st16(t_p + 16 * ch, pk);
+        };
+        chunk(0);
+        if constexpr (C::kTiles == 2) {
+          store(0);
+          chunk(1);
+        } else {
+          // P and O are free once the P V before this one has completed (an item's first block: the epilogue waited)
+          chunk(1);
+          if (begun) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars.o_done[0], (np - 1) & 1, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+          }
+          store(0);
+        }
+        store(1);
+        chunk(2);
+        store(2);
+        chunk(3);
+        store(3);
+        const float2 sum = fadd2(fadd2(sum4[0], sum4[1]), fadd2(sum4[2], sum4[3]));
+        l_sum = l_sum * alpha + (sum.x + sum.y);
+        if (rescale) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(t_o + c, o);
+            tmem_ld_wait(o);
+#pragma unroll
+            for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
+            tmem_st32(t_o + c, o);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&bars.p_full[t]);
+        begun = true;
+        ++np;
+      }
+      if (ok && nb > 0) ok = mbar_wait(&bars.o_done[t], (C::kTiles == 2 ? nq : np - 1) & 1, abort_flag);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const bool valid = row < a.Nq, real = row < x.sq;  // a padding row: o = 0
+      const long long at = (long long)x.head[t] * a.Nq + row;
+      uint8_t* orow = static_cast<uint8_t*>(a.o) + at * (D * 2);
+      const float inv = real ? 1.f / l_sum : 0.f;
+      if (nb > 0) {
+        tc_fence_after();
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          uint32_t o[32];
+          tmem_ld32(t_o + c, o);
+          tmem_ld_wait(o);
+          if (c + 32 == D) {
+            tc_fence_before();
+            mbar_arrive(&bars.o_free[t]);  // O is in registers: the next item may accumulate there
+          }
+          if (valid)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t w[8];
+#pragma unroll
+              for (int q = 0; q < 8; ++q)
+                w[q] = real ? pack_bf16x2(__uint_as_float(o[16 * h + 2 * q]) * inv, __uint_as_float(o[16 * h + 2 * q + 1]) * inv)
+                            : 0u;
+              st_global_32(orow + c * 2 + h * 32, w, o32);
+            }
+        }
+        ++nq;
+      } else if (valid) {
+        const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+        for (int c = 0; c < D; c += 16) st_global_32(orow + c * 2, zero, o32);
+      }
+      if (valid) a.lse[at] = real ? (m_ref + log2f(l_sum)) * kLn2 : -INFINITY;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::kWarpMma) tmem_dealloc(tmem, C::kTmemCols);
+  if (threadIdx.x == 0 && bars.abort) atomicOr(a.status, 1u);
+}
+
+template <int D>
+cudaError_t launch(WindowArgs a, int num_sms, cudaStream_t stream) {
+  using C = WCfg<D>;
+  const int tiles = a.group * ((a.Nq + 127) / 128);
+  a.items_per_head = (tiles + C::kTiles - 1) / C::kTiles;
+  a.items = (long long)a.B * a.Hkv * a.items_per_head;
+  static std::atomic<unsigned long long> done;  // devices (a bit each) that know the kernel's shared memory
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(fa_fwd_window_kernel<D>), C::kSmemBytes, done);
+  if (e != cudaSuccess) return e;
+  const unsigned ctas = (unsigned)std::min<long long>(a.items, (long long)num_sms * C::kCtasPerSm);
+  return launch_dependent(fa_fwd_window_kernel<D>, dim3(ctas), C::kThreads, C::kSmemBytes, stream, a);
+}
+
+}  // namespace
+
+cudaError_t launch_fwd_window(const WindowArgs& a, int num_sms, cudaStream_t stream) {
+  return a.d == 64 ? launch<64>(a, num_sms, stream) : launch<128>(a, num_sms, stream);
+}
+
+}  // namespace fa

@@ -62,8 +62,26 @@ struct BwdArgs {
   unsigned int drop_offset;
   unsigned int drop_rk[20];
   float drop_scale;       // 256 / (256 - drop_p256)
+  // attention with a window (window 0: none; causal): row i of sequence b sees key j iff j <= p and (p - j < window or
+  // j < sinks), p its position; 'group' query heads share a key head (BH and H count query heads)
+  int window, sinks, group;
   int head_group;     // heads per CTA scheduling group of the dK/dV kernel (set by launch_bwd)
   int head_group_dq;  // the same for the dQ kernel
+};
+
+// The forward with a window (fa_fwd_window.cu): q, o, lse over B * Hkv * group heads of Nq rows, k and v over B * Hkv of Nk.
+struct WindowArgs {
+  CUtensorMap tm_q, tm_k, tm_v;  // bf16, box 64 x 128 x 1, 128B swizzle
+  void* o;
+  float* lse;
+  unsigned int* status;
+  int B, Hkv, group, Nq, Nk, d;
+  float scale_log2;
+  int window, sinks;             // at most Nk
+  const int *seqlens_q, *seqlens_k;
+  int test_fault;                // as in FwdArgs
+  int items_per_head;            // set by launch_fwd_window, and their number
+  long long items;
 };
 
 // Status bit a kernel sets when a per-sequence length lies outside [1, N]
@@ -121,6 +139,8 @@ cudaError_t launch_bwd(const BwdArgs& a, int num_sms, cudaStream_t stream);
 // arguments (d = 64, 16-bit, no padding masks, key ranges or dropout), and its launch.
 bool fwd_persist_applies(const FwdArgs& a);
 cudaError_t launch_fwd_persist(const FwdArgs& a, int num_sms, cudaStream_t stream);
+
+cudaError_t launch_fwd_window(const WindowArgs& a, int num_sms, cudaStream_t stream);
 
 // SM count and error word of the current device (FA_OK), or an fa_status error code.
 int device_facts(int* num_sms, unsigned int** status);

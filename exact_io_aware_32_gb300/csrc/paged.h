@@ -42,6 +42,7 @@ struct PagedArgs {
   float scale_log2;  // scale * log2(e), times the key factor
   float o_scale;     // the value factor
   int max_keys;      // max_pages pages of keys
+  int window, sinks; // causal calls with a window: a token sees its last 'window' keys and the first 'sinks' (window 0: all)
   // set by launch_paged
   CUtensorMap tm_q;         // bf16 [T][Hq][d], box 64 x (Hq / Hkv) x tokens of a 128-row (32-row) tile, 128B swizzle
   // A page's rows of one head, up to 128 of them, per copy. bf16: seen as [page, head][row / 8][panel][row % 8][64
@@ -98,8 +99,9 @@ cudaError_t launch_dependent(void (*kernel)(Args, More...), dim3 grid, int threa
 cudaError_t launch_plan(const PlanArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_store(const StoreArgs& a, int num_sms, cudaStream_t stream);
 // The kernels of a call (1 or 2) in p[]; each may use the whole workspace, one after the other.
-int plan_paged(int T, int R, int Hq, int Hkv, int d, int fp8, int max_new, int max_keys, int num_sms,
-               PagedPlan (&p)[2]);
+// (window 0: none).
+int plan_paged(int T, int R, int Hq, int Hkv, int d, int fp8, int max_new, int max_keys, int window, int sinks,
+               int num_sms, PagedPlan (&p)[2]);
 // Encodes the tensor maps, gives the kernel its parts of the workspace and launches it with its join;
 // cudaErrorInvalidValue if the encoding fails.
 cudaError_t launch_paged(PagedArgs a, const PagedPlan& p, void* workspace, cudaStream_t stream);

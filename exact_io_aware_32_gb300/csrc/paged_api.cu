@@ -143,17 +143,21 @@ size_t fa_fwd_paged_workspace_bytes(int T, int R, int Hq, int Hkv, int d, int ma
   size_t most = 0;
   for (int fp8 = 0; fp8 < 2; ++fp8) {  // one size for both kinds of cache
     fa::PagedPlan p[2];
-    const int n = fa::plan_paged(T, R, Hq, Hkv, d, fp8, max_new, INT32_MAX, kMaxSms, p);  // (any table width)
+    const int n = fa::plan_paged(T, R, Hq, Hkv, d, fp8, max_new, INT32_MAX, 0, 0, kMaxSms, p);  // (any table width)
     for (int i = 0; i < n; ++i) most = std::max(most, p[i].bytes());
   }
   return most;
 }
 
-int fa_fwd_paged(const void* q, long long q_stride, const void* k_cache, const void* v_cache, int fp8,
-                 float descale_k, float descale_v, const int* block_table, int max_pages, const int* query_start,
-                 const int* seq_lens, void* o, float* lse, int T, int R, int Hq, int Hkv, int d, int num_pages,
-                 int page_size, int max_new, float scale, int causal, void* workspace, size_t workspace_bytes,
-                 void* stream) {
+}  // extern "C"
+
+namespace {
+
+// Both forms of the attention; window 0: none.
+int fwd_paged(const void* q, long long q_stride, const void* k_cache, const void* v_cache, int fp8, float descale_k,
+              float descale_v, const int* block_table, int max_pages, const int* query_start, const int* seq_lens, void* o,
+              float* lse, int T, int R, int Hq, int Hkv, int d, int num_pages, int page_size, int max_new, float scale,
+              int causal, int window, int sinks, void* workspace, size_t workspace_bytes, void* stream) {
   if (!q || !k_cache || !v_cache || !block_table || !query_start || !seq_lens || !o || !lse) return FA_ERR_INVALID_ARG;
   int st = check_paged(T, R, Hq, Hkv, d, max_new);
   if (st == FA_OK) st = check_cache(num_pages, page_size, Hkv, d);
@@ -172,7 +176,10 @@ int fa_fwd_paged(const void* q, long long q_stride, const void* k_cache, const v
   // places in the row of tiles are 32-bit numbers of key blocks (paged_work.cuh)
   const int max_keys = max_pages * page_size;
   fa::PagedPlan p[2];
-  int n = fa::plan_paged(T, R, Hq, Hkv, d, fp8 ? 1 : 0, max_new, max_keys, kMaxSms, p);
+  // (a window or sinks past every key there can be are the widest that make a difference)
+  window = std::min(window, max_keys);
+  sinks = std::min(sinks, max_keys);
+  int n = fa::plan_paged(T, R, Hq, Hkv, d, fp8 ? 1 : 0, max_new, max_keys, window, sinks, kMaxSms, p);
   for (int i = 0; i < n; ++i)
     if (fa::most_blocks(T, R, Hkv, p[i].tpt, max_keys) >= (double)INT32_MAX) return FA_ERR_INVALID_ARG;
   fa::PagedArgs a;
@@ -201,13 +208,40 @@ int fa_fwd_paged(const void* q, long long q_stride, const void* k_cache, const v
   a.scale_log2 = scale_log2;
   a.o_scale = fp8 ? descale_v : 1.0f;
   a.max_keys = max_keys;
+  a.window = window;
+  a.sinks = sinks;
   a.test_fault = fa::take_test_fault();
-  n = fa::plan_paged(T, R, Hq, Hkv, d, a.fp8, max_new, a.max_keys, std::min(sms, kMaxSms), p);
+  n = fa::plan_paged(T, R, Hq, Hkv, d, a.fp8, max_new, a.max_keys, window, sinks, std::min(sms, kMaxSms), p);
   for (int i = 0; i < n; ++i) {
     a.most = (int)fa::most_blocks(T, R, Hkv, p[i].tpt, max_keys);
     if (fa::launch_paged(a, p[i], workspace, static_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_LAUNCH;
   }
   return FA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fa_fwd_paged(const void* q, long long q_stride, const void* k_cache, const void* v_cache, int fp8,
+                 float descale_k, float descale_v, const int* block_table, int max_pages, const int* query_start,
+                 const int* seq_lens, void* o, float* lse, int T, int R, int Hq, int Hkv, int d, int num_pages,
+                 int page_size, int max_new, float scale, int causal, void* workspace, size_t workspace_bytes,
+                 void* stream) {
+  return fwd_paged(q, q_stride, k_cache, v_cache, fp8, descale_k, descale_v, block_table, max_pages, query_start, seq_lens, o,
+                   lse, T, R, Hq, Hkv, d, num_pages, page_size, max_new, scale, causal, 0, 0, workspace, workspace_bytes,
+                   stream);
+}
+
+int fa_fwd_paged_window(const void* q, long long q_stride, const void* k_cache, const void* v_cache, int fp8,
+                        float descale_k, float descale_v, const int* block_table, int max_pages, const int* query_start,
+                        const int* seq_lens, void* o, float* lse, int T, int R, int Hq, int Hkv, int d, int num_pages,
+                        int page_size, int max_new, float scale, int window, int sinks, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  if (window < 1 || sinks < 0) return FA_ERR_INVALID_ARG;
+  return fwd_paged(q, q_stride, k_cache, v_cache, fp8, descale_k, descale_v, block_table, max_pages, query_start, seq_lens, o,
+                   lse, T, R, Hq, Hkv, d, num_pages, page_size, max_new, scale, 1, window, sinks, workspace, workspace_bytes,
+                   stream);
 }
 
 }  // extern "C"

@@ -78,17 +78,20 @@ struct CBars {
 static_assert(sizeof(CBars) <= 1024, "barriers exceed their shared memory");
 
 // Key blocks that each 128-row half sees of a piece (nb[t] from p.jb on).
-template <int kTiles>
+template <int kTiles, bool WIN>
 __device__ __forceinline__ void half_blocks(const PagedArgs& a, const Piece& p, int (&nb)[2]) {
+  const int skip = WIN ? band_of(a, p.q, p.tok).skip : 0;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int tok = p.tok + t * a.tpt1;
-    const int blocks = t < kTiles && tok < p.q.n ? (keys_seen(a, p.q, tok + a.tpt1) + 127) >> 7 : 0;
+    const int blocks = t < kTiles && tok < p.q.n ? ((keys_seen(a, p.q, tok + a.tpt1) + 127) >> 7) - skip : 0;
     nb[t] = max(0, min(blocks, p.je) - p.jb);
   }
 }
 
-template <int D, bool FP8, bool CAUSAL>
+// WIN (with CAUSAL): a token sees its last a.window keys and the first a.sinks; j counts the blocks of a tile's Band, which
+// both halves stream (the second's window begins a block later at most once in 128 / tpt1 tiles).
+template <int D, bool FP8, bool CAUSAL, bool WIN = false>
 __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPerSm)
     fa_paged_chunk_kernel(const __grid_constant__ PagedArgs a) {
   using C = CCfg<D, FP8>;
@@ -134,7 +137,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     tmem_relinquish();
   }
   tc_fence_before();
-  find_range<C::kThreads>(a, bars.range, reinterpret_cast<int(&)[C::kThreads / 32]>(bars.sums));
+  find_range<C::kThreads, WIN>(a, bars.range, reinterpret_cast<int(&)[C::kThreads / 32]>(bars.sums));
   tc_fence_after();
   const uint32_t tmem = bars.tmem_base;
   if (!bars.range.some) {  // uniform: nothing has been issued
@@ -146,7 +149,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
   Piece p = bars.range.first;
   const bool first = bars.range.use;  // the first piece is there already
   int blocks[2];                      // key blocks that each half sees of it
-  half_blocks<C::kTiles>(a, p, blocks);
+  half_blocks<C::kTiles, WIN>(a, p, blocks);
   auto next_piece = [&] {
     const bool there = in.next(p);
     blocks[0] = in.x;
@@ -181,14 +184,14 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
       }
       withhold = false;
     };
-    Walk walk;
+    Walk<WIN> walk;
     walk.begin(bars.range);
     Piece next = p;
     int next_nb[2] = {blocks[0], blocks[1]}, told = 0;
     bool more = true;
     auto step = [&] {  // works out the next piece and tells the others
       more = walk.step(a, next);
-      half_blocks<C::kTiles>(a, next, next_nb);
+      half_blocks<C::kTiles, WIN>(a, next, next_nb);
       ok = bars.ring.tell(told++, next, more, next_nb[0], next_nb[1], lane, abort_flag);
     };
     if (!first) step();
@@ -199,14 +202,19 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
       note_piece(a, parts, p, walk, bars.range.per);
       const int nbm = max(blocks[0], blocks[1]);
       Pages pages;
-      if (nbm > 0) pages.begin(a, p, lane);
+      Band band{};
+      if (WIN) band = band_of(a, p.q, p.tok);
+      if (nbm > 0) pages.begin(a, p, band.at(p.jb), lane);
       if (blocks[0] > 0) load_q(0);
       for (int j = 0; ok && j < max(nbm, 1); ++j) {
         if (nbm > 0) {
-          const int jj = p.jb + j, page_now = pages.of(a, p, jj, lane);
+          const int jj = band.at(p.jb + j);
+          if (WIN && j > 0 && p.jb + j == band.sunk) pages.begin(a, p, jj, lane);
+          const int page_now = pages.of(a, p, jj, lane);
           const int sk = g % C::kKStages;
           if (!(ok = warp_wait(&bars.k_empty[sk], ((g / C::kKStages) & 1) ^ 1, abort_flag))) break;
-          load_block<D, FP8>(a, p, jj, page_now, lane, &a.tm_k, smem + C::kOffK + sk * C::kKBytes, &bars.k_full[sk]);
+          load_block<D, FP8, WIN>(a, p, jj, page_now, lane, &a.tm_k, smem + C::kOffK + sk * C::kKBytes, &bars.k_full[sk],
+                                  band.low);
           nk = g + 1;
           if (C::kTiles == 2 && j == 0 && blocks[1] > 0) {
             load_q(1);
@@ -214,8 +222,9 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
           }
           const int sv = g % kS;
           if (!(ok = warp_wait(&v_empty[sv], ((g / kS) & 1) ^ 1, abort_flag))) break;
-          load_block<D, FP8>(a, p, jj, page_now, lane, &a.tm_v,
-                             smem + (FP8 ? C::kOffC + sv * C::kCodeBytes : C::kOffV + sv * C::kTileBytes), &v_full[sv]);
+          load_block<D, FP8, WIN>(a, p, jj, page_now, lane, &a.tm_v,
+                                  smem + (FP8 ? C::kOffC + sv * C::kCodeBytes : C::kOffV + sv * C::kTileBytes), &v_full[sv],
+                                  band.low);
           nv = ++g;
         }
         if (j == 0) step();  // while those are on their way
@@ -252,6 +261,8 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     bool ok = true;
     for (bool more = first || next_piece(); ok && more; more = next_piece()) {
       const int nbm = max(blocks[0], blocks[1]);
+      Band band{};
+      if (WIN) band = band_of(a, p.q, p.tok);
       if (nbm > 0) {
         // S of the first block
         ok = warp_wait(&bars.k_full[g % C::kKStages], (g / C::kKStages) & 1, abort_flag);
@@ -280,7 +291,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
                           j < blocks[0] ? (np[0] & 1) : ph, k_next ? &bars.k_full[sn] : &bars.v_full[s],
                           k_next ? ((g + 1) / C::kKStages) & 1 : ph, abort_flag);
           if (!ok) break;
-          const int keys = p.q.len - (p.jb + j) * 128, steps = pv_steps(keys);
+          const int keys = p.q.len - band.at(p.jb + j) * 128, steps = pv_steps(keys);
           if (!FP8 && keys < steps * 16) zero_rows<D>(smem + C::kOffV + s * C::kTileBytes, keys, steps * 16, lane);
           for (int t = 0; t < 2; ++t) {
             if (j < blocks[t]) {
@@ -325,7 +336,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
           ok = warp_wait2(&bars.p_full[0], g & 1, &bars.v_full[s], (g / C::kVStages) & 1, abort_flag);
           if (ok && j == 0) ok = warp_wait(&bars.o_free[0], (nq[0] & 1) ^ 1, abort_flag);
           if (!ok) break;
-          const int keys = p.q.len - (p.jb + j) * 128, steps = pv_steps(keys);
+          const int keys = p.q.len - band.at(p.jb + j) * 128, steps = pv_steps(keys);
           if (keys < steps * 16) zero_rows<D>(smem + C::kOffV + s * C::kTileBytes, keys, steps * 16, lane);
           tc_fence_after();
           if (elect_one()) {
@@ -349,12 +360,14 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     bool ok = true;
     for (bool more = first || next_piece(); ok && more; more = next_piece()) {
       const int nbm = max(blocks[0], blocks[1]);
+      Band band{};
+      if (WIN) band = band_of(a, p.q, p.tok);
       for (int j = 0; ok && j < nbm; ++j, ++g) {
         const int vs = g % C::kVStages, cs = g % kCS;
         ok = warp_wait2(&bars.c_full[cs], (g / kCS) & 1, &bars.v_empty[vs], ((g / C::kVStages) & 1) ^ 1, abort_flag);
         if (!ok) break;
         convert_tile<D, 32 * C::kConvWarps>(smem + C::kOffC + cs * C::kCodeBytes, smem + C::kOffV + vs * C::kTileBytes,
-                                            p.q.len - (p.jb + j) * 128, tid);
+                                            p.q.len - band.at(p.jb + j) * 128, tid);
         conv_arrive(&bars.v_full[vs], &bars.c_empty[cs], lane);
       }
     }
@@ -376,6 +389,12 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
       const int tok0 = p.tok + t * a.tpt1, tok = tok0 + rt;
       const int off = p.q.len - p.q.n;  // causal: token i sees keys 0 .. i + off
       const bool valid = rt < a.tpt1 && tok < p.q.n;
+      Band band{};
+      int out_last = 0;  // window: the last key that is behind the window of this half's last token
+      if (WIN) {
+        band = band_of(a, p.q, p.tok);
+        out_last = min(tok0 + a.tpt1, p.q.n) - 1 + off - band.wide;
+      }
       float sl2 = a.scale_log2;
       if (FP8 && nb > 0) {  // this thread's row of Q to its two 8-bit parts
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars.q_raw[t], nq & 1, abort_flag)))) break;
@@ -401,12 +420,13 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
         }
         float mx = fmax3(fmax3(cmax[0], cmax[1], cmax[2]), cmax[3], -INFINITY);
         // only blocks that reach past the first row's last key, or past the request's, need masking
-        const int kv0 = (p.jb + j) * 128;
-        if ((CAUSAL && kv0 + 127 > tok0 + off) || kv0 + 128 > p.q.len) {
+        const int kv0 = band.at(p.jb + j) * 128;
+        if ((CAUSAL && kv0 + 127 > tok0 + off) || kv0 + 128 > p.q.len || (WIN && kv0 <= out_last && kv0 + 128 > a.sinks)) {
           const int lim = (CAUSAL ? min(tok + off, p.q.len - 1) : p.q.len - 1) - kv0;  // keep column c iff c <= lim
+          const int out = lim - band.wide, sunk = a.sinks - kv0;  // window: hidden too are columns up to 'out', from 'sunk' on
 #pragma unroll
           for (int c = 0; c < 128; ++c)
-            if (c > lim) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+            if (c > lim || (WIN && c <= out && c >= sunk)) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
           float mxc[8];  // row maximum over eight chains of 16 scores, then a tree
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -558,9 +578,11 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
 template <int D, bool FP8>
 cudaError_t launch(const PagedArgs& a, int ctas, cudaStream_t stream) {
   using C = CCfg<D, FP8>;
-  auto kern = a.causal ? fa_paged_chunk_kernel<D, FP8, true> : fa_paged_chunk_kernel<D, FP8, false>;
-  static std::atomic<unsigned long long> done[2];  // devices (a bit each) that know the kernel's shared memory
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes, done[a.causal]);
+  auto kern = a.window   ? fa_paged_chunk_kernel<D, FP8, true, true>
+              : a.causal ? fa_paged_chunk_kernel<D, FP8, true>
+                         : fa_paged_chunk_kernel<D, FP8, false>;
+  static std::atomic<unsigned long long> done[3];  // devices (a bit each) that know the kernel's shared memory
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes, done[a.window ? 2 : a.causal]);
   if (e != cudaSuccess) return e;
   return launch_dependent(kern, dim3((unsigned)ctas), C::kThreads, C::kSmemBytes, stream, a);
 }

@@ -74,7 +74,8 @@ struct FBars {
 };
 static_assert(sizeof(FBars) <= 672, "barriers exceed their shared memory");
 
-template <int D, bool FP8, bool CAUSAL>
+// WIN (with CAUSAL): a token sees its last a.window keys and the first a.sinks; j counts the blocks of a tile's Band.
+template <int D, bool FP8, bool CAUSAL, bool WIN = false>
 __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel(const __grid_constant__ PagedArgs a) {
   using C = FCfg<D, FP8>;
   extern __shared__ uint8_t smem_raw[];
@@ -131,7 +132,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     tmem_relinquish();
   }
   tc_fence_before();
-  find_range<C::kThreads>(a, range, sums);
+  find_range<C::kThreads, WIN>(a, range, sums);
   tc_fence_after();
   const uint32_t tmem = bars.tmem_base;
   if (!range.some) {  // uniform: nothing has been issued
@@ -142,7 +143,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
   PieceReader in(bars.ring, abort_flag, lane);
   Piece p = range.first;
   const bool first = range.use;  // the first piece is there already
-  Walk walk;
+  Walk<WIN> walk;
   if (warp == C::kWarpTmaK) walk.begin(range);
   const int per = range.per;
   __syncthreads();  // all have read the range: the join may write there
@@ -159,13 +160,18 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
       note_piece(a, parts, p, walk, per);
       const int nb = p.je - p.jb;
       Pages pages;
-      if (nb > 0) pages.begin(a, p, lane);
+      Band band{};
+      if (WIN) band = band_of(a, p.q, p.tok);
+      if (nb > 0) pages.begin(a, p, band.at(p.jb), lane);
       for (int j = 0; j < max(nb, 1); ++j) {
         if (nb > 0) {
-          const int jj = p.jb + j, page_now = pages.of(a, p, jj, lane);
+          const int jj = band.at(p.jb + j);
+          if (WIN && j > 0 && p.jb + j == band.sunk) pages.begin(a, p, jj, lane);
+          const int page_now = pages.of(a, p, jj, lane);
           const int s = g % C::kKStages;
           if (!(ok = warp_wait(&bars.k_empty[s], ((g / C::kKStages) & 1) ^ 1, abort_flag))) break;
-          load_block<D, FP8>(a, p, jj, page_now, lane, &a.tm_k, smem + C::kOffK + s * C::kKBytes, &bars.k_full[s]);
+          load_block<D, FP8, WIN>(a, p, jj, page_now, lane, &a.tm_k, smem + C::kOffK + s * C::kKBytes, &bars.k_full[s],
+                                  band.low);
           nk = ++g;
         }
         if (j == 0) {  // before this piece's other blocks: the Q K^T warp looks one piece ahead
@@ -188,12 +194,17 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     for (bool more = first || in.next(p); ok && more; more = in.next(p)) {
       if (p.jb == p.je) continue;
       Pages pages;
-      pages.begin(a, p, lane);
-      for (int jj = p.jb; jj < p.je; ++jj, ++g) {
+      Band band{};
+      if (WIN) band = band_of(a, p.q, p.tok);
+      pages.begin(a, p, band.at(p.jb), lane);
+      for (int j = p.jb; j < p.je; ++j, ++g) {
+        const int jj = band.at(j);
+        if (WIN && j > p.jb && j == band.sunk) pages.begin(a, p, jj, lane);
         const int page_now = pages.of(a, p, jj, lane), s = g % kS;
         if (!(ok = warp_wait(&empty[s], ((g / kS) & 1) ^ 1, abort_flag))) break;
-        load_block<D, FP8>(a, p, jj, page_now, lane, &a.tm_v,
-                           smem + (FP8 ? C::kOffC + s * C::kCodeBytes : C::kOffV + s * C::kTileBytes), &full[s]);
+        load_block<D, FP8, WIN>(a, p, jj, page_now, lane, &a.tm_v,
+                                smem + (FP8 ? C::kOffC + s * C::kCodeBytes : C::kOffV + s * C::kTileBytes), &full[s],
+                                band.low);
         nv = g + 1;
       }
     }
@@ -265,12 +276,14 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     bool ok = true;
     for (bool more = first || in.next(p); ok && more; more = in.next(p)) {
       if (p.jb == p.je) continue;
+      Band band{};
+      if (WIN) band = band_of(a, p.q, p.tok);
       for (int jj = p.jb; jj < p.je; ++jj, ++g) {
         const int s = g % C::kVStages, b = g & 1;
         if (!(ok = warp_wait2(&bars.v_full[s], (g / C::kVStages) & 1, &bars.p_full[b], (g >> 1) & 1, abort_flag))) break;
         // a tile's first P V overwrites O: the tile before has been read out
         if (jj == p.jb && !(ok = warp_wait(&bars.o_free, (n & 1) ^ 1, abort_flag))) break;
-        const int keys = p.q.len - jj * 128, steps = pv_steps(keys);
+        const int keys = p.q.len - band.at(jj) * 128, steps = pv_steps(keys);
         if (!FP8 && keys < steps * 16) zero_rows<D>(smem + C::kOffV + s * C::kTileBytes, keys, steps * 16, lane);
         tc_fence_after();
         if (elect_one()) {
@@ -299,12 +312,14 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
         conv_arrive(&bars.q_full[n % 3], nullptr, lane);
         ++n;
       }
+      Band band{};
+      if (WIN) band = band_of(a, p.q, p.tok);
       for (int j = p.jb; j < p.je; ++j, ++g) {
         const int vs = g % C::kVStages, cs = g % kCS;
         ok = warp_wait2(&bars.c_full[cs], (g / kCS) & 1, &bars.v_empty[vs], ((g / C::kVStages) & 1) ^ 1, abort_flag);
         if (!ok) break;
         convert_tile<D, 32 * C::kConvWarps>(smem + C::kOffC + cs * C::kCodeBytes, smem + C::kOffV + vs * C::kTileBytes,
-                                            p.q.len - j * 128, tid);
+                                            p.q.len - band.at(j) * 128, tid);
         conv_arrive(&bars.v_full[vs], &bars.c_empty[cs], lane);
       }
     }
@@ -338,6 +353,12 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
       const int lim_row = (CAUSAL ? min(p.tok + rt + off, p.q.len - 1) : p.q.len - 1) - warp * 32;
       const int lim_first = (CAUSAL ? min(p.tok + off, p.q.len - 1) : p.q.len - 1) - warp * 32;
       const int rows = min(a.tpt, p.q.n - p.tok) * G;
+      Band band{};
+      int out_last = 0;  // window: the last key, of this warp's, that is behind the last token's
+      if (WIN) {
+        band = band_of(a, p.q, p.tok);
+        out_last = min(p.tok + a.tpt, p.q.n) - 1 + off - band.wide - warp * 32;
+      }
       float m_ref = -INFINITY;  // exponent reference, log2 units of scaled scores
       float l_sum = 0.f;        // sum of 2^(s * sl2 - m_ref) over this warp's keys so far
       for (int j = 0; ok && j < nb; ++j, ++g) {
@@ -352,13 +373,14 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
         tmem_ld_wait(sr, mx);
         tc_fence_before();
         mbar_arrive(&bars.s_free[b]);  // S is in registers: the block after the next may overwrite it
-        const int kv0 = (p.jb + j) * 128;
-        if (kv0 + 31 > lim_first) {  // some row does not see all of these keys
+        const int kv0 = band.at(p.jb + j) * 128;
+        if (kv0 + 31 > lim_first || (WIN && kv0 <= out_last)) {  // some row does not see all of these keys
           const int lim = lim_row - kv0;
+          const int out = lim - band.wide, sunk = a.sinks - warp * 32 - kv0;  // hidden too: keys up to 'out', from 'sunk' on
           mx = -INFINITY;
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
-            if (c > lim) sr[c] = __float_as_uint(-INFINITY);
+            if (c > lim || (WIN && c <= out && c >= sunk)) sr[c] = __float_as_uint(-INFINITY);
             mx = fmaxf(mx, __uint_as_float(sr[c]));
           }
         }
@@ -487,9 +509,11 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
 template <int D, bool FP8>
 cudaError_t launch(const PagedArgs& a, int ctas, cudaStream_t stream) {
   using C = FCfg<D, FP8>;
-  auto kern = a.causal ? fa_paged_few_kernel<D, FP8, true> : fa_paged_few_kernel<D, FP8, false>;
-  static std::atomic<unsigned long long> done[2];  // devices (a bit each) that know the kernel's shared memory
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes, done[a.causal]);
+  auto kern = a.window   ? fa_paged_few_kernel<D, FP8, true, true>
+              : a.causal ? fa_paged_few_kernel<D, FP8, true>
+                         : fa_paged_few_kernel<D, FP8, false>;
+  static std::atomic<unsigned long long> done[3];  // devices (a bit each) that know the kernel's shared memory
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), C::kSmemBytes, done[a.window ? 2 : a.causal]);
   if (e != cudaSuccess) return e;
   return launch_dependent(kern, dim3((unsigned)ctas), C::kThreads, C::kSmemBytes, stream, a);
 }

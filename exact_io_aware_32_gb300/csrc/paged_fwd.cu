@@ -188,7 +188,7 @@ namespace {
 // 87.4 and 84.7 us (E4M3 93.9 and 93.5 us); at 16 blocks 4 requests of up to 1500 keys 12.0 and 13.5 us.
 constexpr int kWholeBlocks = 8;
 
-PagedPlan plan_kernel(bool few, int G, int d, int fp8, int max_new, int max_keys, int num_sms) {
+PagedPlan plan_kernel(bool few, int G, int d, int fp8, int max_new, int max_keys, int window, int sinks, int num_sms) {
   PagedPlan p;
   p.few = few;
   const int halves = few || (d == 64 && !fp8) ? 1 : 2;
@@ -198,7 +198,9 @@ PagedPlan plan_kernel(bool few, int G, int d, int fp8, int max_new, int max_keys
   // Cutting a tile of the chunk kernel costs two more epilogues and a join: short tiles stay whole and parts have at least
   // four blocks (eight prompts of up to 1024 tokens, 12 heads of 64, when it was chosen: 44 us with every cut, 35 us). The
   // decoding kernel's parts are a few rows: there only a call without any cut is worth it.
-  const int blocks = (max_keys >> 7) + (max_keys % 128 != 0);  // of the longest request there can be
+  int blocks = (max_keys >> 7) + (max_keys % 128 != 0);  // of the longest request there can be
+  if (window)  // a tile's sinks, and the window of all its tokens, which may begin anywhere in a block
+    blocks = (int)std::min<long long>(blocks, (sinks + 127ll) / 128 + (window + p.tpt + 126ll) / 128 + 1);
   p.whole = few && blocks > kWholeBlocks ? 0 : kWholeBlocks;
   p.join = blocks > p.whole;
   p.snap = few ? 0 : 4;
@@ -212,15 +214,18 @@ PagedPlan plan_kernel(bool few, int G, int d, int fp8, int max_new, int max_keys
 }
 }  // namespace
 
-int plan_paged(int T, int R, int Hq, int Hkv, int d, int fp8, int max_new, int max_keys, int num_sms,
+int plan_paged(int T, int R, int Hq, int Hkv, int d, int fp8, int max_new, int max_keys, int window, int sinks, int num_sms,
                PagedPlan (&p)[2]) {
   const int G = Hq / Hkv;
+  auto plan_kernel = [&](bool few, int new_tokens) {
+    return fa::plan_kernel(few, G, d, fp8, new_tokens, max_keys, window, sinks, num_sms);
+  };
   // no request has more than 32 rows per key head: the decoding kernel alone
   if ((long long)G * max_new <= 32) {
-    p[0] = plan_kernel(true, G, d, fp8, max_new, max_keys, num_sms);
+    p[0] = plan_kernel(true, max_new);
     return 1;
   }
-  p[0] = plan_kernel(false, G, d, fp8, max_new, max_keys, num_sms);
+  p[0] = plan_kernel(false, max_new);
   // Requests of mostly far fewer tokens than the largest: decoding requests beside chunks of prompts. A tile of 128 rows
   // for a few takes the chunk kernel 3000 cycles per key block and the decoding kernel a third of that, but a second
   // kernel with its join costs 20 us, so each takes its requests only where there may be many keys. Measured with one
@@ -229,12 +234,13 @@ int plan_paged(int T, int R, int Hq, int Hkv, int d, int fp8, int max_new, int m
   //   R = 128, n = 4096, 32 heads over 8        287 and 191 us,      242 and 237 us
   //   R = 64,  n = 8192, 16 heads over 4        158 and 136 us,      144 and 159 us
   //   R = 64,  n = 4096, 16 heads over 4        100 and 101 us,       88 and 106 us
-  const long long keys = (long long)R * max_keys * Hkv;
+  const long long seen = window ? std::min<long long>(max_keys, (long long)window + sinks) : max_keys;  // by one token
+  const long long keys = R * seen * Hkv;
   if (G <= 32 && (long long)T * 2 < (long long)R * max_new && keys >= (fp8 ? 1500000ll : 4000000ll)) {
     const int most = 32 / G;
     p[1] = p[0];
     p[1].n_min = most + 1;
-    p[0] = plan_kernel(true, G, d, fp8, most, max_keys, num_sms);
+    p[0] = plan_kernel(true, most);
     p[0].n_max = most;
     return 2;
   }

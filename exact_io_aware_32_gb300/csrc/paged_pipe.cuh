@@ -23,8 +23,8 @@ struct Pages {
   __device__ __forceinline__ int entry(const PagedArgs& a, const Piece& p, int i) const {
     return i <= (p.q.len - 1) >> a.page_shift ? a.block_table[(long long)p.r * a.max_pages + i] : -1;
   }
-  __device__ __forceinline__ void begin(const PagedArgs& a, const Piece& p, int lane) {
-    base = ((p.jb * 128) >> a.page_shift) & ~31;
+  __device__ __forceinline__ void begin(const PagedArgs& a, const Piece& p, int jj, int lane) {  // jj: the first block
+    base = ((jj * 128) >> a.page_shift) & ~31;
     now = entry(a, p, base + lane);
     next = entry(a, p, base + 32 + lane);
   }
@@ -63,22 +63,29 @@ struct Tile {
 // cache reads as zeros: its copy lies past the tensor map's end. (A copy may
 // complete before lane 0 has said how many bytes are to come: the phase waits
 // for that arrival.)
-template <int D, bool FP8>
+// Under a window (low: its first key) pages of which the tile sees no key read as zeros too, whatever the table says there:
+// they may have been given to others.
+template <int D, bool FP8, bool WIN = false>
 __device__ __forceinline__ void load_block(const PagedArgs& a, const Piece& p, int jj, int page, int lane,
-                                           const CUtensorMap* tm, uint8_t* dst, uint64_t* bar) {
+                                           const CUtensorMap* tm, uint8_t* dst, uint64_t* bar, int low = 0) {
   const int shift = min(a.page_shift, 7), rows = min(128, p.q.len - jj * 128);
   const int n = (rows + (1 << shift) - 1) >> shift;  // pages with keys
   if (lane < n) {
     constexpr int kRow = D * (FP8 ? 1 : 2);
     if (lane == 0) mbar_arrive_expect_tx(bar, (uint32_t)((n << shift) * kRow));
-    const bool ok = (unsigned)page < (unsigned)a.num_pages;
+    bool ok = (unsigned)page < (unsigned)a.num_pages, seen = true;
+    if constexpr (WIN) {
+      const int key = jj * 128 + (lane << shift);  // the first of the copy's keys
+      seen = key + (1 << shift) > low || key < a.sinks;
+      ok = ok && seen;
+    }
     const int z = (ok ? page : a.num_pages) * a.Hkv + (ok ? p.h : 0);
     const int y = (jj * 128) & ((1 << a.page_shift) - 1) & ~127;  // a 256-token page's second half
     if constexpr (FP8)
       tma_load_3d(dst + (lane << shift) * kRow, tm, bar, 0, y, z);
     else
       tma_load_5d(dst + (lane << shift) * kRow, tm, bar, 0, 0, 0, y >> 3, z);
-    if (!ok) atomicOr(a.status, kStatusBadLength);
+    if (!ok && seen) atomicOr(a.status, kStatusBadLength);
   }
   __syncwarp();
 }
@@ -304,23 +311,6 @@ __device__ __forceinline__ void conv_arrive(uint64_t* full, uint64_t* empty, int
   }
 }
 
-// 32 bytes to global memory in one instruction (a whole sector per lane).
-__device__ __forceinline__ void st_global_v8(void* p, const uint32_t (&v)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
-}
-
-// The same to an address that may be only 16-byte aligned.
-__device__ __forceinline__ void st_global_32(void* p, const uint32_t (&v)[8], bool aligned32) {
-  if (aligned32) {
-    st_global_v8(p, v);
-  } else {
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-  }
-}
-
 // The pieces of a CTA's range, worked out by its loading warp and told to the
 // other warps: a step of the walk takes about 1000 cycles, most of them waiting
 // for instructions that run once per tile, and stood in every role's chain.
@@ -377,7 +367,8 @@ struct PieceReader {
 };
 
 // The part descriptor of this CTA, kept up by one thread as it walks the pieces.
-__device__ __forceinline__ void note_piece(const PagedArgs& a, Parts& s, const Piece& p, const Walk& walk,
+template <bool WIN>
+__device__ __forceinline__ void note_piece(const PagedArgs& a, Parts& s, const Piece& p, const Walk<WIN>& walk,
                                            int per) {
   if (p.jb > 0) {
     s.lead = 1;

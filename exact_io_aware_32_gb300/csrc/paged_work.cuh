@@ -65,10 +65,36 @@ __host__ __device__ __forceinline__ int keys_seen(const PagedArgs& a, const Requ
   return a.causal ? max(q.len - q.n + min(upto, q.n), 0) : q.len;
 }
 
+// The key blocks that a tile whose first token is 'tok' streams under a window: those that hold any of the first a.sinks keys,
+// up to the window's first block, and from that on. Its j-th block is the request's block at(j).
+struct Band {
+  int sunk, skip;  // blocks before the window's; blocks between them and it that nobody sees
+  int low;         // the first key of the window of the first token
+  int wide;        // the window, no wider than the request (places behind it stay within 32 bits)
+  __host__ __device__ __forceinline__ int at(int j) const { return j < sunk ? j : j + skip; }
+};
+__host__ __device__ __forceinline__ Band band_of(const PagedArgs& a, const Request& q, int tok) {
+  Band b;
+  b.wide = min(a.window, q.len);
+  b.low = max(q.len - q.n + tok - b.wide + 1, 0);
+  b.sunk = min((int)(((unsigned)a.sinks + 127u) >> 7), b.low >> 7);
+  b.skip = (b.low >> 7) - b.sunk;
+  return b;
+}
+
+// Keys that tiles under a window count for at most, in sum: a tile's tokens, its window, the sinks in whole blocks and half
+// a block where the window begins. (Lengths only say how the work is dealt out.)
+__host__ __device__ __forceinline__ long long band_keys(const PagedArgs& a, const Request& q, int i) {
+  const long long cap = (long long)((a.sinks + 127ll) & ~127ll) + a.window + a.tpt + 64, base = max(q.len - q.n, 0);
+  const long long all = (cap - base) / a.tpt, whole = all < 0 ? 0 : all < i ? all : i;  // tiles that see less than that
+  return whole * base + whole * (whole + 1) / 2 * a.tpt + (i - whole) * cap;
+}
+
 // Length of the first i of a request's nt tiles (for one key head): the keys that their last tokens see, summed and then
 // taken as blocks, and the fixed parts. Where the first tokens see no key it counts more than they see, up to the request's
 // keys for each tile. (Exact sums, with a division for such requests, cost the others too: one short request 10.2 us,
 // with this 9.9 us.)
+template <bool WIN = false>
 __host__ __device__ __forceinline__ int tiles_len(const PagedArgs& a, const Request& q, int i, int nt) {
   long long keys = (long long)i * q.len;
   if (a.causal) {
@@ -77,6 +103,7 @@ __host__ __device__ __forceinline__ int tiles_len(const PagedArgs& a, const Requ
         (long long)i * max(q.len - q.n, 0) + (long long)whole * (whole + 1) / 2 * a.tpt + (i == nt ? q.n : 0);
     keys = min(keys, seen);  // (the sum is the smaller one unless the first tokens see no key)
   }
+  if (WIN) keys = min(keys, band_keys(a, q, i));
   return (int)(keys >> 7) + kTileCost * i;
 }
 // (two lengths or sums of them; INT_MAX: too many to count)
@@ -113,11 +140,13 @@ __device__ __forceinline__ int border(const PagedArgs& a, int x, int nb) {
 // The part of tile i of request q, at pos and len long, that lies in [p0, p1): p.jb, p.je, p.nb; whether it is a piece.
 // A tile of at most a.whole blocks is not cut but goes to the CTA that holds its middle (one that sees no key: its
 // beginning).
+template <bool WIN = false>
 __device__ __forceinline__ bool cut(const PagedArgs& a, const Request& q, int i, int pos, int len, int p0, int p1,
                                     Piece& p) {
   p.q = q;
   p.tok = i * a.tpt;
   p.nb = (keys_seen(a, q, p.tok + a.tpt) + 127) >> 7;
+  if (WIN && p.nb) p.nb -= band_of(a, q, p.tok).skip;
   if (p.nb <= a.whole) {
     p.jb = 0;
     p.je = p.nb;
@@ -134,7 +163,7 @@ __device__ __forceinline__ bool cut(const PagedArgs& a, const Request& q, int i,
 // work, the others wait: every instruction here counts once per warp that runs
 // it, and all warps working it out took 1500 cycles more.
 constexpr int kWarpRequests = 8;
-template <int NT>
+template <int NT, bool WIN = false>
 __device__ __forceinline__ void find_range(const PagedArgs& a, Range& out, int (&s_sum)[NT / 32]) {
   constexpr int kWarps = NT / 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -153,7 +182,7 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, Range& out, int (
       if (r == r0) first = q;
       any_bad |= bad;
       const int nt = tiles_of(a, q);
-      if (nt) mine = add_len(mine, a.Hkv * tiles_len(a, q, nt, nt));
+      if (nt) mine = add_len(mine, a.Hkv * tiles_len<WIN>(a, q, nt, nt));
     }
     int upto = mine;
 #pragma unroll
@@ -185,7 +214,7 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, Range& out, int (
     if (p0 < total && pos <= p0 && p0 < pos + mine) {  // one thread holds p0
       Request q = first;
       for (int r = r0;;) {
-        const int nt = tiles_of(a, q), head = nt ? tiles_len(a, q, nt, nt) : 0;
+        const int nt = tiles_of(a, q), head = nt ? tiles_len<WIN>(a, q, nt, nt) : 0;
         if (p0 >= pos + a.Hkv * head) {
           pos += a.Hkv * head;
           bool bad;
@@ -197,7 +226,7 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, Range& out, int (
         int lo = 0, hi = nt;  // the last tile that begins at or before p0
         while (hi - lo > 1) {
           const int mid = (lo + hi) >> 1;
-          if (tiles_len(a, q, mid, nt) <= p0 - pos)
+          if (tiles_len<WIN>(a, q, mid, nt) <= p0 - pos)
             lo = mid;
           else
             hi = mid;
@@ -207,12 +236,12 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, Range& out, int (
         g.p1 = p1;
         g.per = per;
         g.head = pos;
-        g.pos = pos + tiles_len(a, q, lo, nt);
-        g.len = pos + tiles_len(a, q, lo + 1, nt) - g.pos;
+        g.pos = pos + tiles_len<WIN>(a, q, lo, nt);
+        g.len = pos + tiles_len<WIN>(a, q, lo + 1, nt) - g.pos;
         g.i = lo;
         g.nt = nt;
         g.some = 1;
-        g.use = cut(a, q, lo, g.pos, g.len, p0, p1, g.first);
+        g.use = cut<WIN>(a, q, lo, g.pos, g.len, p0, p1, g.first);
         g.first.r = r;
         g.first.h = h;
         out = g;
@@ -225,6 +254,7 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, Range& out, int (
 
 // Walks a range's pieces in order; every warp role walks the same ones:
 // for (bool more = walk.begin(a, range, p); more; more = walk.step(a, p)).
+template <bool WIN = false>
 struct Walk {
   Request q;
   RawRequest next;         // the request after q, loaded ahead and not looked at before it is needed
@@ -283,7 +313,7 @@ struct Walk {
     }
     while (pos < p1) {
       const bool again = kOne && nt == 1 && p.r == r;  // the same tile of the next key head
-      const int len = again ? last_len : head + tiles_len(a, q, i + 1, nt) - pos;
+      const int len = again ? last_len : head + tiles_len<WIN>(a, q, i + 1, nt) - pos;
       p.r = r;
       p.h = h;
       bool use = true;
@@ -291,7 +321,7 @@ struct Walk {
         p.jb = 0;
         p.je = p.nb;
       } else {
-        use = cut(a, q, i, pos, len, p0, p1, p);
+        use = cut<WIN>(a, q, i, pos, len, p0, p1, p);
       }
       advance(a, len);
       if (use) return true;

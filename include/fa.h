@@ -390,6 +390,139 @@ FA_API int fa_fwd_paged(const void* q, long long q_stride, const void* k_cache, 
                         int Hkv, int d, int num_pages, int page_size, int max_new, float scale, int causal,
                         void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * fa_fwd_paged (causal) with a sliding window: a token sees the last 'window'
+ * keys of its request up to its own (window >= 1), and the request's first
+ * 'sinks' keys (>= 0). Pages of which no token of a tile sees a key are not read
+ * and count as zeros, whatever the table says of them, so those that a request's window has
+ * left may be given to others (their entries stay in range or not, nothing is reported); hidden keys
+ * on pages that are read must hold finite values. The time goes by the keys that are seen. Other
+ * arguments, results and errors as in fa_fwd_paged, with the same workspace.
+ */
+FA_API int fa_fwd_paged_window(const void* q, long long q_stride, const void* k_cache, const void* v_cache, int fp8,
+                               float descale_k, float descale_v, const int* block_table, int max_pages,
+                               const int* query_start, const int* seq_lens, void* o, float* lse, int T, int R, int Hq,
+                               int Hkv, int d, int num_pages, int page_size, int max_new, float scale, int window,
+                               int sinks, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Rotation of queries and keys by their positions, with the norm of each head
+ * in the same pass: what stands before the attention in a layer. (The pages
+ * that this library follows begin at q, k and v; this is its own choice.)
+ *   z = x, or with weights the normed row z = x w / sqrt(mean(x^2) + eps), over the d elements of a head
+ *   pair i of z, (a, b), of a token at position p becomes
+ *     factor (a cos t - b sin t, b cos t + a sin t), t = p * freqs[i],  i = 0 .. rotary / 2 - 1;
+ *   the elements from rotary on stay as they are in z.
+ * Pairs are neighbours, (z[2 i], z[2 i + 1]), where interleaved != 0, else
+ * (z[i], z[i + rotary / 2]). The result is computed in fp32 and rounded once.
+ *
+ * fa_heads: bf16 rows [B, H, N, d] anywhere in device memory: row (b, h, n)
+ * begins at data + 2 (b stride_b + h stride_h + n stride_n) bytes, its d
+ * elements are contiguous. So slices of one projection's output are read as they
+ * are and written as attention takes them. The struct is in host memory.
+ * Strides are at least 0 and (of a dimension longer than one) multiples of 8;
+ * an output's rows do not overlap. An output may be its own input (the same data
+ * and strides); otherwise nothing overlaps.
+ */
+typedef struct {
+  void* data;
+  long long stride_b, stride_h, stride_n; /* in elements */
+} fa_heads;
+
+/*
+ * Forward.
+ *   q, k           [in]  rows [B, Hq, N, d] and [B, Hk, N, d] (Hk = 0: queries alone, k and k_out are not looked at)
+ *   q_out, k_out   [out] the same shapes
+ *   q_weight, k_weight [in] the norms' weights [d], bf16 or (weights_fp32 != 0) fp32, 16-byte aligned; NULL, both of them: no norms
+ *   eps            the norms': finite, >= 0
+ *   freqs          [in]  fp64 [rotary / 2], radians a position. The angle is exact to 2^-53 of a frequency times
+ *                  the position, and 2^-24 of a turn: a position of millions loses nothing
+ *   rotary         rotated elements of a head: a multiple of 16, 0 (norms alone) to d
+ *   factor         of cosine and sine (1, or what a scaling for long texts asks for): finite
+ *   positions      [in]  int32: token n of sequence b stands at positions[b * positions_stride + n]
+ *                  (positions_stride 0: the same for all); NULL: at n
+ * Returns FA_OK or an fa_status error code.
+ */
+FA_API int fa_rope_fwd(const fa_heads* q, const fa_heads* k, const fa_heads* q_out, const fa_heads* k_out,
+                       const void* q_weight, const void* k_weight, int weights_fp32, float eps, const double* freqs,
+                       int rotary, int interleaved, float factor, const int* positions, long long positions_stride,
+                       int B, int Hq, int Hk, int N, int d, void* stream);
+
+/*
+ * Backward: gradients with respect to q, k and the weights, given those of q_out and k_out.
+ *   dq_out, dk_out [in]  rows, as q_out and k_out
+ *   q, k           [in]  the forward's, where there are norms (else not looked at)
+ *   dq, dk         [out] rows, as q and k
+ *   dq_weight, dk_weight [out] fp32 [d], where there are norms
+ *   workspace      with norms: fa_rope_bwd_workspace_bytes bytes, 16-byte aligned; contents do not matter; not
+ *                  shared by calls that may run at once
+ * Repeated calls give identical bits. Other arguments as in fa_rope_fwd.
+ * Returns FA_OK or an fa_status error code.
+ */
+FA_API size_t fa_rope_bwd_workspace_bytes(int Hq, int Hk, int d);
+FA_API int fa_rope_bwd(const fa_heads* dq_out, const fa_heads* dk_out, const fa_heads* q, const fa_heads* k,
+                       const fa_heads* dq, const fa_heads* dk, const void* q_weight, const void* k_weight,
+                       int weights_fp32, float eps, float* dq_weight, float* dk_weight, const double* freqs, int rotary,
+                       int interleaved, float factor, const int* positions, long long positions_stride, int B, int Hq,
+                       int Hk, int N, int d, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Positions of a serving step's packed tokens, from what fa_paged_plan wrote:
+ * new token i of the n of request r stands at seq_lens[r] - n + i. Once per
+ * step, for all layers.
+ *   positions [out] device int32 [T]; -1 for rows of no request
+ * Returns FA_OK or an fa_status error code.
+ */
+FA_API int fa_paged_positions(const int* query_start, const int* seq_lens, int R, int* positions, int T, void* stream);
+
+/*
+ * fa_rope_fwd of a serving step's packed tokens and fa_paged_store in one
+ * launch: queries to q_out, keys, rotated (and normed), and values into the paged cache.
+ *   q, k, v        [in]  bf16 [T, heads, d] with token strides, as in fa_paged_store and fa_fwd_paged
+ *   slots          [in]  device int32 [T]; of a row with a negative slot nothing is written, its row of q_out included
+ *   positions      [in]  device int32 [T]
+ *   q_out          [out] bf16 [T, Hq, d] with token stride q_out_stride (may be q itself, with the same stride)
+ *   k_cache, v_cache [out] as in fa_paged_store. E4M3 keys are rounded from fp32 once, not by way of bf16:
+ *                  to the code nearest to the key / descale_k within that value's own fp32 rounding; values as there
+ * Slots that are not negative must be distinct. One past the cache is left out
+ * with its row of keys and values and reported by fa_device_status as FA_ERR_INVALID_ARG.
+ * Other arguments as in fa_rope_fwd. Returns FA_OK or an fa_status error code.
+ */
+FA_API int fa_paged_rope_store(const void* q, const void* k, const void* v, long long q_stride, long long k_stride,
+                               long long v_stride, const int* slots, const int* positions, const double* freqs,
+                               int rotary, int interleaved, float factor, const void* q_weight, const void* k_weight,
+                               int weights_fp32, float eps, void* q_out, long long q_out_stride, int T, int Hq, int Hkv,
+                               int d, void* k_cache, void* v_cache, int num_pages, int page_size, int fp8,
+                               float descale_k, float descale_v, void* stream);
+
+/*
+ * Attention with a sliding window: of the keys that the causal rule shows it
+ * (key j is visible to query i, at position p = i + Nk - Nq, iff j <= p) a row
+ * sees the last 'window' ones, its own among them, and the first 'sinks' of
+ * the sequence: j <= p and (p - j < window or j < sinks). Blocks of keys that no row of a tile sees
+ * are neither read nor multiplied. Forward and backward as in fa_fwd_kv and
+ * fa_bwd_kv (causal), with grouped heads.
+ *   q, o, dO, dq   bf16 [B, Hq, Nq, d];  lse fp32 [B, Hq, Nq]
+ *   k, v, dk, dv   bf16 [B, Hkv, Nk, d]: query head h reads key head h / (Hq / Hkv) (Hq a multiple of Hkv)
+ *   window         >= 1 (Nk and more: the causal rule alone);  sinks >= 0
+ *   Nq <= Nk
+ *   seqlens_q, seqlens_k
+ *                  as in fa_fwd_kv; the rule above is written for a sequence's own lengths
+ * B * Hq * Nq * d and B * Hkv * Nk * d stay below 2^31. The workspace holds D
+ * for the rows, the work counters and, with sinks, parts of their keys'
+ * gradients. dk and dv of a key head are sums over the query heads that share
+ * it, in a fixed order: repeated calls give identical bits.
+ * Returns FA_OK or an fa_status error code.
+ */
+FA_API int fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv,
+                         int Nq, int Nk, int d, float scale, int window, int sinks, const int* seqlens_q,
+                         const int* seqlens_k, void* stream);
+FA_API size_t fa_bwd_window_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d, int window, int sinks);
+FA_API int fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dO,
+                         void* dq, void* dk, void* dv, int B, int Hq, int Hkv, int Nq, int Nk, int d, float scale,
+                         int window, int sinks, const int* seqlens_q, const int* seqlens_k, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
 /* Static, human-readable name of a status code. Never NULL. */
 FA_API const char* fa_status_string(int status);
 
