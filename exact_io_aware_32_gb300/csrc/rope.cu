@@ -10,7 +10,7 @@
 // Everything is a pass over the rows, bound by HBM where there are many and by
 // latency where there are few. A thread holds 16 elements of a row, those of
 // eight whole pairs, in two 16-byte chunks: D / 16 lanes a row. A warp takes one
-// token and a slice of its heads, so that the eight angles of a lane serve all of them.
+// token and a slice of its heads, so that its lanes make each angle once for all of them.
 //
 // Angles: a position times a frequency may be millions of radians, of which fp32
 // keeps no fraction of a turn. The frequency is taken in turns as a 64-bit
@@ -87,33 +87,78 @@ __device__ __forceinline__ unsigned long long turns(double f) {
   return __double2ull_rn((x - floor(x)) * 18446744073709551616.0);
 }
 
-__device__ __forceinline__ void angles(const RopeArgs& a, const unsigned long long* turn, const Place& p, int position,
-                                       float sign, float (&c)[8], float (&s)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    c[i] = 1.f;
-    s[i] = 0.f;
+// Cosines and sines of the tokens that a warp has at a time, in its part of shared memory: made by its lanes in turn, four
+// pairs' halves of every lane side by side (no bank twice), as place() deals them out.
+template <int D>
+struct Angles {
+  float4 at[D / 2 * 32 / (D / 16) / 2];  // two pairs each, D / 2 a token, up to 32 / (D / 16) tokens
+};
+// Where a token is: number n of sequence b. on(): so many tokens later.
+struct Token {
+  int b, n;
+  __device__ __forceinline__ Token on(int more, int N) const {
+    Token t = {b, n + more};
+    while (t.n >= N) {
+      t.n -= N;
+      ++t.b;
+    }
+    return t;
   }
-  if (p.pair < 0) return;
+};
+template <int D>
+__device__ __forceinline__ void make_angles(const RopeArgs& a, const unsigned long long* turn, Angles<D>& to, int tokens,
+                                            const Token& first, int lane, float sign) {
+  constexpr int kLanes = D / 16;
+  __syncwarp();  // the angles before have been read
+  for (int i = lane; i < tokens * (D / 2); i += 32) {
+    const int which = i / (D / 2), pair = i % (D / 2);
+    float2 cs = make_float2(1.f, 0.f);
+    if (pair < a.rot / 2) {
+      const Token at = first.on(which, a.N);
+      const int position = !a.pos ? at.n : at.b < a.B ? a.pos[at.b * a.pos_b + at.n] : 0;
+      const unsigned long long t = (unsigned long long)(long long)position * turn[pair];
+      sincospif((float)(int)(t >> 32) * 0x1p-31f, &cs.y, &cs.x);
+      cs.x *= a.factor;
+      cs.y *= sign * a.factor;
+    }
+    reinterpret_cast<float2*>(&to.at[which * (D / 4) + (pair % 8 / 2) * kLanes + pair / 8])[pair % 2] = cs;
+  }
+  __syncwarp();
+}
+template <int D>
+__device__ __forceinline__ void take_angles(const Angles<D>& from, int which, int part, float (&c)[8], float (&s)[8]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const unsigned long long t = (unsigned long long)(long long)position * turn[p.pair + i];
-    sincospif((float)(int)(t >> 32) * 0x1p-31f, &s[i], &c[i]);
-    c[i] *= a.factor;
-    s[i] *= sign * a.factor;
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = from.at[which * (D / 4) + i * (D / 16) + part];
+    c[2 * i] = v.x;
+    s[2 * i] = v.y;
+    c[2 * i + 1] = v.z;
+    s[2 * i + 1] = v.w;
   }
 }
 
-__device__ __forceinline__ void load_weights(const RopeArgs& a, const void* w, const Place& p, float (&x)[16]) {
-  if (a.w_fp32) {
-    const float* f = static_cast<const float*>(w);
+// The weights of a part in shared memory, four elements of every lane side by side (no bank twice), as place() deals them out.
+template <int D, bool INTER>
+__device__ __forceinline__ void stage_weights(const RopeArgs& a, const void* w, float4* to) {
+  constexpr int kLanes = D / 16;
+  for (int i = threadIdx.x; i < D; i += kThreads) {
+    const int part = i / 16, e = i % 16;
+    const Place p = place<INTER>(part, a.rot);
+    const int at = e < 8 ? p.a + e : p.b + e - 8;
+    const float x = a.w_fp32 ? static_cast<const float*>(w)[at] : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[at]);
+    reinterpret_cast<float*>(to + (e / 4) * kLanes + part)[e % 4] = x;
+  }
+}
+// x *= f w
+template <int D>
+__device__ __forceinline__ void times_weights(float (&x)[16], const float4* w, int part, float f) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      x[i] = f[p.a + i];
-      x[8 + i] = f[p.b + i];
-    }
-  } else {
-    unpack(load_row(RopeView{const_cast<void*>(w), 0, 0, 0}, 0, p), x);
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = w[i * (D / 16) + part];
+    x[4 * i] *= f * v.x;
+    x[4 * i + 1] *= f * v.y;
+    x[4 * i + 2] *= f * v.z;
+    x[4 * i + 3] *= f * v.w;
   }
 }
 
@@ -143,157 +188,208 @@ __device__ __forceinline__ void store_codes(uint8_t* row, const Place& p, const 
   *reinterpret_cast<uint2*>(row + p.b) = make_uint2(w[2], w[3]);
 }
 
-// Forward and store: units (token, slice of heads), a warp each; of the queries first, then the keys (and the values).
+// What a warp has at a time: 'tokens' tokens' slice of heads, a step of which is one row for each of its groups of kLanes
+// lanes. Several tokens only where a part has fewer heads than the warp has groups; then there is one step.
+struct Unit {
+  Token first, token;  // the first, and this lane's group's
+  int h, h1;           // the group's first head, the slice's end
+  int steps;
+  bool there;
+};
+// (64-bit division takes far longer)
+__device__ __forceinline__ long long divide(long long x, int y) {
+  return x <= 0xFFFFFFFFll ? (long long)((unsigned)x / (unsigned)y) : x / y;
+}
+__device__ __forceinline__ Unit unit(const RopeArgs& a, int kind, long long i, int group) {
+  Unit u;
+  const int many = a.tokens[kind], heads = a.part[kind].heads, slices = a.slices[kind];
+  const long long of = slices == 1 ? i : divide(i, slices), first = of * many;
+  const int h0 = (int)(i - of * slices) * a.slice_heads[kind];
+  u.first.b = (int)divide(first, a.N);
+  u.first.n = (int)(first - (long long)u.first.b * a.N);
+  const int share = a.groups[kind];  // groups of a token
+  u.token = u.first.on(many > 1 ? group / share : 0, a.N);
+  u.there = u.token.b < a.B;
+  if (!u.there) u.token = {a.B - 1, a.N - 1};
+  u.h1 = min(heads, h0 + a.slice_heads[kind]);
+  u.h = h0 + (many > 1 ? group % share : group);
+  u.steps = (u.h1 - h0 + share - 1) / share;
+  if (!u.there) u.h1 = 0;
+  return u;
+}
+
+// Forward and store: units of the queries first, then the keys (and the values).
+constexpr int fwd_ctas_per_sm(bool norm, Mode mode) { return norm || mode == kStore ? 3 : 4; }
 template <int D, bool NORM, bool INTER, Mode MODE>
-__global__ void __launch_bounds__(kThreads) fa_rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, fwd_ctas_per_sm(NORM, MODE)) fa_rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int kLanes = D / 16, kRows = 32 / kLanes;  // lanes of a row, rows a warp has at a time
   __shared__ unsigned long long turn[D / 2];
-  const int lane = threadIdx.x & 31, row = lane / kLanes;
+  __shared__ float4 weights[NORM ? 2 : 1][NORM ? D / 4 : 1];
+  __shared__ Angles<D> angles[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = lane / kLanes, part_of = lane % kLanes;
   ptx::grid_release();
   ptx::grid_wait();
   for (int i = threadIdx.x; i < a.rot / 2; i += kThreads) turn[i] = turns(a.freqs[i]);
+  if constexpr (NORM) {
+    stage_weights<D, INTER>(a, a.part[0].w, weights[0]);
+    if (a.part[1].heads) stage_weights<D, INTER>(a, a.part[1].w, weights[1]);
+  }
   __syncthreads();
-  const long long tokens = (long long)a.B * a.N;
-  const long long first_k = tokens * a.slices[0], first_v = first_k + tokens * a.slices[1];
-  const long long units = MODE == kStore ? first_v + tokens * a.slices[1] : first_v;
-  for (long long u = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += (long long)gridDim.x * kWarps) {
-    const bool value = MODE == kStore && u >= first_v;
-    const int kind = u >= first_k ? 1 : 0;
-    const long long i = u - (value ? first_v : kind ? first_k : 0);
+  const float inv_k = MODE == kStore && a.fp8 ? 1.f / a.descale_k : 1.f;
+  const long long first_k = a.units[0], first_v = first_k + a.units[1];
+  const long long units = MODE == kStore ? first_v + a.units[1] : first_v;
+  for (long long i = (long long)blockIdx.x * kWarps + warp; i < units; i += (long long)gridDim.x * kWarps) {
+    const bool value = MODE == kStore && i >= first_v;
+    const int kind = i >= first_k ? 1 : 0;
+    Unit u = unit(a, kind, i - (value ? first_v : kind ? first_k : 0), group);
     const RopePart& part = a.part[kind];
-    const int slices = a.slices[kind];
-    const long long token = i / slices;
-    const int h0 = (int)(i - token * slices) * a.slice_heads[kind], h1 = min(part.heads, h0 + a.slice_heads[kind]);
-    const int b = (int)(token / a.N), n = (int)(token - (long long)b * a.N);
-    int slot = 0;
-    if constexpr (MODE == kStore) {
-      slot = a.slots[n];
-      if (slot < 0) continue;
-      if (kind && slot >> a.page_shift >= a.num_pages) {
-        if (lane == 0) atomicOr(a.status, kStatusBadLength);
-        continue;
+    long long place_in_cache = 0;
+    if constexpr (MODE == kStore) {  // rows without a slot have no heads
+      const int slot = u.there ? a.slots[u.token.n] : -1;
+      if (slot < 0) u.h1 = 0;
+      if (kind) {
+        const int page = slot >> a.page_shift;
+        if (slot >= 0 && page >= a.num_pages) {
+          u.h1 = 0;
+          if (part_of == 0) atomicOr(a.status, kStatusBadLength);
+        }
+        place_in_cache = (((long long)page * part.heads) << a.page_shift) + (slot & ((1 << a.page_shift) - 1));
       }
     }
-    const Place p = value ? place<true>(lane % kLanes, 0) : place<INTER>(lane % kLanes, a.rot);
+    const Place p = value ? place<true>(part_of, 0) : place<INTER>(part_of, a.rot);
     const RopeView& src = value ? a.v : part.in;
-    const long long from = b * src.b + n * src.n;
-    int h = h0 + row;
-    Raw next{};
-    if (h < h1) next = load_row(src, from + h * src.h, p);
-    float c[8], s[8], w[16];
-    if (!value) {
-      if (NORM) load_weights(a, part.w, p, w);
-      angles(a, turn, p, a.pos ? a.pos[b * a.pos_b + n] : n, 1.f, c, s);
-    }
-    for (int k = h0; k < h1; k += kRows, h += kRows) {  // (uniform: the sums of a row are a warp's work)
-      const Raw raw = next;
-      if (h + kRows < h1) next = load_row(src, from + (h + kRows) * src.h, p);
-      if (MODE == kStore && kind) {
-        const long long at = ((((long long)(slot >> a.page_shift) * part.heads + h) << a.page_shift) +
-                              (slot & ((1 << a.page_shift) - 1))) * D;
-        if (value) {
-          if (h >= h1) continue;
-          if (a.fp8) {
-            const Factor f = factor_of(a.descale_v);
-            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.v_cache) + at + p.a) =
-                make_uint4(quantise4(raw.a.x, raw.a.y, f), quantise4(raw.a.z, raw.a.w, f), quantise4(raw.b.x, raw.b.y, f),
-                           quantise4(raw.b.z, raw.b.w, f));
-          } else {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.v_cache) + at + p.a);
-            dst[0] = raw.a;
-            dst[1] = raw.b;
-          }
-          continue;
-        }
-        float x[16];
-        unpack(raw, x);
-        if (NORM) {
-          const float r = inverse_deviation<D>(x, a.eps);
+    const long long from = u.token.b * src.b + u.token.n * src.n;
+    int h = u.h;
+    const int step = a.groups[kind];
+    // the rows of the next kAhead steps are on their way while one is worked on
+    constexpr int kAhead = 2;
+    Raw ahead[kAhead];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] *= r * w[e];
+    for (int k = 0; k < kAhead; ++k) {
+      ahead[k] = Raw{};
+      if (h + k * step < u.h1) ahead[k] = load_row(src, from + (h + k * step) * src.h, p);
+    }
+    if (MODE == kStore && value) {
+      for (int k = 0; k < u.steps; ++k, h += step) {
+        const Raw raw = ahead[0];
+        ahead[0] = ahead[1];
+        if (h + kAhead * step < u.h1) ahead[1] = load_row(src, from + (h + kAhead * step) * src.h, p);
+        if (h >= u.h1) continue;
+        const long long at = (place_in_cache + ((long long)h << a.page_shift)) * D + p.a;
+        if (a.fp8) {
+          const Factor f = factor_of(a.descale_v);
+          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.v_cache) + at) =
+              make_uint4(quantise4(raw.a.x, raw.a.y, f), quantise4(raw.a.z, raw.a.w, f), quantise4(raw.b.x, raw.b.y, f),
+                         quantise4(raw.b.z, raw.b.w, f));
+        } else {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.v_cache) + at);
+          dst[0] = raw.a;
+          dst[1] = raw.b;
         }
-        rotate<INTER>(x, c, s);
-        if (h >= h1) continue;
+      }
+      continue;
+    }
+    float c[8], s[8];
+    make_angles<D>(a, turn, angles[warp], a.tokens[kind], u.first, lane, 1.f);
+    take_angles<D>(angles[warp], a.tokens[kind] > 1 ? group / step : 0, part_of, c, s);
+    for (int k = 0; k < u.steps; ++k, h += step) {  // (uniform: the sums of a row are a warp's work)
+      float x[16];
+      unpack(ahead[0], x);
+#pragma unroll
+      for (int e = 0; e + 1 < kAhead; ++e) ahead[e] = ahead[e + 1];
+      if (h + kAhead * step < u.h1) ahead[kAhead - 1] = load_row(src, from + (h + kAhead * step) * src.h, p);
+      if (NORM) {
+        const float r = inverse_deviation<D>(x, a.eps);
+        times_weights<D>(x, weights[kind], part_of, r);
+      }
+      rotate<INTER>(x, c, s);
+      if (h >= u.h1) continue;
+      if (MODE == kStore && kind) {
+        const long long at = (place_in_cache + ((long long)h << a.page_shift)) * D;
         if (a.fp8)
-          store_codes(static_cast<uint8_t*>(a.k_cache) + at, p, x, 1.f / a.descale_k);
+          store_codes(static_cast<uint8_t*>(a.k_cache) + at, p, x, inv_k);
         else
           store_row(RopeView{a.k_cache, 0, 0, 0}, at, p, x);
       } else {
-        float x[16];
-        unpack(raw, x);
-        if (NORM) {
-          const float r = inverse_deviation<D>(x, a.eps);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) x[e] *= r * w[e];
-        }
-        rotate<INTER>(x, c, s);
-        if (h < h1) store_row(part.out, b * part.out.b + n * part.out.n + h * part.out.h, p, x);
+        store_row(part.out, u.token.b * part.out.b + u.token.n * part.out.n + h * part.out.h, p, x);
       }
     }
   }
 }
 
-// Backward: the CTAs of a part take its tokens in turn, a warp a token at a time, so that a lane adds up the weights'
+// Backward: the CTAs of a part take its units in turn, a warp one at a time, so that a lane adds up the weights'
 // gradients of its 16 elements in registers; the sums of a CTA go to the workspace, and a second kernel adds those up in
 // order (no atomics: repeated calls give the same bits).
+constexpr int kMaxSms = 160;
+constexpr int bwd_ctas_per_sm(bool norm) { return norm ? 2 : 3; }
 template <int D, bool NORM, bool INTER>
-__global__ void __launch_bounds__(kThreads) fa_rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
-  constexpr int kLanes = D / 16, kRows = 32 / kLanes;
+__global__ void __launch_bounds__(kThreads, bwd_ctas_per_sm(NORM)) fa_rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int kLanes = D / 16;
   __shared__ unsigned long long turn[D / 2];
   __shared__ float sums[NORM ? kWarps : 1][D];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = lane / kLanes;
+  __shared__ float4 weights[NORM ? D / 4 : 1];
+  __shared__ Angles<D> angles[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = lane / kLanes, part_of = lane % kLanes;
   ptx::grid_release();
   ptx::grid_wait();
-  for (int i = threadIdx.x; i < a.rot / 2; i += kThreads) turn[i] = turns(a.freqs[i]);
-  __syncthreads();
   const int kind = (int)blockIdx.x >= a.ctas[0] ? 1 : 0;
   const RopePart& part = a.part[kind];
-  const int cta = (int)blockIdx.x - (kind ? a.ctas[0] : 0), slices = a.slices[kind];
-  const long long units = (long long)a.B * a.N * slices;
-  const Place p = place<INTER>(lane % kLanes, a.rot);
-  float w[16], dw[16];
-  if (NORM) load_weights(a, part.w, p, w);
+  for (int i = threadIdx.x; i < a.rot / 2; i += kThreads) turn[i] = turns(a.freqs[i]);
+  if constexpr (NORM) stage_weights<D, INTER>(a, part.w, weights);
+  __syncthreads();
+  const int cta = (int)blockIdx.x - (kind ? a.ctas[0] : 0), step = a.groups[kind];
+  const Place p = place<INTER>(part_of, a.rot);
+  float dw[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) dw[e] = 0.f;
-  for (long long u = (long long)cta * kWarps + warp; u < units; u += (long long)a.ctas[kind] * kWarps) {
-    const long long token = u / slices;
-    const int h0 = (int)(u - token * slices) * a.slice_heads[kind], h1 = min(part.heads, h0 + a.slice_heads[kind]);
-    const int b = (int)(token / a.N), n = (int)(token - (long long)b * a.N);
-    const long long from = b * part.in.b + n * part.in.n, x_from = b * part.x.b + n * part.x.n;
-    int h = h0 + row;
-    Raw next{}, next_x{};
-    if (h < h1) {
-      next = load_row(part.in, from + h * part.in.h, p);
-      if (NORM) next_x = load_row(part.x, x_from + h * part.x.h, p);
+  for (long long i = (long long)cta * kWarps + warp; i < a.units[kind]; i += (long long)a.ctas[kind] * kWarps) {
+    const Unit u = unit(a, kind, i, group);
+    const long long from = u.token.b * part.in.b + u.token.n * part.in.n, x_from = u.token.b * part.x.b + u.token.n * part.x.n;
+    int h = u.h;
+    constexpr int kAhead = 2;  // as in the forward
+    Raw ahead[kAhead], ahead_x[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      ahead[k] = ahead_x[k] = Raw{};
+      if (h + k * step < u.h1) {
+        ahead[k] = load_row(part.in, from + (h + k * step) * part.in.h, p);
+        if (NORM) ahead_x[k] = load_row(part.x, x_from + (h + k * step) * part.x.h, p);
+      }
     }
     float c[8], s[8];
-    angles(a, turn, p, a.pos ? a.pos[b * a.pos_b + n] : n, -1.f, c, s);
-    for (int k = h0; k < h1; k += kRows, h += kRows) {
-      const Raw raw = next, raw_x = next_x;
-      if (h + kRows < h1) {
-        next = load_row(part.in, from + (h + kRows) * part.in.h, p);
-        if (NORM) next_x = load_row(part.x, x_from + (h + kRows) * part.x.h, p);
+    make_angles<D>(a, turn, angles[warp], a.tokens[kind], u.first, lane, -1.f);
+    take_angles<D>(angles[warp], a.tokens[kind] > 1 ? group / step : 0, part_of, c, s);
+    for (int k = 0; k < u.steps; ++k, h += step) {
+      float g[16], x[16];
+      unpack(ahead[0], g);
+      if (NORM) unpack(ahead_x[0], x);
+#pragma unroll
+      for (int e = 0; e + 1 < kAhead; ++e) {
+        ahead[e] = ahead[e + 1];
+        ahead_x[e] = ahead_x[e + 1];
       }
-      float g[16];
-      unpack(raw, g);
+      if (h + kAhead * step < u.h1) {
+        ahead[kAhead - 1] = load_row(part.in, from + (h + kAhead * step) * part.in.h, p);
+        if (NORM) ahead_x[kAhead - 1] = load_row(part.x, x_from + (h + kAhead * step) * part.x.h, p);
+      }
+      const bool live = h < u.h1;
       rotate<INTER>(g, c, s);
       if (NORM) {
-        float x[16];
-        unpack(raw_x, x);
         const float r = inverse_deviation<D>(x, a.eps);
         float m[2] = {0.f, 0.f};
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
           x[e] *= r;  // the normed row before its weights
-          if (h < h1) dw[e] = fmaf(g[e], x[e], dw[e]);
-          g[e] *= w[e];
-          m[e & 1] = fmaf(g[e], x[e], m[e & 1]);
+          if (live) dw[e] = fmaf(g[e], x[e], dw[e]);
         }
+        times_weights<D>(g, weights, part_of, 1.f);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) m[e & 1] = fmaf(g[e], x[e], m[e & 1]);
         const float mean = row_sum<D>(m[0] + m[1]) * (1.f / D);
 #pragma unroll
         for (int e = 0; e < 16; ++e) g[e] = r * fmaf(-x[e], mean, g[e]);
       }
-      if (h < h1) store_row(part.out, b * part.out.b + n * part.out.n + h * part.out.h, p, g);
+      if (live) store_row(part.out, u.token.b * part.out.b + u.token.n * part.out.n + h * part.out.h, p, g);
     }
   }
   if constexpr (NORM) {
@@ -301,7 +397,7 @@ __global__ void __launch_bounds__(kThreads) fa_rope_bwd_kernel(const __grid_cons
     for (int e = 0; e < 16; ++e) {
 #pragma unroll
       for (int s = kLanes; s < 32; s <<= 1) dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], s);
-      if (row == 0) sums[warp][(e < 8 ? p.a : p.b - 8) + e] = dw[e];
+      if (group == 0) sums[warp][(e < 8 ? p.a : p.b - 8) + e] = dw[e];
     }
     __syncthreads();
     for (int i = threadIdx.x; i < D; i += kThreads) {
@@ -313,20 +409,21 @@ __global__ void __launch_bounds__(kThreads) fa_rope_bwd_kernel(const __grid_cons
   }
 }
 
-// The CTAs' sums of one part's weights: a block per 32 elements, its warps every kWarps-th CTA.
-__global__ void __launch_bounds__(kThreads) fa_rope_dw_kernel(const __grid_constant__ RopeArgs a) {
-  __shared__ float sums[kWarps][32];
+// The CTAs' sums of one part's weights: a block per 32 elements, its warps every kSumWarps-th CTA.
+constexpr int kSumWarps = 32;
+__global__ void __launch_bounds__(32 * kSumWarps) fa_rope_dw_kernel(const __grid_constant__ RopeArgs a) {
+  __shared__ float sums[kSumWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kind = blockIdx.y, e = blockIdx.x * 32 + lane;
   ptx::grid_wait();
   const int first = kind ? a.ctas[0] : 0, last = first + a.ctas[kind];
   float t = 0.f;
-#pragma unroll 4
-  for (int c = first + warp; c < last; c += kWarps) t += a.dw_part[(long long)c * a.d + e];
+#pragma unroll 8
+  for (int c = first + warp; c < last; c += kSumWarps) t += a.dw_part[(long long)c * a.d + e];
   sums[warp][lane] = t;
   __syncthreads();
   if (warp) return;
 #pragma unroll
-  for (int k = 1; k < kWarps; ++k) t += sums[k][lane];
+  for (int k = 1; k < kSumWarps; ++k) t += sums[k][lane];
   if (a.part[kind].heads) a.dw[kind][e] = t;
 }
 
@@ -358,58 +455,78 @@ __global__ void __launch_bounds__(kThreads) fa_paged_positions_kernel(const __gr
   a.positions[t] = s0 <= t && t < s1 ? (int)max(at, -1ll) : -1;
 }
 
-// Warps that share a token's heads, and how many heads each takes: all of them where the tokens alone fill the GPU, fewer
-// the fewer tokens there are.
-void slice(RopeArgs& a, int rows, int num_sms) {
+// Units of each part. Where a part's heads are fewer than a warp's groups of lanes, a warp takes several tokens, a power of
+// two groups each; else all heads of a token where the tokens alone fill the GPU, and fewer the fewer tokens there are.
+void make_units(RopeArgs& a, int groups, int num_sms) {
   const long long want = (long long)num_sms * 32;  // warps
   const long long tokens = (long long)a.B * a.N;
-  const int steps = (a.part[0].heads + rows - 1) / rows + (a.part[1].heads + rows - 1) / rows;  // of a warp, for a token
+  int steps = 0;  // of a warp, for all heads of a token
+  for (const RopePart& p : a.part) steps += (p.heads + groups - 1) / groups;
   for (int k = 0; k < 2; ++k) {
-    const int mine = (a.part[k].heads + rows - 1) / rows;
-    long long per = std::max(1ll, std::min<long long>(steps, tokens * steps / want));  // steps of a warp
-    a.slice_heads[k] = (int)per * rows;
-    a.slices[k] = mine ? (int)((mine + per - 1) / per) : 0;
+    const int heads = a.part[k].heads;
+    a.tokens[k] = a.slices[k] = 1;
+    a.groups[k] = groups;
+    a.slice_heads[k] = heads;
+    a.units[k] = 0;
+    if (!heads) continue;
+    if (heads < groups) {
+      int share = 1;
+      while (share < heads) share *= 2;
+      a.groups[k] = share;
+      a.tokens[k] = groups / share;
+    } else {
+      const long long per = std::max(1ll, std::min<long long>(steps, tokens * steps / want));  // steps of a warp
+      const int mine = (heads + groups - 1) / groups;
+      a.slice_heads[k] = (int)per * groups;
+      a.slices[k] = (int)((mine + per - 1) / per);
+    }
+    a.units[k] = (tokens + a.tokens[k] - 1) / a.tokens[k] * a.slices[k];
   }
 }
 
 template <int D, Mode MODE>
 cudaError_t launch_forward(const RopeArgs& args, bool norm, bool inter, int num_sms, cudaStream_t stream) {
   RopeArgs a = args;
-  slice(a, 32 / (D / 16), num_sms);
-  const long long units = (long long)a.B * a.N * (a.slices[0] + (MODE == kStore ? 2 : 1) * a.slices[1]);
-  const unsigned ctas = (unsigned)std::min<long long>((units + kWarps - 1) / kWarps, 1 << 20);
+  make_units(a, 32 / (D / 16), num_sms);
+  const long long units = a.units[0] + (MODE == kStore ? 2 : 1) * a.units[1];
+  // As many CTAs as run at once, or twice that, their warps over the units in turn: the frequencies and weights are staged
+  // once for all. Once, twice and a warp a unit, for 16384 tokens of 32 + 8 heads of 128: without norms 61.6, 56.9 and 57.5 us
+  // (5.9 TB/s), with norms 66.0 (5.1 TB/s), 66.5 and 68.5 us; the store of 15523 tokens to E4M3 71.6, 70.6 and 78.7 us.
+  const long long resident = (long long)num_sms * fwd_ctas_per_sm(norm, MODE) * (norm ? 1 : 2);
+  const unsigned ctas = (unsigned)std::min<long long>((units + kWarps - 1) / kWarps, resident);
   auto kern = norm ? (inter ? fa_rope_kernel<D, true, true, MODE> : fa_rope_kernel<D, true, false, MODE>)
                    : (inter ? fa_rope_kernel<D, false, true, MODE> : fa_rope_kernel<D, false, false, MODE>);
   return launch_dependent(kern, dim3(ctas), kThreads, 0, stream, a);
 }
 
-// CTAs of the backward for each part, in the ratio of their heads.
-constexpr int kMaxSms = 160, kBwdCtasPerSm = 4;
-void backward_ctas(RopeArgs& a, int rows, int num_sms) {
-  slice(a, rows, num_sms);
-  const int H = a.part[0].heads + a.part[1].heads, all = std::min(num_sms, kMaxSms) * kBwdCtasPerSm;
+// CTAs of the backward for each part, in the ratio of the steps that they have to take.
+void backward_ctas(RopeArgs& a, int groups, bool norm, int num_sms) {
+  make_units(a, groups, num_sms);
+  double steps[2];
+  for (int k = 0; k < 2; ++k)
+    steps[k] = (double)a.units[k] * ((std::min(a.part[k].heads, a.slice_heads[k]) + a.groups[k] - 1) / a.groups[k] + 0.5 + 0.5 * a.tokens[k]);
+  const int all = std::min(num_sms, kMaxSms) * bwd_ctas_per_sm(norm);
   for (int k = 0; k < 2; ++k) {
-    const long long units = (long long)a.B * a.N * a.slices[k];
-    const long long most = std::max(1ll, (long long)all * a.part[k].heads / H);
-    a.ctas[k] = a.part[k].heads ? (int)std::min<long long>((units + kWarps - 1) / kWarps, most) : 0;
+    const int most = std::max(1, (int)(all * steps[k] / (steps[0] + steps[1]) + 0.5));
+    a.ctas[k] = (int)std::min<long long>((a.units[k] + kWarps - 1) / kWarps, most);
   }
 }
 
 template <int D>
 cudaError_t launch_backward(const RopeArgs& args, bool norm, bool inter, int num_sms, cudaStream_t stream) {
   RopeArgs a = args;
-  backward_ctas(a, 32 / (D / 16), num_sms);
+  backward_ctas(a, 32 / (D / 16), norm, num_sms);
   auto kern = norm ? (inter ? fa_rope_bwd_kernel<D, true, true> : fa_rope_bwd_kernel<D, true, false>)
                    : (inter ? fa_rope_bwd_kernel<D, false, true> : fa_rope_bwd_kernel<D, false, false>);
   const cudaError_t e = launch_dependent(kern, dim3((unsigned)(a.ctas[0] + a.ctas[1])), kThreads, 0, stream, a);
   if (e != cudaSuccess || !norm) return e;
-  return launch_dependent(fa_rope_dw_kernel, dim3(D / 32, 2u), kThreads, 0, stream, a);
+  return launch_dependent(fa_rope_dw_kernel, dim3(D / 32, 2u), 32 * kSumWarps, 0, stream, a);
 }
 
 }  // namespace
 
 size_t rope_bwd_bytes(int Hq, int Hk, int d) {
-  return Hq + Hk > 0 ? (size_t)(kMaxSms * kBwdCtasPerSm + 2) * d * sizeof(float) : 0;
+  return Hq + Hk > 0 ? (size_t)(kMaxSms * bwd_ctas_per_sm(true) + 2) * d * sizeof(float) : 0;
 }
 
 cudaError_t launch_rope_fwd(RopeArgs a, bool norm, bool inter, int num_sms, cudaStream_t stream) {

@@ -27,8 +27,10 @@ struct RopeArgs {
   float factor, eps;
   float* dw_part;        // backward with norms: fp32 [CTAs][d], the CTAs of queries first
   float* dw[2];          // [d]
-  int ctas[2];           // set by the launcher: CTAs of each part; warps that share a token's heads, heads of each
-  int slices[2], slice_heads[2];
+  // set by the launcher: CTAs of each part (backward); tokens that a warp has at a time, its groups of lanes that share one,
+  // slices of a token's heads, heads of each; units (slices of so many tokens)
+  int ctas[2], tokens[2], groups[2], slices[2], slice_heads[2];
+  long long units[2];
   // the store (B = 1, N tokens): row t of the keys and values goes to slots[t], nothing of a row with a negative one anywhere
   const int* slots;
   RopeView v;
