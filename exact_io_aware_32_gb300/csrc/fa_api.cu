@@ -68,6 +68,13 @@ int device_info(DeviceInfo** out) {
     di.ready = true;
   }
   if (!di.supported) return FA_ERR_UNSUPPORTED;
+  // A thread that has made no call of the runtime yet (autograd runs backward passes in one of its own) has no context, and
+  // without one no tensor map can be encoded: setting the device binds it.
+  thread_local int bound = -1;
+  if (bound != dev) {
+    if (cudaSetDevice(dev) != cudaSuccess) return fail_launch();
+    bound = dev;
+  }
   *out = &di;
   return FA_OK;
 }
@@ -449,6 +456,7 @@ int fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* l
   fa::WindowArgs a;
   std::memset(&a, 0, sizeof(a));
   if (!encode_3d(&a.tm_q, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, B * Hq, Nq, d, 64, 128) ||
+      !encode_3d(&a.tm_o, o, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, B * Hq, Nq, d, 64, 128) ||
       !encode_3d(&a.tm_k, k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, B * Hkv, Nk, d, 64, 128) ||
       !encode_3d(&a.tm_v, v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, B * Hkv, Nk, d, 64, 128))
     return FA_ERR_LAUNCH;
