@@ -41,10 +41,11 @@ struct WCfg {
   static constexpr int kTiles = D == 64 ? 1 : 2;
   static constexpr int kCtasPerSm = 3 - kTiles;
   static constexpr int kPanels = D / 64, kPanelBytes = 128 * 128, kTileBytes = kPanels * kPanelBytes;
-  static constexpr int kKStages = 2, kVStages = 3;  // V is read last, so it gets the deeper ring
-  // Q: a slot per tile, or two for one tile, so that the next one's is there when this one ends
+  // V is read last, so it gets the deeper ring; with two tiles its third place is where their O are staged in turn
+  static constexpr int kKStages = 2, kVStages = kTiles == 2 ? 2 : 3;
+  // Q: a slot per tile, or two for one tile, so that the next one's is there when this one ends (each also stages its tile's O)
   static constexpr int kOffQ = 0, kOffK = 2 * kTileBytes, kOffV = kOffK + kKStages * kTileBytes;
-  static constexpr int kOffBar = kOffV + kVStages * kTileBytes;
+  static constexpr int kOffO = kOffV + kVStages * kTileBytes, kOffBar = kOffO + (kTiles == 2 ? kTileBytes : 0);
   // No alignment slack (two CTAs share an SM's 228 KB): the kernel checks that shared memory starts on 1024 bytes.
   static constexpr int kSmemBytes = kOffBar + 512;
   static_assert(kSmemBytes <= 232448 && (kCtasPerSm == 1 || 2 * (kSmemBytes + 1024) <= 233472), "shared memory");
@@ -61,11 +62,16 @@ struct WBars {
   uint64_t k_full[2], k_empty[2], v_full[3], v_empty[3];
   uint64_t s_full[2], p_full[2], o_done[2], o_free[2];  // (one tile: o_done follows every P V)
   uint64_t s_free;                                      // one tile: S is in registers
+  uint64_t staged;                                      // two tiles: a staged O has been read by its store
   uint64_t teardown;
   uint32_t tmem_base;
   int abort;
 };
 static_assert(sizeof(WBars) <= 512, "barriers exceed their shared memory");
+
+// The last sinks' block costs as much as any other, six blocks instead of five with a window of 512, unless it is known to
+// be thin: with at most kThin sinks in it only so many columns of S, and keys of P V, are worked on.
+constexpr int kThin = 32;
 
 // What a CTA works on at a time: up to two tiles of 128 rows of one key head, and the key blocks that they stream:
 // block j of the first 'sunk' ones, then block j + skip.
@@ -75,6 +81,7 @@ struct Item {
   int nb[2];            // blocks up to the last one that the tile sees (0: padding rows, or no tile)
   int sunk, skip;
   int miss;             // a block that the second tile does not see (its window begins one later)
+  int thin;             // a block of which only the first 32 keys, sinks, can be seen
   int sq, off;
   bool there[2];        // the tile has rows of the array
   __device__ __forceinline__ int at(int j) const { return j < sunk ? j : j + skip; }
@@ -110,10 +117,14 @@ __device__ __forceinline__ Item item(const WindowArgs& a, int i) {
   x.sunk = min(sunk, low[0]);
   x.skip = low[0] - x.sunk;
   x.miss = low[1] > low[0] && low[0] >= sunk ? x.sunk : -1;
+  x.thin = x.sunk == sunk && sunk > 0 && a.sinks - 128 * (sunk - 1) <= kThin ? sunk - 1 : -1;
 #pragma unroll
   for (int t = 0; t < 2; ++t) x.nb[t] = max(x.nb[t] - x.skip, 0);
   return x;
 }
+
+// The first n bits (none for n <= 0, all from 32 on).
+__device__ __forceinline__ uint32_t first_bits(int n) { return n >= 32 ? ~0u : (1u << max(n, 0)) - 1u; }
 
 template <int D>
 __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
@@ -154,6 +165,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
       mbar_init(&bars.v_empty[s], 1);
     }
     mbar_init(&bars.s_free, 128);
+    mbar_init(&bars.staged, 1);
     mbar_init(&bars.teardown, 1);
     fence_mbar_init();
   }
@@ -179,7 +191,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
     bool ok = true;
     // test hook: without the first Q tile, the MMA warp's first wait expires
     bool withhold = a.test_fault == 1;
-    auto load_q = [&](const Item& x, int t) -> bool {
+    auto load_q = [&](int t, int row, int head) -> bool {
       // the slot and its uses so far: tile t's own, or the two in turn
       const int s = C::kTiles == 2 ? t : nq[t] & 1, use = C::kTiles == 2 ? nq[t] : nq[t] >> 1;
       if (!warp_wait(&bars.q_free[s], (use & 1) ^ 1, abort_flag)) return false;
@@ -188,7 +200,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
           uint64_t* bar = &bars.q_full[t][nq[t] & 1];
           mbar_arrive_expect_tx(bar, C::kTileBytes);
           for (int pn = 0; pn < C::kPanels; ++pn)
-            tma_load_3d(smem + C::kOffQ + s * C::kTileBytes + pn * C::kPanelBytes, &a.tm_q, bar, pn * 64, x.row[t], x.head[t]);
+            tma_load_3d(smem + C::kOffQ + s * C::kTileBytes + pn * C::kPanelBytes, &a.tm_q, bar, pn * 64, row, head);
         }
         __syncwarp();
         ++nq[t];
@@ -207,13 +219,13 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
       const Item x = item<C::kTiles>(a, i);
       if (x.bhk < 0) break;
       const int n = max(x.nb[0], x.nb[1]);
-      if (x.nb[0] > 0 && !(ok = load_q(x, 0))) break;
+      if (x.nb[0] > 0 && !(ok = load_q(0, x.row[0], x.head[0]))) break;
       for (int j = 0; j < n; ++j, ++g) {
         const int ks = g % C::kKStages, vs = g % C::kVStages, row = x.at(j) * 128;
         if (!(ok = warp_wait(&bars.k_empty[ks], ((g / C::kKStages) & 1) ^ 1, abort_flag))) break;
         load(&a.tm_k, smem + C::kOffK + ks * C::kTileBytes, &bars.k_full[ks], row, x.bhk);
         nk = g + 1;
-        if (C::kTiles == 2 && j == 0 && x.nb[1] > 0 && !(ok = load_q(x, 1))) break;
+        if (C::kTiles == 2 && j == 0 && x.nb[1] > 0 && !(ok = load_q(1, x.row[1], x.head[1]))) break;
         if (!(ok = warp_wait(&bars.v_empty[vs], ((g / C::kVStages) & 1) ^ 1, abort_flag))) break;
         load(&a.tm_v, smem + C::kOffV + vs * C::kTileBytes, &bars.v_full[vs], row, x.bhk);
         nv = g + 1;
@@ -230,24 +242,32 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
   } else if (warp == C::kWarpMma) {
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t kIdS = idesc_bf16(128, 128, false, false);  // Q, K both K-major
+    constexpr uint32_t kIdThin = idesc_bf16(128, kThin, false, false);
     constexpr uint32_t kIdO = idesc_bf16(128, D, false, true);     // P from TMEM, V MN-major
     const uint64_t dq0 = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
     const uint64_t dk0 = sdesc_sw128(smem_u32(smem + C::kOffK), 16, 1024);
     const uint64_t dv0 = sdesc_sw128(smem_u32(smem + C::kOffV), C::kPanelBytes, 1024);
-    auto issue_s = [&](int t, int qs, int ks, bool last) {  // by the elected lane
+    auto issue_s = [&](int t, int qs, int ks, bool thin, bool last) {  // by the elected lane
+      const uint32_t id = thin ? kIdThin : kIdS;
       const uint32_t qo = (uint32_t)(qs * C::kTileBytes) >> 4, ko = (uint32_t)(ks * C::kTileBytes) >> 4;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {  // each k-step reads 32 bytes of every row
         const uint32_t o = ((kk >> 2) * C::kPanelBytes + (kk & 3) * 32) >> 4;
-        mma_ss(tmem + C::col_s(t), dq0 + qo + o, dk0 + ko + o, kIdS, kk > 0);
+        mma_ss(tmem + C::col_s(t), dq0 + qo + o, dk0 + ko + o, id, kk > 0);
       }
       mma_commit(&bars.s_full[t]);
-      if (last) mma_commit(&bars.q_free[qs]);  // the tile's last product to read Q
+      // the tile's last product to read Q (one tile: its slot is free once O, staged there, has been stored)
+      if (C::kTiles == 2 && last) mma_commit(&bars.q_free[qs]);
     };
-    auto issue_pv = [&](int t, int vs, bool first) {
+    auto issue_pv = [&](int t, int vs, bool thin, bool first) {
       const uint32_t vo = (uint32_t)(vs * C::kTileBytes) >> 4;
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk)  // P columns [8 kk, 8 kk + 8), V rows [16 kk, 16 kk + 16)
+      for (int kk = 0; kk < kThin / 16; ++kk)  // P columns [8 kk, 8 kk + 8), V rows [16 kk, 16 kk + 16)
+        mma_ts(tmem + C::col_o(t), tmem + C::col_p(t) + kk * 8, dv0 + vo + kk * ((16 * 128) >> 4), kIdO,
+               (!first || kk > 0) ? 1u : 0u);
+      if (thin) return;
+#pragma unroll
+      for (int kk = kThin / 16; kk < 8; ++kk)
         mma_ts(tmem + C::col_o(t), tmem + C::col_p(t) + kk * 8, dv0 + vo + kk * ((16 * 128) >> 4), kIdO,
                (!first || kk > 0) ? 1u : 0u);
     };
@@ -266,7 +286,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
           if (!(ok = warp_wait(&bars.q_full[t][nq[t] & 1], (nq[t] >> 1) & 1, abort_flag))) break;
           tc_fence_after();
           if (x.uses(t, 0)) {
-            if (elect_one()) issue_s(t, C::kTiles == 2 ? t : nq[0] & 1, g % C::kKStages, x.nb[t] == 1);
+            if (elect_one()) issue_s(t, C::kTiles == 2 ? t : nq[0] & 1, g % C::kKStages, x.thin == 0, x.nb[t] == 1);
             __syncwarp();
           }
         }
@@ -294,7 +314,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
               if (!begun[t] && !(ok = warp_wait(&bars.o_free[t], (nq[t] & 1) ^ 1, abort_flag))) break;
               tc_fence_after();
               if (elect_one()) {
-                issue_pv(t, s, !begun[t]);
+                issue_pv(t, s, j == x.thin, !begun[t]);
                 if (j == x.nb[t] - 1) mma_commit(&bars.o_done[t]);
                 if (t == v_last) mma_commit(&bars.v_empty[s]);
               }
@@ -303,7 +323,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
               ++np[t];
             }
             if (x.uses(t, jn)) {
-              if (elect_one()) issue_s(t, t, sn, jn == x.nb[t] - 1);
+              if (elect_one()) issue_s(t, t, sn, jn == x.thin, jn == x.nb[t] - 1);
               __syncwarp();
             }
           }
@@ -322,7 +342,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
-              issue_s(0, nq[0] & 1, sn, j + 2 == n);
+              issue_s(0, nq[0] & 1, sn, j + 1 == x.thin, j + 2 == n);
               mma_commit(&bars.k_empty[sn]);
             }
             __syncwarp();
@@ -333,7 +353,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
           if (!ok) break;
           tc_fence_after();
           if (elect_one()) {
-            issue_pv(0, s, j == 0);
+            issue_pv(0, s, j == x.thin, j == 0);
             mma_commit(&bars.o_done[0]);
             mma_commit(&bars.v_empty[s]);
           }
@@ -354,20 +374,24 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
     const uint32_t t_p = tmem + lane_off + C::col_p(t);
     const uint32_t t_o = tmem + lane_off + C::col_o(t);
     const float sl2 = a.scale_log2;
-    const bool o32 = (reinterpret_cast<uintptr_t>(a.o) & 31u) == 0;
     int np = 0, nq = 0;  // blocks and items of this tile so far
+    int staged = 0;      // O staged before this item's, by both tiles
     bool ok = true;
     for (int i = 0; ok; ++i) {
       const Item x = item<C::kTiles>(a, i);
       if (x.bhk < 0) break;
-      if (!x.there[t]) continue;
-      const int row0 = x.row[t], row = row0 + r, p = row + x.off, nb = x.nb[t];  // p: the row's position
+      if (!(t ? x.there[1] : x.there[0])) {
+        staged += (x.nb[0] > 0) + (x.nb[1] > 0);
+        continue;
+      }
+      const int row0 = t ? x.row[1] : x.row[0], row = row0 + r, p = row + x.off;  // p: the row's position
+      const int nb = t ? x.nb[1] : x.nb[0], head = t ? x.head[1] : x.head[0], miss = t ? x.miss : -1;
       const int p_last = row0 + 127 + x.off;
       float m_ref = -INFINITY;  // exponent reference, log2 units of scaled scores
       float l_sum = 0.f;        // sum of 2^(s * sl2 - m_ref) over the keys seen so far
       bool begun = false;       // whether O holds anything
       for (int j = 0; j < nb; ++j) {
-        if (!x.uses(t, j)) continue;
+        if (j == miss) continue;
         ok = __all_sync(0xffffffffu, mbar_wait(&bars.s_full[t], np & 1, abort_flag));
         if (!ok) break;
         tc_fence_after();
@@ -382,16 +406,21 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
           tc_fence_before();
           mbar_arrive(&bars.s_free);  // S is in registers: the next block's S may overwrite it
         }
+        const bool thin = j == x.thin;
         float mx = fmax3(fmax3(cmax[0], cmax[1], cmax[2]), cmax[3], -INFINITY);
         // Masked: blocks that reach past the first row's position (keys past sk are past every row's) and those with keys
         // behind the last row's window that are not all sinks.
         const int kv0 = x.at(j) * 128;
-        if (kv0 + 127 > row0 + x.off || (p_last - kv0 >= a.window && kv0 + 128 > a.sinks)) {
-          // keep column c iff c <= lim and (c > out or c < sunk)
+        uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};  // a bit for each column of a chunk of 32 that the row sees
+        if (thin || kv0 + 127 > row0 + x.off || (p_last - kv0 >= a.window && kv0 + 128 > a.sinks)) {
+          // column c iff c <= lim and (c > out or c < sunk)
           const int lim = p - kv0, out = lim - a.window, sunk = a.sinks - kv0;
 #pragma unroll
+          for (int c = 0; c < 4; ++c)
+            keep[c] = first_bits(lim + 1 - 32 * c) & ~(first_bits(out + 1 - 32 * c) & ~first_bits(sunk - 32 * c));
+#pragma unroll
           for (int c = 0; c < 128; ++c)
-            if (c > lim || (c <= out && c >= sunk)) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+            if (!(keep[c >> 5] >> (c & 31) & 1u)) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
           float mxc[8];  // row maximum over eight chains of 16 scores, then a tree
 #pragma unroll
           for (int q = 0; q < 8; ++q)
@@ -434,10 +463,10 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
         chunk(0);
         if constexpr (C::kTiles == 2) {
           store(0);
-          chunk(1);
+          if (!thin) chunk(1);
         } else {
           // P and O are free once the P V before this one has completed (an item's first block: the epilogue waited)
-          chunk(1);
+          if (!thin) chunk(1);
           if (begun) {
             ok = __all_sync(0xffffffffu, mbar_wait(&bars.o_done[0], (np - 1) & 1, abort_flag));
             if (!ok) break;
@@ -445,11 +474,13 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
           }
           store(0);
         }
-        store(1);
-        chunk(2);
-        store(2);
-        chunk(3);
-        store(3);
+        if (!thin) {
+          store(1);
+          chunk(2);
+          store(2);
+          chunk(3);
+          store(3);
+        }
         const float2 sum = fadd2(fadd2(sum4[0], sum4[1]), fadd2(sum4[2], sum4[3]));
         l_sum = l_sum * alpha + (sum.x + sum.y);
         if (rescale) {
@@ -473,37 +504,56 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const bool valid = row < a.Nq, real = row < x.sq;  // a padding row: o = 0
-      const long long at = (long long)x.head[t] * a.Nq + row;
-      uint8_t* orow = static_cast<uint8_t*>(a.o) + at * (D * 2);
-      const float inv = real ? 1.f / l_sum : 0.f;
+      const long long at = (long long)head * a.Nq + row;
       if (nb > 0) {
+        // O, normalised, as bf16 into the staging tile (rows of 128 swizzled bytes a panel), which one thread stores
         tc_fence_after();
+        const float inv = 1.f / l_sum;
+        const int turn = staged + (t == 1 && x.nb[0] > 0 ? 1 : 0);  // two tiles: after so many others
+        uint8_t* stage = smem + (C::kTiles == 2 ? C::kOffO : C::kOffQ + (nq & 1) * C::kTileBytes);
+        if (C::kTiles == 2 && turn > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars.staged, (turn - 1) & 1, abort_flag));
+        if (ok) {
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          uint32_t o[32];
-          tmem_ld32(t_o + c, o);
-          tmem_ld_wait(o);
-          if (c + 32 == D) {
-            tc_fence_before();
-            mbar_arrive(&bars.o_free[t]);  // O is in registers: the next item may accumulate there
-          }
-          if (valid)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t w[8];
-#pragma unroll
-              for (int q = 0; q < 8; ++q)
-                w[q] = real ? pack_bf16x2(__uint_as_float(o[16 * h + 2 * q]) * inv, __uint_as_float(o[16 * h + 2 * q + 1]) * inv)
-                            : 0u;
-              st_global_32(orow + c * 2 + h * 32, w, o32);
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tmem_ld32(t_o + c, o);
+            tmem_ld_wait(o);
+            if (c + 32 == D) {
+              tc_fence_before();
+              mbar_arrive(&bars.o_free[t]);  // O is in registers: the next item may accumulate there
             }
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4) {
+              const int piece = ((c & 63) >> 3) + q4;  // 16 bytes of the panel's row
+              uint32_t w[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                w[q] = real ? pack_bf16x2(__uint_as_float(o[8 * q4 + 2 * q]) * inv, __uint_as_float(o[8 * q4 + 2 * q + 1]) * inv)
+                            : 0u;
+              st_shared_v4(smem_u32(stage + (c >> 6) * C::kPanelBytes + r * 128 + ((piece ^ (r & 7)) << 4)), w[0], w[1], w[2],
+                           w[3]);
+            }
+          }
+          fence_proxy_async_smem();
+        }
+        if (!named_bar_and(1 + t, 128, ok)) {  // the four warps agree whether to go on
+          ok = false;
+          break;
+        }
+        if (r == 0) {
+          for (int pn = 0; pn < C::kPanels; ++pn)
+            tma_store_3d(&a.tm_o, stage + pn * C::kPanelBytes, pn * 64, row0, head);
+          bulk_commit();
+          bulk_wait_read0();  // the staging tile has been read; the writes finish on their own
+          mbar_arrive(C::kTiles == 2 ? &bars.staged : &bars.q_free[nq & 1]);
         }
         ++nq;
       } else if (valid) {
-        const uint32_t zero[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-        for (int c = 0; c < D; c += 16) st_global_32(orow + c * 2, zero, o32);
+        uint4* orow = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.o) + at * (D * 2));
+        for (int c = 0; c < D / 8; ++c) orow[c] = make_uint4(0u, 0u, 0u, 0u);
       }
       if (valid) a.lse[at] = real ? (m_ref + log2f(l_sum)) * kLn2 : -INFINITY;
+      staged += (x.nb[0] > 0) + (x.nb[1] > 0);
     }
   }
 

@@ -71,7 +71,7 @@ struct BwdArgs {
 
 // The forward with a window (fa_fwd_window.cu): q, o, lse over B * Hkv * group heads of Nq rows, k and v over B * Hkv of Nk.
 struct WindowArgs {
-  CUtensorMap tm_q, tm_k, tm_v;  // bf16, box 64 x 128 x 1, 128B swizzle
+  CUtensorMap tm_q, tm_k, tm_v, tm_o;  // bf16, box 64 x 128 x 1, 128B swizzle
   void* o;
   float* lse;
   unsigned int* status;
