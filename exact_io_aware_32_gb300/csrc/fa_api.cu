@@ -458,7 +458,9 @@ int fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* l
   if (!encode_3d(&a.tm_q, q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, B * Hq, Nq, d, 64, 128) ||
       !encode_3d(&a.tm_o, o, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, B * Hq, Nq, d, 64, 128) ||
       !encode_3d(&a.tm_k, k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, B * Hkv, Nk, d, 64, 128) ||
-      !encode_3d(&a.tm_v, v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, B * Hkv, Nk, d, 64, 128))
+      !encode_3d(&a.tm_v, v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, B * Hkv, Nk, d, 64, 128) ||
+      !encode_3d(&a.tm_k_thin, k, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, B * Hkv, Nk, d, 64, fa::kThinRows) ||
+      !encode_3d(&a.tm_v_thin, v, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, B * Hkv, Nk, d, 64, fa::kThinRows))
     return FA_ERR_LAUNCH;
   a.o = o;
   a.lse = lse;

@@ -47,31 +47,36 @@ struct WCfg {
   static constexpr int kOffQ = 0, kOffK = 2 * kTileBytes, kOffV = kOffK + kKStages * kTileBytes;
   static constexpr int kOffO = kOffV + kVStages * kTileBytes, kOffBar = kOffO + (kTiles == 2 ? kTileBytes : 0);
   // No alignment slack (two CTAs share an SM's 228 KB): the kernel checks that shared memory starts on 1024 bytes.
-  static constexpr int kSmemBytes = kOffBar + 512;
+  static constexpr int kSmemBytes = kOffBar + 640;
   static_assert(kSmemBytes <= 232448 && (kCtasPerSm == 1 || 2 * (kSmemBytes + 1024) <= 233472), "shared memory");
   static constexpr uint32_t kTmemCols = kTiles == 2 ? 512u : 256u;
   // S (fp32, 128 columns), P (bf16 pairs, 64 columns: over S, or in columns of its own) and O (fp32, D columns) of tile t
   __host__ __device__ static constexpr uint32_t col_s(int t) { return (uint32_t)t * 128u; }
   __host__ __device__ static constexpr uint32_t col_p(int t) { return kTiles == 2 ? col_s(t) : 128u; }
   __host__ __device__ static constexpr uint32_t col_o(int t) { return kTiles == 2 ? 256u + (uint32_t)t * D : 192u; }
-  static constexpr int kWarpTma = 4 * kTiles, kWarpMma = 4 * kTiles + 1, kThreads = 128 * kTiles + 64;
+  // two tiles: a warp that stores their staged O (one tile: the TMA warp does)
+  static constexpr int kWarpTma = 4 * kTiles, kWarpMma = 4 * kTiles + 1, kWarpStore = 4 * kTiles + 2;
+  static constexpr int kThreads = 128 * kTiles + 64 + (kTiles == 2 ? 32 : 0);
 };
 
 struct WBars {
-  uint64_t q_full[2][2], q_free[2];  // by tile (q_full: and its items in turn); one tile: by slot
+  uint64_t q_full[2][2], q_free[2];  // by tile (q_full: and its items in turn); one tile: q_full by its items in turn
   uint64_t k_full[2], k_empty[2], v_full[3], v_empty[3];
   uint64_t s_full[2], p_full[2], o_done[2], o_free[2];  // (one tile: o_done follows every P V)
   uint64_t s_free;                                      // one tile: S is in registers
-  uint64_t staged;                                      // two tiles: a staged O has been read by its store
+  // two tiles: a panel of O has been staged, has been read by its store; one tile: O has been staged in its Q's slot
+  uint64_t o_staged[2], o_read[2];
   uint64_t teardown;
+  uint64_t item_full[4], item_empty[4];
+  int4 items[4][4];
   uint32_t tmem_base;
   int abort;
 };
-static_assert(sizeof(WBars) <= 512, "barriers exceed their shared memory");
+static_assert(sizeof(WBars) <= 640, "barriers exceed their shared memory");
 
 // The last sinks' block costs as much as any other, six blocks instead of five with a window of 512, unless it is known to
-// be thin: with at most kThin sinks in it only so many columns of S, and keys of P V, are worked on.
-constexpr int kThin = 32;
+// be thin: with at most kThin sinks in it only so many keys are loaded, columns of S and keys of P V worked on.
+constexpr int kThin = kThinRows;
 
 // What a CTA works on at a time: up to two tiles of 128 rows of one key head, and the key blocks that they stream:
 // block j of the first 'sunk' ones, then block j + skip.
@@ -126,6 +131,49 @@ __device__ __forceinline__ Item item(const WindowArgs& a, int i) {
 // The first n bits (none for n <= 0, all from 32 on).
 __device__ __forceinline__ uint32_t first_bits(int n) { return n >= 32 ? ~0u : (1u << max(n, 0)) - 1u; }
 
+// The items of a CTA, worked out by its loading warp and told to the others (a step's divisions took every softmax thread
+// 1400 cycles between two items).
+constexpr int kItemRing = 4;
+__device__ __forceinline__ bool tell(WBars& bars, int n, const Item& x, int lane, volatile int* abort_flag) {
+  const int s = n % kItemRing;
+  if (!warp_wait(&bars.item_empty[s], ((n / kItemRing) & 1) ^ 1, abort_flag)) return false;
+  if (lane == 0) {
+    bars.items[s][0] = make_int4(x.bhk, x.head[0], x.head[1], x.row[0]);
+    bars.items[s][1] = make_int4(x.row[1], x.nb[0], x.nb[1], x.sunk);
+    bars.items[s][2] = make_int4(x.skip, x.miss, x.thin, x.sq);
+    bars.items[s][3] = make_int4(x.off, x.there[0], x.there[1], 0);
+    mbar_arrive(&bars.item_full[s]);
+  }
+  __syncwarp();
+  return true;
+}
+// The n-th item; past the last one, and when the wait runs out, bhk < 0.
+__device__ __forceinline__ Item hear(WBars& bars, int n, int lane, volatile int* abort_flag) {
+  const int s = n % kItemRing;
+  Item x;
+  x.bhk = -1;
+  if (!warp_wait(&bars.item_full[s], (n / kItemRing) & 1, abort_flag)) return x;
+  const int4 a = bars.items[s][0], b = bars.items[s][1], c = bars.items[s][2], d = bars.items[s][3];
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&bars.item_empty[s]);
+  x.bhk = a.x;
+  x.head[0] = a.y;
+  x.head[1] = a.z;
+  x.row[0] = a.w;
+  x.row[1] = b.x;
+  x.nb[0] = b.y;
+  x.nb[1] = b.z;
+  x.sunk = b.w;
+  x.skip = c.x;
+  x.miss = c.y;
+  x.thin = c.z;
+  x.sq = c.w;
+  x.off = d.x;
+  x.there[0] = d.y != 0;
+  x.there[1] = d.z != 0;
+  return x;
+}
+
 template <int D>
 __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
     fa_fwd_window_kernel(const __grid_constant__ WindowArgs a) {
@@ -165,7 +213,14 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
       mbar_init(&bars.v_empty[s], 1);
     }
     mbar_init(&bars.s_free, 128);
-    mbar_init(&bars.staged, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&bars.o_staged[s], 128);
+      mbar_init(&bars.o_read[s], 1);
+    }
+    for (int s = 0; s < kItemRing; ++s) {
+      mbar_init(&bars.item_full[s], 1);
+      mbar_init(&bars.item_empty[s], 4 * C::kTiles + (C::kTiles == 2 ? 2 : 1));  // softmax, MMA and store warps
+    }
     mbar_init(&bars.teardown, 1);
     fence_mbar_init();
   }
@@ -191,10 +246,35 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
     bool ok = true;
     // test hook: without the first Q tile, the MMA warp's first wait expires
     bool withhold = a.test_fault == 1;
+    int rows[2] = {0, 0}, heads[2] = {0, 0}, stored = 0;  // one tile: of the last two items, and those whose O has been stored
+    auto store_o = [&]() -> bool {  // of the item 'stored', from its Q's slot
+      const int s = stored & 1;
+      if (!warp_wait(&bars.o_staged[s], (stored >> 1) & 1, abort_flag)) return false;
+      if (elect_one()) {
+        if (!*abort_flag) {
+          tma_store_3d(&a.tm_o, smem + C::kOffQ + s * C::kTileBytes, 0, s ? rows[1] : rows[0], s ? heads[1] : heads[0]);
+          bulk_commit();
+        }
+        bulk_wait_read0();
+      }
+      __syncwarp();
+      ++stored;
+      return true;
+    };
     auto load_q = [&](int t, int row, int head) -> bool {
-      // the slot and its uses so far: tile t's own, or the two in turn
-      const int s = C::kTiles == 2 ? t : nq[t] & 1, use = C::kTiles == 2 ? nq[t] : nq[t] >> 1;
-      if (!warp_wait(&bars.q_free[s], (use & 1) ^ 1, abort_flag)) return false;
+      const int s = C::kTiles == 2 ? t : nq[t] & 1;  // the slot: tile t's own, or the two in turn
+      if (C::kTiles == 2) {
+        if (!warp_wait(&bars.q_free[s], (nq[t] & 1) ^ 1, abort_flag)) return false;
+      } else {
+        if (nq[0] >= 2 && !store_o()) return false;
+        if (s) {
+          rows[1] = row;
+          heads[1] = head;
+        } else {
+          rows[0] = row;
+          heads[0] = head;
+        }
+      }
       if (!withhold) {
         if (elect_one()) {
           uint64_t* bar = &bars.q_full[t][nq[t] & 1];
@@ -208,29 +288,32 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
       withhold = false;
       return true;
     };
-    auto load = [&](const CUtensorMap* tm, uint8_t* dst, uint64_t* bar, int row, int head) {
+    auto load = [&](const CUtensorMap* tm, uint8_t* dst, uint64_t* bar, int row, int head, bool thin) {
       if (elect_one()) {
-        mbar_arrive_expect_tx(bar, C::kTileBytes);
+        mbar_arrive_expect_tx(bar, thin ? C::kTileBytes * kThin / 128 : C::kTileBytes);
         for (int pn = 0; pn < C::kPanels; ++pn) tma_load_3d(dst + pn * C::kPanelBytes, tm, bar, pn * 64, row, head);
       }
       __syncwarp();
     };
     for (int i = 0; ok; ++i) {
       const Item x = item<C::kTiles>(a, i);
-      if (x.bhk < 0) break;
+      if (!(ok = tell(bars, i, x, lane, abort_flag)) || x.bhk < 0) break;
       const int n = max(x.nb[0], x.nb[1]);
       if (x.nb[0] > 0 && !(ok = load_q(0, x.row[0], x.head[0]))) break;
       for (int j = 0; j < n; ++j, ++g) {
         const int ks = g % C::kKStages, vs = g % C::kVStages, row = x.at(j) * 128;
         if (!(ok = warp_wait(&bars.k_empty[ks], ((g / C::kKStages) & 1) ^ 1, abort_flag))) break;
-        load(&a.tm_k, smem + C::kOffK + ks * C::kTileBytes, &bars.k_full[ks], row, x.bhk);
+        const bool thin = j == x.thin;
+        load(thin ? &a.tm_k_thin : &a.tm_k, smem + C::kOffK + ks * C::kTileBytes, &bars.k_full[ks], row, x.bhk, thin);
         nk = g + 1;
         if (C::kTiles == 2 && j == 0 && x.nb[1] > 0 && !(ok = load_q(1, x.row[1], x.head[1]))) break;
         if (!(ok = warp_wait(&bars.v_empty[vs], ((g / C::kVStages) & 1) ^ 1, abort_flag))) break;
-        load(&a.tm_v, smem + C::kOffV + vs * C::kTileBytes, &bars.v_full[vs], row, x.bhk);
+        load(thin ? &a.tm_v_thin : &a.tm_v, smem + C::kOffV + vs * C::kTileBytes, &bars.v_full[vs], row, x.bhk, thin);
         nv = g + 1;
       }
     }
+    if (C::kTiles == 1)
+      while (ok && stored < nq[0]) ok = store_o();
     // Let every issued copy land before the CTA can exit (an earlier load's slot was refilled only after its reader
     // completed, so it has landed).
     for (int t = 0; t < C::kTiles; ++t)
@@ -274,7 +357,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
     int g = 0, nq[2] = {0, 0}, np[2] = {0, 0};  // key blocks; items and P blocks of each tile so far
     bool ok = true;
     for (int i = 0; ok; ++i) {
-      const Item x = item<C::kTiles>(a, i);
+      const Item x = hear(bars, i, lane, abort_flag);
       if (x.bhk < 0) break;
       const int n = max(x.nb[0], x.nb[1]);
       if (n == 0) continue;
@@ -365,6 +448,38 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
     if (elect_one()) mma_commit(&bars.teardown);
     __syncwarp();
     mbar_wait_drain(&bars.teardown, 0);
+  } else if (C::kTiles == 2 && warp == C::kWarpStore) {
+    // ------------------------------------------------------------ stores of staged O, a panel at a time
+    int n = 0;  // O stored so far
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      const Item x = hear(bars, i, lane, abort_flag);
+      if (x.bhk < 0) break;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (x.nb[t] == 0) continue;
+#pragma unroll
+        for (int pn = 0; pn < C::kPanels; ++pn) {
+          if (!(ok = warp_wait(&bars.o_staged[pn], n & 1, abort_flag))) break;
+          if (elect_one()) {
+            tma_store_3d(&a.tm_o, smem + C::kOffO + pn * C::kPanelBytes, pn * 64, x.row[t], x.head[t]);
+            bulk_commit();
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (elect_one()) {
+          bulk_wait_read1();  // the first panel has been read; the writes finish on their own
+          mbar_arrive(&bars.o_read[0]);
+          bulk_wait_read0();
+          mbar_arrive(&bars.o_read[1]);
+        }
+        __syncwarp();
+        ++n;
+      }
+    }
+    if (elect_one()) bulk_wait_read0();
+    __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax + epilogue
     const int t = warp >> 2;
@@ -378,7 +493,7 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
     int staged = 0;      // O staged before this item's, by both tiles
     bool ok = true;
     for (int i = 0; ok; ++i) {
-      const Item x = item<C::kTiles>(a, i);
+      const Item x = hear(bars, i, lane, abort_flag);
       if (x.bhk < 0) break;
       if (!(t ? x.there[1] : x.there[0])) {
         staged += (x.nb[0] > 0) + (x.nb[1] > 0);
@@ -407,20 +522,20 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
           mbar_arrive(&bars.s_free);  // S is in registers: the next block's S may overwrite it
         }
         const bool thin = j == x.thin;
-        float mx = fmax3(fmax3(cmax[0], cmax[1], cmax[2]), cmax[3], -INFINITY);
         // Masked: blocks that reach past the first row's position (keys past sk are past every row's) and those with keys
         // behind the last row's window that are not all sinks.
         const int kv0 = x.at(j) * 128;
-        uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};  // a bit for each column of a chunk of 32 that the row sees
+        float mx = fmax3(fmax3(cmax[0], cmax[1], cmax[2]), cmax[3], -INFINITY);
         if (thin || kv0 + 127 > row0 + x.off || (p_last - kv0 >= a.window && kv0 + 128 > a.sinks)) {
           // column c iff c <= lim and (c > out or c < sunk)
           const int lim = p - kv0, out = lim - a.window, sunk = a.sinks - kv0;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            keep[c] = first_bits(lim + 1 - 32 * c) & ~(first_bits(out + 1 - 32 * c) & ~first_bits(sunk - 32 * c));
+          for (int c = 0; c < 4; ++c) {
+            const uint32_t keep = first_bits(lim + 1 - 32 * c) & ~(first_bits(out + 1 - 32 * c) & ~first_bits(sunk - 32 * c));
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (!(keep[c >> 5] >> (c & 31) & 1u)) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+            for (int q = 0; q < 32; ++q)
+              if (!(keep >> q & 1u)) sr[c][q] = __float_as_uint(-INFINITY);
+          }
           float mxc[8];  // row maximum over eight chains of 16 scores, then a tree
 #pragma unroll
           for (int q = 0; q < 8; ++q)
@@ -506,47 +621,40 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
       const bool valid = row < a.Nq, real = row < x.sq;  // a padding row: o = 0
       const long long at = (long long)head * a.Nq + row;
       if (nb > 0) {
-        // O, normalised, as bf16 into the staging tile (rows of 128 swizzled bytes a panel), which one thread stores
+        // O, normalised, as bf16 into the staging place (rows of 128 swizzled bytes a panel), a panel at a time
         tc_fence_after();
         const float inv = 1.f / l_sum;
         const int turn = staged + (t == 1 && x.nb[0] > 0 ? 1 : 0);  // two tiles: after so many others
-        uint8_t* stage = smem + (C::kTiles == 2 ? C::kOffO : C::kOffQ + (nq & 1) * C::kTileBytes);
-        if (C::kTiles == 2 && turn > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars.staged, (turn - 1) & 1, abort_flag));
-        if (ok) {
 #pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
+        for (int pn = 0; pn < C::kPanels; ++pn) {
+          uint8_t* stage = smem + (C::kTiles == 2 ? C::kOffO : C::kOffQ + (nq & 1) * C::kTileBytes) + pn * C::kPanelBytes;
+          if (C::kTiles == 2 && turn > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars.o_read[pn], (turn - 1) & 1, abort_flag));
+            if (!ok) break;
+          }
+#pragma unroll
+          for (int c = 0; c < 64; c += 32) {
             uint32_t o[32];
-            tmem_ld32(t_o + c, o);
+            tmem_ld32(t_o + pn * 64 + c, o);
             tmem_ld_wait(o);
-            if (c + 32 == D) {
+            if (c == 32 && pn + 1 == C::kPanels) {
               tc_fence_before();
               mbar_arrive(&bars.o_free[t]);  // O is in registers: the next item may accumulate there
             }
 #pragma unroll
             for (int q4 = 0; q4 < 4; ++q4) {
-              const int piece = ((c & 63) >> 3) + q4;  // 16 bytes of the panel's row
               uint32_t w[4];
 #pragma unroll
               for (int q = 0; q < 4; ++q)
                 w[q] = real ? pack_bf16x2(__uint_as_float(o[8 * q4 + 2 * q]) * inv, __uint_as_float(o[8 * q4 + 2 * q + 1]) * inv)
                             : 0u;
-              st_shared_v4(smem_u32(stage + (c >> 6) * C::kPanelBytes + r * 128 + ((piece ^ (r & 7)) << 4)), w[0], w[1], w[2],
-                           w[3]);
+              st_shared_v4(smem_u32(stage + r * 128 + (((c / 8 + q4) ^ (r & 7)) << 4)), w[0], w[1], w[2], w[3]);
             }
           }
           fence_proxy_async_smem();
+          mbar_arrive(&bars.o_staged[C::kTiles == 2 ? pn : nq & 1]);
         }
-        if (!named_bar_and(1 + t, 128, ok)) {  // the four warps agree whether to go on
-          ok = false;
-          break;
-        }
-        if (r == 0) {
-          for (int pn = 0; pn < C::kPanels; ++pn)
-            tma_store_3d(&a.tm_o, stage + pn * C::kPanelBytes, pn * 64, row0, head);
-          bulk_commit();
-          bulk_wait_read0();  // the staging tile has been read; the writes finish on their own
-          mbar_arrive(C::kTiles == 2 ? &bars.staged : &bars.q_free[nq & 1]);
-        }
+        if (!ok) break;
         ++nq;
       } else if (valid) {
         uint4* orow = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.o) + at * (D * 2));

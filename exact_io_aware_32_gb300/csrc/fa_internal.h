@@ -69,9 +69,13 @@ struct BwdArgs {
   int head_group_dq;  // the same for the dQ kernel
 };
 
+// Keys of a block of few sinks that are loaded and worked on (fa_fwd_window.cu).
+constexpr int kThinRows = 32;
+
 // The forward with a window (fa_fwd_window.cu): q, o, lse over B * Hkv * group heads of Nq rows, k and v over B * Hkv of Nk.
 struct WindowArgs {
   CUtensorMap tm_q, tm_k, tm_v, tm_o;  // bf16, box 64 x 128 x 1, 128B swizzle
+  CUtensorMap tm_k_thin, tm_v_thin;    // box 64 x kThinRows x 1: a block of few sinks
   void* o;
   float* lse;
   unsigned int* status;
