@@ -100,7 +100,7 @@ cudaError_t launch_plan(const PlanArgs& a, int num_sms, cudaStream_t stream);
 cudaError_t launch_store(const StoreArgs& a, int num_sms, cudaStream_t stream);
 // The kernels of a call (1 or 2) in p[]; each may use the whole workspace, one after the other.
 // (window 0: none).
-int plan_paged(int T, int R, int Hq, int Hkv, int d, int fp8, int max_new, int max_keys, int window, int sinks,
+int plan_paged(int T, int R, int Hq, int Hkv, int d, int fp8, int max_new, int page_size, int max_keys, int window, int sinks,
                int num_sms, PagedPlan (&p)[2]);
 // Encodes the tensor maps, gives the kernel its parts of the workspace and launches it with its join;
 // cudaErrorInvalidValue if the encoding fails.

@@ -143,7 +143,7 @@ size_t fa_fwd_paged_workspace_bytes(int T, int R, int Hq, int Hkv, int d, int ma
   size_t most = 0;
   for (int fp8 = 0; fp8 < 2; ++fp8) {  // one size for both kinds of cache
     fa::PagedPlan p[2];
-    const int n = fa::plan_paged(T, R, Hq, Hkv, d, fp8, max_new, INT32_MAX, 0, 0, kMaxSms, p);  // (any table width)
+    const int n = fa::plan_paged(T, R, Hq, Hkv, d, fp8, max_new, 16, INT32_MAX, 0, 0, kMaxSms, p);  // (any table width)
     for (int i = 0; i < n; ++i) most = std::max(most, p[i].bytes());
   }
   return most;
@@ -179,7 +179,7 @@ int fwd_paged(const void* q, long long q_stride, const void* k_cache, const void
   // (a window or sinks past every key there can be are the widest that make a difference)
   window = std::min(window, max_keys);
   sinks = std::min(sinks, max_keys);
-  int n = fa::plan_paged(T, R, Hq, Hkv, d, fp8 ? 1 : 0, max_new, max_keys, window, sinks, kMaxSms, p);
+  int n = fa::plan_paged(T, R, Hq, Hkv, d, fp8 ? 1 : 0, max_new, page_size, max_keys, window, sinks, kMaxSms, p);
   for (int i = 0; i < n; ++i)
     if (fa::most_blocks(T, R, Hkv, p[i].tpt, max_keys) >= (double)INT32_MAX) return FA_ERR_INVALID_ARG;
   fa::PagedArgs a;
@@ -211,7 +211,7 @@ int fwd_paged(const void* q, long long q_stride, const void* k_cache, const void
   a.window = window;
   a.sinks = sinks;
   a.test_fault = fa::take_test_fault();
-  n = fa::plan_paged(T, R, Hq, Hkv, d, a.fp8, max_new, a.max_keys, window, sinks, std::min(sms, kMaxSms), p);
+  n = fa::plan_paged(T, R, Hq, Hkv, d, a.fp8, max_new, page_size, a.max_keys, window, sinks, std::min(sms, kMaxSms), p);
   for (int i = 0; i < n; ++i) {
     a.most = (int)fa::most_blocks(T, R, Hkv, p[i].tpt, max_keys);
     if (fa::launch_paged(a, p[i], workspace, static_cast<cudaStream_t>(stream)) != cudaSuccess) return FA_ERR_LAUNCH;

@@ -80,17 +80,17 @@ static_assert(sizeof(CBars) <= 1024, "barriers exceed their shared memory");
 // Key blocks that each 128-row half sees of a piece (nb[t] from p.jb on).
 template <int kTiles, bool WIN>
 __device__ __forceinline__ void half_blocks(const PagedArgs& a, const Piece& p, int (&nb)[2]) {
-  const int skip = WIN ? band_of(a, p.q, p.tok).skip : 0;
+  const int gap = WIN ? band_of(a, p.q, p.tok).gap : 0;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     const int tok = p.tok + t * a.tpt1;
-    const int blocks = t < kTiles && tok < p.q.n ? ((keys_seen(a, p.q, tok + a.tpt1) + 127) >> 7) - skip : 0;
+    const int blocks = t < kTiles && tok < p.q.n ? (max(keys_seen(a, p.q, tok + a.tpt1) - gap, 0) + 127) >> 7 : 0;
     nb[t] = max(0, min(blocks, p.je) - p.jb);
   }
 }
 
-// WIN (with CAUSAL): a token sees its last a.window keys and the first a.sinks; j counts the blocks of a tile's Band, which
-// both halves stream (the second's window begins a block later at most once in 128 / tpt1 tiles).
+// WIN (with CAUSAL): a token sees its last a.window keys and the first a.sinks; keys are counted without a tile's gap (Band),
+// which is that of both halves (the second's window begins a block later at most once in 128 / tpt1 tiles).
 template <int D, bool FP8, bool CAUSAL, bool WIN = false>
 __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPerSm)
     fa_paged_chunk_kernel(const __grid_constant__ PagedArgs a) {
@@ -201,20 +201,18 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
       blocks[1] = next_nb[1];
       note_piece(a, parts, p, walk, bars.range.per);
       const int nbm = max(blocks[0], blocks[1]);
-      Pages pages;
+      Pages<WIN> pages;
       Band band{};
       if (WIN) band = band_of(a, p.q, p.tok);
-      if (nbm > 0) pages.begin(a, p, band.at(p.jb), lane);
+      if (nbm > 0) pages.begin(a, p, band, lane);
       if (blocks[0] > 0) load_q(0);
       for (int j = 0; ok && j < max(nbm, 1); ++j) {
         if (nbm > 0) {
-          const int jj = band.at(p.jb + j);
-          if (WIN && j > 0 && p.jb + j == band.sunk) pages.begin(a, p, jj, lane);
-          const int page_now = pages.of(a, p, jj, lane);
+          const int jj = p.jb + j, page_now = pages.of(a, p, jj, lane);
           const int sk = g % C::kKStages;
           if (!(ok = warp_wait(&bars.k_empty[sk], ((g / C::kKStages) & 1) ^ 1, abort_flag))) break;
           load_block<D, FP8, WIN>(a, p, jj, page_now, lane, &a.tm_k, smem + C::kOffK + sk * C::kKBytes, &bars.k_full[sk],
-                                  band.low);
+                                  p.q.len - band.gap, band.low);
           nk = g + 1;
           if (C::kTiles == 2 && j == 0 && blocks[1] > 0) {
             load_q(1);
@@ -224,7 +222,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
           if (!(ok = warp_wait(&v_empty[sv], ((g / kS) & 1) ^ 1, abort_flag))) break;
           load_block<D, FP8, WIN>(a, p, jj, page_now, lane, &a.tm_v,
                                   smem + (FP8 ? C::kOffC + sv * C::kCodeBytes : C::kOffV + sv * C::kTileBytes), &v_full[sv],
-                                  band.low);
+                                  p.q.len - band.gap, band.low);
           nv = ++g;
         }
         if (j == 0) step();  // while those are on their way
@@ -291,7 +289,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
                           j < blocks[0] ? (np[0] & 1) : ph, k_next ? &bars.k_full[sn] : &bars.v_full[s],
                           k_next ? ((g + 1) / C::kKStages) & 1 : ph, abort_flag);
           if (!ok) break;
-          const int keys = p.q.len - band.at(p.jb + j) * 128, steps = pv_steps(keys);
+          const int keys = p.q.len - band.gap - (p.jb + j) * 128, steps = pv_steps(keys);
           if (!FP8 && keys < steps * 16) zero_rows<D>(smem + C::kOffV + s * C::kTileBytes, keys, steps * 16, lane);
           for (int t = 0; t < 2; ++t) {
             if (j < blocks[t]) {
@@ -336,7 +334,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
           ok = warp_wait2(&bars.p_full[0], g & 1, &bars.v_full[s], (g / C::kVStages) & 1, abort_flag);
           if (ok && j == 0) ok = warp_wait(&bars.o_free[0], (nq[0] & 1) ^ 1, abort_flag);
           if (!ok) break;
-          const int keys = p.q.len - band.at(p.jb + j) * 128, steps = pv_steps(keys);
+          const int keys = p.q.len - band.gap - (p.jb + j) * 128, steps = pv_steps(keys);
           if (keys < steps * 16) zero_rows<D>(smem + C::kOffV + s * C::kTileBytes, keys, steps * 16, lane);
           tc_fence_after();
           if (elect_one()) {
@@ -367,7 +365,7 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
         ok = warp_wait2(&bars.c_full[cs], (g / kCS) & 1, &bars.v_empty[vs], ((g / C::kVStages) & 1) ^ 1, abort_flag);
         if (!ok) break;
         convert_tile<D, 32 * C::kConvWarps>(smem + C::kOffC + cs * C::kCodeBytes, smem + C::kOffV + vs * C::kTileBytes,
-                                            p.q.len - band.at(p.jb + j) * 128, tid);
+                                            p.q.len - band.gap - (p.jb + j) * 128, tid);
         conv_arrive(&bars.v_full[vs], &bars.c_empty[cs], lane);
       }
     }
@@ -387,14 +385,12 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
     for (bool more = first || next_piece(); ok && more; more = next_piece()) {
       const int nb = t ? blocks[1] : blocks[0];
       const int tok0 = p.tok + t * a.tpt1, tok = tok0 + rt;
-      const int off = p.q.len - p.q.n;  // causal: token i sees keys 0 .. i + off
-      const bool valid = rt < a.tpt1 && tok < p.q.n;
       Band band{};
-      int out_last = 0;  // window: the last key that is behind the window of this half's last token
-      if (WIN) {
-        band = band_of(a, p.q, p.tok);
-        out_last = min(tok0 + a.tpt1, p.q.n) - 1 + off - band.wide;
-      }
+      if (WIN) band = band_of(a, p.q, p.tok);
+      const int len = p.q.len - band.gap, off = len - p.q.n;  // causal: token i sees keys 0 .. i + off
+      const bool valid = rt < a.tpt1 && tok < p.q.n;
+      // window: the last key that is behind the window of this half's last token
+      const int out_last = WIN ? min(tok0 + a.tpt1, p.q.n) - 1 + off - band.wide : 0;
       float sl2 = a.scale_log2;
       if (FP8 && nb > 0) {  // this thread's row of Q to its two 8-bit parts
         if (!(ok = __all_sync(0xffffffffu, mbar_wait(&bars.q_raw[t], nq & 1, abort_flag)))) break;
@@ -420,9 +416,9 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
         }
         float mx = fmax3(fmax3(cmax[0], cmax[1], cmax[2]), cmax[3], -INFINITY);
         // only blocks that reach past the first row's last key, or past the request's, need masking
-        const int kv0 = band.at(p.jb + j) * 128;
-        if ((CAUSAL && kv0 + 127 > tok0 + off) || kv0 + 128 > p.q.len || (WIN && kv0 <= out_last && kv0 + 128 > a.sinks)) {
-          const int lim = (CAUSAL ? min(tok + off, p.q.len - 1) : p.q.len - 1) - kv0;  // keep column c iff c <= lim
+        const int kv0 = (p.jb + j) * 128;
+        if ((CAUSAL && kv0 + 127 > tok0 + off) || kv0 + 128 > len || (WIN && kv0 <= out_last && kv0 + 128 > a.sinks)) {
+          const int lim = (CAUSAL ? min(tok + off, len - 1) : len - 1) - kv0;  // keep column c iff c <= lim
           const int out = lim - band.wide, sunk = a.sinks - kv0;  // window: hidden too are columns up to 'out', from 'sunk' on
 #pragma unroll
           for (int c = 0; c < 128; ++c)

@@ -74,7 +74,7 @@ struct FBars {
 };
 static_assert(sizeof(FBars) <= 672, "barriers exceed their shared memory");
 
-// WIN (with CAUSAL): a token sees its last a.window keys and the first a.sinks; j counts the blocks of a tile's Band.
+// WIN (with CAUSAL): a token sees its last a.window keys and the first a.sinks; keys are counted without a tile's gap (Band).
 template <int D, bool FP8, bool CAUSAL, bool WIN = false>
 __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel(const __grid_constant__ PagedArgs a) {
   using C = FCfg<D, FP8>;
@@ -159,19 +159,17 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     for (Piece next = p; ok && more; p = next) {
       note_piece(a, parts, p, walk, per);
       const int nb = p.je - p.jb;
-      Pages pages;
+      Pages<WIN> pages;
       Band band{};
       if (WIN) band = band_of(a, p.q, p.tok);
-      if (nb > 0) pages.begin(a, p, band.at(p.jb), lane);
+      if (nb > 0) pages.begin(a, p, band, lane);
       for (int j = 0; j < max(nb, 1); ++j) {
         if (nb > 0) {
-          const int jj = band.at(p.jb + j);
-          if (WIN && j > 0 && p.jb + j == band.sunk) pages.begin(a, p, jj, lane);
-          const int page_now = pages.of(a, p, jj, lane);
+          const int jj = p.jb + j, page_now = pages.of(a, p, jj, lane);
           const int s = g % C::kKStages;
           if (!(ok = warp_wait(&bars.k_empty[s], ((g / C::kKStages) & 1) ^ 1, abort_flag))) break;
           load_block<D, FP8, WIN>(a, p, jj, page_now, lane, &a.tm_k, smem + C::kOffK + s * C::kKBytes, &bars.k_full[s],
-                                  band.low);
+                                  p.q.len - band.gap, band.low);
           nk = ++g;
         }
         if (j == 0) {  // before this piece's other blocks: the Q K^T warp looks one piece ahead
@@ -193,18 +191,16 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
     bool ok = true;
     for (bool more = first || in.next(p); ok && more; more = in.next(p)) {
       if (p.jb == p.je) continue;
-      Pages pages;
+      Pages<WIN> pages;
       Band band{};
       if (WIN) band = band_of(a, p.q, p.tok);
-      pages.begin(a, p, band.at(p.jb), lane);
-      for (int j = p.jb; j < p.je; ++j, ++g) {
-        const int jj = band.at(j);
-        if (WIN && j > p.jb && j == band.sunk) pages.begin(a, p, jj, lane);
+      pages.begin(a, p, band, lane);
+      for (int jj = p.jb; jj < p.je; ++jj, ++g) {
         const int page_now = pages.of(a, p, jj, lane), s = g % kS;
         if (!(ok = warp_wait(&empty[s], ((g / kS) & 1) ^ 1, abort_flag))) break;
         load_block<D, FP8, WIN>(a, p, jj, page_now, lane, &a.tm_v,
                                 smem + (FP8 ? C::kOffC + s * C::kCodeBytes : C::kOffV + s * C::kTileBytes), &full[s],
-                                band.low);
+                                p.q.len - band.gap, band.low);
         nv = g + 1;
       }
     }
@@ -283,7 +279,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
         if (!(ok = warp_wait2(&bars.v_full[s], (g / C::kVStages) & 1, &bars.p_full[b], (g >> 1) & 1, abort_flag))) break;
         // a tile's first P V overwrites O: the tile before has been read out
         if (jj == p.jb && !(ok = warp_wait(&bars.o_free, (n & 1) ^ 1, abort_flag))) break;
-        const int keys = p.q.len - band.at(jj) * 128, steps = pv_steps(keys);
+        const int keys = p.q.len - band.gap - jj * 128, steps = pv_steps(keys);
         if (!FP8 && keys < steps * 16) zero_rows<D>(smem + C::kOffV + s * C::kTileBytes, keys, steps * 16, lane);
         tc_fence_after();
         if (elect_one()) {
@@ -319,7 +315,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
         ok = warp_wait2(&bars.c_full[cs], (g / kCS) & 1, &bars.v_empty[vs], ((g / C::kVStages) & 1) ^ 1, abort_flag);
         if (!ok) break;
         convert_tile<D, 32 * C::kConvWarps>(smem + C::kOffC + cs * C::kCodeBytes, smem + C::kOffV + vs * C::kTileBytes,
-                                            p.q.len - band.at(j) * 128, tid);
+                                            p.q.len - band.gap - j * 128, tid);
         conv_arrive(&bars.v_full[vs], &bars.c_empty[cs], lane);
       }
     }
@@ -349,16 +345,14 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
         sl2 *= unscale(q_ex[n % 3][lane]);
         ++n;
       }
-      const int off = p.q.len - p.q.n;  // causal: token i sees keys 0 .. i + off
-      const int lim_row = (CAUSAL ? min(p.tok + rt + off, p.q.len - 1) : p.q.len - 1) - warp * 32;
-      const int lim_first = (CAUSAL ? min(p.tok + off, p.q.len - 1) : p.q.len - 1) - warp * 32;
-      const int rows = min(a.tpt, p.q.n - p.tok) * G;
       Band band{};
-      int out_last = 0;  // window: the last key, of this warp's, that is behind the last token's
-      if (WIN) {
-        band = band_of(a, p.q, p.tok);
-        out_last = min(p.tok + a.tpt, p.q.n) - 1 + off - band.wide - warp * 32;
-      }
+      if (WIN) band = band_of(a, p.q, p.tok);
+      const int len = p.q.len - band.gap, off = len - p.q.n;  // causal: token i sees keys 0 .. i + off
+      const int lim_row = (CAUSAL ? min(p.tok + rt + off, len - 1) : len - 1) - warp * 32;
+      const int lim_first = (CAUSAL ? min(p.tok + off, len - 1) : len - 1) - warp * 32;
+      const int rows = min(a.tpt, p.q.n - p.tok) * G;
+      // window: the last key, of this warp's, that is behind the last token's
+      const int out_last = WIN ? min(p.tok + a.tpt, p.q.n) - 1 + off - band.wide - warp * 32 : 0;
       float m_ref = -INFINITY;  // exponent reference, log2 units of scaled scores
       float l_sum = 0.f;        // sum of 2^(s * sl2 - m_ref) over this warp's keys so far
       for (int j = 0; ok && j < nb; ++j, ++g) {
@@ -373,7 +367,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
         tmem_ld_wait(sr, mx);
         tc_fence_before();
         mbar_arrive(&bars.s_free[b]);  // S is in registers: the block after the next may overwrite it
-        const int kv0 = band.at(p.jb + j) * 128;
+        const int kv0 = (p.jb + j) * 128;
         if (kv0 + 31 > lim_first || (WIN && kv0 <= out_last)) {  // some row does not see all of these keys
           const int lim = lim_row - kv0;
           const int out = lim - band.wide, sunk = a.sinks - warp * 32 - kv0;  // hidden too: keys up to 'out', from 'sunk' on

@@ -188,7 +188,8 @@ namespace {
 // 87.4 and 84.7 us (E4M3 93.9 and 93.5 us); at 16 blocks 4 requests of up to 1500 keys 12.0 and 13.5 us.
 constexpr int kWholeBlocks = 8;
 
-PagedPlan plan_kernel(bool few, int G, int d, int fp8, int max_new, int max_keys, int window, int sinks, int num_sms) {
+PagedPlan plan_kernel(bool few, int G, int d, int fp8, int max_new, int page_size, int max_keys, int window, int sinks,
+                      int num_sms) {
   PagedPlan p;
   p.few = few;
   const int halves = few || (d == 64 && !fp8) ? 1 : 2;
@@ -199,8 +200,10 @@ PagedPlan plan_kernel(bool few, int G, int d, int fp8, int max_new, int max_keys
   // four blocks (eight prompts of up to 1024 tokens, 12 heads of 64, when it was chosen: 44 us with every cut, 35 us). The
   // decoding kernel's parts are a few rows: there only a call without any cut is worth it.
   int blocks = (max_keys >> 7) + (max_keys % 128 != 0);  // of the longest request there can be
-  if (window)  // a tile's sinks, and the window of all its tokens, which may begin anywhere in a block
-    blocks = (int)std::min<long long>(blocks, (sinks + 127ll) / 128 + (window + p.tpt + 126ll) / 128 + 1);
+  if (window) {  // a tile's sinks in whole pages, and the window of all its tokens, which may begin anywhere in a page
+    const long long ps = page_size, keys = (sinks + ps - 1) / ps * ps + window + p.tpt - 1 + ps - 1;
+    blocks = (int)std::min<long long>(blocks, (keys + 127) / 128);
+  }
   p.whole = few && blocks > kWholeBlocks ? 0 : kWholeBlocks;
   p.join = blocks > p.whole;
   p.snap = few ? 0 : 4;
@@ -214,11 +217,11 @@ PagedPlan plan_kernel(bool few, int G, int d, int fp8, int max_new, int max_keys
 }
 }  // namespace
 
-int plan_paged(int T, int R, int Hq, int Hkv, int d, int fp8, int max_new, int max_keys, int window, int sinks, int num_sms,
-               PagedPlan (&p)[2]) {
+int plan_paged(int T, int R, int Hq, int Hkv, int d, int fp8, int max_new, int page_size, int max_keys, int window, int sinks,
+               int num_sms, PagedPlan (&p)[2]) {
   const int G = Hq / Hkv;
   auto plan_kernel = [&](bool few, int new_tokens) {
-    return fa::plan_kernel(few, G, d, fp8, new_tokens, max_keys, window, sinks, num_sms);
+    return fa::plan_kernel(few, G, d, fp8, new_tokens, page_size, max_keys, window, sinks, num_sms);
   };
   // no request has more than 32 rows per key head: the decoding kernel alone
   if ((long long)G * max_new <= 32) {

@@ -18,13 +18,21 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units: how far the exponent r
 // A request's block table as one warp reads it: 32 entries in the lanes'
 // registers and the next 32 on their way, so that no key block waits for a load
 // from the table (one block ahead, each took 950 cycles to issue).
+// (WIN: entry i of the tile's own row of pages, its Band.)
+template <bool WIN>
 struct Pages {
   int base, now, next;  // entries base + lane and base + 32 + lane
+  int sunk, skip;
   __device__ __forceinline__ int entry(const PagedArgs& a, const Piece& p, int i) const {
-    return i <= (p.q.len - 1) >> a.page_shift ? a.block_table[(long long)p.r * a.max_pages + i] : -1;
+    const int at = WIN && i >= sunk ? i + skip : i;
+    return at <= (p.q.len - 1) >> a.page_shift ? a.block_table[(long long)p.r * a.max_pages + at] : -1;
   }
-  __device__ __forceinline__ void begin(const PagedArgs& a, const Piece& p, int jj, int lane) {  // jj: the first block
-    base = ((jj * 128) >> a.page_shift) & ~31;
+  __device__ __forceinline__ void begin(const PagedArgs& a, const Piece& p, const Band& band, int lane) {
+    if (WIN) {
+      sunk = band.sunk;
+      skip = band.skip;
+    }
+    base = ((p.jb * 128) >> a.page_shift) & ~31;
     now = entry(a, p, base + lane);
     next = entry(a, p, base + 32 + lane);
   }
@@ -63,12 +71,12 @@ struct Tile {
 // cache reads as zeros: its copy lies past the tensor map's end. (A copy may
 // complete before lane 0 has said how many bytes are to come: the phase waits
 // for that arrival.)
-// Under a window (low: its first key) pages of which the tile sees no key read as zeros too, whatever the table says there:
-// they may have been given to others.
-template <int D, bool FP8, bool WIN = false>
+// len: the request's keys, less its band's gap under a window, where halves of a page of which the tile sees no key read as
+// zeros too.
+template <int D, bool FP8, bool WIN>
 __device__ __forceinline__ void load_block(const PagedArgs& a, const Piece& p, int jj, int page, int lane,
-                                           const CUtensorMap* tm, uint8_t* dst, uint64_t* bar, int low = 0) {
-  const int shift = min(a.page_shift, 7), rows = min(128, p.q.len - jj * 128);
+                                           const CUtensorMap* tm, uint8_t* dst, uint64_t* bar, int len, int low) {
+  const int shift = min(a.page_shift, 7), rows = min(128, len - jj * 128);
   const int n = (rows + (1 << shift) - 1) >> shift;  // pages with keys
   if (lane < n) {
     constexpr int kRow = D * (FP8 ? 1 : 2);

@@ -65,27 +65,34 @@ __host__ __device__ __forceinline__ int keys_seen(const PagedArgs& a, const Requ
   return a.causal ? max(q.len - q.n + min(upto, q.n), 0) : q.len;
 }
 
-// The key blocks that a tile whose first token is 'tok' streams under a window: those that hold any of the first a.sinks keys,
-// up to the window's first block, and from that on. Its j-th block is the request's block at(j).
+// What a tile whose first token is 'tok' streams under a window: the request's pages that hold any of the first a.sinks keys,
+// then those from its window's first key on, one after another as if there were none between them. So blocks of 128 keys hold
+// 128 keys that count: 128 requests, window 500, 4 sinks, 16 heads over 8 of 64 49.5 us where the sinks had a block of their
+// own, 46 us so; three chunks of 1024 tokens, window 2000, 130 sinks, E4M3 117 and 111 us. Keys and positions are those of the
+// request with 'gap' fewer.
 struct Band {
-  int sunk, skip;  // blocks before the window's; blocks between them and it that nobody sees
-  int low;         // the first key of the window of the first token
+  int sunk, skip;  // pages of the sinks before the window's; pages between them and it that nobody sees
+  int gap;         // keys of those
+  int low;         // the first key of the window of the first token, less the gap
   int wide;        // the window, no wider than the request (places behind it stay within 32 bits)
-  __host__ __device__ __forceinline__ int at(int j) const { return j < sunk ? j : j + skip; }
 };
 __host__ __device__ __forceinline__ Band band_of(const PagedArgs& a, const Request& q, int tok) {
   Band b;
   b.wide = min(a.window, q.len);
   b.low = max(q.len - q.n + tok - b.wide + 1, 0);
-  b.sunk = min((int)(((unsigned)a.sinks + 127u) >> 7), b.low >> 7);
-  b.skip = (b.low >> 7) - b.sunk;
+  const int page = b.low >> a.page_shift;
+  b.sunk = min((int)(((unsigned)a.sinks + (1u << a.page_shift) - 1u) >> a.page_shift), page);
+  b.skip = page - b.sunk;
+  b.gap = b.skip << a.page_shift;
+  b.low -= b.gap;
   return b;
 }
 
-// Keys that tiles under a window count for at most, in sum: a tile's tokens, its window, the sinks in whole blocks and half
-// a block where the window begins. (Lengths only say how the work is dealt out.)
+// Keys that tiles under a window count for at most, in sum: a tile's tokens, its window, the sinks in whole pages and half
+// a page where the window begins. (Lengths only say how the work is dealt out.)
 __host__ __device__ __forceinline__ long long band_keys(const PagedArgs& a, const Request& q, int i) {
-  const long long cap = (long long)((a.sinks + 127ll) & ~127ll) + a.window + a.tpt + 64, base = max(q.len - q.n, 0);
+  const long long ps = 1ll << a.page_shift, base = max(q.len - q.n, 0);
+  const long long cap = (a.sinks + ps - 1) / ps * ps + a.window + a.tpt + ps / 2;
   const long long all = (cap - base) / a.tpt, whole = all < 0 ? 0 : all < i ? all : i;  // tiles that see less than that
   return whole * base + whole * (whole + 1) / 2 * a.tpt + (i - whole) * cap;
 }
@@ -145,8 +152,9 @@ __device__ __forceinline__ bool cut(const PagedArgs& a, const Request& q, int i,
                                     Piece& p) {
   p.q = q;
   p.tok = i * a.tpt;
-  p.nb = (keys_seen(a, q, p.tok + a.tpt) + 127) >> 7;
-  if (WIN && p.nb) p.nb -= band_of(a, q, p.tok).skip;
+  int keys = keys_seen(a, q, p.tok + a.tpt);
+  if (WIN && keys) keys -= band_of(a, q, p.tok).gap;
+  p.nb = (keys + 127) >> 7;
   if (p.nb <= a.whole) {
     p.jb = 0;
     p.je = p.nb;

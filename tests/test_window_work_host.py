@@ -16,12 +16,12 @@ int main() {
   Request q{};
   int tile;
   a.causal = 1;
-  while (scanf("%d %d %d %d %d %d", &a.window, &a.sinks, &a.tpt, &q.n, &q.len, &tile) == 6) {
+  while (scanf("%d %d %d %d %d %d %d", &a.window, &a.sinks, &a.tpt, &q.n, &q.len, &tile, &a.page_shift) == 7) {
     const int nt = (q.n + a.tpt - 1) / a.tpt;
     const Band b = band_of(a, q, tile * a.tpt);
-    int nb = (keys_seen(a, q, (tile + 1) * a.tpt) + 127) >> 7;
-    if (nb) nb -= b.skip;
-    printf("%d %d %d %d %d %d\n", b.sunk, b.skip, b.low, nb, tiles_len<true>(a, q, tile, nt), tiles_len<true>(a, q, tile + 1, nt));
+    int keys = keys_seen(a, q, (tile + 1) * a.tpt);
+    if (keys) keys -= b.gap;
+    printf("%d %d %d %d %d %d %d\n", b.sunk, b.skip, b.gap, b.low, keys, tiles_len<true>(a, q, tile, nt), tiles_len<true>(a, q, tile + 1, nt));
   }
   return 0;
 }
@@ -48,23 +48,27 @@ def test_bands_hold_what_the_tokens_see(bands):
         tpt, n = rng.choice([1, 2, 4, 8, 25, 32, 64, 128, 256]), rng.choice([1, 2, 31, 33, 127, rng.randint(1, 600)])
         length = rng.choice([0, 1, n - 1, n, n + 1, n + rng.randint(0, 3000), rng.randint(0, n)])
         window, sinks = rng.choice([1, 2, 127, 128, 129, rng.randint(1, 2000), 10 ** 9]), rng.choice([0, 1, 4, 127, 128, 129, 400])
-        cases.append((window, sinks, tpt, n, length, rng.randrange(-(-n // tpt))))
-    for c, (sunk, skip, low, nb, before, after) in zip(cases, bands(cases)):
-        window, sinks, tpt, n, length, tile = c
-        at = [j if j < sunk else j + skip for j in range(nb)]
-        assert at == sorted(set(at)), c
-        seen, lowest = set(), None
+        cases.append((window, sinks, tpt, n, length, rng.randrange(-(-n // tpt)), rng.choice([4, 5, 6, 7, 8])))
+    for c, (sunk, skip, gap, low, keys, before, after) in zip(cases, bands(cases)):
+        window, sinks, tpt, n, length, tile, shift = c
+        ps = 1 << shift
+        assert gap == skip * ps
+        at = [x if x < sunk * ps else x + gap for x in range(keys)]  # the request's key that stands in each place
+        seen = set()
         for i in range(tile * tpt, min(n, (tile + 1) * tpt)):
             p = length - n + i
-            if p >= 0:
-                seen |= {j // 128 for j in range(max(0, p - window + 1), p + 1)} | {j // 128 for j in range(min(sinks, p + 1))}
-                lowest = max(0, p - window + 1) if lowest is None else min(lowest, max(0, p - window + 1))
+            mine = {j for j in range(p + 1) if p - j < window or j < sinks}
+            seen |= mine
+            if i in (tile * tpt, min(n, (tile + 1) * tpt) - 1):  # the kernels' rule, in places
+                assert {x for x in range(keys) if x <= p - gap and not (x <= p - gap - min(window, length) and x >= sinks)} == \
+                    {x for x, j in enumerate(at) if j in mine}, c
         assert seen <= set(at), c
-        if lowest is not None and length - n + tile * tpt >= 0:  # (else the first token sees no key)
-            assert low == lowest and (set(at) <= seen), c
-        if at:  # the bound by which calls without any cut are chosen
-            assert nb <= -(-sinks // 128) + (window + tpt + 126) // 128 + 1, c
-        assert 2 <= after - before <= nb + 5, c
+        if length - n + tile * tpt >= 0:  # (else the first token sees no key)
+            first = max(0, length - n + tile * tpt - window + 1)
+            assert low == first - gap and {j // ps for j in at} == {j // ps for j in seen}, c
+        # the bound by which calls without any cut are chosen
+        assert keys <= -(-sinks // ps) * ps + window + tpt + ps - 2, c
+        assert 2 <= after - before <= -(-keys // 128) + 5, c
 
 
 def test_widths_near_32_bits(bands):
@@ -72,8 +76,7 @@ def test_widths_near_32_bits(bands):
     big = 2 ** 31 - 512
     for n, length in ((1, big), (4000, big), (1 << 20, 0), (1 << 20, 5), (1, 1)):
         for window in (1, 1000, big):
-            (sunk, skip, low, nb, before, after), = bands([(window, big, 32, n, length, 0)])
-            p = length - n
-            w = min(window, length)
-            assert low == max(p - w + 1, 0) and skip == 0 and sunk == low // 128, (n, length, window)
+            (sunk, skip, gap, low, keys, before, after), = bands([(window, big, 32, n, length, 0, 7)])
+            first = max(length - n - min(window, length) + 1, 0)
+            assert low == first and skip == gap == 0 and sunk == first // 128, (n, length, window)
             assert after - before >= 2
