@@ -227,6 +227,9 @@ int bwd_common(const void* q, const void* k, const void* v, const void* o, const
   a.window = window;
   a.sinks = sinks;
   a.group = H / Hkv;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
   return fa::launch_bwd(a, di->num_sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 

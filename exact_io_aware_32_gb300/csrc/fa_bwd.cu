@@ -160,6 +160,14 @@ __device__ __forceinline__ uint32_t dkdv_pcol(int kk, bool ds) {
 // k-step of the i-th of the four 16-query steps in query half h: {0, 1, 4, 5} or {2, 3, 6, 7}.
 __device__ __forceinline__ constexpr int dkdv_half_kstep(int h, int i) { return 4 * (i >> 1) + 2 * h + (i & 1); }
 
+// Zeros rows [row, row + 128) of a head's gradient of 'rows' rows (padding, or keys that no row sees), by one warp.
+template <int D>
+__device__ __forceinline__ void zero_tile(void* grad, int head, int row, int rows, int lane) {
+  uint4* at = reinterpret_cast<uint4*>(static_cast<uint8_t*>(grad) + ((size_t)head * rows + row) * D * 2);
+  const int n = min(128, rows - row) * (D / 8);
+  for (int i = lane; i < n; i += 32) at[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
 // A dK/dV tile: (head, key block), its first query block and how many it
 // sees, and the sequence's query rows sq and keys sk (padding masks).
 // (WIN: bh is the key head; n counts the nq query blocks from i_start on of each of its a.group query heads in turn.)
@@ -187,10 +195,7 @@ __device__ __forceinline__ DkdvTile dkdv_tile(int L, const BwdArgs& a, int nkv) 
     const int last = key < a.sinks ? t.sq - 1 : min(t.sq - 1, min(key + 127, t.sk - 1) + a.window - 1 - off);
     t.nq = (last >> 7) + 1 - t.i_start;
     t.n = t.nq * a.group;
-    if (key >= t.sk || t.nq <= 0) {  // keys that no row sees: one block, fully masked, gives dk = dv = 0
-      t.i_start = 0;
-      t.nq = t.n = 1;
-    }
+    if (key >= t.sk || t.nq <= 0) t.n = 0;  // keys that no row sees: dk = dv = 0 (the loading warp's work)
     return t;
   }
   grouped_index(L, a.BH, nkv, a.head_group, t.bh, t.kblk);  // key block 0 (the heaviest) first
@@ -338,15 +343,21 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dkdv_kernel(const __grid_consta
       const int is = k % C::kItemSlots;
       if (!warp_wait(&bars.item_empty[is], ((k / C::kItemSlots) & 1) ^ 1, abort_flag)) break;
       int L = 0;
-      if (lane == 0) {
-        L = (int)atomicAdd(&a.work[0], 1u);
-        bars.item[is] = L;
+      DkdvTile t;
+      for (;;) {
+        if (lane == 0) {
+          L = (int)atomicAdd(&a.work[0], 1u);
+          bars.item[is] = L;
+        }
+        L = __shfl_sync(0xffffffffu, L, 0);
+        __syncwarp();
+        if (L < total) t = dkdv_tile<CAUSAL, VARLEN, WIN>(L, a, nkv);
+        if (!WIN || L >= total || t.n > 0) break;
+        zero_tile<D>(a.dk, t.bh, t.kblk * 128, a.Nk, lane);  // and take another
+        zero_tile<D>(a.dv, t.bh, t.kblk * 128, a.Nk, lane);
       }
-      L = __shfl_sync(0xffffffffu, L, 0);
-      __syncwarp();
       if (lane == 0) mbar_arrive(&bars.item_full[is]);  // release: the tile index is visible
       if (L >= total) break;
-      const DkdvTile t = dkdv_tile<CAUSAL, VARLEN, WIN>(L, a, nkv);
       bars.st_bh[k & 7] = t.bh;  // every lane writes the same values
       bars.st_kblk[k & 7] = t.kblk;
       bars.st_last[k & 7] = g + t.n - 1;
@@ -663,10 +674,20 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dkdv_kernel(const __grid_consta
           if ((CAUSAL && q0 + off < (t.kblk + 1) * C::BK - 1) || !keys_all_ok ||
               (WIN && q0 + C::BQ - 1 + off - t.kblk * C::BK >= a.window && (t.kblk + 1) * C::BK > a.sinks)) {
             const int lim = CAUSAL ? key - off - (q0 + 64 * w) : -1;  // drop columns col < lim
-            const int far = WIN ? (key < a.sinks ? 64 : lim + a.window) : 0;  // window: and col >= far
+            if constexpr (WIN) {
+              const int far = !key_ok ? 0 : key < a.sinks ? 64 : lim + a.window;  // and col >= far: bits, one test a column
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (c < lim || !key_ok || (WIN && c >= far)) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t keep = first_bits(far - 32 * h) & ~first_bits(lim - 32 * h);
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  if (!(keep >> c & 1u)) sr[h][c] = __float_as_uint(-INFINITY);
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < 64; ++c)
+                if (c < lim || !key_ok) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+            }
           }
           const float2 scale2 = make_float2(sl2, sl2);
 #pragma unroll
@@ -794,7 +815,7 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dkdv_kernel(const __grid_consta
 // count key blocks over the CTA's whole run, the MMA warp issues S and dP of
 // the next tile's first block while the warpgroups write the previous tile's
 // dQ, and the next tile's Q is loaded while the current one is processed.
-template <int D>
+template <int D, bool WIN = false>
 struct DqCfg {
   static constexpr int BQ = 128;  // queries per tile
   static constexpr int BK = 128;  // keys per iteration
@@ -802,16 +823,21 @@ struct DqCfg {
   static constexpr int kKStages = D == 128 ? 3 : 4;
   static constexpr int kVStages = D == 128 ? 2 : 3;
   static constexpr int kItemSlots = 4;  // tiles fetched ahead by the producer
-  // D = 64: an O tile beside dO, from which the warpgroups form D for the tile
-  static constexpr bool kFuseD = D == 64;
+  // The warpgroups form D for the tile: at d = 64 from an O tile beside dO, under a window at d = 128 from O's rows in global
+  // memory (there is no room for a tile of them), read a tile ahead. Under a window the groups take half a row each, and the
+  // halves are added up in shared memory.
+  static constexpr bool kFuseD = D == 64 || WIN, kTileO = D == 64, kHalves = WIN;
+  // Places for dO and O: under a window a tile has few blocks, and at d = 64 the next one's come while it runs.
+  static constexpr int kDOStages = D == 64 && WIN ? 2 : 1;
   static constexpr int kOffQ = 0;
   static constexpr int kOffDO = kTileBytes;
-  static constexpr int kOffO = 2 * kTileBytes;  // (kFuseD only)
-  static constexpr int kOffK = (kFuseD ? 3 : 2) * kTileBytes;
-  static_assert(!kFuseD || kOffO + kTileBytes <= kOffK, "the O tile overlaps the K ring");
+  static constexpr int kOffO = kOffDO + kDOStages * kTileBytes;  // (kTileO only)
+  static constexpr int kOffK = kOffO + (kTileO ? kDOStages * kTileBytes : 0);
   static constexpr int kOffV = kOffK + kKStages * kTileBytes;
   static constexpr int kOffBar = kOffV + kVStages * kTileBytes;
-  static constexpr int kSmemBytes = kOffBar + 512 + 1024;
+  static constexpr int kOffHalf = kOffBar + 512;  // (kHalves) halves of D, fp32 [2][128]
+  static constexpr int kSmemBytes = kOffHalf + (kHalves ? 1024 : 0) + 1024;
+  static_assert(kSmemBytes <= 232448, "shared memory");
   static constexpr uint32_t kColQ = 0;            // Q, bf16 pairs, D / 2 columns
   static constexpr uint32_t kColDS = D / 2;       // dS, bf16 pairs, 64 columns (warpgroup w: [32 w, 32 w + 32))
   static constexpr uint32_t kColS = D / 2 + 64;   // S fp32, 128 columns
@@ -822,9 +848,10 @@ struct DqCfg {
 struct DqBarriers {
   uint64_t item_full[4], item_empty[4];  // tile ring: producer -> MMA warp and warpgroups
   uint64_t q_full, qt_ready;             // Q buffer (one tile) loaded; Q copied into TMEM
-  uint64_t do_full, do_empty;            // dO buffer (one tile; with kFuseD also the O buffer)
+  uint64_t do_full[2], do_empty[2];      // dO buffer (one tile, or two in turn; with kTileO also the O buffer)
   uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
   uint64_t s_full, s_free, dp_full, dp_free, ds_ready, dq_tile, teardown, teardown_q;
+  uint64_t half_ready;                  // (kHalves) both halves of D are in shared memory
   uint64_t ep_staged, dq_stored;        // dQ of a tile staged in the Q buffer; its store has read it
   int item[4];
   uint32_t tmem_base;
@@ -876,6 +903,7 @@ __device__ __forceinline__ DqTile dq_tile(int L, const BwdArgs& a, int nq) {
   // BQ == BK: query block i sees key blocks 0 .. (128 i + 127 + sk - sq) / 128 (with sq = sk: 0..i);
   // a block of padding rows only takes one key block, whose P = 0 gives dq = 0
   t.nk = VARLEN && t.qblk * 128 >= t.sq ? 1 : CAUSAL ? min((t.qblk * 128 + 127 + t.sk - t.sq) / 128 + 1, nkv) : nkv;
+  if (WIN && t.qblk * 128 >= t.sq) t.nk = 0;  // padding rows alone: dq = 0 (the loading warp's work)
   if (WIN && t.qblk * 128 < t.sq) {
     const int low = max(t.qblk * 128 + t.sk - t.sq - a.window + 1, 0) / 128;  // the first row's window begins in this block
     t.sunk = min((a.sinks + 127) / 128, low);
@@ -887,7 +915,7 @@ __device__ __forceinline__ DqTile dq_tile(int L, const BwdArgs& a, int nq) {
 
 template <int D, bool CAUSAL, bool VARLEN, bool DROP = false, bool WIN = false>
 __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant__ BwdArgs a) {
-  using C = DqCfg<D>;
+  using C = DqCfg<D, WIN>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   DqBarriers& bars = *reinterpret_cast<DqBarriers*>(smem + C::kOffBar);
@@ -906,9 +934,11 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
     }
     mbar_init(&bars.q_full, 1);
     mbar_init(&bars.qt_ready, 256);
-    mbar_init(&bars.do_full, 1);
-    // the tile's last dP; with kFuseD also every warpgroup thread, once it has formed D
-    mbar_init(&bars.do_empty, C::kFuseD ? 1 + 256 : 1);
+    for (int s = 0; s < C::kDOStages; ++s) {
+      mbar_init(&bars.do_full[s], 1);
+      // the tile's last dP; with kFuseD also every warpgroup thread, once it has formed D
+      mbar_init(&bars.do_empty[s], C::kFuseD ? 1 + 256 : 1);
+    }
     for (int s = 0; s < C::kKStages; ++s) {
       mbar_init(&bars.k_full[s], 1);
       mbar_init(&bars.k_empty[s], 1);
@@ -923,6 +953,7 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
     mbar_init(&bars.dp_free, 256);
     mbar_init(&bars.ds_ready, 256);
     mbar_init(&bars.dq_tile, 1);
+    mbar_init(&bars.half_ready, 256);
     mbar_init(&bars.ep_staged, 256);
     mbar_init(&bars.dq_stored, 1);
     mbar_init(&bars.teardown, 1);
@@ -938,6 +969,9 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
   tc_fence_after();
   const uint32_t tmem = bars.tmem_base;
 
+  // Tile k's place of dO and O, and its use of it.
+  auto do_slot = [](int k) { return C::kDOStages == 2 ? k & 1 : 0; };
+  auto do_use = [](int k) -> uint32_t { return (C::kDOStages == 2 ? k >> 1 : k) & 1; };
   // Tile k of this CTA, as published by the producer in the tile ring; -1
   // (and no further tiles) once the counter is exhausted or on abort. Every
   // consumer warp reads each slot once and releases it.
@@ -990,21 +1024,27 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
     };
     int ntiles = 0;
     bool ok = true;
-    for (int k = 0; ok; ++k) {
+    DqTile t{};
+    // takes the CTA's k-th tile, tells the others and loads its Q; false past the last one (or, ok false, after a failed wait)
+    auto take = [&](int k) -> bool {
       const int is = k % C::kItemSlots;
-      if (!warp_wait(&bars.item_empty[is], ((k / C::kItemSlots) & 1) ^ 1, abort_flag)) break;
+      if (!(ok = warp_wait(&bars.item_empty[is], ((k / C::kItemSlots) & 1) ^ 1, abort_flag))) return false;
       int L = 0;
-      if (lane == 0) {
-        L = (int)atomicAdd(&a.work[1], 1u);
-        bars.item[is] = L;
+      for (;;) {
+        if (lane == 0) {
+          L = (int)atomicAdd(&a.work[1], 1u);
+          bars.item[is] = L;
+        }
+        L = __shfl_sync(0xffffffffu, L, 0);
+        __syncwarp();
+        if (L < total) t = dq_tile<CAUSAL, VARLEN, WIN>(L, a, nq);
+        if (!WIN || L >= total || t.nk > 0) break;
+        zero_tile<D>(a.dq, t.bh, t.qblk * 128, Nq, lane);  // and take another
       }
-      L = __shfl_sync(0xffffffffu, L, 0);
-      __syncwarp();
       if (lane == 0) mbar_arrive(&bars.item_full[is]);  // release: the tile index is visible
-      if (L >= total) break;
-      const DqTile t = dq_tile<CAUSAL, VARLEN, WIN>(L, a, nq);
-      if (k == 1 && !(ok = warp_wait(&bars.qt_ready, 0, abort_flag))) break;
-      if (k >= 2 && !(ok = store_dq(k - 2, false))) break;
+      if (L >= total) return false;
+      if (k == 1 && !(ok = warp_wait(&bars.qt_ready, 0, abort_flag))) return false;
+      if (k >= 2 && !(ok = store_dq(k - 2, false))) return false;
       if (k & 1)
         hist_odd = t;
       else
@@ -1017,27 +1057,36 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
       }
       __syncwarp();
       q_loads = k + 1;
-      const int kv_head = WIN ? t.bh / a.group : t.bh;
-      for (int j = 0; j < t.nk; ++j, ++g) {
+      return true;
+    };
+    bool more = take(0);
+    for (int k = 0; ok && more; ++k) {
+      const DqTile now = t;
+      const int kv_head = WIN ? now.bh / a.group : now.bh;
+      // Under a window the next tile is taken when the rings are full with this one's blocks, not after the last of them: its Q
+      // is then there when this tile ends.
+      const int early = WIN ? min(now.nk, C::kKStages) - 1 : INT_MAX;
+      for (int j = 0; j < now.nk; ++j, ++g) {
         const int sk = g % C::kKStages, sv = g % C::kVStages;
         if (!(ok = warp_wait(&bars.k_empty[sk], ((g / C::kKStages) & 1) ^ 1, abort_flag))) break;
         if (elect_one()) {
           mbar_arrive_expect_tx(&bars.k_full[sk], C::kTileBytes);
           for (int pn = 0; pn < D / 64; ++pn)
             tma_load_3d(smem + C::kOffK + sk * C::kTileBytes + pn * kPanelBytes, &a.tm_k, &bars.k_full[sk],
-                        pn * 64, t.template at<WIN>(j) * C::BK, kv_head);
+                        pn * 64, now.template at<WIN>(j) * C::BK, kv_head);
         }
         __syncwarp();
         k_issued = g + 1;
         if (j == 0) {
-          if (!(ok = warp_wait(&bars.do_empty, (k & 1) ^ 1, abort_flag))) break;
+          const int ds = do_slot(k);
+          if (!(ok = warp_wait(&bars.do_empty[ds], do_use(k) ^ 1, abort_flag))) break;
           if (elect_one()) {
-            mbar_arrive_expect_tx(&bars.do_full, (C::kFuseD ? 2 : 1) * C::kTileBytes);
+            mbar_arrive_expect_tx(&bars.do_full[ds], (C::kTileO ? 2 : 1) * C::kTileBytes);
             for (int pn = 0; pn < D / 64; ++pn)
-              tma_load_3d(smem + C::kOffDO + pn * kPanelBytes, &a.tm_do, &bars.do_full, pn * 64, t.qblk * C::BQ,
-                          t.bh);
-            if constexpr (C::kFuseD)
-              tma_load_3d(smem + C::kOffO, &a.tm_o, &bars.do_full, 0, t.qblk * C::BQ, t.bh);
+              tma_load_3d(smem + C::kOffDO + ds * C::kTileBytes + pn * kPanelBytes, &a.tm_do, &bars.do_full[ds], pn * 64,
+                          now.qblk * C::BQ, now.bh);
+            if constexpr (C::kTileO)
+              tma_load_3d(smem + C::kOffO + ds * C::kTileBytes, &a.tm_o, &bars.do_full[ds], 0, now.qblk * C::BQ, now.bh);
           }
           __syncwarp();
           do_loads = k + 1;
@@ -1047,17 +1096,22 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
           mbar_arrive_expect_tx(&bars.v_full[sv], C::kTileBytes);
           for (int pn = 0; pn < D / 64; ++pn)
             tma_load_3d(smem + C::kOffV + sv * C::kTileBytes + pn * kPanelBytes, &a.tm_v, &bars.v_full[sv],
-                        pn * 64, t.template at<WIN>(j) * C::BK, kv_head);
+                        pn * 64, now.template at<WIN>(j) * C::BK, kv_head);
         }
         __syncwarp();
         v_issued = g + 1;
+        if (j == early) {
+          more = take(k + 1);
+          if (!ok) break;
+        }
       }
+      if (!WIN && ok) more = take(k + 1);
     }
     // the last two tiles' dQ, then every copy still in flight lands before the CTA can exit
     if (ok && ntiles >= 2) ok = store_dq(ntiles - 2, false);
     if (ok && ntiles >= 1) ok = store_dq(ntiles - 1, true);
     if (q_loads > 0) mbar_wait_drain(&bars.q_full, (q_loads - 1) & 1);
-    if (do_loads > 0) mbar_wait_drain(&bars.do_full, (do_loads - 1) & 1);
+    for (int i = max(0, do_loads - C::kDOStages); i < do_loads; ++i) mbar_wait_drain(&bars.do_full[do_slot(i)], do_use(i));
     for (int i = max(0, k_issued - C::kKStages); i < k_issued; ++i)
       mbar_wait_drain(&bars.k_full[i % C::kKStages], (i / C::kKStages) & 1);
     for (int i = max(0, v_issued - C::kVStages); i < v_issued; ++i)
@@ -1123,17 +1177,18 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
           }
           __syncwarp();
         };
-        auto issue_dp = [&](int g, bool last_of_tile) {  // dP = dO V_g^T
+        auto issue_dp = [&](int k, int g, bool last_of_tile) {  // dP = dO V_g^T of tile k
           const int sv = g % C::kVStages;
           tc_fence_after();
           const uint32_t vo = (uint32_t)(sv * C::kTileBytes) >> 4;
           if (elect_one()) {
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)
-              mma_ss(tmem + C::kColDP, ddo0 + koff(kk), dv0 + koff(kk) + vo, kIdKK, kk > 0);
+              mma_ss(tmem + C::kColDP, ddo0 + koff(kk) + ((uint32_t)(do_slot(k) * C::kTileBytes) >> 4), dv0 + koff(kk) + vo, kIdKK,
+                     kk > 0);
             mma_commit(&bars.dp_full);
             mma_commit(&bars.v_empty[sv]);
-            if (last_of_tile) mma_commit(&bars.do_empty);  // the tile's last reader of dO
+            if (last_of_tile) mma_commit(&bars.do_empty[do_slot(k)]);  // the tile's last reader of dO
           }
           __syncwarp();
         };
@@ -1150,11 +1205,11 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
                      warp_wait(&bars.k_full[g % C::kKStages], k_phase(g), abort_flag)))
             break;
           issue_s(g);
-          if (!(ok = (g == 0 ? warp_wait(&bars.do_full, k & 1, abort_flag)
-                             : warp_wait2(&bars.dp_free, (g - 1) & 1, &bars.do_full, k & 1, abort_flag)) &&
+          if (!(ok = (g == 0 ? warp_wait(&bars.do_full[do_slot(k)], do_use(k), abort_flag)
+                             : warp_wait2(&bars.dp_free, (g - 1) & 1, &bars.do_full[do_slot(k)], do_use(k), abort_flag)) &&
                      warp_wait(&bars.v_full[g % C::kVStages], v_phase(g), abort_flag)))
             break;
-          issue_dp(g, t.nk == 1);
+          issue_dp(k, g, t.nk == 1);
           for (int j = 1; j < t.nk; ++j) {
             const int gj = g + j;
             if (!(ok = warp_wait2(&bars.s_free, (gj - 1) & 1, &bars.k_full[gj % C::kKStages], k_phase(gj),
@@ -1164,7 +1219,7 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
             if (!(ok = warp_wait2(&bars.dp_free, (gj - 1) & 1, &bars.v_full[gj % C::kVStages], v_phase(gj),
                                   abort_flag)))
               break;
-            issue_dp(gj, j == t.nk - 1);
+            issue_dp(k, gj, j == t.nk - 1);
           }
           if (!ok) break;
           g += t.nk;
@@ -1217,9 +1272,19 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
     bool ok = L >= 0;
     DqTile t = ok ? dq_tile<CAUSAL, VARLEN, WIN>(L, a, nq) : DqTile{0, 0, 0, 1, 1, 0, 0};
     float lse2 = 0.f, dsum = 0.f;
+    uint4 orow[C::kTileO ? 1 : 8];  // (kFuseD without kTileO) this thread's half of O's row
+    auto load_o = [&](const DqTile& t) {
+      if constexpr (C::kFuseD && !C::kTileO) {
+        const uint4* at = reinterpret_cast<const uint4*>(
+            static_cast<const uint8_t*>(a.o) + (((size_t)t.bh * Nq + min(t.qblk * C::BQ + r, Nq - 1)) * D + 64 * w) * 2);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) orow[c] = at[c];
+      }
+    };
     if (ok) {
       float lr, dr;
       load_row_terms(t, lr, dr);
+      load_o(t);
       row_terms(t, lr, dr, lse2, dsum);
       ok = copy_q(0);
     }
@@ -1228,24 +1293,38 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
       if constexpr (C::kFuseD) {
         // D of this thread's row, dO . O over the row's 64 features (every
         // warpgroup thread forms its row's D; warpgroup 0 also writes it for the
-        // dK/dV kernel), then the dO and O tiles are released to the producer
-        ok = __all_sync(0xffffffffu, mbar_wait(&bars.do_full, k & 1, abort_flag));
+        // dK/dV kernel), then the dO and O tiles are released to the producer.
+        // (kHalves: warpgroup w its half of the features.)
+        const int ds = do_slot(k);
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars.do_full[ds], do_use(k), abort_flag));
         if (!ok) break;
         float acc0 = 0.f, acc1 = 0.f;
+        constexpr int kChunks = C::kHalves && C::kTileO ? 4 : 8;  // 16-byte chunks of this thread's part of the row
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          const int off = r * 128 + ((c ^ (r & 7)) << 4);  // 16-byte chunk c of the 128-byte-swizzled row
-          const uint4 x = *reinterpret_cast<const uint4*>(smem + C::kOffDO + off);
-          const uint4 y = *reinterpret_cast<const uint4*>(smem + C::kOffO + off);
+        for (int i = 0; i < kChunks; ++i) {
+          const int c = kChunks == 4 ? 4 * w + i : i;
+          const int off = ds * C::kTileBytes + r * 128 + ((c ^ (r & 7)) << 4);  // chunk c of the 128-byte-swizzled row
+          const uint4 x = *reinterpret_cast<const uint4*>(smem + C::kOffDO + (C::kTileO ? 0 : w * kPanelBytes) + off);
+          const uint4 y = C::kTileO ? *reinterpret_cast<const uint4*>(smem + C::kOffO + off) : orow[C::kTileO ? 0 : c];
           const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            acc0 = fmaf(__uint_as_float(xs[i] << 16), __uint_as_float(ys[i] << 16), acc0);
-            acc1 = fmaf(__uint_as_float(xs[i] & 0xFFFF0000u), __uint_as_float(ys[i] & 0xFFFF0000u), acc1);
+          for (int h = 0; h < 4; ++h) {
+            acc0 = fmaf(__uint_as_float(xs[h] << 16), __uint_as_float(ys[h] << 16), acc0);
+            acc1 = fmaf(__uint_as_float(xs[h] & 0xFFFF0000u), __uint_as_float(ys[h] & 0xFFFF0000u), acc1);
           }
         }
-        mbar_arrive(&bars.do_empty);
-        const float drow = acc0 + acc1;
+        mbar_arrive(&bars.do_empty[ds]);
+        float drow = acc0 + acc1;
+        if constexpr (C::kHalves) {
+          // (read by the other group at once: its next use comes after products that need both groups' dS)
+          float* half = reinterpret_cast<float*>(smem + C::kOffHalf);
+          half[w * 128 + r] = drow;
+          mbar_arrive(&bars.half_ready);
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars.half_ready, k & 1, abort_flag));
+          if (!ok) break;
+          const float other = half[(w ^ 1) * 128 + r];
+          drow = w == 0 ? drow + other : other + drow;
+        }
         if (w == 0 && q < Nq) a.Dsum[(size_t)t.bh * Nq + q] = drow;
         dsum = q < (VARLEN ? t.sq : Nq) ? drow : 0.f;
       }
@@ -1277,10 +1356,21 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
           if ((CAUSAL && kb + C::BK - 1 > t.qblk * C::BQ + off) || kb + C::BK > sk ||
               (WIN && t.qblk * C::BQ + C::BQ - 1 + off - kb >= a.window && kb + C::BK > a.sinks)) {
             const int lim = (CAUSAL ? min(q + off, sk - 1) : sk - 1) - k0;  // keep key k0 + col iff col <= lim
-            const int out = q + off - a.window - k0, sunk = a.sinks - k0;  // window: drop col <= out, from 'sunk' on
+            if constexpr (WIN) {
+              const int out = q + off - a.window - k0, sunk = a.sinks - k0;  // drop col <= out, from 'sunk' on: as bits
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if (c > lim || (WIN && c <= out && c >= sunk)) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+              for (int h = 0; h < 2; ++h) {
+                const uint32_t keep =
+                    first_bits(lim + 1 - 32 * h) & ~(first_bits(out + 1 - 32 * h) & ~first_bits(sunk - 32 * h));
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                  if (!(keep >> c & 1u)) sr[h][c] = __float_as_uint(-INFINITY);
+              }
+            } else {
+#pragma unroll
+              for (int c = 0; c < 64; ++c)
+                if (c > lim) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+            }
           }
           const float2 scale2 = make_float2(sl2, sl2), shift2 = make_float2(-lse2, -lse2);
 #pragma unroll
@@ -1371,6 +1461,7 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
       if (L >= 0) {
         nt = dq_tile<CAUSAL, VARLEN, WIN>(L, a, nq);
         load_row_terms(nt, lse_next, d_next);
+        load_o(nt);
         ok = copy_q(k + 1);
       }
       // Epilogue of the finished tile: dq = bf16(scale * dQ), staged row by row
@@ -1461,18 +1552,17 @@ cudaError_t launch_bwd_t(const BwdArgs& a, int num_sms, cudaStream_t stream) {
   if ((e = cudaFuncSetAttribute(kv, cudaFuncAttributeMaxDynamicSharedMemorySize, DkdvCfg<D>::kSmemBytes)) !=
       cudaSuccess)
     return e;
-  if ((e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, DqCfg<D>::kSmemBytes)) !=
-      cudaSuccess)
-    return e;
+  const int kq_smem = a.window ? DqCfg<D, true>::kSmemBytes : DqCfg<D>::kSmemBytes;
+  if ((e = cudaFuncSetAttribute(kq, cudaFuncAttributeMaxDynamicSharedMemorySize, kq_smem)) != cudaSuccess) return e;
   // persistent: one CTA per SM at most (both main kernels take their tiles from counters)
   const long long kv_tiles = (long long)(a.window ? a.BH / a.group : a.BH) * ((a.Nk + 127) / 128), q_tiles = (long long)a.BH * ((a.Nq + 127) / 128);
   const unsigned kv_ctas = (unsigned)std::min<long long>(kv_tiles, num_sms);
   const unsigned q_ctas = (unsigned)std::min<long long>(q_tiles, num_sms);
-  if constexpr (DqCfg<D>::kFuseD) {
+  if (DqCfg<D>::kFuseD || a.window) {
     // the dQ kernel forms D and writes it; the dK/dV kernel reads it after
     fa_bwd_start_kernel<<<1, 32, 0, stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    kq<<<q_ctas, 352, DqCfg<D>::kSmemBytes, stream>>>(a);
+    kq<<<q_ctas, 352, kq_smem, stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     kv<<<kv_ctas, 352, DkdvCfg<D>::kSmemBytes, stream>>>(a);
   } else {
@@ -1482,7 +1572,7 @@ cudaError_t launch_bwd_t(const BwdArgs& a, int num_sms, cudaStream_t stream) {
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     kv<<<kv_ctas, 352, DkdvCfg<D>::kSmemBytes, stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    kq<<<q_ctas, 352, DqCfg<D>::kSmemBytes, stream>>>(a);
+    kq<<<q_ctas, 352, kq_smem, stream>>>(a);
   }
   return cudaGetLastError();
 }

@@ -128,9 +128,6 @@ __device__ __forceinline__ Item item(const WindowArgs& a, int i) {
   return x;
 }
 
-// The first n bits (none for n <= 0, all from 32 on).
-__device__ __forceinline__ uint32_t first_bits(int n) { return n >= 32 ? ~0u : (1u << max(n, 0)) - 1u; }
-
 // The items of a CTA, worked out by its loading warp and told to the others (a step's divisions took every softmax thread
 // 1400 cycles between two items).
 constexpr int kItemRing = 4;

@@ -47,6 +47,7 @@ struct BwdArgs {
   CUtensorMap tm_q, tm_k, tm_v, tm_do;  // loads
   CUtensorMap tm_o;                     // o, loaded by the d = 64 dQ kernel, which forms D itself
   CUtensorMap tm_dq, tm_dk, tm_dv;      // stores
+  void *dq, *dk, *dv;                   // the stores' arrays (rows that no tile computes are zeroed directly)
   const void* o;                        // bf16 [BH][Nq][d]
   const void* dO;                       // bf16 [BH][Nq][d]
   const float* lse;                     // fp32 [BH][Nq]

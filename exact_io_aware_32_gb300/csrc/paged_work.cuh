@@ -67,8 +67,8 @@ __host__ __device__ __forceinline__ int keys_seen(const PagedArgs& a, const Requ
 
 // What a tile whose first token is 'tok' streams under a window: the request's pages that hold any of the first a.sinks keys,
 // then those from its window's first key on, one after another as if there were none between them. So blocks of 128 keys hold
-// 128 keys that count: 128 requests, window 500, 4 sinks, 16 heads over 8 of 64 49.5 us where the sinks had a block of their
-// own, 46 us so; three chunks of 1024 tokens, window 2000, 130 sinks, E4M3 117 and 111 us. Keys and positions are those of the
+// 128 keys that count: a decoding step of 128 requests, window 500, 4 sinks, 16 heads over 8 of 64 55 us where the sinks had a
+// block of their own, 52 us so; three chunks of 1024 tokens, window 2000, 130 sinks, E4M3 117 and 111 us. Keys and positions are those of the
 // request with 'gap' fewer.
 struct Band {
   int sunk, skip;  // pages of the sinks before the window's; pages between them and it that nobody sees

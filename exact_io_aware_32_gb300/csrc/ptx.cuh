@@ -394,6 +394,9 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+// The first n bits (none for n <= 0, all from 32 on).
+__device__ __forceinline__ uint32_t first_bits(int n) { return n >= 32 ? ~0u : (1u << (n > 0 ? n : 0)) - 1u; }
+
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
                : "memory");
