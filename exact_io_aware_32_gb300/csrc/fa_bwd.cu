@@ -120,7 +120,7 @@ struct DkdvCfg {
   static constexpr int kOffBar = kOffRow + 2 * 2 * 128 * 4;
   // No alignment slack: the kernel checks that dynamic shared memory starts on
   // a 1024-byte boundary (the 128-byte swizzle atoms need it).
-  static constexpr int kSmemBytes = kOffBar + 512;
+  static constexpr int kSmemBytes = kOffBar + 640;
   static constexpr uint32_t kColS = 0;     // S^T fp32
   static constexpr uint32_t kColDP = 128;  // dP^T fp32, then P^T and dS^T as bf16 over it (dkdv_pcol)
   static constexpr uint32_t kColDV = 256;
@@ -143,11 +143,12 @@ struct DkdvBarriers {
   // by parity would be ambiguous.
   uint64_t ep_staged[8];
   int item[4];
+  int4 tile[4][2];  // (WIN) the tiles themselves
   int st_bh[8], st_kblk[8], st_last[8];  // producer: tiles by k % 8 (head, key block, last block)
   uint32_t tmem_base;
   int abort;
 };
-static_assert(sizeof(DkdvBarriers) <= 512, "dK/dV barriers exceed their shared memory");
+static_assert(sizeof(DkdvBarriers) <= 640, "dK/dV barriers exceed their shared memory");
 
 // TMEM column, relative to the dP^T columns, of the packed bf16 operand for
 // k-step kk (16 queries). Warpgroup w holds queries [64 w, 64 w + 64) in
@@ -274,8 +275,9 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dkdv_kernel(const __grid_consta
   // Tile k of this CTA, as published by the producer in the tile ring; -1 once
   // the counter is exhausted. Every consumer warp reads each slot once and
   // releases it. The wait ignores the abort flag (bounded by time only), so
-  // that the warps of a warpgroup agree on their sequence of tiles.
-  auto take_tile = [&](int k) -> int {
+  // that the warps of a warpgroup agree on their sequence of tiles. (WIN: the
+  // producer has worked the tile out for all.)
+  auto take_tile = [&](int k, DkdvTile& t) -> int {
     const int is = k % C::kItemSlots;
     const bool got = __all_sync(0xffffffffu, mbar_wait_drain(&bars.item_full[is], (k / C::kItemSlots) & 1));
     if (!got) {
@@ -283,8 +285,13 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dkdv_kernel(const __grid_consta
       return -1;
     }
     const int L = *reinterpret_cast<volatile int*>(&bars.item[is]);
+    if constexpr (WIN) {
+      const int4 u = bars.tile[is][0], v = bars.tile[is][1];
+      t = {u.x, u.y, u.z, u.w, v.x, v.y, v.z};
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars.item_empty[is]);
+    if (!WIN && L < total) t = dkdv_tile<CAUSAL, VARLEN, WIN>(L, a, nkv);
     return L < total ? L : -1;
   };
 
@@ -339,11 +346,12 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dkdv_kernel(const __grid_consta
       }
       return true;
     };
-    for (int k = 0; ok; ++k) {
+    DkdvTile t_next{};
+    // takes the CTA's k-th tile and tells the others; false past the last one (or, ok false, after a failed wait)
+    auto take = [&](int k) -> bool {
       const int is = k % C::kItemSlots;
-      if (!warp_wait(&bars.item_empty[is], ((k / C::kItemSlots) & 1) ^ 1, abort_flag)) break;
+      if (!(ok = warp_wait(&bars.item_empty[is], ((k / C::kItemSlots) & 1) ^ 1, abort_flag))) return false;
       int L = 0;
-      DkdvTile t;
       for (;;) {
         if (lane == 0) {
           L = (int)atomicAdd(&a.work[0], 1u);
@@ -351,13 +359,24 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dkdv_kernel(const __grid_consta
         }
         L = __shfl_sync(0xffffffffu, L, 0);
         __syncwarp();
-        if (L < total) t = dkdv_tile<CAUSAL, VARLEN, WIN>(L, a, nkv);
-        if (!WIN || L >= total || t.n > 0) break;
-        zero_tile<D>(a.dk, t.bh, t.kblk * 128, a.Nk, lane);  // and take another
-        zero_tile<D>(a.dv, t.bh, t.kblk * 128, a.Nk, lane);
+        if (L < total) t_next = dkdv_tile<CAUSAL, VARLEN, WIN>(L, a, nkv);
+        if (!WIN || L >= total || t_next.n > 0) break;
+        zero_tile<D>(a.dk, t_next.bh, t_next.kblk * 128, a.Nk, lane);  // and take another
+        zero_tile<D>(a.dv, t_next.bh, t_next.kblk * 128, a.Nk, lane);
       }
-      if (lane == 0) mbar_arrive(&bars.item_full[is]);  // release: the tile index is visible
-      if (L >= total) break;
+      if (lane == 0) {
+        if constexpr (WIN) {
+          bars.tile[is][0] = make_int4(t_next.bh, t_next.kblk, t_next.i_start, t_next.n);
+          bars.tile[is][1] = make_int4(t_next.sq, t_next.sk, t_next.nq, 0);
+        }
+        mbar_arrive(&bars.item_full[is]);  // release: the tile is visible
+      }
+      return L < total;
+    };
+    bool more = take(0);
+    for (int k = 0; ok && more; ++k) {
+      const DkdvTile t = t_next;
+      const int early = WIN ? max(t.n - 4, 0) : INT_MAX;  // a short tile's last block would wait for the next tile's number
       bars.st_bh[k & 7] = t.bh;  // every lane writes the same values
       bars.st_kblk[k & 7] = t.kblk;
       bars.st_last[k & 7] = g + t.n - 1;
@@ -414,7 +433,12 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dkdv_kernel(const __grid_consta
           qb = t.i_start;
           ++qh;
         }
+        if (it == early) {
+          more = take(k + 1);
+          if (!ok) break;
+        }
       }
+      if (!WIN && ok) more = take(k + 1);
     }
     // the tiles still staged, the last with a full wait; then every copy in flight lands
     while (ok && next_store < ntiles) {
@@ -463,12 +487,13 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dkdv_kernel(const __grid_consta
           ++cursor.it;
           return cursor;
         }
-        const int L = tiles_done ? -1 : take_tile(cursor.kt + 1);
+        DkdvTile t{};
+        const int L = tiles_done ? -1 : take_tile(cursor.kt + 1, t);
         if (L < 0) {
           tiles_done = true;
           return Blk{0, 0, -1};
         }
-        cursor = Blk{0, dkdv_tile<CAUSAL, VARLEN, WIN>(L, a, nkv).n, cursor.kt + 1};
+        cursor = Blk{0, t.n, cursor.kt + 1};
         return cursor;
       };
       if (warp == 10) {
@@ -615,8 +640,8 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dkdv_kernel(const __grid_consta
     // After a failed wait a warp keeps going without work; at every block the
     // group's named barrier also ANDs the warps' states, so the four warps
     // always agree on their blocks and tiles and meet at the same barriers.
-    int L = take_tile(0);
-    DkdvTile t = L >= 0 ? dkdv_tile<CAUSAL, VARLEN, WIN>(L, a, nkv) : DkdvTile{0, 0, 0, 0, 1, 1, 0};
+    DkdvTile t = {0, 0, 0, 0, 1, 1, 0};
+    int L = take_tile(0, t);
     float next = L >= 0 ? fetch(t, t.i_start, head0(t)) : 0.f;
     bool ok = L >= 0;
     int g = 0;
@@ -642,11 +667,8 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dkdv_kernel(const __grid_consta
           }
           next = fetch(t, qb, qh);
         } else {  // the next tile's first block
-          L_next = take_tile(k + 1);
-          if (L_next >= 0) {
-            nt = dkdv_tile<CAUSAL, VARLEN, WIN>(L_next, a, nkv);
-            next = fetch(nt, nt.i_start, head0(nt));
-          }
+          L_next = take_tile(k + 1, nt);
+          if (L_next >= 0) next = fetch(nt, nt.i_start, head0(nt));
         }
         if (!ok) continue;
         const float4* rb4 = reinterpret_cast<const float4*>(rb);  // lse at [0, 64), D at [64, 128)
@@ -835,7 +857,7 @@ struct DqCfg {
   static constexpr int kOffK = kOffO + (kTileO ? kDOStages * kTileBytes : 0);
   static constexpr int kOffV = kOffK + kKStages * kTileBytes;
   static constexpr int kOffBar = kOffV + kVStages * kTileBytes;
-  static constexpr int kOffHalf = kOffBar + 512;  // (kHalves) halves of D, fp32 [2][128]
+  static constexpr int kOffHalf = kOffBar + 640;  // (kHalves) halves of D, fp32 [2][128]
   static constexpr int kSmemBytes = kOffHalf + (kHalves ? 1024 : 0) + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory");
   static constexpr uint32_t kColQ = 0;            // Q, bf16 pairs, D / 2 columns
@@ -854,10 +876,11 @@ struct DqBarriers {
   uint64_t half_ready;                  // (kHalves) both halves of D are in shared memory
   uint64_t ep_staged, dq_stored;        // dQ of a tile staged in the Q buffer; its store has read it
   int item[4];
+  int4 tile[4][2];  // (WIN) the tiles themselves
   uint32_t tmem_base;
   int abort;
 };
-static_assert(sizeof(DqBarriers) <= 512, "dQ barriers exceed their shared memory");
+static_assert(sizeof(DqBarriers) <= 640, "dQ barriers exceed their shared memory");
 
 // Copies row r (D bf16) of a 128-row, 128-byte-swizzled tile into TMEM as D / 2
 // columns of bf16 pairs at taddr (this thread's lane).
@@ -975,12 +998,17 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
   // Tile k of this CTA, as published by the producer in the tile ring; -1
   // (and no further tiles) once the counter is exhausted or on abort. Every
   // consumer warp reads each slot once and releases it.
-  auto take_tile = [&](int k) -> int {
+  auto take_tile = [&](int k, DqTile& t) -> int {
     const int is = k % C::kItemSlots;
     if (!warp_wait(&bars.item_full[is], (k / C::kItemSlots) & 1, abort_flag)) return -1;
     const int L = *reinterpret_cast<volatile int*>(&bars.item[is]);
+    if constexpr (WIN) {  // (the producer has worked it out for all)
+      const int4 u = bars.tile[is][0], v = bars.tile[is][1];
+      t = {u.x, u.y, u.z, u.w, v.x, v.y, v.z};
+    }
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars.item_empty[is]);
+    if (!WIN && L < total) t = dq_tile<CAUSAL, VARLEN, WIN>(L, a, nq);
     return L < total ? L : -1;
   };
 
@@ -1041,7 +1069,13 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
         if (!WIN || L >= total || t.nk > 0) break;
         zero_tile<D>(a.dq, t.bh, t.qblk * 128, Nq, lane);  // and take another
       }
-      if (lane == 0) mbar_arrive(&bars.item_full[is]);  // release: the tile index is visible
+      if (lane == 0) {
+        if constexpr (WIN) {
+          bars.tile[is][0] = make_int4(t.bh, t.qblk, t.nk, t.sq);
+          bars.tile[is][1] = make_int4(t.sk, t.sunk, t.skip, 0);
+        }
+        mbar_arrive(&bars.item_full[is]);  // release: the tile is visible
+      }
       if (L >= total) return false;
       if (k == 1 && !(ok = warp_wait(&bars.qt_ready, 0, abort_flag))) return false;
       if (k >= 2 && !(ok = store_dq(k - 2, false))) return false;
@@ -1139,8 +1173,8 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
         // the product is K's last reader.
         int k = 0, g = 0;  // tile and key block over the CTA's run
         bool ok = true;
-        for (int L = take_tile(0); ok && L >= 0; L = take_tile(++k)) {
-          const DqTile t = dq_tile<CAUSAL, VARLEN, WIN>(L, a, nq);
+        DqTile t{};
+        for (int L = take_tile(0, t); ok && L >= 0; L = take_tile(++k, t)) {
           for (int j = 0; j < t.nk; ++j) {
             const int gj = g + j;
             if (!(ok = warp_wait2(&bars.ds_ready, gj & 1, &bars.k_full[gj % C::kKStages], k_phase(gj), abort_flag)))
@@ -1193,9 +1227,8 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
           __syncwarp();
         };
         int k = 0, g = 0;  // tile and key block over the CTA's run
-        int L = take_tile(0);
-        DqTile t = L >= 0 ? dq_tile<CAUSAL, VARLEN, WIN>(L, a, nq) : DqTile{0, 0, 0, 1, 1, 0, 0};
-        bool ok = L >= 0;
+        DqTile t = {0, 0, 0, 1, 1, 0, 0};
+        bool ok = take_tile(0, t) >= 0;
         while (ok) {
           // the tile's first block: S needs its Q in TMEM (the warpgroups copy it
           // after the previous tile's last S has been read), dP its dO (loaded
@@ -1224,8 +1257,7 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
           if (!ok) break;
           g += t.nk;
           ++k;
-          if ((L = take_tile(k)) < 0) break;
-          t = dq_tile<CAUSAL, VARLEN, WIN>(L, a, nq);
+          if (take_tile(k, t) < 0) break;
         }
         if (elect_one()) mma_commit(&bars.teardown);  // the same lane as above: elect.sync picks the lowest
         __syncwarp();
@@ -1268,15 +1300,18 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
       return ok;
     };
     int k = 0, g = 0;
-    int L = take_tile(0);
+    DqTile t = {0, 0, 0, 1, 1, 0, 0};
+    int L = take_tile(0, t);
     bool ok = L >= 0;
-    DqTile t = ok ? dq_tile<CAUSAL, VARLEN, WIN>(L, a, nq) : DqTile{0, 0, 0, 1, 1, 0, 0};
     float lse2 = 0.f, dsum = 0.f;
     uint4 orow[C::kTileO ? 1 : 8];  // (kFuseD without kTileO) this thread's half of O's row
+    auto o_at = [&](const DqTile& t) {
+      return reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.o) +
+                                            (((size_t)t.bh * Nq + min(t.qblk * C::BQ + r, Nq - 1)) * D + 64 * w) * 2);
+    };
     auto load_o = [&](const DqTile& t) {
       if constexpr (C::kFuseD && !C::kTileO) {
-        const uint4* at = reinterpret_cast<const uint4*>(
-            static_cast<const uint8_t*>(a.o) + (((size_t)t.bh * Nq + min(t.qblk * C::BQ + r, Nq - 1)) * D + 64 * w) * 2);
+        const uint4* at = o_at(t);
 #pragma unroll
         for (int c = 0; c < 8; ++c) orow[c] = at[c];
       }
@@ -1328,8 +1363,17 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
         if (w == 0 && q < Nq) a.Dsum[(size_t)t.bh * Nq + q] = drow;
         dsum = q < (VARLEN ? t.sq : Nq) ? drow : 0.f;
       }
+      DqTile nt = {0, 0, 0, 1, 1, 0, 0};
+      float lse_next = 0.f, d_next = 0.f;
       for (int j = 0; j < t.nk; ++j) {
         const int gj = g + j;
+        if (WIN && j == t.nk - 1) {  // the next tile, whose loads from global memory are on their way during this block
+          L = take_tile(k + 1, nt);
+          if (L >= 0) {
+            load_row_terms(nt, lse_next, d_next);
+            if constexpr (C::kFuseD && !C::kTileO) asm volatile("prefetch.global.L2 [%0];" ::"l"(o_at(nt)));
+          }
+        }
         ok = mbar_wait(&bars.s_full, gj & 1, abort_flag);
         if (!__all_sync(0xffffffffu, ok)) {
           ok = false;
@@ -1455,14 +1499,11 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
       // so that its first S runs while this tile's dQ is written out; its row
       // terms are loaded here and converted when it starts.
       g += t.nk;
-      L = take_tile(k + 1);
-      DqTile nt = {0, 0, 0};
-      float lse_next = 0.f, d_next = 0.f;
+      if (!WIN) L = take_tile(k + 1, nt);
       if (L >= 0) {
-        nt = dq_tile<CAUSAL, VARLEN, WIN>(L, a, nq);
-        load_row_terms(nt, lse_next, d_next);
-        load_o(nt);
+        if (!WIN) load_row_terms(nt, lse_next, d_next);
         ok = copy_q(k + 1);
+        load_o(nt);
       }
       // Epilogue of the finished tile: dq = bf16(scale * dQ), staged row by row
       // in the Q buffer for the producer warp to store; warpgroup w converts
