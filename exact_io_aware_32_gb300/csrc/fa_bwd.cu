@@ -48,6 +48,7 @@
 
 #include "fa_internal.h"
 #include "block_order.cuh"
+#include "paged.h"
 #include "philox.cuh"
 #include "ptx.cuh"
 
@@ -271,6 +272,10 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dkdv_kernel(const __grid_consta
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars.tmem_base;
+  if (WIN) {  // launched as a programmatic dependent: nothing before this has read or written what other kernels do
+    grid_release();
+    grid_wait();
+  }
 
   // Tile k of this CTA, as published by the producer in the tile ring; -1 once
   // the counter is exhausted. Every consumer warp reads each slot once and
@@ -991,6 +996,10 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars.tmem_base;
+  if (WIN) {  // launched as a programmatic dependent: nothing before this has read or written what other kernels do
+    grid_release();
+    grid_wait();
+  }
 
   // Tile k's place of dO and O, and its use of it.
   auto do_slot = [](int k) { return C::kDOStages == 2 ? k & 1 : 0; };
@@ -1570,6 +1579,8 @@ __global__ void __launch_bounds__(256) fa_bwd_prep_kernel(const __grid_constant_
 // The d = 64 backward's first kernel (its dQ kernel forms D): the work counters
 // of the two main kernels are reset, and one thread per sequence checks its lengths.
 __global__ void __launch_bounds__(32) fa_bwd_start_kernel(const __grid_constant__ BwdArgs a) {
+  grid_release();
+  grid_wait();
   if (threadIdx.x < 2) a.work[threadIdx.x] = 0u;
   if (a.seqlens_q || a.seqlens_k)
     for (int b = (int)threadIdx.x; b < a.BH / a.H; b += 32) {
@@ -1599,7 +1610,13 @@ cudaError_t launch_bwd_t(const BwdArgs& a, int num_sms, cudaStream_t stream) {
   const long long kv_tiles = (long long)(a.window ? a.BH / a.group : a.BH) * ((a.Nk + 127) / 128), q_tiles = (long long)a.BH * ((a.Nq + 127) / 128);
   const unsigned kv_ctas = (unsigned)std::min<long long>(kv_tiles, num_sms);
   const unsigned q_ctas = (unsigned)std::min<long long>(q_tiles, num_sms);
-  if (DqCfg<D>::kFuseD || a.window) {
+  if (a.window) {
+    if ((e = launch_dependent(fa_bwd_start_kernel, dim3(1), 32, 0, stream, a)) != cudaSuccess ||
+        (e = launch_dependent(kq, dim3(q_ctas), 352, kq_smem, stream, a)) != cudaSuccess)
+      return e;
+    return launch_dependent(kv, dim3(kv_ctas), 352, DkdvCfg<D>::kSmemBytes, stream, a);
+  }
+  if constexpr (DqCfg<D>::kFuseD) {
     // the dQ kernel forms D and writes it; the dK/dV kernel reads it after
     fa_bwd_start_kernel<<<1, 32, 0, stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;

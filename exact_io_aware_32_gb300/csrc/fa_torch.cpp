@@ -1,4 +1,4 @@
-// Python module _fa_torch: the paged cache's and the rotation's helpers for torch tensors. It
+// Python module _fa_torch: helpers of the paged cache, the rotation and the windowed attention for torch tensors. It
 // checks the tensors, allocates what the caller did not give and calls the C
 // ABI (by the addresses that bind() is given). A decoding step is a few
 // microseconds on the GPU and these calls run between any two of them: the same
@@ -39,7 +39,13 @@ using RopeBackward = decltype(&fa_rope_bwd);
 using Positions = decltype(&fa_paged_positions);
 using RopeStore = decltype(&fa_paged_rope_store);
 using Window = decltype(&fa_fwd_paged_window);
+using WindowForward = decltype(&fa_fwd_window);
+using WindowBytes = decltype(&fa_bwd_window_workspace_bytes);
+using WindowBackward = decltype(&fa_bwd_window);
 Window g_window = nullptr;
+WindowForward g_window_forward = nullptr;
+WindowBytes g_window_bytes = nullptr;
+WindowBackward g_window_backward = nullptr;
 RopeForward g_rope = nullptr;
 RopeBytes g_rope_bytes = nullptr;
 RopeBackward g_rope_backward = nullptr;
@@ -164,9 +170,10 @@ PyObject* guarded(F body) {
 
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    count(n, 10);
-    void* p[10];
-    for (int i = 0; i < 10; ++i) {
+    constexpr int kFunctions = 13;
+    count(n, kFunctions);
+    void* p[kFunctions];
+    for (int i = 0; i < kFunctions; ++i) {
       p[i] = PyLong_AsVoidPtr(a[i]);
       if (!p[i]) refuse("an address is missing");
     }
@@ -180,6 +187,9 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
     g_positions = reinterpret_cast<Positions>(p[7]);
     g_rope_store = reinterpret_cast<RopeStore>(p[8]);
     g_window = reinterpret_cast<Window>(p[9]);
+    g_window_forward = reinterpret_cast<WindowForward>(p[10]);
+    g_window_bytes = reinterpret_cast<WindowBytes>(p[11]);
+    g_window_backward = reinterpret_cast<WindowBackward>(p[12]);
     Py_RETURN_NONE;
   });
 }
@@ -507,6 +517,80 @@ PyObject* rope_store(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// ---------------------------------------------------------------- attention in a window
+struct WindowSizes {
+  int B, Hq, Hkv, Nq, Nk, d;
+  c10::Device dev;
+};
+WindowSizes window_sizes(const at::Tensor& q, const at::Tensor& k, const at::Tensor& v) {
+  if (!q.is_cuda() || q.dim() != 4 || k.dim() != 4) refuse("expected CUDA tensors q [B, Hq, Nq, d], k and v [B, Hkv, Nk, d]");
+  const c10::Device dev = q.device();
+  contiguous(q, "q", c10::ScalarType::BFloat16, {q.size(0), q.size(1), q.size(2), q.size(3)}, dev);
+  contiguous(k, "k", c10::ScalarType::BFloat16, {q.size(0), k.size(1), k.size(2), q.size(3)}, dev);
+  contiguous(v, "v", c10::ScalarType::BFloat16, {q.size(0), k.size(1), k.size(2), q.size(3)}, dev);
+  return {size(q.size(0), "B"), size(q.size(1), "Hq"), size(k.size(1), "Hkv"), size(q.size(2), "Nq"), size(k.size(2), "Nk"),
+          size(q.size(3), "d"), dev};
+}
+int* lengths(PyObject* o, const char* name, const WindowSizes& s) {
+  return o == Py_None ? nullptr : ints(tensor(o, name), name, {s.B}, s.dev);
+}
+double scale_of(PyObject* o, int d) { return o == Py_None ? 1.0 / std::sqrt((double)d) : number(o); }
+
+// window(q, k, v, window, sinks, scale or None, seqlens_q or None, seqlens_k or None)
+PyObject* window(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    count(n, 8);
+    const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+    const WindowSizes s = window_sizes(q, k, v);
+    const int width = integer(a[3], "window"), sinks = integer(a[4], "sinks");
+    const double scale = scale_of(a[5], s.d);
+    const int *lq = lengths(a[6], "seqlens_q", s), *lk = lengths(a[7], "seqlens_k", s);
+    const c10::cuda::CUDAGuard guard(s.dev);
+    const at::Tensor o = at::empty(q.sizes(), q.options()), lse = at::empty({s.B, s.Hq, s.Nq}, q.options().dtype(at::kFloat));
+    const int st = g_window_forward(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr<float>(), s.B, s.Hq,
+                                    s.Hkv, s.Nq, s.Nk, s.d, (float)scale, width, sinks, lq, lk, stream_of(s.dev));
+    if (st != 0) return PyLong_FromLong(st);
+    PyObject* out = PyTuple_New(2);
+    if (!out) return nullptr;
+    PyTuple_SET_ITEM(out, 0, THPVariable_Wrap(o));
+    PyTuple_SET_ITEM(out, 1, THPVariable_Wrap(lse));
+    return out;
+  });
+}
+
+// window_backward(q, k, v, o, lse, dO, window, sinks, scale or None, seqlens_q or None, seqlens_k or None, workspace or None)
+PyObject* window_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    count(n, 12);
+    const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+    const WindowSizes s = window_sizes(q, k, v);
+    void *o = contiguous(tensor(a[3], "o"), "o", c10::ScalarType::BFloat16, {s.B, s.Hq, s.Nq, s.d}, s.dev),
+         *lse = contiguous(tensor(a[4], "lse"), "lse", c10::ScalarType::Float, {s.B, s.Hq, s.Nq}, s.dev),
+         *g = contiguous(tensor(a[5], "dO"), "dO", c10::ScalarType::BFloat16, {s.B, s.Hq, s.Nq, s.d}, s.dev);
+    const int width = integer(a[6], "window"), sinks = integer(a[7], "sinks");
+    const double scale = scale_of(a[8], s.d);
+    const int *lq = lengths(a[9], "seqlens_q", s), *lk = lengths(a[10], "seqlens_k", s);
+    const c10::cuda::CUDAGuard guard(s.dev);
+    const at::Tensor dq = at::empty(q.sizes(), q.options()), dk = at::empty(k.sizes(), q.options()),
+                     dv = at::empty(k.sizes(), q.options());
+    const at::Tensor ws = a[11] == Py_None
+                              ? at::empty({(int64_t)g_window_bytes(s.B, s.Hq, s.Hkv, s.Nq, s.Nk, s.d, width, sinks)},
+                                          q.options().dtype(at::kByte))
+                              : tensor(a[11], "workspace");
+    if (ws.device() != s.dev || !ws.is_contiguous()) refuse("workspace must be a contiguous tensor on " + s.dev.str());
+    const int st = g_window_backward(q.data_ptr(), k.data_ptr(), v.data_ptr(), o, static_cast<float*>(lse), g, dq.data_ptr(),
+                                     dk.data_ptr(), dv.data_ptr(), s.B, s.Hq, s.Hkv, s.Nq, s.Nk, s.d, (float)scale, width,
+                                     sinks, lq, lk, ws.data_ptr(), ws.nbytes(), stream_of(s.dev));
+    if (st != 0) return PyLong_FromLong(st);
+    PyObject* out = PyTuple_New(3);
+    if (!out) return nullptr;
+    PyTuple_SET_ITEM(out, 0, THPVariable_Wrap(dq));
+    PyTuple_SET_ITEM(out, 1, THPVariable_Wrap(dk));
+    PyTuple_SET_ITEM(out, 2, THPVariable_Wrap(dv));
+    return out;
+  });
+}
+
 PyMethodDef g_methods[] = {
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(bind)), METH_FASTCALL, nullptr},
     {"plan", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(plan)), METH_FASTCALL, nullptr},
@@ -515,6 +599,8 @@ PyMethodDef g_methods[] = {
     {"rope", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(rope)), METH_FASTCALL, nullptr},
     {"rope_backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(rope_backward)), METH_FASTCALL, nullptr},
     {"positions", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(positions)), METH_FASTCALL, nullptr},
+    {"window", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(window)), METH_FASTCALL, nullptr},
+    {"window_backward", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(window_backward)), METH_FASTCALL, nullptr},
     {"rope_store", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(rope_store)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_fa_torch", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

@@ -420,9 +420,20 @@ __global__ void __launch_bounds__(CCfg<D, FP8>::kThreads, CCfg<D, FP8>::kCtasPer
         if ((CAUSAL && kv0 + 127 > tok0 + off) || kv0 + 128 > len || (WIN && kv0 <= out_last && kv0 + 128 > a.sinks)) {
           const int lim = (CAUSAL ? min(tok + off, len - 1) : len - 1) - kv0;  // keep column c iff c <= lim
           const int out = lim - band.wide, sunk = a.sinks - kv0;  // window: hidden too are columns up to 'out', from 'sunk' on
+          if constexpr (WIN) {
 #pragma unroll
-          for (int c = 0; c < 128; ++c)
-            if (c > lim || (WIN && c <= out && c >= sunk)) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+            for (int h = 0; h < 4; ++h) {
+              const uint32_t keep =
+                  first_bits(lim + 1 - 32 * h) & ~(first_bits(out + 1 - 32 * h) & ~first_bits(sunk - 32 * h));
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if (!(keep >> c & 1u)) sr[h][c] = __float_as_uint(-INFINITY);
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 128; ++c)
+              if (c > lim) sr[c >> 5][c & 31] = __float_as_uint(-INFINITY);
+          }
           float mxc[8];  // row maximum over eight chains of 16 scores, then a tree
 #pragma unroll
           for (int i = 0; i < 8; ++i)

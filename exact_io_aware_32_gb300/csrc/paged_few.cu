@@ -372,9 +372,10 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
           const int lim = lim_row - kv0;
           const int out = lim - band.wide, sunk = a.sinks - warp * 32 - kv0;  // hidden too: keys up to 'out', from 'sunk' on
           mx = -INFINITY;
+          const uint32_t keep = WIN ? first_bits(lim + 1) & ~(first_bits(out + 1) & ~first_bits(sunk)) : 0u;
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
-            if (c > lim || (WIN && c <= out && c >= sunk)) sr[c] = __float_as_uint(-INFINITY);
+            if (WIN ? !(keep >> c & 1u) : c > lim) sr[c] = __float_as_uint(-INFINITY);
             mx = fmaxf(mx, __uint_as_float(sr[c]));
           }
         }

@@ -521,7 +521,7 @@ def _paged():
         module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
             lib.fa_paged_plan, lib.fa_paged_store, lib.fa_fwd_paged_workspace_bytes, lib.fa_fwd_paged, lib.fa_rope_fwd,
             lib.fa_rope_bwd_workspace_bytes, lib.fa_rope_bwd, lib.fa_paged_positions, lib.fa_paged_rope_store,
-            lib.fa_fwd_paged_window)))
+            lib.fa_fwd_paged_window, lib.fa_fwd_window, lib.fa_bwd_window_workspace_bytes, lib.fa_bwd_window)))
         _torch_module = module
     return _torch_module
 
@@ -789,72 +789,31 @@ def fa_bwd_window(q, k, v, o, lse, dO, dq, dk, dv, B: int, Hq: int, Hkv: int, Nq
                                 _addr(workspace), workspace_bytes, _stream(stream))
 
 
-def _window_shapes(q, k, v):
-    _bf16(q, k, v)
-    B, Hq, Nq, d = _shape(q)
-    if tuple(k.shape) != tuple(v.shape) or k.dim() != 4 or k.shape[0] != B or k.shape[3] != d:
-        raise ValueError("expected q [B, Hq, Nq, d], k and v [B, Hkv, Nk, d]")
-    if k.device != q.device or v.device != q.device:
-        raise ValueError(f"q, k and v must be on one device, {q.device}")
-    return B, Hq, int(k.shape[1]), Nq, int(k.shape[2]), d
-
-
-def _window_lens(seqlens_q, seqlens_k, q, B):
-    for x in (seqlens_q, seqlens_k):
-        if x is not None and x.device != q.device:
-            raise ValueError(f"sequence lengths must be on {q.device}")
-    return _lens(seqlens_q, B), _lens(seqlens_k, B)
-
-
 def forward_window(q, k, v, window: int, sinks: int = 0, scale: float | None = None, seqlens_q=None, seqlens_k=None,
                    stream=None):
     """Causal attention of q [B, Hq, Nq, d] over k, v [B, Hkv, Nk, d] (bf16; Hq a multiple of Hkv; the queries are the last Nq
     positions) in which a row sees the last ``window`` keys up to its own position, and the first ``sinks`` of the sequence:
     allocate o (bf16) and lse (fp32) with torch and run fa_fwd_window. ``seqlens_q`` / ``seqlens_k``: padding lengths, as in
-    forward_kv. Runs on the device of q, on its current stream or ``stream``. Returns (o, lse)."""
-    import torch
-
+    forward_kv. On the device of q, on its current stream or ``stream``. Returns (o, lse)."""
     if stream is not None:
         with _on(stream, q):
             return forward_window(q, k, v, window, sinks, scale, seqlens_q, seqlens_k)
-    B, Hq, Hkv, Nq, Nk, d = _window_shapes(q, k, v)
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    lq, lk = _window_lens(seqlens_q, seqlens_k, q, B)
-    with torch.cuda.device(q.device):
-        o = torch.empty_like(q)
-        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
-        st = fa_fwd_window(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, window, sinks, lq, lk)
-    if st != FA_OK:
-        raise FAError(st, "fa_fwd_window")
-    return o, lse
+    r = (_torch_module or _paged()).window(q, k, v, window, sinks, scale, seqlens_q, seqlens_k)
+    if type(r) is int:
+        raise FAError(r, "fa_fwd_window")
+    return r
 
 
 def backward_window(q, k, v, o, lse, dO, window: int, sinks: int = 0, scale: float | None = None, seqlens_q=None,
                     seqlens_k=None, workspace=None, stream=None):
     """Gradients of forward_window: allocate dq, dk, dv (and the workspace if none is given) and run fa_bwd_window."""
-    import torch
-
     if stream is not None:
         with _on(stream, q):
             return backward_window(q, k, v, o, lse, dO, window, sinks, scale, seqlens_q, seqlens_k, workspace)
-    B, Hq, Hkv, Nq, Nk, d = _window_shapes(q, k, v)
-    _bf16(o, dO)
-    if tuple(o.shape) != tuple(q.shape) or tuple(dO.shape) != tuple(q.shape) or o.device != q.device or dO.device != q.device:
-        raise ValueError("o and dO must have the shape and device of q")
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (B, Hq, Nq) or not lse.is_contiguous() or lse.device != q.device:
-        raise ValueError("lse must be a contiguous float32 tensor [B, Hq, Nq] on the device of q")
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    lq, lk = _window_lens(seqlens_q, seqlens_k, q, B)
-    with torch.cuda.device(q.device):
-        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-        need = fa_bwd_window_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, window, sinks)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        st = fa_bwd_window(q, k, v, o, lse, dO, dq, dk, dv, B, Hq, Hkv, Nq, Nk, d, scale, window, sinks, lq, lk, workspace,
-                           workspace.numel() * workspace.element_size())
-    if st != FA_OK:
-        raise FAError(st, "fa_bwd_window")
-    return dq, dk, dv
+    r = (_torch_module or _paged()).window_backward(q, k, v, o, lse, dO, window, sinks, scale, seqlens_q, seqlens_k, workspace)
+    if type(r) is int:
+        raise FAError(r, "fa_bwd_window")
+    return r
 
 
 _window_fn = None
