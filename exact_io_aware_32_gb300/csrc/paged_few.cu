@@ -18,10 +18,13 @@
 // Persistent CTAs over ranges of the row of tiles (paged_work.cuh), rings and
 // barriers counting on across tiles.
 //
-// Warp roles: 0-3 softmax and epilogue; 4 walks the range, tells the others its
-// pieces and copies keys, 5 copies values; 6 issues P V and owns TMEM, 7 copies Q
-// and issues Q K^T; with E4M3 caches eight converter warps (value codes to f16, Q
-// to its two parts; by four of them 7% slower where tiles are short).
+// Warp roles: 0-3 softmax and epilogue; 4 walks the range and tells the others its
+// pieces; two warps copy keys, every other block each, and two values; one issues P V
+// and owns TMEM, one copies Q and issues Q K^T; with E4M3 caches eight converter warps
+// (value codes to f16, Q to its two parts; by four of them 7% slower where tiles are
+// short). A block of pages of 16 tokens takes its copying warp 1150 cycles and a step
+// of the walk 1200 to 2200: at d = 64, where a block is 760 cycles of HBM, one
+// warp for the keys and the walk set the pace.
 //
 // Measured, d = 128, 8 key heads, 32 query heads: 64 requests of up to 8192 keys
 // 157 us, 6.6 TB/s of keys and values (bound by them); 48 of up to 16384, E4M3
@@ -57,8 +60,8 @@ struct FCfg {
   static constexpr int kSmemBytes = kOffBar + 768 + 1024;  // barriers, alignment slack
   static_assert(kSmemBytes <= 232448, "shared memory");
   static constexpr uint32_t kColS = 0, kColP = 256, kColO = 384, kTmemCols = 512;  // S and P twice
-  static constexpr int kWarpTmaK = 4, kWarpTmaV = 5, kWarpPv = 6, kWarpQk = 7, kWarpConv = 8, kConvWarps = 8;
-  static constexpr int kThreads = 256 + (FP8_ ? 32 * kConvWarps : 0);
+  static constexpr int kWarpWalk = 4, kWarpTmaK = 5, kWarpTmaV = 7, kWarpPv = 9, kWarpQk = 10, kWarpConv = 11, kConvWarps = 8;
+  static constexpr int kThreads = 32 * (kWarpConv + (FP8_ ? kConvWarps : 0));
 };
 
 struct FBars {
@@ -120,7 +123,7 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
       mbar_init(&bars.teardown[s], 1);
     }
     mbar_init(&bars.o_free, 128);
-    bars.ring.init(7 + (FP8 ? C::kConvWarps : 0));  // four softmax warps, V, Q K^T, P V, converters
+    bars.ring.init(10 + (FP8 ? C::kConvWarps : 0));  // four softmax warps, two for K, two for V, Q K^T, P V, converters
     fence_mbar_init();
   }
   // rows of Q that no copy fills (G that does not divide 32, short tiles) are zeros, not leftovers
@@ -144,50 +147,35 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
   Piece p = range.first;
   const bool first = range.use;  // the first piece is there already
   Walk<WIN> walk;
-  if (warp == C::kWarpTmaK) walk.begin(range);
+  if (warp == C::kWarpWalk) walk.begin(range);
   const int per = range.per;
   __syncthreads();  // all have read the range: the join may write there
-  if (warp == C::kWarpTmaK) {
-    // ------------------------------------------------------------ keys, and the walk for all
+  if (warp == C::kWarpWalk) {
+    // ------------------------------------------------------------ the walk, for all
     Parts parts{};
-    int g = 0, nk = 0, n = 0;  // key blocks, loads issued, pieces
+    int n = 0;  // pieces told
     bool more = true, ok = true;
     if (!first) {
-      more = walk.step<true>(a, p);
+      more = walk.template step<true>(a, p);
       ok = bars.ring.tell(n++, p, more, 0, 0, lane, abort_flag);
     }
-    for (Piece next = p; ok && more; p = next) {
+    while (ok && more) {
       note_piece(a, parts, p, walk, per);
-      const int nb = p.je - p.jb;
-      Pages<WIN> pages;
-      Band band{};
-      if (WIN) band = band_of(a, p.q, p.tok);
-      if (nb > 0) pages.begin(a, p, band, lane);
-      for (int j = 0; j < max(nb, 1); ++j) {
-        if (nb > 0) {
-          const int jj = p.jb + j, page_now = pages.of(a, p, jj, lane);
-          const int s = g % C::kKStages;
-          if (!(ok = warp_wait(&bars.k_empty[s], ((g / C::kKStages) & 1) ^ 1, abort_flag))) break;
-          load_block<D, FP8, WIN>(a, p, jj, page_now, lane, &a.tm_k, smem + C::kOffK + s * C::kKBytes, &bars.k_full[s],
-                                  p.q.len - band.gap, band.low);
-          nk = ++g;
-        }
-        if (j == 0) {  // before this piece's other blocks: the Q K^T warp looks one piece ahead
-          more = walk.step<true>(a, next);
-          if (!(ok = bars.ring.tell(n++, next, more, 0, 0, lane, abort_flag))) break;
-        }
-      }
+      more = walk.template step<true>(a, p);
+      ok = bars.ring.tell(n++, p, more, 0, 0, lane, abort_flag);
     }
     if (lane == 0) static_cast<Parts*>(a.parts)[blockIdx.x] = parts;
-    // Let every issued copy land before the CTA can exit.
-    for (int x = max(0, nk - C::kKStages); x < nk; ++x)
-      mbar_wait_drain(&bars.k_full[x % C::kKStages], (x / C::kKStages) & 1);
-  } else if (warp == C::kWarpTmaV) {
-    // ------------------------------------------------------------ values
-    // (a warp of their own: a copy holds its warp for about 150 cycles, and with pages of 16 tokens a block has 16)
-    constexpr int kS = FP8 ? C::kCStages : C::kVStages;
-    uint64_t *full = FP8 ? bars.c_full : bars.v_full, *empty = FP8 ? bars.c_empty : bars.v_empty;
-    int g = 0, nv = 0;
+  } else if (warp >= C::kWarpTmaK && warp < C::kWarpPv) {
+    // ------------------------------------------------------------ keys, values: every other block each
+    const bool value = warp >= C::kWarpTmaV;
+    const int mine = (warp - C::kWarpTmaK) & 1;
+    const int stages = !value ? C::kKStages : FP8 ? C::kCStages : C::kVStages;
+    const int bytes = !value ? C::kKBytes : FP8 ? C::kCodeBytes : C::kTileBytes;
+    uint8_t* ring = smem + (!value ? C::kOffK : FP8 ? C::kOffC : C::kOffV);
+    uint64_t *full = !value ? bars.k_full : FP8 ? bars.c_full : bars.v_full,
+             *empty = !value ? bars.k_empty : FP8 ? bars.c_empty : bars.v_empty;
+    const CUtensorMap* tm = value ? &a.tm_v : &a.tm_k;
+    int g = 0, last = 0;  // key blocks; the end of those that this warp has copied
     bool ok = true;
     for (bool more = first || in.next(p); ok && more; more = in.next(p)) {
       if (p.jb == p.je) continue;
@@ -196,15 +184,17 @@ __global__ void __launch_bounds__(FCfg<D, FP8>::kThreads, 1) fa_paged_few_kernel
       if (WIN) band = band_of(a, p.q, p.tok);
       pages.begin(a, p, band, lane);
       for (int jj = p.jb; jj < p.je; ++jj, ++g) {
-        const int page_now = pages.of(a, p, jj, lane), s = g % kS;
-        if (!(ok = warp_wait(&empty[s], ((g / kS) & 1) ^ 1, abort_flag))) break;
-        load_block<D, FP8, WIN>(a, p, jj, page_now, lane, &a.tm_v,
-                                smem + (FP8 ? C::kOffC + s * C::kCodeBytes : C::kOffV + s * C::kTileBytes), &full[s],
-                                p.q.len - band.gap, band.low);
-        nv = g + 1;
+        const int page_now = pages.of(a, p, jj, lane), s = g % stages;
+        if ((g & 1) != mine) continue;
+        if (!(ok = warp_wait(&empty[s], ((g / stages) & 1) ^ 1, abort_flag))) break;
+        load_block<D, FP8, WIN>(a, p, jj, page_now, lane, tm, ring + s * bytes, &full[s], p.q.len - band.gap, band.low);
+        last = g + 1;
       }
     }
-    for (int x = max(0, nv - kS); x < nv; ++x) mbar_wait_drain(&full[x % kS], (x / kS) & 1);
+    // Let every issued copy land before the CTA can exit: those of the run's last blocks. (A place that the other warp has filled
+    // since is another phase, and was filled only after this warp's copy had been read.)
+    for (int x = max(0, (ok ? g : last) - stages); x < last; ++x)
+      if ((x & 1) == mine) mbar_wait_drain(&full[x % stages], (x / stages) & 1);
   } else if (warp == C::kWarpQk) {
     // ------------------------------------------------------------ S = Q K^T, up to two blocks ahead of the softmax
     const uint64_t dq = sdesc_sw128(smem_u32(smem + C::kOffQ), 16, 1024);
