@@ -523,7 +523,16 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
         // behind the last row's window that are not all sinks.
         const int kv0 = x.at(j) * 128;
         float mx = fmax3(fmax3(cmax[0], cmax[1], cmax[2]), cmax[3], -INFINITY);
-        if (thin || kv0 + 127 > row0 + x.off || (p_last - kv0 >= a.window && kv0 + 128 > a.sinks)) {
+        if (thin) {  // the sinks alone, which every row sees
+          const uint32_t keep = first_bits(a.sinks - kv0);
+          float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int q = 0; q < 32; ++q) {
+            if (!(keep >> q & 1u)) sr[0][q] = __float_as_uint(-INFINITY);
+            m[q & 3] = fmaxf(m[q & 3], __uint_as_float(sr[0][q]));
+          }
+          mx = fmaxf(fmax3(m[0], m[1], m[2]), m[3]);
+        } else if (kv0 + 127 > row0 + x.off || (p_last - kv0 >= a.window && kv0 + 128 > a.sinks)) {
           // column c iff c <= lim and (c > out or c < sunk)
           const int lim = p - kv0, out = lim - a.window, sunk = a.sinks - kv0;
 #pragma unroll
