@@ -8,9 +8,12 @@
 //   dx = rstd (u - xh mean(u o xh)),  u = w o g, xh = x rstd.
 //
 // Everything is a pass over the rows, bound by HBM where there are many and by
-// latency where there are few. A thread holds 16 elements of a row, those of
-// eight whole pairs, in two 16-byte chunks: D / 16 lanes a row. A warp takes one
-// token and a slice of its heads, so that its lanes make each angle once for all of them.
+// latency where there are few; the norms add enough instructions to stay behind it
+// (16384 tokens of 32 + 8 heads of 128: 55 us forward, 6.1 TB/s; with norms 58 us,
+// 5.7 TB/s, and backward, where three passes move, 87 us, 5.8 TB/s). A thread holds
+// 16 elements of a row, those of eight whole pairs, in two 16-byte chunks: D / 16
+// lanes a row. A warp takes one token and a slice of its heads, so that its lanes
+// make each angle once for all of them.
 //
 // Angles: a position times a frequency may be millions of radians, of which fp32
 // keeps no fraction of a turn. The frequency is taken in turns as a 64-bit
@@ -18,6 +21,7 @@
 // the exact place in the turn (an integer multiplication; the frequency's own
 // rounding, 2^-53 of it, is all that is lost), of which the upper 32 bits go to sincospi.
 #include <algorithm>
+#include <atomic>
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -35,49 +39,111 @@ constexpr int kThreads = 256, kWarps = kThreads / 32;
 
 enum Mode { kForward, kBackward, kStore };
 
-// A lane's place in its row: where its two chunks of 8 elements begin, and its first pair (< 0: not rotated).
+// A lane's place in its row: where its two chunks of 8 elements begin, each beside its neighbours' (so that a load or store of
+// a row's lanes is of whole sectors). Neighbours make pairs in any chunk; halves apart, the second chunk is the first one's.
 struct Place {
-  int a, b, pair;
+  int a, b;
 };
-template <bool INTER>
+template <int D, bool INTER>
 __device__ __forceinline__ Place place(int part, int rot) {
-  if (INTER || 16 * part >= rot) return {16 * part, 16 * part + 8, 16 * part < rot ? 8 * part : -1};
-  return {8 * part, rot / 2 + 8 * part, 8 * part};
+  const int half = INTER ? D / 2 : rot / 2, past = part - rot / 16;
+  if (INTER || past < 0) return {8 * part, half + 8 * part};
+  return {rot + 8 * past, rot + (D - rot) / 2 + 8 * past};  // not rotated
 }
 
 struct Raw {
   uint4 a, b;
 };
-__device__ __forceinline__ Raw load_row(const RopeView& v, long long at, const Place& p) {
-  const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(v.at) + at;
-  return {*reinterpret_cast<const uint4*>(row + p.a), *reinterpret_cast<const uint4*>(row + p.b)};
-}
-__device__ __forceinline__ void unpack(const Raw& r, float (&x)[16]) {
+// Rows on their way, DEPTH steps ahead, T tensors a step: copied past the registers into a thread's own slots of shared
+// memory, so that the registers are free for the work. A slot is filled again a step after it was read, when what was read
+// of it has been used. 16384 tokens of 32 + 8 heads of 128 with norms, forward and backward: 162.9 us with the rows in
+// registers, 142 to 143 us with 2 steps ahead, 149 us with 3 (of an SM's shared memory more is a ring, and less a cache).
+constexpr int kAhead = 2;
+template <int DEPTH, int T>
+struct Ring {
+  static constexpr int kSlots = DEPTH + 1, kBytes = kSlots * T * 2 * kThreads * 16;
+  uint32_t at;  // this thread's first slot
+  uint32_t fill, take;
+  __device__ __forceinline__ explicit Ring(const void* smem) : at(ptx::smem_u32(smem) + threadIdx.x * 16), fill(0), take(0) {}
+  __device__ __forceinline__ static uint32_t next(uint32_t i) { return i + 1 == kSlots ? 0 : i + 1; }
+  // Tensor t of the step to come: the row's two chunks, or (there is no row) zeros.
+  __device__ __forceinline__ void load(int t, const __nv_bfloat16* row, const Place& p, bool there) {
+    const uint32_t to = at + (fill * T + t) * (2 * kThreads * 16);
+    const int bytes = there ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(row + p.a), "r"(bytes) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + kThreads * 16), "l"(row + p.b), "r"(bytes) : "memory");
+  }
+  // The step's loads are under way ('step': there is one, else nothing was loaded).
+  __device__ __forceinline__ void loaded(bool step) {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (step) fill = next(fill);
+  }
+  // The oldest of DEPTH steps that are on their way has come.
+  __device__ __forceinline__ void wait() { asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory"); }
+  __device__ __forceinline__ Raw get(int t) const {
+    const uint32_t from = at + (take * T + t) * (2 * kThreads * 16);
+    Raw r;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.a.x), "=r"(r.a.y), "=r"(r.a.z), "=r"(r.a.w) : "r"(from) : "memory");
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.b.x), "=r"(r.b.y), "=r"(r.b.z), "=r"(r.b.w) : "r"(from + kThreads * 16) : "memory");
+    return r;
+  }
+  __device__ __forceinline__ void taken() { take = next(take); }
+};
+// A lane's 16 elements in fp32: of pairs 2 i and 2 i + 1 the first elements in a[i], the second in b[i], so that the work on
+// them is packed, two at an instruction.
+struct Row {
+  float2 a[4], b[4];
+};
+// INTER: a word is a pair, else the chunks' elements stand side by side.
+template <bool INTER>
+__device__ __forceinline__ Row unpack(const Raw& r) {
   const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+  float lo[8], hi[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    lo[i] = __uint_as_float(w[i] << 16);
+    hi[i] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+  Row x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x.a[i] = INTER ? make_float2(lo[2 * i], lo[2 * i + 1]) : make_float2(lo[i], hi[i]);
+    x.b[i] = INTER ? make_float2(hi[2 * i], hi[2 * i + 1]) : make_float2(lo[4 + i], hi[4 + i]);
+  }
+  return x;
+}
+// The elements in the order of the row's two chunks.
+template <bool INTER>
+__device__ __forceinline__ void in_order(const Row& x, float (&y)[16]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    y[INTER ? 4 * i : 2 * i] = x.a[i].x;
+    y[INTER ? 4 * i + 2 : 2 * i + 1] = x.a[i].y;
+    y[INTER ? 4 * i + 1 : 8 + 2 * i] = x.b[i].x;
+    y[INTER ? 4 * i + 3 : 9 + 2 * i] = x.b[i].y;
   }
 }
-__device__ __forceinline__ void store_row(const RopeView& v, long long at, const Place& p, const float (&x)[16]) {
-  __nv_bfloat16* row = static_cast<__nv_bfloat16*>(v.at) + at;
+template <bool INTER>
+__device__ __forceinline__ void store_row(__nv_bfloat16* row, const Place& p, const Row& x) {
+  float y[16];
+  in_order<INTER>(x, y);
   uint32_t w[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i] = ptx::pack_bf16x2(x[2 * i], x[2 * i + 1]);
+  for (int i = 0; i < 8; ++i) w[i] = ptx::pack_bf16x2(y[2 * i], y[2 * i + 1]);
   *reinterpret_cast<uint4*>(row + p.a) = make_uint4(w[0], w[1], w[2], w[3]);
   *reinterpret_cast<uint4*>(row + p.b) = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
-// The pairs of a lane's 16 elements: neighbours, or the two chunks' elements side by side.
-template <bool INTER>
-__device__ __forceinline__ void rotate(float (&x)[16], const float (&c)[8], const float (&s)[8]) {
+// Cosines and sines of a lane's pairs, as a Row's.
+struct Turn {
+  float2 c[4], s[4];
+};
+__device__ __forceinline__ void rotate(Row& x, const Turn& t) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float &a = x[INTER ? 2 * i : i], &b = x[INTER ? 2 * i + 1 : 8 + i];
-    const float a0 = a;
-    a = fmaf(a0, c[i], -b * s[i]);
-    b = fmaf(b, c[i], a0 * s[i]);
+  for (int i = 0; i < 4; ++i) {
+    const float2 a = x.a[i], bs = ptx::fmul2(x.b[i], t.s[i]);
+    x.b[i] = ptx::ffma2(a, t.s[i], ptx::fmul2(x.b[i], t.c[i]));
+    x.a[i] = make_float2(fmaf(a.x, t.c[i].x, -bs.x), fmaf(a.y, t.c[i].y, -bs.y));
   }
 }
 
@@ -91,7 +157,7 @@ __device__ __forceinline__ unsigned long long turns(double f) {
 // pairs' halves of every lane side by side (no bank twice), as place() deals them out.
 template <int D>
 struct Angles {
-  float4 at[D / 2 * 32 / (D / 16) / 2];  // two pairs each, D / 2 a token, up to 32 / (D / 16) tokens
+  float4 at[D / 2 * 32 / (D / 16) / 2];  // two pairs' cosines, then their sines; D / 2 pairs a token, up to 32 / (D / 16) tokens
 };
 // Where a token is: number n of sequence b. on(): so many tokens later.
 struct Token {
@@ -105,7 +171,7 @@ struct Token {
     return t;
   }
 };
-template <int D>
+template <int D, bool INTER>
 __device__ __forceinline__ void make_angles(const RopeArgs& a, const unsigned long long* turn, Angles<D>& to, int tokens,
                                             const Token& first, int lane, float sign) {
   constexpr int kLanes = D / 16;
@@ -121,45 +187,65 @@ __device__ __forceinline__ void make_angles(const RopeArgs& a, const unsigned lo
       cs.x *= a.factor;
       cs.y *= sign * a.factor;
     }
-    reinterpret_cast<float2*>(&to.at[which * (D / 4) + (pair % 8 / 2) * kLanes + pair / 8])[pair % 2] = cs;
+    const int part = INTER ? pair % (D / 4) / 4 : pair / 8, own = INTER ? pair / (D / 4) * 4 + pair % 4 : pair % 8;
+    float* at = reinterpret_cast<float*>(&to.at[which * (D / 4) + own / 2 * kLanes + part]) + own % 2;
+    at[0] = cs.x;
+    at[2] = cs.y;
   }
   __syncwarp();
 }
 template <int D>
-__device__ __forceinline__ void take_angles(const Angles<D>& from, int which, int part, float (&c)[8], float (&s)[8]) {
+__device__ __forceinline__ Turn take_angles(const Angles<D>& from, int which, int part) {
+  Turn t;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float4 v = from.at[which * (D / 4) + i * (D / 16) + part];
-    c[2 * i] = v.x;
-    s[2 * i] = v.y;
-    c[2 * i + 1] = v.z;
-    s[2 * i + 1] = v.w;
+    t.c[i] = make_float2(v.x, v.y);
+    t.s[i] = make_float2(v.z, v.w);
   }
+  return t;
 }
 
-// The weights of a part in shared memory, four elements of every lane side by side (no bank twice), as place() deals them out.
+// The weights of a part in shared memory, a[i] and b[i] of every lane side by side (no bank twice), as place() deals them out.
 template <int D, bool INTER>
 __device__ __forceinline__ void stage_weights(const RopeArgs& a, const void* w, float4* to) {
   constexpr int kLanes = D / 16;
   for (int i = threadIdx.x; i < D; i += kThreads) {
     const int part = i / 16, e = i % 16;
-    const Place p = place<INTER>(part, a.rot);
+    const Place p = place<D, INTER>(part, a.rot);
     const int at = e < 8 ? p.a + e : p.b + e - 8;
     const float x = a.w_fp32 ? static_cast<const float*>(w)[at] : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[at]);
-    reinterpret_cast<float*>(to + (e / 4) * kLanes + part)[e % 4] = x;
+    const int pair = INTER ? e / 2 : e % 8, second = INTER ? e % 2 : e / 8;
+    reinterpret_cast<float*>(to + (pair / 2) * kLanes + part)[2 * second + pair % 2] = x;
   }
 }
-// x *= f w
 template <int D>
-__device__ __forceinline__ void times_weights(float (&x)[16], const float4* w, int part, float f) {
+__device__ __forceinline__ void times_weights(Row& x, const float4* w, int part) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float4 v = w[i * (D / 16) + part];
-    x[4 * i] *= f * v.x;
-    x[4 * i + 1] *= f * v.y;
-    x[4 * i + 2] *= f * v.z;
-    x[4 * i + 3] *= f * v.w;
+    x.a[i] = ptx::fmul2(x.a[i], make_float2(v.x, v.y));
+    x.b[i] = ptx::fmul2(x.b[i], make_float2(v.z, v.w));
   }
+}
+__device__ __forceinline__ void times(Row& x, float f) {
+  const float2 ff = make_float2(f, f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x.a[i] = ptx::fmul2(x.a[i], ff);
+    x.b[i] = ptx::fmul2(x.b[i], ff);
+  }
+}
+// This lane's part of the rows' product.
+__device__ __forceinline__ float dot(const Row& x, const Row& y) {
+  float2 a = ptx::fmul2(x.a[0], y.a[0]), b = ptx::fmul2(x.b[0], y.b[0]);
+#pragma unroll
+  for (int i = 1; i < 4; ++i) {
+    a = ptx::ffma2(x.a[i], y.a[i], a);
+    b = ptx::ffma2(x.b[i], y.b[i], b);
+  }
+  a = ptx::fadd2(a, b);
+  return a.x + a.y;
 }
 
 // Sum over the lanes of a row.
@@ -171,15 +257,15 @@ __device__ __forceinline__ float row_sum(float x) {
 }
 
 template <int D>
-__device__ __forceinline__ float inverse_deviation(const float (&x)[16], float eps) {
-  float q[2] = {0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < 16; ++i) q[i & 1] = fmaf(x[i], x[i], q[i & 1]);
-  return rsqrtf(fmaf(row_sum<D>(q[0] + q[1]), 1.f / D, eps));
+__device__ __forceinline__ float inverse_deviation(const Row& x, float eps) {
+  return rsqrtf(fmaf(row_sum<D>(dot(x, x)), 1.f / D, eps));
 }
 
 // Sixteen codes of a lane's row into a cache page.
-__device__ __forceinline__ void store_codes(uint8_t* row, const Place& p, const float (&x)[16], float inv) {
+template <bool INTER>
+__device__ __forceinline__ void store_codes(uint8_t* row, const Place& p, const Row& y, float inv) {
+  float x[16];
+  in_order<INTER>(y, x);
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -226,6 +312,7 @@ __global__ void __launch_bounds__(kThreads, fwd_ctas_per_sm(NORM, MODE)) fa_rope
   __shared__ unsigned long long turn[D / 2];
   __shared__ float4 weights[NORM ? 2 : 1][NORM ? D / 4 : 1];
   __shared__ Angles<D> angles[kWarps];
+  extern __shared__ __align__(16) unsigned char ring_at[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = lane / kLanes, part_of = lane % kLanes;
   ptx::grid_release();
   ptx::grid_wait();
@@ -235,6 +322,7 @@ __global__ void __launch_bounds__(kThreads, fwd_ctas_per_sm(NORM, MODE)) fa_rope
     if (a.part[1].heads) stage_weights<D, INTER>(a, a.part[1].w, weights[1]);
   }
   __syncthreads();
+  Ring<kAhead, 1> ring(ring_at);
   const float inv_k = MODE == kStore && a.fp8 ? 1.f / a.descale_k : 1.f;
   const long long first_k = a.units[0], first_v = first_k + a.units[1];
   const long long units = MODE == kStore ? first_v + a.units[1] : first_v;
@@ -256,62 +344,64 @@ __global__ void __launch_bounds__(kThreads, fwd_ctas_per_sm(NORM, MODE)) fa_rope
         place_in_cache = (((long long)page * part.heads) << a.page_shift) + (slot & ((1 << a.page_shift) - 1));
       }
     }
-    const Place p = value ? place<true>(part_of, 0) : place<INTER>(part_of, a.rot);
+    const Place p = value ? place<D, true>(part_of, 0) : place<D, INTER>(part_of, a.rot);
     const RopeView& src = value ? a.v : part.in;
-    const long long from = u.token.b * src.b + u.token.n * src.n;
     int h = u.h;
     const int step = a.groups[kind];
-    // the rows of the next kAhead steps are on their way while one is worked on
-    constexpr int kAhead = 2;
-    Raw ahead[kAhead];
+    const __nv_bfloat16* row = static_cast<const __nv_bfloat16*>(src.at) + (u.token.b * src.b + u.token.n * src.n);
+    auto load = [&](int k, int ahead) {  // for step k, 'ahead' steps on
+      if (k < u.steps) {
+        const bool there = h + ahead * step < u.h1;
+        ring.load(0, row + (there ? (h + ahead * step) * src.h : 0), p, there);
+      }
+      ring.loaded(k < u.steps);
+    };
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      ahead[k] = Raw{};
-      if (h + k * step < u.h1) ahead[k] = load_row(src, from + (h + k * step) * src.h, p);
-    }
+    for (int k = 0; k < kAhead; ++k) load(k, k);
     if (MODE == kStore && value) {
       for (int k = 0; k < u.steps; ++k, h += step) {
-        const Raw raw = ahead[0];
-        ahead[0] = ahead[1];
-        if (h + kAhead * step < u.h1) ahead[1] = load_row(src, from + (h + kAhead * step) * src.h, p);
+        ring.wait();
+        const Raw raw = ring.get(0);
+        ring.taken();
+        load(k + kAhead, kAhead);
         if (h >= u.h1) continue;
-        const long long at = (place_in_cache + ((long long)h << a.page_shift)) * D + p.a;
+        const long long at = (place_in_cache + ((long long)h << a.page_shift)) * D;
         if (a.fp8) {
           const Factor f = factor_of(a.descale_v);
-          *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.v_cache) + at) =
-              make_uint4(quantise4(raw.a.x, raw.a.y, f), quantise4(raw.a.z, raw.a.w, f), quantise4(raw.b.x, raw.b.y, f),
-                         quantise4(raw.b.z, raw.b.w, f));
+          uint8_t* dst = static_cast<uint8_t*>(a.v_cache) + at;
+          *reinterpret_cast<uint2*>(dst + p.a) = make_uint2(quantise4(raw.a.x, raw.a.y, f), quantise4(raw.a.z, raw.a.w, f));
+          *reinterpret_cast<uint2*>(dst + p.b) = make_uint2(quantise4(raw.b.x, raw.b.y, f), quantise4(raw.b.z, raw.b.w, f));
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.v_cache) + at);
-          dst[0] = raw.a;
-          dst[1] = raw.b;
+          __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.v_cache) + at;
+          *reinterpret_cast<uint4*>(dst + p.a) = raw.a;
+          *reinterpret_cast<uint4*>(dst + p.b) = raw.b;
         }
       }
       continue;
     }
-    float c[8], s[8];
-    make_angles<D>(a, turn, angles[warp], a.tokens[kind], u.first, lane, 1.f);
-    take_angles<D>(angles[warp], a.tokens[kind] > 1 ? group / step : 0, part_of, c, s);
+    make_angles<D, INTER>(a, turn, angles[warp], a.tokens[kind], u.first, lane, 1.f);
+    const Turn t = take_angles<D>(angles[warp], a.tokens[kind] > 1 ? group / step : 0, part_of);
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(part.out.at) + (u.token.b * part.out.b + u.token.n * part.out.n);
     for (int k = 0; k < u.steps; ++k, h += step) {  // (uniform: the sums of a row are a warp's work)
-      float x[16];
-      unpack(ahead[0], x);
-#pragma unroll
-      for (int e = 0; e + 1 < kAhead; ++e) ahead[e] = ahead[e + 1];
-      if (h + kAhead * step < u.h1) ahead[kAhead - 1] = load_row(src, from + (h + kAhead * step) * src.h, p);
+      ring.wait();
+      Row x = unpack<INTER>(ring.get(0));
+      ring.taken();
+      load(k + kAhead, kAhead);
       if (NORM) {
         const float r = inverse_deviation<D>(x, a.eps);
-        times_weights<D>(x, weights[kind], part_of, r);
+        times_weights<D>(x, weights[kind], part_of);
+        times(x, r);
       }
-      rotate<INTER>(x, c, s);
+      rotate(x, t);
       if (h >= u.h1) continue;
       if (MODE == kStore && kind) {
         const long long at = (place_in_cache + ((long long)h << a.page_shift)) * D;
         if (a.fp8)
-          store_codes(static_cast<uint8_t*>(a.k_cache) + at, p, x, inv_k);
+          store_codes<INTER>(static_cast<uint8_t*>(a.k_cache) + at, p, x, inv_k);
         else
-          store_row(RopeView{a.k_cache, 0, 0, 0}, at, p, x);
+          store_row<INTER>(static_cast<__nv_bfloat16*>(a.k_cache) + at, p, x);
       } else {
-        store_row(part.out, u.token.b * part.out.b + u.token.n * part.out.n + h * part.out.h, p, x);
+        store_row<INTER>(out + h * part.out.h, p, x);
       }
     }
   }
@@ -321,14 +411,16 @@ __global__ void __launch_bounds__(kThreads, fwd_ctas_per_sm(NORM, MODE)) fa_rope
 // gradients of its 16 elements in registers; the sums of a CTA go to the workspace, and a second kernel adds those up in
 // order (no atomics: repeated calls give the same bits).
 constexpr int kMaxSms = 160;
-constexpr int bwd_ctas_per_sm(bool norm) { return norm ? 2 : 3; }
+// (Without norms 3 and 4 of them, 16384 tokens of 32 + 8 heads of 128 and 32768 of 64: 53.0 and 57.1 us, 65.9 and 58.3 us.)
+constexpr int bwd_ctas_per_sm(bool norm, int d) { return norm ? 2 : d == 64 ? 4 : 3; }
 template <int D, bool NORM, bool INTER>
-__global__ void __launch_bounds__(kThreads, bwd_ctas_per_sm(NORM)) fa_rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, bwd_ctas_per_sm(NORM, D)) fa_rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int kLanes = D / 16;
   __shared__ unsigned long long turn[D / 2];
   __shared__ float sums[NORM ? kWarps : 1][D];
   __shared__ float4 weights[NORM ? D / 4 : 1];
   __shared__ Angles<D> angles[kWarps];
+  extern __shared__ __align__(16) unsigned char ring_at[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = lane / kLanes, part_of = lane % kLanes;
   ptx::grid_release();
   ptx::grid_wait();
@@ -337,67 +429,69 @@ __global__ void __launch_bounds__(kThreads, bwd_ctas_per_sm(NORM)) fa_rope_bwd_k
   for (int i = threadIdx.x; i < a.rot / 2; i += kThreads) turn[i] = turns(a.freqs[i]);
   if constexpr (NORM) stage_weights<D, INTER>(a, part.w, weights);
   __syncthreads();
+  Ring<kAhead, NORM ? 2 : 1> ring(ring_at);
   const int cta = (int)blockIdx.x - (kind ? a.ctas[0] : 0), step = a.groups[kind];
-  const Place p = place<INTER>(part_of, a.rot);
-  float dw[16];
+  const Place p = place<D, INTER>(part_of, a.rot);
+  Row dw;
 #pragma unroll
-  for (int e = 0; e < 16; ++e) dw[e] = 0.f;
+  for (int e = 0; e < 4; ++e) dw.a[e] = dw.b[e] = make_float2(0.f, 0.f);
   for (long long i = (long long)cta * kWarps + warp; i < a.units[kind]; i += (long long)a.ctas[kind] * kWarps) {
     const Unit u = unit(a, kind, i, group);
-    const long long from = u.token.b * part.in.b + u.token.n * part.in.n, x_from = u.token.b * part.x.b + u.token.n * part.x.n;
     int h = u.h;
-    constexpr int kAhead = 2;  // as in the forward
-    Raw ahead[kAhead], ahead_x[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      ahead[k] = ahead_x[k] = Raw{};
-      if (h + k * step < u.h1) {
-        ahead[k] = load_row(part.in, from + (h + k * step) * part.in.h, p);
-        if (NORM) ahead_x[k] = load_row(part.x, x_from + (h + k * step) * part.x.h, p);
+    const __nv_bfloat16 *in = static_cast<const __nv_bfloat16*>(part.in.at) + (u.token.b * part.in.b + u.token.n * part.in.n),
+                        *in_x = static_cast<const __nv_bfloat16*>(part.x.at) + (u.token.b * part.x.b + u.token.n * part.x.n);
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(part.out.at) + (u.token.b * part.out.b + u.token.n * part.out.n);
+    auto load = [&](int k, int ahead) {
+      if (k < u.steps) {
+        const bool there = h + ahead * step < u.h1;
+        const int hh = there ? h + ahead * step : 0;
+        ring.load(0, in + hh * part.in.h, p, there);
+        if (NORM) ring.load(NORM ? 1 : 0, in_x + hh * part.x.h, p, there);
       }
-    }
-    float c[8], s[8];
-    make_angles<D>(a, turn, angles[warp], a.tokens[kind], u.first, lane, -1.f);
-    take_angles<D>(angles[warp], a.tokens[kind] > 1 ? group / step : 0, part_of, c, s);
+      ring.loaded(k < u.steps);
+    };
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) load(k, k);
+    make_angles<D, INTER>(a, turn, angles[warp], a.tokens[kind], u.first, lane, -1.f);
+    const Turn t = take_angles<D>(angles[warp], a.tokens[kind] > 1 ? group / step : 0, part_of);
     for (int k = 0; k < u.steps; ++k, h += step) {
-      float g[16], x[16];
-      unpack(ahead[0], g);
-      if (NORM) unpack(ahead_x[0], x);
-#pragma unroll
-      for (int e = 0; e + 1 < kAhead; ++e) {
-        ahead[e] = ahead[e + 1];
-        ahead_x[e] = ahead_x[e + 1];
-      }
-      if (h + kAhead * step < u.h1) {
-        ahead[kAhead - 1] = load_row(part.in, from + (h + kAhead * step) * part.in.h, p);
-        if (NORM) ahead_x[kAhead - 1] = load_row(part.x, x_from + (h + kAhead * step) * part.x.h, p);
-      }
+      ring.wait();
+      Row g = unpack<INTER>(ring.get(0)), x;
+      if (NORM) x = unpack<INTER>(ring.get(NORM ? 1 : 0));
+      ring.taken();
+      load(k + kAhead, kAhead);
       const bool live = h < u.h1;
-      rotate<INTER>(g, c, s);
+      rotate(g, t);
       if (NORM) {
-        const float r = inverse_deviation<D>(x, a.eps);
-        float m[2] = {0.f, 0.f};
+        const float all = inverse_deviation<D>(x, a.eps);  // (sums over lanes: every lane takes part)
+        const float r = live ? all : 0.f;  // no row: zeros, which add nothing to dw, whatever eps
+        times(x, r);  // the normed row before its weights
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          x[e] *= r;  // the normed row before its weights
-          if (live) dw[e] = fmaf(g[e], x[e], dw[e]);
+        for (int e = 0; e < 4; ++e) {
+          dw.a[e] = ptx::ffma2(g.a[e], x.a[e], dw.a[e]);
+          dw.b[e] = ptx::ffma2(g.b[e], x.b[e], dw.b[e]);
         }
-        times_weights<D>(g, weights, part_of, 1.f);
+        times_weights<D>(g, weights, part_of);
+        const float mean = row_sum<D>(dot(g, x)) * (1.f / D);
+        const float2 m = make_float2(-mean, -mean);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) m[e & 1] = fmaf(g[e], x[e], m[e & 1]);
-        const float mean = row_sum<D>(m[0] + m[1]) * (1.f / D);
-#pragma unroll
-        for (int e = 0; e < 16; ++e) g[e] = r * fmaf(-x[e], mean, g[e]);
+        for (int e = 0; e < 4; ++e) {
+          g.a[e] = ptx::ffma2(x.a[e], m, g.a[e]);
+          g.b[e] = ptx::ffma2(x.b[e], m, g.b[e]);
+        }
+        times(g, r);
       }
-      if (live) store_row(part.out, u.token.b * part.out.b + u.token.n * part.out.n + h * part.out.h, p, g);
+      if (live) store_row<INTER>(out + h * part.out.h, p, g);
     }
   }
   if constexpr (NORM) {
+    float sum[16];
+    in_order<INTER>(dw, sum);
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
 #pragma unroll
-      for (int s = kLanes; s < 32; s <<= 1) dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], s);
-      if (group == 0) sums[warp][(e < 8 ? p.a : p.b - 8) + e] = dw[e];
+      for (int s = kLanes; s < 32; s <<= 1) sum[e] += __shfl_xor_sync(0xffffffffu, sum[e], s);
+      if (group == 0) sums[warp][(e < 8 ? p.a : p.b - 8) + e] = sum[e];
     }
     __syncthreads();
     for (int i = threadIdx.x; i < D; i += kThreads) {
@@ -489,14 +583,20 @@ cudaError_t launch_forward(const RopeArgs& args, bool norm, bool inter, int num_
   RopeArgs a = args;
   make_units(a, 32 / (D / 16), num_sms);
   const long long units = a.units[0] + (MODE == kStore ? 2 : 1) * a.units[1];
-  // As many CTAs as run at once, or twice that, their warps over the units in turn: the frequencies and weights are staged
-  // once for all. Once, twice and a warp a unit, for 16384 tokens of 32 + 8 heads of 128: without norms 61.6, 56.9 and 57.5 us
-  // (5.9 TB/s), with norms 66.0 (5.1 TB/s), 66.5 and 68.5 us; the store of 15523 tokens to E4M3 71.6, 70.6 and 78.7 us.
-  const long long resident = (long long)num_sms * fwd_ctas_per_sm(norm, MODE) * (norm ? 1 : 2);
+  // As many CTAs as run at once, or twice that where their warps have five units each and more, the units in turn: the
+  // frequencies and weights are staged once for all. Once, twice and a warp a unit, for 16384 tokens of 32 + 8 heads of 128:
+  // without norms 64.2, 55.5 and 54.2 us, with norms 63.3, 58.4 and 61.0 us; the store of 15523 tokens to E4M3 70.0, 68.3 and
+  // 74.7 us; with four units a warp, norms of 8008 tokens of 12 + 12 heads of 64, 13.5, 15.0 and 15.7 us.
+  const long long once = (long long)num_sms * fwd_ctas_per_sm(norm, MODE);
+  const long long resident = units >= 5 * once * kWarps ? 2 * once : once;
   const unsigned ctas = (unsigned)std::min<long long>((units + kWarps - 1) / kWarps, resident);
   auto kern = norm ? (inter ? fa_rope_kernel<D, true, true, MODE> : fa_rope_kernel<D, true, false, MODE>)
                    : (inter ? fa_rope_kernel<D, false, true, MODE> : fa_rope_kernel<D, false, false, MODE>);
-  return launch_dependent(kern, dim3(ctas), kThreads, 0, stream, a);
+  constexpr int kBytes = Ring<kAhead, 1>::kBytes;
+  static std::atomic<unsigned long long> known[4];  // devices that know the kernels' shared memory
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), kBytes, known[2 * norm + inter]);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kern, dim3(ctas), kThreads, kBytes, stream, a);
 }
 
 // CTAs of the backward for each part, in the ratio of the steps that they have to take.
@@ -505,7 +605,7 @@ void backward_ctas(RopeArgs& a, int groups, bool norm, int num_sms) {
   double steps[2];
   for (int k = 0; k < 2; ++k)
     steps[k] = (double)a.units[k] * ((std::min(a.part[k].heads, a.slice_heads[k]) + a.groups[k] - 1) / a.groups[k] + 0.5 + 0.5 * a.tokens[k]);
-  const int all = std::min(num_sms, kMaxSms) * bwd_ctas_per_sm(norm);
+  const int all = std::min(num_sms, kMaxSms) * bwd_ctas_per_sm(norm, a.d);
   for (int k = 0; k < 2; ++k) {
     const int most = std::max(1, (int)(all * steps[k] / (steps[0] + steps[1]) + 0.5));
     a.ctas[k] = (int)std::min<long long>((a.units[k] + kWarps - 1) / kWarps, most);
@@ -518,7 +618,11 @@ cudaError_t launch_backward(const RopeArgs& args, bool norm, bool inter, int num
   backward_ctas(a, 32 / (D / 16), norm, num_sms);
   auto kern = norm ? (inter ? fa_rope_bwd_kernel<D, true, true> : fa_rope_bwd_kernel<D, true, false>)
                    : (inter ? fa_rope_bwd_kernel<D, false, true> : fa_rope_bwd_kernel<D, false, false>);
-  const cudaError_t e = launch_dependent(kern, dim3((unsigned)(a.ctas[0] + a.ctas[1])), kThreads, 0, stream, a);
+  const int bytes = norm ? Ring<kAhead, 2>::kBytes : Ring<kAhead, 1>::kBytes;
+  static std::atomic<unsigned long long> known[4];
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), bytes, known[2 * norm + inter]);
+  if (e != cudaSuccess) return e;
+  e = launch_dependent(kern, dim3((unsigned)(a.ctas[0] + a.ctas[1])), kThreads, bytes, stream, a);
   if (e != cudaSuccess || !norm) return e;
   return launch_dependent(fa_rope_dw_kernel, dim3(D / 32, 2u), 32 * kSumWarps, 0, stream, a);
 }
@@ -526,7 +630,7 @@ cudaError_t launch_backward(const RopeArgs& args, bool norm, bool inter, int num
 }  // namespace
 
 size_t rope_bwd_bytes(int Hq, int Hk, int d) {
-  return Hq + Hk > 0 ? (size_t)(kMaxSms * bwd_ctas_per_sm(true) + 2) * d * sizeof(float) : 0;
+  return Hq + Hk > 0 ? (size_t)(kMaxSms * bwd_ctas_per_sm(true, d) + 2) * d * sizeof(float) : 0;
 }
 
 cudaError_t launch_rope_fwd(RopeArgs a, bool norm, bool inter, int num_sms, cudaStream_t stream) {
