@@ -15,10 +15,11 @@
 //      accumulates dK and dV in tensor memory (TMEM).
 //   3. bwd_dq:   one CTA per 128-row query block, looping over 128-key blocks;
 //      accumulates dQ in TMEM.
-// At d = 64 the dQ kernel runs first and forms D itself, from the dO tile it
-// loads anyway and an O tile loaded beside it, and writes it for the dK/dV
-// kernel after it: a small start kernel only resets the work counters, and dO
-// is read from device memory twice instead of three times.
+// At d = 64, and under a window at both sizes, the dQ kernel runs first and forms
+// D itself, from the dO tile it loads anyway and an O tile loaded beside it (at
+// d = 128 O's rows in global memory), and writes it for the dK/dV kernel after
+// it: a small start kernel only resets the work counters, and dO is read from
+// device memory twice instead of three times.
 // Both main kernels rebuild S and dP; dQ is summed on chip in a fixed order,
 // so the result is deterministic and no fp32 atomics are needed (on GB300 the
 // L2's atomic-add rate, about 1.1-1.4e12 fp32 adds/s, would otherwise bound
@@ -42,6 +43,14 @@
 // grouped heads (each tile walks only the blocks that it sees, and a dK/dV tile
 // the query heads that share its key head one after another) without changing
 // the plain kernels.
+//
+// Under a window tiles are short, so a tile's start and end count: the next tile is
+// taken, and its row terms, Q and O are on their way, during the last blocks of the
+// one before; tiles without work are the loading warp's. 4 x 4096 tokens, 32 heads
+// over 8 of 128, window 512: 414 us (780 TFLOP/s of the pairs seen), about 200 us of them dQ
+// (an unmasked block 1550 cycles, one at the window's edge 2100, a tile 3000 besides); with 4
+// sinks 465 us, since a sink's dK/dV tile walks all N / 128 query blocks of all its
+// heads; 8 x 4096 at d = 64 702 us. Window 4096, 16384 tokens: 1.93 ms, 1245 TFLOP/s.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -683,7 +692,10 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dkdv_kernel(const __grid_consta
           continue;
         }
         tc_fence_after();
-        uint32_t pk[32];  // P^T row r, queries 64 w .. 64 w + 63, as bf16 pairs
+        // P^T row r, queries 64 w .. 64 w + 63, as bf16 pairs; WIN: fp32, so that dS is of the exact P and only the product
+        // with dO of the rounded one (dk off by 0.0024 of its size instead of 0.0029, and no unpacking)
+        uint32_t pk[WIN ? 1 : 32];
+        float2 pf[WIN ? 32 : 1];
         {
           uint32_t sr[2][32];
           tmem_ld32(t_s, sr[0]);
@@ -727,8 +739,14 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dkdv_kernel(const __grid_consta
                                        scale2, make_float2(nl.x, nl.y));
               const float2 x23 = ffma2(make_float2(__uint_as_float(sr[h][c + 2]), __uint_as_float(sr[h][c + 3])),
                                        scale2, make_float2(nl.z, nl.w));
-              pk[col >> 1] = pack_bf16x2(ex2(x01.x), ex2(x01.y));
-              pk[(col >> 1) + 1] = pack_bf16x2(ex2(x23.x), ex2(x23.y));
+              const float2 p01 = make_float2(ex2(x01.x), ex2(x01.y)), p23 = make_float2(ex2(x23.x), ex2(x23.y));
+              if constexpr (WIN) {
+                pf[col >> 1] = p01;
+                pf[(col >> 1) + 1] = p23;
+              } else {
+                pk[col >> 1] = pack_bf16x2(p01.x, p01.y);
+                pk[(col >> 1) + 1] = pack_bf16x2(p23.x, p23.y);
+              }
             }
           }
         }
@@ -766,7 +784,15 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dkdv_kernel(const __grid_consta
           for (int c = 0; c < 32; c += 4) {
             const int col = 32 * h + c;
             const float4 nd = rb4[16 + (col >> 2)];  // -D
-            const uint32_t pa = pk[col >> 1], pb = pk[(col >> 1) + 1];
+            float2 p01, p23;
+            if constexpr (WIN) {
+              p01 = pf[col >> 1];
+              p23 = pf[(col >> 1) + 1];
+            } else {
+              const uint32_t pa = pk[col >> 1], pb = pk[(col >> 1) + 1];
+              p01 = make_float2(__uint_as_float(pa << 16), __uint_as_float(pa & 0xFFFF0000u));
+              p23 = make_float2(__uint_as_float(pb << 16), __uint_as_float(pb & 0xFFFF0000u));
+            }
             const float2 dp01 = make_float2(__uint_as_float(dp[c]), __uint_as_float(dp[c + 1]));
             const float2 dp23 = make_float2(__uint_as_float(dp[c + 2]), __uint_as_float(dp[c + 3]));
             float2 e01, e23;  // dP - D, with dropout Z dP - D (Z = 0 or 1 / (1 - p))
@@ -781,14 +807,13 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dkdv_kernel(const __grid_consta
               e01 = fadd2(dp01, make_float2(nd.x, nd.y));
               e23 = fadd2(dp23, make_float2(nd.z, nd.w));
             }
-            const float2 d01 = fmul2(make_float2(__uint_as_float(pa << 16), __uint_as_float(pa & 0xFFFF0000u)), e01);
-            const float2 d23 = fmul2(make_float2(__uint_as_float(pb << 16), __uint_as_float(pb & 0xFFFF0000u)), e23);
+            const float2 d01 = fmul2(p01, e01), d23 = fmul2(p23, e23);
             dsk[c >> 1] = pack_bf16x2(d01.x, d01.y);
             dsk[(c >> 1) + 1] = pack_bf16x2(d23.x, d23.y);
           }
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            pkh[i] = pk[16 * h + i];
+            pkh[i] = WIN ? pack_bf16x2(pf[WIN ? 16 * h + i : 0].x, pf[WIN ? 16 * h + i : 0].y) : pk[WIN ? 0 : 16 * h + i];
             if constexpr (DROP)  // the dropped P^T feeds dV (pair 16 h + i: queries 32 h + 2 i, + 1)
               pkh[i] &= (i & 1) ? philox::pair_mask_hi(kw[(16 * h + i) >> 1]) : philox::pair_mask_lo(kw[(16 * h + i) >> 1]);
           }

@@ -20,6 +20,14 @@
 // Every block but those where a window begins or ends (and a sink block beyond its sinks) is
 // unmasked: its row maximum comes with the TMEM load.
 //
+// Bound by a block's chain of S, softmax and P V (about 2950 cycles for the blocks of
+// two tiles, 2048 of them products) and, where windows are short, by what a tile costs besides: 16384
+// tokens, 32 heads over 8 of 128, window 4096, 4 sinks 669 us, 1440 TFLOP/s of the pairs seen;
+// 4 x 4096 tokens, window 512, 143 us (900 TFLOP/s; of the blocks' keys a fifth is hidden),
+// with 4 sinks 163 us. Issuing both tiles' first S of the next item before this one's last
+// products cost more than it gave (158 and 162 us, window 4096 692 and 721 us): what stands
+// in the MMA warp's way delays every block.
+//
 // Warp roles: a softmax warpgroup per tile, the TMA warp, the MMA warp.
 #include <algorithm>
 

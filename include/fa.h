@@ -393,10 +393,10 @@ FA_API int fa_fwd_paged(const void* q, long long q_stride, const void* k_cache, 
 /*
  * fa_fwd_paged (causal) with a sliding window: a token sees the last 'window'
  * keys of its request up to its own (window >= 1), and the request's first
- * 'sinks' keys (>= 0). Pages of which no token of a tile sees a key are not read
- * and count as zeros, whatever the table says of them, so those that a request's window has
- * left may be given to others (their entries stay in range or not, nothing is reported); hidden keys
- * on pages that are read must hold finite values. The time goes by the keys that are seen. Other
+ * 'sinks' keys (>= 0). A page between the sinks and the windows of all the
+ * request's new tokens is not read, whatever its entry in the table says, so it
+ * may be given to another request; keys beside visible ones on a page that is
+ * read must hold finite values. The time goes by the keys that are seen. Other
  * arguments, results and errors as in fa_fwd_paged, with the same workspace.
  */
 FA_API int fa_fwd_paged_window(const void* q, long long q_stride, const void* k_cache, const void* v_cache, int fp8,
@@ -508,10 +508,11 @@ FA_API int fa_paged_rope_store(const void* q, const void* k, const void* v, long
  *   Nq <= Nk
  *   seqlens_q, seqlens_k
  *                  as in fa_fwd_kv; the rule above is written for a sequence's own lengths
- * B * Hq * Nq * d and B * Hkv * Nk * d stay below 2^31. The workspace holds D
- * for the rows, the work counters and, with sinks, parts of their keys'
- * gradients. dk and dv of a key head are sums over the query heads that share
- * it, in a fixed order: repeated calls give identical bits.
+ * B * Hq * Nq * d and B * Hkv * Nk * d stay below 2^31. The backward's workspace
+ * holds D for the rows and the work counters (16-byte aligned; contents do not
+ * matter; not shared by calls that may run at once). dk and dv of a key head are
+ * sums over the query heads that share it, in a fixed order: repeated calls give
+ * identical bits.
  * Returns FA_OK or an fa_status error code.
  */
 FA_API int fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int B, int Hq, int Hkv,

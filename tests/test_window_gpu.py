@@ -2,7 +2,7 @@
 
 Tolerances: the bounds that window_ref.attention derives from the roundings; over whole tensors the relative RMS errors of
 independent roundings spread over half a step (2^-8 / sqrt(3) = 0.00226 each): o has two of them (0.0032), dv two, dq and dk
-three, of which that of P stands in D too: below 0.005 with room for few rows; one key too many or too few of a window of 200
+two and those of o in D: below 0.005 with room for few rows; one key too many or too few of a window of 200
 is 0.07.
 """
 import math

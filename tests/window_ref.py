@@ -19,7 +19,7 @@ def attention(q, k, v, window, sinks, scale, sq=None, sk=None, dO=None):
     The scores are fp32 sums of d products: off by at most d 2^-23 sum |q_i k_i| scale, below e = 2^-10 for the normal inputs
     here (|s| below 16), which moves every weight by that much relatively and the logsumexp absolutely. P enters both
     products with V (forward) and dO (dV) as bf16, half a step; o, dq, dk and dv are rounded to bf16 once. The backward's D
-    is the row sum of dO times the rounded o; dS is made of P, in dK/dV the rounded one, and of dP - D, and rounded to bf16."""
+    is the row sum of dO times the rounded o; dS is made of the fp32 P and of dP - D, and rounded to bf16."""
     Nq, Nk = q.shape[0], k.shape[0]
     sq, sk = sq or Nq, sk or Nk
     q, k, v = q.double(), k.double(), v.double()
@@ -39,7 +39,7 @@ def attention(q, k, v, window, sinks, scale, sq=None, sk=None, dO=None):
         dP = g @ v.T
         D = (g * o).sum(1, keepdim=True)
         dS = P * (dP - D)
-        off = P * (bo * g.abs()).sum(1, keepdim=True) + (2 * HALF + 2 * e) * dS.abs() + e * P * (g.abs() @ v.abs().T)
+        off = P * (bo * g.abs()).sum(1, keepdim=True) + (HALF + 2 * e) * dS.abs() + e * P * (g.abs() @ v.abs().T)
         r.update(dq=scale * dS @ k, dk=scale * dS.T @ q, dv=P.T @ g)
         r.update(bound_dq=HALF * r["dq"].abs() + scale * off @ k.abs() + tiny, bound_dk=HALF * r["dk"].abs() + scale * off.T @ q.abs() + tiny,
                  bound_dv=HALF * r["dv"].abs() + (HALF + e) * (P.T @ g.abs()) + tiny)
