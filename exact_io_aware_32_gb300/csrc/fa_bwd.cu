@@ -47,10 +47,10 @@
 // Under a window tiles are short, so a tile's start and end count: the next tile is
 // taken, and its row terms, Q and O are on their way, during the last blocks of the
 // one before; tiles without work are the loading warp's. 4 x 4096 tokens, 32 heads
-// over 8 of 128, window 512: 414 us (780 TFLOP/s of the pairs seen), about 200 us of them dQ
-// (an unmasked block 1550 cycles, one at the window's edge 2100, a tile 3000 besides); with 4
-// sinks 465 us, since a sink's dK/dV tile walks all N / 128 query blocks of all its
-// heads; 8 x 4096 at d = 64 702 us. Window 4096, 16384 tokens: 1.93 ms, 1245 TFLOP/s.
+// over 8 of 128, window 512: 411 us (783 TFLOP/s of the pairs seen), about 200 us of them dQ
+// (an unmasked block 1650 cycles, one with a mask 2100, a tile 3900 besides); with 4
+// sinks 460 us, since a sink's dK/dV tile walks all N / 128 query blocks of all its
+// heads; 8 x 4096 at d = 64 700 us. Window 4096, 16384 tokens: 1.94 ms, 1240 TFLOP/s.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -1338,16 +1338,25 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
     int L = take_tile(0, t);
     bool ok = L >= 0;
     float lse2 = 0.f, dsum = 0.f;
-    uint4 orow[C::kTileO ? 1 : 8];  // (kFuseD without kTileO) this thread's half of O's row
-    auto o_at = [&](const DqTile& t) {
-      return reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.o) +
-                                            (((size_t)t.bh * Nq + min(t.qblk * C::BQ + r, Nq - 1)) * D + 64 * w) * 2);
+    // (kFuseD without kTileO) the group's half of O's rows: of the warp's 32 rows, eight lanes take a row's eight chunks, four
+    // rows at a time (a row a lane would be 32 lines a load, 2000 cycles of a tile)
+    uint4 o_part[C::kTileO ? 1 : 8];
+    auto o_row = [&](const DqTile& t, int row) {
+      return static_cast<const uint8_t*>(a.o) + (((size_t)t.bh * Nq + min(t.qblk * C::BQ + row, Nq - 1)) * D + 64 * w) * 2;
     };
     auto load_o = [&](const DqTile& t) {
       if constexpr (C::kFuseD && !C::kTileO) {
-        const uint4* at = o_at(t);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) orow[c] = at[c];
+        for (int i = 0; i < 8; ++i)
+          o_part[i] = *reinterpret_cast<const uint4*>(o_row(t, (warp & 3) * 32 + 4 * i + (lane >> 3)) + 16 * (lane & 7));
+      }
+    };
+    auto dot8 = [](const uint4& x, const uint4& y, float& acc0, float& acc1) {  // of two chunks of eight
+      const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        acc0 = fmaf(__uint_as_float(xs[h] << 16), __uint_as_float(ys[h] << 16), acc0);
+        acc1 = fmaf(__uint_as_float(xs[h] & 0xFFFF0000u), __uint_as_float(ys[h] & 0xFFFF0000u), acc1);
       }
     };
     if (ok) {
@@ -1367,32 +1376,51 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
         const int ds = do_slot(k);
         ok = __all_sync(0xffffffffu, mbar_wait(&bars.do_full[ds], do_use(k), abort_flag));
         if (!ok) break;
-        float acc0 = 0.f, acc1 = 0.f;
-        constexpr int kChunks = C::kHalves && C::kTileO ? 4 : 8;  // 16-byte chunks of this thread's part of the row
+        float drow;
+        int own = r;  // the row that this thread has summed
+        if constexpr (C::kTileO) {
+          float acc0 = 0.f, acc1 = 0.f;
+          constexpr int kChunks = C::kHalves ? 4 : 8;  // 16-byte chunks of this thread's part of the row
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-          const int c = kChunks == 4 ? 4 * w + i : i;
-          const int off = ds * C::kTileBytes + r * 128 + ((c ^ (r & 7)) << 4);  // chunk c of the 128-byte-swizzled row
-          const uint4 x = *reinterpret_cast<const uint4*>(smem + C::kOffDO + (C::kTileO ? 0 : w * kPanelBytes) + off);
-          const uint4 y = C::kTileO ? *reinterpret_cast<const uint4*>(smem + C::kOffO + off) : orow[C::kTileO ? 0 : c];
-          const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-          for (int h = 0; h < 4; ++h) {
-            acc0 = fmaf(__uint_as_float(xs[h] << 16), __uint_as_float(ys[h] << 16), acc0);
-            acc1 = fmaf(__uint_as_float(xs[h] & 0xFFFF0000u), __uint_as_float(ys[h] & 0xFFFF0000u), acc1);
+          for (int i = 0; i < kChunks; ++i) {
+            const int c = kChunks == 4 ? 4 * w + i : i;
+            const int off = ds * C::kTileBytes + r * 128 + ((c ^ (r & 7)) << 4);  // chunk c of the 128-byte-swizzled row
+            dot8(*reinterpret_cast<const uint4*>(smem + C::kOffDO + off), *reinterpret_cast<const uint4*>(smem + C::kOffO + off), acc0,
+                 acc1);
           }
+          drow = acc0 + acc1;
+        } else {
+          float sum[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int row = (warp & 3) * 32 + 4 * i + (lane >> 3);
+            const int off = ds * C::kTileBytes + row * 128 + (((lane & 7) ^ (row & 7)) << 4);
+            float acc0 = 0.f, acc1 = 0.f;
+            dot8(*reinterpret_cast<const uint4*>(smem + C::kOffDO + w * kPanelBytes + off), o_part[i], acc0, acc1);
+            sum[i] = acc0 + acc1;
+          }
+          // the eight lanes' sums of eight rows: at each step a lane keeps half of the rows and adds its partner's part
+#pragma unroll
+          for (int s = 4; s > 0; s >>= 1) {
+            const bool upper = lane & s;
+#pragma unroll
+            for (int i = 0; i < s; ++i) {
+              const float keep = upper ? sum[i + s] : sum[i], give = upper ? sum[i] : sum[i + s];
+              sum[i] = keep + __shfl_xor_sync(0xffffffffu, give, s);
+            }
+          }
+          drow = sum[0];
+          own = (warp & 3) * 32 + 4 * (lane & 7) + (lane >> 3);
         }
         mbar_arrive(&bars.do_empty[ds]);
-        float drow = acc0 + acc1;
         if constexpr (C::kHalves) {
-          // (read by the other group at once: its next use comes after products that need both groups' dS)
+          // (read at once: its next use comes after products that need both groups' dS)
           float* half = reinterpret_cast<float*>(smem + C::kOffHalf);
-          half[w * 128 + r] = drow;
+          half[w * 128 + own] = drow;
           mbar_arrive(&bars.half_ready);
           ok = __all_sync(0xffffffffu, mbar_wait(&bars.half_ready, k & 1, abort_flag));
           if (!ok) break;
-          const float other = half[(w ^ 1) * 128 + r];
-          drow = w == 0 ? drow + other : other + drow;
+          drow = half[r] + half[128 + r];
         }
         if (w == 0 && q < Nq) a.Dsum[(size_t)t.bh * Nq + q] = drow;
         dsum = q < (VARLEN ? t.sq : Nq) ? drow : 0.f;
@@ -1405,7 +1433,7 @@ __global__ void __launch_bounds__(352, 1) fa_bwd_dq_kernel(const __grid_constant
           L = take_tile(k + 1, nt);
           if (L >= 0) {
             load_row_terms(nt, lse_next, d_next);
-            if constexpr (C::kFuseD && !C::kTileO) asm volatile("prefetch.global.L2 [%0];" ::"l"(o_at(nt)));
+            if constexpr (C::kFuseD && !C::kTileO) asm volatile("prefetch.global.L2 [%0];" ::"l"(o_row(nt, r)));
           }
         }
         ok = mbar_wait(&bars.s_full, gj & 1, abort_flag);
