@@ -28,9 +28,11 @@
 //
 // Measured, d = 128, 8 key heads, 32 query heads: 64 requests of up to 8192 keys
 // 157 us, 6.6 TB/s of keys and values (bound by them); 48 of up to 16384, E4M3
-// caches, 138 us (the tensor cores, which take 128 rows, and the bytes about alike);
-// 256 requests of up to 1000 keys 85 and 94 us, of up to 100 keys 39 and 51 us
+// caches, 140 us (the tensor cores, which take 128 rows, and the bytes about alike;
+// at d = 64 with pages of 16 tokens 107 us, 126 with one copying warp for keys and one for values);
+// 256 requests of up to 1000 keys, bf16 and E4M3, 94 and 91 us, of up to 100 keys 37 and 48 us
 // (bound by a tile's chain: its first S, softmax, last product, join).
+// Under a window of 1024 with 4 sinks 64 requests of 8192 keys 52 us, 5.0 TB/s of what they see.
 #include "paged_pipe.cuh"
 
 namespace fa {
