@@ -744,7 +744,8 @@ _rope_fn = None
 def rope(q, k, freqs, positions=None, interleaved: bool = False, factor: float = 1.0, q_weight=None, k_weight=None,
          eps: float = 1e-6):
     """Differentiable forward_rope: a torch.autograd.Function over forward_rope and backward_rope, with gradients of q, k and
-    the weights. Returns (q_out, k_out); k may be None."""
+    the weights. Returns (q_out, k_out); k may be None. (As with any function of torch's: before a backward pass is captured
+    into a CUDA graph, results of eager calls on the same leaves have to be gone.)"""
     global _rope_fn
     if _rope_fn is None:
         import torch
@@ -820,7 +821,8 @@ _window_fn = None
 
 
 def attention_window(q, k, v, window: int, sinks: int = 0, scale: float | None = None, seqlens_q=None, seqlens_k=None):
-    """Differentiable forward_window: a torch.autograd.Function over forward_window and backward_window. Returns o."""
+    """Differentiable forward_window: a torch.autograd.Function over forward_window and backward_window. Returns o. (Captured
+    into a CUDA graph as rope is.)"""
     global _window_fn
     if _window_fn is None:
         import torch
