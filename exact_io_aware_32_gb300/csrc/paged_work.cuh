@@ -186,9 +186,15 @@ __device__ __forceinline__ void find_range(const PagedArgs& a, Range& out, int (
     int mine = 0;  // length of this thread's requests
     bool any_bad = false;
     Request first{};
+    RawRequest ahead[2];  // the lengths of the next two, on their way
+#pragma unroll
+    for (int k = 0; k < 2; ++k) ahead[k] = load_request(a, min(r0 + k, a.R - 1));
     for (int r = r0; r < r1; ++r) {
+      const RawRequest raw = ahead[0];
+      ahead[0] = ahead[1];
+      ahead[1] = load_request(a, min(r + 2, a.R - 1));
       bool bad;
-      const Request q = request(a, r, bad);
+      const Request q = request(a, raw, bad);
       if (r == r0) first = q;
       any_bad |= bad;
       const int nt = tiles_of(a, q);
