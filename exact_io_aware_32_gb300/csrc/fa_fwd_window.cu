@@ -72,8 +72,9 @@ struct WBars {
   uint64_t k_full[2], k_empty[2], v_full[3], v_empty[3];
   uint64_t s_full[2], p_full[2], o_done[2], o_free[2];  // (one tile: o_done follows every P V)
   uint64_t s_free;                                      // one tile: S is in registers
-  // two tiles: a panel of O has been staged, has been read by its store; one tile: O has been staged in its Q's slot
-  uint64_t o_staged[2], o_read[2];
+  // two tiles: a panel of O has been staged; tile t may stage a panel (the O staged there before has been read by its store);
+  // one tile: O has been staged in its Q's slot
+  uint64_t o_staged[2], o_place[2][2];
   uint64_t teardown;
   uint64_t item_full[4], item_empty[4];
   int4 items[4][4];
@@ -220,7 +221,8 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
     mbar_init(&bars.s_free, 128);
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars.o_staged[s], 128);
-      mbar_init(&bars.o_read[s], 1);
+      mbar_init(&bars.o_place[s][0], 1);
+      mbar_init(&bars.o_place[s][1], 1);
     }
     for (int s = 0; s < kItemRing; ++s) {
       mbar_init(&bars.item_full[s], 1);
@@ -455,6 +457,10 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
     mbar_wait_drain(&bars.teardown, 0);
   } else if (C::kTiles == 2 && warp == C::kWarpStore) {
     // ------------------------------------------------------------ stores of staged O, a panel at a time
+    // Both tiles stage in one place, in the items' order. It is given to them by this warp, which knows that order and waits
+    // for the reads before, over a barrier of each tile's own: a tile waits for each of its phases in turn. (One barrier for
+    // both, told after every read, would be waited for by parity two phases on by a tile that staged two O ago, and the
+    // phase of that O still open looks like the one after it complete.)
     int n = 0;  // O stored so far
     bool ok = true;
     for (int i = 0; ok; ++i) {
@@ -463,6 +469,13 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if (x.nb[t] == 0) continue;
+        if (elect_one()) {
+          bulk_wait_read1();  // the first panel has been read; the writes finish on their own
+          mbar_arrive(&bars.o_place[t][0]);
+          bulk_wait_read0();
+          mbar_arrive(&bars.o_place[t][1]);
+        }
+        __syncwarp();
 #pragma unroll
         for (int pn = 0; pn < C::kPanels; ++pn) {
           if (!(ok = warp_wait(&bars.o_staged[pn], n & 1, abort_flag))) break;
@@ -473,13 +486,6 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
           __syncwarp();
         }
         if (!ok) break;
-        if (elect_one()) {
-          bulk_wait_read1();  // the first panel has been read; the writes finish on their own
-          mbar_arrive(&bars.o_read[0]);
-          bulk_wait_read0();
-          mbar_arrive(&bars.o_read[1]);
-        }
-        __syncwarp();
         ++n;
       }
     }
@@ -495,15 +501,11 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
     const uint32_t t_o = tmem + lane_off + C::col_o(t);
     const float sl2 = a.scale_log2;
     int np = 0, nq = 0;  // blocks and items of this tile so far
-    int staged = 0;      // O staged before this item's, by both tiles
     bool ok = true;
     for (int i = 0; ok; ++i) {
       const Item x = hear(bars, i, lane, abort_flag);
       if (x.bhk < 0) break;
-      if (!(t ? x.there[1] : x.there[0])) {
-        staged += (x.nb[0] > 0) + (x.nb[1] > 0);
-        continue;
-      }
+      if (!(t ? x.there[1] : x.there[0])) continue;
       const int row0 = t ? x.row[1] : x.row[0], row = row0 + r, p = row + x.off;  // p: the row's position
       const int nb = t ? x.nb[1] : x.nb[0], head = t ? x.head[1] : x.head[0], miss = t ? x.miss : -1;
       const int p_last = row0 + 127 + x.off;
@@ -638,12 +640,11 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
         // O, normalised, as bf16 into the staging place (rows of 128 swizzled bytes a panel), a panel at a time
         tc_fence_after();
         const float inv = 1.f / l_sum;
-        const int turn = staged + (t == 1 && x.nb[0] > 0 ? 1 : 0);  // two tiles: after so many others
 #pragma unroll 1
         for (int pn = 0; pn < C::kPanels; ++pn) {
           uint8_t* stage = smem + (C::kTiles == 2 ? C::kOffO : C::kOffQ + (nq & 1) * C::kTileBytes) + pn * C::kPanelBytes;
-          if (C::kTiles == 2 && turn > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&bars.o_read[pn], (turn - 1) & 1, abort_flag));
+          if (C::kTiles == 2) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars.o_place[t][pn], nq & 1, abort_flag));
             if (!ok) break;
           }
 #pragma unroll
@@ -675,7 +676,6 @@ __global__ void __launch_bounds__(WCfg<D>::kThreads, WCfg<D>::kCtasPerSm)
         for (int c = 0; c < D / 8; ++c) orow[c] = make_uint4(0u, 0u, 0u, 0u);
       }
       if (valid) a.lse[at] = real ? (m_ref + log2f(l_sum)) * kLn2 : -INFINITY;
-      staged += (x.nb[0] > 0) + (x.nb[1] > 0);
     }
   }
 
