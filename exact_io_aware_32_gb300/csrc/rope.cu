@@ -138,9 +138,14 @@ __device__ __forceinline__ void store_row(__nv_bfloat16* row, const Place& p, co
 struct Turn {
   float2 c[4], s[4];
 };
-__device__ __forceinline__ void rotate(Row& x, const Turn& t) {
+// (Chunks are rotated wholly or not at all, and those from rot on are left out: turned by cosine 1 and sine 0 their infinities
+// and NaN would reach the elements that stand where their pairs would. Halves apart, both of a lane's chunks are alike.
+// Whole heads, the same test for all lanes, cost nothing; without that test the backward with norms took 83.9 us, with it 83.3.)
+template <int D, bool INTER>
+__device__ __forceinline__ void rotate(Row& x, const Turn& t, const Place& p, int rot) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
+    if (rot != D && (INTER && i >= 2 ? p.b : p.a) >= rot) continue;
     const float2 a = x.a[i], bs = ptx::fmul2(x.b[i], t.s[i]);
     x.b[i] = ptx::ffma2(a, t.s[i], ptx::fmul2(x.b[i], t.c[i]));
     x.a[i] = make_float2(fmaf(a.x, t.c[i].x, -bs.x), fmaf(a.y, t.c[i].y, -bs.y));
@@ -178,15 +183,14 @@ __device__ __forceinline__ void make_angles(const RopeArgs& a, const unsigned lo
   __syncwarp();  // the angles before have been read
   for (int i = lane; i < tokens * (D / 2); i += 32) {
     const int which = i / (D / 2), pair = i % (D / 2);
-    float2 cs = make_float2(1.f, 0.f);
-    if (pair < a.rot / 2) {
-      const Token at = first.on(which, a.N);
-      const int position = !a.pos ? at.n : at.b < a.B ? a.pos[at.b * a.pos_b + at.n] : 0;
-      const unsigned long long t = (unsigned long long)(long long)position * turn[pair];
-      sincospif((float)(int)(t >> 32) * 0x1p-31f, &cs.y, &cs.x);
-      cs.x *= a.factor;
-      cs.y *= sign * a.factor;
-    }
+    if (pair >= a.rot / 2) continue;
+    const Token at_token = first.on(which, a.N);
+    const int position = !a.pos ? at_token.n : at_token.b < a.B ? a.pos[at_token.b * a.pos_b + at_token.n] : 0;
+    const unsigned long long t = (unsigned long long)(long long)position * turn[pair];
+    float2 cs;
+    sincospif((float)(int)(t >> 32) * 0x1p-31f, &cs.y, &cs.x);
+    cs.x *= a.factor;
+    cs.y *= sign * a.factor;
     const int part = INTER ? pair % (D / 4) / 4 : pair / 8, own = INTER ? pair / (D / 4) * 4 + pair % 4 : pair % 8;
     float* at = reinterpret_cast<float*>(&to.at[which * (D / 4) + own / 2 * kLanes + part]) + own % 2;
     at[0] = cs.x;
@@ -392,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, fwd_ctas_per_sm(NORM, MODE)) fa_rope
         times_weights<D>(x, weights[kind], part_of);
         times(x, r);
       }
-      rotate(x, t);
+      rotate<D, INTER>(x, t, p, a.rot);
       if (h >= u.h1) continue;
       if (MODE == kStore && kind) {
         const long long at = (place_in_cache + ((long long)h << a.page_shift)) * D;
@@ -461,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, bwd_ctas_per_sm(NORM, D)) fa_rope_bw
       ring.taken();
       load(k + kAhead, kAhead);
       const bool live = h < u.h1;
-      rotate(g, t);
+      rotate<D, INTER>(g, t, p, a.rot);
       if (NORM) {
         const float all = inverse_deviation<D>(x, a.eps);  // (sums over lanes: every lane takes part)
         const float r = live ? all : 0.f;  // no row: zeros, which add nothing to dw, whatever eps
