@@ -265,15 +265,18 @@ __device__ __forceinline__ float inverse_deviation(const Row& x, float eps) {
   return rsqrtf(fmaf(row_sum<D>(dot(x, x)), 1.f / D, eps));
 }
 
-// Sixteen codes of a lane's row into a cache page.
+// Sixteen codes of a lane's row into a cache page. (Factors far from 1 with the values' scale: without it 1 / f may be infinite,
+// and zero times that is no zero, or subnormal and short of bits. Keys are made smaller before their rotation, where the
+// largest would overflow, and larger after it, where infinities would meet.)
 template <bool INTER>
-__device__ __forceinline__ void store_codes(uint8_t* row, const Place& p, const Row& y, float inv) {
+__device__ __forceinline__ void store_codes(uint8_t* row, const Place& p, Row& y, const Factor& f) {
+  if (f.scale > 1.f) times(y, f.scale);
   float x[16];
   in_order<INTER>(y, x);
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    w[i] = e4m3x4(x[4 * i] * inv, x[4 * i + 1] * inv, x[4 * i + 2] * inv, x[4 * i + 3] * inv);
+    w[i] = e4m3x4(x[4 * i] * f.inv, x[4 * i + 1] * f.inv, x[4 * i + 2] * f.inv, x[4 * i + 3] * f.inv);
   *reinterpret_cast<uint2*>(row + p.a) = make_uint2(w[0], w[1]);
   *reinterpret_cast<uint2*>(row + p.b) = make_uint2(w[2], w[3]);
 }
@@ -327,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, fwd_ctas_per_sm(NORM, MODE)) fa_rope
   }
   __syncthreads();
   Ring<kAhead, 1> ring(ring_at);
-  const float inv_k = MODE == kStore && a.fp8 ? 1.f / a.descale_k : 1.f;
+  const Factor key_factor = factor_of(MODE == kStore && a.fp8 ? a.descale_k : 1.f);
   const long long first_k = a.units[0], first_v = first_k + a.units[1];
   const long long units = MODE == kStore ? first_v + a.units[1] : first_v;
   for (long long i = (long long)blockIdx.x * kWarps + warp; i < units; i += (long long)gridDim.x * kWarps) {
@@ -396,12 +399,13 @@ __global__ void __launch_bounds__(kThreads, fwd_ctas_per_sm(NORM, MODE)) fa_rope
         times_weights<D>(x, weights[kind], part_of);
         times(x, r);
       }
+      if (MODE == kStore && kind && key_factor.scale < 1.f) times(x, key_factor.scale);
       rotate<D, INTER>(x, t, p, a.rot);
       if (h >= u.h1) continue;
       if (MODE == kStore && kind) {
         const long long at = (place_in_cache + ((long long)h << a.page_shift)) * D;
         if (a.fp8)
-          store_codes<INTER>(static_cast<uint8_t*>(a.k_cache) + at, p, x, inv_k);
+          store_codes<INTER>(static_cast<uint8_t*>(a.k_cache) + at, p, x, key_factor);
         else
           store_row<INTER>(static_cast<__nv_bfloat16*>(a.k_cache) + at, p, x);
       } else {

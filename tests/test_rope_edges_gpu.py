@@ -75,3 +75,38 @@ def test_a_rotated_infinity_stays_in_its_pair(inter):
     for h, n, e in ((0, 1, 10), (1, 2, 95), (2, 3, 47)):
         hit[0, h, n, list(pair[e])] = True
     assert torch.equal(~y.isfinite(), hit) and torch.equal(y[~hit], r[~hit])
+
+
+@pytest.mark.parametrize("rotary", [0, 32])
+@pytest.mark.parametrize("factor", [1e-45, 1e-40, 2.0 ** -128, 2.0 ** -126, 2.0 ** -101, 2.0 ** -100, 2.0 ** -99, 0.37, 2.0 ** 99, 2.0 ** 100,
+                                    2.0 ** 120, 1.1 * 2.0 ** 126, 3e38])
+def test_key_factors_far_from_one(factor, rotary):
+    """Codes of keys for every factor that is taken, zeros among the keys: the nearest one, half a step of E4M3 (2^-4 of the
+    value, 2^-10 below the normal codes), with room for the key's and the quotient's fp32 roundings: 2^-23 of the value for the
+    quotient, and where the key is rotated 2^-19 of its pair's size; 2^-18 of both here."""
+    f = float(torch.tensor(factor, dtype=torch.float32))
+    T, Hk, d = 40, 3, 64
+    g = torch.Generator().manual_seed(3)
+    want = torch.randn((T, Hk, d), generator=g, dtype=torch.float64) * torch.tensor([0.01, 1.0, 200.0])[:, None]
+    want[:, :, ::7] = 0.0
+    want[5] = 0.0
+    k = (want * f).clamp(-3e38, 3e38).to(torch.bfloat16).cuda()
+    q = randn((T, 2, d), 1)
+    freqs = fa.rope_frequencies(32)[:rotary // 2].contiguous()
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    caches = [torch.full((3, Hk, 16, d), 1.0, device="cuda").to(torch.float8_e4m3fn) for _ in range(2)]
+    y = fa.paged_rope_store(q, k, k, pos, pos, freqs, *caches, descale_k=f, descale_v=f)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(True) == fa.FA_OK and y.isfinite().all()
+    ref = window_ref.rope(k.transpose(0, 1), None, pos, freqs, False, 1.0, 1e-6)[0].transpose(0, 1) / f if rotary else k.double() / f
+    for cache, r in zip(caches, (ref, k.double() / f)):
+        got = cache.double().transpose(1, 2).reshape(48, Hk, d)[:T]
+        r = r.clamp(-448, 448)
+        # (the pair's size: at most twice the row's largest element)
+        size = r.abs() + (2 * r.abs().amax(-1, keepdim=True) if cache is caches[0] and rotary else 0)
+        step = torch.exp2(torch.floor(torch.log2(r.abs().clamp_min(2.0 ** -6))) - 4)
+        assert got.isfinite().all()
+        over = (got - r).abs() - step - 2.0 ** -18 * size
+        assert float(over.max()) <= 0, (float(over.max()), factor)
+        zero = r == 0
+        assert not got[zero].any()
