@@ -188,7 +188,8 @@ int bwd_common(const void* q, const void* k, const void* v, const void* o, const
       !aligned16(dq) || !aligned16(dk) || !aligned16(dv) || !aligned4(seqlens_q) || !aligned4(seqlens_k))
     return FA_ERR_MISALIGNED;
   const size_t need = fa_bwd_kv_workspace_bytes(B, H, Nq, Nq, d);
-  if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+  const uintptr_t align = window ? 16 : 256;  // as each entry point states it (the kernels want 4: floats and counters)
+  if (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & (align - 1)) != 0)
     return FA_ERR_WORKSPACE;
   DeviceInfo* di = nullptr;
   if ((st = device_info(&di)) != FA_OK) return st;

@@ -1,0 +1,24 @@
+"""Calls of the windowed attention and the rotation that their documentation allows, on the GPU."""
+import pytest
+import torch
+
+from exact_io_aware_32_gb300 import fa
+from test_window_gpu import inputs
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_workspace_anywhere_on_16_bytes(d):
+    """The same bits whatever 16-byte boundary the workspace begins at, and nothing behind its end is touched."""
+    q, k, v, dO = inputs(2, 4, 2, 333, 400, d, 1)
+    o, lse = fa.forward_window(q, k, v, 100, 3)
+    ref = fa.backward_window(q, k, v, o, lse, dO, 100, 3)
+    need = fa.fa_bwd_window_workspace_bytes(2, 4, 2, 333, 400, d, 100, 3)
+    arena = torch.empty(need + 512, dtype=torch.uint8, device="cuda")
+    for at in (16, 48, 240, 256):
+        arena.fill_(0xA5)
+        got = fa.backward_window(q, k, v, o, lse, dO, 100, 3, workspace=arena[at:at + need])
+        assert all(torch.equal(x, r) for x, r in zip(got, ref)), at
+        assert (arena[:at] == 0xA5).all() and (arena[at + need:] == 0xA5).all()
+    assert fa.fa_device_status(True) == fa.FA_OK
