@@ -435,8 +435,8 @@ typedef struct {
  *   q_out, k_out   [out] the same shapes
  *   q_weight, k_weight [in] the norms' weights [d], bf16 or (weights_fp32 != 0) fp32, 16-byte aligned; NULL, both of them: no norms
  *   eps            the norms': finite, >= 0
- *   freqs          [in]  fp64 [rotary / 2], radians a position. The angle is exact to 2^-53 of a frequency times
- *                  the position, and 2^-24 of a turn: a position of millions loses nothing
+ *   freqs          [in]  fp64 [rotary / 2], radians a position. The angle is that of the given numbers to 2^-24 of
+ *                  a turn, whatever the position: one of millions loses nothing (frequencies below 2^32 in size)
  *   rotary         rotated elements of a head: a multiple of 16, 0 (norms alone) to d
  *   factor         of cosine and sine (1, or what a scaling for long texts asks for): finite
  *   positions      [in]  int32: token n of sequence b stands at positions[b * positions_stride + n]

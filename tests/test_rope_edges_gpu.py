@@ -1,5 +1,6 @@
 """Rotation by position at the edges of its values and factors, on the GPU."""
 import math
+from fractions import Fraction
 
 import pytest
 import torch
@@ -110,3 +111,37 @@ def test_key_factors_far_from_one(factor, rotary):
         assert float(over.max()) <= 0, (float(over.max()), factor)
         zero = r == 0
         assert not got[zero].any()
+
+
+def inverse_turn():
+    """1 / (2 pi) to 400 bits, by Machin's formula."""
+    one = 1 << 420
+
+    def atan_inverse(x):
+        term = total = one // x
+        n = 1
+        while term:
+            term //= -x * x
+            n += 2
+            total += term // n
+        return total
+    return Fraction(one, 2 * 4 * (4 * atan_inverse(5) - atan_inverse(239)))
+
+
+def test_angles_are_those_of_the_given_frequencies():
+    """Frequencies of 2^-60 to 2^32 radians a position, of both signs, at the farthest positions, against angles in whole numbers:
+    2^-24 of a turn, so the bounds of test_rope_gpu.py."""
+    d = 128
+    g = torch.Generator().manual_seed(4)
+    f = torch.exp2(torch.linspace(-60, 31, d // 2, dtype=torch.float64) + torch.rand(d // 2, generator=g, dtype=torch.float64))
+    f[1::2] *= -1
+    places = [2 ** 31 - 1, 2 ** 31 - 2, -2 ** 31, 1234567890, 2 ** 20 + 1, 1, 0, -7]
+    inverse = inverse_turn()
+    at = [[Fraction(w) * p * inverse % 1 for w in f.tolist()] for p in places]
+    angle = 2 * math.pi * torch.tensor([[float(x if x < Fraction(1, 2) else x - 1) for x in row] for row in at], dtype=torch.float64)
+    q = randn((1, 3, len(places), d), 9)
+    y, _ = fa.forward_rope(q, None, f.cuda(), torch.tensor(places, dtype=torch.int64).to(torch.int32).cuda())
+    a, b = q.double()[..., :64], q.double()[..., 64:]
+    c, s = angle.cos().cuda(), angle.sin().cuda()
+    size = a.abs() + b.abs()
+    check(y, torch.cat((a * c - b * s, b * c + a * s), -1), torch.cat((size, size), -1))
