@@ -273,6 +273,14 @@ def _bf16(*ts):
 _attention_fn = None
 
 
+def _gradient(x):
+    """A gradient as the attention kernels read it: bf16, contiguous and 16-byte aligned (a contiguous view may begin anywhere)."""
+    import torch
+
+    x = x.to(torch.bfloat16).contiguous()
+    return x if x.data_ptr() % 16 == 0 else x.clone()
+
+
 def attention(q, k, v, causal: bool = False, scale: float | None = None, dropout_p256: int = 0, seed: int = 0,
               offset: int = 0):
     """Differentiable attention o = softmax(scale q k^T [causal]) v (with dropout of probability
@@ -298,7 +306,7 @@ def attention(q, k, v, causal: bool = False, scale: float | None = None, dropout
             def backward(ctx, dO):
                 q, k, v, o, lse = ctx.saved_tensors
                 causal, scale, p256, seed, offset = ctx.args
-                dO = dO.to(torch.bfloat16).contiguous()
+                dO = _gradient(dO)
                 if p256:
                     dq, dk, dv = backward_dropout(q, k, v, o, lse, dO, p256, seed, offset, causal=causal, scale=scale)
                 else:
@@ -735,7 +743,7 @@ def _rows_contiguous(x):
 
     x = x.to(torch.bfloat16)
     ok = x.stride(-1) == 1 and all(s % 8 == 0 for s, n in zip(x.stride()[:-1], x.shape[:-1]) if n > 1) and x.data_ptr() % 16 == 0
-    return x if ok else x.contiguous()
+    return x if ok else _gradient(x)
 
 
 _rope_fn = None
@@ -838,8 +846,7 @@ def attention_window(q, k, v, window: int, sinks: int = 0, scale: float | None =
             @staticmethod
             def backward(ctx, dO):
                 q, k, v, o, lse, seqlens_q, seqlens_k = ctx.saved_tensors
-                dO = dO.to(torch.bfloat16).contiguous()
-                return (*backward_window(q, k, v, o, lse, dO, *ctx.args, seqlens_q, seqlens_k), None, None, None)
+                return (*backward_window(q, k, v, o, lse, _gradient(dO), *ctx.args, seqlens_q, seqlens_k), None, None, None)
 
         _window_fn = _Window
     scale = 1.0 / math.sqrt(int(q.shape[-1])) if scale is None else scale

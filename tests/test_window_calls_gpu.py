@@ -22,3 +22,26 @@ def test_workspace_anywhere_on_16_bytes(d):
         assert all(torch.equal(x, r) for x, r in zip(got, ref)), at
         assert (arena[:at] == 0xA5).all() and (arena[at + need:] == 0xA5).all()
     assert fa.fa_device_status(True) == fa.FA_OK
+
+
+def off_by(x, n):
+    """x as a contiguous view that begins n elements into its storage."""
+    y = torch.empty(x.numel() + n, dtype=x.dtype, device=x.device)[n:].view(x.shape)
+    y.copy_(x)
+    assert y.is_contiguous() and y.data_ptr() % 16
+    return y
+
+
+@pytest.mark.parametrize("n", [1, 4])
+def test_gradients_that_begin_anywhere(n):
+    """Contiguous gradients off 16 bytes, as a slice of a larger buffer is, give what aligned ones give."""
+    q, k, v, dO = inputs(1, 4, 2, 130, 130, 64, 2)
+    freqs = fa.rope_frequencies(64)
+    dk = dO[:, :2].contiguous()
+    x = [y.requires_grad_() for y in (q, k, v)]
+    for out, leaves, g in ((fa.attention_window(*x, 50, 1), x, (dO,)), (fa.rope(q, k, freqs), x[:2], (dO, dk)),
+                           (fa.attention(q, q, q, causal=True), x[:1], (dO,)),
+                           (fa.attention(q, q, q, dropout_p256=25, seed=3), x[:1], (dO,))):
+        ref = torch.autograd.grad(out, leaves, g, retain_graph=True)
+        got = torch.autograd.grad(out, leaves, [off_by(y, n) for y in g])
+        assert all(torch.equal(a, b) for a, b in zip(got, ref))
