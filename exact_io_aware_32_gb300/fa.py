@@ -286,7 +286,7 @@ def attention(q, k, v, causal: bool = False, scale: float | None = None, dropout
     """Differentiable attention o = softmax(scale q k^T [causal]) v (with dropout of probability
     dropout_p256 / 256 after the softmax if given) for q, k, v of shape [B, H, N, d], bf16: a
     torch.autograd.Function whose forward runs fa_fwd (fa_fwd_dropout) and whose backward runs fa_bwd
-    (fa_bwd_dropout, the same mask made again from seed and offset)."""
+    (fa_bwd_dropout, the same mask made again from seed and offset). Gradients of the gradients are refused."""
     global _attention_fn
     if _attention_fn is None:
         import torch
@@ -303,6 +303,7 @@ def attention(q, k, v, causal: bool = False, scale: float | None = None, dropout
                 return o
 
             @staticmethod
+            @torch.autograd.function.once_differentiable
             def backward(ctx, dO):
                 q, k, v, o, lse = ctx.saved_tensors
                 causal, scale, p256, seed, offset = ctx.args
@@ -752,7 +753,7 @@ _rope_fn = None
 def rope(q, k, freqs, positions=None, interleaved: bool = False, factor: float = 1.0, q_weight=None, k_weight=None,
          eps: float = 1e-6):
     """Differentiable forward_rope: a torch.autograd.Function over forward_rope and backward_rope, with gradients of q, k and
-    the weights. Returns (q_out, k_out); k may be None. (As with any function of torch's: before a backward pass is captured
+    the weights (gradients of those are refused). Returns (q_out, k_out); k may be None. (As with any function of torch's: before a backward pass is captured
     into a CUDA graph, results of eager calls on the same leaves have to be gone.)"""
     global _rope_fn
     if _rope_fn is None:
@@ -768,6 +769,7 @@ def rope(q, k, freqs, positions=None, interleaved: bool = False, factor: float =
                 return q_out, k_out
 
             @staticmethod
+            @torch.autograd.function.once_differentiable
             def backward(ctx, dq_out, dk_out):
                 q, k, q_weight, k_weight, freqs, positions = ctx.saved_tensors
                 interleaved, factor, eps, has_k = ctx.args
@@ -829,8 +831,8 @@ _window_fn = None
 
 
 def attention_window(q, k, v, window: int, sinks: int = 0, scale: float | None = None, seqlens_q=None, seqlens_k=None):
-    """Differentiable forward_window: a torch.autograd.Function over forward_window and backward_window. Returns o. (Captured
-    into a CUDA graph as rope is.)"""
+    """Differentiable forward_window: a torch.autograd.Function over forward_window and backward_window (gradients of the
+    gradients are refused). Returns o. (Captured into a CUDA graph as rope is.)"""
     global _window_fn
     if _window_fn is None:
         import torch
@@ -844,6 +846,7 @@ def attention_window(q, k, v, window: int, sinks: int = 0, scale: float | None =
                 return o
 
             @staticmethod
+            @torch.autograd.function.once_differentiable
             def backward(ctx, dO):
                 q, k, v, o, lse, seqlens_q, seqlens_k = ctx.saved_tensors
                 return (*backward_window(q, k, v, o, lse, _gradient(dO), *ctx.args, seqlens_q, seqlens_k), None, None, None)

@@ -45,3 +45,20 @@ def test_gradients_that_begin_anywhere(n):
         ref = torch.autograd.grad(out, leaves, g, retain_graph=True)
         got = torch.autograd.grad(out, leaves, [off_by(y, n) for y in g])
         assert all(torch.equal(a, b) for a, b in zip(got, ref))
+
+
+@pytest.mark.parametrize("kind", ["attention", "dropout", "attention_window", "rope", "norm rope"])
+def test_second_derivatives_are_refused(kind):
+    """A gradient made with create_graph is right, and the gradient of it an error, not one that leaves terms out."""
+    q, k, v, _ = (x.requires_grad_() for x in inputs(1, 2, 2, 40, 40, 64, 3))
+    w = torch.ones(64, device="cuda", requires_grad=True)
+    freqs = fa.rope_frequencies(64)
+    out = {"attention": lambda: fa.attention(q, k, v), "dropout": lambda: fa.attention(q, k, v, dropout_p256=20, seed=1),
+           "attention_window": lambda: fa.attention_window(q, k, v, 9), "rope": lambda: fa.rope(q, k, freqs)[0],
+           "norm rope": lambda: fa.rope(q, k, freqs, q_weight=w, k_weight=w)[0]}[kind]
+    first, = torch.autograd.grad(out().float().square().sum(), q, create_graph=True)
+    plain, = torch.autograd.grad(out().float().square().sum(), q)
+    assert torch.equal(first, plain)
+    loss = q.float().square().sum() + first.float().square().sum()  # a penalty on the gradient beside another term
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        loss.backward()
