@@ -145,3 +145,26 @@ def test_angles_are_those_of_the_given_frequencies():
     c, s = angle.cos().cuda(), angle.sin().cuda()
     size = a.abs() + b.abs()
     check(y, torch.cat((a * c - b * s, b * c + a * s), -1), torch.cat((size, size), -1))
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_products_depend_on_the_distance_alone(inter):
+    """q . k of rows that stand 'apart' positions from one another is the same wherever they stand, and that of the 64-bit form at
+    this distance. Each side's elements are off by 2^-8 of themselves (their rounding) and 2^-17 of their pairs' sizes."""
+    d = 128
+    q, k = (randn((1, 1, 1, d), s).expand(1, 1, 6, d) for s in (11, 12))
+    freqs = fa.rope_frequencies(d)
+    starts = torch.tensor([0, 1, 77, 4096, 1 << 20, (1 << 31) - 2000], dtype=torch.int64)
+    sums = {}
+    for apart in (0, 1, 5, 300, 1999):
+        yq, _ = fa.forward_rope(q, None, freqs, (starts + apart).to(torch.int32).cuda(), interleaved=inter)
+        yk, _ = fa.forward_rope(k, None, freqs, starts.to(torch.int32).cuda(), interleaved=inter)
+        got = (yq.double() * yk.double()).sum(-1).flatten()
+        (rq, sq), (rk, sk) = (window_ref.rope(x[:, :, :1], None, torch.tensor([p], device="cuda"), freqs, inter, 1.0, 1e-6)
+                              for x, p in ((q, apart), (k, 0)))
+        ref = float((rq * rk).sum())
+        # (an element is at most its pair's size, which the rotation keeps)
+        bound = float((sq * sk).sum()) * (2 * 2.0 ** -8 + 2 * 2.0 ** -17 + 2.0 ** -15)
+        assert float((got - ref).abs().max()) <= bound, (apart, float((got - ref).abs().max()), bound)
+        sums[apart] = (ref, bound)
+    assert abs(sums[0][0] - sums[300][0]) > sums[0][1] + sums[300][1]  # distances differ by more than that
