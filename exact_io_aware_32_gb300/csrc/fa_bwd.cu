@@ -47,10 +47,15 @@
 // Under a window tiles are short, so a tile's start and end count: the next tile is
 // taken, and its row terms, Q and O are on their way, during the last blocks of the
 // one before; tiles without work are the loading warp's. 4 x 4096 tokens, 32 heads
-// over 8 of 128, window 512: 411 us (783 TFLOP/s of the pairs seen), about 200 us of them dQ
-// (an unmasked block 1650 cycles, one with a mask 2100, a tile 3900 besides); with 4
-// sinks 460 us, since a sink's dK/dV tile walks all N / 128 query blocks of all its
-// heads; 8 x 4096 at d = 64 700 us. Window 4096, 16384 tokens: 1.94 ms, 1240 TFLOP/s.
+// over 8 of 128, window 512: 406 to 429 us (793 to 750 TFLOP/s of the pairs seen), about 200 us of them
+// dQ (an unmasked block 1650 cycles, one with a mask 2100, a tile 3900 besides); 8 x 4096 at
+// d = 64 613 us. Window 4096, 16384 tokens: 1.94 to 2.13 ms, 1240 to 1130 TFLOP/s.
+// A sink's dK/dV tile walks all N / 128 query blocks of all heads of its group in one CTA: with 4
+// sinks the two cases of window 512 take 466 to 489 and 701 us; one text of 16384 tokens, 16 heads, 313 us (248
+// without sinks); the longer the text and the fewer the key heads the worse: 8 heads over 1 1360 us (125).
+//
+// P^T and dS enter their products as bf16, the type of dO, q and k beside them, and D is the sum over the rounded
+// o: dq, dk and dv are off by 0.0023 to 0.0025 (relative RMS) where their own rounding leaves 0.0017.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -1629,8 +1634,10 @@ __global__ void __launch_bounds__(256) fa_bwd_prep_kernel(const __grid_constant_
   }
 }
 
-// The d = 64 backward's first kernel (its dQ kernel forms D): the work counters
-// of the two main kernels are reset, and one thread per sequence checks its lengths.
+// First kernel where the dQ kernel forms D (d = 64, and under a window at both sizes): the work counters of
+// the two main kernels are reset, and its threads check the sequences' lengths. Under a window all three are programmatic
+// dependents, each of which waits for the one before to end before it touches the workspace: this one for what
+// used the same workspace last, dQ for the reset counters, dK/dV for D.
 __global__ void __launch_bounds__(32) fa_bwd_start_kernel(const __grid_constant__ BwdArgs a) {
   grid_release();
   grid_wait();

@@ -22,13 +22,19 @@
 //
 // Bound by a block's chain of S, softmax and P V (about 2950 cycles for the blocks of
 // two tiles, 2048 of them products) and, where windows are short, by what a tile costs besides: 16384
-// tokens, 32 heads over 8 of 128, window 4096, 4 sinks 669 us, 1440 TFLOP/s of the pairs seen;
-// 4 x 4096 tokens, window 512, 143 us (900 TFLOP/s; of the blocks' keys a fifth is hidden),
-// with 4 sinks 163 us. Issuing both tiles' first S of the next item before this one's last
+// tokens, 32 heads over 8 of 128, window 4096, 4 sinks 669 us in a CUDA graph, 1440 TFLOP/s of the
+// pairs seen, 693 to 730 us as calls one after another; 4 x 4096 tokens, window 512, 150 to 169 us from
+// run to run (860 to 760 TFLOP/s; of the blocks' keys a fifth is hidden), with 4 sinks 160 to 163 us;
+// 8 x 4096 at d = 64 198 to 213 us (650 to 605). Issuing both tiles' first S of the next item before this one's last
 // products cost more than it gave (158 and 162 us, window 4096 692 and 721 us): what stands
 // in the MMA warp's way delays every block.
 //
-// Warp roles: a softmax warpgroup per tile, the TMA warp, the MMA warp.
+// P enters P V as bf16, as in fa_fwd.cu: the product takes both operands in V's type, and a
+// second one with P's remainder would add 1024 cycles to a block of two tiles. The errors of
+// a row's weights are independent, so o is off by 0.0021 to 0.0022 (relative RMS) where its own rounding to
+// bf16 leaves 0.0016. Scores, maxima, sums and O are fp32.
+//
+// Warp roles: a softmax warpgroup per tile, the TMA warp, the MMA warp; two tiles: a warp that stores O.
 #include <algorithm>
 
 #include "fa_internal.h"

@@ -500,8 +500,11 @@ FA_API int fa_paged_rope_store(const void* q, const void* k, const void* v, long
  * (key j is visible to query i, at position p = i + Nk - Nq, iff j <= p) a row
  * sees the last 'window' ones, its own among them, and the first 'sinks' of
  * the sequence: j <= p and (p - j < window or j < sinks). Blocks of keys that no row of a tile sees
- * are neither read nor multiplied. Forward and backward as in fa_fwd_kv and
- * fa_bwd_kv (causal), with grouped heads.
+ * are neither read nor multiplied; hidden keys and values that share a block of 128 with visible ones are
+ * multiplied by weights of zero and must hold finite values. Forward and backward as in fa_fwd_kv and
+ * fa_bwd_kv (causal), with grouped heads, and with their roundings: the weights enter their product with v as bf16
+ * (o within 0.0022 of the exact one, relative RMS, 0.0016 of it its own rounding), and the backward's weights
+ * and score gradients theirs (0.0025).
  *   q, o, dO, dq   bf16 [B, Hq, Nq, d];  lse fp32 [B, Hq, Nq]
  *   k, v, dk, dv   bf16 [B, Hkv, Nk, d]: query head h reads key head h / (Hq / Hkv) (Hq a multiple of Hkv)
  *   window         >= 1 (Nk and more: the causal rule alone);  sinks >= 0
