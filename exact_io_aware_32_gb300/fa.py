@@ -23,6 +23,7 @@ there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 import threading
@@ -270,6 +271,36 @@ def _bf16(*ts):
             raise ValueError("expected contiguous bf16 CUDA tensors")
 
 
+_refused_fn = None
+
+
+def _once(backward):
+    """Decorator of a backward method: gradients that it makes under create_graph stand in the graph behind everything they were made of
+    (its arguments and saved tensors, so also where the loss is linear in the outputs), and differentiating them raises."""
+    global _refused_fn
+    import torch
+
+    if _refused_fn is None:
+        class _Refused(torch.autograd.Function):
+            @staticmethod
+            def forward(ctx, n, *tensors):
+                return tensors[:n]
+
+            @staticmethod
+            def backward(ctx, *_):
+                raise RuntimeError("second derivatives of attention, attention_window and rope are not implemented")
+
+        _refused_fn = _Refused
+
+    @functools.wraps(backward)
+    def once(ctx, *grads):
+        with torch.no_grad():
+            r = backward(ctx, *grads)
+        return _refused_fn.apply(len(r), *r, *grads, *ctx.saved_tensors) if torch.is_grad_enabled() else r
+
+    return once
+
+
 _attention_fn = None
 
 
@@ -303,7 +334,7 @@ def attention(q, k, v, causal: bool = False, scale: float | None = None, dropout
                 return o
 
             @staticmethod
-            @torch.autograd.function.once_differentiable
+            @_once
             def backward(ctx, dO):
                 q, k, v, o, lse = ctx.saved_tensors
                 causal, scale, p256, seed, offset = ctx.args
@@ -769,7 +800,7 @@ def rope(q, k, freqs, positions=None, interleaved: bool = False, factor: float =
                 return q_out, k_out
 
             @staticmethod
-            @torch.autograd.function.once_differentiable
+            @_once
             def backward(ctx, dq_out, dk_out):
                 q, k, q_weight, k_weight, freqs, positions = ctx.saved_tensors
                 interleaved, factor, eps, has_k = ctx.args
@@ -846,7 +877,7 @@ def attention_window(q, k, v, window: int, sinks: int = 0, scale: float | None =
                 return o
 
             @staticmethod
-            @torch.autograd.function.once_differentiable
+            @_once
             def backward(ctx, dO):
                 q, k, v, o, lse, seqlens_q, seqlens_k = ctx.saved_tensors
                 return (*backward_window(q, k, v, o, lse, _gradient(dO), *ctx.args, seqlens_q, seqlens_k), None, None, None)

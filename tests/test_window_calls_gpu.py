@@ -47,18 +47,41 @@ def test_gradients_that_begin_anywhere(n):
         assert all(torch.equal(a, b) for a, b in zip(got, ref))
 
 
+@pytest.mark.parametrize("linear", [False, True])
 @pytest.mark.parametrize("kind", ["attention", "dropout", "attention_window", "rope", "norm rope"])
-def test_second_derivatives_are_refused(kind):
-    """A gradient made with create_graph is right, and the gradient of it an error, not one that leaves terms out."""
+def test_second_derivatives_are_refused(kind, linear):
+    """A gradient made with create_graph is right, and the gradient of it an error, not one that leaves terms out, also where the
+    loss is linear in the outputs. (Of a rotation without norms it is then zero, which is right.)"""
     q, k, v, _ = (x.requires_grad_() for x in inputs(1, 2, 2, 40, 40, 64, 3))
     w = torch.ones(64, device="cuda", requires_grad=True)
     freqs = fa.rope_frequencies(64)
     out = {"attention": lambda: fa.attention(q, k, v), "dropout": lambda: fa.attention(q, k, v, dropout_p256=20, seed=1),
            "attention_window": lambda: fa.attention_window(q, k, v, 9), "rope": lambda: fa.rope(q, k, freqs)[0],
            "norm rope": lambda: fa.rope(q, k, freqs, q_weight=w, k_weight=w)[0]}[kind]
-    first, = torch.autograd.grad(out().float().square().sum(), q, create_graph=True)
-    plain, = torch.autograd.grad(out().float().square().sum(), q)
+
+    def gradients(**kw):
+        y = out().float()
+        return torch.autograd.grad((y if linear else y.square()).sum(), q, **kw)[0]
+    first, plain = gradients(create_graph=True), gradients()
     assert torch.equal(first, plain)
     loss = q.float().square().sum() + first.float().square().sum()  # a penalty on the gradient beside another term
-    with pytest.raises(RuntimeError, match="once_differentiable"):
+    if kind == "rope" and linear:
+        assert torch.equal(torch.autograd.grad(loss, q)[0], 2 * q)
+        return
+    with pytest.raises(RuntimeError, match="second derivatives"):
         loss.backward()
+
+
+def test_gradients_with_create_graph_accumulate():
+    """backward(create_graph=True) fills the leaves' gradients as without it, unused ones left out."""
+    for kw in (dict(), dict(create_graph=True)):
+        q, k, v, dO = inputs(1, 4, 2, 60, 60, 128, 4)
+        q.requires_grad_()
+        w = torch.ones(128, device="cuda", requires_grad=True)
+        freqs = fa.rope_frequencies(128)
+        x, y = fa.rope(q, k, freqs, q_weight=w, k_weight=w)
+        fa.attention_window(x, y, v, 20, 1).backward(dO, **kw)
+        if not kw:
+            ref = q.grad, w.grad
+    assert torch.equal(q.grad, ref[0]) and torch.equal(w.grad, ref[1])
+    q.grad = w.grad = None  # (a gradient with a graph refers to its leaf)
