@@ -38,3 +38,23 @@ def test_many_short_items(B, Hq, Hkv, N, window, sinks, lens, d):
     check("lse", runs[0][1], ref)
     for o, lse in runs[1:]:
         assert torch.equal(o, runs[0][0]) and torch.equal(lse, runs[0][1])
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_short_items_beside_copies(d):
+    """The same with the memory kept busy by copies on another stream, which delay the stores of the outputs."""
+    q, k, v, _ = inputs(4, 402, 134, 128, 128, d, 5)
+    alone = fa.forward_window(q, k, v, 70, 2)
+    a, b = (torch.empty(1 << 28, dtype=torch.uint8, device="cuda") for _ in range(2))
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    runs = []
+    with torch.cuda.stream(other):
+        for _ in range(40):
+            b.copy_(a)
+    for _ in range(20):
+        runs.append(fa.forward_window(q, k, v, 70, 2))
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(True) == fa.FA_OK
+    for o, lse in runs:
+        assert torch.equal(o, alone[0]) and torch.equal(lse, alone[1])
